@@ -56,6 +56,23 @@ SIGNATURES = {
     "sinkattn_decode_static_scratch": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_float,
                                                 _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
                                                 _c_int, _c_int, _c_int, _vp]),
+    "sinkattn_decode_window_plan": (_c_int, [_c_int] * 9 + [ctypes.POINTER(_c_int),
+                                                            ctypes.POINTER(_c_size)]),
+    "sinkattn_decode_window": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_float, _c_int,
+                                        _c_int, _vp, _vp] + [_c_int] * 8 +
+                               [_vp, _c_size, _c_int, _vp]),
+    "sinkattn_prefill_window": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_float,
+                                         _c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp]),
+    "sinkattn_prefill_paged_window": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp,
+                                               _c_int, _vp, _c_int, _c_int, _vp, _c_float, _c_int,
+                                               _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                                               _vp]),
+    "sinkattn_decode_mass": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_float, _vp] +
+                             [_c_int] * 8 + [_vp]),
+    "sinkattn_prefill_mass": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _vp,
+                                       _c_int, _c_int, _vp, _c_float, _vp] + [_c_int] * 5 + [_vp]),
+    "sinkattn_evict": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                                _vp, _c_int, _vp, _c_int, _vp, _vp] + [_c_int] * 6 + [_vp]),
 }
 
 STATIC_SCRATCH_BYTES = 16 << 20
@@ -392,3 +409,248 @@ def qkv_prologue(qkv, bias, positions, slot_mapping, inv_freq, mscale, k_cache, 
             int(rope_style), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), tokens, num_qo_heads,
             num_kv_heads, d, page, num_pages, _stream(stream)))
     return q_out
+
+
+# ------------------------------------------------- bounding a long context
+_INT_MAX = 2**31 - 1
+
+
+@contextlib.contextmanager
+def _at(dev, stream):
+    """Makes `dev` the current device and `stream` (if given) its current
+    stream, so that what a call allocates or clears is ordered on the stream
+    that it launches on."""
+    with _on(dev), (contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)):
+        yield
+
+
+def _size(v, name, least=0):
+    """v as an int that fits the C ABI's (larger bounds mean no bound)."""
+    v = int(v)
+    if v < least:
+        raise ValueError(f"{name} must be at least {least}, got {v}")
+    return min(v, _INT_MAX)
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _paged_args(dev, batch, page_table, kv_lens, k_cache, v_cache=None):
+    _want(k_cache, "k_cache", torch.bfloat16, 4, dev)
+    _want(page_table, "page_table", torch.int32, 2, dev)
+    _want(kv_lens, "kv_lens", torch.int32, 1, dev)
+    if v_cache is not None:
+        _want(v_cache, "v_cache", torch.bfloat16, 4, dev)
+        _shape(v_cache, "v_cache", k_cache.shape)
+    if batch is not None:
+        _shape(page_table, "page_table", (batch, page_table.shape[1]))
+        _shape(kv_lens, "kv_lens", (batch,))
+
+
+def _rows_out(q, out, lse, want_lse):
+    """The bf16 result and the fp32 lse of the rows of q, checked or new."""
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _want(out, "out", torch.bfloat16, q.dim(), q.device)
+        _shape(out, "out", q.shape)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, q.dim() - 1, q.device)
+        _shape(lse, "lse", q.shape[:-1])
+    elif want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    return out, lse
+
+
+def decode_window_plan(batch, num_qo_heads, num_kv_heads, max_kv_len, window, first_tokens=0,
+                       num_splits=0, num_sms=0, head_dim=64, page_size=16):
+    """(split count, workspace bytes) that `decode_window` will use (host only)."""
+    s = _c_int(num_splits)
+    w = _c_size(0)
+    _check("sinkattn_decode_window_plan",
+           load().sinkattn_decode_window_plan(batch, num_qo_heads, num_kv_heads, head_dim,
+                                              page_size, max_kv_len, window, first_tokens, num_sms,
+                                              ctypes.byref(s), ctypes.byref(w)))
+    return s.value, w.value
+
+
+def decode_window(q, k_cache, v_cache, page_table, kv_lens, sinks, scale, max_kv_len, window,
+                  first_tokens=0, *, out=None, lse=None, num_splits=0, workspace=None, stream=None,
+                  want_lse=True, programmatic=None):
+    """`decode` with a sliding window: the token sees its request's `window`
+    newest keys (its own included) and the `first_tokens` oldest.  Pages
+    without a visible key are not looked up (their page_table entries may hold
+    anything).  Returns (out [B, Hq, 64] bf16, lse [B, Hq] fp32 or None)."""
+    dev = q.device
+    _want(q, "q", torch.bfloat16, 3)
+    batch, hq, d = q.shape
+    _paged_args(dev, batch, page_table, kv_lens, k_cache, v_cache)
+    _want(sinks, "sinks", torch.float32, 1, dev)
+    _shape(sinks, "sinks", (hq,))
+    num_pages, hkv, page, d2 = k_cache.shape
+    if d2 != d:
+        raise ValueError("k_cache and q disagree in head_dim")
+    window, first = _size(window, "window", 1), _size(first_tokens, "first_tokens")
+    max_kv_len, num_splits = _size(max_kv_len, "max_kv_len"), _size(num_splits, "num_splits")
+    with _at(dev, stream):
+        out, lse = _rows_out(q, out, lse, want_lse)
+        splits, ws_bytes = _plan(decode_window_plan, batch, hq, hkv, max_kv_len, window, first,
+                                 num_splits, 0, d, page) if batch else (1, 0)
+        if workspace is None and ws_bytes:
+            # zero-filled once; the call leaves it ready for the next one
+            workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=dev)
+        ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check("sinkattn_decode_window", load().sinkattn_decode_window(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), page_table.shape[1],
+            _ptr(kv_lens), _ptr(sinks), float(scale), window, first, _ptr(out), _ptr(lse), batch,
+            hq, hkv, d, page, num_pages, max_kv_len, num_splits, _ptr(workspace), ws_len,
+            _launch_flags(programmatic), _stream(None)))
+    return out, lse
+
+
+def prefill_window(q, k, v, cu_seqlens, sinks, scale, max_seqlen, window, first_tokens=0, *,
+                   out=None, lse=None, stream=None, want_lse=True):
+    """`prefill` with a sliding window: token i of a sequence sees tokens
+    i - window + 1 .. i and the sequence's `first_tokens` first ones (up to
+    itself).  Returns (out [T, Hq, 64], lse [T, Hq] or None)."""
+    dev = q.device
+    _want(q, "q", torch.bfloat16, 3)
+    _want(k, "k", torch.bfloat16, 3, dev)
+    _want(v, "v", torch.bfloat16, 3, dev)
+    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, dev)
+    _want(sinks, "sinks", torch.float32, 1, dev)
+    total, hq, d = q.shape
+    hkv = k.shape[1]
+    _shape(k, "k", (total, hkv, d))
+    _shape(v, "v", k.shape)
+    _shape(sinks, "sinks", (hq,))
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 entries")
+    window, first = _size(window, "window", 1), _size(first_tokens, "first_tokens")
+    with _at(dev, stream):
+        out, lse = _rows_out(q, out, lse, want_lse)
+        _check("sinkattn_prefill_window", load().sinkattn_prefill_window(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), cu_seqlens.numel() - 1, total,
+            _size(max_seqlen, "max_seqlen"), _ptr(sinks), float(scale), window, first, _ptr(out),
+            _ptr(lse), hq, hkv, d, _stream(None)))
+    return out, lse
+
+
+def prefill_paged_window(q, cu_seqlens_q, k_cache, v_cache, page_table, kv_lens, sinks, scale,
+                         max_q_len, max_kv_len, window, first_tokens=0, *, out=None, lse=None,
+                         stream=None, want_lse=True):
+    """`prefill_paged` with a sliding window (see `prefill_window`; positions
+    count from the request's first cached key)."""
+    dev = q.device
+    _want(q, "q", torch.bfloat16, 3)
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
+    total, hq, d = q.shape
+    _paged_args(dev, cu_seqlens_q.numel() - 1, page_table, kv_lens, k_cache, v_cache)
+    _want(sinks, "sinks", torch.float32, 1, dev)
+    _shape(sinks, "sinks", (hq,))
+    num_pages, hkv, page, d2 = k_cache.shape
+    if d2 != d:
+        raise ValueError("k_cache and q disagree in head_dim")
+    window, first = _size(window, "window", 1), _size(first_tokens, "first_tokens")
+    with _at(dev, stream):
+        out, lse = _rows_out(q, out, lse, want_lse)
+        _check("sinkattn_prefill_paged_window", load().sinkattn_prefill_paged_window(
+            _ptr(q), _ptr(cu_seqlens_q), cu_seqlens_q.numel() - 1, total,
+            _size(max_q_len, "max_q_len"), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
+            page_table.shape[1], _ptr(kv_lens), num_pages, _size(max_kv_len, "max_kv_len"),
+            _ptr(sinks), float(scale), window, first, _ptr(out), _ptr(lse), hq, hkv, d, page,
+            _stream(None)))
+    return out, lse
+
+
+def _mass_args(q, k_cache, page_table, kv_lens, lse, mass, batch):
+    dev = q.device
+    _want(q, "q", torch.bfloat16, 3)
+    _paged_args(dev, batch, page_table, kv_lens, k_cache)
+    _want(lse, "lse", torch.float32, 2, dev)
+    _shape(lse, "lse", q.shape[:2])
+    _want(mass, "mass", torch.float32, 3, dev)
+    _shape(mass, "mass", (batch, k_cache.shape[1], mass.shape[2]))
+    if k_cache.shape[3] != q.shape[2]:
+        raise ValueError("k_cache and q disagree in head_dim")
+
+
+def decode_mass(q, k_cache, page_table, kv_lens, lse, scale, max_kv_len, mass, *, stream=None):
+    """Adds the attention weight that one new token per request gives to each
+    cached key: mass[b, g, j] += sum over the heads h of KV head g of
+    exp(scale * q_bh . k_gj - lse_bh), lse from `decode` on the same inputs.
+    mass [B, Hkv, at least max_kv_len] fp32, updated in place and returned."""
+    _mass_args(q, k_cache, page_table, kv_lens, lse, mass, q.shape[0])
+    batch, hq, d = q.shape
+    num_pages, hkv, page, _ = k_cache.shape
+    with _at(q.device, stream):
+        _check("sinkattn_decode_mass", load().sinkattn_decode_mass(
+            _ptr(q), _ptr(k_cache), _ptr(page_table), page_table.shape[1], _ptr(kv_lens),
+            _ptr(lse), float(scale), _ptr(mass), mass.shape[2], batch, hq, hkv, d, page, num_pages,
+            _size(max_kv_len, "max_kv_len"), _stream(None)))
+    return mass
+
+
+def prefill_mass(q, cu_seqlens_q, k_cache, page_table, kv_lens, lse, scale, max_q_len, max_kv_len,
+                 mass, *, stream=None):
+    """`decode_mass` for ragged rows: the queries of `prefill_paged` (or the
+    last few of each prompt, so that only those vote), each row counting the
+    keys up to its own position."""
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, q.device)
+    batch = cu_seqlens_q.numel() - 1
+    _mass_args(q, k_cache, page_table, kv_lens, lse, mass, batch)
+    total, hq, d = q.shape
+    num_pages, hkv, page, _ = k_cache.shape
+    with _at(q.device, stream):
+        _check("sinkattn_prefill_mass", load().sinkattn_prefill_mass(
+            _ptr(q), _ptr(cu_seqlens_q), batch, total, _size(max_q_len, "max_q_len"),
+            _ptr(k_cache), _ptr(page_table), page_table.shape[1], _ptr(kv_lens), num_pages,
+            _size(max_kv_len, "max_kv_len"), _ptr(lse), float(scale), _ptr(mass), mass.shape[2],
+            hq, hkv, d, page, _stream(None)))
+    return mass
+
+
+def evict(k_cache, v_cache, page_table, kv_lens, mass, budget, max_kv_len, *, first_tokens=0,
+          recent=0, dst_page_table=None, dst_mass=None, new_kv_lens=None, kept=None, stream=None):
+    """Cuts each request to `budget` keys: every KV head keeps its first
+    `first_tokens`, its last `recent` and the heaviest others by `mass` (ties:
+    the lower index), in order, moved to the request's first slots -- in place,
+    or to the pages of dst_page_table [B, pages] and to dst_mass
+    [B, Hkv, budget or more].  Returns (new_kv_lens [B] int32,
+    kept [B, Hkv, budget] int32: former indices, -1 past the new length);
+    a request that cannot be moved (lengths or pages out of range) is left
+    alone with new length -1."""
+    dev = k_cache.device
+    batch = kv_lens.shape[0]
+    _paged_args(dev, batch, page_table, kv_lens, k_cache, v_cache)
+    num_pages, hkv, page, d = k_cache.shape
+    _want(mass, "mass", torch.float32, 3, dev)
+    _shape(mass, "mass", (batch, hkv, mass.shape[2]))
+    if dst_page_table is not None:
+        _want(dst_page_table, "dst_page_table", torch.int32, 2, dev)
+        _shape(dst_page_table, "dst_page_table", (batch, dst_page_table.shape[1]))
+    if dst_mass is not None:
+        _want(dst_mass, "dst_mass", torch.float32, 3, dev)
+        _shape(dst_mass, "dst_mass", (batch, hkv, dst_mass.shape[2]))
+    budget = _size(budget, "budget", 1)
+    first, recent = _size(first_tokens, "first_tokens"), _size(recent, "recent")
+    with _at(dev, stream):
+        if new_kv_lens is None:
+            new_kv_lens = torch.empty(batch, dtype=torch.int32, device=dev)
+        else:
+            _want(new_kv_lens, "new_kv_lens", torch.int32, 1, dev)
+            _shape(new_kv_lens, "new_kv_lens", (batch,))
+        if kept is None:
+            kept = torch.empty(batch, hkv, budget, dtype=torch.int32, device=dev)
+        else:
+            _want(kept, "kept", torch.int32, 3, dev)
+            _shape(kept, "kept", (batch, hkv, budget))
+        _check("sinkattn_evict", load().sinkattn_evict(
+            _ptr(k_cache), _ptr(v_cache), _ptr(page_table), page_table.shape[1], _ptr(kv_lens),
+            _ptr(mass), mass.shape[2], budget, first, recent, _ptr(dst_page_table),
+            0 if dst_page_table is None else dst_page_table.shape[1], _ptr(dst_mass),
+            0 if dst_mass is None else dst_mass.shape[2], _ptr(new_kv_lens), _ptr(kept), batch,
+            hkv, d, page, num_pages, _size(max_kv_len, "max_kv_len"), _stream(None)))
+    return new_kv_lens, kept

@@ -76,6 +76,9 @@ struct DecodeParams {
   int head_blocks;              // CTAs per (request, KV head, chunk) = ceil(rows / (8 col_blocks))
   int num_pages, num_splits, pages_per_chunk;
   int sorted_dispatch;          // one chunk per request: requests heaviest first
+  // Sliding window (plain decode only; 0: none): the token sees the keys
+  // j >= kv_len - window and j < first_tokens.
+  int window, first_tokens, max_kv_len;
 };
 
 // Column blocks per CTA for q_len * group query rows per KV head.
@@ -121,6 +124,66 @@ cudaError_t launch_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,
                            const CUtensorMap &vmap, const PrefillParams &p,
                            cudaStream_t stream, bool programmatic);
 
+// --------------------------------------------------------- windowed prefill
+struct WindowPrefillParams {
+  const int32_t *cu_seqlens_q;   // [n+1]; ragged K/V share it
+  const int32_t *page_table;     // paged K/V: [n][max_pages_per_seq], null: ragged K/V [Tq][Hkv][64]
+  const int32_t *kv_lens;        // paged K/V: [n]
+  const float *sinks;            // [Hq]
+  uint16_t *out;                 // bf16 [Tq][Hq][64]
+  float *lse;                    // [Tq][Hq] or null
+  float scale_log2;              // not 0: masked scores are infinities that it keeps infinite
+  int num_seqs, total_q, max_q_len, max_kv_len;
+  int num_qo_heads, num_kv_heads, group;
+  int max_pages_per_seq, num_pages;
+  int window, first_tokens;      // both <= max_kv_len, window >= 1
+  int tile_tokens;               // tokens per query tile = 128 / group
+  int num_q_tiles;               // query tiles of the longest request
+};
+
+cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,
+                                  const CUtensorMap &vmap, const WindowPrefillParams &p,
+                                  cudaStream_t stream);
+
+// ---------------------------------------------------------- attention weight
+struct MassParams {
+  const uint16_t *q;             // bf16 [Tq][Hq][64]
+  const int32_t *cu_seqlens_q;   // [n+1] (prefill form)
+  const uint16_t *k_cache;       // bf16 [num_pages][Hkv][16][64]
+  const int32_t *page_table;     // [n][max_pages_per_seq]
+  const int32_t *kv_lens;        // [n]
+  const float *lse;              // [Tq][Hq]
+  float *mass;                   // [n][Hkv][mass_stride]
+  float scale_log2;              // not 0, as above
+  int num_seqs, total_q, max_q_len, max_kv_len, mass_stride;
+  int num_qo_heads, num_kv_heads, group;
+  int max_pages_per_seq, num_pages;
+  int num_chunks, pages_per_chunk;   // decode form: CTAs per (request, KV head)
+  int tile_tokens;                   // prefill form: tokens per query tile = 128 / group
+};
+
+int decode_mass_warps();         // pages a CTA of the decode form works on at a time
+cudaError_t launch_decode_mass(const MassParams &p, cudaStream_t stream);
+cudaError_t launch_prefill_mass(const CUtensorMap &qmap, const CUtensorMap &kmap,
+                                const MassParams &p, cudaStream_t stream);
+
+// ----------------------------------------------------------------- eviction
+struct EvictParams {
+  uint16_t *k_cache, *v_cache;   // bf16 [num_pages][Hkv][16][64]
+  const int32_t *page_table;     // [B][max_pages_per_seq]
+  const int32_t *kv_lens;        // [B]
+  const float *mass;             // [B][Hkv][mass_stride]
+  const int32_t *dst_page_table; // [B][dst_max_pages] (page_table itself: in place)
+  float *dst_mass;               // [B][Hkv][dst_mass_stride] (mass itself: in place)
+  int32_t *new_kv_lens;          // [B]
+  int32_t *kept;                 // [B][Hkv][budget]
+  int batch, num_kv_heads, num_pages, max_kv_len;
+  int max_pages_per_seq, dst_max_pages, mass_stride, dst_mass_stride;
+  int budget, first_tokens, recent;
+};
+
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
+
 // --------------------------------------------------------------- prologue
 struct PrologueParams {
   const uint16_t *qkv;           // bf16 [T][(Hq + 2 Hkv) * 64], q heads, then k, then v
@@ -144,12 +207,14 @@ cudaError_t launch_prologue(const PrologueParams &p, cudaStream_t stream);
 // the launch.  launch_flags is one of SINKATTN_LAUNCH_*.  With zero_counters,
 // a plan of more than one split first clears the workspace's merge counters
 // on the stream (cudaMemsetAsync, queued only after every check has passed);
-// a single-split plan touches no workspace at all.
+// a single-split plan touches no workspace at all.  window > 0 (q_len 1, no
+// mask) is the sliding-window form.
 int decode_entry(const void *q, const void *k_cache, const void *v_cache,
                  const int32_t *page_table, int max_pages_per_seq, const int32_t *kv_lens,
                  const uint64_t *tree_mask, const float *sinks, float scale, void *out, float *lse,
                  int batch, int q_len, int num_qo_heads, int num_kv_heads, int head_dim,
                  int page_size, int num_pages, int max_kv_len, int num_splits, void *workspace,
-                 size_t workspace_bytes, int launch_flags, bool zero_counters, void *stream);
+                 size_t workspace_bytes, int launch_flags, bool zero_counters, void *stream,
+                 int window = 0, int first_tokens = 0);
 
 }  // namespace sa

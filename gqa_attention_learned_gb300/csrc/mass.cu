@@ -1,0 +1,419 @@
+// Attention weight drawn by each cached key ("mass"):
+//
+//   mass[b][g][j] += sum over the call's rows (token i, head h of KV head g)
+//                    that see key j of e^(scale q_ih . k_gj - lse_ih),
+//
+// the column sums of the attention's own weights: lse is what decode /
+// prefill returned for the row, so one pass over K suffices and no softmax
+// state is carried.  Exponents, weights and sums are fp32.  Every sum has a
+// fixed order (no atomics), so equal inputs give equal bits.
+//
+// decode_mass (one token per request) reads 128 bytes of K per (key, KV head)
+// and is bound by HBM.  Each warp takes whole 16-key pages: S^T[16 keys x 8
+// heads] = K Q^T by mma.sync.m16n8k16, K straight from global memory into the
+// A fragments.  A dot product does not care about the order of its terms, so
+// the k index of the MMA is permuted to make each lane's share of a K row two
+// 16-byte pieces: no shared memory, no copies to wait for, several pages in
+// flight per warp.
+//
+// prefill_mass (ragged rows at the end of the keys) is bound by its
+// exponentials, one per (row, key).  A CTA owns 128 keys of one KV head and
+// streams the query rows that see them, 128 (token, head) rows at a time, past
+// the resident K tile: S^T[128 keys x 128 rows] by tcgen05 into tensor memory,
+// one thread per key adds its row of weights in registers.
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+#include <cmath>
+
+namespace sa {
+namespace {
+
+__host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ bool bad_request(const MassParams &p, int kv_len) {
+  return kv_len < 0 || kv_len > p.max_kv_len || kv_len > p.mass_stride ||
+         cdiv(kv_len, kPageSize) > p.max_pages_per_seq;
+}
+
+// NaN over the whole mass row of a request whose arguments are out of range.
+__device__ __forceinline__ void poison_row(const MassParams &p, float *row) {
+  for (int j = threadIdx.x; j < p.mass_stride; j += blockDim.x) row[j] = NAN;
+}
+
+// ------------------------------------------------------------------ decode
+constexpr int kDecodeWarps = 8;
+constexpr int kDecodeAhead = 4;        // pages in flight per warp
+
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// A 16-key page as A fragments: row g and row g + 8 of the page, 16-byte
+// pieces t and t + 4 of each.
+struct PageFrag {
+  uint4 lo0, lo1, hi0, hi1;
+  float before;                       // the mass this lane adds to
+};
+
+__global__ void __launch_bounds__(kDecodeWarps * 32, 2)
+decode_mass_kernel(const MassParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int chunk = static_cast<int>(blockIdx.x % p.num_chunks);
+  const int unit = static_cast<int>(blockIdx.x / p.num_chunks);
+  const int kvh = unit % p.num_kv_heads, b = unit / p.num_kv_heads;
+  grid_dependency_wait();
+  const int kv_len = p.kv_lens[b];
+  float *mass = p.mass + static_cast<size_t>(unit) * p.mass_stride;
+  if (bad_request(p, kv_len)) {
+    if (chunk == 0) poison_row(p, mass);
+    return;
+  }
+  const int npages = cdiv(kv_len, kPageSize);
+  const int first = chunk * p.pages_per_chunk + warp;
+  const int end = min(npages, (chunk + 1) * p.pages_per_chunk);
+  const int n_my = first < end ? cdiv(end - first, kDecodeWarps) : 0;
+  if (n_my == 0) return;                                 // warp-uniform; no barriers below
+  const int32_t *table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
+
+  auto page_id = [&](int i) -> int {                     // page i of this warp, -1: none or bad
+    if (i >= n_my) return -1;
+    const int id = __ldg(table + first + i * kDecodeWarps);
+    return id < p.num_pages ? id : -1;
+  };
+  // lane 0 of a quad adds to key g of a page, lane 1 to key g + 8
+  const int my_slot = g + (t == 1 ? 8 : 0);
+  auto my_key = [&](int i) { return (first + i * kDecodeWarps) * kPageSize + my_slot; };
+  auto fetch = [&](int i, int id, PageFrag &f) {
+    if (i < n_my && t < 2 && my_key(i) < kv_len) f.before = mass[my_key(i)];
+    if (id < 0) return;
+    const uint4 *base = reinterpret_cast<const uint4 *>(
+        p.k_cache + (static_cast<size_t>(id) * p.num_kv_heads + kvh) * kPageSize * kHeadDim);
+    f.lo0 = ld_stream(base + g * 8 + t);
+    f.lo1 = ld_stream(base + g * 8 + t + 4);
+    f.hi0 = ld_stream(base + (g + 8) * 8 + t);
+    f.hi1 = ld_stream(base + (g + 8) * 8 + t + 4);
+  };
+  PageFrag f[kDecodeAhead];
+  int ids[kDecodeAhead];
+#pragma unroll
+  for (int u = 0; u < kDecodeAhead; ++u) {
+    ids[u] = page_id(u);
+    fetch(u, ids[u], f[u]);
+  }
+
+  // Q as B fragments with the same permuted k index: column g holds dims
+  // 8t..8t+7 and 32+8t..32+8t+7 of its head
+  const int blocks = cdiv(p.group, 8);
+  const int head0 = kvh * p.group;
+  const size_t row0 = static_cast<size_t>(b) * p.num_qo_heads + head0;
+  uint4 q0, q1;
+  float nl0, nl1;                     // -lse (base 2) of columns 2t, 2t+1
+  auto load_block = [&](int nb) {
+    const int col = nb * 8 + g;
+    const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (row0 + col) * kHeadDim);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    q0 = col < p.group ? __ldg(q + t) : zero;
+    q1 = col < p.group ? __ldg(q + t + 4) : zero;
+    auto neg = [&](int c) {
+      const float l = c < p.group ? __ldg(p.lse + row0 + c) : INFINITY;
+      return l == -INFINITY ? -INFINITY : -l * kLog2e;   // a row that sees nothing adds nothing
+    };
+    nl0 = neg(nb * 8 + 2 * t);
+    nl1 = neg(nb * 8 + 2 * t + 1);
+  };
+  if (blocks == 1) load_block(0);
+
+  for (int i0 = 0; i0 < n_my; i0 += kDecodeAhead) {
+#pragma unroll
+    for (int u = 0; u < kDecodeAhead; ++u) {
+      const int i = i0 + u;
+      if (i >= n_my) break;
+      float w_lo = 0.f, w_hi = 0.f;
+      for (int nb = 0; nb < blocks; ++nb) {
+        if (blocks > 1) load_block(nb);
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t a0[4] = {f[u].lo0.x, f[u].hi0.x, f[u].lo0.y, f[u].hi0.y};
+        const uint32_t a1[4] = {f[u].lo0.z, f[u].hi0.z, f[u].lo0.w, f[u].hi0.w};
+        const uint32_t a2[4] = {f[u].lo1.x, f[u].hi1.x, f[u].lo1.y, f[u].hi1.y};
+        const uint32_t a3[4] = {f[u].lo1.z, f[u].hi1.z, f[u].lo1.w, f[u].hi1.w};
+        mma_bf16_16816(s, a0, q0.x, q0.y);
+        mma_bf16_16816(s, a1, q0.z, q0.w);
+        mma_bf16_16816(s, a2, q1.x, q1.y);
+        mma_bf16_16816(s, a3, q1.z, q1.w);
+        w_lo += ex2(fmaf(s[0], p.scale_log2, nl0)) + ex2(fmaf(s[1], p.scale_log2, nl1));
+        w_hi += ex2(fmaf(s[2], p.scale_log2, nl0)) + ex2(fmaf(s[3], p.scale_log2, nl1));
+      }
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        w_lo += __shfl_xor_sync(0xffffffffu, w_lo, off);
+        w_hi += __shfl_xor_sync(0xffffffffu, w_hi, off);
+      }
+      if (t < 2 && my_key(i) < kv_len)
+        mass[my_key(i)] = ids[u] < 0 ? NAN : f[u].before + (t == 0 ? w_lo : w_hi);
+      ids[u] = page_id(i + kDecodeAhead);
+      fetch(i + kDecodeAhead, ids[u], f[u]);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- prefill
+constexpr int kKeys = 128;                       // keys per CTA
+constexpr int kRows = 128;                       // query rows per streamed tile
+constexpr int kQStages = 3;
+constexpr int kTileBytes = 128 * kHeadDim * 2;
+constexpr int kThreads = 192;
+constexpr int kLoadWarp = 4, kMmaWarp = 5;
+constexpr uint32_t kTmemCols = 256;              // two score buffers
+
+constexpr int kOffK = 0;
+constexpr int kOffQ = kTileBytes;
+constexpr int kOffL = kOffQ + kQStages * kTileBytes;
+constexpr int kOffBars = kOffL + kQStages * kRows * 4;
+constexpr int kSmemBytes = kOffBars + 256 + 1024;
+
+struct Bars {
+  uint64_t k_full;
+  uint64_t q_full[kQStages], q_empty[kQStages];  // Q and -lse of a tile
+  uint64_t s_full[2], s_free[2];
+  uint32_t tmem_base;
+  int bad;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+constexpr uint32_t kIdesc = umma_idesc_bf16(128, 128, false, false);
+
+// Sum over 32 columns of 2^(s * scale + nl), s in r, nl in shared memory.
+template <int E = 0>
+__device__ __forceinline__ void add_chunk(uint32_t (&r)[32], const float4 *nl, uint64_t scale2,
+                                          uint64_t &acc0, uint64_t &acc1) {
+  if constexpr (E < 8) {
+    const float4 l = nl[E];
+    float x0, x1, x2, x3;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * E]), __uint_as_float(r[4 * E + 1])), scale2,
+                     f2_pack(l.x, l.y)), x0, x1);
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * E + 2]), __uint_as_float(r[4 * E + 3])), scale2,
+                     f2_pack(l.z, l.w)), x2, x3);
+    acc0 = f2_add(acc0, f2_pack(ex2(x0), ex2(x1)));
+    acc1 = f2_add(acc1, f2_pack(ex2(x2), ex2(x3)));
+    add_chunk<E + 1>(r, nl, scale2, acc0, acc1);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 2)
+prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
+                    const __grid_constant__ CUtensorMap kmap, const MassParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // ---- work item: (key tile, request, KV head); earlier tiles, which more
+  // rows see, first
+  const int per_tile = p.num_seqs * p.num_kv_heads;
+  const int kt = static_cast<int>(blockIdx.x / per_tile);
+  const int unit = static_cast<int>(blockIdx.x % per_tile);
+  const int kvh = unit % p.num_kv_heads, seq = unit / p.num_kv_heads;
+  const int q_start = p.cu_seqlens_q[seq], q_end = p.cu_seqlens_q[seq + 1];
+  const int q_len = q_end - q_start, kv_len = p.kv_lens[seq];
+  float *mass = p.mass + static_cast<size_t>(unit) * p.mass_stride;
+  if (bad_request(p, kv_len) || q_start < 0 || q_len < 0 || q_end > p.total_q ||
+      q_len > p.max_q_len || kv_len < q_len) {
+    if (kt == 0) poison_row(p, mass);
+    return;
+  }
+  const int key0 = kt * kKeys;
+  if (key0 >= kv_len || q_len == 0) return;
+  const int shift = kv_len - q_len;                      // position of the first row's token
+  const int i_first = max(0, key0 - shift);              // first token that sees a key of the tile
+  const int n_tiles = cdiv(q_len - i_first, p.tile_tokens);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  Bars &bar = *reinterpret_cast<Bars *>(smem + kOffBars);
+  auto sQ = [&](int s) { return smem + kOffQ + s * kTileBytes; };
+  auto sL = [&](int s) { return reinterpret_cast<float *>(smem + kOffL) + s * kRows; };
+
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bar.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      mbar_init(&bar.k_full, 1);
+      for (int s = 0; s < kQStages; ++s) {
+        mbar_init(&bar.q_full[s], 1 + 32);
+        mbar_init(&bar.q_empty[s], 1 + 128);             // the MMAs, and the readers of -lse
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&bar.s_full[s], 1);
+        mbar_init(&bar.s_free[s], 128);
+      }
+      bar.bad = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    // K: lanes 0..7 each own one 16-key page of the tile
+    const int pg = key0 / kPageSize + lane;
+    int id = -1;
+    if (lane < kKeys / kPageSize && pg < cdiv(kv_len, kPageSize)) {
+      id = p.page_table[static_cast<size_t>(seq) * p.max_pages_per_seq + pg];
+      if (id < 0 || id >= p.num_pages) {
+        atomicOr(&bar.bad, 1 << lane);
+        id = -1;
+      }
+    }
+    const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
+    if (lane == 0) mbar_arrive_expect_tx(&bar.k_full, __popc(mask) * kPageSize * kHeadDim * 2);
+    __syncwarp();
+    if (id >= 0)
+      tma_load_3d(smem + kOffK + lane * kPageSize * kHeadDim * 2, &kmap, &bar.k_full, 0,
+                  kvh * kPageSize, id);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem_base;
+
+  if (warp == kLoadWarp) {
+    // ----------------------------------------------- query tiles and -lse
+    for (int j = 0; j < n_tiles; ++j) {
+      const int s = j % kQStages;
+      if (j >= kQStages && !__all_sync(0xffffffffu, mbar_wait(&bar.q_empty[s], ((j / kQStages) + 1) & 1))) {
+        if (lane == 0) atomicOr(&bar.bad, 1 << 30);
+        break;
+      }
+      const int tok0 = q_start + i_first + j * p.tile_tokens;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar.q_full[s], p.tile_tokens * p.group * kHeadDim * 2);
+        tma_load_3d(sQ(s), &qmap, &bar.q_full[s], 0, kvh * p.group, tok0);
+      }
+      const int rows = min(p.tile_tokens, q_end - tok0) * p.group;
+      for (int r = lane; r < kRows; r += 32) {
+        float l = INFINITY;                              // columns past the rows add nothing
+        if (r < rows) {
+          const int tk = r / p.group;
+          l = __ldg(p.lse + static_cast<size_t>(tok0 + tk) * p.num_qo_heads + kvh * p.group +
+                    (r - tk * p.group));
+        }
+        sL(s)[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+      }
+      mbar_arrive(&bar.q_full[s]);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------ S^T = K Q^T (one thread)
+    const uint64_t dk = umma_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
+    bool ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_full, 0));
+    for (int j = 0; ok && j < n_tiles; ++j) {
+      const int s = j % kQStages, e = j & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full[s], (j / kQStages) & 1)) ||
+          (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar.s_free[e], ((j / 2) + 1) & 1)))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t dq = umma_desc_sw128(smem_u32(sQ(s)), 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kHeadDim / 16; ++kk)
+          umma_ss(tmem + e * kRows, dk + 2 * kk, dq + 2 * kk, kIdesc, kk > 0);
+        umma_commit(&bar.s_full[e]);
+        umma_commit(&bar.q_empty[s]);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) atomicOr(&bar.bad, 1 << 30);
+  } else {
+    // ------------------------------------------------ one thread per key
+    const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int key = key0 + threadIdx.x;
+    const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
+    uint64_t acc0 = 0, acc1 = 0;                         // (+0.f, +0.f)
+    bool ok = true;
+    uint32_t x[4][32];
+    for (int j = 0; j < n_tiles; ++j) {
+      const int s = j % kQStages, e = j & 1;
+      const int tok = i_first + j * p.tile_tokens;
+      const int rows = min(p.tile_tokens, q_len - tok) * p.group;
+      // columns [from, rows) see this key
+      const int from = max(0, key - shift - tok) * p.group;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[e], (j / 2) & 1))) {
+        ok = false;
+        break;
+      }
+      // the scores wait for Q, but -lse arrives with the loading warp
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full[s], (j / kQStages) & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(trow + e * kRows + 32 * c, x[c]);
+      tmem_ld_wait32(x[0]);
+#pragma unroll
+      for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
+      tc_fence_before();
+      mbar_arrive(&bar.s_free[e]);
+      if (__any_sync(0xffffffffu, from > 0 || rows < kRows)) {
+        const uint32_t masked = p.scale_log2 >= 0.f ? 0xff800000u : 0x7f800000u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k < from || 32 * c + k >= rows) x[c][k] = masked;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        add_chunk(x[c], reinterpret_cast<const float4 *>(sL(s) + 32 * c), scale2, acc0, acc1);
+      mbar_arrive(&bar.q_empty[s]);
+    }
+    if (!ok) atomicOr(&bar.bad, 1 << 30);
+    tc_fence_before();
+    __syncthreads();
+    float a, b, c, d;
+    f2_unpack(acc0, a, b);
+    f2_unpack(acc1, c, d);
+    // a key on a page outside the pool, or a wait that ran out: NaN
+    const bool failed = (bar.bad >> (threadIdx.x / kPageSize) & 1) || (bar.bad >> 30);
+    if (key < kv_len) mass[key] = failed ? NAN : mass[key] + ((a + b) + (c + d));
+    return;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_mass(const MassParams &p, cudaStream_t stream) {
+  const unsigned long long ctas =
+      static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads * p.num_chunks;
+  if (ctas == 0) return cudaSuccess;
+  if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+  return launch_kernel(decode_mass_kernel, static_cast<unsigned>(ctas), kDecodeWarps * 32, 0,
+                       stream, true, p);
+}
+
+int decode_mass_warps() { return kDecodeWarps; }
+
+cudaError_t launch_prefill_mass(const CUtensorMap &qmap, const CUtensorMap &kmap,
+                                const MassParams &p, cudaStream_t stream) {
+  static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
+  const unsigned long long ctas = static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads *
+                                  cdiv(p.max_kv_len, kKeys);
+  if (ctas == 0) return cudaSuccess;
+  if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+  cudaError_t err = set_smem_once<prefill_mass_kernel>(kSmemBytes);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(prefill_mass_kernel, static_cast<unsigned>(ctas), kThreads, kSmemBytes,
+                       stream, false, qmap, kmap, p);
+}
+
+}  // namespace sa

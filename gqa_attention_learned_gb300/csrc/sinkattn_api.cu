@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cstdio>
 #include <atomic>
 #include <cmath>
@@ -108,6 +109,7 @@ bool encode_map(CUtensorMap *map, const void *base, unsigned long long d1, unsig
 
 constexpr int kPrefillTile = 128;     // query rows per prefill CTA
 constexpr int kPrefillKvTile = 128;   // keys per prefill K/V tile
+constexpr int kMassPagesPerWarp = 8;  // decode mass: pages a warp takes, one CTA's share
 
 struct DecodePlan {
   int num_splits = 1;
@@ -161,14 +163,21 @@ void decode_blocks_for(int batch, int q_len, int group, int num_kv_heads, int nu
 // waves of the GPU, chunks of at least kMinPagesPerChunk pages; an explicit
 // count is honoured up to one page per chunk.
 DecodePlan plan_decode(int batch, int q_len, int num_qo_heads, int num_kv_heads, int max_kv_len,
-                       int num_sms, int requested) {
+                       int num_sms, int requested, int window = 0, int first_tokens = 0) {
   DecodePlan plan;
   const int group = num_qo_heads / num_kv_heads;
   int col_blocks, head_blocks;
   decode_blocks_for(batch, q_len, group, num_kv_heads, num_sms, &col_blocks, &head_blocks);
   plan.col_blocks = col_blocks;
   plan.head_blocks = head_blocks;
-  const int max_pages = std::max(1, ceil_div(max_kv_len, kPageSize));
+  int max_pages = std::max(1, ceil_div(max_kv_len, kPageSize));
+  if (window > 0) {
+    // pages with a visible key: the first tokens', and the window's, which
+    // may start on any slot of its first page
+    const long long seen = static_cast<long long>(ceil_div(first_tokens, kPageSize)) +
+                           ceil_div(static_cast<long long>(window) + kPageSize - 1, kPageSize);
+    max_pages = static_cast<int>(std::min<long long>(max_pages, seen));
+  }
   if (requested == 0 &&
       verify_on_tensor_cores(batch, q_len, num_qo_heads, num_kv_heads, max_pages, num_sms)) {
     plan.tensor_cores = 1;
@@ -242,7 +251,7 @@ const char *sinkattn_status_string(int status) {
   }
 }
 
-int sinkattn_version(void) { return 400; }   // 0.4.0: launch mode per call
+int sinkattn_version(void) { return 500; }   // 0.5.0: windowed attention, attention mass, eviction
 
 int sinkattn_set_programmatic_launch(int enable) {
   return sa::g_programmatic.exchange(enable != 0 ? 1 : 0);
@@ -307,7 +316,8 @@ int decode_entry(const void *q, const void *k_cache, const void *v_cache,
                  const uint64_t *tree_mask, const float *sinks, float scale, void *out, float *lse,
                  int batch, int q_len, int num_qo_heads, int num_kv_heads, int head_dim,
                  int page_size, int num_pages, int max_kv_len, int num_splits, void *workspace,
-                 size_t workspace_bytes, int launch_flags, bool zero_counters, void *stream) {
+                 size_t workspace_bytes, int launch_flags, bool zero_counters, void *stream,
+                 int window, int first_tokens) {
   if (launch_flags != SINKATTN_LAUNCH_DEFAULT && launch_flags != SINKATTN_LAUNCH_PLAIN &&
       launch_flags != SINKATTN_LAUNCH_PROGRAMMATIC)
     return SINKATTN_INVALID_ARGUMENT;
@@ -336,7 +346,7 @@ int decode_entry(const void *q, const void *k_cache, const void *v_cache,
   const int sms = device_sm_count();
   if (sms == 0) return fail_msg("no CUDA device (SM count query failed)");
   const DecodePlan plan = plan_decode(batch, q_len, num_qo_heads, num_kv_heads, max_kv_len, sms,
-                                      num_splits);
+                                      num_splits, window, first_tokens);
   const int col_blocks = plan.col_blocks, head_blocks = plan.head_blocks;
   if (plan.num_splits > 1) {
     if (!workspace || workspace_bytes < plan.workspace_bytes) return SINKATTN_WORKSPACE_TOO_SMALL;
@@ -413,6 +423,9 @@ int decode_entry(const void *q, const void *k_cache, const void *v_cache,
   p.num_splits = plan.num_splits;
   p.pages_per_chunk = plan.pages_per_chunk;
   p.sorted_dispatch = plan.sorted_dispatch;
+  p.window = std::min(window, std::max(max_kv_len, 1));       // 0 stays 0: no window
+  p.first_tokens = std::min(first_tokens, max_kv_len);
+  p.max_kv_len = max_kv_len;
   if (zero_counters && plan.num_splits > 1) {
     // the counters are the workspace's first plan.counters_bytes bytes, all
     // within workspace_bytes (checked above)
@@ -621,6 +634,275 @@ int sinkattn_qkv_prologue(const void *qkv, const void *bias, const int32_t *posi
   p.num_pages = num_pages;
   p.interleaved = rope_style == SINKATTN_ROPE_INTERLEAVED;
   return cuda_status(sa::launch_prologue(p, static_cast<cudaStream_t>(stream)), "prologue launch");
+}
+
+
+int sinkattn_decode_window_plan(int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                                int page_size, int max_kv_len, int window, int first_tokens,
+                                int num_sms, int *num_splits, size_t *workspace_bytes) {
+  if (!num_splits || !workspace_bytes) return SINKATTN_INVALID_ARGUMENT;
+  if (head_dim != kHeadDim || page_size != kPageSize) return SINKATTN_UNSUPPORTED;
+  if (batch < 0 || num_qo_heads <= 0 || num_kv_heads <= 0 || max_kv_len < 0 || *num_splits < 0 ||
+      num_sms < 0 || num_qo_heads % num_kv_heads || window < 1 || first_tokens < 0)
+    return SINKATTN_INVALID_ARGUMENT;
+  if (num_sms == 0) {
+    num_sms = device_sm_count();
+    if (num_sms == 0) return fail_msg("no CUDA device to plan for");
+  }
+  const DecodePlan plan = plan_decode(batch, 1, num_qo_heads, num_kv_heads, max_kv_len, num_sms,
+                                      *num_splits, window, first_tokens);
+  *num_splits = plan.num_splits;
+  *workspace_bytes = plan.workspace_bytes;
+  return SINKATTN_OK;
+}
+
+int sinkattn_decode_window(const void *q, const void *k_cache, const void *v_cache,
+                           const int32_t *page_table, int max_pages_per_seq,
+                           const int32_t *kv_lens, const float *sinks, float scale, int window,
+                           int first_tokens, void *out, float *lse, int batch, int num_qo_heads,
+                           int num_kv_heads, int head_dim, int page_size, int num_pages,
+                           int max_kv_len, int num_splits, void *workspace,
+                           size_t workspace_bytes, int launch_flags, void *stream) {
+  if (window < 1 || first_tokens < 0) return SINKATTN_INVALID_ARGUMENT;
+  return sa::decode_entry(q, k_cache, v_cache, page_table, max_pages_per_seq, kv_lens, nullptr,
+                         sinks, scale, out, lse, batch, 1, num_qo_heads, num_kv_heads, head_dim,
+                         page_size, num_pages, max_kv_len, num_splits, workspace, workspace_bytes,
+                         launch_flags, false, stream, window, first_tokens);
+}
+
+}  // extern "C"
+
+namespace {
+
+// scale in base 2 for the kernels that mask a score before they scale it: an
+// infinity has to stay one, so a scale of 0 becomes the smallest normal
+// number (every finite score then still scales to nothing).
+float masked_scale_log2(float scale) { return scale == 0.f ? FLT_MIN : scale * sa::kLog2e; }
+
+// Both forms of windowed prefill; page_table null: ragged K/V.
+int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seqs, int total_q,
+                         int max_q_len, const void *k, const void *v, bool paged,
+                         const int32_t *page_table, int max_pages_per_seq, const int32_t *kv_lens,
+                         int num_pages, int max_kv_len, const float *sinks, float scale,
+                         int window, int first_tokens, void *out, float *lse, int num_qo_heads,
+                         int num_kv_heads, int head_dim, int page_size, void *stream) {
+  if (head_dim != kHeadDim || page_size != kPageSize) return SINKATTN_UNSUPPORTED;
+  if (num_seqs < 0 || total_q < 0 || max_q_len < 0 || max_kv_len < 0 || num_qo_heads <= 0 ||
+      num_kv_heads <= 0 || num_qo_heads % num_kv_heads || window < 1 || first_tokens < 0 ||
+      !std::isfinite(scale) || (paged && (num_pages <= 0 || max_pages_per_seq <= 0)))
+    return SINKATTN_INVALID_ARGUMENT;
+  const int group = num_qo_heads / num_kv_heads;
+  if (group > kPrefillTile) return SINKATTN_UNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return SINKATTN_OK;
+  if (!q || !k || !v || !cu_seqlens_q || !sinks || !out || (paged && (!page_table || !kv_lens)))
+    return SINKATTN_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(sinks, 4) || !aligned(page_table, 4) ||
+      !aligned(kv_lens, 4) || !aligned(lse, 4))
+    return SINKATTN_INVALID_ARGUMENT;
+  const int tile_tokens = kPrefillTile / group;
+  CUtensorMap qmap, kmap, vmap;
+  const unsigned long long d1 =
+      static_cast<unsigned long long>(num_kv_heads) * (paged ? kPageSize : 1);
+  const unsigned long long d2 = paged ? num_pages : total_q;
+  const unsigned b1 = paged ? kPageSize : 1, b2 = paged ? 1 : kPageSize;
+  if (!encode_map(&qmap, q, num_qo_heads, total_q, group, tile_tokens) ||
+      !encode_map(&kmap, k, d1, d2, b1, b2) || !encode_map(&vmap, v, d1, d2, b1, b2))
+    return fail_msg("cuTensorMapEncodeTiled failed");
+  sa::WindowPrefillParams p{};
+  p.cu_seqlens_q = cu_seqlens_q;
+  p.page_table = paged ? page_table : nullptr;
+  p.kv_lens = kv_lens;
+  p.sinks = sinks;
+  p.out = static_cast<uint16_t *>(out);
+  p.lse = lse;
+  p.scale_log2 = masked_scale_log2(scale);
+  p.num_seqs = num_seqs;
+  p.total_q = total_q;
+  p.max_q_len = max_q_len;
+  p.max_kv_len = max_kv_len;
+  p.num_qo_heads = num_qo_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = group;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.num_pages = num_pages;
+  p.window = std::min(window, std::max(max_kv_len, 1));
+  p.first_tokens = std::min(first_tokens, max_kv_len);
+  p.tile_tokens = tile_tokens;
+  p.num_q_tiles = ceil_div(max_q_len, tile_tokens);
+  return cuda_status(sa::launch_window_prefill(qmap, kmap, vmap, p, static_cast<cudaStream_t>(stream)),
+                     "windowed prefill launch");
+}
+
+// Checks shared by both forms of attention mass; fills the parameters.
+int mass_params(sa::MassParams &p, const void *q, const void *k_cache, const int32_t *page_table,
+                int max_pages_per_seq, const int32_t *kv_lens, const float *lse, float scale,
+                float *mass, int mass_stride, int num_seqs, int total_q, int num_qo_heads,
+                int num_kv_heads, int head_dim, int page_size, int num_pages, int max_kv_len) {
+  if (head_dim != kHeadDim || page_size != kPageSize) return SINKATTN_UNSUPPORTED;
+  if (num_seqs < 0 || total_q < 0 || num_qo_heads <= 0 || num_kv_heads <= 0 ||
+      num_qo_heads % num_kv_heads || max_kv_len < 0 || num_pages <= 0 || max_pages_per_seq <= 0 ||
+      mass_stride < max_kv_len || !std::isfinite(scale))
+    return SINKATTN_INVALID_ARGUMENT;
+  if (num_seqs > 0 && total_q > 0) {
+    if (!q || !k_cache || !page_table || !kv_lens || !lse || !mass) return SINKATTN_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(page_table, 4) ||
+        !aligned(kv_lens, 4) || !aligned(lse, 4) || !aligned(mass, 4))
+      return SINKATTN_INVALID_ARGUMENT;
+  }
+  p.q = static_cast<const uint16_t *>(q);
+  p.k_cache = static_cast<const uint16_t *>(k_cache);
+  p.page_table = page_table;
+  p.kv_lens = kv_lens;
+  p.lse = lse;
+  p.mass = mass;
+  p.mass_stride = mass_stride;
+  p.scale_log2 = masked_scale_log2(scale);
+  p.num_seqs = num_seqs;
+  p.total_q = total_q;
+  p.max_kv_len = max_kv_len;
+  p.num_qo_heads = num_qo_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_qo_heads / num_kv_heads;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.num_pages = num_pages;
+  return SINKATTN_OK;
+}
+
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sinkattn_prefill_window(const void *q, const void *k, const void *v,
+                            const int32_t *cu_seqlens, int num_seqs, int total_tokens,
+                            int max_seqlen, const float *sinks, float scale, int window,
+                            int first_tokens, void *out, float *lse, int num_qo_heads,
+                            int num_kv_heads, int head_dim, void *stream) {
+  return window_prefill_entry(q, cu_seqlens, num_seqs, total_tokens, max_seqlen, k, v, false,
+                              nullptr, 0, nullptr, 0, max_seqlen, sinks, scale, window,
+                              first_tokens, out, lse, num_qo_heads, num_kv_heads, head_dim,
+                              kPageSize, stream);
+}
+
+int sinkattn_prefill_paged_window(const void *q, const int32_t *cu_seqlens_q, int num_seqs,
+                                  int total_q, int max_q_len, const void *k_cache,
+                                  const void *v_cache, const int32_t *page_table,
+                                  int max_pages_per_seq, const int32_t *kv_lens, int num_pages,
+                                  int max_kv_len, const float *sinks, float scale, int window,
+                                  int first_tokens, void *out, float *lse, int num_qo_heads,
+                                  int num_kv_heads, int head_dim, int page_size, void *stream) {
+  return window_prefill_entry(q, cu_seqlens_q, num_seqs, total_q, max_q_len, k_cache, v_cache,
+                              true, page_table, max_pages_per_seq, kv_lens, num_pages, max_kv_len,
+                              sinks, scale, window, first_tokens, out, lse, num_qo_heads,
+                              num_kv_heads, head_dim, page_size, stream);
+}
+
+int sinkattn_decode_mass(const void *q, const void *k_cache, const int32_t *page_table,
+                         int max_pages_per_seq, const int32_t *kv_lens, const float *lse,
+                         float scale, float *mass, int mass_stride, int batch, int num_qo_heads,
+                         int num_kv_heads, int head_dim, int page_size, int num_pages,
+                         int max_kv_len, void *stream) {
+  sa::MassParams p{};
+  const int st = mass_params(p, q, k_cache, page_table, max_pages_per_seq, kv_lens, lse, scale,
+                             mass, mass_stride, batch, batch, num_qo_heads, num_kv_heads, head_dim,
+                             page_size, num_pages, max_kv_len);
+  if (st != SINKATTN_OK || batch == 0) return st;
+  p.pages_per_chunk = kMassPagesPerWarp * sa::decode_mass_warps();
+  p.num_chunks = std::max(1, ceil_div(ceil_div(max_kv_len, kPageSize), p.pages_per_chunk));
+  return cuda_status(sa::launch_decode_mass(p, static_cast<cudaStream_t>(stream)),
+                     "decode mass launch");
+}
+
+int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_seqs, int total_q,
+                          int max_q_len, const void *k_cache, const int32_t *page_table,
+                          int max_pages_per_seq, const int32_t *kv_lens, int num_pages,
+                          int max_kv_len, const float *lse, float scale, float *mass,
+                          int mass_stride, int num_qo_heads, int num_kv_heads, int head_dim,
+                          int page_size, void *stream) {
+  sa::MassParams p{};
+  if (max_q_len < 0) return SINKATTN_INVALID_ARGUMENT;
+  const int st = mass_params(p, q, k_cache, page_table, max_pages_per_seq, kv_lens, lse, scale,
+                             mass, mass_stride, num_seqs, total_q, num_qo_heads, num_kv_heads,
+                             head_dim, page_size, num_pages, max_kv_len);
+  if (st != SINKATTN_OK) return st;
+  if (p.group > kPrefillTile) return SINKATTN_UNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return SINKATTN_OK;
+  if (!cu_seqlens_q || !aligned(cu_seqlens_q, 4)) return SINKATTN_INVALID_ARGUMENT;
+  p.cu_seqlens_q = cu_seqlens_q;
+  p.max_q_len = max_q_len;
+  p.tile_tokens = kPrefillTile / p.group;
+  CUtensorMap qmap, kmap;
+  if (!encode_map(&qmap, q, num_qo_heads, total_q, p.group, p.tile_tokens) ||
+      !encode_map(&kmap, k_cache, static_cast<unsigned long long>(num_kv_heads) * kPageSize,
+                  num_pages, kPageSize, 1))
+    return fail_msg("cuTensorMapEncodeTiled failed");
+  return cuda_status(sa::launch_prefill_mass(qmap, kmap, p, static_cast<cudaStream_t>(stream)),
+                     "prefill mass launch");
+}
+
+int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *page_table, int max_pages_per_seq,
+                   const int32_t *kv_lens, float *mass, int mass_stride, int budget,
+                   int first_tokens, int recent, const int32_t *dst_page_table,
+                   int dst_max_pages_per_seq, float *dst_mass, int dst_mass_stride,
+                   int32_t *new_kv_lens, int32_t *kept, int batch, int num_kv_heads, int head_dim,
+                   int page_size, int num_pages, int max_kv_len, void *stream) {
+  if (head_dim != kHeadDim || page_size != kPageSize) return SINKATTN_UNSUPPORTED;
+  if (!dst_page_table) {
+    dst_page_table = page_table;
+    dst_max_pages_per_seq = max_pages_per_seq;
+  }
+  if (!dst_mass) {
+    dst_mass = mass;
+    dst_mass_stride = mass_stride;
+  }
+  if (batch < 0 || num_kv_heads <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 ||
+      dst_max_pages_per_seq <= 0 || max_kv_len < 0 || mass_stride < max_kv_len || budget < 1 ||
+      dst_mass_stride < std::min(budget, max_kv_len) || first_tokens < 0 || recent < 0 ||
+      static_cast<long long>(first_tokens) + recent > budget)
+    return SINKATTN_INVALID_ARGUMENT;
+  if (batch == 0) return SINKATTN_OK;
+  if (!k_cache || !v_cache || !page_table || !kv_lens || !mass || !new_kv_lens || !kept)
+    return SINKATTN_INVALID_ARGUMENT;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(page_table, 4) ||
+      !aligned(kv_lens, 4) || !aligned(mass, 4) || !aligned(dst_page_table, 4) ||
+      !aligned(dst_mass, 4) || !aligned(new_kv_lens, 4) || !aligned(kept, 4))
+    return SINKATTN_INVALID_ARGUMENT;
+  // the old lengths are read until the end; mass is compacted either in place
+  // (same buffer, same rows) or into another buffer
+  const size_t lens_bytes = static_cast<size_t>(batch) * sizeof(int32_t);
+  const size_t rows = static_cast<size_t>(batch) * num_kv_heads;
+  if (overlap(kv_lens, lens_bytes, new_kv_lens, lens_bytes)) return SINKATTN_INVALID_ARGUMENT;
+  if (!(dst_mass == mass && dst_mass_stride == mass_stride) &&
+      overlap(mass, rows * mass_stride * sizeof(float), dst_mass,
+              rows * dst_mass_stride * sizeof(float)))
+    return SINKATTN_INVALID_ARGUMENT;
+  sa::EvictParams p{};
+  p.k_cache = static_cast<uint16_t *>(k_cache);
+  p.v_cache = static_cast<uint16_t *>(v_cache);
+  p.page_table = page_table;
+  p.kv_lens = kv_lens;
+  p.mass = mass;
+  p.dst_page_table = dst_page_table;
+  p.dst_mass = dst_mass;
+  p.new_kv_lens = new_kv_lens;
+  p.kept = kept;
+  p.batch = batch;
+  p.num_kv_heads = num_kv_heads;
+  p.num_pages = num_pages;
+  p.max_kv_len = max_kv_len;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.dst_max_pages = dst_max_pages_per_seq;
+  p.mass_stride = mass_stride;
+  p.dst_mass_stride = dst_mass_stride;
+  p.budget = budget;
+  p.first_tokens = first_tokens;
+  p.recent = recent;
+  return cuda_status(sa::launch_evict(p, static_cast<cudaStream_t>(stream)), "eviction launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,539 @@
+// Prefill with a sliding window and first tokens that stay visible (ragged, or
+// appended to a paged KV prefix), learned sinks, on the 5th-generation tensor
+// cores (tcgen05 + tensor memory).
+//
+// Mathematics: the row of the token at position i sees the keys
+//   { j <= i : j < first_tokens or j > i - window },
+// and its softmax starts at the head's sink (running max = sink, running sum
+// = 1) as in plain prefill.
+//
+// Tile: the 128 rows of a CTA are 128 / group tokens times the query heads of
+// one KV head, ordered (token, head).  With the heads in one tile its rows
+// span few positions, so a window of W needs W + 128 / group - 1 keys instead
+// of the W + 127 that 128 tokens of one head would (window 128, group 8: 143
+// keys against 255).
+// Keys: the keys that some row of the tile sees are the first tokens and one
+// run that ends at the tile's last position.  They are numbered through
+// ("slots"): boxes of 16 keys (a page, or 16 rows of ragged K/V) holding the
+// first tokens, then boxes from the run's start on; tiles take 8 boxes = 128
+// slots each, so the two parts share tiles and nothing between them is
+// copied or looked up.  The last tile's MMAs cover its own boxes only.
+// Rows see at most two slot ranges, kept as 32-bit masks per 32 slots; a warp
+// skips the chunks of 32 slots that none of its rows sees (no load, no
+// exponentials) and masks only those on an edge.
+// Warp roles, barriers and the softmax are those of plain prefill: warp 4
+// loads Q and K and issues S = Q K^T, warp 5 loads V and issues O += P V,
+// warps 0..3 run the online softmax, one thread per row, between them.
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+#include <cmath>
+
+namespace sa {
+namespace {
+
+constexpr int kBM = 128;                       // query rows per CTA
+constexpr int kBN = 128;                       // key slots per tile
+constexpr int kBox = 16;                       // keys per copied box
+constexpr int kBoxes = kBN / kBox;
+constexpr int kBoxBytes = kBox * kHeadDim * 2;
+constexpr int kKStages = 3, kVStages = 2;
+constexpr int kTileBytes = kBN * kHeadDim * 2;
+constexpr int kThreads = 192;
+constexpr int kQkWarp = 4, kPvWarp = 5;
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 192;
+constexpr float kRescaleLog2 = 8.f;     // lazy O rescale threshold (P < 256)
+
+constexpr int kOffQ = 0;
+constexpr int kOffK = kTileBytes;
+constexpr int kOffV = kOffK + kKStages * kTileBytes;
+constexpr int kOffBars = kOffV + kVStages * kTileBytes;
+constexpr int kSmemBytes = kOffBars + 256 + 1024;           // barriers + alignment slack
+static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full;     // S of the current tile is in tensor memory
+  uint64_t s_free;     // the softmax has read S
+  uint64_t p_full;     // P of the current tile is in tensor memory
+  uint64_t pv_done;    // the P V of the previous tile has finished
+  uint64_t o_final;
+  uint32_t tmem_base;
+  int bad;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+constexpr uint32_t kIdescPV = umma_idesc_bf16(128, 64, false, true);
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// Bits e of a 32-slot chunk starting at v0 with v0 + e < x.
+__device__ __forceinline__ uint32_t bits_below(int x, int v0) {
+  const int n = x - v0;
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// P = 2^(s * sl2 - mu) for 32 scores, packed as bf16 pairs into r[0..15];
+// the pair sums accumulate in `acc` (fp32x2).
+template <int E = 0>
+__device__ __forceinline__ void pack_chunk(uint32_t (&r)[32], uint64_t scale2, uint64_t negmu2,
+                                           uint64_t &acc) {
+  if constexpr (E < 16) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * E]), __uint_as_float(r[2 * E + 1])), scale2,
+                     negmu2),
+              x0, x1);
+    const float p0 = ex2(x0);
+    const float p1 = ex2(x1);
+    acc = f2_add(acc, f2_pack(p0, p1));
+    r[E] = pack_bf16(p0, p1);
+    pack_chunk<E + 1>(r, scale2, negmu2, acc);
+  }
+}
+
+// Slot ranges a row sees: [0, a) and [b, c).
+struct RowSlots {
+  int a, b, c;
+  __device__ __forceinline__ uint32_t mask(int v0) const {
+    return bits_below(c, v0) & (bits_below(a, v0) | ~bits_below(b, v0));
+  }
+};
+
+// One 128-slot tile of the online softmax for this thread's row.  Returns
+// false when a wait timed out.
+__device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, int chunks,
+                                             const RowSlots &see, float sl2, bool pos_scale,
+                                             uint32_t masked_raw, float &m, float &d,
+                                             uint32_t (&x)[4][32]) {
+  uint32_t mask[4];
+  bool live[4], edge[4];               // warp-uniform
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    mask[c] = see.mask(j * kBN + 32 * c);
+    live[c] = __any_sync(0xffffffffu, mask[c] != 0u);
+    edge[c] = __any_sync(0xffffffffu, mask[c] != 0xffffffffu);
+  }
+  if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full, j & 1))) return false;
+  tc_fence_after();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (live[c]) tmem_ld32(trow + kColS + 32 * c, x[c]);
+  tmem_ld_wait32(x[0]);
+#pragma unroll
+  for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
+  tc_fence_before();
+  mbar_arrive(&bar.s_free);
+  float mx = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (!live[c]) continue;
+    if (edge[c]) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!((mask[c] >> e) & 1u)) x[c][e] = masked_raw;
+    }
+    if (pos_scale) {
+      float r = __uint_as_float(x[c][0]);
+#pragma unroll
+      for (int e = 1; e < 31; e += 2)
+        r = fmax3(r, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+      mx = fmaxf(mx, fmaxf(r, __uint_as_float(x[c][31])) * sl2);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[c][e]) * sl2);
+    }
+  }
+  const float m_new = fmaxf(m, mx);
+  float alpha = 1.f;
+  bool rescale = false;
+  if (j == 0) {                        // O holds nothing yet: just re-base d
+    if (m_new != -INFINITY) {
+      d *= ex2(m - m_new);
+      m = m_new;
+    }
+  } else if (m_new > m + kRescaleLog2) {
+    alpha = ex2(m - m_new);
+    d *= alpha;
+    m = m_new;
+    rescale = true;
+  }
+  const float mu = m == -INFINITY ? 0.f : m;
+  const uint64_t scale2 = f2_pack(sl2, sl2), negmu2 = f2_pack(-mu, -mu);
+  uint64_t acc = 0;                                  // (+0.f, +0.f)
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (live[c]) {
+      uint64_t part = 0;
+      pack_chunk(x[c], scale2, negmu2, part);
+      acc = f2_add(acc, part);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[c][e] = 0u;
+    }
+  }
+  float s0, s1;
+  f2_unpack(acc, s0, s1);
+  d += s0 + s1;
+  // the previous tile's P V reads P and accumulates O: wait for it
+  if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (j - 1) & 1))) return false;
+  tc_fence_after();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c < chunks)                    // the P columns that this tile's P V reads
+      tmem_st16(trow + kColP + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[c][0]));
+  tmem_st_wait();
+  if (__any_sync(0xffffffffu, rescale)) {
+    // rare: scale this row's O (the previous P V has finished, the next one
+    // is issued only after p_full below)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) tmem_ld32(trow + kColO + 32 * h, x[h]);
+    tmem_ld_wait32(x[0]);
+    reg_tie32(x[1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[h][e] = __float_as_uint(__uint_as_float(x[h][e]) * alpha);
+    tmem_st16(trow + kColO, *reinterpret_cast<uint32_t(*)[16]>(&x[0][0]));
+    tmem_st16(trow + kColO + 16, *reinterpret_cast<uint32_t(*)[16]>(&x[0][16]));
+    tmem_st16(trow + kColO + 32, *reinterpret_cast<uint32_t(*)[16]>(&x[1][0]));
+    tmem_st16(trow + kColO + 48, *reinterpret_cast<uint32_t(*)[16]>(&x[1][16]));
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  mbar_arrive(&bar.p_full);
+  return true;
+}
+
+template <bool kPaged>
+__global__ void __launch_bounds__(kThreads, 2)
+window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, const WindowPrefillParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint4 nan4 = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+
+  // ---- work item: (query tile, request, KV head), later tiles (whose windows
+  // are full) first
+  const int per_tile = p.num_seqs * p.num_kv_heads;
+  const int qt = p.num_q_tiles - 1 - static_cast<int>(blockIdx.x / per_tile);
+  const int rem = static_cast<int>(blockIdx.x % per_tile);
+  const int kvh = rem % p.num_kv_heads, seq = rem / p.num_kv_heads;
+  const int q_start = p.cu_seqlens_q[seq];
+  const int q_end = p.cu_seqlens_q[seq + 1], q_len = q_end - q_start;
+  const int kv_len = kPaged ? p.kv_lens[seq] : q_len;
+  bool bad = q_start < 0 || q_len < 0 || q_end > p.total_q || q_len > p.max_q_len ||
+             kv_len < q_len || kv_len > p.max_kv_len;
+  if constexpr (kPaged) bad = bad || cdiv(kv_len, kPageSize) > p.max_pages_per_seq;
+  if (bad) {
+    // poison every row of this request that lies inside the buffers (once)
+    if (qt != 0 || q_start < 0 || q_start >= p.total_q) return;
+    const int stop = min(max(q_end, q_start), p.total_q);
+    for (long long idx = threadIdx.x; idx < static_cast<long long>(stop - q_start) * p.group;
+         idx += kThreads) {
+      const size_t row = static_cast<size_t>(q_start + idx / p.group) * p.num_qo_heads +
+                         kvh * p.group + idx % p.group;
+      uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kHeadDim);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dst[i] = nan4;
+      if (p.lse) p.lse[row] = NAN;
+    }
+    return;
+  }
+  const int i0 = qt * p.tile_tokens;
+  if (i0 >= q_len) return;
+  const int tokens = min(p.tile_tokens, q_len - i0);
+  const int rows = tokens * p.group;
+  const int pos0 = kv_len - q_len + i0;                 // position of the tile's first token
+  // keys some row sees: [0, min(first, hi)) and [lo, hi)
+  const int hi = pos0 + tokens;
+  const int lo = max(0, pos0 - p.window + 1);
+  const int first_boxes = cdiv(min(p.first_tokens, lo), kBox);
+  const int run = max(kPaged ? lo - lo % kBox : lo, first_boxes * kBox);   // first key of the run's boxes
+  const int gap = run - first_boxes * kBox;             // keys left out between the two parts
+  const int n_boxes = first_boxes + cdiv(max(hi - run, 0), kBox);
+  const int n_tiles = cdiv(n_boxes, kBoxes);
+  auto slot_of = [&](int key) { return key <= first_boxes * kBox ? key : max(key - gap, first_boxes * kBox); };
+  const int live_threads = min(kBM, 32 * cdiv(rows, 32));
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  Bars &bar = *reinterpret_cast<Bars *>(smem + kOffBars);
+  uint8_t *sQ = smem + kOffQ;
+  auto sK = [&](int s) { return smem + kOffK + s * kTileBytes; };
+  auto sV = [&](int s) { return smem + kOffV + s * kTileBytes; };
+
+  if (warp == kPvWarp) {
+    tmem_alloc(&bar.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  const int32_t *table =
+      kPaged ? p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq : nullptr;
+  // where this lane's box of tile j comes from (lanes 0..7): a page id, or the
+  // first row of the box in the ragged K/V; -1 past the last box
+  auto source_of = [&](int j) -> int {
+    const int bx = j * kBoxes + lane;
+    if (lane >= kBoxes || bx >= n_boxes) return -1;
+    const int key = bx < first_boxes ? bx * kBox : run + (bx - first_boxes) * kBox;
+    if constexpr (kPaged) {
+      const int id = table[key / kPageSize];
+      if (id < 0 || id >= p.num_pages) {
+        atomicOr(&bar.bad, 1);
+        return -1;
+      }
+      return id;
+    } else {
+      return q_start + key;
+    }
+  };
+  // K (t = 0) or V (t = 1) of tile j into its ring slot, once the slot is free
+  auto load = [&](int j, int t, int src) -> bool {
+    const int ns = t == 0 ? kKStages : kVStages;
+    const int s = j % ns;
+    uint64_t *full = t == 0 ? &bar.k_full[s] : &bar.v_full[s];
+    uint64_t *empty = t == 0 ? &bar.k_empty[s] : &bar.v_empty[s];
+    uint8_t *dst = (t == 0 ? sK(s) : sV(s)) + lane * kBoxBytes;
+    const CUtensorMap *map = t == 0 ? &kmap : &vmap;
+    if (j >= ns && !__all_sync(0xffffffffu, mbar_wait(empty, ((j / ns) + 1) & 1))) return false;
+    const unsigned mask = __ballot_sync(0xffffffffu, src >= 0);
+    if (lane == 0) mbar_arrive_expect_tx(full, __popc(mask) * kBoxBytes);
+    __syncwarp();
+    if (src >= 0) {
+      if constexpr (kPaged) tma_load_3d(dst, map, full, 0, kvh * kPageSize, src);
+      else tma_load_3d(dst, map, full, 0, kvh, src);
+    }
+    __syncwarp();
+    return true;
+  };
+
+  if (warp == kQkWarp) {
+    if (lane == 0) {
+      mbar_init(&bar.q_full, 1);
+      for (int s = 0; s < kKStages; ++s) {
+        mbar_init(&bar.k_full[s], 1);
+        mbar_init(&bar.k_empty[s], 1);
+      }
+      for (int s = 0; s < kVStages; ++s) {
+        mbar_init(&bar.v_full[s], 1);
+        mbar_init(&bar.v_empty[s], 1);
+      }
+      mbar_init(&bar.s_full, 1);
+      mbar_init(&bar.s_free, live_threads);
+      mbar_init(&bar.p_full, live_threads);
+      mbar_init(&bar.pv_done, 1);
+      mbar_init(&bar.o_final, 1);
+      bar.bad = 0;
+      fence_mbar_init();
+      mbar_arrive_expect_tx(&bar.q_full, p.tile_tokens * p.group * kHeadDim * 2);
+      // box {64, group, tile_tokens}: rows (token, head)
+      tma_load_3d(sQ, &qmap, &bar.q_full, 0, kvh * p.group, q_start + i0);
+    }
+    __syncwarp();
+    for (int j = 0; j < min(n_tiles, kKStages); ++j) load(j, 0, source_of(j));   // fresh slots
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem_base;
+
+  if (warp == kQkWarp) {
+    // ------------------------------------------- loads and QK^T (one thread)
+    const uint64_t dq = umma_desc_sw128(smem_u32(sQ), 16, 1024);
+    auto issue_qk = [&](int j) -> bool {
+      const int s = j % kKStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.k_full[s], (j / kKStages) & 1))) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t dk = umma_desc_sw128(smem_u32(sK(s)), 16, 1024);
+        const uint32_t idesc =
+            umma_idesc_bf16(128, kBox * min(kBoxes, n_boxes - j * kBoxes), false, false);
+#pragma unroll
+        for (int kk = 0; kk < kHeadDim / 16; ++kk)
+          umma_ss(tmem + kColS, dq + 2 * kk, dk + 2 * kk, idesc, kk > 0);   // +32 bytes per k-step
+        umma_commit(&bar.s_full);
+        umma_commit(&bar.k_empty[s]);
+      }
+      __syncwarp();
+      return true;
+    };
+    int src = source_of(kKStages);
+    bool ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_full, 0));
+    ok = ok && issue_qk(0);
+    for (int j = 0; ok && j + 1 < n_tiles; ++j) {
+      // S of tile j has been read: compute S of tile j+1 during this softmax
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_free, j & 1))) { ok = false; break; }
+      tc_fence_after();
+      ok = issue_qk(j + 1);
+      if (ok && j + kKStages < n_tiles) {             // K slot freed by QK^T of tile j
+        ok = load(j + kKStages, 0, src);
+        src = source_of(j + kKStages + 1);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&bar.bad, 1);
+  } else if (warp == kPvWarp) {
+    // ---------------------------------------------------- P V (one thread)
+    const uint32_t tP = tmem + kColP, tO = tmem + kColO;
+    // slots no row sees: [dead_from, dead_to) between the parts, and from end on
+    const int dead_from = slot_of(min(p.first_tokens, hi)), dead_to = slot_of(lo), end = slot_of(hi);
+    bool ok = true;
+    for (int j = 0; ok && j < min(n_tiles, kVStages); ++j) ok = load(j, 1, source_of(j));
+    int src = source_of(kVStages);
+    for (int j = 0; ok && j < n_tiles; ++j) {
+      const int s = j % kVStages;
+      const int boxes = min(kBoxes, n_boxes - j * kBoxes);
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.p_full, j & 1)) ||
+          !__all_sync(0xffffffffu, mbar_wait(&bar.v_full[s], (j / kVStages) & 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // zero the V rows of this tile that no row sees (0 * NaN would poison
+      // whole rows): whole 128-byte rows, so the swizzle is irrelevant
+      const int v0 = j * kBN, v1 = v0 + boxes * kBox;
+      uint4 *v = reinterpret_cast<uint4 *>(sV(s));
+      auto clear = [&](int from, int to) {
+        for (int idx = (max(from, v0) - v0) * 8 + lane; idx < (min(to, v1) - v0) * 8; idx += 32)
+          v[idx] = make_uint4(0, 0, 0, 0);
+      };
+      if ((dead_from < dead_to && dead_from < v1 && dead_to > v0) || end < v1) {
+        clear(dead_from, dead_to);
+        clear(end, v1);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        const uint64_t dv = umma_desc_sw128(smem_u32(sV(s)), kTileBytes, 1024);
+        for (int kk = 0; kk < boxes; ++kk)
+          umma_ts(tO, tP + 8 * kk, dv + (kBoxBytes >> 4) * kk, kIdescPV, (j > 0) || (kk > 0));
+        umma_commit(&bar.v_empty[s]);
+        umma_commit(&bar.pv_done);
+      }
+      __syncwarp();
+      if (j + kVStages < n_tiles) {
+        if (!load(j + kVStages, 1, src)) { ok = false; break; }
+        src = source_of(j + kVStages + 1);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(&bar.bad, 1);
+    if (lane == 0) umma_commit(&bar.o_final);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int r = threadIdx.x;                          // row = TMEM lane
+    const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int token = r / p.group;
+    const int head = kvh * p.group + (r - token * p.group);
+    const int pos = pos0 + min(token, tokens - 1);      // lanes past the rows repeat the last one
+    RowSlots see;
+    see.a = slot_of(min(p.first_tokens, pos + 1));
+    see.b = slot_of(max(0, pos - p.window + 1));
+    see.c = slot_of(pos + 1);
+    const float sl2 = p.scale_log2;
+    const bool pos_scale = sl2 >= 0.f;
+    // Masked scores are replaced (by index, so NaN keys cannot leak) with the
+    // raw value whose scaled logit is -inf.
+    const uint32_t masked_raw = pos_scale ? 0xff800000u : 0x7f800000u;
+    // reference max (base 2) and sum, started at the sink
+    float m = r < rows ? p.sinks[head] * kLog2e : -INFINITY;
+    float d = 1.f;
+    bool ok = true;
+    uint32_t x[4][32];
+    const bool live = warp * 32 < live_threads;         // warp-uniform
+    for (int j = 0; live && j < n_tiles; ++j) {
+      const int chunks = (min(kBoxes, n_boxes - j * kBoxes) + 1) / 2;
+      if (!softmax_tile(bar, trow, j, chunks, see, sl2, pos_scale, masked_raw, m, d, x)) {
+        ok = false;
+        break;
+      }
+    }
+    if (live) {
+      if (__all_sync(0xffffffffu, mbar_wait(&bar.o_final, 0))) {
+        tc_fence_after();
+        if (ok) {
+          tmem_ld32(trow + kColO, x[0]);
+          tmem_ld32(trow + kColO + 32, x[1]);
+          tmem_ld_wait32(x[0]);
+          reg_tie32(x[1]);
+        }
+      } else {
+        ok = false;
+      }
+    }
+    if (!ok) atomicOr(&bar.bad, 1);
+    // Outputs are written after the CTA-wide barrier below.  Tensor memory is
+    // read no more: the P V warp frees it meanwhile.
+    tc_fence_before();
+    __syncthreads();
+    if (!live) return;
+    const bool failed = bar.bad != 0;
+    const float inv = d > 0.f ? 1.f / d : 0.f;
+    auto o = [&](int e) { return __uint_as_float(x[e >> 5][e & 31]) * inv; };
+    // Each warp puts its rows in the query buffer (free since the last QK^T
+    // completed) and reads them back so that 8 lanes cover one row's 128
+    // contiguous bytes.
+    uint4 *sw = reinterpret_cast<uint4 *>(sQ) + (r - lane) * 8;     // this warp's 32 rows
+#pragma unroll
+    for (int c = 0; c < kHeadDim / 8; ++c) {
+      uint4 w = nan4;
+      if (!failed) {
+        w.x = pack_bf16(o(8 * c + 0), o(8 * c + 1));
+        w.y = pack_bf16(o(8 * c + 2), o(8 * c + 3));
+        w.z = pack_bf16(o(8 * c + 4), o(8 * c + 5));
+        w.w = pack_bf16(o(8 * c + 6), o(8 * c + 7));
+      }
+      sw[lane * 8 + (c ^ (lane & 7))] = w;
+    }
+    __syncwarp();
+    const int cc = lane & 7;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int rr = 4 * k + (lane >> 3);                  // row within the warp's slice
+      const int tr = r - lane + rr, tok = tr / p.group;
+      if (tr < rows) {
+        const size_t row = static_cast<size_t>(q_start + i0 + tok) * p.num_qo_heads +
+                           kvh * p.group + (tr - tok * p.group);
+        reinterpret_cast<uint4 *>(p.out + row * kHeadDim)[cc] = sw[rr * 8 + (cc ^ (rr & 7))];
+      }
+    }
+    if (r < rows && p.lse) {
+      const size_t row = static_cast<size_t>(q_start + i0 + token) * p.num_qo_heads + head;
+      p.lse[row] = failed ? NAN : (d > 0.f ? (m + lg2(d)) * kLn2 : -INFINITY);
+    }
+    return;
+  }
+  tc_fence_before();
+  __syncthreads();          // the softmax warps have read O: tensor memory is free
+  if (warp == kPvWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <bool kPaged>
+cudaError_t launch_variant(const CUtensorMap &qmap, const CUtensorMap &kmap,
+                           const CUtensorMap &vmap, const WindowPrefillParams &p, unsigned ctas,
+                           cudaStream_t stream) {
+  cudaError_t err = set_smem_once<window_prefill_kernel<kPaged>>(kSmemBytes);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(window_prefill_kernel<kPaged>, ctas, kThreads, kSmemBytes, stream, false,
+                       qmap, kmap, vmap, p);
+}
+
+}  // namespace
+
+cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,
+                                  const CUtensorMap &vmap, const WindowPrefillParams &p,
+                                  cudaStream_t stream) {
+  const unsigned long long ctas =
+      static_cast<unsigned long long>(p.num_q_tiles) * p.num_seqs * p.num_kv_heads;
+  if (ctas == 0) return cudaSuccess;
+  if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+  return p.page_table ? launch_variant<true>(qmap, kmap, vmap, p, static_cast<unsigned>(ctas), stream)
+                      : launch_variant<false>(qmap, kmap, vmap, p, static_cast<unsigned>(ctas), stream);
+}
+
+}  // namespace sa

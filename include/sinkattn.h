@@ -389,6 +389,146 @@ SINKATTN_API int sinkattn_decode_static_scratch(
     float *lse, int batch, int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
     int num_pages, int max_kv_len, int num_splits, void *stream);
 
+/*
+ * Attention with a sliding window and first tokens that stay visible.
+ *
+ * The row of the token at position i (0-based among its request's keys) sees
+ *     { j <= i : j < first_tokens  or  j > i - window }
+ * -- the `window` newest keys, its own among them, and the first_tokens
+ * oldest -- and is otherwise the operation at the top of this file, the
+ * head's sink logit included.  window >= 1 and first_tokens >= 0 (else
+ * SINKATTN_INVALID_ARGUMENT); a window of max_kv_len or more is full
+ * attention.
+ *   - A page that holds no visible key is neither read nor looked up: its
+ *     page-table entry may hold anything, so a caller may free the pages
+ *     between the first tokens and the window.
+ *   - Keys outside a row's range do not enter its result, whatever they
+ *     hold, with one exception in prefill: a value row (v) that is not finite
+ *     makes NaN every row of the same tile (128 / group consecutive tokens of
+ *     a KV head) if one row of the tile sees it.
+ *   - kv_len > max_kv_len is checked exactly.
+ * Errors, launch modes, workspace rules and the remaining arguments are those
+ * of the forms without a window.
+ *
+ * sinkattn_decode_window: one new token per request, the last of its keys
+ * (i = kv_len - 1); arguments as for sinkattn_decode_ex.  The plan splits the
+ * visible pages into chunks.
+ */
+SINKATTN_API int sinkattn_decode_window_plan(int batch, int num_qo_heads, int num_kv_heads,
+                         int head_dim, int page_size, int max_kv_len, int window,
+                         int first_tokens, int num_sms, int *num_splits,
+                         size_t *workspace_bytes);
+
+SINKATTN_API int sinkattn_decode_window(const void *q, const void *k_cache, const void *v_cache,
+                         const int32_t *page_table, int max_pages_per_seq,
+                         const int32_t *kv_lens, const float *sinks, float scale, int window,
+                         int first_tokens, void *out, float *lse,
+                         int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                         int page_size, int num_pages, int max_kv_len, int num_splits,
+                         void *workspace, size_t workspace_bytes, int launch_flags,
+                         void *stream);
+
+/* Windowed prefill, ragged (as sinkattn_prefill) and appended to a paged
+ * prefix (as sinkattn_prefill_paged; with few new tokens it also serves
+ * causal verification in a windowed layer).  At most 128 query heads per KV
+ * head (else SINKATTN_UNSUPPORTED). */
+SINKATTN_API int sinkattn_prefill_window(const void *q, const void *k, const void *v,
+                         const int32_t *cu_seqlens, int num_seqs, int total_tokens,
+                         int max_seqlen, const float *sinks, float scale, int window,
+                         int first_tokens, void *out, float *lse,
+                         int num_qo_heads, int num_kv_heads, int head_dim, void *stream);
+
+SINKATTN_API int sinkattn_prefill_paged_window(const void *q, const int32_t *cu_seqlens_q,
+                         int num_seqs, int total_q, int max_q_len,
+                         const void *k_cache, const void *v_cache,
+                         const int32_t *page_table, int max_pages_per_seq,
+                         const int32_t *kv_lens, int num_pages, int max_kv_len,
+                         const float *sinks, float scale, int window, int first_tokens,
+                         void *out, float *lse, int num_qo_heads, int num_kv_heads,
+                         int head_dim, int page_size, void *stream);
+
+/*
+ * Attention mass: the weight that each cached key has drawn, summed over the
+ * query heads of its KV head and over the rows of the call, added to what
+ * `mass` holds:
+ *     mass[b][g][j] += sum over rows i of request b that see key j (j <= the
+ *                      row's position) and heads h of KV head g of
+ *                      exp(scale * dot(q_ih, k_gj) - lse_ih)
+ * with lse what sinkattn_decode / sinkattn_prefill[_paged] / sinkattn_verify
+ * returned for these rows (sink included: a row's weights sum to less than 1).
+ *   mass        : fp32 [batch][num_kv_heads][mass_stride], mass_stride >=
+ *                 max_kv_len; entry j of a row belongs to key j of the request.
+ *                 Entries from kv_len on are neither read nor written.
+ *   lse         : fp32 [rows][num_qo_heads]; a row with lse = -inf adds nothing
+ *   other arguments as for the attention call of the same form
+ * Sums are in fp32 and in a fixed order: equal calls give equal bits.  No two
+ * calls that add to the same mass may overlap on the GPU.  A request whose
+ * lengths are out of range gets a NaN mass row (all mass_stride entries of
+ * each KV head); keys on a page outside the pool get NaN.
+ *
+ * sinkattn_decode_mass: one new token per request (q [batch][num_qo_heads]
+ * [head_dim]).  Launched programmatically whatever the default: it reads and
+ * writes nothing before the kernel before it on the stream has finished.
+ * sinkattn_prefill_mass: the rows of a (chunked) prefill, cu_seqlens_q as for
+ * sinkattn_prefill_paged; handing in only the last rows of each prompt lets
+ * just those vote.  At most 128 query heads per KV head.
+ */
+SINKATTN_API int sinkattn_decode_mass(const void *q, const void *k_cache,
+                         const int32_t *page_table, int max_pages_per_seq,
+                         const int32_t *kv_lens, const float *lse, float scale,
+                         float *mass, int mass_stride, int batch, int num_qo_heads,
+                         int num_kv_heads, int head_dim, int page_size, int num_pages,
+                         int max_kv_len, void *stream);
+
+SINKATTN_API int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_seqs,
+                         int total_q, int max_q_len, const void *k_cache,
+                         const int32_t *page_table, int max_pages_per_seq,
+                         const int32_t *kv_lens, int num_pages, int max_kv_len,
+                         const float *lse, float scale, float *mass, int mass_stride,
+                         int num_qo_heads, int num_kv_heads, int head_dim,
+                         int page_size, void *stream);
+
+/*
+ * Eviction from the cache by attention mass.  Of a request with more than
+ * `budget` keys, each KV head keeps its first first_tokens keys, its last
+ * `recent` keys, and of the others those of the largest mass (equal masses:
+ * the lower index first; NaN counts below every number), budget keys in all;
+ * a request with no more than budget keys keeps all.  The kept keys, in their
+ * order, become keys 0, 1, ... of the request: their K and V rows and their
+ * mass move there.  Keys carry their rotary position already; new tokens go on
+ * with their true positions.
+ *   k_cache, v_cache : written in place (see the conventions)
+ *   mass             : fp32 [batch][num_kv_heads][mass_stride >= max_kv_len]
+ *   dst_page_table   : int32 [batch][dst_max_pages_per_seq] (> 0), the pages
+ *                      that take the kept keys; NULL: page_table itself, in
+ *                      place.  Other pages than the request's own must belong
+ *                      to no request of the call, and no page may appear
+ *                      twice.  With them the old pages stay as they are (they
+ *                      may be shared by requests); in place, pages must not be
+ *                      shared.
+ *   dst_mass         : fp32 [batch][num_kv_heads][dst_mass_stride >=
+ *                      min(budget, max_kv_len)], not overlapping mass; NULL:
+ *                      mass itself, in place.  Entries from the new length to
+ *                      the old one (within the row) become 0, so that later
+ *                      tokens start from nothing; further ones stay.
+ *   new_kv_lens      : int32 [batch] out, min(kv_len, budget); must not
+ *                      overlap kv_lens
+ *   kept             : int32 [batch][num_kv_heads][budget] out, the kept
+ *                      keys' former indices in order, -1 past the new length
+ *   budget >= 1, first_tokens >= 0, recent >= 0, first_tokens + recent <= budget
+ * A request whose lengths do not fit, or with a page outside the pool among
+ * those of its keys or their destinations, is left as it was: its new length
+ * is -1 (a decode on that gives NaN) and its kept entries are -1.
+ * Launched programmatically whatever the default (as sinkattn_decode_mass).
+ */
+SINKATTN_API int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *page_table,
+                         int max_pages_per_seq, const int32_t *kv_lens, float *mass,
+                         int mass_stride, int budget, int first_tokens, int recent,
+                         const int32_t *dst_page_table, int dst_max_pages_per_seq,
+                         float *dst_mass, int dst_mass_stride, int32_t *new_kv_lens,
+                         int32_t *kept, int batch, int num_kv_heads, int head_dim,
+                         int page_size, int num_pages, int max_kv_len, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

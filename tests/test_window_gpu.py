@@ -1,0 +1,222 @@
+"""Windowed attention on the GPU against the float64 oracle: one token,
+ragged prefill, prefill on a paged prefix.
+
+Bars: those of the other attention kernels (tolerances.py).  They hold here
+too: the kernels round the same things (weights to bf16 for the product with
+V, the output once to bf16), and a window only takes keys away.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import gqa_attention_learned_gb300 as sa
+from bounded_inputs import DEV, Paged, bf16, np64
+from oracle import bounded
+from tolerances import assert_lse_close, assert_out_close
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(64, 8), (4, 1), (8, 8), (10, 2), (32, 2)]
+WINDOWS = [(1, 0), (2, 1), (16, 0), (17, 5), (128, 4), (130, 33), (1000, 0), (40, 64)]
+LENS = [0, 1, 2, 15, 16, 17, 31, 33, 128, 129, 144, 145, 300, 301]
+
+
+def _decode_ref(c, q, window, first):
+    outs, lses = [], []
+    for b, n in enumerate(c.lens):
+        o, l = bounded.window_rows(np64(q[b:b + 1]), np64(c.k[b]), np64(c.v[b]), [n - 1],
+                                   np64(c.sinks), c.scale, window, first)
+        outs.append(o[0])
+        lses.append(l[0])
+    return np.stack(outs), np.stack(lses)
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("window,first", WINDOWS)
+def test_decode_window(heads, window, first):
+    c = Paged(LENS, *heads, seed=window)
+    q = bf16(c.rng, len(LENS), heads[0], 64)
+    ro, rl = _decode_ref(c, q, window, first)
+    for b, n in enumerate(c.lens):
+        c.hide(b, bounded.visible(n - 1, n, window, first))
+    args = (q.to(DEV), *c.paged(), c.sinks.to(DEV), c.scale, c.max_kv, window, first)
+    for splits in (0, 1, 3):
+        out, lse = sa.decode_window(*args, num_splits=splits)
+        assert_out_close(out, ro)
+        assert_lse_close(lse, rl)
+    again, lse2 = sa.decode_window(*args, num_splits=3, programmatic=True)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+def test_a_window_without_bound_is_decode():
+    c = Paged([300, 17, 1], 64, 8)
+    q = bf16(c.rng, 3, 64, 64).to(DEV)
+    args = (q, *c.paged(), c.sinks.to(DEV), c.scale, c.max_kv)
+    for splits in (1, 4):
+        a = sa.decode(*args, num_splits=splits)
+        b = sa.decode_window(*args, 2**40, num_splits=splits)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_window_masked_heads_and_zero_scale():
+    # a sink of -inf on some heads; a request that sees nothing; scale 0 and below
+    c = Paged([40, 0, 200], 8, 2)
+    c.sinks[::2] = -np.inf
+    q = bf16(c.rng, 3, 8, 64)
+    for scale in (0.0, -0.125):
+        c.scale = scale
+        ro, rl = _decode_ref(c, q, 9, 2)
+        out, lse = sa.decode_window(q.to(DEV), *c.paged(), c.sinks.to(DEV), scale, c.max_kv, 9, 2)
+        assert_out_close(out, ro)
+        assert_lse_close(lse, rl)
+
+
+def test_decode_window_out_of_range_requests_give_nan():
+    c = Paged([20, 300, 20, 64], 4, 1)
+    q = bf16(c.rng, 4, 4, 64).to(DEV)
+    k, v, table, lens = c.paged()
+    lens[0] = -1
+    lens[1] = 301                                       # past max_kv_len
+    table[2, 1] = c.pages                               # a visible page outside the pool
+    out, lse = sa.decode_window(q, k, v, table, lens, c.sinks.to(DEV), c.scale, 300, 8)
+    assert torch.isnan(out[:3]).all() and torch.isnan(lse[:3]).all()
+    assert torch.isfinite(out[3]).all()
+
+
+def _prefill_ref(c_or_kv, q, cu, shift, sinks, scale, window, first):
+    k, v = c_or_kv
+    outs, lses = [], []
+    for b in range(len(cu) - 1):
+        rows = range(cu[b], cu[b + 1])
+        o, l = bounded.window_rows(np64(q[cu[b]:cu[b + 1]]), np64(k[b]), np64(v[b]),
+                                   [shift[b] + i for i in range(len(rows))], sinks, scale, window, first)
+        outs.append(o)
+        lses.append(l)
+    return np.concatenate(outs), np.concatenate(lses)
+
+
+@pytest.mark.parametrize("heads", [(64, 8), (4, 1), (8, 8), (10, 2), (32, 2)])
+@pytest.mark.parametrize("window,first", [(1, 0), (17, 5), (128, 0), (130, 33), (1000, 0), (40, 64)])
+def test_prefill_window_ragged(heads, window, first):
+    hq, hkv = heads
+    rng = np.random.default_rng(window)
+    lens = [1, 17, 300, 0, 129]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v = bf16(rng, cu[-1], hq, 64), bf16(rng, cu[-1], hkv, 64), bf16(rng, cu[-1], hkv, 64)
+    sinks = torch.from_numpy(rng.standard_normal(hq).astype(np.float32))
+    parts = [slice(cu[b], cu[b + 1]) for b in range(len(lens))]
+    ro, rl = _prefill_ref(([k[p] for p in parts], [v[p] for p in parts]), q, cu, [0] * len(lens),
+                          np64(sinks), 0.125, window, first)
+    out, lse = sa.prefill_window(q.to(DEV), k.to(DEV), v.to(DEV),
+                                 torch.tensor(cu, dtype=torch.int32, device=DEV), sinks.to(DEV), 0.125,
+                                 300, window, first)
+    assert_out_close(out, ro)
+    assert_lse_close(lse, rl)
+
+
+@pytest.mark.parametrize("heads", [(64, 8), (4, 1), (6, 2)])
+@pytest.mark.parametrize("window,first", [(1, 0), (17, 5), (128, 4), (130, 33), (1000, 0), (40, 64), (300, 150)])
+def test_prefill_paged_window(heads, window, first):
+    # new tokens on prefixes of every alignment; what no row sees is NaN or has no page
+    q_lens, prefix = [1, 5, 140, 33, 16], [0, 400, 259, 31, 512]
+    c = Paged([a + b for a, b in zip(q_lens, prefix)], *heads, seed=first)
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    q = bf16(c.rng, cu[-1], heads[0], 64)
+    ro, rl = _prefill_ref((c.k, c.v), q, cu, prefix, np64(c.sinks), c.scale, window, first)
+    for b, n in enumerate(c.lens):
+        seen = np.zeros(n, bool)
+        for p in range(prefix[b], n):
+            seen |= bounded.visible(p, n, window, first)
+        c.hide(b, seen)
+    out, lse = sa.prefill_paged_window(q.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV),
+                                       *c.paged(), c.sinks.to(DEV), c.scale, max(q_lens), c.max_kv,
+                                       window, first)
+    assert_out_close(out, ro)
+    assert_lse_close(lse, rl)
+
+
+def test_prefill_window_zero_and_negative_scale():
+    rng = np.random.default_rng(3)
+    q, k, v = bf16(rng, 200, 4, 64), bf16(rng, 200, 1, 64), bf16(rng, 200, 1, 64)
+    sinks = torch.tensor([0.5, -np.inf, 3.0, -1.0])
+    cu = torch.tensor([0, 200], dtype=torch.int32, device=DEV)
+    for scale in (0.0, -0.125):
+        ro, rl = bounded.window_rows(np64(q), np64(k), np64(v), range(200), np64(sinks), scale, 30, 3)
+        out, lse = sa.prefill_window(q.to(DEV), k.to(DEV), v.to(DEV), cu, sinks.to(DEV), scale, 200, 30, 3)
+        assert_out_close(out, ro)
+        assert_lse_close(lse, rl)
+
+
+def test_prefill_window_leaves_other_rows_alone_and_flags_bad_ones():
+    # rows behind the last sequence stay as they were; a sequence longer than
+    # the bound gives NaN; cu_seqlens past the rows give NaN up to their end
+    rng = np.random.default_rng(4)
+    q, k, v = (bf16(rng, 100, h, 64).to(DEV) for h in (4, 1, 1))
+    sinks = torch.zeros(4, device=DEV)
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((100, 4), 7.0, device=DEV)
+    sa.prefill_window(q, k, v, torch.tensor([0, 20, 60], dtype=torch.int32, device=DEV), sinks, 0.125,
+                      30, 8, out=out, lse=lse)
+    assert torch.isfinite(out[:20]).all()
+    assert torch.isnan(out[20:60]).all() and torch.isnan(lse[20:60]).all()
+    assert (out[60:] == 7).all() and (lse[60:] == 7).all()
+    sa.prefill_window(q, k, v, torch.tensor([0, 90, 120], dtype=torch.int32, device=DEV), sinks, 0.125,
+                      90, 8, out=out, lse=lse)
+    assert torch.isfinite(out[:90]).all() and torch.isnan(out[90:]).all()
+
+
+def test_prefill_paged_window_bad_page_and_short_cache():
+    c = Paged([200, 50, 90], 4, 1)
+    cu = torch.tensor([0, 100, 160, 200], dtype=torch.int32, device=DEV)
+    q = bf16(c.rng, 200, 4, 64).to(DEV)
+    k, v, table, lens = c.paged()
+    table[0, 12] = -5                                    # keys 192..199: seen by the last rows
+    out, lse = sa.prefill_paged_window(q, cu, k, v, table, lens, c.sinks.to(DEV), c.scale, 100, 200, 16)
+    assert torch.isnan(out[99]).all() and torch.isnan(lse[99]).all()
+    assert torch.isfinite(out[0]).all()
+    assert torch.isnan(out[100:160]).all()               # 60 new tokens, 50 keys
+    assert torch.isfinite(out[160:]).all()
+
+
+def test_windowed_forms_agree_and_replay_from_a_graph():
+    # decode of the last token = the last row of the paged and ragged prefill
+    c = Paged([333], 64, 8)
+    q = bf16(c.rng, 333, 64, 64).to(DEV)
+    cu = torch.tensor([0, 333], dtype=torch.int32, device=DEV)
+    paged, sinks = c.paged(), c.sinks.to(DEV)
+    k, v = c.k[0].to(DEV), c.v[0].to(DEV)
+
+    def run():
+        a = sa.prefill_window(q, k, v, cu, sinks, c.scale, 333, 100, 7)
+        b = sa.prefill_paged_window(q, cu, *paged, sinks, c.scale, 333, 333, 100, 7)
+        d = sa.decode_window(q[-1:].contiguous(), *paged, sinks, c.scale, 333, 100, 7)
+        return a, b, d
+
+    a, b, d = run()
+    assert_out_close(b[0], np64(a[0]))
+    assert_lse_close(b[1], np64(a[1]))
+    assert_out_close(d[0], np64(a[0][-1:]))
+    assert_lse_close(d[1], np64(a[1][-1:]))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ga, gb, gd = run()
+    q.copy_(bf16(np.random.default_rng(9), 333, 64, 64))
+    g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip((ga, gb, gd), run()):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+def test_another_stream_orders_its_own_workspace():
+    c = Paged([2000, 1999], 64, 8)
+    q = bf16(c.rng, 2, 64, 64).to(DEV)
+    args = (q, *c.paged(), c.sinks.to(DEV), c.scale, 2000, 1500, 4)
+    want = sa.decode_window(*args, num_splits=8)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = [sa.decode_window(*args, num_splits=8, stream=side) for _ in range(4)]
+    side.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
