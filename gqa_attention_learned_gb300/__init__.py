@@ -415,13 +415,25 @@ def qkv_prologue(qkv, bias, positions, slot_mapping, inv_freq, mscale, k_cache, 
 _INT_MAX = 2**31 - 1
 
 
-@contextlib.contextmanager
+_AS_IS = contextlib.nullcontext()
+
+
 def _at(dev, stream):
     """Makes `dev` the current device and `stream` (if given) its current
     stream, so that what a call allocates or clears is ordered on the stream
-    that it launches on."""
-    with _on(dev), (contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)):
-        yield
+    that it launches on (no-op when both already are)."""
+    if stream is None and (dev.index is None or dev.index == torch.cuda.current_device()):
+        return _AS_IS
+    stack = contextlib.ExitStack()
+    stack.enter_context(_on(dev))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def _raw_stream(dev):
+    """Handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _size(v, name, least=0):
@@ -433,7 +445,7 @@ def _size(v, name, least=0):
 
 
 def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -506,7 +518,7 @@ def decode_window(q, k_cache, v_cache, page_table, kv_lens, sinks, scale, max_kv
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), page_table.shape[1],
             _ptr(kv_lens), _ptr(sinks), float(scale), window, first, _ptr(out), _ptr(lse), batch,
             hq, hkv, d, page, num_pages, max_kv_len, num_splits, _ptr(workspace), ws_len,
-            _launch_flags(programmatic), _stream(None)))
+            _launch_flags(programmatic), _raw_stream(q.device)))
     return out, lse
 
 
@@ -534,7 +546,7 @@ def prefill_window(q, k, v, cu_seqlens, sinks, scale, max_seqlen, window, first_
         _check("sinkattn_prefill_window", load().sinkattn_prefill_window(
             _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), cu_seqlens.numel() - 1, total,
             _size(max_seqlen, "max_seqlen"), _ptr(sinks), float(scale), window, first, _ptr(out),
-            _ptr(lse), hq, hkv, d, _stream(None)))
+            _ptr(lse), hq, hkv, d, _raw_stream(q.device)))
     return out, lse
 
 
@@ -561,7 +573,7 @@ def prefill_paged_window(q, cu_seqlens_q, k_cache, v_cache, page_table, kv_lens,
             _size(max_q_len, "max_q_len"), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
             page_table.shape[1], _ptr(kv_lens), num_pages, _size(max_kv_len, "max_kv_len"),
             _ptr(sinks), float(scale), window, first, _ptr(out), _ptr(lse), hq, hkv, d, page,
-            _stream(None)))
+            _raw_stream(q.device)))
     return out, lse
 
 
@@ -589,7 +601,7 @@ def decode_mass(q, k_cache, page_table, kv_lens, lse, scale, max_kv_len, mass, *
         _check("sinkattn_decode_mass", load().sinkattn_decode_mass(
             _ptr(q), _ptr(k_cache), _ptr(page_table), page_table.shape[1], _ptr(kv_lens),
             _ptr(lse), float(scale), _ptr(mass), mass.shape[2], batch, hq, hkv, d, page, num_pages,
-            _size(max_kv_len, "max_kv_len"), _stream(None)))
+            _size(max_kv_len, "max_kv_len"), _raw_stream(q.device)))
     return mass
 
 
@@ -608,7 +620,7 @@ def prefill_mass(q, cu_seqlens_q, k_cache, page_table, kv_lens, lse, scale, max_
             _ptr(q), _ptr(cu_seqlens_q), batch, total, _size(max_q_len, "max_q_len"),
             _ptr(k_cache), _ptr(page_table), page_table.shape[1], _ptr(kv_lens), num_pages,
             _size(max_kv_len, "max_kv_len"), _ptr(lse), float(scale), _ptr(mass), mass.shape[2],
-            hq, hkv, d, page, _stream(None)))
+            hq, hkv, d, page, _raw_stream(q.device)))
     return mass
 
 
@@ -652,5 +664,5 @@ def evict(k_cache, v_cache, page_table, kv_lens, mass, budget, max_kv_len, *, fi
             _ptr(mass), mass.shape[2], budget, first, recent, _ptr(dst_page_table),
             0 if dst_page_table is None else dst_page_table.shape[1], _ptr(dst_mass),
             0 if dst_mass is None else dst_mass.shape[2], _ptr(new_kv_lens), _ptr(kept), batch,
-            hkv, d, page, num_pages, _size(max_kv_len, "max_kv_len"), _stream(None)))
+            hkv, d, page, num_pages, _size(max_kv_len, "max_kv_len"), _raw_stream(dev)))
     return new_kv_lens, kept

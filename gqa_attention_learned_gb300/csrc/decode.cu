@@ -32,9 +32,6 @@
 //    finished in place; otherwise each chunk CTA writes (o/d, lse) to the
 //    workspace and bumps the (request, KV head)'s counter, and the last one
 //    to arrive merges the chunks by log-sum-exp -- no second launch.
-//  * With a sliding window (kWindow) the same pipeline runs over the pages that
-//    hold a visible key only; keys of those pages outside the window and the
-//    first tokens are masked by index.
 // There is no tensor-memory (tcgen05) path here: 8 query heads per KV head
 // would fill 8 rows of a 128-row tcgen05 tile, or (keys as the rows) need
 // 128-key tiles at the tensor pipe's ~46 cycles per instruction, while the
@@ -75,40 +72,14 @@ static_assert(sizeof(MergeSmem<2>) <= kPipeBytes, "merge scratch aliases the sta
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Pages of a request that hold a key its token sees.  Without a window: all.
-// With one (keys [0, first) and [start, kv_len), start = kv_len - window): the
-// pages of the first tokens, then those from start's page on; the pages
-// between are neither copied nor looked up.  Chunks, warps and pipelines count
-// visited pages 0..count-1; page(v) is the request's page behind number v.
-template <bool kWindow>
-struct VisiblePages {
-  int count, skip_from, skip, start;
-  __device__ __forceinline__ VisiblePages(const DecodeParams &p, int kv_len) {
-    const int npages = ceil_div(max(kv_len, 0), kPageSize);
-    if constexpr (kWindow) {
-      start = max(0, kv_len - p.window);
-      skip_from = min(ceil_div(p.first_tokens, kPageSize), start / kPageSize);
-      skip = start / kPageSize - skip_from;
-      count = npages - skip;
-    } else {
-      start = skip_from = skip = 0;
-      count = npages;
-    }
-  }
-  __device__ __forceinline__ int page(int v) const {
-    return kWindow && v >= skip_from ? v + skip : v;
-  }
-};
-
 // Chunk count of one request under the plan; 0 marks a request whose
 // arguments are out of range (its outputs become NaN).
-template <bool kWindow>
-__device__ __forceinline__ int request_chunks(const DecodeParams &p, int kv_len, int min_len) {
-  if (kv_len < min_len || (kWindow && kv_len > p.max_kv_len)) return 0;
-  if (ceil_div(kv_len, kPageSize) > p.max_pages_per_seq) return 0;
-  const int npages = VisiblePages<kWindow>(p, kv_len).count;
-  if (npages > p.num_splits * p.pages_per_chunk) return 0;
-  return npages == 0 ? 1 : ceil_div(npages, p.pages_per_chunk);
+__device__ __forceinline__ int request_chunks(int kv_len, int min_len, int max_pages_per_seq,
+                                              int num_splits, int pages_per_chunk) {
+  if (kv_len < min_len) return 0;
+  const int npages = ceil_div(kv_len, kPageSize);
+  if (npages > max_pages_per_seq || npages > num_splits * pages_per_chunk) return 0;
+  return npages == 0 ? 1 : ceil_div(npages, pages_per_chunk);
 }
 
 // Query row r of KV head kvh -> index of its [.., Hq] row in q/out/lse
@@ -135,10 +106,10 @@ constexpr int kBuckets = 8;   // size classes of shorter requests in the dispatc
 // limit in the top class kBuckets, shorter ones in classes 0..kBuckets-1 by
 // page count; empty and out-of-range requests in class 0.  Every CTA
 // evaluates the same instructions on the same lengths, so all agree.
-template <bool kVerify, bool kWindow>
+template <bool kVerify>
 __device__ __forceinline__ int size_class(const DecodeParams &p, int kv_len, float per_page) {
-  const int pages = VisiblePages<kWindow>(p, kv_len).count;
-  if (kv_len < (kVerify ? p.q_len : 0) || ceil_div(kv_len, kPageSize) > p.max_pages_per_seq ||
+  const int pages = ceil_div(kv_len, kPageSize);
+  if (kv_len < (kVerify ? p.q_len : 0) || pages > p.max_pages_per_seq ||
       pages > p.pages_per_chunk)
     return 0;
   if (pages == p.pages_per_chunk) return kBuckets;
@@ -152,7 +123,7 @@ __device__ __forceinline__ int size_class(const DecodeParams &p, int kv_len, flo
 // group of 32 requests come from two warp reductions of 6-bit fields, the
 // request from one ballot per group.  Returns -1 past the last request;
 // `kv_len` gets the request's length.
-template <bool kVerify, bool kWindow>
+template <bool kVerify>
 __device__ int request_by_size(const DecodeParams &p, int item, int &kv_len) {
   constexpr int kClasses = kBuckets + 1;
   constexpr int kLow = 5;                       // classes 0..4 in the first word, 5..8 in the second
@@ -179,7 +150,7 @@ __device__ int request_by_size(const DecodeParams &p, int item, int &kv_len) {
       }
     if (u >= kHeld) {
       l = b < p.batch ? __ldg(p.kv_lens + b) : 0;
-      c = b < p.batch ? size_class<kVerify, kWindow>(p, l, per_page) : -1;
+      c = b < p.batch ? size_class<kVerify>(p, l, per_page) : -1;
     }
     return c;
   };
@@ -193,7 +164,7 @@ __device__ int request_by_size(const DecodeParams &p, int item, int &kv_len) {
     for (int v = 0; v < kHeld; ++v)
       if (v == u) l = len[v];
     if (u >= kHeld) l = b < p.batch ? __ldg(p.kv_lens + b) : 0;
-    const int c = b < p.batch ? size_class<kVerify, kWindow>(p, l, per_page) : -1;
+    const int c = b < p.batch ? size_class<kVerify>(p, l, per_page) : -1;
 #pragma unroll
     for (int v = 0; v < kHeld; ++v)
       if (v == u) cls_of[v] = c;
@@ -228,11 +199,10 @@ __device__ int request_by_size(const DecodeParams &p, int item, int &kv_len) {
   return -1;                                    // not reached: the classes cover the batch
 }
 
-template <int NB, bool kVerify, bool kWindow>
+template <int NB, bool kVerify>
 __global__ void __launch_bounds__(kNW * 32, 2)
 decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const DecodeParams p) {
-  static_assert(!kVerify || !kWindow, "verification has no window");
   // CTA blockIdx.x: (KV head, head block) unit blockIdx.x % U of (request,
   // chunk) slot blockIdx.x / U.  Plans with one chunk per request and at
   // most a few waves of CTAs take the requests heaviest first; other plans
@@ -247,7 +217,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   int kv_len;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (p.sorted_dispatch) {                 // one chunk per request
-    b = request_by_size<kVerify, kWindow>(p, slot, kv_len);
+    b = request_by_size<kVerify>(p, slot, kv_len);
     chunk = 0;
     if (b < 0) return;
   } else {
@@ -257,7 +227,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   constexpr int kCols = kHeadsPerTile * NB;       // query rows of this CTA
 
   // verification needs its q_len tokens among the keys; plain decode allows kv_len = 0
-  const int nchunks = request_chunks<kWindow>(p, kv_len, kVerify ? p.q_len : 0);
+  const int nchunks = request_chunks(kv_len, kVerify ? p.q_len : 0, p.max_pages_per_seq,
+                                     p.num_splits, p.pages_per_chunk);
   bool bad = nchunks == 0;
   if (!bad && chunk >= nchunks) return;        // uniform over the CTA
   if (bad && chunk != 0) return;
@@ -269,8 +240,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   uint8_t *stages = smem + warp * kStages * kStageBytes;
 
   const int row0 = hb * kCols;                  // first query row of this CTA
-  const VisiblePages<kWindow> visible(p, bad ? 0 : kv_len);
-  const int npages = visible.count;
+  const int npages = bad ? 0 : ceil_div(kv_len, kPageSize);
   const int p_begin = chunk * p.pages_per_chunk;
   const int p_end = min(npages, p_begin + p.pages_per_chunk);
   const int first = p_begin + warp;
@@ -293,7 +263,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   // Page ids of this warp's pages, 32 at a time (lane j holds page j of the batch).
   auto load_ids = [&](int base) -> int {
     const int j = base + lane;
-    return j < n_my ? table[visible.page(first + j * kNW)] : -1;
+    return j < n_my ? table[first + j * kNW] : -1;
   };
   int ids_cur = load_ids(0), ids_next = load_ids(32);
   // page ids of this warp's first kStages pages, uniform over the warp
@@ -445,12 +415,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       for (int nb = 0; nb < NB; ++nb) mma_bf16_16816(s[nb], a, qb[nb][ks][0], qb[nb][ks][1]);
     }
 
-    const int tok0 = visible.page(first + i * kNW) * kPageSize;
-    const bool partial = tok0 + kPageSize > kv_len ||
-                         (kWindow && tok0 < visible.start && tok0 + kPageSize > p.first_tokens);
-    auto sees = [&](int tok) {
-      return tok < kv_len && (!kWindow || tok >= visible.start || tok < p.first_tokens);
-    };
+    const int tok0 = (first + i * kNW) * kPageSize;
+    const bool partial = tok0 + kPageSize > kv_len;
     // s[.][0]: token g / column 2t, [1]: token g / column 2t+1, [2], [3]: token g+8.
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -459,8 +425,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     if (partial) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        if (!sees(tok0 + g)) s[nb][0] = s[nb][1] = -INFINITY;
-        if (!sees(tok0 + g + 8)) s[nb][2] = s[nb][3] = -INFINITY;
+        if (tok0 + g >= kv_len) s[nb][0] = s[nb][1] = -INFINITY;
+        if (tok0 + g + 8 >= kv_len) s[nb][2] = s[nb][3] = -INFINITY;
       }
     }
     if constexpr (kVerify) {
@@ -516,17 +482,17 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
     uint32_t keep01 = 0xffffffffu, keep23 = 0xffffffffu;
     if (partial) {
-      keep01 = (sees(tok0 + 2 * t) ? 0x0000ffffu : 0u) |
-               (sees(tok0 + 2 * t + 1) ? 0xffff0000u : 0u);
-      keep23 = (sees(tok0 + 2 * t + 8) ? 0x0000ffffu : 0u) |
-               (sees(tok0 + 2 * t + 9) ? 0xffff0000u : 0u);
+      keep01 = (tok0 + 2 * t < kv_len ? 0x0000ffffu : 0u) |
+               (tok0 + 2 * t + 1 < kv_len ? 0xffff0000u : 0u);
+      keep23 = (tok0 + 2 * t + 8 < kv_len ? 0x0000ffffu : 0u) |
+               (tok0 + 2 * t + 9 < kv_len ? 0xffff0000u : 0u);
     }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       uint32_t a[4];
       const int c = 2 * mt + v_hi;
       ldsm_x4_trans(vbase + v_row * 128 + ((c ^ (v_row & 7)) << 4), a);
-      a[0] &= keep01;       // padded and masked slots may hold anything (even NaN)
+      a[0] &= keep01;       // padded slots may hold anything (even NaN)
       a[1] &= keep01;
       a[2] &= keep23;
       a[3] &= keep23;
@@ -670,15 +636,15 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   if (threadIdx.x == 0) p.counters[unit] = 0;
 }
 
-template <int NB, bool kVerify, bool kWindow = false>
+template <int NB, bool kVerify>
 cudaError_t launch_variant(const CUtensorMap &kmap, const CUtensorMap &vmap, const DecodeParams &p,
                            cudaStream_t stream, bool programmatic) {
-  cudaError_t err = set_smem_once<decode_kernel<NB, kVerify, kWindow>>(kSmemBytes);
+  cudaError_t err = set_smem_once<decode_kernel<NB, kVerify>>(kSmemBytes);
   if (err != cudaSuccess) return err;
   const unsigned long long ctas =
       static_cast<unsigned long long>(p.num_splits) * p.batch * p.num_kv_heads * p.head_blocks;
   if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-  return launch_kernel(decode_kernel<NB, kVerify, kWindow>, static_cast<unsigned>(ctas), kNW * 32,
+  return launch_kernel(decode_kernel<NB, kVerify>, static_cast<unsigned>(ctas), kNW * 32,
                        kSmemBytes, stream, programmatic, kmap, vmap, p);
 }
 
@@ -694,10 +660,6 @@ int decode_max_splits() { return 1024; }
 cudaError_t launch_decode(const CUtensorMap &kmap, const CUtensorMap &vmap, const DecodeParams &p,
                           cudaStream_t stream, bool programmatic) {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-  if (p.window > 0) {
-    return p.col_blocks == 1 ? launch_variant<1, false, true>(kmap, vmap, p, stream, programmatic)
-                             : launch_variant<2, false, true>(kmap, vmap, p, stream, programmatic);
-  }
   const bool verify = p.q_len > 1 || p.tree_mask != nullptr;
   if (!verify) {
     return p.col_blocks == 1 ? launch_variant<1, false>(kmap, vmap, p, stream, programmatic)

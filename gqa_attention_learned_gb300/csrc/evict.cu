@@ -4,29 +4,45 @@
 // and their mass move to the first slots of the request's pages (in place) or
 // of other pages.
 //
-// Two kernels.  select: one CTA per (request, KV head) finds the weight of the
-// last key that stays by a radix select over the weights' bits (exact, four
-// passes of 8 bits), takes ties from the lowest index on, and writes the kept
-// indices in order.  move: copies rows by that list.  In place is safe because
-// the r-th kept key has index >= r: a batch of rows is read whole before any
-// of it is written, and a write to slot r can only hit rows of this batch or
-// earlier ones.
+// Two kernels, the second launched under the first's end.
+// select: a cluster of CTAs per (request, KV head), each with a contiguous
+//   share of the keys.  A radix select over the weights' order-preserving bits
+//   (11 + 11 + 10 bits; histograms in shared memory, joined in the first CTA's
+//   through distributed shared memory) gives the weight of the last key that
+//   stays and how many of its equals stay, lowest index first.  Two more
+//   passes count and write the kept indices in order, by ballots and prefix
+//   sums over warps and CTAs.  Weights after the first pass come from L1 / L2.
+// move: copies rows by that list; a CTA owns a 32-byte column (one sector) of
+//   a (request, KV head)'s K or V rows, or its mass.  In place is safe within
+//   a column because the r-th kept key has index >= r: a batch of rows is read
+//   whole before any of it is written, and a write to slot r can only hit rows
+//   of this batch or earlier ones.
 // Bound by HBM: 4 bytes of mass per key, 512 bytes of K and V per kept one.
 
 #include "kernels.cuh"
 #include "ptx.cuh"
 
+#include <cooperative_groups.h>
+
+#include <algorithm>
 #include <cmath>
 
 namespace sa {
 namespace {
 
-constexpr int kSelectThreads = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxSplit = 8;             // CTAs per (request, KV head)
+constexpr int kKeysPerCta = 4096;        // keys per CTA to aim for
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 4;             // rows in flight per thread and batch
+constexpr int kColumns = 4;              // 32-byte columns of a row
+constexpr int kRoles = 2 * kColumns + 1; // K columns, V columns, mass
 
-__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Order-preserving bits of a weight: larger weight, larger number; -0 = +0,
 // NaN below everything.
@@ -36,37 +52,57 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sum of v over the block; `total` gets the sum.
-__device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total) {
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+struct SelectSmem {
+  int hist[kBins];
+  int warp_sure[kSelectWarps], warp_equal[kSelectWarps];
+  int cta_sure[kMaxSplit], cta_equal[kMaxSplit];
+  uint32_t prefix;
+  int left;
+};
+
+// The bin of rank 0's joined histogram that holds the `left`-th largest, and
+// what is left to take within it.  Called by the whole CTA.
+__device__ void find_bin(SelectSmem &s, int left, int &bin, int &rest) {
+  constexpr int kPer = kBins / kSelectThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  // thread 0 owns the highest bins
+  const int top = kBins - 1 - static_cast<int>(threadIdx.x) * kPer;
+  int mine = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) mine += s.hist[top - k];
+  int upto = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
+    const int y = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += y;
   }
-  __syncthreads();                                       // the previous scan's sums are read
-  if (lane == 31) warp_sums[warp] = x;
+  if (lane == 31) s.warp_sure[warp] = upto;
   __syncthreads();
-  int before = 0, sum = 0;
 #pragma unroll
-  for (int w = 0; w < kSelectWarps; ++w) {
-    const int s = warp_sums[w];
-    before += w < warp ? s : 0;
-    sum += s;
+  for (int w = 0; w < kSelectWarps; ++w)
+    if (w < warp) upto += s.warp_sure[w];
+  int above = upto - mine;
+  if (above < left && upto >= left) {                    // exactly one thread
+    int b = top;
+    while (above + s.hist[b] < left) above += s.hist[b--];
+    s.prefix = static_cast<uint32_t>(b);
+    s.left = left - above;
   }
-  total = sum;
-  return before + x - v;
+  __syncthreads();
+  bin = static_cast<int>(s.prefix);
+  rest = s.left;
 }
 
 __global__ void __launch_bounds__(kSelectThreads)
 evict_select_kernel(const EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[kSelectWarps];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_left;
-  const int unit = blockIdx.x, kvh = unit % p.num_kv_heads, b = unit / p.num_kv_heads;
-  const int tid = threadIdx.x;
+  __shared__ SelectSmem s;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int split = p.split;
+  const int rank = static_cast<int>(blockIdx.x % split), unit = static_cast<int>(blockIdx.x / split);
+  const int kvh = unit % p.num_kv_heads, b = unit / p.num_kv_heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependency_wait();
   const int n = p.kv_lens[b];
   int *kept = p.kept + static_cast<size_t>(unit) * p.budget;
@@ -81,128 +117,235 @@ evict_select_kernel(const EvictParams p) {
     for (int i = tid; i < npages; i += kSelectThreads) bad = bad || src[i] < 0 || src[i] >= p.num_pages;
     for (int i = tid; i < dst_pages; i += kSelectThreads) bad = bad || dst[i] < 0 || dst[i] >= p.num_pages;
   }
-  bad = __syncthreads_or(bad);
-  if (tid == 0 && kvh == 0) p.new_kv_lens[b] = bad ? -1 : count;
-  for (int i = bad ? tid : count + tid; i < p.budget; i += kSelectThreads) kept[i] = -1;
+  bad = __syncthreads_or(bad);                           // the same in every CTA of the cluster
+  if (tid == 0 && rank == 0 && kvh == 0) p.new_kv_lens[b] = bad ? -1 : count;
+  const int step = split * kSelectThreads;
+  for (int i = (bad ? 0 : count) + rank * kSelectThreads + tid; i < p.budget; i += step) kept[i] = -1;
   if (bad) return;
   if (n <= p.budget) {
-    for (int i = tid; i < n; i += kSelectThreads) kept[i] = i;
+    for (int i = rank * kSelectThreads + tid; i < n; i += step) kept[i] = i;
     return;
   }
 
   const float *mass = p.mass + static_cast<size_t>(unit) * p.mass_stride;
   const int lo = p.first_tokens, hi = n - p.recent;       // the keys that compete
-  int want = p.budget - p.first_tokens - p.recent;        // how many of them stay
-  // the want-th largest weight, from the top 8 bits down
+  const int want = p.budget - p.first_tokens - p.recent;  // how many of them stay
+  // this warp's keys: a contiguous run, whole multiples of 32
+  const int run = cdiv(cdiv(n, split * kSelectWarps), 32) * 32;
+  const long long from = static_cast<long long>(rank * kSelectWarps + warp) * run;
+  const int begin = static_cast<int>(min(static_cast<long long>(n), from));
+  const int end = static_cast<int>(min(static_cast<long long>(n), from + run));
+
+  // ---- the want-th largest weight, from the top bits down
   uint32_t prefix = 0;
   int left = want;                                        // to take among those with the prefix
   if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t high = shift == 24 ? 0u : ~((1u << (shift + 8)) - 1u);
-      for (int i = lo + tid; i < hi; i += kSelectThreads) {
-        const uint32_t u = order_bits(mass[i]);
-        if ((u & high) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1);
+    uint32_t known = 0;                                   // bits of the prefix found so far
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
+      for (int i = tid; i < kBins; i += kSelectThreads) s.hist[i] = 0;
+      cluster.sync();
+      constexpr int kUnroll = 4;
+      for (int i0 = begin; i0 < end; i0 += 32 * kUnroll) {
+        float v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int i = i0 + 32 * u + lane;
+          v[u] = i < end ? mass[i] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int i = i0 + 32 * u + lane;
+          const uint32_t bits = order_bits(v[u]);
+          if (i < end && i >= lo && i < hi && (bits & known) == prefix)
+            atomicAdd(&s.hist[(bits >> shift) & digits], 1);
+        }
       }
-      __syncthreads();
-      if (tid == 0) {
-        int bin = 255, rest = left;
-        while (hist[bin] < rest) rest -= hist[bin--];
-        s_prefix = prefix | (static_cast<uint32_t>(bin) << shift);
-        s_left = rest;
+      if (split > 1) {
+        __syncthreads();
+        if (rank != 0) {
+          int *joined = cluster.map_shared_rank(s.hist, 0);
+          for (int i = tid; i < kBins; i += kSelectThreads)
+            if (s.hist[i]) atomicAdd(joined + i, s.hist[i]);
+        }
+        cluster.sync();
+        if (rank == 0) {
+          int bin, rest;
+          find_bin(s, left, bin, rest);
+          if (tid < split) {
+            SelectSmem *peer = cluster.map_shared_rank(&s, tid);
+            peer->prefix = static_cast<uint32_t>(bin);
+            peer->left = rest;
+          }
+        }
+        cluster.sync();
+        prefix |= s.prefix << shift;
+        left = s.left;
+      } else {
+        __syncthreads();
+        int bin, rest;
+        find_bin(s, left, bin, rest);
+        prefix |= static_cast<uint32_t>(bin) << shift;
+        left = rest;
       }
-      __syncthreads();
-      prefix = s_prefix;
-      left = s_left;
+      known |= digits << shift;
+      __syncthreads();                                    // prefix and hist are read
     }
   }
-  // ordered compaction: weights above the threshold, and the first `left` equal to it
-  int at = 0, equal_before = 0;
-  for (int base = 0; base < n; base += kSelectThreads) {
-    const int i = base + tid;
-    bool keep = false, equal = false;
-    if (i < n) {
-      if (i < lo || i >= hi) {
-        keep = true;
-      } else if (want > 0) {
-        const uint32_t u = order_bits(mass[i]);
-        keep = u > prefix;
-        equal = u == prefix;
-      }
+
+  // ---- how many stay for sure, and how many equal the threshold, per warp
+  // and CTA
+  auto kind = [&](int i, bool &sure, bool &equal) {
+    sure = equal = false;
+    if (i >= end) return;
+    if (i < lo || i >= hi) {
+      sure = true;
+    } else if (want > 0) {
+      const uint32_t bits = order_bits(mass[i]);
+      sure = bits > prefix;
+      equal = bits == prefix;
     }
-    int total;
-    const int e = block_scan(equal ? 1 : 0, warp_sums, total);
-    keep = keep || (equal && equal_before + e < left);
-    equal_before += total;
-    const int r = block_scan(keep ? 1 : 0, warp_sums, total);
-    if (keep) kept[at + r] = i;
-    at += total;
+  };
+  int n_sure = 0, n_equal = 0;
+#pragma unroll 4
+  for (int i = begin + lane; i < end; i += 32) {
+    bool sure, equal;
+    kind(i, sure, equal);
+    n_sure += sure;
+    n_equal += equal;
   }
+  n_sure = warp_sum(n_sure);
+  n_equal = warp_sum(n_equal);
+  if (lane == 0) {
+    s.warp_sure[warp] = n_sure;
+    s.warp_equal[warp] = n_equal;
+  }
+  __syncthreads();
+  int cta_sure = 0, cta_equal = 0, sure_before = 0, equal_before = 0;
+#pragma unroll
+  for (int w = 0; w < kSelectWarps; ++w) {
+    if (w == warp) {
+      sure_before = cta_sure;
+      equal_before = cta_equal;
+    }
+    cta_sure += s.warp_sure[w];
+    cta_equal += s.warp_equal[w];
+  }
+  if (split > 1) {
+    if (tid < split) {
+      SelectSmem *peer = cluster.map_shared_rank(&s, tid);
+      peer->cta_sure[rank] = cta_sure;
+      peer->cta_equal[rank] = cta_equal;
+    }
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) {
+      sure_before += s.cta_sure[r];
+      equal_before += s.cta_equal[r];
+    }
+  }
+
+  // ---- the kept indices, in order
+  int at = sure_before + min(equal_before, left);         // kept before this warp's keys
+  const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    bool sure, equal;
+    kind(i0 + lane, sure, equal);
+    const unsigned eq = __ballot_sync(0xffffffffu, equal);
+    const bool keep = sure || (equal && equal_before + __popc(eq & below) < left);
+    const unsigned all = __ballot_sync(0xffffffffu, keep);
+    if (keep) kept[at + __popc(all & below)] = i0 + lane;
+    at += __popc(all);
+    equal_before += __popc(eq);
+  }
+  if (split > 1) cluster.sync();                          // peers have written this CTA's counts
 }
 
 __global__ void __launch_bounds__(kMoveThreads)
 evict_move_kernel(const EvictParams p) {
-  // CTA: K rows, V rows or mass of one (request, KV head)
-  const int unit = blockIdx.x % (p.batch * p.num_kv_heads);
-  const int what = blockIdx.x / (p.batch * p.num_kv_heads);
+  const int role = static_cast<int>(blockIdx.x % kRoles), unit = static_cast<int>(blockIdx.x / kRoles);
   const int kvh = unit % p.num_kv_heads, b = unit / p.num_kv_heads;
   grid_dependency_wait();
   const int count = p.new_kv_lens[b];
   if (count < 0) return;
   const int n = p.kv_lens[b];
   const int *kept = p.kept + static_cast<size_t>(unit) * p.budget;
-  if (what == 2) {
+  if (role == 2 * kColumns) {
     const float *src = p.mass + static_cast<size_t>(unit) * p.mass_stride;
     float *dst = p.dst_mass + static_cast<size_t>(unit) * p.dst_mass_stride;
-    for (int base = 0; base < count; base += kMoveThreads) {
-      const int r = base + threadIdx.x;
-      const float v = r < count ? src[kept[r]] : 0.f;
+    for (int base = 0; base < count; base += kMoveThreads * kMoveRows) {
+      float v[kMoveRows];
+#pragma unroll
+      for (int u = 0; u < kMoveRows; ++u) {
+        const int r = base + u * kMoveThreads + static_cast<int>(threadIdx.x);
+        if (r < count) v[u] = src[kept[r]];
+      }
       __syncthreads();
-      if (r < count) dst[r] = v;
+#pragma unroll
+      for (int u = 0; u < kMoveRows; ++u) {
+        const int r = base + u * kMoveThreads + static_cast<int>(threadIdx.x);
+        if (r < count) dst[r] = v[u];
+      }
     }
     __syncthreads();
     // evicted places start again from nothing
     for (int i = count + threadIdx.x; i < min(n, p.dst_mass_stride); i += kMoveThreads) dst[i] = 0.f;
     return;
   }
-  uint4 *cache = reinterpret_cast<uint4 *>(what == 0 ? p.k_cache : p.v_cache);
+  uint4 *cache = reinterpret_cast<uint4 *>(role < kColumns ? p.k_cache : p.v_cache);
   const int32_t *src_table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
   const int32_t *dst_table = p.dst_page_table + static_cast<size_t>(b) * p.dst_max_pages;
+  const bool in_place = src_table == dst_table;
   constexpr int kPieces = kHeadDim * 2 / 16;              // 16-byte pieces of a row
-  constexpr int kRowsAtOnce = kMoveThreads / kPieces;
-  const int piece = threadIdx.x % kPieces, row = threadIdx.x / kPieces;
+  const int piece = (role % kColumns) * (kPieces / kColumns);
   auto address = [&](const int32_t *table, int key) {
-    return (static_cast<size_t>(table[key / kPageSize]) * p.num_kv_heads + kvh) * kPageSize * kPieces +
+    return cache + (static_cast<size_t>(table[key / kPageSize]) * p.num_kv_heads + kvh) * (kPageSize * kPieces) +
            (key % kPageSize) * kPieces + piece;
   };
-  for (int base = 0; base < count; base += kRowsAtOnce * kMoveRows) {
-    uint4 v[kMoveRows];
+  for (int base = 0; base < count; base += kMoveThreads * kMoveRows) {
+    uint4 v[kMoveRows][2];
+    bool moves[kMoveRows];
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
-      const int r = base + u * kRowsAtOnce + row;
-      if (r < count) v[u] = cache[address(src_table, kept[r])];
+      const int r = base + u * kMoveThreads + static_cast<int>(threadIdx.x);
+      const int from = r < count ? kept[r] : r;
+      moves[u] = r < count && !(in_place && from == r);   // a row may be where it belongs already
+      if (moves[u]) {
+        const uint4 *src = address(src_table, from);
+        v[u][0] = src[0];
+        v[u][1] = src[1];
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
-      const int r = base + u * kRowsAtOnce + row;
-      if (r < count) cache[address(dst_table, r)] = v[u];
+      const int r = base + u * kMoveThreads + static_cast<int>(threadIdx.x);
+      if (moves[u]) {
+        uint4 *dst = address(dst_table, r);
+        dst[0] = v[u][0];
+        dst[1] = v[u][1];
+      }
     }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream) {
+cudaError_t launch_evict(EvictParams &p, cudaStream_t stream) {
   const unsigned long long units = static_cast<unsigned long long>(p.batch) * p.num_kv_heads;
   if (units == 0) return cudaSuccess;
-  if (3 * units > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-  const cudaError_t err = launch_kernel(evict_select_kernel, static_cast<unsigned>(units),
-                                        kSelectThreads, 0, stream, true, p);
+  p.split = 1;
+  while (p.split < kMaxSplit && p.max_kv_len > kKeysPerCta * p.split) p.split *= 2;
+  if (kRoles * units > 0x7fffffffull || p.split * units > 0x7fffffffull)
+    return cudaErrorInvalidConfiguration;
+  const cudaError_t err =
+      launch_clusters(evict_select_kernel, static_cast<unsigned>(p.split * units),
+                      static_cast<unsigned>(p.split), kSelectThreads, 0, stream, true, p);
   if (err != cudaSuccess) return err;
-  return launch_kernel(evict_move_kernel, static_cast<unsigned>(3 * units), kMoveThreads, 0, stream,
-                       true, p);
+  return launch_kernel(evict_move_kernel, static_cast<unsigned>(kRoles * units), kMoveThreads, 0,
+                       stream, true, p);
 }
 
 }  // namespace sa

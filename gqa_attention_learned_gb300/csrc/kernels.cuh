@@ -48,6 +48,27 @@ inline cudaError_t launch_kernel(void (*kernel)(Params...), unsigned grid, unsig
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The same with clusters of `cluster` CTAs (`grid` counts CTAs, a multiple).
+template <typename... Params, typename... Args>
+inline cudaError_t launch_clusters(void (*kernel)(Params...), unsigned grid, unsigned cluster,
+                                   unsigned block, int smem, cudaStream_t stream,
+                                   bool programmatic, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = programmatic ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 constexpr int kPageSize = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -76,9 +97,6 @@ struct DecodeParams {
   int head_blocks;              // CTAs per (request, KV head, chunk) = ceil(rows / (8 col_blocks))
   int num_pages, num_splits, pages_per_chunk;
   int sorted_dispatch;          // one chunk per request: requests heaviest first
-  // Sliding window (plain decode only; 0: none): the token sees the keys
-  // j >= kv_len - window and j < first_tokens.
-  int window, first_tokens, max_kv_len;
 };
 
 // Column blocks per CTA for q_len * group query rows per KV head.
@@ -94,6 +112,32 @@ int decode_max_splits();
 // but kv_lens and the page table).
 cudaError_t launch_decode(const CUtensorMap &kmap, const CUtensorMap &vmap,
                           const DecodeParams &p, cudaStream_t stream, bool programmatic);
+
+// ---------------------------------------------------------- windowed decode
+// One token per request that sees the keys j >= kv_len - window and j <
+// first_tokens.  Chunks and CTAs count pages with a visible key.
+struct WindowDecodeParams {
+  const uint16_t *q;               // bf16 [B][Hq][64]
+  const uint16_t *k_cache, *v_cache;   // bf16 [num_pages][Hkv][16][64]
+  const int32_t *page_table;       // [B][max_pages_per_seq]
+  const int32_t *kv_lens;          // [B]
+  const float *sinks;              // [Hq]
+  uint16_t *out;                   // bf16 [B][Hq][64]
+  float *lse;                      // [B][Hq] or null
+  int *counters;                   // [B][Hkv * head_blocks], zero between calls (splits > 1)
+  float *ws_o;                     // fp32 [splits][B][Hq][64] (splits > 1)
+  float *ws_lse;                   // fp32 [splits][B][Hq] (base-2 lse)
+  float scale_log2;
+  int max_pages_per_seq, batch, num_qo_heads, num_kv_heads, group;
+  int col_blocks;                  // 8-head blocks per CTA (1 or 2)
+  int head_blocks;                 // CTAs per (request, KV head, chunk)
+  int num_pages, num_splits, pages_per_chunk;
+  int window, first_tokens, max_kv_len;   // window and first_tokens <= max_kv_len
+};
+
+int window_decode_ctas_per_sm();
+cudaError_t launch_window_decode(const WindowDecodeParams &p, cudaStream_t stream,
+                                 bool programmatic);
 
 // ---------------------------------------------------------------- prefill
 struct PrefillParams {
@@ -160,7 +204,11 @@ struct MassParams {
   int max_pages_per_seq, num_pages;
   int num_chunks, pages_per_chunk;   // decode form: CTAs per (request, KV head)
   int tile_tokens;                   // prefill form: tokens per query tile = 128 / group
+  int split;                         // prefill form: CTAs that share the query tiles of a key pair
+  int pairs_per_cta;                 // prefill form: key pairs a CTA takes (1 when split > 1)
 };
+
+int prefill_mass_pair_keys();        // keys of a key pair
 
 int decode_mass_warps();         // pages a CTA of the decode form works on at a time
 cudaError_t launch_decode_mass(const MassParams &p, cudaStream_t stream);
@@ -180,9 +228,10 @@ struct EvictParams {
   int batch, num_kv_heads, num_pages, max_kv_len;
   int max_pages_per_seq, dst_max_pages, mass_stride, dst_mass_stride;
   int budget, first_tokens, recent;
+  int split;                     // CTAs per (request, KV head) that select
 };
 
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams &p, cudaStream_t stream);   // sets p.split
 
 // --------------------------------------------------------------- prologue
 struct PrologueParams {
@@ -207,14 +256,12 @@ cudaError_t launch_prologue(const PrologueParams &p, cudaStream_t stream);
 // the launch.  launch_flags is one of SINKATTN_LAUNCH_*.  With zero_counters,
 // a plan of more than one split first clears the workspace's merge counters
 // on the stream (cudaMemsetAsync, queued only after every check has passed);
-// a single-split plan touches no workspace at all.  window > 0 (q_len 1, no
-// mask) is the sliding-window form.
+// a single-split plan touches no workspace at all.
 int decode_entry(const void *q, const void *k_cache, const void *v_cache,
                  const int32_t *page_table, int max_pages_per_seq, const int32_t *kv_lens,
                  const uint64_t *tree_mask, const float *sinks, float scale, void *out, float *lse,
                  int batch, int q_len, int num_qo_heads, int num_kv_heads, int head_dim,
                  int page_size, int num_pages, int max_kv_len, int num_splits, void *workspace,
-                 size_t workspace_bytes, int launch_flags, bool zero_counters, void *stream,
-                 int window = 0, int first_tokens = 0);
+                 size_t workspace_bytes, int launch_flags, bool zero_counters, void *stream);
 
 }  // namespace sa

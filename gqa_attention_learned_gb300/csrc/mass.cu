@@ -17,13 +17,19 @@
 // flight per warp.
 //
 // prefill_mass (ragged rows at the end of the keys) is bound by its
-// exponentials, one per (row, key).  A CTA owns 128 keys of one KV head and
-// streams the query rows that see them, 128 (token, head) rows at a time, past
-// the resident K tile: S^T[128 keys x 128 rows] by tcgen05 into tensor memory,
-// one thread per key adds its row of weights in registers.
+// exponentials, one per (row, key).  A CTA holds 256 keys of one KV head and
+// streams the query rows that see them past the resident K, 128 (token, head)
+// rows at a time: S^T[128 keys x 128 rows] by tcgen05 into tensor memory for
+// each of two groups of four warps, in which one thread per key adds its row
+// of weights in registers -- no sums across threads.  Long prompts split the
+// query tiles of a key pair over a cluster of CTAs, joined in rank order
+// through distributed shared memory; few query rows give each CTA a run of key
+// pairs instead, whose K tiles stream as well.
 
 #include "kernels.cuh"
 #include "ptx.cuh"
+
+#include <cooperative_groups.h>
 
 #include <cmath>
 
@@ -82,9 +88,19 @@ decode_mass_kernel(const MassParams p) {
   if (n_my == 0) return;                                 // warp-uniform; no barriers below
   const int32_t *table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
 
+  // ids of this warp's pages, 32 at a time (lane j holds page j of the batch)
+  auto load_ids = [&](int base) -> int {
+    const int j = base + lane;
+    return j < n_my ? __ldg(table + first + j * kDecodeWarps) : -1;
+  };
+  int batch_ids = load_ids(0), next_ids = load_ids(32);
   auto page_id = [&](int i) -> int {                     // page i of this warp, -1: none or bad
     if (i >= n_my) return -1;
-    const int id = __ldg(table + first + i * kDecodeWarps);
+    if ((i & 31) == 0 && i > 0) {
+      batch_ids = next_ids;
+      next_ids = load_ids(i + 32);
+    }
+    const int id = __shfl_sync(0xffffffffu, batch_ids, i & 31);
     return id < p.num_pages ? id : -1;
   };
   // lane 0 of a quad adds to key g of a page, lane 1 to key g + 8
@@ -164,26 +180,29 @@ decode_mass_kernel(const MassParams p) {
 }
 
 // ----------------------------------------------------------------- prefill
-constexpr int kKeys = 128;                       // keys per CTA
-constexpr int kRows = 128;                       // query rows per streamed tile
-constexpr int kQStages = 3;
+constexpr int kKeys = 128;                       // keys per tile: rows of S^T
+constexpr int kRows = 128;                       // query rows per streamed tile: columns of S^T
+constexpr int kKStages = 3, kQStages = 3;
 constexpr int kTileBytes = 128 * kHeadDim * 2;
-constexpr int kThreads = 192;
-constexpr int kLoadWarp = 4, kMmaWarp = 5;
-constexpr uint32_t kTmemCols = 256;              // two score buffers
+constexpr int kGroups = 2;                       // groups of four warps, one key tile each
+constexpr int kThreads = 128 * kGroups + 64;
+constexpr int kLoadWarp = 4 * kGroups, kMmaWarp = kLoadWarp + 1;
+constexpr uint32_t kTmemCols = 128 * kGroups;    // one score buffer per group
 
 constexpr int kOffK = 0;
-constexpr int kOffQ = kTileBytes;
+constexpr int kOffQ = kOffK + kKStages * kTileBytes;
 constexpr int kOffL = kOffQ + kQStages * kTileBytes;
-constexpr int kOffBars = kOffL + kQStages * kRows * 4;
+constexpr int kOffSum = kOffL + kQStages * kRows * 4;
+constexpr int kOffBars = kOffSum + kGroups * kKeys * 4;
 constexpr int kSmemBytes = kOffBars + 256 + 1024;
+static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
 
 struct Bars {
-  uint64_t k_full;
+  uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t q_full[kQStages], q_empty[kQStages];  // Q and -lse of a tile
-  uint64_t s_full[2], s_free[2];
+  uint64_t s_full[kGroups], s_free[kGroups];
   uint32_t tmem_base;
-  int bad;
+  int bad_wait;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
@@ -206,73 +225,87 @@ __device__ __forceinline__ void add_chunk(uint32_t (&r)[32], const float4 *nl, u
   }
 }
 
+// The steps of one CTA: for each of its key pairs (256 keys, one tile of 128
+// per group of warps) the query tiles that see it, of which this CTA of the
+// cluster takes every split-th.  Every role walks the same steps.
+struct Steps {
+  int q_len, kv_len, shift, tile_tokens, split, rank;
+  int key0, i_start, n;               // of the current pair: first key, first token, steps
+  int skip[kGroups];                  // first step that group takes part in (n: none)
+  __device__ __forceinline__ void pair(int kp) {
+    key0 = kp * kKeys * kGroups;
+    i_start = max(0, key0 - shift);   // first token that sees a key of the pair
+    const int tiles = cdiv(q_len - i_start, tile_tokens);
+    n = tiles > rank ? cdiv(tiles - rank, split) : 0;
+#pragma unroll
+    for (int w = 0; w < kGroups; ++w) {
+      const int first_key = key0 + w * kKeys;
+      // tile that holds the first token to see the group's keys
+      const int tile = (max(0, first_key - shift) - i_start) / tile_tokens;
+      skip[w] = first_key >= kv_len ? n : min(n, max(0, cdiv(tile - rank, split)));
+    }
+  }
+  __device__ __forceinline__ int token(int step) const {
+    return i_start + (step * split + rank) * tile_tokens;
+  }
+};
+
 __global__ void __launch_bounds__(kThreads, 2)
 prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap, const MassParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // ---- work item: (key tile, request, KV head); earlier tiles, which more
-  // rows see, first
-  const int per_tile = p.num_seqs * p.num_kv_heads;
-  const int kt = static_cast<int>(blockIdx.x / per_tile);
-  const int unit = static_cast<int>(blockIdx.x % per_tile);
+  // ---- work item: (run of key pairs, request, KV head, share of the query
+  // tiles); earlier keys, which more rows see, first
+  const int item = static_cast<int>(blockIdx.x / p.split);
+  const int per_run = p.num_seqs * p.num_kv_heads;
+  const int run = item / per_run, unit = item % per_run;
   const int kvh = unit % p.num_kv_heads, seq = unit / p.num_kv_heads;
   const int q_start = p.cu_seqlens_q[seq], q_end = p.cu_seqlens_q[seq + 1];
-  const int q_len = q_end - q_start, kv_len = p.kv_lens[seq];
+  Steps st;
+  st.q_len = q_end - q_start;
+  st.kv_len = p.kv_lens[seq];
+  st.shift = st.kv_len - st.q_len;                       // position of the first row's token
+  st.tile_tokens = p.tile_tokens;
+  st.split = p.split;
+  st.rank = static_cast<int>(blockIdx.x % p.split);
   float *mass = p.mass + static_cast<size_t>(unit) * p.mass_stride;
-  if (bad_request(p, kv_len) || q_start < 0 || q_len < 0 || q_end > p.total_q ||
-      q_len > p.max_q_len || kv_len < q_len) {
-    if (kt == 0) poison_row(p, mass);
-    return;
+  if (bad_request(p, st.kv_len) || q_start < 0 || st.q_len < 0 || q_end > p.total_q ||
+      st.q_len > p.max_q_len || st.kv_len < st.q_len) {
+    if (run == 0 && st.rank == 0) poison_row(p, mass);
+    return;                                              // the whole cluster returns
   }
-  const int key0 = kt * kKeys;
-  if (key0 >= kv_len || q_len == 0) return;
-  const int shift = kv_len - q_len;                      // position of the first row's token
-  const int i_first = max(0, key0 - shift);              // first token that sees a key of the tile
-  const int n_tiles = cdiv(q_len - i_first, p.tile_tokens);
+  const int kp_begin = run * p.pairs_per_cta;
+  const int kp_end = min(kp_begin + p.pairs_per_cta, cdiv(st.kv_len, kKeys * kGroups));
+  if (kp_begin >= kp_end || st.q_len == 0) return;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
   Bars &bar = *reinterpret_cast<Bars *>(smem + kOffBars);
+  auto sK = [&](int s) { return smem + kOffK + s * kTileBytes; };
   auto sQ = [&](int s) { return smem + kOffQ + s * kTileBytes; };
   auto sL = [&](int s) { return reinterpret_cast<float *>(smem + kOffL) + s * kRows; };
+  float *sums = reinterpret_cast<float *>(smem + kOffSum);
 
   if (warp == kMmaWarp) {
     tmem_alloc(&bar.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kLoadWarp) {
-    if (lane == 0) {
-      mbar_init(&bar.k_full, 1);
-      for (int s = 0; s < kQStages; ++s) {
-        mbar_init(&bar.q_full[s], 1 + 32);
-        mbar_init(&bar.q_empty[s], 1 + 128);             // the MMAs, and the readers of -lse
-      }
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(&bar.s_full[s], 1);
-        mbar_init(&bar.s_free[s], 128);
-      }
-      bar.bad = 0;
-      fence_mbar_init();
+  if (threadIdx.x == kLoadWarp * 32) {
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&bar.k_full[s], 1);
+      mbar_init(&bar.k_empty[s], 1);
     }
-    __syncwarp();
-    // K: lanes 0..7 each own one 16-key page of the tile
-    const int pg = key0 / kPageSize + lane;
-    int id = -1;
-    if (lane < kKeys / kPageSize && pg < cdiv(kv_len, kPageSize)) {
-      id = p.page_table[static_cast<size_t>(seq) * p.max_pages_per_seq + pg];
-      if (id < 0 || id >= p.num_pages) {
-        atomicOr(&bar.bad, 1 << lane);
-        id = -1;
-      }
+    for (int s = 0; s < kQStages; ++s) {
+      mbar_init(&bar.q_full[s], 1 + 32);                 // the copy, and the lanes that write -lse
+      mbar_init(&bar.q_empty[s], 1 + 128 * kGroups);     // the MMAs, and the readers of -lse
     }
-    const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
-    if (lane == 0) mbar_arrive_expect_tx(&bar.k_full, __popc(mask) * kPageSize * kHeadDim * 2);
-    __syncwarp();
-    if (id >= 0)
-      tma_load_3d(smem + kOffK + lane * kPageSize * kHeadDim * 2, &kmap, &bar.k_full, 0,
-                  kvh * kPageSize, id);
-    __syncwarp();
+    for (int w = 0; w < kGroups; ++w) {
+      mbar_init(&bar.s_full[w], 1);
+      mbar_init(&bar.s_free[w], 128);
+    }
+    bar.bad_wait = 0;
+    fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
@@ -280,113 +313,196 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
   const uint32_t tmem = bar.tmem_base;
 
   if (warp == kLoadWarp) {
-    // ----------------------------------------------- query tiles and -lse
-    for (int j = 0; j < n_tiles; ++j) {
-      const int s = j % kQStages;
-      if (j >= kQStages && !__all_sync(0xffffffffu, mbar_wait(&bar.q_empty[s], ((j / kQStages) + 1) & 1))) {
-        if (lane == 0) atomicOr(&bar.bad, 1 << 30);
-        break;
-      }
-      const int tok0 = q_start + i_first + j * p.tile_tokens;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar.q_full[s], p.tile_tokens * p.group * kHeadDim * 2);
-        tma_load_3d(sQ(s), &qmap, &bar.q_full[s], 0, kvh * p.group, tok0);
-      }
-      const int rows = min(p.tile_tokens, q_end - tok0) * p.group;
-      for (int r = lane; r < kRows; r += 32) {
-        float l = INFINITY;                              // columns past the rows add nothing
-        if (r < rows) {
-          const int tk = r / p.group;
-          l = __ldg(p.lse + static_cast<size_t>(tok0 + tk) * p.num_qo_heads + kvh * p.group +
-                    (r - tk * p.group));
+    // ---------------------------------------- key tiles, query tiles and -lse
+    bool ok = true;
+    int kn = 0, qn = 0;                                  // tiles loaded so far
+    for (int kp = kp_begin; ok && kp < kp_end; ++kp) {
+      st.pair(kp);
+      for (int j = 0; ok && j < st.n; ++j, ++qn) {
+        for (int w = 0; w < kGroups; ++w) {
+          if (j != 0 || st.skip[w] >= st.n) continue;
+          // lanes 0..7 each own one 16-key page of the tile
+          const int s = kn % kKStages;
+          const int pg = (st.key0 + w * kKeys) / kPageSize + lane;
+          int id = -1;                                   // not in the pool: not copied
+          if (lane < kKeys / kPageSize && pg < cdiv(st.kv_len, kPageSize)) {
+            id = p.page_table[static_cast<size_t>(seq) * p.max_pages_per_seq + pg];
+            if (id >= p.num_pages) id = -1;
+          }
+          if (kn >= kKStages && !__all_sync(0xffffffffu, mbar_wait(&bar.k_empty[s], ((kn / kKStages) + 1) & 1))) {
+            ok = false;
+            break;
+          }
+          const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
+          if (lane == 0)
+            mbar_arrive_expect_tx(&bar.k_full[s], __popc(mask) * kPageSize * kHeadDim * 2);
+          __syncwarp();
+          if (id >= 0)
+            tma_load_3d(sK(s) + lane * kPageSize * kHeadDim * 2, &kmap, &bar.k_full[s], 0,
+                        kvh * kPageSize, id);
+          __syncwarp();
+          ++kn;
         }
-        sL(s)[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        const int s = qn % kQStages;
+        if (ok && qn >= kQStages && !__all_sync(0xffffffffu, mbar_wait(&bar.q_empty[s], ((qn / kQStages) + 1) & 1)))
+          ok = false;
+        if (!ok) break;
+        const int tok0 = q_start + st.token(j);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.q_full[s], p.tile_tokens * p.group * kHeadDim * 2);
+          tma_load_3d(sQ(s), &qmap, &bar.q_full[s], 0, kvh * p.group, tok0);
+        }
+        const int rows = min(p.tile_tokens, q_end - tok0) * p.group;
+#pragma unroll
+        for (int r = lane; r < kRows; r += 32) {
+          float l = INFINITY;                            // columns past the rows add nothing
+          if (r < rows) {
+            const int tk = r / p.group;
+            l = __ldg(p.lse + static_cast<size_t>(tok0 + tk) * p.num_qo_heads + kvh * p.group +
+                      (r - tk * p.group));
+          }
+          sL(s)[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        }
+        mbar_arrive(&bar.q_full[s]);
       }
-      mbar_arrive(&bar.q_full[s]);
     }
+    if (!ok && lane == 0) atomicOr(&bar.bad_wait, 1);
   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------ S^T = K Q^T (one thread)
-    const uint64_t dk = umma_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
-    bool ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_full, 0));
-    for (int j = 0; ok && j < n_tiles; ++j) {
-      const int s = j % kQStages, e = j & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full[s], (j / kQStages) & 1)) ||
-          (j >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar.s_free[e], ((j / 2) + 1) & 1)))) {
-        ok = false;
-        break;
+    // ---------------------------------------------- S^T = K Q^T (one thread)
+    bool ok = true;
+    int kn = 0, qn = 0, sn[kGroups] = {0, 0};
+    for (int kp = kp_begin; ok && kp < kp_end; ++kp) {
+      st.pair(kp);
+      int ks[kGroups];                                   // each group's key tile (load number)
+#pragma unroll
+      for (int w = 0; w < kGroups; ++w) {
+        ks[w] = kn;
+        if (st.skip[w] < st.n) ++kn;
       }
-      tc_fence_after();
-      if (lane == 0) {
+      for (int j = 0; ok && j < st.n; ++j, ++qn) {
+        const int s = qn % kQStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_full[s], (qn / kQStages) & 1));
         const uint64_t dq = umma_desc_sw128(smem_u32(sQ(s)), 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kHeadDim / 16; ++kk)
-          umma_ss(tmem + e * kRows, dk + 2 * kk, dq + 2 * kk, kIdesc, kk > 0);
-        umma_commit(&bar.s_full[e]);
-        umma_commit(&bar.q_empty[s]);
+        for (int w = 0; w < kGroups; ++w) {
+          if (!ok || j < st.skip[w]) continue;
+          const int k = ks[w] % kKStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_full[k], (ks[w] / kKStages) & 1)) &&
+               (sn[w] == 0 || __all_sync(0xffffffffu, mbar_wait(&bar.s_free[w], (sn[w] - 1) & 1)));
+          if (!ok) continue;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t dk = umma_desc_sw128(smem_u32(sK(k)), 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kHeadDim / 16; ++kk)
+              umma_ss(tmem + w * kRows, dk + 2 * kk, dq + 2 * kk, kIdesc, kk > 0);
+            umma_commit(&bar.s_full[w]);
+            if (j == st.n - 1) umma_commit(&bar.k_empty[k]);
+          }
+          __syncwarp();
+          ++sn[w];
+        }
+        if (ok && lane == 0) umma_commit(&bar.q_empty[s]);
+        __syncwarp();
       }
-      __syncwarp();
     }
-    if (!ok && lane == 0) atomicOr(&bar.bad, 1 << 30);
+    if (!ok && lane == 0) atomicOr(&bar.bad_wait, 1);
   } else {
     // ------------------------------------------------ one thread per key
-    const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const int key = key0 + threadIdx.x;
+    const int w = warp / 4;                              // group
+    const uint32_t trow = tmem + w * kRows + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int row = threadIdx.x & 127;
     const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
-    uint64_t acc0 = 0, acc1 = 0;                         // (+0.f, +0.f)
+    const uint32_t masked = p.scale_log2 >= 0.f ? 0xff800000u : 0x7f800000u;
     bool ok = true;
-    uint32_t x[4][32];
-    for (int j = 0; j < n_tiles; ++j) {
-      const int s = j % kQStages, e = j & 1;
-      const int tok = i_first + j * p.tile_tokens;
-      const int rows = min(p.tile_tokens, q_len - tok) * p.group;
-      // columns [from, rows) see this key
-      const int from = max(0, key - shift - tok) * p.group;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[e], (j / 2) & 1))) {
-        ok = false;
-        break;
+    int qn = 0, sn = 0;
+    for (int kp = kp_begin; ok && kp < kp_end; ++kp) {
+      st.pair(kp);
+      const int my_skip = w == 0 ? st.skip[0] : st.skip[kGroups - 1];
+      const int key = st.key0 + w * kKeys + row;
+      const bool writes = key < st.kv_len && st.rank == 0;
+      const float before = writes ? mass[key] : 0.f;
+      bool bad_page = false;                             // a key on a page outside the pool: NaN
+      if (key < st.kv_len) {
+        const int id = __ldg(p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq + key / kPageSize);
+        bad_page = id < 0 || id >= p.num_pages;
       }
-      // the scores wait for Q, but -lse arrives with the loading warp
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full[s], (j / kQStages) & 1))) {
-        ok = false;
-        break;
+      uint64_t acc0 = 0, acc1 = 0;                       // (+0.f, +0.f)
+      for (int j = 0; j < st.n; ++j, ++qn) {
+        const int s = qn % kQStages;
+        // -lse of the tile (and, for a group that skips it, its turn)
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full[s], (qn / kQStages) & 1))) {
+          ok = false;
+          break;
+        }
+        if (j < my_skip) {
+          mbar_arrive(&bar.q_empty[s]);
+          continue;
+        }
+        const int tok = st.token(j);
+        // columns [from, rows) see this key
+        const int rows = min(p.tile_tokens, st.q_len - tok) * p.group;
+        const int from = max(0, key - st.shift - tok) * p.group;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[w], sn & 1))) {
+          ok = false;
+          break;
+        }
+        ++sn;
+        tc_fence_after();
+        const bool edge = __any_sync(0xffffffffu, from > 0 || rows < kRows);
+        const float4 *nl = reinterpret_cast<const float4 *>(sL(s));
+        uint32_t x[2][32];
+        tmem_ld32(trow, x[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait32(x[c & 1]);
+          if (c < 3) {
+            tmem_ld32(trow + 32 * (c + 1), x[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            mbar_arrive(&bar.s_free[w]);
+          }
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e < from || 32 * c + e >= rows) x[c & 1][e] = masked;
+          }
+          add_chunk(x[c & 1], nl + 8 * c, scale2, acc0, acc1);
+        }
+        mbar_arrive(&bar.q_empty[s]);
       }
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(trow + e * kRows + 32 * c, x[c]);
-      tmem_ld_wait32(x[0]);
-#pragma unroll
-      for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
-      tc_fence_before();
-      mbar_arrive(&bar.s_free[e]);
-      if (__any_sync(0xffffffffu, from > 0 || rows < kRows)) {
-        const uint32_t masked = p.scale_log2 >= 0.f ? 0xff800000u : 0x7f800000u;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (32 * c + k < from || 32 * c + k >= rows) x[c][k] = masked;
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        add_chunk(x[c], reinterpret_cast<const float4 *>(sL(s) + 32 * c), scale2, acc0, acc1);
-      mbar_arrive(&bar.q_empty[s]);
+      float a, b, c, d;
+      f2_unpack(acc0, a, b);
+      f2_unpack(acc1, c, d);
+      const float sum = bad_page ? NAN : (a + b) + (c + d);
+      if (p.split > 1) sums[threadIdx.x] = sum;
+      else if (ok && writes) mass[key] = before + sum;
     }
-    if (!ok) atomicOr(&bar.bad, 1 << 30);
+    if (!ok) atomicOr(&bar.bad_wait, 1);
     tc_fence_before();
-    __syncthreads();
-    float a, b, c, d;
-    f2_unpack(acc0, a, b);
-    f2_unpack(acc1, c, d);
-    // a key on a page outside the pool, or a wait that ran out: NaN
-    const bool failed = (bar.bad >> (threadIdx.x / kPageSize) & 1) || (bar.bad >> 30);
-    if (key < kv_len) mass[key] = failed ? NAN : mass[key] + ((a + b) + (c + d));
-    return;
   }
-  tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+  }
+  const int key = kp_begin * kKeys * kGroups + static_cast<int>(threadIdx.x);
+  if (p.split > 1) {
+    // the shares of the cluster's CTAs, in rank order (one key pair per CTA);
+    // a wait that ran out gives NaN
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    if (bar.bad_wait && threadIdx.x < kKeys * kGroups) sums[threadIdx.x] = NAN;
+    cluster.sync();
+    if (st.rank == 0 && threadIdx.x < kKeys * kGroups && key < st.kv_len) {
+      float total = mass[key];
+      for (int r = 0; r < p.split; ++r) total += *cluster.map_shared_rank(sums + threadIdx.x, r);
+      mass[key] = total;
+    }
+    cluster.sync();                                      // peers keep their sums until here
+  } else if (bar.bad_wait) {
+    const int stop = min(st.kv_len, kp_end * kKeys * kGroups);
+    for (int k = key; k < stop; k += kThreads) mass[k] = NAN;
   }
 }
 
@@ -405,15 +521,19 @@ int decode_mass_warps() { return kDecodeWarps; }
 
 cudaError_t launch_prefill_mass(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                 const MassParams &p, cudaStream_t stream) {
-  static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
-  const unsigned long long ctas = static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads *
-                                  cdiv(p.max_kv_len, kKeys);
+  const unsigned long long runs =
+      cdiv(cdiv(p.max_kv_len, kKeys * kGroups), p.pairs_per_cta);
+  const unsigned long long ctas =
+      static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads * runs * p.split;
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
   cudaError_t err = set_smem_once<prefill_mass_kernel>(kSmemBytes);
   if (err != cudaSuccess) return err;
-  return launch_kernel(prefill_mass_kernel, static_cast<unsigned>(ctas), kThreads, kSmemBytes,
-                       stream, false, qmap, kmap, p);
+  return launch_clusters(prefill_mass_kernel, static_cast<unsigned>(ctas),
+                         static_cast<unsigned>(p.split), kThreads, kSmemBytes, stream, false, qmap,
+                         kmap, p);
 }
+
+int prefill_mass_pair_keys() { return kKeys * kGroups; }
 
 }  // namespace sa

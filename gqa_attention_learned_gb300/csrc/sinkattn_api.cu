@@ -109,6 +109,10 @@ bool encode_map(CUtensorMap *map, const void *base, unsigned long long d1, unsig
 
 constexpr int kPrefillTile = 128;     // query rows per prefill CTA
 constexpr int kPrefillKvTile = 128;   // keys per prefill K/V tile
+constexpr int kWindowWaves = 2;       // windowed decode: split up to this many CTA slots
+constexpr int kWindowMinPages = 16;   // and no finer than this
+constexpr int kMassSteps = 16;        // prefill mass: query tiles per CTA to aim for
+constexpr int kMaxCluster = 8;        // portable cluster size
 constexpr int kMassPagesPerWarp = 8;  // decode mass: pages a warp takes, one CTA's share
 
 struct DecodePlan {
@@ -163,21 +167,14 @@ void decode_blocks_for(int batch, int q_len, int group, int num_kv_heads, int nu
 // waves of the GPU, chunks of at least kMinPagesPerChunk pages; an explicit
 // count is honoured up to one page per chunk.
 DecodePlan plan_decode(int batch, int q_len, int num_qo_heads, int num_kv_heads, int max_kv_len,
-                       int num_sms, int requested, int window = 0, int first_tokens = 0) {
+                       int num_sms, int requested) {
   DecodePlan plan;
   const int group = num_qo_heads / num_kv_heads;
   int col_blocks, head_blocks;
   decode_blocks_for(batch, q_len, group, num_kv_heads, num_sms, &col_blocks, &head_blocks);
   plan.col_blocks = col_blocks;
   plan.head_blocks = head_blocks;
-  int max_pages = std::max(1, ceil_div(max_kv_len, kPageSize));
-  if (window > 0) {
-    // pages with a visible key: the first tokens', and the window's, which
-    // may start on any slot of its first page
-    const long long seen = static_cast<long long>(ceil_div(first_tokens, kPageSize)) +
-                           ceil_div(static_cast<long long>(window) + kPageSize - 1, kPageSize);
-    max_pages = static_cast<int>(std::min<long long>(max_pages, seen));
-  }
+  const int max_pages = std::max(1, ceil_div(max_kv_len, kPageSize));
   if (requested == 0 &&
       verify_on_tensor_cores(batch, q_len, num_qo_heads, num_kv_heads, max_pages, num_sms)) {
     plan.tensor_cores = 1;
@@ -218,6 +215,40 @@ DecodePlan plan_decode(int batch, int q_len, int num_qo_heads, int num_kv_heads,
     const size_t units = static_cast<size_t>(batch) * num_kv_heads * head_blocks;
     plan.counters_bytes = (units * sizeof(int) + 255) & ~size_t(255);
     const size_t rows = static_cast<size_t>(plan.num_splits) * batch * q_len * num_qo_heads;
+    plan.workspace_bytes = plan.counters_bytes + rows * kHeadDim * sizeof(float) +
+                           ((rows * sizeof(float) + 255) & ~size_t(255));
+  }
+  return plan;
+}
+
+// Windowed decode: CTAs of 8 or 16 query heads over the pages with a visible
+// key; split only while the CTAs do not fill the GPU twice, and into chunks of
+// at least kWindowMinPages pages.
+DecodePlan plan_window_decode(int batch, int num_qo_heads, int num_kv_heads, int max_kv_len,
+                              int window, int first_tokens, int num_sms, int requested) {
+  DecodePlan plan;
+  const int group = num_qo_heads / num_kv_heads;
+  plan.col_blocks = group > 8 ? 2 : 1;
+  plan.head_blocks = ceil_div(group, 8 * plan.col_blocks);
+  // the first tokens' pages, and the window's, which may start on any slot
+  const long long seen = ceil_div(first_tokens, kPageSize) +
+                         (static_cast<long long>(window) + 2 * kPageSize - 2) / kPageSize;
+  const int max_pages = static_cast<int>(
+      std::min<long long>(std::max(1, ceil_div(max_kv_len, kPageSize)), seen));
+  const long long units = static_cast<long long>(batch) * num_kv_heads * plan.head_blocks;
+  int s = requested;
+  if (s == 0) {
+    const long long slots = static_cast<long long>(std::max(num_sms, 1)) * sa::window_decode_ctas_per_sm();
+    s = static_cast<int>(std::min<long long>(kWindowWaves * slots / std::max(units, 1ll), 1 << 20));
+    s = std::max(s, ceil_div(max_pages, kMaxChunkPages));
+    s = std::min(s, max_pages / kWindowMinPages);
+  }
+  s = std::max(1, std::min({s, sa::decode_max_splits(), max_pages}));
+  plan.pages_per_chunk = ceil_div(max_pages, s);
+  plan.num_splits = ceil_div(max_pages, plan.pages_per_chunk);
+  if (plan.num_splits > 1) {
+    plan.counters_bytes = (static_cast<size_t>(units) * sizeof(int) + 255) & ~size_t(255);
+    const size_t rows = static_cast<size_t>(plan.num_splits) * batch * num_qo_heads;
     plan.workspace_bytes = plan.counters_bytes + rows * kHeadDim * sizeof(float) +
                            ((rows * sizeof(float) + 255) & ~size_t(255));
   }
@@ -316,8 +347,7 @@ int decode_entry(const void *q, const void *k_cache, const void *v_cache,
                  const uint64_t *tree_mask, const float *sinks, float scale, void *out, float *lse,
                  int batch, int q_len, int num_qo_heads, int num_kv_heads, int head_dim,
                  int page_size, int num_pages, int max_kv_len, int num_splits, void *workspace,
-                 size_t workspace_bytes, int launch_flags, bool zero_counters, void *stream,
-                 int window, int first_tokens) {
+                 size_t workspace_bytes, int launch_flags, bool zero_counters, void *stream) {
   if (launch_flags != SINKATTN_LAUNCH_DEFAULT && launch_flags != SINKATTN_LAUNCH_PLAIN &&
       launch_flags != SINKATTN_LAUNCH_PROGRAMMATIC)
     return SINKATTN_INVALID_ARGUMENT;
@@ -346,7 +376,7 @@ int decode_entry(const void *q, const void *k_cache, const void *v_cache,
   const int sms = device_sm_count();
   if (sms == 0) return fail_msg("no CUDA device (SM count query failed)");
   const DecodePlan plan = plan_decode(batch, q_len, num_qo_heads, num_kv_heads, max_kv_len, sms,
-                                      num_splits, window, first_tokens);
+                                      num_splits);
   const int col_blocks = plan.col_blocks, head_blocks = plan.head_blocks;
   if (plan.num_splits > 1) {
     if (!workspace || workspace_bytes < plan.workspace_bytes) return SINKATTN_WORKSPACE_TOO_SMALL;
@@ -423,9 +453,6 @@ int decode_entry(const void *q, const void *k_cache, const void *v_cache,
   p.num_splits = plan.num_splits;
   p.pages_per_chunk = plan.pages_per_chunk;
   p.sorted_dispatch = plan.sorted_dispatch;
-  p.window = std::min(window, std::max(max_kv_len, 1));       // 0 stays 0: no window
-  p.first_tokens = std::min(first_tokens, max_kv_len);
-  p.max_kv_len = max_kv_len;
   if (zero_counters && plan.num_splits > 1) {
     // the counters are the workspace's first plan.counters_bytes bytes, all
     // within workspace_bytes (checked above)
@@ -649,8 +676,8 @@ int sinkattn_decode_window_plan(int batch, int num_qo_heads, int num_kv_heads, i
     num_sms = device_sm_count();
     if (num_sms == 0) return fail_msg("no CUDA device to plan for");
   }
-  const DecodePlan plan = plan_decode(batch, 1, num_qo_heads, num_kv_heads, max_kv_len, num_sms,
-                                      *num_splits, window, first_tokens);
+  const DecodePlan plan = plan_window_decode(batch, num_qo_heads, num_kv_heads, max_kv_len, window,
+                                             first_tokens, num_sms, *num_splits);
   *num_splits = plan.num_splits;
   *workspace_bytes = plan.workspace_bytes;
   return SINKATTN_OK;
@@ -663,11 +690,60 @@ int sinkattn_decode_window(const void *q, const void *k_cache, const void *v_cac
                            int num_kv_heads, int head_dim, int page_size, int num_pages,
                            int max_kv_len, int num_splits, void *workspace,
                            size_t workspace_bytes, int launch_flags, void *stream) {
-  if (window < 1 || first_tokens < 0) return SINKATTN_INVALID_ARGUMENT;
-  return sa::decode_entry(q, k_cache, v_cache, page_table, max_pages_per_seq, kv_lens, nullptr,
-                         sinks, scale, out, lse, batch, 1, num_qo_heads, num_kv_heads, head_dim,
-                         page_size, num_pages, max_kv_len, num_splits, workspace, workspace_bytes,
-                         launch_flags, false, stream, window, first_tokens);
+  if (launch_flags != SINKATTN_LAUNCH_DEFAULT && launch_flags != SINKATTN_LAUNCH_PLAIN &&
+      launch_flags != SINKATTN_LAUNCH_PROGRAMMATIC)
+    return SINKATTN_INVALID_ARGUMENT;
+  if (head_dim != kHeadDim || page_size != kPageSize) return SINKATTN_UNSUPPORTED;
+  if (batch < 0 || num_qo_heads <= 0 || num_kv_heads <= 0 || num_qo_heads % num_kv_heads ||
+      max_kv_len < 0 || num_splits < 0 || num_pages <= 0 || max_pages_per_seq <= 0 || window < 1 ||
+      first_tokens < 0 || !std::isfinite(scale))
+    return SINKATTN_INVALID_ARGUMENT;
+  if (batch == 0) return SINKATTN_OK;
+  if (!q || !k_cache || !v_cache || !page_table || !kv_lens || !sinks || !out)
+    return SINKATTN_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(sinks, 4) || !aligned(lse, 4))
+    return SINKATTN_INVALID_ARGUMENT;
+  const int sms = device_sm_count();
+  if (sms == 0) return fail_msg("no CUDA device (SM count query failed)");
+  const DecodePlan plan = plan_window_decode(batch, num_qo_heads, num_kv_heads, max_kv_len, window,
+                                             first_tokens, sms, num_splits);
+  if (plan.num_splits > 1) {
+    if (!workspace || workspace_bytes < plan.workspace_bytes) return SINKATTN_WORKSPACE_TOO_SMALL;
+    if (!aligned(workspace, 256)) return SINKATTN_INVALID_ARGUMENT;
+  }
+  sa::WindowDecodeParams p{};
+  p.q = static_cast<const uint16_t *>(q);
+  p.k_cache = static_cast<const uint16_t *>(k_cache);
+  p.v_cache = static_cast<const uint16_t *>(v_cache);
+  p.page_table = page_table;
+  p.kv_lens = kv_lens;
+  p.sinks = sinks;
+  p.out = static_cast<uint16_t *>(out);
+  p.lse = lse;
+  if (plan.num_splits > 1) {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.counters = reinterpret_cast<int *>(ws);
+    p.ws_o = reinterpret_cast<float *>(ws + plan.counters_bytes);
+    p.ws_lse = p.ws_o + static_cast<size_t>(plan.num_splits) * batch * num_qo_heads * kHeadDim;
+  }
+  p.scale_log2 = scale * sa::kLog2e;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.batch = batch;
+  p.num_qo_heads = num_qo_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_qo_heads / num_kv_heads;
+  p.col_blocks = plan.col_blocks;
+  p.head_blocks = plan.head_blocks;
+  p.num_pages = num_pages;
+  p.num_splits = plan.num_splits;
+  p.pages_per_chunk = plan.pages_per_chunk;
+  p.window = std::min(window, std::max(max_kv_len, 1));
+  p.first_tokens = std::min(first_tokens, max_kv_len);
+  p.max_kv_len = max_kv_len;
+  return cuda_status(sa::launch_window_decode(p, static_cast<cudaStream_t>(stream),
+                                              sa::programmatic_for(launch_flags)),
+                     "windowed decode launch");
 }
 
 }  // extern "C"
@@ -769,6 +845,23 @@ int mass_params(sa::MassParams &p, const void *q, const void *k_cache, const int
   return SINKATTN_OK;
 }
 
+// How the prefill form of attention mass spreads over CTAs: many query tiles
+// per key pair are shared by a cluster, few leave a CTA time for several key
+// pairs (as long as the CTAs still fill the GPU twice).
+void plan_prefill_mass(sa::MassParams &p) {
+  const int tiles = ceil_div(p.max_q_len, p.tile_tokens);
+  const int pairs = std::max(1, ceil_div(p.max_kv_len, sa::prefill_mass_pair_keys()));
+  p.split = p.pairs_per_cta = 1;
+  if (tiles >= 2 * kMassSteps) {
+    while (p.split < kMaxCluster && tiles / (2 * p.split) >= kMassSteps) p.split *= 2;
+  } else {
+    const long long all = static_cast<long long>(pairs) * p.num_seqs * p.num_kv_heads;
+    const long long fill = all / (4ll * std::max(device_sm_count(), 1));
+    p.pairs_per_cta = static_cast<int>(
+        std::max<long long>(1, std::min<long long>({kMassSteps / tiles, fill, pairs})));
+  }
+}
+
 bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + b_bytes && y < x + a_bytes;
@@ -836,6 +929,7 @@ int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_se
   p.cu_seqlens_q = cu_seqlens_q;
   p.max_q_len = max_q_len;
   p.tile_tokens = kPrefillTile / p.group;
+  plan_prefill_mass(p);
   CUtensorMap qmap, kmap;
   if (!encode_map(&qmap, q, num_qo_heads, total_q, p.group, p.tile_tokens) ||
       !encode_map(&kmap, k_cache, static_cast<unsigned long long>(num_kv_heads) * kPageSize,

@@ -103,106 +103,153 @@ struct RowSlots {
   }
 };
 
-// One 128-slot tile of the online softmax for this thread's row.  Returns
-// false when a wait timed out.
+// Masks one chunk of raw scores, and their maximum in base 2.
+__device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t mask, uint32_t masked_raw) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!((mask >> e) & 1u)) x[e] = masked_raw;
+}
+__device__ __forceinline__ float max_chunk(const uint32_t (&x)[32], float sl2) {
+  float r;
+  if (sl2 >= 0.f) {
+    r = __uint_as_float(x[0]);
+#pragma unroll
+    for (int e = 1; e < 31; e += 2) r = fmax3(r, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+    r = fmaxf(r, __uint_as_float(x[31]));
+  } else {
+    r = INFINITY;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) r = fminf(r, __uint_as_float(x[e]));
+  }
+  return r * sl2;
+}
+
+// Running softmax of a row: reference max m (base 2) that P and the
+// tensor-memory O are relative to, sum d.  m starts at the sink and moves only
+// when a row max exceeds it by more than kRescaleLog2.
+struct RowState {
+  float m, d;
+  // Takes in the max of a tile; returns the factor that O has to be scaled by.
+  __device__ __forceinline__ float advance(float mx, bool first_tile) {
+    const float m_new = fmaxf(m, mx);
+    if (first_tile) {                  // O holds nothing yet: just re-base d
+      if (m_new != -INFINITY) {
+        d *= ex2(m - m_new);
+        m = m_new;
+      }
+      return 1.f;
+    }
+    if (!(m_new > m + kRescaleLog2)) return 1.f;
+    const float alpha = ex2(m - m_new);
+    d *= alpha;
+    m = m_new;
+    return alpha;
+  }
+  __device__ __forceinline__ float reference() const { return m == -INFINITY ? 0.f : m; }
+};
+
+// Scales this row's O (rare: the previous P V has finished, the next one is
+// issued only after p_full).
+__device__ __forceinline__ void rescale_o(uint32_t trow, float alpha) {
+  uint32_t x[32];
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    tmem_ld32(trow + kColO + 32 * h, x);
+    tmem_ld_wait32(x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+    tmem_st16(trow + kColO + 32 * h, *reinterpret_cast<uint32_t(*)[16]>(&x[0]));
+    tmem_st16(trow + kColO + 32 * h + 16, *reinterpret_cast<uint32_t(*)[16]>(&x[16]));
+  }
+  tmem_st_wait();
+}
+
+// One 128-slot tile of the online softmax for this thread's row.  `chunks`:
+// 32-slot chunks of P that this tile's P V reads.  Returns false when a wait
+// timed out.
 __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, int chunks,
-                                             const RowSlots &see, float sl2, bool pos_scale,
-                                             uint32_t masked_raw, float &m, float &d,
-                                             uint32_t (&x)[4][32]) {
-  uint32_t mask[4];
-  bool live[4], edge[4];               // warp-uniform
+                                             const RowSlots &see, float sl2, uint32_t masked_raw,
+                                             RowState &row) {
+  unsigned live = 0, edge = 0;         // warp-uniform bits per chunk
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    mask[c] = see.mask(j * kBN + 32 * c);
-    live[c] = __any_sync(0xffffffffu, mask[c] != 0u);
-    edge[c] = __any_sync(0xffffffffu, mask[c] != 0xffffffffu);
+    const uint32_t mask = see.mask(j * kBN + 32 * c);
+    live |= __any_sync(0xffffffffu, mask != 0u) ? 1u << c : 0u;
+    edge |= __any_sync(0xffffffffu, mask != 0xffffffffu) ? 1u << c : 0u;
   }
   if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full, j & 1))) return false;
   tc_fence_after();
+  const uint64_t scale2 = f2_pack(sl2, sl2);
+  float alpha, s0, s1;
+  if (live == 15u) {
+    // a full tile: S is read once and held in registers
+    uint32_t x[4][32];
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (live[c]) tmem_ld32(trow + kColS + 32 * c, x[c]);
-  tmem_ld_wait32(x[0]);
-#pragma unroll
-  for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
-  tc_fence_before();
-  mbar_arrive(&bar.s_free);
-  float mx = -INFINITY;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (!live[c]) continue;
-    if (edge[c]) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!((mask[c] >> e) & 1u)) x[c][e] = masked_raw;
-    }
-    if (pos_scale) {
-      float r = __uint_as_float(x[c][0]);
-#pragma unroll
-      for (int e = 1; e < 31; e += 2)
-        r = fmax3(r, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-      mx = fmaxf(mx, fmaxf(r, __uint_as_float(x[c][31])) * sl2);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[c][e]) * sl2);
-    }
-  }
-  const float m_new = fmaxf(m, mx);
-  float alpha = 1.f;
-  bool rescale = false;
-  if (j == 0) {                        // O holds nothing yet: just re-base d
-    if (m_new != -INFINITY) {
-      d *= ex2(m - m_new);
-      m = m_new;
-    }
-  } else if (m_new > m + kRescaleLog2) {
-    alpha = ex2(m - m_new);
-    d *= alpha;
-    m = m_new;
-    rescale = true;
-  }
-  const float mu = m == -INFINITY ? 0.f : m;
-  const uint64_t scale2 = f2_pack(sl2, sl2), negmu2 = f2_pack(-mu, -mu);
-  uint64_t acc = 0;                                  // (+0.f, +0.f)
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (live[c]) {
-      uint64_t part = 0;
-      pack_chunk(x[c], scale2, negmu2, part);
-      acc = f2_add(acc, part);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[c][e] = 0u;
-    }
-  }
-  float s0, s1;
-  f2_unpack(acc, s0, s1);
-  d += s0 + s1;
-  // the previous tile's P V reads P and accumulates O: wait for it
-  if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (j - 1) & 1))) return false;
-  tc_fence_after();
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (c < chunks)                    // the P columns that this tile's P V reads
-      tmem_st16(trow + kColP + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[c][0]));
-  tmem_st_wait();
-  if (__any_sync(0xffffffffu, rescale)) {
-    // rare: scale this row's O (the previous P V has finished, the next one
-    // is issued only after p_full below)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) tmem_ld32(trow + kColO + 32 * h, x[h]);
+    for (int c = 0; c < 4; ++c) tmem_ld32(trow + kColS + 32 * c, x[c]);
     tmem_ld_wait32(x[0]);
-    reg_tie32(x[1]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
+    tc_fence_before();
+    mbar_arrive(&bar.s_free);
+    if (edge) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) x[h][e] = __float_as_uint(__uint_as_float(x[h][e]) * alpha);
-    tmem_st16(trow + kColO, *reinterpret_cast<uint32_t(*)[16]>(&x[0][0]));
-    tmem_st16(trow + kColO + 16, *reinterpret_cast<uint32_t(*)[16]>(&x[0][16]));
-    tmem_st16(trow + kColO + 32, *reinterpret_cast<uint32_t(*)[16]>(&x[1][0]));
-    tmem_st16(trow + kColO + 48, *reinterpret_cast<uint32_t(*)[16]>(&x[1][16]));
-    tmem_st_wait();
+      for (int c = 0; c < 4; ++c)
+        if ((edge >> c) & 1u) mask_chunk(x[c], see.mask(j * kBN + 32 * c), masked_raw);
+    }
+    alpha = row.advance(fmaxf(fmax3(max_chunk(x[0], sl2), max_chunk(x[1], sl2), max_chunk(x[2], sl2)),
+                              max_chunk(x[3], sl2)),
+                        j == 0);
+    const float mu = row.reference();
+    const uint64_t negmu2 = f2_pack(-mu, -mu);
+    uint64_t acc[4] = {0, 0, 0, 0};                    // (+0.f, +0.f)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) pack_chunk(x[c], scale2, negmu2, acc[c]);
+    f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+    // the previous tile's P V reads P and accumulates O: wait for it
+    if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (j - 1) & 1))) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      tmem_st16(trow + kColP + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[c][0]));
+  } else {
+    // an edge tile: its live chunks one by one, once for the max and once more
+    // for the weights (fewer exponentials, and few registers)
+    uint32_t x[32];
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      if (!((live >> c) & 1u)) continue;
+      tmem_ld32(trow + kColS + 32 * c, x);
+      tmem_ld_wait32(x);
+      if ((edge >> c) & 1u) mask_chunk(x, see.mask(j * kBN + 32 * c), masked_raw);
+      mx = fmaxf(mx, max_chunk(x, sl2));
+    }
+    alpha = row.advance(mx, j == 0);
+    const float mu = row.reference();
+    const uint64_t negmu2 = f2_pack(-mu, -mu);
+    uint64_t acc = 0;
+    if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (j - 1) & 1))) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      if ((live >> c) & 1u) {
+        tmem_ld32(trow + kColS + 32 * c, x);
+        tmem_ld_wait32(x);
+        if ((edge >> c) & 1u) mask_chunk(x, see.mask(j * kBN + 32 * c), masked_raw);
+        pack_chunk(x, scale2, negmu2, acc);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = 0u;
+      }
+      tmem_st16(trow + kColP + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[0]));
+    }
+    f2_unpack(acc, s0, s1);
+    tc_fence_before();
+    mbar_arrive(&bar.s_free);
   }
+  row.d += s0 + s1;
+  tmem_st_wait();
+  if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o(trow, alpha);
   tc_fence_before();
   mbar_arrive(&bar.p_full);
   return true;
@@ -433,23 +480,20 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     see.b = slot_of(max(0, pos - p.window + 1));
     see.c = slot_of(pos + 1);
     const float sl2 = p.scale_log2;
-    const bool pos_scale = sl2 >= 0.f;
     // Masked scores are replaced (by index, so NaN keys cannot leak) with the
     // raw value whose scaled logit is -inf.
-    const uint32_t masked_raw = pos_scale ? 0xff800000u : 0x7f800000u;
-    // reference max (base 2) and sum, started at the sink
-    float m = r < rows ? p.sinks[head] * kLog2e : -INFINITY;
-    float d = 1.f;
+    const uint32_t masked_raw = sl2 >= 0.f ? 0xff800000u : 0x7f800000u;
+    RowState state{r < rows ? p.sinks[head] * kLog2e : -INFINITY, 1.f};   // started at the sink
     bool ok = true;
-    uint32_t x[4][32];
     const bool live = warp * 32 < live_threads;         // warp-uniform
     for (int j = 0; live && j < n_tiles; ++j) {
       const int chunks = (min(kBoxes, n_boxes - j * kBoxes) + 1) / 2;
-      if (!softmax_tile(bar, trow, j, chunks, see, sl2, pos_scale, masked_raw, m, d, x)) {
+      if (!softmax_tile(bar, trow, j, chunks, see, sl2, masked_raw, state)) {
         ok = false;
         break;
       }
     }
+    uint32_t x[2][32];
     if (live) {
       if (__all_sync(0xffffffffu, mbar_wait(&bar.o_final, 0))) {
         tc_fence_after();
@@ -470,6 +514,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     __syncthreads();
     if (!live) return;
     const bool failed = bar.bad != 0;
+    const float m = state.m, d = state.d;
     const float inv = d > 0.f ? 1.f / d : 0.f;
     auto o = [&](int e) { return __uint_as_float(x[e >> 5][e & 31]) * inv; };
     // Each warp puts its rows in the query buffer (free since the last QK^T

@@ -83,9 +83,11 @@ def test_the_window_plan_covers_the_visible_pages_only(lib):
     s, ws = sa.decode_window_plan(1, 64, 8, 131072, 128, 4, num_splits=64, num_sms=152)
     assert s <= 10 and ws > 0
     assert sa.decode_window_plan(64, 64, 8, 131072, 128, 4, num_sms=152)[0] == 1
-    # a window without bound plans as full attention does
-    full = sa.decode_plan(8, 64, 8, 131072, num_sms=152)
-    assert sa.decode_window_plan(8, 64, 8, 131072, 2**31 - 1, 0, num_sms=152) == full
+    # a window without bound plans for every page
+    whole = sa.decode_window_plan(8, 64, 8, 131072, 131072, 0, num_sms=152)
+    assert whole[0] > 8
+    assert sa.decode_window_plan(8, 64, 8, 131072, 2**31 - 1, 2**31 - 1, num_sms=152) == whole
+    assert sa.decode_window_plan(1, 8, 1, 0, 5, num_sms=152) == (1, 0)
     for bad in (dict(window=0), dict(window=-1), dict(first_tokens=-1), dict(head_dim=128)):
         kw = dict(window=1, first_tokens=0)
         kw.update(bad)
