@@ -189,6 +189,13 @@ cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &km
                                   const CUtensorMap &vmap, const WindowPrefillParams &p,
                                   cudaStream_t stream);
 
+// Whether the keys of every query tile fit the kernel that holds them all at
+// once, and that kernel (one persistent CTA per SM).
+bool window_prefill_is_short(const WindowPrefillParams &p);
+cudaError_t launch_window_short(const CUtensorMap &qmap, const CUtensorMap &kmap,
+                                const CUtensorMap &vmap, const WindowPrefillParams &p, int num_sms,
+                                cudaStream_t stream);
+
 // ---------------------------------------------------------- attention weight
 struct MassParams {
   const uint16_t *q;             // bf16 [Tq][Hq][64]

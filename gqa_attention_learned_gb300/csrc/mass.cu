@@ -13,8 +13,10 @@
 // heads] = K Q^T by mma.sync.m16n8k16, K straight from global memory into the
 // A fragments.  A dot product does not care about the order of its terms, so
 // the k index of the MMA is permuted to make each lane's share of a K row two
-// 16-byte pieces: no shared memory, no copies to wait for, several pages in
-// flight per warp.
+// 16-byte pieces: no shared memory and no copies to wait for; many resident
+// warps with one page each in flight hide the latency better than few warps
+// with several (a page's 16 registers per lane cost occupancy, and the loads
+// of several pages wait for one another).
 //
 // prefill_mass (ragged rows at the end of the keys) is bound by its
 // exponentials, one per (row, key).  A CTA holds 256 keys of one KV head and
@@ -49,8 +51,15 @@ __device__ __forceinline__ void poison_row(const MassParams &p, float *row) {
 }
 
 // ------------------------------------------------------------------ decode
-constexpr int kDecodeWarps = 8;
-constexpr int kDecodeAhead = 4;        // pages in flight per warp
+#ifndef MD_WARPS
+#define MD_WARPS 8
+#endif
+#ifndef MD_CTAS
+#define MD_CTAS 4
+#endif
+constexpr int kDecodeWarps = MD_WARPS;
+constexpr int kDecodeCtas = MD_CTAS;
+constexpr int kPieces = kHeadDim * 2 / 16;       // 16-byte pieces of a row
 
 __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
   uint4 v;
@@ -60,14 +69,29 @@ __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
   return v;
 }
 
-// A 16-key page as A fragments: row g and row g + 8 of the page, 16-byte
-// pieces t and t + 4 of each.
-struct PageFrag {
-  uint4 lo0, lo1, hi0, hi1;
-  float before;                       // the mass this lane adds to
+// Columns 8 nb .. 8 nb + 7 of the query heads: Q as B fragments (column g holds
+// pieces t and t + 4 of its head, the k order of K's pieces) and -lse in base 2
+// of columns 2t, 2t + 1.
+struct HeadBlock {
+  uint4 q0, q1;
+  float nl0, nl1;
+  __device__ __forceinline__ void load(const MassParams &p, size_t row0, int nb, int g, int t) {
+    const int col = nb * 8 + g;
+    const uint4 *q = reinterpret_cast<const uint4 *>(p.q) + (row0 + col) * kPieces;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    q0 = col < p.group ? __ldg(q + t) : zero;
+    q1 = col < p.group ? __ldg(q + t + 4) : zero;
+    auto neg = [&](int c) {
+      const float l = c < p.group ? __ldg(p.lse + row0 + c) : INFINITY;
+      return l == -INFINITY ? -INFINITY : -l * kLog2e;   // a row that sees nothing adds nothing
+    };
+    nl0 = neg(nb * 8 + 2 * t);
+    nl1 = neg(nb * 8 + 2 * t + 1);
+  }
 };
 
-__global__ void __launch_bounds__(kDecodeWarps * 32, 2)
+template <bool kOneBlock>             // at most 8 query heads per KV head
+__global__ void __launch_bounds__(kDecodeWarps * 32, kOneBlock ? kDecodeCtas : 3)
 decode_mass_kernel(const MassParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -81,101 +105,54 @@ decode_mass_kernel(const MassParams p) {
     if (chunk == 0) poison_row(p, mass);
     return;
   }
-  const int npages = cdiv(kv_len, kPageSize);
-  const int first = chunk * p.pages_per_chunk + warp;
-  const int end = min(npages, (chunk + 1) * p.pages_per_chunk);
-  const int n_my = first < end ? cdiv(end - first, kDecodeWarps) : 0;
-  if (n_my == 0) return;                                 // warp-uniform; no barriers below
+  const int end = min(cdiv(kv_len, kPageSize), (chunk + 1) * p.pages_per_chunk);
+  int page = chunk * p.pages_per_chunk + warp;
+  if (page >= end) return;                               // warp-uniform; no barriers below
   const int32_t *table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
-
-  // ids of this warp's pages, 32 at a time (lane j holds page j of the batch)
-  auto load_ids = [&](int base) -> int {
-    const int j = base + lane;
-    return j < n_my ? __ldg(table + first + j * kDecodeWarps) : -1;
-  };
-  int batch_ids = load_ids(0), next_ids = load_ids(32);
-  auto page_id = [&](int i) -> int {                     // page i of this warp, -1: none or bad
-    if (i >= n_my) return -1;
-    if ((i & 31) == 0 && i > 0) {
-      batch_ids = next_ids;
-      next_ids = load_ids(i + 32);
-    }
-    const int id = __shfl_sync(0xffffffffu, batch_ids, i & 31);
-    return id < p.num_pages ? id : -1;
-  };
-  // lane 0 of a quad adds to key g of a page, lane 1 to key g + 8
-  const int my_slot = g + (t == 1 ? 8 : 0);
-  auto my_key = [&](int i) { return (first + i * kDecodeWarps) * kPageSize + my_slot; };
-  auto fetch = [&](int i, int id, PageFrag &f) {
-    if (i < n_my && t < 2 && my_key(i) < kv_len) f.before = mass[my_key(i)];
-    if (id < 0) return;
-    const uint4 *base = reinterpret_cast<const uint4 *>(
-        p.k_cache + (static_cast<size_t>(id) * p.num_kv_heads + kvh) * kPageSize * kHeadDim);
-    f.lo0 = ld_stream(base + g * 8 + t);
-    f.lo1 = ld_stream(base + g * 8 + t + 4);
-    f.hi0 = ld_stream(base + (g + 8) * 8 + t);
-    f.hi1 = ld_stream(base + (g + 8) * 8 + t + 4);
-  };
-  PageFrag f[kDecodeAhead];
-  int ids[kDecodeAhead];
-#pragma unroll
-  for (int u = 0; u < kDecodeAhead; ++u) {
-    ids[u] = page_id(u);
-    fetch(u, ids[u], f[u]);
-  }
-
-  // Q as B fragments with the same permuted k index: column g holds dims
-  // 8t..8t+7 and 32+8t..32+8t+7 of its head
-  const int blocks = cdiv(p.group, 8);
-  const int head0 = kvh * p.group;
-  const size_t row0 = static_cast<size_t>(b) * p.num_qo_heads + head0;
-  uint4 q0, q1;
-  float nl0, nl1;                     // -lse (base 2) of columns 2t, 2t+1
-  auto load_block = [&](int nb) {
-    const int col = nb * 8 + g;
-    const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (row0 + col) * kHeadDim);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    q0 = col < p.group ? __ldg(q + t) : zero;
-    q1 = col < p.group ? __ldg(q + t + 4) : zero;
-    auto neg = [&](int c) {
-      const float l = c < p.group ? __ldg(p.lse + row0 + c) : INFINITY;
-      return l == -INFINITY ? -INFINITY : -l * kLog2e;   // a row that sees nothing adds nothing
+  const size_t row0 = static_cast<size_t>(b) * p.num_qo_heads + kvh * p.group;
+  const uint4 *cache = reinterpret_cast<const uint4 *>(p.k_cache) + g * kPieces + t;
+  int id = __ldg(table + page);
+  HeadBlock q;
+  if constexpr (kOneBlock) q.load(p, row0, 0, g, t);
+  for (; page < end; page += kDecodeWarps) {
+    const int next = page + kDecodeWarps < end ? __ldg(table + page + kDecodeWarps) : 0;
+    const bool bad = id < 0 || id >= p.num_pages;        // never dereferenced
+    const uint4 *k =
+        cache + (static_cast<size_t>(bad ? 0 : id) * p.num_kv_heads + kvh) * (kPageSize * kPieces);
+    // A fragments: key rows g and g + 8, pieces t and t + 4
+    const uint4 lo0 = ld_stream(k), lo1 = ld_stream(k + 4);
+    const uint4 hi0 = ld_stream(k + 8 * kPieces), hi1 = ld_stream(k + 8 * kPieces + 4);
+    // lane 0 of a quad adds to key g of the page, lane 1 to key g + 8
+    const int key = page * kPageSize + g + (t == 1 ? 8 : 0);
+    const bool writes = t < 2 && key < kv_len;
+    const float before = writes ? mass[key] : 0.f;
+    float w_lo = 0.f, w_hi = 0.f;
+    auto add = [&]() {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t a0[4] = {lo0.x, hi0.x, lo0.y, hi0.y}, a1[4] = {lo0.z, hi0.z, lo0.w, hi0.w};
+      const uint32_t a2[4] = {lo1.x, hi1.x, lo1.y, hi1.y}, a3[4] = {lo1.z, hi1.z, lo1.w, hi1.w};
+      mma_bf16_16816(s, a0, q.q0.x, q.q0.y);
+      mma_bf16_16816(s, a1, q.q0.z, q.q0.w);
+      mma_bf16_16816(s, a2, q.q1.x, q.q1.y);
+      mma_bf16_16816(s, a3, q.q1.z, q.q1.w);
+      w_lo += ex2(fmaf(s[0], p.scale_log2, q.nl0)) + ex2(fmaf(s[1], p.scale_log2, q.nl1));
+      w_hi += ex2(fmaf(s[2], p.scale_log2, q.nl0)) + ex2(fmaf(s[3], p.scale_log2, q.nl1));
     };
-    nl0 = neg(nb * 8 + 2 * t);
-    nl1 = neg(nb * 8 + 2 * t + 1);
-  };
-  if (blocks == 1) load_block(0);
-
-  for (int i0 = 0; i0 < n_my; i0 += kDecodeAhead) {
-#pragma unroll
-    for (int u = 0; u < kDecodeAhead; ++u) {
-      const int i = i0 + u;
-      if (i >= n_my) break;
-      float w_lo = 0.f, w_hi = 0.f;
-      for (int nb = 0; nb < blocks; ++nb) {
-        if (blocks > 1) load_block(nb);
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t a0[4] = {f[u].lo0.x, f[u].hi0.x, f[u].lo0.y, f[u].hi0.y};
-        const uint32_t a1[4] = {f[u].lo0.z, f[u].hi0.z, f[u].lo0.w, f[u].hi0.w};
-        const uint32_t a2[4] = {f[u].lo1.x, f[u].hi1.x, f[u].lo1.y, f[u].hi1.y};
-        const uint32_t a3[4] = {f[u].lo1.z, f[u].hi1.z, f[u].lo1.w, f[u].hi1.w};
-        mma_bf16_16816(s, a0, q0.x, q0.y);
-        mma_bf16_16816(s, a1, q0.z, q0.w);
-        mma_bf16_16816(s, a2, q1.x, q1.y);
-        mma_bf16_16816(s, a3, q1.z, q1.w);
-        w_lo += ex2(fmaf(s[0], p.scale_log2, nl0)) + ex2(fmaf(s[1], p.scale_log2, nl1));
-        w_hi += ex2(fmaf(s[2], p.scale_log2, nl0)) + ex2(fmaf(s[3], p.scale_log2, nl1));
+    if constexpr (kOneBlock) {
+      add();
+    } else {
+      for (int nb = 0; nb < cdiv(p.group, 8); ++nb) {
+        q.load(p, row0, nb, g, t);
+        add();
       }
-#pragma unroll
-      for (int off = 1; off < 4; off <<= 1) {
-        w_lo += __shfl_xor_sync(0xffffffffu, w_lo, off);
-        w_hi += __shfl_xor_sync(0xffffffffu, w_hi, off);
-      }
-      if (t < 2 && my_key(i) < kv_len)
-        mass[my_key(i)] = ids[u] < 0 ? NAN : f[u].before + (t == 0 ? w_lo : w_hi);
-      ids[u] = page_id(i + kDecodeAhead);
-      fetch(i + kDecodeAhead, ids[u], f[u]);
     }
+    // sums over the quad; lanes 0 and 1 end up with keys g and g + 8
+    w_lo += __shfl_xor_sync(0xffffffffu, w_lo, 1);
+    w_hi += __shfl_xor_sync(0xffffffffu, w_hi, 1);
+    float w = (t & 1) ? w_hi : w_lo;
+    w += __shfl_xor_sync(0xffffffffu, w, 2);
+    if (writes) mass[key] = bad ? NAN : before + w;
+    id = next;
   }
 }
 
@@ -513,8 +490,8 @@ cudaError_t launch_decode_mass(const MassParams &p, cudaStream_t stream) {
       static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads * p.num_chunks;
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-  return launch_kernel(decode_mass_kernel, static_cast<unsigned>(ctas), kDecodeWarps * 32, 0,
-                       stream, true, p);
+  return launch_kernel(p.group <= 8 ? decode_mass_kernel<true> : decode_mass_kernel<false>,
+                       static_cast<unsigned>(ctas), kDecodeWarps * 32, 0, stream, true, p);
 }
 
 int decode_mass_warps() { return kDecodeWarps; }

@@ -109,11 +109,17 @@ bool encode_map(CUtensorMap *map, const void *base, unsigned long long d1, unsig
 
 constexpr int kPrefillTile = 128;     // query rows per prefill CTA
 constexpr int kPrefillKvTile = 128;   // keys per prefill K/V tile
-constexpr int kWindowWaves = 2;       // windowed decode: split up to this many CTA slots
+#ifndef WD_WAVES
+#define WD_WAVES 2
+#endif
+constexpr int kWindowWaves = WD_WAVES;       // windowed decode: split up to this many CTA slots
 constexpr int kWindowMinPages = 16;   // and no finer than this
 constexpr int kMassSteps = 16;        // prefill mass: query tiles per CTA to aim for
 constexpr int kMaxCluster = 8;        // portable cluster size
-constexpr int kMassPagesPerWarp = 8;  // decode mass: pages a warp takes, one CTA's share
+#ifndef MD_PAGES
+#define MD_PAGES 8
+#endif
+constexpr int kMassPagesPerWarp = MD_PAGES;  // decode mass: pages a warp takes, one CTA's share
 
 struct DecodePlan {
   int num_splits = 1;
@@ -806,8 +812,13 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
   p.first_tokens = std::min(first_tokens, max_kv_len);
   p.tile_tokens = tile_tokens;
   p.num_q_tiles = ceil_div(max_q_len, tile_tokens);
-  return cuda_status(sa::launch_window_prefill(qmap, kmap, vmap, p, static_cast<cudaStream_t>(stream)),
-                     "windowed prefill launch");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (sa::window_prefill_is_short(p)) {
+    const int sms = device_sm_count();
+    if (sms == 0) return fail_msg("no CUDA device (SM count query failed)");
+    return cuda_status(sa::launch_window_short(qmap, kmap, vmap, p, sms, st), "windowed prefill launch");
+  }
+  return cuda_status(sa::launch_window_prefill(qmap, kmap, vmap, p, st), "windowed prefill launch");
 }
 
 // Checks shared by both forms of attention mass; fills the parameters.

@@ -25,19 +25,13 @@
 // loads Q and K and issues S = Q K^T, warp 5 loads V and issues O += P V,
 // warps 0..3 run the online softmax, one thread per row, between them.
 
-#include "kernels.cuh"
-#include "ptx.cuh"
-
-#include <cmath>
+#include "window_tile.cuh"
 
 namespace sa {
 namespace {
 
-constexpr int kBM = 128;                       // query rows per CTA
 constexpr int kBN = 128;                       // key slots per tile
-constexpr int kBox = 16;                       // keys per copied box
-constexpr int kBoxes = kBN / kBox;
-constexpr int kBoxBytes = kBox * kHeadDim * 2;
+constexpr int kBoxes = kBN / 16;               // copied boxes per tile
 constexpr int kKStages = 3, kVStages = 2;
 constexpr int kTileBytes = kBN * kHeadDim * 2;
 constexpr int kThreads = 192;
@@ -67,62 +61,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-constexpr uint32_t kIdescPV = umma_idesc_bf16(128, 64, false, true);
-
-__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
-
-// Bits e of a 32-slot chunk starting at v0 with v0 + e < x.
-__device__ __forceinline__ uint32_t bits_below(int x, int v0) {
-  const int n = x - v0;
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
-// P = 2^(s * sl2 - mu) for 32 scores, packed as bf16 pairs into r[0..15];
-// the pair sums accumulate in `acc` (fp32x2).
-template <int E = 0>
-__device__ __forceinline__ void pack_chunk(uint32_t (&r)[32], uint64_t scale2, uint64_t negmu2,
-                                           uint64_t &acc) {
-  if constexpr (E < 16) {
-    float x0, x1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(r[2 * E]), __uint_as_float(r[2 * E + 1])), scale2,
-                     negmu2),
-              x0, x1);
-    const float p0 = ex2(x0);
-    const float p1 = ex2(x1);
-    acc = f2_add(acc, f2_pack(p0, p1));
-    r[E] = pack_bf16(p0, p1);
-    pack_chunk<E + 1>(r, scale2, negmu2, acc);
-  }
-}
-
-// Slot ranges a row sees: [0, a) and [b, c).
-struct RowSlots {
-  int a, b, c;
-  __device__ __forceinline__ uint32_t mask(int v0) const {
-    return bits_below(c, v0) & (bits_below(a, v0) | ~bits_below(b, v0));
-  }
-};
-
-// Masks one chunk of raw scores, and their maximum in base 2.
-__device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t mask, uint32_t masked_raw) {
-#pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (!((mask >> e) & 1u)) x[e] = masked_raw;
-}
-__device__ __forceinline__ float max_chunk(const uint32_t (&x)[32], float sl2) {
-  float r;
-  if (sl2 >= 0.f) {
-    r = __uint_as_float(x[0]);
-#pragma unroll
-    for (int e = 1; e < 31; e += 2) r = fmax3(r, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-    r = fmaxf(r, __uint_as_float(x[31]));
-  } else {
-    r = INFINITY;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) r = fminf(r, __uint_as_float(x[e]));
-  }
-  return r * sl2;
-}
+using namespace window;
 
 // Running softmax of a row: reference max m (base 2) that P and the
 // tensor-memory O are relative to, sum d.  m starts at the sink and moves only
@@ -261,49 +200,22 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const WindowPrefillParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint4 nan4 = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
 
   // ---- work item: (query tile, request, KV head), later tiles (whose windows
   // are full) first
   const int per_tile = p.num_seqs * p.num_kv_heads;
   const int qt = p.num_q_tiles - 1 - static_cast<int>(blockIdx.x / per_tile);
   const int rem = static_cast<int>(blockIdx.x % per_tile);
-  const int kvh = rem % p.num_kv_heads, seq = rem / p.num_kv_heads;
-  const int q_start = p.cu_seqlens_q[seq];
-  const int q_end = p.cu_seqlens_q[seq + 1], q_len = q_end - q_start;
-  const int kv_len = kPaged ? p.kv_lens[seq] : q_len;
-  bool bad = q_start < 0 || q_len < 0 || q_end > p.total_q || q_len > p.max_q_len ||
-             kv_len < q_len || kv_len > p.max_kv_len;
-  if constexpr (kPaged) bad = bad || cdiv(kv_len, kPageSize) > p.max_pages_per_seq;
-  if (bad) {
-    // poison every row of this request that lies inside the buffers (once)
-    if (qt != 0 || q_start < 0 || q_start >= p.total_q) return;
-    const int stop = min(max(q_end, q_start), p.total_q);
-    for (long long idx = threadIdx.x; idx < static_cast<long long>(stop - q_start) * p.group;
-         idx += kThreads) {
-      const size_t row = static_cast<size_t>(q_start + idx / p.group) * p.num_qo_heads +
-                         kvh * p.group + idx % p.group;
-      uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kHeadDim);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) dst[i] = nan4;
-      if (p.lse) p.lse[row] = NAN;
-    }
+  const int kvh = rem % p.num_kv_heads;
+  const Request req = Request::load<kPaged>(p, rem / p.num_kv_heads);
+  if (req.bad) {
+    if (qt == 0) poison(p, kvh, req.q_start, max(req.q_len, 0), threadIdx.x, kThreads);
     return;
   }
-  const int i0 = qt * p.tile_tokens;
-  if (i0 >= q_len) return;
-  const int tokens = min(p.tile_tokens, q_len - i0);
-  const int rows = tokens * p.group;
-  const int pos0 = kv_len - q_len + i0;                 // position of the tile's first token
-  // keys some row sees: [0, min(first, hi)) and [lo, hi)
-  const int hi = pos0 + tokens;
-  const int lo = max(0, pos0 - p.window + 1);
-  const int first_boxes = cdiv(min(p.first_tokens, lo), kBox);
-  const int run = max(kPaged ? lo - lo % kBox : lo, first_boxes * kBox);   // first key of the run's boxes
-  const int gap = run - first_boxes * kBox;             // keys left out between the two parts
-  const int n_boxes = first_boxes + cdiv(max(hi - run, 0), kBox);
-  const int n_tiles = cdiv(n_boxes, kBoxes);
-  auto slot_of = [&](int key) { return key <= first_boxes * kBox ? key : max(key - gap, first_boxes * kBox); };
+  if (qt * p.tile_tokens >= req.q_len) return;
+  const Tile tile = Tile::make<kPaged>(p, req, qt);
+  const int rows = tile.tokens * p.group;
+  const int n_tiles = cdiv(tile.n_boxes, kBoxes);
   const int live_threads = min(kBM, 32 * cdiv(rows, 32));
 
   extern __shared__ uint8_t smem_raw[];
@@ -318,24 +230,13 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     tmem_alloc(&bar.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  const int32_t *table =
-      kPaged ? p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq : nullptr;
-  // where this lane's box of tile j comes from (lanes 0..7): a page id, or the
-  // first row of the box in the ragged K/V; -1 past the last box
+  // source of this lane's box of tile j (lanes 0..7), -1 past the last box
   auto source_of = [&](int j) -> int {
     const int bx = j * kBoxes + lane;
-    if (lane >= kBoxes || bx >= n_boxes) return -1;
-    const int key = bx < first_boxes ? bx * kBox : run + (bx - first_boxes) * kBox;
-    if constexpr (kPaged) {
-      const int id = table[key / kPageSize];
-      if (id < 0 || id >= p.num_pages) {
-        atomicOr(&bar.bad, 1);
-        return -1;
-      }
-      return id;
-    } else {
-      return q_start + key;
-    }
+    if (lane >= kBoxes || bx >= tile.n_boxes) return -1;
+    const int src = tile.source<kPaged>(p, req, bx);
+    if (src < 0) atomicOr(&bar.bad, 1);
+    return src;
   };
   // K (t = 0) or V (t = 1) of tile j into its ring slot, once the slot is free
   auto load = [&](int j, int t, int src) -> bool {
@@ -377,7 +278,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       fence_mbar_init();
       mbar_arrive_expect_tx(&bar.q_full, p.tile_tokens * p.group * kHeadDim * 2);
       // box {64, group, tile_tokens}: rows (token, head)
-      tma_load_3d(sQ, &qmap, &bar.q_full, 0, kvh * p.group, q_start + i0);
+      tma_load_3d(sQ, &qmap, &bar.q_full, 0, kvh * p.group, req.q_start + tile.i0);
     }
     __syncwarp();
     for (int j = 0; j < min(n_tiles, kKStages); ++j) load(j, 0, source_of(j));   // fresh slots
@@ -397,7 +298,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       if (lane == 0) {
         const uint64_t dk = umma_desc_sw128(smem_u32(sK(s)), 16, 1024);
         const uint32_t idesc =
-            umma_idesc_bf16(128, kBox * min(kBoxes, n_boxes - j * kBoxes), false, false);
+            umma_idesc_bf16(128, kBox * min(kBoxes, tile.n_boxes - j * kBoxes), false, false);
 #pragma unroll
         for (int kk = 0; kk < kHeadDim / 16; ++kk)
           umma_ss(tmem + kColS, dq + 2 * kk, dk + 2 * kk, idesc, kk > 0);   // +32 bytes per k-step
@@ -424,33 +325,19 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   } else if (warp == kPvWarp) {
     // ---------------------------------------------------- P V (one thread)
     const uint32_t tP = tmem + kColP, tO = tmem + kColO;
-    // slots no row sees: [dead_from, dead_to) between the parts, and from end on
-    const int dead_from = slot_of(min(p.first_tokens, hi)), dead_to = slot_of(lo), end = slot_of(hi);
     bool ok = true;
     for (int j = 0; ok && j < min(n_tiles, kVStages); ++j) ok = load(j, 1, source_of(j));
     int src = source_of(kVStages);
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kVStages;
-      const int boxes = min(kBoxes, n_boxes - j * kBoxes);
+      const int boxes = min(kBoxes, tile.n_boxes - j * kBoxes);
       if (!__all_sync(0xffffffffu, mbar_wait(&bar.p_full, j & 1)) ||
           !__all_sync(0xffffffffu, mbar_wait(&bar.v_full[s], (j / kVStages) & 1))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      // zero the V rows of this tile that no row sees (0 * NaN would poison
-      // whole rows): whole 128-byte rows, so the swizzle is irrelevant
-      const int v0 = j * kBN, v1 = v0 + boxes * kBox;
-      uint4 *v = reinterpret_cast<uint4 *>(sV(s));
-      auto clear = [&](int from, int to) {
-        for (int idx = (max(from, v0) - v0) * 8 + lane; idx < (min(to, v1) - v0) * 8; idx += 32)
-          v[idx] = make_uint4(0, 0, 0, 0);
-      };
-      if ((dead_from < dead_to && dead_from < v1 && dead_to > v0) || end < v1) {
-        clear(dead_from, dead_to);
-        clear(end, v1);
-        fence_proxy_async_smem();
-      }
+      if (tile.clear_unseen(p, sV(s), j * kBN, j * kBN + boxes * kBox)) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         const uint64_t dv = umma_desc_sw128(smem_u32(sV(s)), kTileBytes, 1024);
@@ -474,11 +361,8 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int token = r / p.group;
     const int head = kvh * p.group + (r - token * p.group);
-    const int pos = pos0 + min(token, tokens - 1);      // lanes past the rows repeat the last one
-    RowSlots see;
-    see.a = slot_of(min(p.first_tokens, pos + 1));
-    see.b = slot_of(max(0, pos - p.window + 1));
-    see.c = slot_of(pos + 1);
+    // lanes past the rows repeat the last token
+    const RowSlots see = tile.row(p, tile.pos0 + min(token, tile.tokens - 1));
     const float sl2 = p.scale_log2;
     // Masked scores are replaced (by index, so NaN keys cannot leak) with the
     // raw value whose scaled logit is -inf.
@@ -487,7 +371,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     bool ok = true;
     const bool live = warp * 32 < live_threads;         // warp-uniform
     for (int j = 0; live && j < n_tiles; ++j) {
-      const int chunks = (min(kBoxes, n_boxes - j * kBoxes) + 1) / 2;
+      const int chunks = (min(kBoxes, tile.n_boxes - j * kBoxes) + 1) / 2;
       if (!softmax_tile(bar, trow, j, chunks, see, sl2, masked_raw, state)) {
         ok = false;
         break;
@@ -515,39 +399,16 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     if (!live) return;
     const bool failed = bar.bad != 0;
     const float m = state.m, d = state.d;
-    const float inv = d > 0.f ? 1.f / d : 0.f;
-    auto o = [&](int e) { return __uint_as_float(x[e >> 5][e & 31]) * inv; };
-    // Each warp puts its rows in the query buffer (free since the last QK^T
-    // completed) and reads them back so that 8 lanes cover one row's 128
-    // contiguous bytes.
-    uint4 *sw = reinterpret_cast<uint4 *>(sQ) + (r - lane) * 8;     // this warp's 32 rows
-#pragma unroll
-    for (int c = 0; c < kHeadDim / 8; ++c) {
-      uint4 w = nan4;
-      if (!failed) {
-        w.x = pack_bf16(o(8 * c + 0), o(8 * c + 1));
-        w.y = pack_bf16(o(8 * c + 2), o(8 * c + 3));
-        w.z = pack_bf16(o(8 * c + 4), o(8 * c + 5));
-        w.w = pack_bf16(o(8 * c + 6), o(8 * c + 7));
-      }
-      sw[lane * 8 + (c ^ (lane & 7))] = w;
-    }
-    __syncwarp();
-    const int cc = lane & 7;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int rr = 4 * k + (lane >> 3);                  // row within the warp's slice
-      const int tr = r - lane + rr, tok = tr / p.group;
-      if (tr < rows) {
-        const size_t row = static_cast<size_t>(q_start + i0 + tok) * p.num_qo_heads +
-                           kvh * p.group + (tr - tok * p.group);
-        reinterpret_cast<uint4 *>(p.out + row * kHeadDim)[cc] = sw[rr * 8 + (cc ^ (rr & 7))];
-      }
-    }
-    if (r < rows && p.lse) {
-      const size_t row = static_cast<size_t>(q_start + i0 + token) * p.num_qo_heads + head;
-      p.lse[row] = failed ? NAN : (d > 0.f ? (m + lg2(d)) * kLn2 : -INFINITY);
-    }
+    const size_t first_row = static_cast<size_t>(req.q_start + tile.i0) * p.num_qo_heads + kvh * p.group;
+    auto row_index = [&](int i) -> long long {           // row i of the tile
+      const int tok = i / p.group;
+      return i < rows ? static_cast<long long>(first_row + static_cast<size_t>(tok) * p.num_qo_heads + (i - tok * p.group)) : -1;
+    };
+    // the query buffer is free since the last QK^T completed
+    store_rows(p, reinterpret_cast<uint4 *>(sQ) + (r - lane) * 8, x,
+               failed ? NAN : d > 0.f ? 1.f / d : 0.f, [&](int i) { return row_index(r - lane + i); });
+    if (r < rows && p.lse)
+      p.lse[row_index(r)] = failed ? NAN : (d > 0.f ? (m + lg2(d)) * kLn2 : -INFINITY);
     return;
   }
   tc_fence_before();
