@@ -182,6 +182,7 @@ struct WindowPrefillParams {
   int max_pages_per_seq, num_pages;
   int window, first_tokens;      // both <= max_kv_len, window >= 1
   int tile_tokens;               // tokens per query tile = 128 / group
+  unsigned inv_group;            // ceil(2^16 / group): i / group for i < 128
   int num_q_tiles;               // query tiles of the longest request
 };
 

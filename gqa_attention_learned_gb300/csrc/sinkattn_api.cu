@@ -811,6 +811,7 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
   p.window = std::min(window, std::max(max_kv_len, 1));
   p.first_tokens = std::min(first_tokens, max_kv_len);
   p.tile_tokens = tile_tokens;
+  p.inv_group = static_cast<unsigned>((65536 + group - 1) / group);
   p.num_q_tiles = ceil_div(max_q_len, tile_tokens);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (sa::window_prefill_is_short(p)) {

@@ -1,22 +1,26 @@
 // Windowed prefill when the keys of a whole query tile fit at once (up to 192
 // slots: window 128 with groups of 4 and more, and short prompts).
 //
-// Such a tile is little work -- two matrix products of 128 x 192 x 64 and 24k
-// exponentials -- so a CTA per tile spends most of its life waiting for its
-// first loads, its one score tile, its one P V and its stores (window 128, 20.9k
-// tokens, 64 / 8 heads: 299 us).  Here one persistent CTA per SM keeps two
-// tiles in work and up to three more loads in flight:
-//   warp 10     walks the CTA's tiles, copies Q, K and V of each into a ring of
-//               three stages and leaves the tile's geometry beside them;
-//   warps 8, 9  one per lane of work ("slot", 256 tensor-memory columns): S =
-//               Q K^T over all of the tile's boxes, later O = P V;
-//   warps 0..7  four per slot, one thread per row: the softmax has all scores
-//               before it, so it takes the max in one pass over tensor memory
-//               and writes P over S in a second; no running state.
-// Tiles alternate between the slots, so one slot's softmax runs under the
-// other's products, loads and stores.  Rounding is that of the other prefill
-// kernels: P to bf16 for the product with V, the output once to bf16; max, sum
-// and O in fp32.
+// Such a tile is little work -- two matrix products of 128 x 144 x 64 and 18k
+// exponentials for window 128 -- so a CTA per tile spends most of its life
+// waiting for its first loads, its few score tiles, its P V and its stores.
+// Here one persistent CTA per SM keeps several tiles in work and up to three
+// in flight.  Each tile in work has a lane of its own ("slot"): a part of
+// tensor memory, a warp that issues its products and four warps of softmax.
+//   last warp   walks the CTA's tiles, copies Q and K of each into one ring of
+//               stages (free again after S) and V into another, and leaves the
+//               tile's geometry beside them;
+//   MMA warps   one per slot: S = Q K^T over all of the tile's boxes, later
+//               O = P V;
+//   softmax     one thread per row: all scores are there before it starts, so
+//               it takes the max in one pass over tensor memory and writes P
+//               over S in a second, with no running state; O then goes where
+//               the last scores were, and out by way of the tile's V stage.
+// Tiles go round the slots, so one slot's softmax runs under the others'
+// products, loads and stores.  Three slots of 160 columns serve tiles of up to
+// 10 boxes of 16 keys (window 128, group 8, without first tokens), two of 256
+// columns up to 12.  Rounding is that of the other prefill kernels: P to bf16
+// for the product with V, the output once to bf16; max, sum and O in fp32.
 
 #include "window_tile.cuh"
 
@@ -27,21 +31,31 @@ namespace {
 
 using namespace window;
 
-constexpr int kMaxBoxes = 12;                  // 192 slots
-constexpr int kMaxChunks = kMaxBoxes / 2;
-constexpr int kStages = 3, kSlots = 2;
 constexpr int kQBytes = kBM * kHeadDim * 2;
-constexpr int kKBytes = kMaxBoxes * kBoxBytes;
-constexpr int kStageBytes = kQBytes + 2 * kKBytes;
-constexpr int kThreads = (4 * kSlots + kSlots + 1) * 32;
-constexpr int kMmaWarp = 4 * kSlots, kLoadWarp = kMmaWarp + kSlots;
-constexpr uint32_t kTmemCols = 512, kSlotCols = 256;
-constexpr uint32_t kColO = 192;                // S (and P over it) from column 0 of the slot
+constexpr uint32_t kTmemCols = 512;
 
-constexpr int kOffOut = kStages * kStageBytes;
-constexpr int kOffBars = kOffOut + kSlots * kQBytes;
-constexpr int kSmemBytes = kOffBars + 1024 + 1024;          // barriers + alignment slack
-static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
+// Sizes of a variant: tiles in work, boxes of 16 keys per tile at most, stages
+// of Q and K, stages of V (a tile in work holds one).
+template <int S, int B, int NK, int NV>
+struct Shape {
+  static constexpr int kKStages = NK, kVStages = NV;
+  static constexpr int kSlots = S, kBoxes = B, kChunks = (B + 1) / 2;
+  static constexpr int kKBytes = B * kBoxBytes;
+  static constexpr int kKStageBytes = kQBytes + kKBytes;
+  static constexpr int kMmaWarp = 4 * S, kLoadWarp = 5 * S;
+  static constexpr int kThreads = (5 * S + 1) * 32;
+  // tensor memory of a slot: S from column 0, P over it, O over the last scores
+  static constexpr uint32_t kSlotCols = S == 3 ? 160 : 256;
+  static constexpr uint32_t kColO = kSlotCols - kHeadDim;
+  static constexpr int kOffV = NK * kKStageBytes;
+  static constexpr int kOffBars = kOffV + NV * kKBytes;
+  static constexpr int kSmemBytes = kOffBars + 1024 + 1024;   // barriers + alignment slack
+  static_assert(kSmemBytes <= 227 * 1024, "one CTA per SM");
+  static_assert(S * kSlotCols <= kTmemCols && 16 * B <= static_cast<int>(kSlotCols), "tensor memory");
+  static_assert(kKBytes >= kQBytes, "the output rows pass through the V stage");
+  static_assert(8 * B <= static_cast<int>(kColO), "P ends before O");
+};
+constexpr int kMaxSlots = 3, kMaxStages = 5;
 
 struct Work {
   Request req;
@@ -52,19 +66,18 @@ struct Work {
 };
 
 struct Bars {
-  uint64_t full[kStages];      // Q, K and the geometry
-  uint64_t v_full[kStages];
-  uint64_t empty[kStages];     // the stage's P V has completed
-  uint64_t s_full[kSlots], p_full[kSlots], o_full[kSlots];
-  uint64_t free[kSlots];       // O has been read
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages];   // Q, K and the geometry
+  uint64_t v_full[kMaxStages], v_empty[kMaxStages];
+  uint64_t s_full[kMaxSlots], p_full[kMaxSlots], o_full[kMaxSlots];
+  uint64_t info[kMaxSlots];    // the slot's next geometry may be read
+  uint64_t free[kMaxSlots];    // O has been read
   uint32_t tmem_base;
   int dead;                    // a wait ran out
-  Work work[kStages];
+  Work work[kMaxStages];       // by V stage
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 
 // The i-th work item of the launch.
-template <bool kPaged>
 __device__ __forceinline__ void locate(const WindowPrefillParams &p, int item, int &qt, int &seq, int &kvh) {
   kvh = item % p.num_kv_heads;
   const int rest = item / p.num_kv_heads;
@@ -72,11 +85,14 @@ __device__ __forceinline__ void locate(const WindowPrefillParams &p, int item, i
   seq = rest / p.num_q_tiles;
 }
 
-template <bool kPaged>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool kPaged, typename Sh>
+__global__ void __launch_bounds__(Sh::kThreads, 1)
 window_short_kernel(const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, const WindowPrefillParams p) {
+  constexpr int kSlots = Sh::kSlots, kMmaWarp = Sh::kMmaWarp, kLoadWarp = Sh::kLoadWarp;
+  constexpr int kThreads = Sh::kThreads, kNK = Sh::kKStages, kNV = Sh::kVStages;
+  constexpr int kKBytes = Sh::kKBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int items = p.num_q_tiles * p.num_seqs * p.num_kv_heads;
   const int stride = static_cast<int>(gridDim.x);
@@ -84,10 +100,10 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
-  Bars &bar = *reinterpret_cast<Bars *>(smem + kOffBars);
-  auto sQ = [&](int s) { return smem + s * kStageBytes; };
-  auto sK = [&](int s) { return smem + s * kStageBytes + kQBytes; };
-  auto sV = [&](int s) { return smem + s * kStageBytes + kQBytes + kKBytes; };
+  Bars &bar = *reinterpret_cast<Bars *>(smem + Sh::kOffBars);
+  auto sQ = [&](int n) { return smem + n % kNK * Sh::kKStageBytes; };     // of tile n
+  auto sK = [&](int n) { return sQ(n) + kQBytes; };
+  auto sV = [&](int n) { return smem + Sh::kOffV + n % kNV * kKBytes; };
   // a bounded wait of the whole warp; once one has run out, all fail at once
   auto wait = [&](uint64_t *b, int uses) -> bool {
     if (__all_sync(0xffffffffu, mbar_wait(b, uses & 1))) return true;
@@ -100,16 +116,20 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     tmem_relinquish();
   }
   if (threadIdx.x == kLoadWarp * 32) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bar.full[s], 1);
+    for (int s = 0; s < kNK; ++s) {
+      mbar_init(&bar.k_full[s], 1);
+      mbar_init(&bar.k_empty[s], 1);
+    }
+    for (int s = 0; s < kNV; ++s) {
       mbar_init(&bar.v_full[s], 1);
-      mbar_init(&bar.empty[s], 1);
+      mbar_init(&bar.v_empty[s], 128);
     }
     for (int l = 0; l < kSlots; ++l) {
       mbar_init(&bar.s_full[l], 1);
       mbar_init(&bar.p_full[l], 128);
       mbar_init(&bar.o_full[l], 1);
       mbar_init(&bar.free[l], 128);
+      mbar_init(&bar.info[l], 1);
     }
     bar.dead = 0;
     fence_mbar_init();
@@ -133,7 +153,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       int qt = 0, seq = 0, kvh = 0;
       Request r{};
       if (mine < items) {
-        locate<kPaged>(p, static_cast<int>(mine), qt, seq, kvh);
+        locate(p, static_cast<int>(mine), qt, seq, kvh);
         r = Request::load<kPaged>(p, seq);
         valid = !r.bad && qt * p.tile_tokens < r.q_len;
         poisoned = r.bad && qt == 0;
@@ -144,7 +164,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
                max(__shfl_sync(0xffffffffu, r.q_len, l), 0), lane, 32);
       }
       for (unsigned m = __ballot_sync(0xffffffffu, valid); ok && m; m &= m - 1, ++n) {
-        const int l = __ffs(m) - 1, s = n % kStages;
+        const int l = __ffs(m) - 1;
         Work w;
         w.req.seq = __shfl_sync(0xffffffffu, r.seq, l);
         w.req.q_start = __shfl_sync(0xffffffffu, r.q_start, l);
@@ -158,23 +178,26 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
         const int src = have ? w.tile.source<kPaged>(p, w.req, lane) : -1;
         const unsigned boxes = __ballot_sync(0xffffffffu, src >= 0);
         w.bad = __popc(boxes) != w.tile.n_boxes;
-        if (n >= kStages && !wait(&bar.empty[s], n / kStages + 1)) {
+        uint64_t *k_full = &bar.k_full[n % kNK], *v_full = &bar.v_full[n % kNV];
+        // the geometry goes by V stage, so that one has to be free first
+        if ((n >= kNV && !wait(&bar.v_empty[n % kNV], n / kNV + 1)) ||
+            (n >= kNK && !wait(&bar.k_empty[n % kNK], n / kNK + 1))) {
           ok = false;
           break;
         }
         if (lane == 0) {
-          bar.work[s] = w;                               // published by the arrival below
+          bar.work[n % kNV] = w;                         // published by the arrival below
           const uint32_t bytes = __popc(boxes) * kBoxBytes;
-          mbar_arrive_expect_tx(&bar.full[s], p.tile_tokens * p.group * kHeadDim * 2 + bytes);
-          mbar_arrive_expect_tx(&bar.v_full[s], bytes);
+          mbar_arrive_expect_tx(k_full, p.tile_tokens * p.group * kHeadDim * 2 + bytes);
+          mbar_arrive_expect_tx(v_full, bytes);
           // box {64, group, tile_tokens}: rows (token, head)
-          tma_load_3d(sQ(s), &qmap, &bar.full[s], 0, w.kvh * p.group, w.req.q_start + w.tile.i0);
+          tma_load_3d(sQ(n), &qmap, k_full, 0, w.kvh * p.group, w.req.q_start + w.tile.i0);
         }
         __syncwarp();
         if (src >= 0) {
           const int y = kPaged ? w.kvh * kPageSize : w.kvh;
-          tma_load_3d(sK(s) + lane * kBoxBytes, &kmap, &bar.full[s], 0, y, src);
-          tma_load_3d(sV(s) + lane * kBoxBytes, &vmap, &bar.v_full[s], 0, y, src);
+          tma_load_3d(sK(n) + lane * kBoxBytes, &kmap, k_full, 0, y, src);
+          tma_load_3d(sV(n) + lane * kBoxBytes, &vmap, v_full, 0, y, src);
         }
         __syncwarp();
       }
@@ -183,46 +206,50 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     }
     // one last entry per slot
     for (int l = 0; ok && l < kSlots; ++l, ++n) {
-      const int s = n % kStages;
-      if (n >= kStages && !wait(&bar.empty[s], n / kStages + 1)) break;
+      if ((n >= kNV && !wait(&bar.v_empty[n % kNV], n / kNV + 1)) ||
+          (n >= kNK && !wait(&bar.k_empty[n % kNK], n / kNK + 1)))
+        break;
       if (lane == 0) {
-        bar.work[s].stop = 1;
-        mbar_arrive(&bar.full[s]);
+        bar.work[n % kNV].stop = 1;
+        mbar_arrive(&bar.k_full[n % kNK]);
       }
       __syncwarp();
     }
   } else if (warp >= kMmaWarp) {
     // ------------------------------------- the products of one slot (one thread)
     const int slot = warp - kMmaWarp;
-    const uint32_t tS = tmem + slot * kSlotCols;
+    const uint32_t tS = tmem + slot * Sh::kSlotCols;
     for (int n = slot, k = 0;; n += kSlots, ++k) {
-      const int s = n % kStages;
-      if (!wait(&bar.full[s], n / kStages)) break;
-      if (bar.work[s].stop) break;
-      const Tile tile = bar.work[s].tile;
+      if (!wait(&bar.k_full[n % kNK], n / kNK)) break;
+      // hands the geometry on: the softmax warps cannot wait for k_full, whose
+      // stage may be filled twice more while they store the previous tile
+      if (lane == 0) mbar_arrive(&bar.info[slot]);
+      __syncwarp();
+      if (bar.work[n % kNV].stop) break;
+      const Tile tile = bar.work[n % kNV].tile;
       if (k > 0 && !wait(&bar.free[slot], k - 1)) break;
       tc_fence_after();
       if (lane == 0) {
-        const uint64_t dq = umma_desc_sw128(smem_u32(sQ(s)), 16, 1024);
-        const uint64_t dk = umma_desc_sw128(smem_u32(sK(s)), 16, 1024);
+        const uint64_t dq = umma_desc_sw128(smem_u32(sQ(n)), 16, 1024);
+        const uint64_t dk = umma_desc_sw128(smem_u32(sK(n)), 16, 1024);
         const uint32_t idesc = umma_idesc_bf16(128, kBox * tile.n_boxes, false, false);
 #pragma unroll
         for (int kk = 0; kk < kHeadDim / 16; ++kk)
           umma_ss(tS, dq + 2 * kk, dk + 2 * kk, idesc, kk > 0);   // +32 bytes per k-step
         umma_commit(&bar.s_full[slot]);
+        umma_commit(&bar.k_empty[n % kNK]);
       }
       __syncwarp();
-      if (!wait(&bar.v_full[s], n / kStages)) break;
-      if (tile.clear_unseen(p, sV(s), 0, tile.n_boxes * kBox)) fence_proxy_async_smem();
+      if (!wait(&bar.v_full[n % kNV], n / kNV)) break;
+      if (tile.clear_unseen(p, sV(n), 0, tile.n_boxes * kBox)) fence_proxy_async_smem();
       __syncwarp();
       if (!wait(&bar.p_full[slot], k)) break;
       tc_fence_after();
       if (lane == 0) {
-        const uint64_t dv = umma_desc_sw128(smem_u32(sV(s)), kKBytes, 1024);
+        const uint64_t dv = umma_desc_sw128(smem_u32(sV(n)), kKBytes, 1024);
         for (int kk = 0; kk < tile.n_boxes; ++kk)
-          umma_ts(tS + kColO, tS + 8 * kk, dv + (kBoxBytes >> 4) * kk, kIdescPV, kk > 0);
+          umma_ts(tS + Sh::kColO, tS + 8 * kk, dv + (kBoxBytes >> 4) * kk, kIdescPV, kk > 0);
         umma_commit(&bar.o_full[slot]);
-        umma_commit(&bar.empty[s]);
       }
       __syncwarp();
     }
@@ -230,16 +257,18 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     // ------------------------------------------------------- softmax, output
     const int slot = warp / 4;
     const int r = threadIdx.x & 127;                     // row = tensor-memory lane
-    const uint32_t trow = tmem + slot * kSlotCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const int token = r / p.group, in_group = r - token * p.group;
+    const uint32_t trow = tmem + slot * Sh::kSlotCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    // token of row i of a tile: i / group, exact for i < 128 and group <= 128
+    auto token_of = [&](int i) { return static_cast<int>((static_cast<uint32_t>(i) * p.inv_group) >> 16); };
+    const int token = token_of(r), in_group = r - token * p.group;
+    const int warp_first = token_of(r - lane), warp_last = token_of(r - lane + 31);
+    const int row_skip = p.num_qo_heads - p.group;       // from a token's last row to the next one's first
     const float sl2 = p.scale_log2;
     const uint64_t scale2 = f2_pack(sl2, sl2);
     const uint32_t masked_raw = sl2 >= 0.f ? 0xff800000u : 0x7f800000u;
-    uint4 *stage = reinterpret_cast<uint4 *>(smem + kOffOut + slot * kQBytes) + (r - lane) * 8;
     for (int n = slot, k = 0;; n += kSlots, ++k) {
-      const int s = n % kStages;
-      if (!wait(&bar.full[s], n / kStages)) break;       // the geometry
-      const Work &w = bar.work[s];
+      if (!wait(&bar.info[slot], k)) break;              // the geometry
+      const Work &w = bar.work[n % kNV];
       if (w.stop) break;
       const Tile tile = w.tile;
       const bool bad = w.bad != 0;
@@ -247,75 +276,89 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       const int head = w.kvh * p.group + in_group;
       const size_t first_row =
           static_cast<size_t>(w.req.q_start + tile.i0) * p.num_qo_heads + w.kvh * p.group;
-      const int chunks = (tile.n_boxes + 1) / 2;
       // lanes past the rows repeat the last token
-      const RowSlots see = tile.row(p, tile.pos0 + min(token, tile.tokens - 1));
+      const int last = tile.tokens - 1;
+      const RowSlots see = tile.row(p, tile.pos0 + min(token, last));
       const float sink = r < rows ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
-      uint32_t mask[kMaxChunks];
-      unsigned live = 0, edge = 0;                       // warp-uniform bits per chunk
-#pragma unroll
-      for (int c = 0; c < kMaxChunks; ++c) {
-        mask[c] = see.mask(32 * c);
-        live |= __any_sync(0xffffffffu, mask[c] != 0u) ? 1u << c : 0u;
-        edge |= __any_sync(0xffffffffu, mask[c] != 0xffffffffu) ? 1u << c : 0u;
-      }
+      uint32_t live, full;                               // per 16 slots, warp-uniform
+      piece_bits(tile.row(p, tile.pos0 + min(warp_first, last)), tile.row(p, tile.pos0 + min(warp_last, last)),
+                 live, full);
       if (!wait(&bar.s_full[slot], k)) break;
       tc_fence_after();
+      // pass 1: the row's max; chunks of 32 scores, the next one on its way
+      // while one is looked at (all chunks are read, whatever the tile needs:
+      // no branch decides about a load in flight)
+      uint32_t x[2][32];
       float mx = -INFINITY;
+      tmem_ld32(trow, x[0]);
 #pragma unroll
-      for (int c = 0; c < kMaxChunks; ++c) {
-        if (!((live >> c) & 1u)) continue;
-        uint32_t x[32];
-        tmem_ld32(trow + 32 * c, x);
-        tmem_ld_wait32(x);
-        if ((edge >> c) & 1u) mask_chunk(x, mask[c], masked_raw);
-        mx = fmaxf(mx, max_chunk(x, sl2));
+      for (int c = 0; c < Sh::kChunks; ++c) {
+        tmem_ld_wait32(x[c & 1]);
+        if (c + 1 < Sh::kChunks) tmem_ld32(trow + 32 * (c + 1), x[(c + 1) & 1]);
+        const uint32_t pieces = (live >> (2 * c)) & 3u, whole = (full >> (2 * c)) & 3u;
+        const uint32_t mask = pieces & ~whole ? see.mask(32 * c) : 0u;
+        if (pieces & 1u) {
+          if (!(whole & 1u)) mask_piece<0>(x[c & 1], mask, masked_raw);
+          mx = fmaxf(mx, (sl2 >= 0.f ? max_piece<0>(x[c & 1]) : min_piece<0>(x[c & 1])) * sl2);
+        }
+        if (pieces & 2u) {
+          if (!(whole & 2u)) mask_piece<16>(x[c & 1], mask, masked_raw);
+          mx = fmaxf(mx, (sl2 >= 0.f ? max_piece<16>(x[c & 1]) : min_piece<16>(x[c & 1])) * sl2);
+        }
       }
       const float m = fmaxf(sink, mx);
       const float mu = m == -INFINITY ? 0.f : m;
       const uint64_t negmu2 = f2_pack(-mu, -mu);
-      uint64_t acc = 0;                                  // (+0.f, +0.f)
-      // P over S: chunk c goes to columns 16 c .., whose scores (chunk c / 2)
-      // are in registers or used up by then
+      uint64_t acc = 0, acc1 = 0;                        // (+0.f, +0.f)
+      // pass 2: P over S: chunk c goes to columns 16 c .., whose scores (chunk
+      // c / 2) are in registers or used up by then
+      tmem_ld32(trow, x[0]);
 #pragma unroll
-      for (int c = 0; c < kMaxChunks; ++c) {
-        if (c >= chunks) continue;
-        uint32_t x[32];
-        if ((live >> c) & 1u) {
-          tmem_ld32(trow + 32 * c, x);
-          tmem_ld_wait32(x);
-          if ((edge >> c) & 1u) mask_chunk(x, mask[c], masked_raw);
-          pack_chunk(x, scale2, negmu2, acc);
+      for (int c = 0; c < Sh::kChunks; ++c) {
+        tmem_ld_wait32(x[c & 1]);
+        if (c + 1 < Sh::kChunks) tmem_ld32(trow + 32 * (c + 1), x[(c + 1) & 1]);
+        const uint32_t pieces = (live >> (2 * c)) & 3u, whole = (full >> (2 * c)) & 3u;
+        const uint32_t mask = pieces & ~whole ? see.mask(32 * c) : 0u;
+        uint32_t w[16];
+        if (pieces & 1u) {
+          if (!(whole & 1u)) mask_piece<0>(x[c & 1], mask, masked_raw);
+          pack_piece<0>(x[c & 1], w, scale2, negmu2, acc, acc1);
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = 0u;
+          for (int e = 0; e < 8; ++e) w[e] = 0u;
         }
-        tmem_st16(trow + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[0]));
+        if (pieces & 2u) {
+          if (!(whole & 2u)) mask_piece<16>(x[c & 1], mask, masked_raw);
+          pack_piece<16>(x[c & 1], w, scale2, negmu2, acc, acc1);
+        } else {
+#pragma unroll
+          for (int e = 8; e < 16; ++e) w[e] = 0u;
+        }
+        tmem_st16(trow + 16 * c, w);
       }
       float s0, s1;
-      f2_unpack(acc, s0, s1);
+      f2_unpack(f2_add(acc, acc1), s0, s1);
       const float d = ex2(sink - mu) + s0 + s1;          // the sink's term; nothing where it is -inf
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bar.p_full[slot]);
       if (!wait(&bar.o_full[slot], k)) break;
       tc_fence_after();
-      uint32_t o[2][32];
-      tmem_ld32(trow + kColO, o[0]);
-      tmem_ld32(trow + kColO + 32, o[1]);
-      tmem_ld_wait32(o[0]);
-      reg_tie32(o[1]);
+      tmem_ld32(trow + Sh::kColO, x[0]);
+      tmem_ld32(trow + Sh::kColO + 32, x[1]);
+      tmem_ld_wait32(x[0]);
+      reg_tie32(x[1]);
       tc_fence_before();
       mbar_arrive(&bar.free[slot]);
       auto row_index = [&](int i) -> long long {         // row i of the tile
-        const int tok = i / p.group;
-        return i < rows ? static_cast<long long>(first_row + static_cast<size_t>(tok) * p.num_qo_heads +
-                                                 (i - tok * p.group))
-                        : -1;
+        return i < rows ? static_cast<long long>(first_row + static_cast<size_t>(token_of(i)) * row_skip + i) : -1;
       };
-      __syncwarp();                                      // the previous tile's rows are out
-      store_rows(p, stage, o, bad ? NAN : d > 0.f ? 1.f / d : 0.f,
+      // P V has read V: the stage takes the rows on their way out, then the next
+      // copy (written by the asynchronous proxy)
+      store_rows(p, reinterpret_cast<uint4 *>(sV(n)) + (r - lane) * 8, x, bad ? NAN : d > 0.f ? 1.f / d : 0.f,
                  [&](int i) { return row_index(r - lane + i); });
+      fence_proxy_async_smem();
+      mbar_arrive(&bar.v_empty[n % kNV]);
       if (r < rows && p.lse) p.lse[row_index(r)] = bad ? NAN : d > 0.f ? (mu + lg2(d)) * kLn2 : -INFINITY;
     }
   }
@@ -329,7 +372,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     // a wait ran out: none of this CTA's tiles can be trusted
     for (long long item = blockIdx.x; item < items; item += stride) {
       int qt, seq, kvh;
-      locate<kPaged>(p, static_cast<int>(item), qt, seq, kvh);
+      locate(p, static_cast<int>(item), qt, seq, kvh);
       const Request r = Request::load<kPaged>(p, seq);
       const int i0 = qt * p.tile_tokens;
       if (!r.bad && i0 < r.q_len)
@@ -338,27 +381,33 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-template <bool kPaged>
+template <bool kPaged, typename Sh>
 cudaError_t launch_variant(const CUtensorMap &qmap, const CUtensorMap &kmap,
                            const CUtensorMap &vmap, const WindowPrefillParams &p, int num_sms,
                            cudaStream_t stream) {
-  cudaError_t err = set_smem_once<window_short_kernel<kPaged>>(kSmemBytes);
+  cudaError_t err = set_smem_once<window_short_kernel<kPaged, Sh>>(Sh::kSmemBytes);
   if (err != cudaSuccess) return err;
   const long long items = static_cast<long long>(p.num_q_tiles) * p.num_seqs * p.num_kv_heads;
-  return launch_kernel(window_short_kernel<kPaged>, static_cast<unsigned>(std::min<long long>(items, num_sms)),
-                       kThreads, kSmemBytes, stream, false, qmap, kmap, vmap, p);
+  return launch_kernel(window_short_kernel<kPaged, Sh>,
+                       static_cast<unsigned>(std::min<long long>(items, num_sms)), Sh::kThreads,
+                       Sh::kSmemBytes, stream, false, qmap, kmap, vmap, p);
+}
+
+using Three = Shape<3, 10, 3, 5>;
+using Two = Shape<2, 12, 3, 4>;
+
+// Boxes that a tile can need: the first tokens', and those of the run, which
+// may start anywhere in its first page; no more than the longest request has.
+int most_boxes(const WindowPrefillParams &p) {
+  const long long seen = cdiv(p.first_tokens, kBox) +
+                         (static_cast<long long>(p.window) + p.tile_tokens - 1 +
+                          (p.page_table ? kPageSize - 1 : 0) + kBox - 1) / kBox;
+  return static_cast<int>(std::min<long long>(seen, cdiv(p.max_kv_len, kBox)));
 }
 
 }  // namespace
 
-bool window_prefill_is_short(const WindowPrefillParams &p) {
-  // boxes of the first tokens, and of the run, which may start anywhere in its
-  // first page; or every box of the longest request
-  const long long seen = cdiv(p.first_tokens, kBox) +
-                         (static_cast<long long>(p.window) + p.tile_tokens - 1 +
-                          (p.page_table ? kPageSize - 1 : 0) + kBox - 1) / kBox;
-  return std::min<long long>(seen, cdiv(p.max_kv_len, kBox)) <= kMaxBoxes;
-}
+bool window_prefill_is_short(const WindowPrefillParams &p) { return most_boxes(p) <= Two::kBoxes; }
 
 cudaError_t launch_window_short(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, const WindowPrefillParams &p, int num_sms,
@@ -366,8 +415,11 @@ cudaError_t launch_window_short(const CUtensorMap &qmap, const CUtensorMap &kmap
   const long long items = static_cast<long long>(p.num_q_tiles) * p.num_seqs * p.num_kv_heads;
   if (items == 0) return cudaSuccess;
   if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  return p.page_table ? launch_variant<true>(qmap, kmap, vmap, p, num_sms, stream)
-                      : launch_variant<false>(qmap, kmap, vmap, p, num_sms, stream);
+  if (most_boxes(p) <= Three::kBoxes)
+    return p.page_table ? launch_variant<true, Three>(qmap, kmap, vmap, p, num_sms, stream)
+                        : launch_variant<false, Three>(qmap, kmap, vmap, p, num_sms, stream);
+  return p.page_table ? launch_variant<true, Two>(qmap, kmap, vmap, p, num_sms, stream)
+                      : launch_variant<false, Two>(qmap, kmap, vmap, p, num_sms, stream);
 }
 
 }  // namespace sa
