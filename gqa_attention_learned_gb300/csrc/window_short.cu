@@ -261,11 +261,11 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     // token of row i of a tile: i / group, exact for i < 128 and group <= 128
     auto token_of = [&](int i) { return static_cast<int>((static_cast<uint32_t>(i) * p.inv_group) >> 16); };
     const int token = token_of(r), in_group = r - token * p.group;
-    const int warp_first = token_of(r - lane), warp_last = token_of(r - lane + 31);
     const int row_skip = p.num_qo_heads - p.group;       // from a token's last row to the next one's first
     const float sl2 = p.scale_log2;
     const uint64_t scale2 = f2_pack(sl2, sl2);
-    const uint32_t masked_raw = sl2 >= 0.f ? 0xff800000u : 0x7f800000u;
+    const bool largest = sl2 >= 0.f;                     // the largest raw score is the largest scaled one
+    const uint32_t masked_raw = largest ? 0xff800000u : 0x7f800000u;
     for (int n = slot, k = 0;; n += kSlots, ++k) {
       if (!wait(&bar.info[slot], k)) break;              // the geometry
       const Work &w = bar.work[n % kNV];
@@ -277,64 +277,62 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       const size_t first_row =
           static_cast<size_t>(w.req.q_start + tile.i0) * p.num_qo_heads + w.kvh * p.group;
       // lanes past the rows repeat the last token
-      const int last = tile.tokens - 1;
-      const RowSlots see = tile.row(p, tile.pos0 + min(token, last));
+      const RowSlots see = tile.row(p, tile.pos0 + min(token, tile.tokens - 1));
       const float sink = r < rows ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
-      uint32_t live, full;                               // per 16 slots, warp-uniform
-      piece_bits(tile.row(p, tile.pos0 + min(warp_first, last)), tile.row(p, tile.pos0 + min(warp_last, last)),
-                 live, full);
+      uint32_t live, full;                               // per piece of 16 slots, warp-uniform
+      piece_bits(see, live, full);
+      live = __reduce_or_sync(0xffffffffu, live);
+      full = __reduce_and_sync(0xffffffffu, full);
       if (!wait(&bar.s_full[slot], k)) break;
       tc_fence_after();
-      // pass 1: the row's max; chunks of 32 scores, the next one on its way
-      // while one is looked at (all chunks are read, whatever the tile needs:
-      // no branch decides about a load in flight)
-      uint32_t x[2][32];
+      // pass 1: the row's max; two pieces at a time, the next two on their way
+      // while these are looked at (all are read, whatever the tile needs: no
+      // branch decides about a load in flight)
+      uint32_t x[4][16];
+      auto fetch = [&](int c) {
+        tmem_ld16(trow + 32 * c, x[2 * (c & 1)]);
+        tmem_ld16(trow + 32 * c + 16, x[2 * (c & 1) + 1]);
+      };
+      auto arrived = [&](int c) {
+        tmem_ld_wait();
+        reg_tie16(x[2 * (c & 1)]);
+        reg_tie16(x[2 * (c & 1) + 1]);
+      };
       float mx = -INFINITY;
-      tmem_ld32(trow, x[0]);
+      fetch(0);
 #pragma unroll
       for (int c = 0; c < Sh::kChunks; ++c) {
-        tmem_ld_wait32(x[c & 1]);
-        if (c + 1 < Sh::kChunks) tmem_ld32(trow + 32 * (c + 1), x[(c + 1) & 1]);
-        const uint32_t pieces = (live >> (2 * c)) & 3u, whole = (full >> (2 * c)) & 3u;
-        const uint32_t mask = pieces & ~whole ? see.mask(32 * c) : 0u;
-        if (pieces & 1u) {
-          if (!(whole & 1u)) mask_piece<0>(x[c & 1], mask, masked_raw);
-          mx = fmaxf(mx, (sl2 >= 0.f ? max_piece<0>(x[c & 1]) : min_piece<0>(x[c & 1])) * sl2);
-        }
-        if (pieces & 2u) {
-          if (!(whole & 2u)) mask_piece<16>(x[c & 1], mask, masked_raw);
-          mx = fmaxf(mx, (sl2 >= 0.f ? max_piece<16>(x[c & 1]) : min_piece<16>(x[c & 1])) * sl2);
+        arrived(c);
+        if (c + 1 < Sh::kChunks) fetch(c + 1);
+#pragma unroll
+        for (int i = 2 * c; i < 2 * c + 2; ++i) {
+          if (!((live >> i) & 1u)) continue;
+          if (!((full >> i) & 1u)) mask_piece(x[i & 3], see.mask(16 * i), masked_raw);
+          mx = fmaxf(mx, max_piece(x[i & 3], largest) * sl2);
         }
       }
       const float m = fmaxf(sink, mx);
       const float mu = m == -INFINITY ? 0.f : m;
       const uint64_t negmu2 = f2_pack(-mu, -mu);
       uint64_t acc = 0, acc1 = 0;                        // (+0.f, +0.f)
-      // pass 2: P over S: chunk c goes to columns 16 c .., whose scores (chunk
-      // c / 2) are in registers or used up by then
-      tmem_ld32(trow, x[0]);
+      // pass 2: P over S: piece i goes to columns 8 i .., whose scores (piece
+      // i / 2) are in registers or used up by then
+      fetch(0);
 #pragma unroll
       for (int c = 0; c < Sh::kChunks; ++c) {
-        tmem_ld_wait32(x[c & 1]);
-        if (c + 1 < Sh::kChunks) tmem_ld32(trow + 32 * (c + 1), x[(c + 1) & 1]);
-        const uint32_t pieces = (live >> (2 * c)) & 3u, whole = (full >> (2 * c)) & 3u;
-        const uint32_t mask = pieces & ~whole ? see.mask(32 * c) : 0u;
-        uint32_t w[16];
-        if (pieces & 1u) {
-          if (!(whole & 1u)) mask_piece<0>(x[c & 1], mask, masked_raw);
-          pack_piece<0>(x[c & 1], w, scale2, negmu2, acc, acc1);
-        } else {
+        arrived(c);
+        if (c + 1 < Sh::kChunks) fetch(c + 1);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = 0u;
-        }
-        if (pieces & 2u) {
-          if (!(whole & 2u)) mask_piece<16>(x[c & 1], mask, masked_raw);
-          pack_piece<16>(x[c & 1], w, scale2, negmu2, acc, acc1);
-        } else {
+        for (int i = 2 * c; i < 2 * c + 2; ++i) {
+          if ((live >> i) & 1u) {
+            if (!((full >> i) & 1u)) mask_piece(x[i & 3], see.mask(16 * i), masked_raw);
+            pack_piece(x[i & 3], scale2, negmu2, acc, acc1);
+          } else {
 #pragma unroll
-          for (int e = 8; e < 16; ++e) w[e] = 0u;
+            for (int e = 0; e < 8; ++e) x[i & 3][e] = 0u;
+          }
+          tmem_st8(trow + 8 * i, x[i & 3]);
         }
-        tmem_st16(trow + 16 * c, w);
       }
       float s0, s1;
       f2_unpack(f2_add(acc, acc1), s0, s1);
@@ -344,10 +342,11 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       mbar_arrive(&bar.p_full[slot]);
       if (!wait(&bar.o_full[slot], k)) break;
       tc_fence_after();
-      tmem_ld32(trow + Sh::kColO, x[0]);
-      tmem_ld32(trow + Sh::kColO + 32, x[1]);
-      tmem_ld_wait32(x[0]);
-      reg_tie32(x[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld16(trow + Sh::kColO + 16 * i, x[i]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reg_tie16(x[i]);
       tc_fence_before();
       mbar_arrive(&bar.free[slot]);
       auto row_index = [&](int i) -> long long {         // row i of the tile

@@ -73,51 +73,45 @@ __device__ __forceinline__ float max_chunk(const uint32_t (&x)[32], float sl2) {
 // Bits below n (n <= 0: none).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// The 16-slot pieces that the rows of a warp see, from the ranges of its first
-// and last row (every bound grows with the position): bit i of `live` if some
-// row sees a slot of piece i, bit i of `full` if every row sees all of it.
-__device__ __forceinline__ void piece_bits(const RowSlots &first, const RowSlots &last,
-                                           uint32_t &live, uint32_t &full) {
-  live = low_bits((last.a + 15) / 16) | (low_bits((last.c + 15) / 16) & ~low_bits(first.b / 16));
-  full = low_bits(first.a / 16) | (low_bits(first.c / 16) & ~low_bits((last.b + 15) / 16));
+// The 16-slot pieces that a row sees: bit i of `live` if it sees a slot of
+// piece i, bit i of `full` if it sees all of it.
+__device__ __forceinline__ void piece_bits(const RowSlots &r, uint32_t &live, uint32_t &full) {
+  live = low_bits((r.a + 15) / 16) | (low_bits((r.c + 15) / 16) & ~low_bits(r.b / 16));
+  full = low_bits(r.a / 16) | (low_bits(r.c / 16) & ~low_bits((r.b + 15) / 16));
 }
 
-// 16 scores from x[E0] on: masked, their maximum (raw), their weights.
-template <int E0>
-__device__ __forceinline__ void mask_piece(uint32_t (&x)[32], uint32_t mask, uint32_t masked_raw) {
+// 16 raw scores: masked by the low bits of `mask`, their maximum, and their
+// weights P = 2^(s * sl2 - mu) as bf16 pairs in x[0..7], summed into two
+// accumulators.
+__device__ __forceinline__ void mask_piece(uint32_t (&x)[16], uint32_t mask, uint32_t masked_raw) {
 #pragma unroll
-  for (int e = E0; e < E0 + 16; ++e)
+  for (int e = 0; e < 16; ++e)
     if (!((mask >> e) & 1u)) x[e] = masked_raw;
 }
-template <int E0>
-__device__ __forceinline__ float max_piece(const uint32_t (&x)[32]) {
-  auto f = [&](int e) { return __uint_as_float(x[E0 + e]); };
-  const float a = fmax3(f(0), f(1), f(2)), b = fmax3(f(3), f(4), f(5)), c = fmax3(f(6), f(7), f(8));
-  const float d = fmax3(f(9), f(10), f(11)), e = fmax3(f(12), f(13), f(14));
-  return fmax3(fmax3(a, b, c), fmax3(d, e, f(15)), f(0));
-}
-template <int E0>
-__device__ __forceinline__ float min_piece(const uint32_t (&x)[32]) {
-  float r = INFINITY;
+__device__ __forceinline__ float max_piece(const uint32_t (&x)[16], bool largest) {
+  auto f = [&](int e) { return __uint_as_float(x[e]); };
+  if (largest) {
+    const float a = fmax3(f(0), f(1), f(2)), b = fmax3(f(3), f(4), f(5)), c = fmax3(f(6), f(7), f(8));
+    const float d = fmax3(f(9), f(10), f(11)), e = fmax3(f(12), f(13), f(14));
+    return fmaxf(fmax3(a, b, c), fmax3(d, e, f(15)));
+  }
+  float r = f(0);
 #pragma unroll
-  for (int e = E0; e < E0 + 16; ++e) r = fminf(r, __uint_as_float(x[e]));
+  for (int e = 1; e < 16; ++e) r = fminf(r, f(e));
   return r;
 }
-// P = 2^(s * sl2 - mu) of 16 scores as bf16 pairs into out[E0 / 2 ..]; sums
-// into two accumulators.
-template <int E0, int I = 0>
-__device__ __forceinline__ void pack_piece(const uint32_t (&x)[32], uint32_t (&out)[16], uint64_t scale2,
-                                           uint64_t negmu2, uint64_t &acc0, uint64_t &acc1) {
+template <int I = 0>
+__device__ __forceinline__ void pack_piece(uint32_t (&x)[16], uint64_t scale2, uint64_t negmu2,
+                                           uint64_t &acc0, uint64_t &acc1) {
   if constexpr (I < 8) {
     float x0, x1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[E0 + 2 * I]), __uint_as_float(x[E0 + 2 * I + 1])), scale2,
-                     negmu2),
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * I]), __uint_as_float(x[2 * I + 1])), scale2, negmu2),
               x0, x1);
     const float p0 = ex2(x0), p1 = ex2(x1);
     if constexpr (I & 1) acc1 = f2_add(acc1, f2_pack(p0, p1));
     else acc0 = f2_add(acc0, f2_pack(p0, p1));
-    out[E0 / 2 + I] = pack_bf16(p0, p1);
-    pack_piece<E0, I + 1>(x, out, scale2, negmu2, acc0, acc1);
+    x[I] = pack_bf16(p0, p1);
+    pack_piece<I + 1>(x, scale2, negmu2, acc0, acc1);
   }
 }
 
@@ -216,22 +210,26 @@ struct Tile {
   }
 };
 
-// Writes a warp's 32 finished rows (one per lane, o: 64 fp32 in two halves,
-// times inv) as whole 128-byte lines, through 4 KB of shared memory: 8 lanes
-// cover one row.  row_of(i) is the row index of the warp's i-th row, < 0: none.
-template <typename RowOf>
+// Writes a warp's 32 finished rows (one per lane, x: 64 fp32, times inv) as
+// whole 128-byte lines, through 4 KB of shared memory: 8 lanes cover one row.
+// row_of(i) is the row index of the warp's i-th row, < 0: none.
+template <int N, typename RowOf>
 __device__ __forceinline__ void store_rows(const WindowPrefillParams &p, uint4 *stage,
-                                           const uint32_t (&x)[2][32], float inv, RowOf row_of) {
+                                           const uint32_t (&x)[kHeadDim / N][N], float inv, RowOf row_of) {
   const int lane = threadIdx.x & 31;
-  auto o = [&](int e) { return __uint_as_float(x[e >> 5][e & 31]) * inv; };
+  const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
   for (int c = 0; c < kHeadDim / 8; ++c) {
-    uint4 w;
-    w.x = pack_bf16(o(8 * c + 0), o(8 * c + 1));
-    w.y = pack_bf16(o(8 * c + 2), o(8 * c + 3));
-    w.z = pack_bf16(o(8 * c + 4), o(8 * c + 5));
-    w.w = pack_bf16(o(8 * c + 6), o(8 * c + 7));
-    stage[lane * 8 + (c ^ (lane & 7))] = w;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = 8 * c + 2 * e;
+      float lo, hi;
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(x[at / N][at % N]), __uint_as_float(x[at / N][at % N + 1])), inv2),
+                lo, hi);
+      w[e] = pack_bf16(lo, hi);
+    }
+    stage[lane * 8 + (c ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncwarp();
   const int cc = lane & 7;
