@@ -213,10 +213,9 @@ struct MassParams {
   int num_chunks, pages_per_chunk;   // decode form: CTAs per (request, KV head)
   int tile_tokens;                   // prefill form: tokens per query tile = 128 / group
   int split;                         // prefill form: CTAs that share the query tiles of a key pair
-  int pairs_per_cta;                 // prefill form: key pairs a CTA takes (1 when split > 1)
+  int num_sms;
 };
 
-int prefill_mass_pair_keys();        // keys of a key pair
 
 int decode_mass_warps();         // pages a CTA of the decode form works on at a time
 cudaError_t launch_decode_mass(const MassParams &p, cudaStream_t stream);

@@ -23,7 +23,8 @@
 // streams the query rows that see them past the resident K, 128 (token, head)
 // rows at a time: S^T[128 keys x 128 rows] by tcgen05 into tensor memory for
 // each of two groups of four warps, in which one thread per key adds its row
-// of weights in registers -- no sums across threads.  Long prompts split the
+// of weights in registers -- no sums across threads.  A group has two score
+// buffers of 64 columns, so the next scores are made while these are summed.  Long prompts split the
 // query tiles of a key pair over a cluster of CTAs, joined in rank order
 // through distributed shared memory; few query rows give each CTA a run of key
 // pairs instead, whose K tiles stream as well.
@@ -33,6 +34,7 @@
 
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cmath>
 
 namespace sa {
@@ -162,28 +164,29 @@ constexpr int kRows = 128;                       // query rows per streamed tile
 constexpr int kKStages = 3, kQStages = 3;
 constexpr int kTileBytes = 128 * kHeadDim * 2;
 constexpr int kGroups = 2;                       // groups of four warps, one key tile each
-constexpr int kThreads = 128 * kGroups + 64;
-constexpr int kLoadWarp = 4 * kGroups, kMmaWarp = kLoadWarp + 1;
-constexpr uint32_t kTmemCols = 128 * kGroups;    // one score buffer per group
+constexpr int kLoadWarp = 4 * kGroups, kMmaWarp = kLoadWarp + 1;   // one issuing warp per group
+constexpr int kThreads = (kMmaWarp + kGroups) * 32;
+constexpr int kHalf = kRows / 2;                 // columns per score buffer: one is read, one filled
+constexpr uint32_t kTmemCols = 2 * kHalf * kGroups;
 
 constexpr int kOffK = 0;
 constexpr int kOffQ = kOffK + kKStages * kTileBytes;
 constexpr int kOffL = kOffQ + kQStages * kTileBytes;
 constexpr int kOffSum = kOffL + kQStages * kRows * 4;
-constexpr int kOffBars = kOffSum + kGroups * kKeys * 4;
+constexpr int kOffBars = kOffSum + 2 * kGroups * kKeys * 4;
 constexpr int kSmemBytes = kOffBars + 256 + 1024;
 static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
 
 struct Bars {
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t q_full[kQStages], q_empty[kQStages];  // Q and -lse of a tile
-  uint64_t s_full[kGroups], s_free[kGroups];
+  uint64_t s_full[kGroups][2], s_free[kGroups][2];
   uint32_t tmem_base;
   int bad_wait;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-constexpr uint32_t kIdesc = umma_idesc_bf16(128, 128, false, false);
+constexpr uint32_t kIdesc = umma_idesc_bf16(128, kHalf, false, false);
 
 // Sum over 32 columns of 2^(s * scale + nl), s in r, nl in shared memory.
 template <int E = 0>
@@ -202,28 +205,115 @@ __device__ __forceinline__ void add_chunk(uint32_t (&r)[32], const float4 *nl, u
   }
 }
 
-// The steps of one CTA: for each of its key pairs (256 keys, one tile of 128
-// per group of warps) the query tiles that see it, of which this CTA of the
-// cluster takes every split-th.  Every role walks the same steps.
+// The query tiles that a CTA of a cluster takes of one key pair (256 keys, one
+// tile of 128 per group of warps): of those with a row that sees the pair,
+// every split-th.
 struct Steps {
-  int q_len, kv_len, shift, tile_tokens, split, rank;
-  int key0, i_start, n;               // of the current pair: first key, first token, steps
-  int skip[kGroups];                  // first step that group takes part in (n: none)
-  __device__ __forceinline__ void pair(int kp) {
-    key0 = kp * kKeys * kGroups;
-    i_start = max(0, key0 - shift);   // first token that sees a key of the pair
-    const int tiles = cdiv(q_len - i_start, tile_tokens);
-    n = tiles > rank ? cdiv(tiles - rank, split) : 0;
+  int key0, i_start, n;               // first key, first token that sees one of the keys, tiles
+  int skip[kGroups];                  // first tile that the group takes part in (n: none)
+};
+
+// What a CTA works on: key pairs of (request, KV head) units.  Every role walks
+// the same sequence.
+//   split > 1   : pair c of the unit and its mirror image n - 1 - c, which
+//                 together are seen by about as many rows whatever c is; the
+//                 cluster's CTAs share the rows.
+//   split == 1  : an equal share of all pairs of the launch, in order.
+struct Walk {
+  int seq, kvh, kp, pairs;            // current pair, pairs of its request
+  int left;                           // pairs to go, this one included
+  int q_start, q_len, kv_len, shift;  // shift: position of the first row's token
+
+  // Loads request `seq`; pairs = 0 if there is nothing to add.  True if its
+  // arguments are out of range.
+  __device__ __forceinline__ bool request(const MassParams &p, int r) {
+    seq = r;
+    q_start = p.cu_seqlens_q[r];
+    const int q_end = p.cu_seqlens_q[r + 1];
+    q_len = q_end - q_start;
+    kv_len = p.kv_lens[r];
+    shift = kv_len - q_len;
+    const bool bad = bad_request(p, kv_len) || q_start < 0 || q_len < 0 || q_end > p.total_q ||
+                     q_len > p.max_q_len || kv_len < q_len;
+    pairs = bad || q_len == 0 ? 0 : cdiv(kv_len, kKeys * kGroups);
+    return bad;
+  }
+  // Called by whole warps.
+  __device__ void begin(const MassParams &p) {
+    if (p.split > 1) {
+      const int item = static_cast<int>(blockIdx.x / p.split), units = p.num_seqs * p.num_kv_heads;
+      const int unit = item % units;
+      kp = item / units;
+      kvh = unit % p.num_kv_heads;
+      request(p, unit / p.num_kv_heads);
+      left = kp >= (pairs + 1) / 2 ? 0 : kp == pairs - 1 - kp ? 1 : 2;
+      return;
+    }
+    // pairs before each request, 32 requests at a time: first their number,
+    // then where this CTA's share begins
+    const int lane = threadIdx.x & 31;
+    long long total = 0, first = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      long long before = 0;
+      for (int r0 = 0; r0 < p.num_seqs; r0 += 32) {
+        pairs = 0;
+        if (r0 + lane < p.num_seqs) request(p, r0 + lane);
+        long long upto = static_cast<long long>(pairs) * p.num_kv_heads;
 #pragma unroll
-    for (int w = 0; w < kGroups; ++w) {
-      const int first_key = key0 + w * kKeys;
-      // tile that holds the first token to see the group's keys
-      const int tile = (max(0, first_key - shift) - i_start) / tile_tokens;
-      skip[w] = first_key >= kv_len ? n : min(n, max(0, cdiv(tile - rank, split)));
+        for (int off = 1; off < 32; off <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += y;
+        }
+        const unsigned reach = __ballot_sync(0xffffffffu, pass == 1 && before + upto > first);
+        if (reach) {                                     // the request of this CTA's first pair
+          const int l = __ffs(reach) - 1;
+          const long long at =
+              first - before - (l ? __shfl_sync(0xffffffffu, upto, max(l - 1, 0)) : 0);
+          request(p, r0 + l);
+          kvh = static_cast<int>(at / pairs);
+          kp = static_cast<int>(at % pairs);
+          return;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      total = before;
+      first = total * blockIdx.x / gridDim.x;
+      left = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - first);
+      if (left == 0) return;
     }
   }
-  __device__ __forceinline__ int token(int step) const {
-    return i_start + (step * split + rank) * tile_tokens;
+  __device__ __forceinline__ void next(const MassParams &p) {
+    if (--left == 0) return;
+    if (p.split > 1) {
+      kp = pairs - 1 - kp;
+    } else if (++kp == pairs) {
+      kp = 0;
+      if (++kvh == p.num_kv_heads) {
+        kvh = 0;
+        do request(p, seq + 1);
+        while (pairs == 0);
+      }
+    }
+  }
+  __device__ __forceinline__ Steps steps(const MassParams &p) const {
+    Steps s;
+    const int rank = static_cast<int>(blockIdx.x % p.split);
+    s.key0 = kp * kKeys * kGroups;
+    s.i_start = max(0, s.key0 - shift);
+    const int tiles = cdiv(q_len - s.i_start, p.tile_tokens);
+    s.n = tiles > rank ? cdiv(tiles - rank, p.split) : 0;
+#pragma unroll
+    for (int w = 0; w < kGroups; ++w) {
+      const int first_key = s.key0 + w * kKeys;
+      // tile that holds the first token to see the group's keys
+      const int tile = (max(0, first_key - shift) - s.i_start) / p.tile_tokens;
+      s.skip[w] = first_key >= kv_len ? s.n : min(s.n, max(0, cdiv(tile - rank, p.split)));
+    }
+    s.i_start += rank * p.tile_tokens;                   // of this CTA's first tile
+    return s;
+  }
+  __device__ __forceinline__ float *row(const MassParams &p) const {
+    return p.mass + (static_cast<size_t>(seq) * p.num_kv_heads + kvh) * p.mass_stride;
   }
 };
 
@@ -231,29 +321,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap, const MassParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // ---- work item: (run of key pairs, request, KV head, share of the query
-  // tiles); earlier keys, which more rows see, first
-  const int item = static_cast<int>(blockIdx.x / p.split);
-  const int per_run = p.num_seqs * p.num_kv_heads;
-  const int run = item / per_run, unit = item % per_run;
-  const int kvh = unit % p.num_kv_heads, seq = unit / p.num_kv_heads;
-  const int q_start = p.cu_seqlens_q[seq], q_end = p.cu_seqlens_q[seq + 1];
-  Steps st;
-  st.q_len = q_end - q_start;
-  st.kv_len = p.kv_lens[seq];
-  st.shift = st.kv_len - st.q_len;                       // position of the first row's token
-  st.tile_tokens = p.tile_tokens;
-  st.split = p.split;
-  st.rank = static_cast<int>(blockIdx.x % p.split);
-  float *mass = p.mass + static_cast<size_t>(unit) * p.mass_stride;
-  if (bad_request(p, st.kv_len) || q_start < 0 || st.q_len < 0 || q_end > p.total_q ||
-      st.q_len > p.max_q_len || st.kv_len < st.q_len) {
-    if (run == 0 && st.rank == 0) poison_row(p, mass);
-    return;                                              // the whole cluster returns
+  Walk walk;
+  walk.begin(p);
+  const int step_tokens = p.split * p.tile_tokens;       // from one tile of this CTA to its next
+  // requests whose arguments are out of range: NaN over their mass rows
+  for (int r = static_cast<int>(blockIdx.x); r < p.num_seqs; r += static_cast<int>(gridDim.x)) {
+    Walk bad;
+    if (bad.request(p, r))
+      for (int h = 0; h < p.num_kv_heads; ++h)
+        poison_row(p, p.mass + (static_cast<size_t>(r) * p.num_kv_heads + h) * p.mass_stride);
   }
-  const int kp_begin = run * p.pairs_per_cta;
-  const int kp_end = min(kp_begin + p.pairs_per_cta, cdiv(st.kv_len, kKeys * kGroups));
-  if (kp_begin >= kp_end || st.q_len == 0) return;
+  if (walk.left == 0) return;                            // the whole cluster returns
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -275,11 +353,13 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     }
     for (int s = 0; s < kQStages; ++s) {
       mbar_init(&bar.q_full[s], 1 + 32);                 // the copy, and the lanes that write -lse
-      mbar_init(&bar.q_empty[s], 1 + 128 * kGroups);     // the MMAs, and the readers of -lse
+      mbar_init(&bar.q_empty[s], kGroups + 128 * kGroups);   // the MMAs, and the readers of -lse
     }
     for (int w = 0; w < kGroups; ++w) {
-      mbar_init(&bar.s_full[w], 1);
-      mbar_init(&bar.s_free[w], 128);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&bar.s_full[w][h], 1);
+        mbar_init(&bar.s_free[w][h], 128);
+      }
     }
     bar.bad_wait = 0;
     fence_mbar_init();
@@ -293,8 +373,31 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     // ---------------------------------------- key tiles, query tiles and -lse
     bool ok = true;
     int kn = 0, qn = 0;                                  // tiles loaded so far
-    for (int kp = kp_begin; ok && kp < kp_end; ++kp) {
-      st.pair(kp);
+    // this lane's rows of a query tile, and their lse (read two steps ahead:
+    // the copies are asynchronous, so these loads are the latency that counts)
+    constexpr int kMine = kRows / 32;
+    int in_tile[kMine], row_at[kMine];
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+      const int r = lane + 32 * u, tk = r / p.group;
+      in_tile[u] = r;
+      row_at[u] = tk * p.num_qo_heads + (r - tk * p.group);
+    }
+    auto load_lse = [&](const Steps &st, int step, float (&l)[kMine]) {
+      if (step >= st.n) return;
+      const int tok = st.i_start + step * step_tokens;
+      const int rows = min(p.tile_tokens, walk.q_len - tok) * p.group;
+      const float *from = p.lse + static_cast<size_t>(walk.q_start + tok) * p.num_qo_heads +
+                          walk.kvh * p.group;
+#pragma unroll
+      for (int u = 0; u < kMine; ++u)                    // columns past the rows add nothing
+        l[u] = in_tile[u] < rows ? __ldg(from + row_at[u]) : INFINITY;
+    };
+    for (; ok && walk.left > 0; walk.next(p)) {
+      const Steps st = walk.steps(p);
+      float lse[2][kMine];
+      load_lse(st, 0, lse[0]);
+      load_lse(st, 1, lse[1]);
       for (int j = 0; ok && j < st.n; ++j, ++qn) {
         for (int w = 0; w < kGroups; ++w) {
           if (j != 0 || st.skip[w] >= st.n) continue;
@@ -302,8 +405,8 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
           const int s = kn % kKStages;
           const int pg = (st.key0 + w * kKeys) / kPageSize + lane;
           int id = -1;                                   // not in the pool: not copied
-          if (lane < kKeys / kPageSize && pg < cdiv(st.kv_len, kPageSize)) {
-            id = p.page_table[static_cast<size_t>(seq) * p.max_pages_per_seq + pg];
+          if (lane < kKeys / kPageSize && pg < cdiv(walk.kv_len, kPageSize)) {
+            id = p.page_table[static_cast<size_t>(walk.seq) * p.max_pages_per_seq + pg];
             if (id >= p.num_pages) id = -1;
           }
           if (kn >= kKStages && !__all_sync(0xffffffffu, mbar_wait(&bar.k_empty[s], ((kn / kKStages) + 1) & 1))) {
@@ -316,7 +419,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
           __syncwarp();
           if (id >= 0)
             tma_load_3d(sK(s) + lane * kPageSize * kHeadDim * 2, &kmap, &bar.k_full[s], 0,
-                        kvh * kPageSize, id);
+                        walk.kvh * kPageSize, id);
           __syncwarp();
           ++kn;
         }
@@ -324,62 +427,61 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
         if (ok && qn >= kQStages && !__all_sync(0xffffffffu, mbar_wait(&bar.q_empty[s], ((qn / kQStages) + 1) & 1)))
           ok = false;
         if (!ok) break;
-        const int tok0 = q_start + st.token(j);
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar.q_full[s], p.tile_tokens * p.group * kHeadDim * 2);
-          tma_load_3d(sQ(s), &qmap, &bar.q_full[s], 0, kvh * p.group, tok0);
+          tma_load_3d(sQ(s), &qmap, &bar.q_full[s], 0, walk.kvh * p.group,
+                      walk.q_start + st.i_start + j * step_tokens);
         }
-        const int rows = min(p.tile_tokens, q_end - tok0) * p.group;
 #pragma unroll
-        for (int r = lane; r < kRows; r += 32) {
-          float l = INFINITY;                            // columns past the rows add nothing
-          if (r < rows) {
-            const int tk = r / p.group;
-            l = __ldg(p.lse + static_cast<size_t>(tok0 + tk) * p.num_qo_heads + kvh * p.group +
-                      (r - tk * p.group));
-          }
-          sL(s)[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        for (int u = 0; u < kMine; ++u) {
+          const float l = lse[0][u];
+          sL(s)[in_tile[u]] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+          lse[0][u] = lse[1][u];
         }
+        load_lse(st, j + 2, lse[1]);
         mbar_arrive(&bar.q_full[s]);
       }
     }
     if (!ok && lane == 0) atomicOr(&bar.bad_wait, 1);
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------- S^T = K Q^T (one thread)
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------- S^T = K Q^T of one group (one thread).  A
+    // thread each: with one for both, each group waited for the other's turn.
+    const int w = warp - kMmaWarp;
     bool ok = true;
-    int kn = 0, qn = 0, sn[kGroups] = {0, 0};
-    for (int kp = kp_begin; ok && kp < kp_end; ++kp) {
-      st.pair(kp);
-      int ks[kGroups];                                   // each group's key tile (load number)
-#pragma unroll
-      for (int w = 0; w < kGroups; ++w) {
-        ks[w] = kn;
-        if (st.skip[w] < st.n) ++kn;
-      }
+    int kn = 0, qn = 0, sn = 0;
+    for (; ok && walk.left > 0; walk.next(p)) {
+      const Steps st = walk.steps(p);
+      // number of this group's key tile among those loaded
+      const int tile = kn + (w == 1 && st.skip[0] < st.n ? 1 : 0);
+      kn += (st.skip[0] < st.n ? 1 : 0) + (st.skip[1] < st.n ? 1 : 0);
+      const int my_skip = w == 0 ? st.skip[0] : st.skip[1];
+      const int k = tile % kKStages;
+      const uint64_t dk = umma_desc_sw128(smem_u32(sK(k)), 16, 1024);
       for (int j = 0; ok && j < st.n; ++j, ++qn) {
         const int s = qn % kQStages;
         ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_full[s], (qn / kQStages) & 1));
-        const uint64_t dq = umma_desc_sw128(smem_u32(sQ(s)), 16, 1024);
+        if (ok && j == my_skip) ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_full[k], (tile / kKStages) & 1));
+        if (j >= my_skip) {
 #pragma unroll
-        for (int w = 0; w < kGroups; ++w) {
-          if (!ok || j < st.skip[w]) continue;
-          const int k = ks[w] % kKStages;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_full[k], (ks[w] / kKStages) & 1)) &&
-               (sn[w] == 0 || __all_sync(0xffffffffu, mbar_wait(&bar.s_free[w], (sn[w] - 1) & 1)));
-          if (!ok) continue;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t dk = umma_desc_sw128(smem_u32(sK(k)), 16, 1024);
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && (sn == 0 || __all_sync(0xffffffffu, mbar_wait(&bar.s_free[w][h], (sn - 1) & 1)));
+            if (!ok) continue;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint64_t dq = umma_desc_sw128(smem_u32(sQ(s) + h * (kTileBytes / 2)), 16, 1024);
 #pragma unroll
-            for (int kk = 0; kk < kHeadDim / 16; ++kk)
-              umma_ss(tmem + w * kRows, dk + 2 * kk, dq + 2 * kk, kIdesc, kk > 0);
-            umma_commit(&bar.s_full[w]);
-            if (j == st.n - 1) umma_commit(&bar.k_empty[k]);
+              for (int kk = 0; kk < kHeadDim / 16; ++kk)
+                umma_ss(tmem + (2 * w + h) * kHalf, dk + 2 * kk, dq + 2 * kk, kIdesc, kk > 0);
+              umma_commit(&bar.s_full[w][h]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          ++sn[w];
+          ++sn;
         }
-        if (ok && lane == 0) umma_commit(&bar.q_empty[s]);
+        if (ok && lane == 0) {
+          umma_commit(&bar.q_empty[s]);
+          if (j == st.n - 1 && my_skip < st.n) umma_commit(&bar.k_empty[k]);
+        }
         __syncwarp();
       }
     }
@@ -387,23 +489,27 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
   } else {
     // ------------------------------------------------ one thread per key
     const int w = warp / 4;                              // group
-    const uint32_t trow = tmem + w * kRows + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t trow = tmem + 2 * w * kHalf + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int row = threadIdx.x & 127;
     const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
     const uint32_t masked = p.scale_log2 >= 0.f ? 0xff800000u : 0x7f800000u;
     bool ok = true;
     int qn = 0, sn = 0;
-    for (int kp = kp_begin; ok && kp < kp_end; ++kp) {
-      st.pair(kp);
+    for (int item = 0; ok && walk.left > 0; ++item, walk.next(p)) {
+      const Steps st = walk.steps(p);
       const int my_skip = w == 0 ? st.skip[0] : st.skip[kGroups - 1];
       const int key = st.key0 + w * kKeys + row;
-      const bool writes = key < st.kv_len && st.rank == 0;
-      const float before = writes ? mass[key] : 0.f;
+      const bool writes = key < walk.kv_len;
+      float *sum_to = walk.row(p) + key;
+      const float before = writes && p.split == 1 ? *sum_to : 0.f;
       bool bad_page = false;                             // a key on a page outside the pool: NaN
-      if (key < st.kv_len) {
-        const int id = __ldg(p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq + key / kPageSize);
+      if (writes) {
+        const int id = __ldg(p.page_table + static_cast<size_t>(walk.seq) * p.max_pages_per_seq + key / kPageSize);
         bad_page = id < 0 || id >= p.num_pages;
       }
+      // tokens from this CTA's current tile to the first one that sees the key
+      int ahead = key - walk.shift - st.i_start;
+      int tokens_left = walk.q_len - st.i_start;
       uint64_t acc0 = 0, acc1 = 0;                       // (+0.f, +0.f)
       for (int j = 0; j < st.n; ++j, ++qn) {
         const int s = qn % kQStages;
@@ -412,50 +518,60 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
           ok = false;
           break;
         }
+        // columns [from, rows) see this key
+        const int rows = min(p.tile_tokens, tokens_left) * p.group, from = max(0, ahead) * p.group;
+        ahead -= step_tokens;
+        tokens_left -= step_tokens;
         if (j < my_skip) {
           mbar_arrive(&bar.q_empty[s]);
           continue;
         }
-        const int tok = st.token(j);
-        // columns [from, rows) see this key
-        const int rows = min(p.tile_tokens, st.q_len - tok) * p.group;
-        const int from = max(0, key - st.shift - tok) * p.group;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[w], sn & 1))) {
-          ok = false;
-          break;
-        }
-        ++sn;
-        tc_fence_after();
         const bool edge = __any_sync(0xffffffffu, from > 0 || rows < kRows);
-        const float4 *nl = reinterpret_cast<const float4 *>(sL(s));
-        uint32_t x[2][32];
-        tmem_ld32(trow, x[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait32(x[c & 1]);
-          if (c < 3) {
-            tmem_ld32(trow + 32 * (c + 1), x[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            mbar_arrive(&bar.s_free[w]);
+        for (int h = 0; h < 2; ++h) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[w][h], sn & 1))) {
+            ok = false;
+            break;
           }
-          if (edge) {
+          tc_fence_after();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e < from || 32 * c + e >= rows) x[c & 1][e] = masked;
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            tmem_ld32(trow + h * kHalf + 32 * c, x);
+            tmem_ld_wait32(x);
+            if (c == 1) {
+              tc_fence_before();
+              mbar_arrive(&bar.s_free[w][h]);
+            }
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int col = h * kHalf + 32 * c + e;
+                if (col < from || col >= rows) x[e] = masked;
+              }
+            }
+            add_chunk(x, reinterpret_cast<const float4 *>(sL(s) + h * kHalf + 32 * c), scale2, acc0, acc1);
           }
-          add_chunk(x[c & 1], nl + 8 * c, scale2, acc0, acc1);
         }
+        if (!ok) break;
+        ++sn;
         mbar_arrive(&bar.q_empty[s]);
       }
       float a, b, c, d;
       f2_unpack(acc0, a, b);
       f2_unpack(acc1, c, d);
       const float sum = bad_page ? NAN : (a + b) + (c + d);
-      if (p.split > 1) sums[threadIdx.x] = sum;
-      else if (ok && writes) mass[key] = before + sum;
+      if (p.split > 1) sums[item * kKeys * kGroups + threadIdx.x] = sum;
+      else if (writes) *sum_to = ok ? before + sum : NAN;
     }
-    if (!ok) atomicOr(&bar.bad_wait, 1);
+    if (!ok) {
+      // a wait ran out: none of the sums to come can be made
+      atomicOr(&bar.bad_wait, 1);
+      for (; p.split == 1 && walk.left > 0; walk.next(p)) {
+        const int key = walk.kp * kKeys * kGroups + w * kKeys + row;
+        if (key < walk.kv_len) walk.row(p)[key] = NAN;
+      }
+    }
     tc_fence_before();
   }
   __syncthreads();
@@ -463,23 +579,29 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  const int key = kp_begin * kKeys * kGroups + static_cast<int>(threadIdx.x);
   if (p.split > 1) {
-    // the shares of the cluster's CTAs, in rank order (one key pair per CTA);
-    // a wait that ran out gives NaN
+    // the shares of the cluster's CTAs, in rank order; a wait that ran out
+    // gives NaN
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    if (bar.bad_wait && threadIdx.x < kKeys * kGroups) sums[threadIdx.x] = NAN;
+    if (bar.bad_wait)
+      for (int i = threadIdx.x; i < 2 * kKeys * kGroups; i += kThreads) sums[i] = NAN;
     cluster.sync();
-    if (st.rank == 0 && threadIdx.x < kKeys * kGroups && key < st.kv_len) {
-      float total = mass[key];
-      for (int r = 0; r < p.split; ++r) total += *cluster.map_shared_rank(sums + threadIdx.x, r);
-      mass[key] = total;
+    Walk mine;
+    mine.begin(p);
+    for (int item = 0; mine.left > 0; ++item, mine.next(p)) {
+      // rank r writes keys r, r + split, ... of the pair
+      for (int i = static_cast<int>(blockIdx.x % p.split) + p.split * static_cast<int>(threadIdx.x);
+           i < kKeys * kGroups; i += p.split * kThreads) {
+        const int key = mine.kp * kKeys * kGroups + i;
+        if (key >= mine.kv_len) continue;
+        float total = mine.row(p)[key];
+        for (int r = 0; r < p.split; ++r)
+          total += *cluster.map_shared_rank(sums + item * kKeys * kGroups + i, r);
+        mine.row(p)[key] = total;
+      }
     }
     cluster.sync();                                      // peers keep their sums until here
-  } else if (bar.bad_wait) {
-    const int stop = min(st.kv_len, kp_end * kKeys * kGroups);
-    for (int k = key; k < stop; k += kThreads) mass[k] = NAN;
   }
 }
 
@@ -498,10 +620,12 @@ int decode_mass_warps() { return kDecodeWarps; }
 
 cudaError_t launch_prefill_mass(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                 const MassParams &p, cudaStream_t stream) {
-  const unsigned long long runs =
-      cdiv(cdiv(p.max_kv_len, kKeys * kGroups), p.pairs_per_cta);
-  const unsigned long long ctas =
-      static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads * runs * p.split;
+  // a cluster per (unit, pair and its mirror image), or a share of everything
+  // for each CTA that the GPU holds
+  const unsigned long long units = static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads;
+  const unsigned long long pairs = cdiv(p.max_kv_len, kKeys * kGroups);
+  const unsigned long long ctas = p.split > 1 ? units * ((pairs + 1) / 2) * p.split
+                                              : std::min<unsigned long long>(units * pairs, 2 * p.num_sms);
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
   cudaError_t err = set_smem_once<prefill_mass_kernel>(kSmemBytes);
@@ -510,7 +634,5 @@ cudaError_t launch_prefill_mass(const CUtensorMap &qmap, const CUtensorMap &kmap
                          static_cast<unsigned>(p.split), kThreads, kSmemBytes, stream, false, qmap,
                          kmap, p);
 }
-
-int prefill_mass_pair_keys() { return kKeys * kGroups; }
 
 }  // namespace sa

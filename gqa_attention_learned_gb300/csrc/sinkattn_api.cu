@@ -857,23 +857,6 @@ int mass_params(sa::MassParams &p, const void *q, const void *k_cache, const int
   return SINKATTN_OK;
 }
 
-// How the prefill form of attention mass spreads over CTAs: many query tiles
-// per key pair are shared by a cluster, few leave a CTA time for several key
-// pairs (as long as the CTAs still fill the GPU twice).
-void plan_prefill_mass(sa::MassParams &p) {
-  const int tiles = ceil_div(p.max_q_len, p.tile_tokens);
-  const int pairs = std::max(1, ceil_div(p.max_kv_len, sa::prefill_mass_pair_keys()));
-  p.split = p.pairs_per_cta = 1;
-  if (tiles >= 2 * kMassSteps) {
-    while (p.split < kMaxCluster && tiles / (2 * p.split) >= kMassSteps) p.split *= 2;
-  } else {
-    const long long all = static_cast<long long>(pairs) * p.num_seqs * p.num_kv_heads;
-    const long long fill = all / (4ll * std::max(device_sm_count(), 1));
-    p.pairs_per_cta = static_cast<int>(
-        std::max<long long>(1, std::min<long long>({kMassSteps / tiles, fill, pairs})));
-  }
-}
-
 bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + b_bytes && y < x + a_bytes;
@@ -941,7 +924,12 @@ int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_se
   p.cu_seqlens_q = cu_seqlens_q;
   p.max_q_len = max_q_len;
   p.tile_tokens = kPrefillTile / p.group;
-  plan_prefill_mass(p);
+  p.num_sms = device_sm_count();
+  if (p.num_sms == 0) return fail_msg("no CUDA device (SM count query failed)");
+  // many query tiles per key pair are shared by a cluster (as long as each CTA
+  // gets kMassSteps of them); with few, every CTA takes several key pairs
+  p.split = 1;
+  while (p.split < kMaxCluster && ceil_div(max_q_len, p.tile_tokens) >= 2 * p.split * kMassSteps) p.split *= 2;
   CUtensorMap qmap, kmap;
   if (!encode_map(&qmap, q, num_qo_heads, total_q, p.group, p.tile_tokens) ||
       !encode_map(&kmap, k_cache, static_cast<unsigned long long>(num_kv_heads) * kPageSize,
