@@ -212,7 +212,7 @@ struct MassParams {
   int max_pages_per_seq, num_pages;
   int num_chunks, pages_per_chunk;   // decode form: CTAs per (request, KV head)
   int tile_tokens;                   // prefill form: tokens per query tile = 128 / group
-  int split;                         // prefill form: CTAs that share the query tiles of a key pair
+  int split, split_log2;             // prefill form: CTAs that share the query tiles of a key pair
   int num_sms;
 };
 

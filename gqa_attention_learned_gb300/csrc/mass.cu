@@ -162,6 +162,7 @@ decode_mass_kernel(const MassParams p) {
 constexpr int kKeys = 128;                       // keys per tile: rows of S^T
 constexpr int kRows = 128;                       // query rows per streamed tile: columns of S^T
 constexpr int kKStages = 3, kQStages = 3;
+constexpr int kMaxSplit = 8;                     // CTAs per cluster (the portable limit)
 constexpr int kTileBytes = 128 * kHeadDim * 2;
 constexpr int kGroups = 2;                       // groups of four warps, one key tile each
 constexpr int kLoadWarp = 4 * kGroups, kMmaWarp = kLoadWarp + 1;   // one issuing warp per group
@@ -223,7 +224,13 @@ struct Walk {
   int seq, kvh, kp, pairs;            // current pair, pairs of its request
   int left;                           // pairs to go, this one included
   int q_start, q_len, kv_len, shift;  // shift: position of the first row's token
+  int tiles;                          // this CTA's query tiles of a pair that every row sees
 
+  // How many of `n` tiles (this rank's, then every split-th) are this CTA's.
+  __device__ __forceinline__ static int share(const MassParams &p, int n) {
+    const int rank = static_cast<int>(blockIdx.x) & (p.split - 1);    // split: a power of two
+    return n > rank ? (n - rank + p.split - 1) >> p.split_log2 : 0;
+  }
   // Loads request `seq`; pairs = 0 if there is nothing to add.  True if its
   // arguments are out of range.
   __device__ __forceinline__ bool request(const MassParams &p, int r) {
@@ -236,12 +243,13 @@ struct Walk {
     const bool bad = bad_request(p, kv_len) || q_start < 0 || q_len < 0 || q_end > p.total_q ||
                      q_len > p.max_q_len || kv_len < q_len;
     pairs = bad || q_len == 0 ? 0 : cdiv(kv_len, kKeys * kGroups);
+    tiles = share(p, cdiv(q_len, p.tile_tokens));
     return bad;
   }
   // Called by whole warps.
   __device__ void begin(const MassParams &p) {
     if (p.split > 1) {
-      const int item = static_cast<int>(blockIdx.x / p.split), units = p.num_seqs * p.num_kv_heads;
+      const int item = static_cast<int>(blockIdx.x) >> p.split_log2, units = p.num_seqs * p.num_kv_heads;
       const int unit = item % units;
       kp = item / units;
       kvh = unit % p.num_kv_heads;
@@ -297,17 +305,21 @@ struct Walk {
   }
   __device__ __forceinline__ Steps steps(const MassParams &p) const {
     Steps s;
-    const int rank = static_cast<int>(blockIdx.x % p.split);
+    const int rank = static_cast<int>(blockIdx.x) & (p.split - 1);
     s.key0 = kp * kKeys * kGroups;
-    s.i_start = max(0, s.key0 - shift);
-    const int tiles = cdiv(q_len - s.i_start, p.tile_tokens);
-    s.n = tiles > rank ? cdiv(tiles - rank, p.split) : 0;
-#pragma unroll
-    for (int w = 0; w < kGroups; ++w) {
-      const int first_key = s.key0 + w * kKeys;
-      // tile that holds the first token to see the group's keys
-      const int tile = (max(0, first_key - shift) - s.i_start) / p.tile_tokens;
-      s.skip[w] = first_key >= kv_len ? s.n : min(s.n, max(0, cdiv(tile - rank, p.split)));
+    const int key1 = s.key0 + kKeys;
+    if (key1 + kKeys <= shift) {                         // every row sees every key
+      s.i_start = 0;
+      s.n = tiles;
+      s.skip[0] = s.skip[1] = 0;
+    } else {
+      s.i_start = max(0, s.key0 - shift);
+      s.n = share(p, cdiv(q_len - s.i_start, p.tile_tokens));
+      // the second tile's first row is some tiles further on
+      s.skip[0] = 0;
+      s.skip[1] = key1 >= kv_len
+                      ? s.n
+                      : min(s.n, share(p, (max(0, key1 - shift) - s.i_start) / p.tile_tokens));
     }
     s.i_start += rank * p.tile_tokens;                   // of this CTA's first tile
     return s;
@@ -596,8 +608,12 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
         const int key = mine.kp * kKeys * kGroups + i;
         if (key >= mine.kv_len) continue;
         float total = mine.row(p)[key];
-        for (int r = 0; r < p.split; ++r)
-          total += *cluster.map_shared_rank(sums + item * kKeys * kGroups + i, r);
+        float part[kMaxSplit];                           // all on their way before the first is added
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r)
+          part[r] = r < p.split ? *cluster.map_shared_rank(sums + item * kKeys * kGroups + i, r) : 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r) total += part[r];
         mine.row(p)[key] = total;
       }
     }

@@ -114,7 +114,10 @@ constexpr int kPrefillKvTile = 128;   // keys per prefill K/V tile
 #endif
 constexpr int kWindowWaves = WD_WAVES;       // windowed decode: split up to this many CTA slots
 constexpr int kWindowMinPages = 16;   // and no finer than this
-constexpr int kMassSteps = 16;        // prefill mass: query tiles per CTA to aim for
+#ifndef MS
+#define MS 33
+#endif
+constexpr int kMassSteps = MS;        // prefill mass: query tiles per CTA to aim for
 constexpr int kMaxCluster = 8;        // portable cluster size
 #ifndef MD_PAGES
 #define MD_PAGES 8
@@ -928,8 +931,10 @@ int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_se
   if (p.num_sms == 0) return fail_msg("no CUDA device (SM count query failed)");
   // many query tiles per key pair are shared by a cluster (as long as each CTA
   // gets kMassSteps of them); with few, every CTA takes several key pairs
-  p.split = 1;
-  while (p.split < kMaxCluster && ceil_div(max_q_len, p.tile_tokens) >= 2 * p.split * kMassSteps) p.split *= 2;
+  while ((1 << p.split_log2) < kMaxCluster &&
+         ceil_div(max_q_len, p.tile_tokens) >= (2 << p.split_log2) * kMassSteps)
+    ++p.split_log2;
+  p.split = 1 << p.split_log2;
   CUtensorMap qmap, kmap;
   if (!encode_map(&qmap, q, num_qo_heads, total_q, p.group, p.tile_tokens) ||
       !encode_map(&kmap, k_cache, static_cast<unsigned long long>(num_kv_heads) * kPageSize,
