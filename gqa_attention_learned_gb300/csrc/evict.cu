@@ -6,17 +6,21 @@
 //
 // Two kernels, the second launched under the first's end.
 // select: a cluster of CTAs per (request, KV head), each with a contiguous
-//   share of the keys.  A radix select over the weights' order-preserving bits
-//   (11 + 11 + 10 bits; histograms in shared memory, joined in the first CTA's
-//   through distributed shared memory) gives the weight of the last key that
-//   stays and how many of its equals stay, lowest index first.  Two more
-//   passes count and write the kept indices in order, by ballots and prefix
-//   sums over warps and CTAs.  Weights after the first pass come from L1 / L2.
-// move: copies rows by that list; a CTA owns a 32-byte column (one sector) of
-//   a (request, KV head)'s K or V rows, or its mass.  In place is safe within
-//   a column because the r-th kept key has index >= r: a batch of rows is read
-//   whole before any of it is written, and a write to slot r can only hit rows
-//   of this batch or earlier ones.
+//   share of the keys, whose weights it reads once into registers (longer
+//   shares are read again, from L2, in each pass).  A radix select over
+//   the weights' order-preserving bits (11 + 11 + 10 bits; histograms in shared
+//   memory, joined in the first CTA's through distributed shared memory) gives
+//   the weight of the last key that stays and how many of its equals stay,
+//   lowest index first; ballots and prefix sums over warps and CTAs then place
+//   the kept indices in order.  A row is split only while all CTAs are
+//   resident at once: the passes are chains of cluster-wide steps, and a second
+//   wave of them costs more than longer shares (8 rows of 80k keys, 8 heads:
+//   53 us in two waves of eighths).
+// move: copies rows by that list, whole 128-byte rows, 64 KB of them in flight
+//   per CTA; a CTA owns a (request, KV head)'s K rows, V rows or mass.  In
+//   place is safe because the r-th kept key has index >= r: a batch of rows is
+//   read whole before any of it is written, and a write to slot r can only hit
+//   rows of this batch or earlier ones.
 // Bound by HBM: 4 bytes of mass per key, 512 bytes of K and V per kept one.
 
 #include "kernels.cuh"
@@ -36,11 +40,8 @@ constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxSplit = 8;             // CTAs per (request, KV head)
-constexpr int kKeysPerCta = 4096;        // keys per CTA to aim for
-constexpr int kMoveThreads = 256;
+constexpr int kKeysPerCta = 4096;        // keys per CTA at least, where a row has more than one
 constexpr int kMoveRows = 4;             // rows in flight per thread and batch
-constexpr int kColumns = 4;              // 32-byte columns of a row
-constexpr int kRoles = 2 * kColumns + 1; // K columns, V columns, mass
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
@@ -95,7 +96,9 @@ __device__ void find_bin(SelectSmem &s, int left, int &bin, int &rest) {
   rest = s.left;
 }
 
-__global__ void __launch_bounds__(kSelectThreads)
+// kHeld: weights a thread holds.
+template <int kHeld>
+__global__ void __launch_bounds__(kSelectThreads, kHeld == 8 ? 4 : 2)
 evict_select_kernel(const EvictParams p) {
   __shared__ SelectSmem s;
   cg::cluster_group cluster = cg::this_cluster();
@@ -114,8 +117,11 @@ evict_select_kernel(const EvictParams p) {
   if (!bad) {
     const int32_t *src = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
     const int32_t *dst = p.dst_page_table + static_cast<size_t>(b) * p.dst_max_pages;
-    for (int i = tid; i < npages; i += kSelectThreads) bad = bad || src[i] < 0 || src[i] >= p.num_pages;
-    for (int i = tid; i < dst_pages; i += kSelectThreads) bad = bad || dst[i] < 0 || dst[i] >= p.num_pages;
+    // (bitwise, so that the loads do not wait for one another)
+#pragma unroll 8
+    for (int i = tid; i < npages; i += kSelectThreads) bad |= (src[i] < 0) | (src[i] >= p.num_pages);
+#pragma unroll 4
+    for (int i = tid; i < dst_pages; i += kSelectThreads) bad |= (dst[i] < 0) | (dst[i] >= p.num_pages);
   }
   bad = __syncthreads_or(bad);                           // the same in every CTA of the cluster
   if (tid == 0 && rank == 0 && kvh == 0) p.new_kv_lens[b] = bad ? -1 : count;
@@ -130,11 +136,26 @@ evict_select_kernel(const EvictParams p) {
   const float *mass = p.mass + static_cast<size_t>(unit) * p.mass_stride;
   const int lo = p.first_tokens, hi = n - p.recent;       // the keys that compete
   const int want = p.budget - p.first_tokens - p.recent;  // how many of them stay
-  // this warp's keys: a contiguous run, whole multiples of 32
+  // this warp's keys: a contiguous run, whole multiples of 32, in blocks of
+  // kHeld keys per lane (one block unless the row is very long)
   const int run = cdiv(cdiv(n, split * kSelectWarps), 32) * 32;
   const long long from = static_cast<long long>(rank * kSelectWarps + warp) * run;
   const int begin = static_cast<int>(min(static_cast<long long>(n), from));
   const int end = static_cast<int>(min(static_cast<long long>(n), from + run));
+  constexpr int kBlock = 32 * kHeld;
+  uint32_t bits[kHeld];                                   // key i0 + 32 u + lane
+  auto load = [&](int i0) {
+    float v[kHeld];
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const int i = i0 + 32 * u + lane;
+      v[u] = i < end ? mass[i] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) bits[u] = order_bits(v[u]);
+  };
+  const bool held = run <= kBlock;
+  if (held) load(begin);
 
   // ---- the want-th largest weight, from the top bits down
   uint32_t prefix = 0;
@@ -147,28 +168,24 @@ evict_select_kernel(const EvictParams p) {
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
       for (int i = tid; i < kBins; i += kSelectThreads) s.hist[i] = 0;
       cluster.sync();
-      constexpr int kUnroll = 4;
-      for (int i0 = begin; i0 < end; i0 += 32 * kUnroll) {
-        float v[kUnroll];
+      for (int i0 = begin; i0 < end; i0 += kBlock) {
+        if (!held) load(i0);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kHeld; ++u) {
+          if (i0 + 32 * u >= end) break;
           const int i = i0 + 32 * u + lane;
-          v[u] = i < end ? mass[i] : 0.f;
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int i = i0 + 32 * u + lane;
-          const uint32_t bits = order_bits(v[u]);
-          if (i < end && i >= lo && i < hi && (bits & known) == prefix)
-            atomicAdd(&s.hist[(bits >> shift) & digits], 1);
+          if (i < end && i >= lo && i < hi && (bits[u] & known) == prefix)
+            atomicAdd(&s.hist[(bits[u] >> shift) & digits], 1);
         }
       }
       if (split > 1) {
         __syncthreads();
         if (rank != 0) {
           int *joined = cluster.map_shared_rank(s.hist, 0);
-          for (int i = tid; i < kBins; i += kSelectThreads)
-            if (s.hist[i]) atomicAdd(joined + i, s.hist[i]);
+          for (int i = tid; i < kBins; i += kSelectThreads) {
+            const int mine = s.hist[i];
+            if (mine) atomicAdd(joined + i, mine);
+          }
         }
         cluster.sync();
         if (rank == 0) {
@@ -197,24 +214,22 @@ evict_select_kernel(const EvictParams p) {
 
   // ---- how many stay for sure, and how many equal the threshold, per warp
   // and CTA
-  auto kind = [&](int i, bool &sure, bool &equal) {
-    sure = equal = false;
-    if (i >= end) return;
-    if (i < lo || i >= hi) {
-      sure = true;
-    } else if (want > 0) {
-      const uint32_t bits = order_bits(mass[i]);
-      sure = bits > prefix;
-      equal = bits == prefix;
-    }
+  auto kind = [&](int i, uint32_t w, bool &sure, bool &equal) {
+    const bool competes = i >= lo && i < hi;
+    sure = i < end && (!competes || (want > 0 && w > prefix));
+    equal = i < end && competes && want > 0 && w == prefix;
   };
   int n_sure = 0, n_equal = 0;
-#pragma unroll 4
-  for (int i = begin + lane; i < end; i += 32) {
-    bool sure, equal;
-    kind(i, sure, equal);
-    n_sure += sure;
-    n_equal += equal;
+  for (int i0 = begin; i0 < end; i0 += kBlock) {
+    if (!held) load(i0);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      if (i0 + 32 * u >= end) break;
+      bool sure, equal;
+      kind(i0 + 32 * u + lane, bits[u], sure, equal);
+      n_sure += sure;
+      n_equal += equal;
+    }
   }
   n_sure = warp_sum(n_sure);
   n_equal = warp_sum(n_equal);
@@ -249,103 +264,125 @@ evict_select_kernel(const EvictParams p) {
   // ---- the kept indices, in order
   int at = sure_before + min(equal_before, left);         // kept before this warp's keys
   const unsigned below = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    bool sure, equal;
-    kind(i0 + lane, sure, equal);
-    const unsigned eq = __ballot_sync(0xffffffffu, equal);
-    const bool keep = sure || (equal && equal_before + __popc(eq & below) < left);
-    const unsigned all = __ballot_sync(0xffffffffu, keep);
-    if (keep) kept[at + __popc(all & below)] = i0 + lane;
-    at += __popc(all);
-    equal_before += __popc(eq);
+  for (int i0 = begin; i0 < end; i0 += kBlock) {
+    if (!held) load(i0);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      if (i0 + 32 * u >= end) break;
+      const int i = i0 + 32 * u + lane;
+      bool sure, equal;
+      kind(i, bits[u], sure, equal);
+      const unsigned eq = __ballot_sync(0xffffffffu, equal);
+      const bool keep = sure || (equal && equal_before + __popc(eq & below) < left);
+      const unsigned all = __ballot_sync(0xffffffffu, keep);
+      if (keep) kept[at + __popc(all & below)] = i;
+      at += __popc(all);
+      equal_before += __popc(eq);
+    }
   }
   if (split > 1) cluster.sync();                          // peers have written this CTA's counts
 }
 
+template <int kMoveThreads>
 __global__ void __launch_bounds__(kMoveThreads)
 evict_move_kernel(const EvictParams p) {
-  const int role = static_cast<int>(blockIdx.x % kRoles), unit = static_cast<int>(blockIdx.x / kRoles);
+  const int units = p.batch * p.num_kv_heads;
+  const int role = static_cast<int>(blockIdx.x) / units;  // K rows, V rows, mass
+  const int unit = static_cast<int>(blockIdx.x) % units;
   const int kvh = unit % p.num_kv_heads, b = unit / p.num_kv_heads;
   grid_dependency_wait();
   const int count = p.new_kv_lens[b];
   if (count < 0) return;
   const int n = p.kv_lens[b];
   const int *kept = p.kept + static_cast<size_t>(unit) * p.budget;
-  if (role == 2 * kColumns) {
+  const int tid = static_cast<int>(threadIdx.x);
+  if (role == 2) {
     const float *src = p.mass + static_cast<size_t>(unit) * p.mass_stride;
     float *dst = p.dst_mass + static_cast<size_t>(unit) * p.dst_mass_stride;
     for (int base = 0; base < count; base += kMoveThreads * kMoveRows) {
       float v[kMoveRows];
 #pragma unroll
       for (int u = 0; u < kMoveRows; ++u) {
-        const int r = base + u * kMoveThreads + static_cast<int>(threadIdx.x);
+        const int r = base + u * kMoveThreads + tid;
         if (r < count) v[u] = src[kept[r]];
       }
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kMoveRows; ++u) {
-        const int r = base + u * kMoveThreads + static_cast<int>(threadIdx.x);
+        const int r = base + u * kMoveThreads + tid;
         if (r < count) dst[r] = v[u];
       }
     }
     __syncthreads();
     // evicted places start again from nothing
-    for (int i = count + threadIdx.x; i < min(n, p.dst_mass_stride); i += kMoveThreads) dst[i] = 0.f;
+    for (int i = count + tid; i < min(n, p.dst_mass_stride); i += kMoveThreads) dst[i] = 0.f;
     return;
   }
-  uint4 *cache = reinterpret_cast<uint4 *>(role < kColumns ? p.k_cache : p.v_cache);
+  uint4 *cache = reinterpret_cast<uint4 *>(role == 0 ? p.k_cache : p.v_cache);
   const int32_t *src_table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
   const int32_t *dst_table = p.dst_page_table + static_cast<size_t>(b) * p.dst_max_pages;
   const bool in_place = src_table == dst_table;
   constexpr int kPieces = kHeadDim * 2 / 16;              // 16-byte pieces of a row
-  const int piece = (role % kColumns) * (kPieces / kColumns);
+  constexpr int kAtOnce = kMoveThreads / kPieces, kBatch = kAtOnce * kMoveRows;
+  const int row = tid / kPieces, piece = tid % kPieces;
   auto address = [&](const int32_t *table, int key) {
     return cache + (static_cast<size_t>(table[key / kPageSize]) * p.num_kv_heads + kvh) * (kPageSize * kPieces) +
            (key % kPageSize) * kPieces + piece;
   };
-  for (int base = 0; base < count; base += kMoveThreads * kMoveRows) {
-    uint4 v[kMoveRows][2];
+  // the indices of a batch are read while the one before is on its way
+  int from[kMoveRows];
+  auto look_up = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int r = base + u * kAtOnce + row;
+      from[u] = r < count ? kept[r] : -1;
+      if (in_place && from[u] == r) from[u] = -1;         // where it belongs already
+    }
+  };
+  look_up(0);
+  for (int base = 0; base < count; base += kBatch) {
+    uint4 v[kMoveRows];
     bool moves[kMoveRows];
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
-      const int r = base + u * kMoveThreads + static_cast<int>(threadIdx.x);
-      const int from = r < count ? kept[r] : r;
-      moves[u] = r < count && !(in_place && from == r);   // a row may be where it belongs already
-      if (moves[u]) {
-        const uint4 *src = address(src_table, from);
-        v[u][0] = src[0];
-        v[u][1] = src[1];
-      }
+      moves[u] = from[u] >= 0;
+      if (moves[u]) v[u] = *address(src_table, from[u]);
     }
+    look_up(base + kBatch);
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int r = base + u * kMoveThreads + static_cast<int>(threadIdx.x);
-      if (moves[u]) {
-        uint4 *dst = address(dst_table, r);
-        dst[0] = v[u][0];
-        dst[1] = v[u][1];
-      }
-    }
+    for (int u = 0; u < kMoveRows; ++u)
+      if (moves[u]) *address(dst_table, base + u * kAtOnce + row) = v[u];
   }
 }
 
 }  // namespace
 
-cudaError_t launch_evict(EvictParams &p, cudaStream_t stream) {
+cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream) {
   const unsigned long long units = static_cast<unsigned long long>(p.batch) * p.num_kv_heads;
   if (units == 0) return cudaSuccess;
+  // CTAs per row: as many as are resident at once (two per SM), of
+  // kKeysPerCta keys at least
   p.split = 1;
-  while (p.split < kMaxSplit && p.max_kv_len > kKeysPerCta * p.split) p.split *= 2;
-  if (kRoles * units > 0x7fffffffull || p.split * units > 0x7fffffffull)
+  while (p.split < kMaxSplit && p.max_kv_len > kKeysPerCta * p.split &&
+         units * 2 * p.split <= 2ull * num_sms)
+    p.split *= 2;
+  if (3 * units > 0x7fffffffull || p.split * units > 0x7fffffffull)
     return cudaErrorInvalidConfiguration;
+  // rows of up to 4096 keys per CTA fit 8 registers per thread, which lets twice
+  // as many CTAs be resident
+  const bool small = p.max_kv_len <= 8 * kSelectThreads * p.split;
   const cudaError_t err =
-      launch_clusters(evict_select_kernel, static_cast<unsigned>(p.split * units),
-                      static_cast<unsigned>(p.split), kSelectThreads, 0, stream, true, p);
+      launch_clusters(small ? evict_select_kernel<8> : evict_select_kernel<32>,
+                      static_cast<unsigned>(p.split * units), static_cast<unsigned>(p.split),
+                      kSelectThreads, 0, stream, true, p);
   if (err != cudaSuccess) return err;
-  return launch_kernel(evict_move_kernel, static_cast<unsigned>(kRoles * units), kMoveThreads, 0,
-                       stream, true, p);
+  // bytes in flight: few rows of units get larger CTAs (64 requests x 8 heads,
+  // 1024 keys kept: 64 us in all with 512 threads, 74 with 1024; 8 x 8, 8192
+  // kept: 146 and 101)
+  if (2 * units >= 2ull * num_sms)
+    return launch_kernel(evict_move_kernel<512>, static_cast<unsigned>(3 * units), 512, 0, stream, true, p);
+  return launch_kernel(evict_move_kernel<1024>, static_cast<unsigned>(3 * units), 1024, 0, stream, true, p);
 }
 
 }  // namespace sa

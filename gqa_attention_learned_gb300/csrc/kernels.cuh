@@ -238,7 +238,7 @@ struct EvictParams {
   int split;                     // CTAs per (request, KV head) that select
 };
 
-cudaError_t launch_evict(EvictParams &p, cudaStream_t stream);   // sets p.split
+cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream);   // sets p.split
 
 // --------------------------------------------------------------- prologue
 struct PrologueParams {

@@ -189,6 +189,11 @@ static_assert(sizeof(Bars) <= 256, "barrier block");
 
 constexpr uint32_t kIdesc = umma_idesc_bf16(128, kHalf, false, false);
 
+// Bits below n (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 // Sum over 32 columns of 2^(s * scale + nl), s in r, nl in shared memory.
 template <int E = 0>
 __device__ __forceinline__ void add_chunk(uint32_t (&r)[32], const float4 *nl, uint64_t scale2,
@@ -333,8 +338,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap, const MassParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Walk walk;
-  walk.begin(p);
+  // in shared memory, a copy per warp (every lane writes the same values): it is
+  // looked at between key pairs, and registers are what the loops run out of
+  __shared__ Walk walks[kThreads / 32];
+  Walk &walk = walks[warp];
+  {
+    Walk first;
+    first.begin(p);
+    walk = first;
+  }
   const int step_tokens = p.split * p.tile_tokens;       // from one tile of this CTA to its next
   // requests whose arguments are out of range: NaN over their mass rows
   for (int r = static_cast<int>(blockIdx.x); r < p.num_seqs; r += static_cast<int>(gridDim.x)) {
@@ -385,7 +397,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     // ---------------------------------------- key tiles, query tiles and -lse
     bool ok = true;
     int kn = 0, qn = 0;                                  // tiles loaded so far
-    // this lane's rows of a query tile, and their lse (read two steps ahead:
+    // this lane's rows of a query tile, and their lse (read a step ahead:
     // the copies are asynchronous, so these loads are the latency that counts)
     constexpr int kMine = kRows / 32;
     int in_tile[kMine], row_at[kMine];
@@ -407,29 +419,38 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     };
     for (; ok && walk.left > 0; walk.next(p)) {
       const Steps st = walk.steps(p);
-      float lse[2][kMine];
+      float lse[1][kMine];
       load_lse(st, 0, lse[0]);
-      load_lse(st, 1, lse[1]);
       for (int j = 0; ok && j < st.n; ++j, ++qn) {
         for (int w = 0; w < kGroups; ++w) {
           if (j != 0 || st.skip[w] >= st.n) continue;
           // lanes 0..7 each own one 16-key page of the tile
           const int s = kn % kKStages;
           const int pg = (st.key0 + w * kKeys) / kPageSize + lane;
-          int id = -1;                                   // not in the pool: not copied
+          int id = -1;
+          bool bad = false;
           if (lane < kKeys / kPageSize && pg < cdiv(walk.kv_len, kPageSize)) {
             id = p.page_table[static_cast<size_t>(walk.seq) * p.max_pages_per_seq + pg];
-            if (id >= p.num_pages) id = -1;
+            bad = id < 0 || id >= p.num_pages;
           }
           if (kn >= kKStages && !__all_sync(0xffffffffu, mbar_wait(&bar.k_empty[s], ((kn / kKStages) + 1) & 1))) {
             ok = false;
             break;
           }
-          const unsigned mask = __ballot_sync(0xffffffffu, id >= 0);
+          // a page outside the pool is never read: its keys are NaN, and so
+          // become their scores and sums
+          for (unsigned m = __ballot_sync(0xffffffffu, bad); m; m &= m - 1) {
+            uint4 *to = reinterpret_cast<uint4 *>(sK(s) + (__ffs(m) - 1) * kPageSize * kHeadDim * 2);
+            for (int i = lane; i < kPageSize * kPieces; i += 32)
+              to[i] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          const unsigned mask = __ballot_sync(0xffffffffu, id >= 0 && !bad);
           if (lane == 0)
             mbar_arrive_expect_tx(&bar.k_full[s], __popc(mask) * kPageSize * kHeadDim * 2);
           __syncwarp();
-          if (id >= 0)
+          if (id >= 0 && !bad)
             tma_load_3d(sK(s) + lane * kPageSize * kHeadDim * 2, &kmap, &bar.k_full[s], 0,
                         walk.kvh * kPageSize, id);
           __syncwarp();
@@ -448,9 +469,8 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
         for (int u = 0; u < kMine; ++u) {
           const float l = lse[0][u];
           sL(s)[in_tile[u]] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-          lse[0][u] = lse[1][u];
         }
-        load_lse(st, j + 2, lse[1]);
+        load_lse(st, j + 1, lse[0]);
         mbar_arrive(&bar.q_full[s]);
       }
     }
@@ -514,11 +534,6 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
       const bool writes = key < walk.kv_len;
       float *sum_to = walk.row(p) + key;
       const float before = writes && p.split == 1 ? *sum_to : 0.f;
-      bool bad_page = false;                             // a key on a page outside the pool: NaN
-      if (writes) {
-        const int id = __ldg(p.page_table + static_cast<size_t>(walk.seq) * p.max_pages_per_seq + key / kPageSize);
-        bad_page = id < 0 || id >= p.num_pages;
-      }
       // tokens from this CTA's current tile to the first one that sees the key
       int ahead = key - walk.shift - st.i_start;
       int tokens_left = walk.q_len - st.i_start;
@@ -556,11 +571,11 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
               mbar_arrive(&bar.s_free[w][h]);
             }
             if (edge) {
+              const int c0 = h * kHalf + 32 * c;
+              const uint32_t see = first_bits(rows - c0) & ~first_bits(from - c0);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int col = h * kHalf + 32 * c + e;
-                if (col < from || col >= rows) x[e] = masked;
-              }
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1u)) x[e] = masked;
             }
             add_chunk(x, reinterpret_cast<const float4 *>(sL(s) + h * kHalf + 32 * c), scale2, acc0, acc1);
           }
@@ -572,7 +587,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
       float a, b, c, d;
       f2_unpack(acc0, a, b);
       f2_unpack(acc1, c, d);
-      const float sum = bad_page ? NAN : (a + b) + (c + d);
+      const float sum = (a + b) + (c + d);
       if (p.split > 1) sums[item * kKeys * kGroups + threadIdx.x] = sum;
       else if (writes) *sum_to = ok ? before + sum : NAN;
     }

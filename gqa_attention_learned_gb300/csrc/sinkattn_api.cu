@@ -1001,7 +1001,9 @@ int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *page_table, int 
   p.budget = budget;
   p.first_tokens = first_tokens;
   p.recent = recent;
-  return cuda_status(sa::launch_evict(p, static_cast<cudaStream_t>(stream)), "eviction launch");
+  const int sms = device_sm_count();
+  if (sms == 0) return fail_msg("no CUDA device (SM count query failed)");
+  return cuda_status(sa::launch_evict(p, sms, static_cast<cudaStream_t>(stream)), "eviction launch");
 }
 
 }  // extern "C"
