@@ -422,7 +422,7 @@ def _at(dev, stream):
     """Makes `dev` the current device and `stream` (if given) its current
     stream, so that what a call allocates or clears is ordered on the stream
     that it launches on (no-op when both already are)."""
-    if stream is None and (dev.index is None or dev.index == torch.cuda.current_device()):
+    if stream is None and dev.index == torch._C._cuda_getDevice():
         return _AS_IS
     stack = contextlib.ExitStack()
     stack.enter_context(_on(dev))
@@ -438,6 +438,8 @@ def _raw_stream(dev):
 
 def _size(v, name, least=0):
     """v as an int that fits the C ABI's (larger bounds mean no bound)."""
+    if type(v) is int and least <= v <= _INT_MAX:
+        return v
     v = int(v)
     if v < least:
         raise ValueError(f"{name} must be at least {least}, got {v}")
@@ -455,10 +457,11 @@ def _paged_args(dev, batch, page_table, kv_lens, k_cache, v_cache=None):
     _want(kv_lens, "kv_lens", torch.int32, 1, dev)
     if v_cache is not None:
         _want(v_cache, "v_cache", torch.bfloat16, 4, dev)
-        _shape(v_cache, "v_cache", k_cache.shape)
-    if batch is not None:
-        _shape(page_table, "page_table", (batch, page_table.shape[1]))
-        _shape(kv_lens, "kv_lens", (batch,))
+        if v_cache.shape != k_cache.shape:
+            raise ValueError(f"v_cache must be {list(k_cache.shape)}, got {list(v_cache.shape)}")
+    if page_table.shape[0] != batch or kv_lens.shape[0] != batch:
+        raise ValueError(f"page_table and kv_lens must have {batch} rows, got "
+                         f"{page_table.shape[0]} and {kv_lens.shape[0]}")
 
 
 def _rows_out(q, out, lse, want_lse):
@@ -495,30 +498,45 @@ def decode_window(q, k_cache, v_cache, page_table, kv_lens, sinks, scale, max_kv
     newest keys (its own included) and the `first_tokens` oldest.  Pages
     without a visible key are not looked up (their page_table entries may hold
     anything).  Returns (out [B, Hq, 64] bf16, lse [B, Hq] fp32 or None)."""
+    # the smallest calls last a few microseconds on the GPU: the checks below
+    # are kept to what an argument can get wrong, and the plan is made by the
+    # library alone when the caller brings the workspace
     dev = q.device
     _want(q, "q", torch.bfloat16, 3)
     batch, hq, d = q.shape
     _paged_args(dev, batch, page_table, kv_lens, k_cache, v_cache)
     _want(sinks, "sinks", torch.float32, 1, dev)
-    _shape(sinks, "sinks", (hq,))
     num_pages, hkv, page, d2 = k_cache.shape
-    if d2 != d:
-        raise ValueError("k_cache and q disagree in head_dim")
+    if d2 != d or sinks.shape[0] != hq:
+        raise ValueError("k_cache, sinks and q disagree in head_dim or heads")
     window, first = _size(window, "window", 1), _size(first_tokens, "first_tokens")
     max_kv_len, num_splits = _size(max_kv_len, "max_kv_len"), _size(num_splits, "num_splits")
     with _at(dev, stream):
-        out, lse = _rows_out(q, out, lse, want_lse)
-        splits, ws_bytes = _plan(decode_window_plan, batch, hq, hkv, max_kv_len, window, first,
-                                 num_splits, 0, d, page) if batch else (1, 0)
-        if workspace is None and ws_bytes:
-            # zero-filled once; the call leaves it ready for the next one
-            workspace = torch.zeros(ws_bytes, dtype=torch.uint8, device=dev)
-        ws_len = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check("sinkattn_decode_window", load().sinkattn_decode_window(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), page_table.shape[1],
-            _ptr(kv_lens), _ptr(sinks), float(scale), window, first, _ptr(out), _ptr(lse), batch,
-            hq, hkv, d, page, num_pages, max_kv_len, num_splits, _ptr(workspace), ws_len,
-            _launch_flags(programmatic), _raw_stream(q.device)))
+        if out is None and lse is None and want_lse:
+            out = torch.empty_like(q)
+            lse = torch.empty((batch, hq), dtype=torch.float32, device=dev)
+        else:
+            out, lse = _rows_out(q, out, lse, want_lse)
+        if workspace is None:
+            ws_ptr = ws_len = None
+            if batch:
+                _, ws_len = _plan(decode_window_plan, batch, hq, hkv, max_kv_len, window, first,
+                                  num_splits, 0, d, page)
+            if ws_len:
+                # zero-filled once; the call leaves it ready for the next one
+                workspace = torch.zeros(ws_len, dtype=torch.uint8, device=dev)
+                ws_ptr = workspace.data_ptr()
+        else:
+            _want(workspace, "workspace", workspace.dtype, None, dev)
+            ws_ptr, ws_len = workspace.data_ptr(), workspace.nbytes
+        status = load().sinkattn_decode_window(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+            page_table.shape[1], kv_lens.data_ptr(), sinks.data_ptr(), scale, window, first,
+            out.data_ptr(), None if lse is None else lse.data_ptr(), batch, hq, hkv, d, page,
+            num_pages, max_kv_len, num_splits, ws_ptr, ws_len or 0,
+            0 if programmatic is None else _launch_flags(programmatic), _raw_stream(dev))
+        if status:
+            _check("sinkattn_decode_window", status)
     return out, lse
 
 

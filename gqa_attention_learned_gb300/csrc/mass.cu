@@ -53,14 +53,8 @@ __device__ __forceinline__ void poison_row(const MassParams &p, float *row) {
 }
 
 // ------------------------------------------------------------------ decode
-#ifndef MD_WARPS
-#define MD_WARPS 8
-#endif
-#ifndef MD_CTAS
-#define MD_CTAS 4
-#endif
-constexpr int kDecodeWarps = MD_WARPS;
-constexpr int kDecodeCtas = MD_CTAS;
+constexpr int kDecodeWarps = 8;
+constexpr int kDecodeCtas = 4;                   // per SM
 constexpr int kPieces = kHeadDim * 2 / 16;       // 16-byte pieces of a row
 
 __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {

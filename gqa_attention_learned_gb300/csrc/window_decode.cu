@@ -19,8 +19,10 @@
 //     2t+8, 2t+9, pairs the keys by byte permutes, and n-tile i holds dims
 //     8n + i: each lane ends up with 16 consecutive dims of its row.
 // One CTA = one (request, KV head, block of 8 or 16 query heads, chunk of
-// visited pages), 4 warps taking pages round-robin with kAhead pages in
-// flight each.  Warps join through shared memory; chunks through the
+// visited pages), 4 warps taking pages round-robin with two pages in
+// flight each (with one, and 4 CTAs per SM: 10.4 us instead of 12.5 for 64
+// requests of window 128, 52.9 instead of 50.7 for 8 of window 16384; more pages
+// per warp, or more CTAs with fewer registers, are slower in both).  Warps join through shared memory; chunks through the
 // workspace, by the last CTA of a request to finish (as in plain decode).
 
 #include "kernels.cuh"
@@ -32,17 +34,9 @@
 namespace sa {
 namespace {
 
-#ifndef WD_CTAS
-#define WD_CTAS 3
-#endif
-#ifndef WD_AHEAD
-#define WD_AHEAD 2
-#endif
-#ifndef WD_NW
-#define WD_NW 4
-#endif
-constexpr int kNW = WD_NW;              // warps per CTA
-constexpr int kCtasPerSm = WD_CTAS;
+constexpr int kNW = 4;                       // warps per CTA
+constexpr int kCtasPerSm = 3;
+constexpr int kAhead = 2;                    // pages in flight per warp
 constexpr int kPieces = kHeadDim * 2 / 16;   // 16-byte pieces of a row
 constexpr int kStride = kHeadDim + 4;        // floats per joined row
 
@@ -78,7 +72,6 @@ struct Page {
 template <int NB>       // 8-head blocks per CTA: 1 or 2
 __global__ void __launch_bounds__(kNW * 32, kCtasPerSm)
 window_decode_kernel(const WindowDecodeParams p) {
-  constexpr int kAhead = WD_AHEAD;                            // pages in flight per warp
   constexpr int kRows = 8 * NB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
