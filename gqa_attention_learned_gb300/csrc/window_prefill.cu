@@ -18,9 +18,9 @@
 // first tokens, then boxes from the run's start on; tiles take 8 boxes = 128
 // slots each, so the two parts share tiles and nothing between them is
 // copied or looked up.  The last tile's MMAs cover its own boxes only.
-// Rows see at most two slot ranges, kept as 32-bit masks per 32 slots; a warp
-// skips the chunks of 32 slots that none of its rows sees (no load, no
-// exponentials) and masks only those on an edge.
+// Rows see at most two slot ranges.  Tiles that all rows of a warp see whole,
+// most of them in a long window, take a path without masks; on the others the
+// warp goes by chunks of 32 slots and skips those that none of its rows sees.
 // Warp roles, barriers and the softmax are those of plain prefill: warp 4
 // loads Q and K and issues S = Q K^T, warp 5 loads V and issues O += P V,
 // warps 0..3 run the online softmax, one thread per row, between them.
@@ -29,6 +29,8 @@
 
 namespace sa {
 namespace {
+
+using namespace window;
 
 constexpr int kBN = 128;                       // key slots per tile
 constexpr int kBoxes = kBN / 16;               // copied boxes per tile
@@ -44,7 +46,7 @@ constexpr int kOffQ = 0;
 constexpr int kOffK = kTileBytes;
 constexpr int kOffV = kOffK + kKStages * kTileBytes;
 constexpr int kOffBars = kOffV + kVStages * kTileBytes;
-constexpr int kSmemBytes = kOffBars + 256 + 1024;           // barriers + alignment slack
+constexpr int kSmemBytes = kOffBars + 2048 + 1024;          // barriers + alignment slack
 static_assert(kSmemBytes <= 113 * 1024, "two CTAs per SM");
 
 struct Bars {
@@ -58,10 +60,13 @@ struct Bars {
   uint64_t o_final;
   uint32_t tmem_base;
   int bad;
+  // what the softmax needs only on edge tiles and at its end: registers are
+  // what its loop runs out of
+  Tile tile;
+  int q_start, kvh;
+  RowSlots see[kBM];
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
-
-using namespace window;
+static_assert(sizeof(Bars) <= 2048, "barrier block");
 
 // Running softmax of a row: reference max m (base 2) that P and the
 // tensor-memory O are relative to, sum d.  m starts at the sink and moves only
@@ -103,25 +108,16 @@ __device__ __forceinline__ void rescale_o(uint32_t trow, float alpha) {
   tmem_st_wait();
 }
 
-// One 128-slot tile of the online softmax for this thread's row.  `chunks`:
-// 32-slot chunks of P that this tile's P V reads.  Returns false when a wait
-// timed out.
-__device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, int chunks,
-                                             const RowSlots &see, float sl2, uint32_t masked_raw,
+// One 128-slot tile of the online softmax for this thread's row.  `whole`:
+// every row of the warp sees all of it.  Returns false when a wait timed out.
+__device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, bool whole, float sl2,
                                              RowState &row) {
-  unsigned live = 0, edge = 0;         // warp-uniform bits per chunk
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t mask = see.mask(j * kBN + 32 * c);
-    live |= __any_sync(0xffffffffu, mask != 0u) ? 1u << c : 0u;
-    edge |= __any_sync(0xffffffffu, mask != 0xffffffffu) ? 1u << c : 0u;
-  }
   if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full, j & 1))) return false;
   tc_fence_after();
   const uint64_t scale2 = f2_pack(sl2, sl2);
   float alpha, s0, s1;
-  if (live == 15u) {
-    // a full tile: S is read once and held in registers
+  if (whole) {
+    // S is read once and held in registers
     uint32_t x[4][32];
 #pragma unroll
     for (int c = 0; c < 4; ++c) tmem_ld32(trow + kColS + 32 * c, x[c]);
@@ -130,11 +126,6 @@ __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, in
     for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
     tc_fence_before();
     mbar_arrive(&bar.s_free);
-    if (edge) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if ((edge >> c) & 1u) mask_chunk(x[c], see.mask(j * kBN + 32 * c), masked_raw);
-    }
     alpha = row.advance(fmaxf(fmax3(max_chunk(x[0], sl2), max_chunk(x[1], sl2), max_chunk(x[2], sl2)),
                               max_chunk(x[3], sl2)),
                         j == 0);
@@ -151,16 +142,25 @@ __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, in
     for (int c = 0; c < 4; ++c)
       tmem_st16(trow + kColP + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[c][0]));
   } else {
-    // an edge tile: its live chunks one by one, once for the max and once more
-    // for the weights (fewer exponentials, and few registers)
+    // an edge tile: the chunks that the warp sees one by one, once for the max
+    // and once more for the weights (fewer exponentials, and few registers)
+    const RowSlots see = bar.see[threadIdx.x];
+    // 32-slot chunks of P that this tile's P V reads
+    const int chunks = (min(kBoxes, bar.tile.n_boxes - j * kBoxes) + 1) / 2;
+    // Masked scores are replaced (by index, so NaN keys cannot leak) with the
+    // raw value whose scaled logit is -inf.
+    const uint32_t masked_raw = sl2 >= 0.f ? 0xff800000u : 0x7f800000u;
     uint32_t x[32];
     float mx = -INFINITY;
+    unsigned live = 0;                 // warp-uniform
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      if (!((live >> c) & 1u)) continue;
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t mask = see.mask(j * kBN + 32 * c);
+      if (!__any_sync(0xffffffffu, mask != 0u)) continue;
+      live |= 1u << c;
       tmem_ld32(trow + kColS + 32 * c, x);
       tmem_ld_wait32(x);
-      if ((edge >> c) & 1u) mask_chunk(x, see.mask(j * kBN + 32 * c), masked_raw);
+      mask_chunk(x, mask, masked_raw);
       mx = fmaxf(mx, max_chunk(x, sl2));
     }
     alpha = row.advance(mx, j == 0);
@@ -174,7 +174,7 @@ __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, in
       if ((live >> c) & 1u) {
         tmem_ld32(trow + kColS + 32 * c, x);
         tmem_ld_wait32(x);
-        if ((edge >> c) & 1u) mask_chunk(x, see.mask(j * kBN + 32 * c), masked_raw);
+        mask_chunk(x, see.mask(j * kBN + 32 * c), masked_raw);
         pack_chunk(x, scale2, negmu2, acc);
       } else {
 #pragma unroll
@@ -275,6 +275,9 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       mbar_init(&bar.pv_done, 1);
       mbar_init(&bar.o_final, 1);
       bar.bad = 0;
+      bar.tile = tile;
+      bar.q_start = req.q_start;
+      bar.kvh = kvh;
       fence_mbar_init();
       mbar_arrive_expect_tx(&bar.q_full, p.tile_tokens * p.group * kHeadDim * 2);
       // box {64, group, tile_tokens}: rows (token, head)
@@ -359,24 +362,30 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     // ------------------------------------------------------------- softmax
     const int r = threadIdx.x;                          // row = TMEM lane
     const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const int token = r / p.group;
-    const int head = kvh * p.group + (r - token * p.group);
-    // lanes past the rows repeat the last token
-    const RowSlots see = tile.row(p, tile.pos0 + min(token, tile.tokens - 1));
     const float sl2 = p.scale_log2;
-    // Masked scores are replaced (by index, so NaN keys cannot leak) with the
-    // raw value whose scaled logit is -inf.
-    const uint32_t masked_raw = sl2 >= 0.f ? 0xff800000u : 0x7f800000u;
-    RowState state{r < rows ? p.sinks[head] * kLog2e : -INFINITY, 1.f};   // started at the sink
+    RowState state;
+    int tiles, whole_b, whole_c;
+    {
+      const int token = r / p.group;
+      const int tile_rows = bar.tile.tokens * p.group;
+      tiles = warp * 32 < tile_rows ? cdiv(bar.tile.n_boxes, kBoxes) : 0;   // none without rows
+      // lanes past the rows repeat the last token
+      const RowSlots see = bar.tile.row(p, bar.tile.pos0 + min(token, bar.tile.tokens - 1));
+      bar.see[r] = see;
+      // tiles of the run that every row of the warp sees whole: [whole_b, whole_c)
+      whole_b = (__reduce_max_sync(0xffffffffu, see.b) + kBN - 1) / kBN;
+      whole_c = __reduce_min_sync(0xffffffffu, see.c) / kBN;
+      state.m = r < tile_rows ? p.sinks[bar.kvh * p.group + (r - token * p.group)] * kLog2e : -INFINITY;
+      state.d = 1.f;                                    // started at the sink
+    }
     bool ok = true;
-    const bool live = warp * 32 < live_threads;         // warp-uniform
-    for (int j = 0; live && j < n_tiles; ++j) {
-      const int chunks = (min(kBoxes, tile.n_boxes - j * kBoxes) + 1) / 2;
-      if (!softmax_tile(bar, trow, j, chunks, see, sl2, masked_raw, state)) {
+    for (int j = 0; j < tiles; ++j) {
+      if (!softmax_tile(bar, trow, j, j >= whole_b && j < whole_c, sl2, state)) {
         ok = false;
         break;
       }
     }
+    const bool live = tiles > 0;                        // warp-uniform
     uint32_t x[2][32];
     if (live) {
       if (__all_sync(0xffffffffu, mbar_wait(&bar.o_final, 0))) {
@@ -399,7 +408,9 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     if (!live) return;
     const bool failed = bar.bad != 0;
     const float m = state.m, d = state.d;
-    const size_t first_row = static_cast<size_t>(req.q_start + tile.i0) * p.num_qo_heads + kvh * p.group;
+    const int rows = bar.tile.tokens * p.group;
+    const size_t first_row =
+        static_cast<size_t>(bar.q_start + bar.tile.i0) * p.num_qo_heads + bar.kvh * p.group;
     auto row_index = [&](int i) -> long long {           // row i of the tile
       const int tok = i / p.group;
       return i < rows ? static_cast<long long>(first_row + static_cast<size_t>(tok) * p.num_qo_heads + (i - tok * p.group)) : -1;
