@@ -176,7 +176,8 @@ struct WindowPrefillParams {
   const float *sinks;            // [Hq]
   uint16_t *out;                 // bf16 [Tq][Hq][64]
   float *lse;                    // [Tq][Hq] or null
-  float scale_log2;              // not 0: masked scores are infinities that it keeps infinite
+  float scale_log2;              // |scale|, not 0: masked scores are -inf, and stay so
+  uint32_t negate_q;             // the scale's sign: 0 or the descriptor bit that negates Q
   int num_seqs, total_q, max_q_len, max_kv_len;
   int num_qo_heads, num_kv_heads, group;
   int max_pages_per_seq, num_pages;
@@ -189,6 +190,8 @@ struct WindowPrefillParams {
 cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                   const CUtensorMap &vmap, const WindowPrefillParams &p,
                                   cudaStream_t stream);
+
+uint32_t window_negate_q(bool negative);   // WindowPrefillParams::negate_q
 
 // Whether the keys of every query tile fit the kernel that holds them all at
 // once, and that kernel (one persistent CTA per SM).
@@ -206,7 +209,7 @@ struct MassParams {
   const int32_t *kv_lens;        // [n]
   const float *lse;              // [Tq][Hq]
   float *mass;                   // [n][Hkv][mass_stride]
-  float scale_log2;              // not 0, as above
+  float scale_log2;              // not 0: masked scores are infinities that it keeps infinite
   int num_seqs, total_q, max_q_len, max_kv_len, mass_stride;
   int num_qo_heads, num_kv_heads, group;
   int max_pages_per_seq, num_pages;

@@ -261,6 +261,9 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool a_mn_m
          | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// Instruction descriptor bit that negates the A operand (kind::f16).
+constexpr uint32_t kIdescNegateA = 1u << 13;
+
 // D[tmem] (+)= A[smem desc] * B[smem desc]
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                         uint32_t idesc, uint32_t accumulate) {

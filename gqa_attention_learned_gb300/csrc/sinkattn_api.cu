@@ -793,7 +793,8 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
   p.sinks = sinks;
   p.out = static_cast<uint16_t *>(out);
   p.lse = lse;
-  p.scale_log2 = masked_scale_log2(scale);
+  p.scale_log2 = masked_scale_log2(std::fabs(scale));
+  p.negate_q = sa::window_negate_q(scale < 0.f);
   p.num_seqs = num_seqs;
   p.total_q = total_q;
   p.max_q_len = max_q_len;

@@ -126,9 +126,8 @@ __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, bo
     for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
     tc_fence_before();
     mbar_arrive(&bar.s_free);
-    alpha = row.advance(fmaxf(fmax3(max_chunk(x[0], sl2), max_chunk(x[1], sl2), max_chunk(x[2], sl2)),
-                              max_chunk(x[3], sl2)),
-                        j == 0);
+    alpha = row.advance(
+        fmaxf(fmax3(max_chunk(x[0]), max_chunk(x[1]), max_chunk(x[2])), max_chunk(x[3])) * sl2, j == 0);
     const float mu = row.reference();
     const uint64_t negmu2 = f2_pack(-mu, -mu);
     uint64_t acc[4] = {0, 0, 0, 0};                    // (+0.f, +0.f)
@@ -147,9 +146,6 @@ __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, bo
     const RowSlots see = bar.see[threadIdx.x];
     // 32-slot chunks of P that this tile's P V reads
     const int chunks = (min(kBoxes, bar.tile.n_boxes - j * kBoxes) + 1) / 2;
-    // Masked scores are replaced (by index, so NaN keys cannot leak) with the
-    // raw value whose scaled logit is -inf.
-    const uint32_t masked_raw = sl2 >= 0.f ? 0xff800000u : 0x7f800000u;
     uint32_t x[32];
     float mx = -INFINITY;
     unsigned live = 0;                 // warp-uniform
@@ -160,8 +156,8 @@ __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, bo
       live |= 1u << c;
       tmem_ld32(trow + kColS + 32 * c, x);
       tmem_ld_wait32(x);
-      mask_chunk(x, mask, masked_raw);
-      mx = fmaxf(mx, max_chunk(x, sl2));
+      mask_chunk(x, mask);
+      mx = fmaxf(mx, max_chunk(x) * sl2);
     }
     alpha = row.advance(mx, j == 0);
     const float mu = row.reference();
@@ -174,7 +170,7 @@ __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, bo
       if ((live >> c) & 1u) {
         tmem_ld32(trow + kColS + 32 * c, x);
         tmem_ld_wait32(x);
-        mask_chunk(x, see.mask(j * kBN + 32 * c), masked_raw);
+        mask_chunk(x, see.mask(j * kBN + 32 * c));
         pack_chunk(x, scale2, negmu2, acc);
       } else {
 #pragma unroll
@@ -301,7 +297,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       if (lane == 0) {
         const uint64_t dk = umma_desc_sw128(smem_u32(sK(s)), 16, 1024);
         const uint32_t idesc =
-            umma_idesc_bf16(128, kBox * min(kBoxes, tile.n_boxes - j * kBoxes), false, false);
+            umma_idesc_bf16(128, kBox * min(kBoxes, tile.n_boxes - j * kBoxes), false, false) | p.negate_q;
 #pragma unroll
         for (int kk = 0; kk < kHeadDim / 16; ++kk)
           umma_ss(tmem + kColS, dq + 2 * kk, dk + 2 * kk, idesc, kk > 0);   // +32 bytes per k-step
@@ -441,6 +437,8 @@ cudaError_t launch_variant(const CUtensorMap &qmap, const CUtensorMap &kmap,
 }
 
 }  // namespace
+
+uint32_t window_negate_q(bool negative) { return negative ? kIdescNegateA : 0u; }
 
 cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                   const CUtensorMap &vmap, const WindowPrefillParams &p,

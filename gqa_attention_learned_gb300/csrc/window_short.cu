@@ -232,7 +232,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       if (lane == 0) {
         const uint64_t dq = umma_desc_sw128(smem_u32(sQ(n)), 16, 1024);
         const uint64_t dk = umma_desc_sw128(smem_u32(sK(n)), 16, 1024);
-        const uint32_t idesc = umma_idesc_bf16(128, kBox * tile.n_boxes, false, false);
+        const uint32_t idesc = umma_idesc_bf16(128, kBox * tile.n_boxes, false, false) | p.negate_q;
 #pragma unroll
         for (int kk = 0; kk < kHeadDim / 16; ++kk)
           umma_ss(tS, dq + 2 * kk, dk + 2 * kk, idesc, kk > 0);   // +32 bytes per k-step
@@ -264,8 +264,6 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     const int row_skip = p.num_qo_heads - p.group;       // from a token's last row to the next one's first
     const float sl2 = p.scale_log2;
     const uint64_t scale2 = f2_pack(sl2, sl2);
-    const bool largest = sl2 >= 0.f;                     // the largest raw score is the largest scaled one
-    const uint32_t masked_raw = largest ? 0xff800000u : 0x7f800000u;
     for (int n = slot, k = 0;; n += kSlots, ++k) {
       if (!wait(&bar.info[slot], k)) break;              // the geometry
       const Work &w = bar.work[n % kNV];
@@ -307,11 +305,15 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
         for (int i = 2 * c; i < 2 * c + 2; ++i) {
           if (!((live >> i) & 1u)) continue;
-          if (!((full >> i) & 1u)) mask_piece(x[i & 3], see.mask(16 * i), masked_raw);
-          mx = fmaxf(mx, max_piece(x[i & 3], largest) * sl2);
+          if (!((full >> i) & 1u)) {                     // an edge: masked, for pass 2 too
+            mask_piece(x[i & 3], see.mask(16 * i));
+            tmem_st16(trow + 16 * i, x[i & 3]);
+          }
+          mx = fmaxf(mx, max_piece(x[i & 3]));
         }
       }
-      const float m = fmaxf(sink, mx);
+      tmem_st_wait();
+      const float m = fmaxf(sink, mx * sl2);
       const float mu = m == -INFINITY ? 0.f : m;
       const uint64_t negmu2 = f2_pack(-mu, -mu);
       uint64_t acc = 0, acc1 = 0;                        // (+0.f, +0.f)
@@ -325,7 +327,6 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
         for (int i = 2 * c; i < 2 * c + 2; ++i) {
           if ((live >> i) & 1u) {
-            if (!((full >> i) & 1u)) mask_piece(x[i & 3], see.mask(16 * i), masked_raw);
             pack_piece(x[i & 3], scale2, negmu2, acc, acc1);
           } else {
 #pragma unroll

@@ -49,25 +49,21 @@ struct RowSlots {
   }
 };
 
-// Masks one chunk of raw scores, and their maximum in base 2.
-__device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t mask, uint32_t masked_raw) {
+// Masked scores are replaced (by index, so NaN keys cannot leak).  The scale is
+// positive -- a negative one negates Q in the product -- so -inf it is.
+constexpr uint32_t kMasked = 0xff800000u;
+
+// Masks one chunk of raw scores; their maximum.
+__device__ __forceinline__ void mask_chunk(uint32_t (&x)[32], uint32_t mask) {
 #pragma unroll
   for (int e = 0; e < 32; ++e)
-    if (!((mask >> e) & 1u)) x[e] = masked_raw;
+    if (!((mask >> e) & 1u)) x[e] = kMasked;
 }
-__device__ __forceinline__ float max_chunk(const uint32_t (&x)[32], float sl2) {
-  float r;
-  if (sl2 >= 0.f) {
-    r = __uint_as_float(x[0]);
+__device__ __forceinline__ float max_chunk(const uint32_t (&x)[32]) {
+  float r = __uint_as_float(x[0]);
 #pragma unroll
-    for (int e = 1; e < 31; e += 2) r = fmax3(r, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-    r = fmaxf(r, __uint_as_float(x[31]));
-  } else {
-    r = INFINITY;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) r = fminf(r, __uint_as_float(x[e]));
-  }
-  return r * sl2;
+  for (int e = 1; e < 31; e += 2) r = fmax3(r, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+  return fmaxf(r, __uint_as_float(x[31]));
 }
 
 // Bits below n (n <= 0: none).
@@ -83,22 +79,16 @@ __device__ __forceinline__ void piece_bits(const RowSlots &r, uint32_t &live, ui
 // 16 raw scores: masked by the low bits of `mask`, their maximum, and their
 // weights P = 2^(s * sl2 - mu) as bf16 pairs in x[0..7], summed into two
 // accumulators.
-__device__ __forceinline__ void mask_piece(uint32_t (&x)[16], uint32_t mask, uint32_t masked_raw) {
+__device__ __forceinline__ void mask_piece(uint32_t (&x)[16], uint32_t mask) {
 #pragma unroll
   for (int e = 0; e < 16; ++e)
-    if (!((mask >> e) & 1u)) x[e] = masked_raw;
+    if (!((mask >> e) & 1u)) x[e] = kMasked;
 }
-__device__ __forceinline__ float max_piece(const uint32_t (&x)[16], bool largest) {
+__device__ __forceinline__ float max_piece(const uint32_t (&x)[16]) {
   auto f = [&](int e) { return __uint_as_float(x[e]); };
-  if (largest) {
-    const float a = fmax3(f(0), f(1), f(2)), b = fmax3(f(3), f(4), f(5)), c = fmax3(f(6), f(7), f(8));
-    const float d = fmax3(f(9), f(10), f(11)), e = fmax3(f(12), f(13), f(14));
-    return fmaxf(fmax3(a, b, c), fmax3(d, e, f(15)));
-  }
-  float r = f(0);
-#pragma unroll
-  for (int e = 1; e < 16; ++e) r = fminf(r, f(e));
-  return r;
+  const float a = fmax3(f(0), f(1), f(2)), b = fmax3(f(3), f(4), f(5)), c = fmax3(f(6), f(7), f(8));
+  const float d = fmax3(f(9), f(10), f(11)), e = fmax3(f(12), f(13), f(14));
+  return fmaxf(fmax3(a, b, c), fmax3(d, e, f(15)));
 }
 template <int I = 0>
 __device__ __forceinline__ void pack_piece(uint32_t (&x)[16], uint64_t scale2, uint64_t negmu2,
