@@ -39,7 +39,7 @@ constexpr uint32_t kTmemCols = 512;
 template <int S, int B, int NK, int NV>
 struct Shape {
   static constexpr int kKStages = NK, kVStages = NV;
-  static constexpr int kSlots = S, kBoxes = B, kChunks = (B + 1) / 2;
+  static constexpr int kSlots = S, kBoxes = B;
   static constexpr int kKBytes = B * kBoxBytes;
   static constexpr int kKStageBytes = kQBytes + kKBytes;
   static constexpr int kMmaWarp = 4 * S, kLoadWarp = 5 * S;
@@ -277,40 +277,49 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       // lanes past the rows repeat the last token
       const RowSlots see = tile.row(p, tile.pos0 + min(token, tile.tokens - 1));
       const float sink = r < rows ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
-      uint32_t live, full;                               // per piece of 16 slots, warp-uniform
-      piece_bits(see, live, full);
-      live = __reduce_or_sync(0xffffffffu, live);
-      full = __reduce_and_sync(0xffffffffu, full);
+      // Pieces of 16 slots.  Away from a request's ends only the first pieces of
+      // each part and the last two can hold slots that some row does not see;
+      // elsewhere all are taken as such edges.
+      const int pieces = tile.n_boxes;
+      int lead = tile.first_boxes + 2, edges = lead + 2;
+      const uint32_t inner = low_bits(pieces - 2) & ~low_bits(lead);
+      if (edges > pieces || (__reduce_and_sync(0xffffffffu, full_pieces(see)) & inner) != inner)
+        lead = edges = pieces;
       if (!wait(&bar.s_full[slot], k)) break;
       tc_fence_after();
-      // pass 1: the row's max; two pieces at a time, the next two on their way
-      // while these are looked at (all are read, whatever the tile needs: no
-      // branch decides about a load in flight)
+      // four pieces at a time, straight-line code: `at(u)` is the u-th piece
       uint32_t x[4][16];
-      auto fetch = [&](int c) {
-        tmem_ld16(trow + 32 * c, x[2 * (c & 1)]);
-        tmem_ld16(trow + 32 * c + 16, x[2 * (c & 1) + 1]);
-      };
-      auto arrived = [&](int c) {
+      auto fetch = [&](auto at) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) tmem_ld16(trow + 16 * at(u), x[u]);
         tmem_ld_wait();
-        reg_tie16(x[2 * (c & 1)]);
-        reg_tie16(x[2 * (c & 1) + 1]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) reg_tie16(x[u]);
       };
+      auto largest = [&]() {
+        return fmaxf(fmax3(max_piece(x[0]), max_piece(x[1]), max_piece(x[2])), max_piece(x[3]));
+      };
+      // pass 1: the row's max; edges are masked for both passes.  (A piece may
+      // come twice at the end of a run of pieces, which changes nothing.)
       float mx = -INFINITY;
-      fetch(0);
+#pragma unroll 1
+      for (int e0 = 0; e0 < edges; e0 += 4) {
+        auto at = [&](int u) {
+          const int e = min(e0 + u, edges - 1);
+          return e < lead ? e : pieces - edges + e;
+        };
+        fetch(at);
 #pragma unroll
-      for (int c = 0; c < Sh::kChunks; ++c) {
-        arrived(c);
-        if (c + 1 < Sh::kChunks) fetch(c + 1);
-#pragma unroll
-        for (int i = 2 * c; i < 2 * c + 2; ++i) {
-          if (!((live >> i) & 1u)) continue;
-          if (!((full >> i) & 1u)) {                     // an edge: masked, for pass 2 too
-            mask_piece(x[i & 3], see.mask(16 * i));
-            tmem_st16(trow + 16 * i, x[i & 3]);
-          }
-          mx = fmaxf(mx, max_piece(x[i & 3]));
+        for (int u = 0; u < 4; ++u) {
+          mask_piece(x[u], see.mask(16 * at(u)));
+          tmem_st16(trow + 16 * at(u), x[u]);
         }
+        mx = fmaxf(mx, largest());
+      }
+#pragma unroll 1
+      for (int i0 = lead; i0 < pieces - 2; i0 += 4) {
+        fetch([&](int u) { return min(i0 + u, pieces - 3); });
+        mx = fmaxf(mx, largest());
       }
       tmem_st_wait();
       const float m = fmaxf(sink, mx * sl2);
@@ -319,20 +328,23 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       uint64_t acc = 0, acc1 = 0;                        // (+0.f, +0.f)
       // pass 2: P over S: piece i goes to columns 8 i .., whose scores (piece
       // i / 2) are in registers or used up by then
-      fetch(0);
+      int i0 = 0;
+#pragma unroll 1
+      for (; i0 + 4 <= pieces; i0 += 4) {
+        fetch([&](int u) { return i0 + u; });
 #pragma unroll
-      for (int c = 0; c < Sh::kChunks; ++c) {
-        arrived(c);
-        if (c + 1 < Sh::kChunks) fetch(c + 1);
+        for (int u = 0; u < 4; ++u) {
+          pack_piece(x[u], scale2, negmu2, acc, acc1);
+          tmem_st8(trow + 8 * (i0 + u), x[u]);
+        }
+      }
+      if (i0 < pieces) {
+        fetch([&](int u) { return min(i0 + u, pieces - 1); });
 #pragma unroll
-        for (int i = 2 * c; i < 2 * c + 2; ++i) {
-          if ((live >> i) & 1u) {
-            pack_piece(x[i & 3], scale2, negmu2, acc, acc1);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[i & 3][e] = 0u;
-          }
-          tmem_st8(trow + 8 * i, x[i & 3]);
+        for (int u = 0; u < 3; ++u) {
+          if (i0 + u >= pieces) continue;
+          pack_piece(x[u], scale2, negmu2, acc, acc1);
+          tmem_st8(trow + 8 * (i0 + u), x[u]);
         }
       }
       float s0, s1;

@@ -69,11 +69,9 @@ __device__ __forceinline__ float max_chunk(const uint32_t (&x)[32]) {
 // Bits below n (n <= 0: none).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// The 16-slot pieces that a row sees: bit i of `live` if it sees a slot of
-// piece i, bit i of `full` if it sees all of it.
-__device__ __forceinline__ void piece_bits(const RowSlots &r, uint32_t &live, uint32_t &full) {
-  live = low_bits((r.a + 15) / 16) | (low_bits((r.c + 15) / 16) & ~low_bits(r.b / 16));
-  full = low_bits(r.a / 16) | (low_bits(r.c / 16) & ~low_bits((r.b + 15) / 16));
+// The 16-slot pieces that a row sees whole, as bits.
+__device__ __forceinline__ uint32_t full_pieces(const RowSlots &r) {
+  return low_bits(r.a / 16) | (low_bits(r.c / 16) & ~low_bits((r.b + 15) / 16));
 }
 
 // 16 raw scores: masked by the low bits of `mask`, their maximum, and their
