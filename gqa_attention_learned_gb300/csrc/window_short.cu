@@ -25,6 +25,7 @@
 #include "window_tile.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace sa {
 namespace {
@@ -277,25 +278,28 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       // lanes past the rows repeat the last token
       const RowSlots see = tile.row(p, tile.pos0 + min(token, tile.tokens - 1));
       const float sink = r < rows ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
-      // Pieces of 16 slots.  Away from a request's ends only the first pieces of
-      // each part and the last two can hold slots that some row does not see;
-      // elsewhere all are taken as such edges.
+      // Pieces of 16 slots.  Away from a request's ends only the first one or two
+      // of the run, the last one or two, and the first tokens' can hold slots
+      // that some row does not see; elsewhere all are taken as such edges.
       const int pieces = tile.n_boxes;
-      int lead = tile.first_boxes + 2, edges = lead + 2;
-      const uint32_t inner = low_bits(pieces - 2) & ~low_bits(lead);
-      if (edges > pieces || (__reduce_and_sync(0xffffffffu, full_pieces(see)) & inner) != inner)
-        lead = edges = pieces;
+      const uint32_t full = __reduce_and_sync(0xffffffffu, full_pieces(see));
+      int lead = tile.first_boxes + ((full >> (tile.first_boxes + 1)) & 1u ? 1 : 2);
+      int edges = lead + ((full >> max(pieces - 2, 0)) & 1u ? 1 : 2);
+      const uint32_t inner = low_bits(pieces - (edges - lead)) & ~low_bits(lead);
+      if (edges > pieces || (full & inner) != inner) lead = edges = pieces;
       if (!wait(&bar.s_full[slot], k)) break;
       tc_fence_after();
-      // four pieces at a time, straight-line code: `at(u)` is the u-th piece
+      // several pieces at a time, straight-line code: `at(u)` is the u-th piece
       uint32_t x[4][16];
-      auto fetch = [&](auto at) {
+      auto fetch = [&](auto count, auto at) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) tmem_ld16(trow + 16 * at(u), x[u]);
+        for (int u = 0; u < count.value; ++u) tmem_ld16(trow + 16 * at(u), x[u]);
         tmem_ld_wait();
 #pragma unroll
-        for (int u = 0; u < 4; ++u) reg_tie16(x[u]);
+        for (int u = 0; u < count.value; ++u) reg_tie16(x[u]);
       };
+      const std::integral_constant<int, 2> two;
+      const std::integral_constant<int, 4> four;
       auto largest = [&]() {
         return fmaxf(fmax3(max_piece(x[0]), max_piece(x[1]), max_piece(x[2])), max_piece(x[3]));
       };
@@ -303,22 +307,23 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       // come twice at the end of a run of pieces, which changes nothing.)
       float mx = -INFINITY;
 #pragma unroll 1
-      for (int e0 = 0; e0 < edges; e0 += 4) {
+      for (int e0 = 0; e0 < edges; e0 += 2) {
         auto at = [&](int u) {
           const int e = min(e0 + u, edges - 1);
           return e < lead ? e : pieces - edges + e;
         };
-        fetch(at);
+        fetch(two, at);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 2; ++u) {
           mask_piece(x[u], see.mask(16 * at(u)));
           tmem_st16(trow + 16 * at(u), x[u]);
+          mx = fmaxf(mx, max_piece(x[u]));
         }
-        mx = fmaxf(mx, largest());
       }
+      const int inner_end = pieces - (edges - lead);
 #pragma unroll 1
-      for (int i0 = lead; i0 < pieces - 2; i0 += 4) {
-        fetch([&](int u) { return min(i0 + u, pieces - 3); });
+      for (int i0 = lead; i0 < inner_end; i0 += 4) {
+        fetch(four, [&](int u) { return min(i0 + u, inner_end - 1); });
         mx = fmaxf(mx, largest());
       }
       tmem_st_wait();
@@ -331,7 +336,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       int i0 = 0;
 #pragma unroll 1
       for (; i0 + 4 <= pieces; i0 += 4) {
-        fetch([&](int u) { return i0 + u; });
+        fetch(four, [&](int u) { return i0 + u; });
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           pack_piece(x[u], scale2, negmu2, acc, acc1);
@@ -339,7 +344,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
         }
       }
       if (i0 < pieces) {
-        fetch([&](int u) { return min(i0 + u, pieces - 1); });
+        fetch(four, [&](int u) { return min(i0 + u, pieces - 1); });
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
           if (i0 + u >= pieces) continue;
