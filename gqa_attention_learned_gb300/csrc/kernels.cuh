@@ -215,9 +215,12 @@ struct MassParams {
   int max_pages_per_seq, num_pages;
   int num_chunks, pages_per_chunk;   // decode form: CTAs per (request, KV head)
   int tile_tokens;                   // prefill form: tokens per query tile = 128 / group
-  int split, split_log2;             // prefill form: CTAs that share the query tiles of a key pair
+  int mirror;                        // prefill form: many query tiles per key pair
+  int split, split_log2;             // then: CTAs that share them (a power of two), else 1
   int num_sms;
 };
+
+int prefill_mass_pair_keys();        // keys that a CTA holds at a time
 
 
 int decode_mass_warps();         // pages a CTA of the decode form works on at a time

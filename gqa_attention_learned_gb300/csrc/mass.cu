@@ -215,10 +215,10 @@ struct Steps {
 
 // What a CTA works on: key pairs of (request, KV head) units.  Every role walks
 // the same sequence.
-//   split > 1   : pair c of the unit and its mirror image n - 1 - c, which
+//   mirror      : pair c of the unit and its mirror image n - 1 - c, which
 //                 together are seen by about as many rows whatever c is; the
-//                 cluster's CTAs share the rows.
-//   split == 1  : an equal share of all pairs of the launch, in order.
+//                 CTAs of a cluster share the rows.  For many rows per key.
+//   not mirror  : an equal share of all pairs of the launch, in order.  For few.
 struct Walk {
   int seq, kvh, kp, pairs;            // current pair, pairs of its request
   int left;                           // pairs to go, this one included
@@ -247,12 +247,30 @@ struct Walk {
   }
   // Called by whole warps.
   __device__ void begin(const MassParams &p) {
-    if (p.split > 1) {
-      const int item = static_cast<int>(blockIdx.x) >> p.split_log2, units = p.num_seqs * p.num_kv_heads;
-      const int unit = item % units;
-      kp = item / units;
-      kvh = unit % p.num_kv_heads;
-      request(p, unit / p.num_kv_heads);
+    if (p.mirror) {
+      // heaviest requests first (as many as a warp can rank; the others after
+      // them in order), so that the last wave holds the light ones
+      const int item = static_cast<int>(blockIdx.x) >> p.split_log2;
+      const int per_seq = (cdiv(p.max_kv_len, kKeys * kGroups) + 1) / 2 * p.num_kv_heads;
+      const int place = item / per_seq, rest = item % per_seq;
+      kvh = rest % p.num_kv_heads;
+      kp = rest / p.num_kv_heads;
+      int r = place;
+      if (place < 32) {
+        const int lane = threadIdx.x & 31;
+        float weight = -1.f;                             // no request: after all that exist
+        if (lane < p.num_seqs)
+          weight = static_cast<float>(max(0, p.cu_seqlens_q[lane + 1] - p.cu_seqlens_q[lane])) *
+                   static_cast<float>(max(0, p.kv_lens[lane]));
+        int rank = 0;
+#pragma unroll
+        for (int l = 0; l < 32; ++l) {
+          const float other = __shfl_sync(0xffffffffu, weight, l);
+          rank += other > weight || (other == weight && l < lane);
+        }
+        r = __ffs(__ballot_sync(0xffffffffu, rank == place)) - 1;
+      }
+      request(p, r);
       left = kp >= (pairs + 1) / 2 ? 0 : kp == pairs - 1 - kp ? 1 : 2;
       return;
     }
@@ -291,7 +309,7 @@ struct Walk {
   }
   __device__ __forceinline__ void next(const MassParams &p) {
     if (--left == 0) return;
-    if (p.split > 1) {
+    if (p.mirror) {
       kp = pairs - 1 - kp;
     } else if (++kp == pairs) {
       kp = 0;
@@ -527,7 +545,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
       const int key = st.key0 + w * kKeys + row;
       const bool writes = key < walk.kv_len;
       float *sum_to = walk.row(p) + key;
-      const float before = writes && p.split == 1 ? *sum_to : 0.f;
+      const float before = writes && !p.mirror ? *sum_to : 0.f;
       // tokens from this CTA's current tile to the first one that sees the key
       int ahead = key - walk.shift - st.i_start;
       int tokens_left = walk.q_len - st.i_start;
@@ -582,13 +600,13 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
       f2_unpack(acc0, a, b);
       f2_unpack(acc1, c, d);
       const float sum = (a + b) + (c + d);
-      if (p.split > 1) sums[item * kKeys * kGroups + threadIdx.x] = sum;
+      if (p.mirror) sums[item * kKeys * kGroups + threadIdx.x] = sum;
       else if (writes) *sum_to = ok ? before + sum : NAN;
     }
     if (!ok) {
       // a wait ran out: none of the sums to come can be made
       atomicOr(&bar.bad_wait, 1);
-      for (; p.split == 1 && walk.left > 0; walk.next(p)) {
+      for (; !p.mirror && walk.left > 0; walk.next(p)) {
         const int key = walk.kp * kKeys * kGroups + w * kKeys + row;
         if (key < walk.kv_len) walk.row(p)[key] = NAN;
       }
@@ -600,7 +618,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (p.split > 1) {
+  if (p.mirror) {
     // the shares of the cluster's CTAs, in rank order; a wait that ran out
     // gives NaN
     namespace cg = cooperative_groups;
@@ -643,13 +661,15 @@ cudaError_t launch_decode_mass(const MassParams &p, cudaStream_t stream) {
 
 int decode_mass_warps() { return kDecodeWarps; }
 
+int prefill_mass_pair_keys() { return kKeys * kGroups; }
+
 cudaError_t launch_prefill_mass(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                 const MassParams &p, cudaStream_t stream) {
   // a cluster per (unit, pair and its mirror image), or a share of everything
   // for each CTA that the GPU holds
   const unsigned long long units = static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads;
   const unsigned long long pairs = cdiv(p.max_kv_len, kKeys * kGroups);
-  const unsigned long long ctas = p.split > 1 ? units * ((pairs + 1) / 2) * p.split
+  const unsigned long long ctas = p.mirror ? units * ((pairs + 1) / 2) * p.split
                                               : std::min<unsigned long long>(units * pairs, 2 * p.num_sms);
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;

@@ -112,7 +112,7 @@ constexpr int kPrefillKvTile = 128;   // keys per prefill K/V tile
 constexpr int kWindowWaves = 1;       // windowed decode: split up to this many times the CTA slots (2:
                                       // 59.7 us instead of 50.7 for 8 requests of window 16384)
 constexpr int kWindowMinPages = 16;   // and no finer than this
-constexpr int kMassSteps = 33;        // prefill mass: query tiles per key pair and CTA, at least
+constexpr int kMassTiles = 16;        // prefill mass: query tiles that count as many
 constexpr int kMaxCluster = 8;        // portable cluster size
 constexpr int kMassPagesPerWarp = 8;  // decode mass: pages a warp takes, one CTA's share
 
@@ -922,11 +922,19 @@ int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_se
   p.tile_tokens = kPrefillTile / p.group;
   p.num_sms = device_sm_count();
   if (p.num_sms == 0) return fail_msg("no CUDA device (SM count query failed)");
-  // many query tiles per key pair are shared by a cluster (as long as each CTA
-  // gets kMassSteps of them); with few, every CTA takes several key pairs
-  while ((1 << p.split_log2) < kMaxCluster &&
-         ceil_div(max_q_len, p.tile_tokens) >= (2 << p.split_log2) * kMassSteps)
-    ++p.split_log2;
+  // Many query tiles per key pair: a pair and its mirror image per cluster,
+  // with as many CTAs to share them as fill the GPU one and a half times (4
+  // prompts of up to 4096 tokens, 64 / 8 heads: 241 us with 2, 254 with 4, 278
+  // with 8, which each start and end more often).
+  const long long tiles = ceil_div(max_q_len, p.tile_tokens);
+  p.mirror = tiles >= kMassTiles;
+  if (p.mirror) {
+    const long long pairs = ceil_div(ceil_div(max_kv_len, sa::prefill_mass_pair_keys()), 2);
+    const long long clusters = pairs * num_seqs * num_kv_heads;
+    while ((1 << p.split_log2) < kMaxCluster && (clusters << p.split_log2) < 3ll * p.num_sms &&
+           tiles >= (kMassTiles << p.split_log2))
+      ++p.split_log2;
+  }
   p.split = 1 << p.split_log2;
   CUtensorMap qmap, kmap;
   if (!encode_map(&qmap, q, num_qo_heads, total_q, p.group, p.tile_tokens) ||

@@ -69,6 +69,51 @@ def test_prefill_mass(heads, q_lens, prefix):
         _mass_close(mass, times * want)
 
 
+@pytest.mark.parametrize("heads,lens", [((8, 1), [1111, 2300, 40]), ((32, 1), [700, 9, 1500]), ((4, 1), [2205])])
+def test_prefill_mass_of_long_prompts(heads, lens):
+    # prompts long enough that a cluster of CTAs shares each key's rows
+    hq, hkv = heads
+    c = Paged(lens, hq, hkv, seed=3)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q = bf16(c.rng, cu[-1], hq, 64)
+    k, v, table, kv = c.paged()
+    cu_gpu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    _, lse = sa.prefill_paged(q.to(DEV), cu_gpu, k, v, table, kv, c.sinks.to(DEV), c.scale, max(lens), c.max_kv)
+    bad = [b for b, n in enumerate(lens) if n == 40]
+    for b in bad:
+        kv[b] = -7                                        # out of range: among the long ones
+    mass = torch.zeros(len(lens), hkv, c.max_kv, device=DEV)
+    sa.prefill_mass(q.to(DEV), cu_gpu, k, table, kv, lse, c.scale, max(lens), c.max_kv, mass)
+    for b, n in enumerate(lens):
+        if b in bad:
+            assert torch.isnan(mass[b]).all()
+            continue
+        s = np.einsum("ihd,jd->hij", np64(q[cu[b]:cu[b + 1]]), np64(c.k[b][:, 0])) * c.scale
+        w = np.exp(s - np64(lse[cu[b]:cu[b + 1]]).T[:, :, None])
+        w[:, np.arange(n)[:, None] < np.arange(n)] = 0
+        _mass_close(mass[b, 0, :n], w.sum((0, 1)))
+        assert (mass[b, :, n:] == 0).all()
+
+
+def test_prefill_mass_of_many_prompts():
+    # enough (request, KV head) units that none is shared
+    lens = [300 + 7 * (b % 5) for b in range(60)]
+    c = Paged(lens, 64, 8, seed=4)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q = bf16(c.rng, cu[-1], 64, 64)
+    k, v, table, kv = c.paged()
+    cu_gpu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    _, lse = sa.prefill_paged(q.to(DEV), cu_gpu, k, v, table, kv, c.sinks.to(DEV), c.scale, max(lens), c.max_kv)
+    mass = torch.zeros(60, 8, c.max_kv, device=DEV)
+    sa.prefill_mass(q.to(DEV), cu_gpu, k, table, kv, lse, c.scale, max(lens), c.max_kv, mass)
+    for b in (0, 13, 59):
+        n = lens[b]
+        s = np.einsum("ighd,jgd->ghij", np64(q[cu[b]:cu[b + 1]]).reshape(n, 8, 8, 64), np64(c.k[b])) * c.scale
+        w = np.exp(s - np64(lse[cu[b]:cu[b + 1]]).T.reshape(8, 8, n, 1))
+        w[..., np.arange(n)[:, None] < np.arange(n)] = 0
+        _mass_close(mass[b, :, :n], w.sum((1, 2)))
+
+
 def test_mass_is_the_same_bits_every_time_and_in_a_graph():
     c = Paged([700, 333], 64, 8)
     q, q1 = bf16(c.rng, 300, 64, 64).to(DEV), bf16(c.rng, 2, 64, 64).to(DEV)
