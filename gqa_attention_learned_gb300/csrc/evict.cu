@@ -6,8 +6,8 @@
 //
 // Two kernels, the second launched under the first's end.
 // select: a cluster of CTAs per (request, KV head), each with a contiguous
-//   share of the keys, whose weights it reads once into registers (longer
-//   shares are read again, from L2, in each pass).  A radix select over
+//   share of the keys, whose weights it keeps in shared memory (what exceeds
+//   100 KB is read again, from L2, in each pass).  A radix select over
 //   the weights' order-preserving bits (11 + 11 + 10 bits; histograms in shared
 //   memory, joined in the first CTA's through distributed shared memory) gives
 //   the weight of the last key that stays and how many of its equals stay,
@@ -41,6 +41,8 @@ constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxSplit = 8;             // CTAs per (request, KV head)
 constexpr int kKeysPerCta = 4096;        // keys per CTA at least, where a row has more than one
+constexpr int kGroup = 128;              // keys a warp looks at together, four per lane
+constexpr int kMaxCached = 1536;         // weights per warp in shared memory
 constexpr int kMoveRows = 4;             // rows in flight per thread and batch
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -96,11 +98,25 @@ __device__ void find_bin(SelectSmem &s, int left, int &bin, int &rest) {
   rest = s.left;
 }
 
-// kHeld: weights a thread holds.
-template <int kHeld>
-__global__ void __launch_bounds__(kSelectThreads, kHeld == 8 ? 4 : 2)
+// Sum of a number over the lanes before this one, as ballots of its four bits.
+struct Four {
+  unsigned b[4];
+  __device__ __forceinline__ explicit Four(const bool (&v)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) b[q] = __ballot_sync(0xffffffffu, v[q]);
+  }
+  __device__ __forceinline__ int before(unsigned below) const {
+    return __popc(b[0] & below) + __popc(b[1] & below) + __popc(b[2] & below) + __popc(b[3] & below);
+  }
+  __device__ __forceinline__ int total() const {
+    return __popc(b[0]) + __popc(b[1]) + __popc(b[2]) + __popc(b[3]);
+  }
+};
+
+__global__ void __launch_bounds__(kSelectThreads, 3)
 evict_select_kernel(const EvictParams p) {
   __shared__ SelectSmem s;
+  extern __shared__ uint4 kept_bits[];                    // [warps][p.cached / 4]
   cg::cluster_group cluster = cg::this_cluster();
   const int split = p.split;
   const int rank = static_cast<int>(blockIdx.x % split), unit = static_cast<int>(blockIdx.x / split);
@@ -136,26 +152,47 @@ evict_select_kernel(const EvictParams p) {
   const float *mass = p.mass + static_cast<size_t>(unit) * p.mass_stride;
   const int lo = p.first_tokens, hi = n - p.recent;       // the keys that compete
   const int want = p.budget - p.first_tokens - p.recent;  // how many of them stay
-  // this warp's keys: a contiguous run, whole multiples of 32, in blocks of
-  // kHeld keys per lane (one block unless the row is very long)
-  const int run = cdiv(cdiv(n, split * kSelectWarps), 32) * 32;
+  // This warp's keys: a contiguous run, whole multiples of kGroup, of which a
+  // lane takes four neighbours at a time.  Order bits of the first p.cached of
+  // them are kept, the others come from global memory in every pass.
+  const int run = cdiv(cdiv(n, split * kSelectWarps), kGroup) * kGroup;
   const long long from = static_cast<long long>(rank * kSelectWarps + warp) * run;
   const int begin = static_cast<int>(min(static_cast<long long>(n), from));
   const int end = static_cast<int>(min(static_cast<long long>(n), from + run));
-  constexpr int kBlock = 32 * kHeld;
-  uint32_t bits[kHeld];                                   // key i0 + 32 u + lane
-  auto load = [&](int i0) {
-    float v[kHeld];
+  uint4 *cache = kept_bits + warp * (p.cached / 4);
+  const int cached_end = min(begin + min(run, p.cached), cdiv(end - begin, kGroup) * kGroup + begin);
+  constexpr int kUnroll = 8;
+  for (int i0 = begin; i0 < cached_end; i0 += 32 * kUnroll) {
+    float v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + 32 * u + lane;
       v[u] = i < end ? mass[i] : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) bits[u] = order_bits(v[u]);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + 32 * u + lane;
+      if (i < cached_end) reinterpret_cast<uint32_t *>(cache)[i - begin] = order_bits(v[u]);
+    }
+  }
+  __syncwarp();
+  // f(key, order bits of key .. key + 3, whether all 128 keys of the warp
+  // compete); keys >= end do not exist
+  auto each = [&](auto f) {
+    auto plain = [&](int i0) { return i0 >= lo && i0 + kGroup <= min(hi, end); };
+#pragma unroll 2
+    for (int i0 = begin; i0 < cached_end; i0 += kGroup) {
+      const uint4 w = cache[(i0 - begin) / 4 + lane];
+      const uint32_t four[4] = {w.x, w.y, w.z, w.w};
+      f(i0 + 4 * lane, four, plain(i0));
+    }
+    for (int i0 = cached_end; i0 < end; i0 += kGroup) {
+      uint32_t four[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) four[q] = i0 + 4 * lane + q < end ? order_bits(mass[i0 + 4 * lane + q]) : 0u;
+      f(i0 + 4 * lane, four, plain(i0));
+    }
   };
-  const bool held = run <= kBlock;
-  if (held) load(begin);
 
   // ---- the want-th largest weight, from the top bits down
   uint32_t prefix = 0;
@@ -168,16 +205,12 @@ evict_select_kernel(const EvictParams p) {
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
       for (int i = tid; i < kBins; i += kSelectThreads) s.hist[i] = 0;
       cluster.sync();
-      for (int i0 = begin; i0 < end; i0 += kBlock) {
-        if (!held) load(i0);
+      each([&](int i, const uint32_t (&w)[4], bool plain) {
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-          if (i0 + 32 * u >= end) break;
-          const int i = i0 + 32 * u + lane;
-          if (i < end && i >= lo && i < hi && (bits[u] & known) == prefix)
-            atomicAdd(&s.hist[(bits[u] >> shift) & digits], 1);
-        }
-      }
+        for (int q = 0; q < 4; ++q)
+          if ((w[q] & known) == prefix && (plain || (i + q >= lo && i + q < min(hi, end))))
+            atomicAdd(&s.hist[(w[q] >> shift) & digits], 1);
+      });
       if (split > 1) {
         __syncthreads();
         if (rank != 0) {
@@ -220,17 +253,15 @@ evict_select_kernel(const EvictParams p) {
     equal = i < end && competes && want > 0 && w == prefix;
   };
   int n_sure = 0, n_equal = 0;
-  for (int i0 = begin; i0 < end; i0 += kBlock) {
-    if (!held) load(i0);
+  each([&](int i, const uint32_t (&w)[4], bool plain) {
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      if (i0 + 32 * u >= end) break;
-      bool sure, equal;
-      kind(i0 + 32 * u + lane, bits[u], sure, equal);
+    for (int q = 0; q < 4; ++q) {
+      bool sure = w[q] > prefix, equal = w[q] == prefix;
+      if (!plain || want == 0) kind(i + q, w[q], sure, equal);
       n_sure += sure;
       n_equal += equal;
     }
-  }
+  });
   n_sure = warp_sum(n_sure);
   n_equal = warp_sum(n_equal);
   if (lane == 0) {
@@ -264,22 +295,29 @@ evict_select_kernel(const EvictParams p) {
   // ---- the kept indices, in order
   int at = sure_before + min(equal_before, left);         // kept before this warp's keys
   const unsigned below = (1u << lane) - 1u;
-  for (int i0 = begin; i0 < end; i0 += kBlock) {
-    if (!held) load(i0);
+  each([&](int i, const uint32_t (&w)[4], bool plain) {
+    bool keep[4], equal[4];
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      if (i0 + 32 * u >= end) break;
-      const int i = i0 + 32 * u + lane;
-      bool sure, equal;
-      kind(i, bits[u], sure, equal);
-      const unsigned eq = __ballot_sync(0xffffffffu, equal);
-      const bool keep = sure || (equal && equal_before + __popc(eq & below) < left);
-      const unsigned all = __ballot_sync(0xffffffffu, keep);
-      if (keep) kept[at + __popc(all & below)] = i;
-      at += __popc(all);
-      equal_before += __popc(eq);
+    for (int q = 0; q < 4; ++q) {
+      keep[q] = w[q] > prefix;
+      equal[q] = w[q] == prefix;
+      if (!plain || want == 0) kind(i + q, w[q], keep[q], equal[q]);
     }
-  }
+    if (n_equal) {                                        // warp-uniform: ties to number
+      const Four eq(equal);
+      int e = equal_before + eq.before(below);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (equal[q]) keep[q] = e++ < left;
+      equal_before += eq.total();
+    }
+    const Four all(keep);
+    int r = at + all.before(below);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (keep[q]) kept[r++] = i + q;
+    at += all.total();
+  });
   if (split > 1) cluster.sync();                          // peers have written this CTA's counts
 }
 
@@ -369,13 +407,14 @@ cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream) {
     p.split *= 2;
   if (3 * units > 0x7fffffffull || p.split * units > 0x7fffffffull)
     return cudaErrorInvalidConfiguration;
-  // rows of up to 4096 keys per CTA fit 8 registers per thread, which lets twice
-  // as many CTAs be resident
-  const bool small = p.max_kv_len <= 8 * kSelectThreads * p.split;
-  const cudaError_t err =
-      launch_clusters(small ? evict_select_kernel<8> : evict_select_kernel<32>,
-                      static_cast<unsigned>(p.split * units), static_cast<unsigned>(p.split),
-                      kSelectThreads, 0, stream, true, p);
+  // every weight of a CTA's share where 100 KB hold them
+  const long long share = cdiv(p.max_kv_len, p.split * kSelectWarps);
+  p.cached = static_cast<int>(std::min<long long>((share + kGroup - 1) / kGroup * kGroup, kMaxCached));
+  cudaError_t err = set_smem_once<evict_select_kernel>(kSelectWarps * kMaxCached * 4);
+  if (err != cudaSuccess) return err;
+  err = launch_clusters(evict_select_kernel, static_cast<unsigned>(p.split * units),
+                        static_cast<unsigned>(p.split), kSelectThreads,
+                        kSelectWarps * p.cached * 4, stream, true, p);
   if (err != cudaSuccess) return err;
   // bytes in flight: few rows of units get larger CTAs (64 requests x 8 heads,
   // 1024 keys kept: 64 us in all with 512 threads, 74 with 1024; 8 x 8, 8192

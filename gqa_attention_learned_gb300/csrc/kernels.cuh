@@ -242,9 +242,10 @@ struct EvictParams {
   int max_pages_per_seq, dst_max_pages, mass_stride, dst_mass_stride;
   int budget, first_tokens, recent;
   int split;                     // CTAs per (request, KV head) that select
+  int cached;                    // weights per warp that they keep in shared memory
 };
 
-cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream);   // sets p.split
+cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream);   // sets p.split, p.cached
 
 // --------------------------------------------------------------- prologue
 struct PrologueParams {

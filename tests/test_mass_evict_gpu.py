@@ -263,6 +263,20 @@ def test_evict_long(in_place):
     _check(c, ref, kept.cpu(), new.cpu(), 4099, dst, k, v, c.k_cache, c.v_cache, dst_mass, mass, before)
 
 
+def test_evict_one_long_row_among_many():
+    # so many rows that none is shared, one of them longer than a CTA holds
+    lens = [30001] + [5] * 160
+    c = Paged(lens, 1, 1, seed=6)
+    for kind in ("normal", "ties"):
+        mass = torch.from_numpy(_weights(c.rng, kind, len(lens), 1, 30001))
+        ref = _evict_ref(c, mass, 4099, 4, 100)
+        k, v, table, kv = c.paged()
+        m = mass.to(DEV)
+        new, kept = sa.evict(k, v, table, kv, m, 4099, 30001, first_tokens=4, recent=100)
+        torch.cuda.synchronize()
+        _check(c, ref, kept.cpu(), new.cpu(), 4099, c.table, k, v, c.k_cache, c.v_cache, m, mass, mass)
+
+
 def test_evict_leaves_bad_requests_alone():
     c = Paged([100, 100, 100, 100, 100], 1, 1)
     mass = torch.from_numpy(_weights(c.rng, "normal", 5, 1, 100)).to(DEV)
