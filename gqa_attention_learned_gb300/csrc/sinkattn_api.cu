@@ -829,7 +829,9 @@ int mass_params(sa::MassParams &p, const void *q, const void *k_cache, const int
       mass_stride < max_kv_len || !std::isfinite(scale))
     return SINKATTN_INVALID_ARGUMENT;
   if (num_seqs > 0 && total_q > 0) {
-    if (!q || !k_cache || !page_table || !kv_lens || !lse || !mass) return SINKATTN_INVALID_ARGUMENT;
+    // an empty mass (no request has keys) needs no memory
+    if (!q || !k_cache || !page_table || !kv_lens || !lse || (!mass && mass_stride > 0))
+      return SINKATTN_INVALID_ARGUMENT;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(page_table, 4) ||
         !aligned(kv_lens, 4) || !aligned(lse, 4) || !aligned(mass, 4))
       return SINKATTN_INVALID_ARGUMENT;
@@ -895,7 +897,7 @@ int sinkattn_decode_mass(const void *q, const void *k_cache, const int32_t *page
   const int st = mass_params(p, q, k_cache, page_table, max_pages_per_seq, kv_lens, lse, scale,
                              mass, mass_stride, batch, batch, num_qo_heads, num_kv_heads, head_dim,
                              page_size, num_pages, max_kv_len);
-  if (st != SINKATTN_OK || batch == 0) return st;
+  if (st != SINKATTN_OK || batch == 0 || mass_stride == 0) return st;
   p.pages_per_chunk = kMassPagesPerWarp * sa::decode_mass_warps();
   p.num_chunks = std::max(1, ceil_div(ceil_div(max_kv_len, kPageSize), p.pages_per_chunk));
   return cuda_status(sa::launch_decode_mass(p, static_cast<cudaStream_t>(stream)),
@@ -915,7 +917,7 @@ int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_se
                              head_dim, page_size, num_pages, max_kv_len);
   if (st != SINKATTN_OK) return st;
   if (p.group > kPrefillTile) return SINKATTN_UNSUPPORTED;
-  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return SINKATTN_OK;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0 || mass_stride == 0) return SINKATTN_OK;
   if (!cu_seqlens_q || !aligned(cu_seqlens_q, 4)) return SINKATTN_INVALID_ARGUMENT;
   p.cu_seqlens_q = cu_seqlens_q;
   p.max_q_len = max_q_len;
@@ -966,7 +968,8 @@ int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *page_table, int 
       static_cast<long long>(first_tokens) + recent > budget)
     return SINKATTN_INVALID_ARGUMENT;
   if (batch == 0) return SINKATTN_OK;
-  if (!k_cache || !v_cache || !page_table || !kv_lens || !mass || !new_kv_lens || !kept)
+  if (!k_cache || !v_cache || !page_table || !kv_lens || (!mass && mass_stride > 0) ||
+      !new_kv_lens || !kept)
     return SINKATTN_INVALID_ARGUMENT;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(page_table, 4) ||
       !aligned(kv_lens, 4) || !aligned(mass, 4) || !aligned(dst_page_table, 4) ||

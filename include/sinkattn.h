@@ -501,11 +501,11 @@ SINKATTN_API int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_
  *   mass             : fp32 [batch][num_kv_heads][mass_stride >= max_kv_len]
  *   dst_page_table   : int32 [batch][dst_max_pages_per_seq] (> 0), the pages
  *                      that take the kept keys; NULL: page_table itself, in
- *                      place.  Other pages than the request's own must belong
- *                      to no request of the call, and no page may appear
- *                      twice.  With them the old pages stay as they are (they
- *                      may be shared by requests); in place, pages must not be
- *                      shared.
+ *                      place.  A row either lists the request's own pages in
+ *                      their order, or pages that belong to no request of the
+ *                      call; no page may appear twice.  With new pages the old
+ *                      ones stay as they are (they may be shared by requests);
+ *                      in place, pages must not be shared.
  *   dst_mass         : fp32 [batch][num_kv_heads][dst_mass_stride >=
  *                      min(budget, max_kv_len)], not overlapping mass; NULL:
  *                      mass itself, in place.  Entries from the new length to
@@ -520,6 +520,8 @@ SINKATTN_API int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_
  * those of its keys or their destinations, is left as it was: its new length
  * is -1 (a decode on that gives NaN) and its kept entries are -1.
  * Launched programmatically whatever the default (as sinkattn_decode_mass).
+ * It writes new_kv_lens: a decode on them that follows it directly on the
+ * stream has to be an ordinary launch (SINKATTN_LAUNCH_PLAIN).
  */
 SINKATTN_API int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *page_table,
                          int max_pages_per_seq, const int32_t *kv_lens, float *mass,

@@ -164,6 +164,7 @@ def test_mass_refusals(lib):
         return _call(lib.sinkattn_decode_mass, order, good, **kw)
 
     assert call(batch=0) == sa.OK
+    assert call(mass=None, stride=0, maxkv=0) == sa.OK
     for kw in (dict(stride=15), dict(lse=None), dict(mass=None), dict(hq=6, hkv=4), dict(q=ODD),
                dict(mass=ctypes.c_void_p(0x10002)), dict(scale=float("nan")), dict(batch=-1)):
         assert call(**kw) == sa.INVALID_ARGUMENT, kw

@@ -298,6 +298,57 @@ def test_evict_leaves_bad_requests_alone():
     assert torch.equal(mass[:4], before[2][:4])
 
 
+def test_nothing_to_weigh_or_evict():
+    c = Paged([0, 0], 4, 1)
+    k, v, table, kv = c.paged()
+    q = bf16(c.rng, 2, 4, 64).to(DEV)
+    lse = torch.zeros(2, 4, device=DEV)
+    mass = torch.zeros(2, 1, 0, device=DEV)
+    sa.decode_mass(q, k, table, kv, lse, c.scale, 0, mass)
+    sa.prefill_mass(q, torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV), k, table, kv, lse, c.scale, 1, 0, mass)
+    new, kept = sa.evict(k, v, table, kv, mass, 8, 0)
+    assert new.tolist() == [0, 0] and (kept == -1).all()
+
+
+def test_evict_from_a_graph_and_on_two_streams():
+    # a captured eviction replays on new weights and lengths; two evictions of
+    # different requests run side by side
+    cs = [Paged([900, 40, 333], 2, 2, seed=s) for s in (1, 2)]
+    sides = [torch.cuda.Stream() for _ in cs]
+    runs = []
+    for c, side in zip(cs, sides):
+        k, v, table, kv = c.paged()
+        mass = torch.zeros(3, 2, 900, device=DEV)
+        new, kept = torch.empty_like(kv), torch.empty(3, 2, 100, dtype=torch.int32, device=DEV)
+
+        def call(k=k, v=v, table=table, kv=kv, mass=mass, new=new, kept=kept):
+            sa.evict(k, v, table, kv, mass, 100, 900, first_tokens=3, recent=20, new_kv_lens=new, kept=kept)
+
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            call()                                        # weights 0: ties, then put everything back
+        side.synchronize()
+        k.copy_(c.k_cache), v.copy_(c.v_cache)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call()
+        runs.append((c, g, side, k, v, mass, new, kept))
+    for rep in range(2):
+        weights = []
+        for c, g, side, k, v, mass, new, kept in runs:
+            w = torch.from_numpy(_weights(c.rng, "normal", 3, 2, 900))
+            weights.append(w)
+            k.copy_(c.k_cache), v.copy_(c.v_cache), mass.copy_(w)
+        torch.cuda.synchronize()
+        for c, g, side, *_ in runs:
+            with torch.cuda.stream(side):
+                g.replay()
+        torch.cuda.synchronize()
+        for w, (c, g, side, k, v, mass, new, kept) in zip(weights, runs):
+            _check(c, _evict_ref(c, w, 100, 3, 20), kept.cpu(), new.cpu(), 100, c.table, k, v, c.k_cache,
+                   c.v_cache, mass, w, w)
+
+
 # ------------------------------------------------------------ all together
 def test_a_serving_loop_with_eviction():
     # prompt -> its weights -> cut to a budget -> new tokens that attend to

@@ -17,7 +17,7 @@ from tolerances import assert_lse_close, assert_out_close
 
 pytestmark = pytest.mark.gpu
 
-HEADS = [(64, 8), (4, 1), (8, 8), (10, 2), (32, 2)]
+HEADS = [(64, 8), (4, 1), (8, 8), (10, 2), (32, 2), (24, 1)]
 WINDOWS = [(1, 0), (2, 1), (16, 0), (17, 5), (128, 4), (130, 33), (1000, 0), (40, 64)]
 LENS = [0, 1, 2, 15, 16, 17, 31, 33, 128, 129, 144, 145, 300, 301]
 
@@ -165,6 +165,49 @@ def test_prefill_window_leaves_other_rows_alone_and_flags_bad_ones():
     sa.prefill_window(q, k, v, torch.tensor([0, 90, 120], dtype=torch.int32, device=DEV), sinks, 0.125,
                       90, 8, out=out, lse=lse)
     assert torch.isfinite(out[:90]).all() and torch.isnan(out[90:]).all()
+
+
+def test_long_windows_leave_other_rows_alone_and_flag_bad_ones():
+    # the same where a tile's keys do not fit at once
+    rng = np.random.default_rng(5)
+    q, k, v = (bf16(rng, 700, h, 64).to(DEV) for h in (4, 1, 1))
+    sinks = torch.zeros(4, device=DEV)
+    for cu, bad, good in (([0, 300, 600], [], [(0, 600)]), ([0, 250, 600], [(250, 600)], [(0, 250)]),
+                          ([0, 290, 580, 900], [(580, 700)], [(0, 580)])):
+        out = torch.full_like(q, 7.0)
+        lse = torch.full((700, 4), 7.0, device=DEV)
+        sa.prefill_window(q, k, v, torch.tensor(cu, dtype=torch.int32, device=DEV), sinks, 0.125, 300, 280,
+                          out=out, lse=lse)
+        touched = torch.zeros(700, dtype=torch.bool, device=DEV)
+        for a, z in good:
+            touched[a:z] = True
+            assert torch.isfinite(out[a:z]).all() and not (out[a:z] == 7).all(-1).any()
+        for a, z in bad:
+            touched[a:z] = True
+            assert torch.isnan(out[a:z]).all() and torch.isnan(lse[a:z]).all()
+        assert (out[~touched] == 7).all() and (lse[~touched] == 7).all()
+
+
+def test_windowed_calls_without_lse_and_without_keys():
+    c = Paged([0, 0], 4, 1)
+    q = bf16(c.rng, 2, 4, 64).to(DEV)
+    k, v, table, lens = c.paged()
+    out, lse = sa.decode_window(q, k, v, table, lens, c.sinks.to(DEV), c.scale, 0, 5, 3)
+    assert (out == 0).all()
+    assert_lse_close(lse, np.broadcast_to(np64(c.sinks), (2, 4)))
+    c = Paged([500], 4, 1)
+    q = bf16(c.rng, 500, 4, 64).to(DEV)
+    cu = torch.tensor([0, 500], dtype=torch.int32, device=DEV)
+    kv = c.paged()
+    for window in (20, 400):
+        args = (q, cu, *kv, c.sinks.to(DEV), c.scale, 500, 500, window, 2)
+        a, none = sa.prefill_paged_window(*args, want_lse=False)
+        b, _ = sa.prefill_paged_window(*args)
+        assert none is None and torch.equal(a, b)
+    q1 = q[:1].contiguous()
+    a, none = sa.decode_window(q1, *kv, c.sinks.to(DEV), c.scale, 500, 20, want_lse=False)
+    b, _ = sa.decode_window(q1, *kv, c.sinks.to(DEV), c.scale, 500, 20)
+    assert none is None and torch.equal(a, b)
 
 
 def test_prefill_paged_window_bad_page_and_short_cache():
