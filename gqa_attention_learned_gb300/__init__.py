@@ -451,14 +451,27 @@ def _shape(t, name, shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+_Tensor, _BF16, _F32, _I32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
+
+
+def _is(t, dtype, dims, dev):
+    """What `_want` asks for, as one quick test: the small calls spend more
+    time on the host than on the GPU."""
+    return (type(t) is _Tensor and t.dtype is dtype and t.dim() == dims and t.device == dev
+            and t.is_contiguous())
+
+
 def _paged_args(dev, batch, page_table, kv_lens, k_cache, v_cache=None):
-    _want(k_cache, "k_cache", torch.bfloat16, 4, dev)
-    _want(page_table, "page_table", torch.int32, 2, dev)
-    _want(kv_lens, "kv_lens", torch.int32, 1, dev)
-    if v_cache is not None:
-        _want(v_cache, "v_cache", torch.bfloat16, 4, dev)
-        if v_cache.shape != k_cache.shape:
-            raise ValueError(f"v_cache must be {list(k_cache.shape)}, got {list(v_cache.shape)}")
+    if not (_is(k_cache, _BF16, 4, dev) and _is(page_table, _I32, 2, dev)
+            and _is(kv_lens, _I32, 1, dev) and (v_cache is None or _is(v_cache, _BF16, 4, dev))
+            and dev.type == "cuda"):
+        _want(k_cache, "k_cache", _BF16, 4, dev)
+        _want(page_table, "page_table", _I32, 2, dev)
+        _want(kv_lens, "kv_lens", _I32, 1, dev)
+        if v_cache is not None:
+            _want(v_cache, "v_cache", _BF16, 4, dev)
+    if v_cache is not None and v_cache.shape != k_cache.shape:
+        raise ValueError(f"v_cache must be {list(k_cache.shape)}, got {list(v_cache.shape)}")
     if page_table.shape[0] != batch or kv_lens.shape[0] != batch:
         raise ValueError(f"page_table and kv_lens must have {batch} rows, got "
                          f"{page_table.shape[0]} and {kv_lens.shape[0]}")
@@ -498,14 +511,16 @@ def decode_window(q, k_cache, v_cache, page_table, kv_lens, sinks, scale, max_kv
     newest keys (its own included) and the `first_tokens` oldest.  Pages
     without a visible key are not looked up (their page_table entries may hold
     anything).  Returns (out [B, Hq, 64] bf16, lse [B, Hq] fp32 or None)."""
-    # the smallest calls last a few microseconds on the GPU: the checks below
-    # are kept to what an argument can get wrong, and the plan is made by the
-    # library alone when the caller brings the workspace
+    # the smallest calls last a few microseconds on the GPU: the checks are kept
+    # to what an argument can get wrong, and the plan is made by the library
+    # alone when the caller brings the workspace
     dev = q.device
-    _want(q, "q", torch.bfloat16, 3)
+    if not _is(q, _BF16, 3, dev):
+        _want(q, "q", _BF16, 3)
     batch, hq, d = q.shape
     _paged_args(dev, batch, page_table, kv_lens, k_cache, v_cache)
-    _want(sinks, "sinks", torch.float32, 1, dev)
+    if not _is(sinks, _F32, 1, dev):
+        _want(sinks, "sinks", _F32, 1, dev)
     num_pages, hkv, page, d2 = k_cache.shape
     if d2 != d or sinks.shape[0] != hq:
         raise ValueError("k_cache, sinks and q disagree in head_dim or heads")
@@ -527,7 +542,8 @@ def decode_window(q, k_cache, v_cache, page_table, kv_lens, sinks, scale, max_kv
                 workspace = torch.zeros(ws_len, dtype=torch.uint8, device=dev)
                 ws_ptr = workspace.data_ptr()
         else:
-            _want(workspace, "workspace", workspace.dtype, None, dev)
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be contiguous and on {dev}")
             ws_ptr, ws_len = workspace.data_ptr(), workspace.nbytes
         status = load().sinkattn_decode_window(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
@@ -656,14 +672,18 @@ def evict(k_cache, v_cache, page_table, kv_lens, mass, budget, max_kv_len, *, fi
     batch = kv_lens.shape[0]
     _paged_args(dev, batch, page_table, kv_lens, k_cache, v_cache)
     num_pages, hkv, page, d = k_cache.shape
-    _want(mass, "mass", torch.float32, 3, dev)
-    _shape(mass, "mass", (batch, hkv, mass.shape[2]))
+    for name, m in (("mass", mass), ("dst_mass", dst_mass)):
+        if m is None and name == "dst_mass":
+            continue
+        if not _is(m, _F32, 3, dev):
+            _want(m, name, _F32, 3, dev)
+        if m.shape[0] != batch or m.shape[1] != hkv:
+            raise ValueError(f"{name} must be [{batch}, {hkv}, ...], got {list(m.shape)}")
     if dst_page_table is not None:
-        _want(dst_page_table, "dst_page_table", torch.int32, 2, dev)
-        _shape(dst_page_table, "dst_page_table", (batch, dst_page_table.shape[1]))
-    if dst_mass is not None:
-        _want(dst_mass, "dst_mass", torch.float32, 3, dev)
-        _shape(dst_mass, "dst_mass", (batch, hkv, dst_mass.shape[2]))
+        if not _is(dst_page_table, _I32, 2, dev):
+            _want(dst_page_table, "dst_page_table", _I32, 2, dev)
+        if dst_page_table.shape[0] != batch:
+            raise ValueError(f"dst_page_table must have {batch} rows")
     budget = _size(budget, "budget", 1)
     first, recent = _size(first_tokens, "first_tokens"), _size(recent, "recent")
     with _at(dev, stream):
