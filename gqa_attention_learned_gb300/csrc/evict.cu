@@ -43,6 +43,7 @@ constexpr int kMaxSplit = 8;             // CTAs per (request, KV head)
 constexpr int kKeysPerCta = 4096;        // keys per CTA at least, where a row has more than one
 constexpr int kGroup = 128;              // keys a warp looks at together, four per lane
 constexpr int kMaxCached = 1536;         // weights per warp in shared memory
+constexpr int kMoveThreads = 1024;
 constexpr int kMoveRows = 4;             // rows in flight per thread and batch
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -98,6 +99,85 @@ __device__ void find_bin(SelectSmem &s, int left, int &bin, int &rest) {
   rest = s.left;
 }
 
+// The mass of one (request, KV head), by a whole CTA.
+template <int kThreads>
+__device__ __forceinline__ void move_mass(const EvictParams &p, int unit, int count) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const int *kept = p.kept + static_cast<size_t>(unit) * p.budget;
+  const float *src = p.mass + static_cast<size_t>(unit) * p.mass_stride;
+  float *dst = p.dst_mass + static_cast<size_t>(unit) * p.dst_mass_stride;
+  for (int base = 0; base < count; base += kThreads * kMoveRows) {
+    float v[kMoveRows];
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int r = base + u * kThreads + tid;
+      if (r < count) v[u] = src[kept[r]];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int r = base + u * kThreads + tid;
+      if (r < count) dst[r] = v[u];
+    }
+  }
+  __syncthreads();
+  // evicted places start again from nothing
+  const int n = p.kv_lens[unit / p.num_kv_heads];
+  for (int i = count + tid; i < min(n, p.dst_mass_stride); i += kThreads) dst[i] = 0.f;
+}
+
+// The K rows, V rows or both (kPools 2) of one (request, KV head), by a whole
+// CTA: K and V rows lie at the same place of their pools.
+template <int kThreads, int kPools, int kRows>      // kRows: of each pool in flight per thread
+__device__ __forceinline__ void move_rows(const EvictParams &p, int unit, int count, uint16_t *first) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const int kvh = unit % p.num_kv_heads, b = unit / p.num_kv_heads;
+  const int *kept = p.kept + static_cast<size_t>(unit) * p.budget;
+  uint4 *pool[2] = {reinterpret_cast<uint4 *>(first), reinterpret_cast<uint4 *>(p.v_cache)};
+  const int32_t *src_table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
+  const int32_t *dst_table = p.dst_page_table + static_cast<size_t>(b) * p.dst_max_pages;
+  const bool in_place = src_table == dst_table;
+  constexpr int kPieces = kHeadDim * 2 / 16;              // 16-byte pieces of a row
+  constexpr int kAtOnce = kThreads / kPieces, kBatch = kAtOnce * kRows;
+  const int row = tid / kPieces, piece = tid % kPieces;
+  auto address = [&](const int32_t *table, int key) {
+    return (static_cast<size_t>(table[key / kPageSize]) * p.num_kv_heads + kvh) * (kPageSize * kPieces) +
+           (key % kPageSize) * kPieces + piece;
+  };
+  // the indices of a batch are read while the one before is on its way
+  int from[kRows];
+  auto look_up = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int r = base + u * kAtOnce + row;
+      from[u] = r < count ? kept[r] : -1;
+      if (in_place && from[u] == r) from[u] = -1;         // where it belongs already
+    }
+  };
+  look_up(0);
+  for (int base = 0; base < count; base += kBatch) {
+    uint4 v[kPools][kRows];
+    bool moves[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      moves[u] = from[u] >= 0;
+      if (!moves[u]) continue;
+      const size_t at = address(src_table, from[u]);
+#pragma unroll
+      for (int q = 0; q < kPools; ++q) v[q][u] = pool[q][at];
+    }
+    look_up(base + kBatch);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (!moves[u]) continue;
+      const size_t at = address(dst_table, base + u * kAtOnce + row);
+#pragma unroll
+      for (int q = 0; q < kPools; ++q) pool[q][at] = v[q][u];
+    }
+  }
+}
+
 // Sum of a number over the lanes before this one, as ballots of its four bits.
 struct Four {
   unsigned b[4];
@@ -113,6 +193,15 @@ struct Four {
   }
 };
 
+// What a CTA of the first kernel does with its list where it has the row to
+// itself.
+__device__ __forceinline__ void move_all(const EvictParams &p, int unit, int count) {
+  __syncthreads();                                        // the kept indices are written
+  move_rows<kSelectThreads, 2, 2>(p, unit, count, p.k_cache);
+  move_mass<kSelectThreads>(p, unit, count);
+}
+
+template <bool kMoves>        // the row is this CTA's alone: it moves what it keeps, too
 __global__ void __launch_bounds__(kSelectThreads, 3)
 evict_select_kernel(const EvictParams p) {
   __shared__ SelectSmem s;
@@ -146,6 +235,7 @@ evict_select_kernel(const EvictParams p) {
   if (bad) return;
   if (n <= p.budget) {
     for (int i = rank * kSelectThreads + tid; i < n; i += step) kept[i] = i;
+    if (kMoves) move_all(p, unit, count);
     return;
   }
 
@@ -318,80 +408,20 @@ evict_select_kernel(const EvictParams p) {
       if (keep[q]) kept[r++] = i + q;
     at += all.total();
   });
+  if (kMoves) move_all(p, unit, count);
   if (split > 1) cluster.sync();                          // peers have written this CTA's counts
 }
 
-template <int kMoveThreads>
-__global__ void __launch_bounds__(kMoveThreads)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads)
 evict_move_kernel(const EvictParams p) {
   const int units = p.batch * p.num_kv_heads;
-  const int role = static_cast<int>(blockIdx.x) / units;  // K rows, V rows, mass
-  const int unit = static_cast<int>(blockIdx.x) % units;
-  const int kvh = unit % p.num_kv_heads, b = unit / p.num_kv_heads;
+  const int role = static_cast<int>(blockIdx.x) / units, unit = static_cast<int>(blockIdx.x) % units;
   grid_dependency_wait();
-  const int count = p.new_kv_lens[b];
+  const int count = p.new_kv_lens[unit / p.num_kv_heads];
   if (count < 0) return;
-  const int n = p.kv_lens[b];
-  const int *kept = p.kept + static_cast<size_t>(unit) * p.budget;
-  const int tid = static_cast<int>(threadIdx.x);
-  if (role == 2) {
-    const float *src = p.mass + static_cast<size_t>(unit) * p.mass_stride;
-    float *dst = p.dst_mass + static_cast<size_t>(unit) * p.dst_mass_stride;
-    for (int base = 0; base < count; base += kMoveThreads * kMoveRows) {
-      float v[kMoveRows];
-#pragma unroll
-      for (int u = 0; u < kMoveRows; ++u) {
-        const int r = base + u * kMoveThreads + tid;
-        if (r < count) v[u] = src[kept[r]];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kMoveRows; ++u) {
-        const int r = base + u * kMoveThreads + tid;
-        if (r < count) dst[r] = v[u];
-      }
-    }
-    __syncthreads();
-    // evicted places start again from nothing
-    for (int i = count + tid; i < min(n, p.dst_mass_stride); i += kMoveThreads) dst[i] = 0.f;
-    return;
-  }
-  uint4 *cache = reinterpret_cast<uint4 *>(role == 0 ? p.k_cache : p.v_cache);
-  const int32_t *src_table = p.page_table + static_cast<size_t>(b) * p.max_pages_per_seq;
-  const int32_t *dst_table = p.dst_page_table + static_cast<size_t>(b) * p.dst_max_pages;
-  const bool in_place = src_table == dst_table;
-  constexpr int kPieces = kHeadDim * 2 / 16;              // 16-byte pieces of a row
-  constexpr int kAtOnce = kMoveThreads / kPieces, kBatch = kAtOnce * kMoveRows;
-  const int row = tid / kPieces, piece = tid % kPieces;
-  auto address = [&](const int32_t *table, int key) {
-    return cache + (static_cast<size_t>(table[key / kPageSize]) * p.num_kv_heads + kvh) * (kPageSize * kPieces) +
-           (key % kPageSize) * kPieces + piece;
-  };
-  // the indices of a batch are read while the one before is on its way
-  int from[kMoveRows];
-  auto look_up = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int r = base + u * kAtOnce + row;
-      from[u] = r < count ? kept[r] : -1;
-      if (in_place && from[u] == r) from[u] = -1;         // where it belongs already
-    }
-  };
-  look_up(0);
-  for (int base = 0; base < count; base += kBatch) {
-    uint4 v[kMoveRows];
-    bool moves[kMoveRows];
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      moves[u] = from[u] >= 0;
-      if (moves[u]) v[u] = *address(src_table, from[u]);
-    }
-    look_up(base + kBatch);
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u)
-      if (moves[u]) *address(dst_table, base + u * kAtOnce + row) = v[u];
-  }
+  if (role == 2) move_mass<kThreads>(p, unit, count);
+  else move_rows<kThreads, 1, kMoveRows>(p, unit, count, role == 0 ? p.k_cache : p.v_cache);
 }
 
 }  // namespace
@@ -410,18 +440,20 @@ cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream) {
   // every weight of a CTA's share where 100 KB hold them
   const long long share = cdiv(p.max_kv_len, p.split * kSelectWarps);
   p.cached = static_cast<int>(std::min<long long>((share + kGroup - 1) / kGroup * kGroup, kMaxCached));
-  cudaError_t err = set_smem_once<evict_select_kernel>(kSelectWarps * kMaxCached * 4);
+  if (p.split == 1) {
+    const cudaError_t err = set_smem_once<evict_select_kernel<true>>(kSelectWarps * kMaxCached * 4);
+    if (err != cudaSuccess) return err;
+    return launch_clusters(evict_select_kernel<true>, static_cast<unsigned>(units), 1, kSelectThreads,
+                           kSelectWarps * p.cached * 4, stream, true, p);
+  }
+  cudaError_t err = set_smem_once<evict_select_kernel<false>>(kSelectWarps * kMaxCached * 4);
   if (err != cudaSuccess) return err;
-  err = launch_clusters(evict_select_kernel, static_cast<unsigned>(p.split * units),
+  err = launch_clusters(evict_select_kernel<false>, static_cast<unsigned>(p.split * units),
                         static_cast<unsigned>(p.split), kSelectThreads,
                         kSelectWarps * p.cached * 4, stream, true, p);
   if (err != cudaSuccess) return err;
-  // bytes in flight: few rows of units get larger CTAs (64 requests x 8 heads,
-  // 1024 keys kept: 64 us in all with 512 threads, 74 with 1024; 8 x 8, 8192
-  // kept: 146 and 101)
-  if (2 * units >= 2ull * num_sms)
-    return launch_kernel(evict_move_kernel<512>, static_cast<unsigned>(3 * units), 512, 0, stream, true, p);
-  return launch_kernel(evict_move_kernel<1024>, static_cast<unsigned>(3 * units), 1024, 0, stream, true, p);
+  return launch_kernel(evict_move_kernel<kMoveThreads>, static_cast<unsigned>(3 * units),
+                       kMoveThreads, 0, stream, true, p);
 }
 
 }  // namespace sa
