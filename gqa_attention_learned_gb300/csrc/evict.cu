@@ -4,7 +4,6 @@
 // and their mass move to the first slots of the request's pages (in place) or
 // of other pages.
 //
-// Two kernels, the second launched under the first's end.
 // select: a cluster of CTAs per (request, KV head), each with a contiguous
 //   share of the keys, whose weights it keeps in shared memory (what exceeds
 //   100 KB is read again, from L2, in each pass).  A radix select over
@@ -13,15 +12,19 @@
 //   the weight of the last key that stays and how many of its equals stay,
 //   lowest index first; ballots and prefix sums over warps and CTAs then place
 //   the kept indices in order.  A row is split only while all CTAs are
-//   resident at once: the passes are chains of cluster-wide steps, and a second
-//   wave of them costs more than longer shares (8 rows of 80k keys, 8 heads:
-//   53 us in two waves of eighths).
-// move: copies rows by that list, whole 128-byte rows, 64 KB of them in flight
-//   per CTA; a CTA owns a (request, KV head)'s K rows, V rows or mass.  In
+//   resident at once: its passes are chains of cluster-wide steps, so a second
+//   wave of CTAs costs more than longer shares do.
+// move: copies rows by that list, whole 128-byte rows.  A row that one CTA
+//   selects is moved by it as well, K and V side by side (64 rows of up to 4096
+//   keys, 8 heads, cut to 1024: 53 us, 4.5 TB/s, against 60 us with a second
+//   kernel); where a cluster shares a row a second kernel, launched under the
+//   first one's end, moves K, V and mass in CTAs of their own with 64 KB in
+//   flight (8 rows of up to 131072 keys cut to 8192: 97 us, half of it the
+//   selection's 5 passes over each weight, bound by their instructions).  In
 //   place is safe because the r-th kept key has index >= r: a batch of rows is
 //   read whole before any of it is written, and a write to slot r can only hit
 //   rows of this batch or earlier ones.
-// Bound by HBM: 4 bytes of mass per key, 512 bytes of K and V per kept one.
+// The least it can move: 4 bytes of mass per key, 520 bytes per kept key.
 
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -429,8 +432,8 @@ evict_move_kernel(const EvictParams p) {
 cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream) {
   const unsigned long long units = static_cast<unsigned long long>(p.batch) * p.num_kv_heads;
   if (units == 0) return cudaSuccess;
-  // CTAs per row: as many as are resident at once (two per SM), of
-  // kKeysPerCta keys at least
+  // CTAs per row: as many as are resident at once (two per SM with 100 KB of
+  // weights each), of kKeysPerCta keys at least
   p.split = 1;
   while (p.split < kMaxSplit && p.max_kv_len > kKeysPerCta * p.split &&
          units * 2 * p.split <= 2ull * num_sms)

