@@ -121,73 +121,45 @@ __device__ __forceinline__ bool softmax_tile(Bars &bar, uint32_t trow, int j, bo
   if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full, j & 1))) return false;
   tc_fence_after();
   const uint64_t scale2 = f2_pack(sl2, sl2);
-  float alpha, s0, s1;
-  if (whole) {
-    // S is read once and held in registers
-    uint32_t x[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(trow + kColS + 32 * c, x[c]);
-    tmem_ld_wait32(x[0]);
-#pragma unroll
-    for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
-    tc_fence_before();
-    mbar_arrive(&bar.s_free);
-    alpha = row.advance(
-        fmaxf(fmax3(max_chunk(x[0]), max_chunk(x[1]), max_chunk(x[2])), max_chunk(x[3])) * sl2, j == 0);
-    const float mu = row.reference();
-    const uint64_t negmu2 = f2_pack(-mu, -mu);
-    uint64_t acc[4] = {0, 0, 0, 0};                    // (+0.f, +0.f)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) pack_chunk(x[c], scale2, negmu2, acc[c]);
-    f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
-    // the previous tile's P V reads P and accumulates O: wait for it
-    if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (j - 1) & 1))) return false;
-    tc_fence_after();
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      tmem_st16(trow + kColP + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[c][0]));
-  } else {
-    // an edge tile: the chunks that the warp sees one by one, once for the max
-    // and once more for the weights (fewer exponentials, and few registers)
+  uint32_t x[4][32];
+  if (!whole) {
+    // an edge tile: the chunks with unseen slots are masked in tensor memory
     const RowSlots see = bar.see[threadIdx.x];
-    // 32-slot chunks of P that this tile's P V reads
-    const int chunks = (min(kBoxes, bar.tile.n_boxes - j * kBoxes) + 1) / 2;
-    uint32_t x[32];
-    float mx = -INFINITY;
-    unsigned live = 0;                 // warp-uniform
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; c < 4; ++c) {
       const uint32_t mask = see.mask(j * kBN + 32 * c);
-      if (!__any_sync(0xffffffffu, mask != 0u)) continue;
-      live |= 1u << c;
-      tmem_ld32(trow + kColS + 32 * c, x);
-      tmem_ld_wait32(x);
-      mask_chunk(x, mask);
-      mx = fmaxf(mx, max_chunk(x) * sl2);
+      if (__all_sync(0xffffffffu, mask == 0xffffffffu)) continue;
+      tmem_ld32(trow + kColS + 32 * c, x[0]);
+      tmem_ld_wait32(x[0]);
+      mask_chunk(x[0], mask);
+      tmem_st16(trow + kColS + 32 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[0][0]));
+      tmem_st16(trow + kColS + 32 * c + 16, *reinterpret_cast<uint32_t(*)[16]>(&x[0][16]));
     }
-    alpha = row.advance(mx, j == 0);
-    const float mu = row.reference();
-    const uint64_t negmu2 = f2_pack(-mu, -mu);
-    uint64_t acc = 0;
-    if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (j - 1) & 1))) return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      if ((live >> c) & 1u) {
-        tmem_ld32(trow + kColS + 32 * c, x);
-        tmem_ld_wait32(x);
-        mask_chunk(x, see.mask(j * kBN + 32 * c));
-        pack_chunk(x, scale2, negmu2, acc);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0u;
-      }
-      tmem_st16(trow + kColP + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[0]));
-    }
-    f2_unpack(acc, s0, s1);
-    tc_fence_before();
-    mbar_arrive(&bar.s_free);
+    tmem_st_wait();
   }
+  // S is read once and held in registers
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32(trow + kColS + 32 * c, x[c]);
+  tmem_ld_wait32(x[0]);
+#pragma unroll
+  for (int c = 1; c < 4; ++c) reg_tie32(x[c]);
+  tc_fence_before();
+  mbar_arrive(&bar.s_free);
+  const float alpha = row.advance(
+      fmaxf(fmax3(max_chunk(x[0]), max_chunk(x[1]), max_chunk(x[2])), max_chunk(x[3])) * sl2, j == 0);
+  const float mu = row.reference();
+  const uint64_t negmu2 = f2_pack(-mu, -mu);
+  uint64_t acc[4] = {0, 0, 0, 0};                    // (+0.f, +0.f)
+#pragma unroll
+  for (int c = 0; c < 4; ++c) pack_chunk(x[c], scale2, negmu2, acc[c]);
+  float s0, s1;
+  f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+  // the previous tile's P V reads P and accumulates O: wait for it
+  if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar.pv_done, (j - 1) & 1))) return false;
+  tc_fence_after();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    tmem_st16(trow + kColP + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[c][0]));
   row.d += s0 + s1;
   tmem_st_wait();
   if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o(trow, alpha);
