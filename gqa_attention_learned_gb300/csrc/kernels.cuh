@@ -184,7 +184,7 @@ struct WindowPrefillParams {
   int window, first_tokens;      // both <= max_kv_len, window >= 1
   int tile_tokens;               // tokens per query tile = 128 / group
   unsigned inv_group;            // ceil(2^16 / group): i / group for i < 128
-  int num_q_tiles;               // query tiles of the longest request
+  int num_tiles;                 // query tiles per KV head, at most
 };
 
 cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,

@@ -808,7 +808,11 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
   p.first_tokens = std::min(first_tokens, max_kv_len);
   p.tile_tokens = tile_tokens;
   p.inv_group = static_cast<unsigned>((65536 + group - 1) / group);
-  p.num_q_tiles = ceil_div(max_q_len, tile_tokens);
+  // each request has a tile for every tile_tokens tokens and one more at most
+  const long long tiles = std::min(static_cast<long long>(ceil_div(max_q_len, tile_tokens)) * num_seqs,
+                                   static_cast<long long>(total_q / tile_tokens) + num_seqs);
+  if (tiles * num_kv_heads > 0x7fffffffll) return SINKATTN_UNSUPPORTED;
+  p.num_tiles = static_cast<int>(tiles);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (sa::window_prefill_is_short(p)) {
     const int sms = device_sm_count();

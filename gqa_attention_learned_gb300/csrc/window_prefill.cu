@@ -175,19 +175,21 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap vmap, const WindowPrefillParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- work item: (query tile, request, KV head), later tiles (whose windows
-  // are full) first
-  const int per_tile = p.num_seqs * p.num_kv_heads;
-  const int qt = p.num_q_tiles - 1 - static_cast<int>(blockIdx.x / per_tile);
-  const int rem = static_cast<int>(blockIdx.x % per_tile);
-  const int kvh = rem % p.num_kv_heads;
-  const Request req = Request::load<kPaged>(p, rem / p.num_kv_heads);
+  // ---- work item: (query tile, KV head), a request's last tiles (whose
+  // windows are full) first
+  const int item = static_cast<int>(blockIdx.x) / p.num_kv_heads;
+  const int kvh = static_cast<int>(blockIdx.x) - item * p.num_kv_heads;
+  Walk<kPaged> walk;
+  do {
+    if (!walk.advance(p)) return;
+  } while (walk.next <= item);
+  int first;
+  const Request req = walk.request(walk.lane_of(item), first);
   if (req.bad) {
-    if (qt == 0) poison(p, kvh, req.q_start, max(req.q_len, 0), threadIdx.x, kThreads);
+    poison(p, kvh, req.q_start, max(req.q_len, 0), threadIdx.x, kThreads);
     return;
   }
-  if (qt * p.tile_tokens >= req.q_len) return;
-  const Tile tile = Tile::make<kPaged>(p, req, qt);
+  const Tile tile = Tile::make<kPaged>(p, req, cdiv(req.q_len, p.tile_tokens) - 1 - (item - first));
   const int rows = tile.tokens * p.group;
   const int n_tiles = cdiv(tile.n_boxes, kBoxes);
   const int live_threads = min(kBM, 32 * cdiv(rows, 32));
@@ -258,7 +260,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       tma_load_3d(sQ, &qmap, &bar.q_full, 0, kvh * p.group, req.q_start + tile.i0);
     }
     __syncwarp();
-    for (int j = 0; j < min(n_tiles, kKStages); ++j) load(j, 0, source_of(j));   // fresh slots
+    load(0, 0, source_of(0));
   }
   tc_fence_before();
   __syncthreads();
@@ -285,9 +287,13 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       __syncwarp();
       return true;
     };
-    int src = source_of(kKStages);
-    bool ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_full, 0));
-    ok = ok && issue_qk(0);
+    // A load costs its warp about 100 cycles a box: the second tile's are issued
+    // while the first's are on their way, the third's under the first product.
+    bool ok = n_tiles < 2 || load(1, 0, source_of(1));
+    int src = source_of(2);
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(&bar.q_full, 0)) && issue_qk(0);
+    if (ok && n_tiles > 2) ok = load(2, 0, src);
+    src = source_of(kKStages);
     for (int j = 0; ok && j + 1 < n_tiles; ++j) {
       // S of tile j has been read: compute S of tile j+1 during this softmax
       if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_free, j & 1))) { ok = false; break; }
@@ -337,10 +343,12 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     const int r = threadIdx.x;                          // row = TMEM lane
     const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float sl2 = p.scale_log2;
+    // token of row i of a tile: i / group, exact for i < 128 and group <= 128
+    auto token_of = [&](int i) { return static_cast<int>((static_cast<uint32_t>(i) * p.inv_group) >> 16); };
     RowState state;
     int tiles, whole_b, whole_c;
     {
-      const int token = r / p.group;
+      const int token = token_of(r);
       const int tile_rows = bar.tile.tokens * p.group;
       tiles = warp * 32 < tile_rows ? cdiv(bar.tile.n_boxes, kBoxes) : 0;   // none without rows
       // lanes past the rows repeat the last token
@@ -386,7 +394,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     const size_t first_row =
         static_cast<size_t>(bar.q_start + bar.tile.i0) * p.num_qo_heads + bar.kvh * p.group;
     auto row_index = [&](int i) -> long long {           // row i of the tile
-      const int tok = i / p.group;
+      const int tok = token_of(i);
       return i < rows ? static_cast<long long>(first_row + static_cast<size_t>(tok) * p.num_qo_heads + (i - tok * p.group)) : -1;
     };
     // the query buffer is free since the last QK^T completed
@@ -421,12 +429,9 @@ uint32_t window_negate_q(bool negative) { return negative ? kIdescNegateA : 0u; 
 cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                   const CUtensorMap &vmap, const WindowPrefillParams &p,
                                   cudaStream_t stream) {
-  const unsigned long long ctas =
-      static_cast<unsigned long long>(p.num_q_tiles) * p.num_seqs * p.num_kv_heads;
-  if (ctas == 0) return cudaSuccess;
-  if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-  return p.page_table ? launch_variant<true>(qmap, kmap, vmap, p, static_cast<unsigned>(ctas), stream)
-                      : launch_variant<false>(qmap, kmap, vmap, p, static_cast<unsigned>(ctas), stream);
+  const unsigned ctas = static_cast<unsigned>(p.num_tiles) * p.num_kv_heads;
+  return p.page_table ? launch_variant<true>(qmap, kmap, vmap, p, ctas, stream)
+                      : launch_variant<false>(qmap, kmap, vmap, p, ctas, stream);
 }
 
 }  // namespace sa

@@ -85,14 +85,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 
-// The i-th work item of the launch.
-__device__ __forceinline__ void locate(const WindowPrefillParams &p, int item, int &qt, int &seq, int &kvh) {
-  kvh = item % p.num_kv_heads;
-  const int rest = item / p.num_kv_heads;
-  qt = rest % p.num_q_tiles;
-  seq = rest / p.num_q_tiles;
-}
-
 template <bool kPaged, typename Sh>
 __global__ void __launch_bounds__(Sh::kThreads, 1)
 window_short_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -102,7 +94,8 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   constexpr int kThreads = Sh::kThreads, kNK = Sh::kKStages, kNV = Sh::kVStages;
   constexpr int kKBytes = Sh::kKBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int items = p.num_q_tiles * p.num_seqs * p.num_kv_heads;
+  // item i: query tile i / num_kv_heads of KV head i % num_kv_heads
+  const int items = p.num_tiles * p.num_kv_heads;
   const int stride = static_cast<int>(gridDim.x);
 
   extern __shared__ uint8_t smem_raw[];
@@ -154,18 +147,25 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     // -------------------------------------------------------------- loads
     int n = 0;                                           // tiles handed out
     bool ok = true;
+    Walk<kPaged> walk;
+    walk.advance(p);
     for (int base = static_cast<int>(blockIdx.x); ok && base < items;) {
-      // 32 items at a time, one per lane: most ragged batches have empty ones
+      // 32 items at a time, one per lane
       const long long mine = base + static_cast<long long>(lane) * stride;
-      bool valid = false, poisoned = false;
-      int qt = 0, seq = 0, kvh = 0;
+      const int tile_no = mine < items ? static_cast<int>(mine) / p.num_kv_heads : -1;
+      const int kvh = static_cast<int>(mine) - tile_no * p.num_kv_heads;
+      int qt = -1;
       Request r{};
-      if (mine < items) {
-        locate(p, static_cast<int>(mine), qt, seq, kvh);
-        r = Request::load<kPaged>(p, seq);
-        valid = !r.bad && qt * p.tile_tokens < r.q_len;
-        poisoned = r.bad && qt == 0;
+      while (true) {
+        int first;
+        const Request x = walk.request(walk.lane_of(tile_no), first);
+        if (qt < 0 && tile_no >= 0 && tile_no < walk.next) {
+          r = x;
+          qt = tile_no - first;
+        }
+        if (!__any_sync(0xffffffffu, qt < 0 && tile_no >= 0) || !walk.advance(p)) break;
       }
+      const bool valid = qt >= 0 && !r.bad, poisoned = qt >= 0 && r.bad;
       for (unsigned m = __ballot_sync(0xffffffffu, poisoned); m; m &= m - 1) {
         const int l = __ffs(m) - 1;
         poison(p, __shfl_sync(0xffffffffu, kvh, l), __shfl_sync(0xffffffffu, r.q_start, l),
@@ -394,13 +394,18 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   }
   if (bar.dead) {
     // a wait ran out: none of this CTA's tiles can be trusted
+    Walk<kPaged> walk;
+    walk.advance(p);
     for (long long item = blockIdx.x; item < items; item += stride) {
-      int qt, seq, kvh;
-      locate(p, static_cast<int>(item), qt, seq, kvh);
-      const Request r = Request::load<kPaged>(p, seq);
-      const int i0 = qt * p.tile_tokens;
-      if (!r.bad && i0 < r.q_len)
-        poison(p, kvh, r.q_start + i0, min(p.tile_tokens, r.q_len - i0), threadIdx.x, kThreads);
+      const int tile_no = static_cast<int>(item) / p.num_kv_heads;
+      while (walk.next <= tile_no)
+        if (!walk.advance(p)) return;
+      int first;
+      const Request r = walk.request(walk.lane_of(tile_no), first);
+      const int i0 = (tile_no - first) * p.tile_tokens;
+      if (!r.bad)
+        poison(p, static_cast<int>(item) - tile_no * p.num_kv_heads, r.q_start + i0,
+               min(p.tile_tokens, r.q_len - i0), threadIdx.x, kThreads);
     }
   }
 }
@@ -411,9 +416,9 @@ cudaError_t launch_variant(const CUtensorMap &qmap, const CUtensorMap &kmap,
                            cudaStream_t stream) {
   cudaError_t err = set_smem_once<window_short_kernel<kPaged, Sh>>(Sh::kSmemBytes);
   if (err != cudaSuccess) return err;
-  const long long items = static_cast<long long>(p.num_q_tiles) * p.num_seqs * p.num_kv_heads;
+  const int items = p.num_tiles * p.num_kv_heads;
   return launch_kernel(window_short_kernel<kPaged, Sh>,
-                       static_cast<unsigned>(std::min<long long>(items, num_sms)), Sh::kThreads,
+                       static_cast<unsigned>(std::min(items, num_sms)), Sh::kThreads,
                        Sh::kSmemBytes, stream, false, qmap, kmap, vmap, p);
 }
 
@@ -436,9 +441,6 @@ bool window_prefill_is_short(const WindowPrefillParams &p) { return most_boxes(p
 cudaError_t launch_window_short(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, const WindowPrefillParams &p, int num_sms,
                                 cudaStream_t stream) {
-  const long long items = static_cast<long long>(p.num_q_tiles) * p.num_seqs * p.num_kv_heads;
-  if (items == 0) return cudaSuccess;
-  if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   if (most_boxes(p) <= Three::kBoxes)
     return p.page_table ? launch_variant<true, Three>(qmap, kmap, vmap, p, num_sms, stream)
                         : launch_variant<false, Three>(qmap, kmap, vmap, p, num_sms, stream);

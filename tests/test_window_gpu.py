@@ -188,6 +188,68 @@ def test_long_windows_leave_other_rows_alone_and_flag_bad_ones():
         assert (out[~touched] == 7).all() and (lse[~touched] == 7).all()
 
 
+@pytest.mark.parametrize("window", [20, 280])
+def test_prefill_window_of_many_requests(window):
+    # 100 requests, some without tokens, one longer than the bound, one of cu_seqlens
+    # that falls back: its neighbours' rows stay right
+    rng = np.random.default_rng(6)
+    lens = [int(n) for n in rng.integers(0, 40, 100)]
+    lens[40] = 290                                       # the kernel for long windows needs long requests
+    lens[41] = 0
+    lens[70] = 310
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    total = int(cu[-1])
+    q, k, v = bf16(rng, total, 16, 64), bf16(rng, total, 1, 64), bf16(rng, total, 1, 64)
+    sinks = torch.from_numpy(rng.standard_normal(16).astype(np.float32))
+    parts = [slice(cu[b], cu[b + 1]) for b in range(100)]
+    ro, rl = _prefill_ref(([k[p] for p in parts], [v[p] for p in parts]), q, cu, [0] * 100,
+                          np64(sinks), 0.125, window, 3)
+    out, lse = sa.prefill_window(q.to(DEV), k.to(DEV), v.to(DEV),
+                                 torch.tensor(cu, dtype=torch.int32, device=DEV), sinks.to(DEV), 0.125,
+                                 300, window, 3)
+    good = np.ones(total, bool)
+    good[parts[70]] = False
+    assert torch.isnan(out[parts[70]]).all() and torch.isnan(lse[parts[70]]).all()
+    assert_out_close(out[good], ro[good])
+    assert_lse_close(lse[good], rl[good])
+    # entry 51 before entry 50: request 50 has no rows, request 51 is out of order
+    back = cu.copy()
+    back[51] = cu[50] - 5
+    out, lse = sa.prefill_window(q.to(DEV), k.to(DEV), v.to(DEV),
+                                 torch.tensor(back, dtype=torch.int32, device=DEV), sinks.to(DEV), 0.125,
+                                 300, window, 3)
+    assert torch.isnan(out[cu[50]:cu[52]]).all()
+    good[cu[50] - 5:cu[52]] = False
+    assert_out_close(out[good], ro[good])
+    assert_lse_close(lse[good], rl[good])
+
+
+@pytest.mark.parametrize("window", [100, 400])
+def test_prefill_window_of_a_request_does_not_depend_on_the_batch(window):
+    # more tiles than the persistent CTAs look up at a time
+    rng = np.random.default_rng(7)
+    lens = [int(n) for n in rng.integers(0, 300, 90)]
+    lens[5] = 450
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    total = int(cu[-1])
+    gen = torch.Generator(DEV).manual_seed(0)
+    q, k, v = (torch.randn(total, h, 64, generator=gen, device=DEV).bfloat16() for h in (64, 1, 1))
+    sinks = torch.zeros(64, device=DEV)
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+    out, lse = sa.prefill_window(q, k, v, ints(cu), sinks, 0.125, 450, window)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    for b in (0, 5, 31, 32, 50, 63, 64, 88, 89):
+        at = slice(cu[b], cu[b + 1])
+        if lens[b]:
+            # the same bound on lengths: the same kernel
+            a, c = sa.prefill_window(q[at].contiguous(), k[at].contiguous(), v[at].contiguous(),
+                                     ints([0, lens[b]]), sinks, 0.125, 450, window)
+            assert torch.equal(out[at], a) and torch.equal(lse[at], c)
+
+
 def test_windowed_calls_without_lse_and_without_keys():
     c = Paged([0, 0], 4, 1)
     q = bf16(c.rng, 2, 4, 64).to(DEV)
