@@ -184,7 +184,8 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     if (!walk.advance(p)) return;
   } while (walk.next <= item);
   int first;
-  const Request req = walk.request(walk.lane_of(item), first);
+  // the last lane with from <= item
+  const Request req = walk.request(31 - __clz(__ballot_sync(0xffffffffu, walk.from <= item)), first);
   if (req.bad) {
     poison(p, kvh, req.q_start, max(req.q_len, 0), threadIdx.x, kThreads);
     return;

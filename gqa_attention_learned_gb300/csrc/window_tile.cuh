@@ -284,12 +284,16 @@ __device__ __forceinline__ void store_rows(const WindowPrefillParams &p, uint4 *
   }
   __syncwarp();
   const int cc = lane & 7;
+  uint4 line[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int i = 4 * k + (lane >> 3);
-    const long long row = row_of(i);
-    if (row >= 0)
-      reinterpret_cast<uint4 *>(p.out + row * kHeadDim)[cc] = stage[i * 8 + (cc ^ (i & 7))];
+    line[k] = stage[i * 8 + (cc ^ (i & 7))];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const long long row = row_of(4 * k + (lane >> 3));
+    if (row >= 0) reinterpret_cast<uint4 *>(p.out + row * kHeadDim)[cc] = line[k];
   }
 }
 
