@@ -550,9 +550,6 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
       const Steps st = walk.steps(p);
       const int my_skip = w == 0 ? st.skip[0] : st.skip[kGroups - 1];
       const int key = st.key0 + w * kKeys + row;
-      const bool writes = key < walk.kv_len;
-      float *sum_to = walk.row(p) + key;
-      const float before = writes && !p.mirror ? *sum_to : 0.f;
       // tokens from this CTA's current tile to the first one that sees the key
       int ahead = key - walk.shift - st.i_start;
       int tokens_left = walk.q_len - st.i_start;
@@ -608,7 +605,14 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
       f2_unpack(acc1, c, d);
       const float sum = (a + b) + (c + d);
       if (p.mirror) sums[item * kKeys * kGroups + threadIdx.x] = sum;
-      else if (writes) *sum_to = ok ? before + sum : NAN;
+      else if (row + w * kKeys + walk.kp * kKeys * kGroups < walk.kv_len) {
+        // The key's only sum of the launch, so the order of additions is fixed;
+        // added in memory, as a value read before the loop cost its latency
+        // (2500 of 8300 cycles per pair) where no register was left for it.
+        float *to = walk.row(p) + walk.kp * kKeys * kGroups + w * kKeys + row;
+        if (ok) atomicAdd(to, sum);
+        else *to = NAN;
+      }
     }
     if (!ok) {
       // a wait ran out: none of the sums to come can be made
