@@ -377,8 +377,8 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
   if (walk.left == 0) return;                            // the whole cluster returns
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: accesses stay known to be shared memory's)
+  uint8_t *smem = smem_raw + (0u - smem_u32(smem_raw)) % 1024;
   Bars &bar = *reinterpret_cast<Bars *>(smem + kOffBars);
   auto sK = [&](int s) { return smem + kOffK + s * kTileBytes; };
   auto sQ = [&](int s) { return smem + kOffQ + s * kTileBytes; };

@@ -196,8 +196,8 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   const int live_threads = min(kBM, 32 * cdiv(rows, 32));
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: accesses stay known to be shared memory's)
+  uint8_t *smem = smem_raw + (0u - smem_u32(smem_raw)) % 1024;
   Bars &bar = *reinterpret_cast<Bars *>(smem + kOffBars);
   uint8_t *sQ = smem + kOffQ;
   auto sK = [&](int s) { return smem + kOffK + s * kTileBytes; };

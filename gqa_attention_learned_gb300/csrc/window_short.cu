@@ -99,8 +99,8 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   const int stride = static_cast<int>(gridDim.x);
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: accesses stay known to be shared memory's)
+  uint8_t *smem = smem_raw + (0u - smem_u32(smem_raw)) % 1024;
   Bars &bar = *reinterpret_cast<Bars *>(smem + Sh::kOffBars);
   auto sQ = [&](int n) { return smem + n % kNK * Sh::kKStageBytes; };     // of tile n
   auto sK = [&](int n) { return sQ(n) + kQBytes; };
