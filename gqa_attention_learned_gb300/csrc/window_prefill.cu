@@ -18,18 +18,19 @@
 // first tokens, then boxes from the run's start on; tiles take 8 boxes = 128
 // slots each, so the two parts share tiles and nothing between them is
 // copied or looked up.  The last tile's MMAs cover its own boxes only.
-// Rows see at most two slot ranges.  Tiles that all rows of a warp see whole,
-// most of them in a long window, take a path without masks; on the others the
-// warp goes by chunks of 32 slots and skips those that none of its rows sees.
+// Rows see at most two slot ranges.  Most tiles of a long window are seen whole
+// by all rows of a warp; on the others the warp first masks the chunks of 32 slots
+// that some row does not see, in tensor memory, and then goes the same way.
 // Warp roles, barriers and the softmax are those of plain prefill: warp 4
 // loads Q and K and issues S = Q K^T, warp 5 loads V and issues O += P V,
 // warps 0..3 run the online softmax, one thread per row, between them.
 //
-// Measured: 600 us for 4 chunks of 2048 new tokens on up to 14336 cached ones
-// with window 4096 (64 / 8 heads): 853 TFLOP/s of the pairs that are seen, tensor
-// pipe 51%, exponential unit 38%, issue slots 49% busy: as in plain prefill the
-// tile's chain of S, softmax, P V binds, here with an edge at both ends and
-// the start and end of a CTA every 33 tiles.
+// Measured (64 / 8 heads): 568 us for 4 chunks of 2048 new tokens on up to 14336
+// cached ones with window 4096, 901 TFLOP/s of the pairs that are seen: tensor pipe
+// 52%, exponential unit 40%, issue slots 50% busy; as in plain prefill the tile's
+// chain of S, softmax, P V binds.  Few tiles per CTA cost more: 59 us for 7.6k
+// tokens of 16 / 2 heads with window 1023 (16.5 us by the tensor peak), where a CTA
+// lasts 30k cycles, 2.4k for each of its 9 tiles and the rest for its start and end.
 
 #include "window_tile.cuh"
 
