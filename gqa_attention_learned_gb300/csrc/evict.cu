@@ -26,8 +26,8 @@
 //   rows of this batch or earlier ones.
 // The least it can move: 4 bytes of mass per key, 520 bytes per kept key.
 
-#include "kernels.cuh"
-#include "ptx.cuh"
+#include "bounded.cuh"
+#include "bounded_ptx.cuh"
 
 #include <cooperative_groups.h>
 

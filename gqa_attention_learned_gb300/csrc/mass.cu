@@ -39,8 +39,8 @@
 // next ones on their way (225 us), 64 at once (285, spills), both key tiles of a
 // pair by each thread, lse read once for both (239).
 
-#include "kernels.cuh"
-#include "ptx.cuh"
+#include "bounded.cuh"
+#include "bounded_ptx.cuh"
 
 #include <cooperative_groups.h>
 

@@ -3,7 +3,7 @@
 // include/sinkattn.h.  Nothing here allocates device memory or synchronises.
 
 #include "sinkattn.h"
-#include "kernels.cuh"
+#include "bounded.cuh"
 
 #include <cudaTypedefs.h>
 

@@ -29,8 +29,8 @@
 // one page per warp and 4 CTAs per SM 10.4 us for the 64 and 52.9 us for the 8;
 // more pages per warp, or more CTAs with fewer registers, are slower in both.
 
-#include "kernels.cuh"
-#include "ptx.cuh"
+#include "bounded.cuh"
+#include "bounded_ptx.cuh"
 
 #include <algorithm>
 #include <cmath>

@@ -2,8 +2,8 @@
 // needs, the slots that a row sees, and the arithmetic on chunks of scores.
 #pragma once
 
-#include "kernels.cuh"
-#include "ptx.cuh"
+#include "bounded.cuh"
+#include "bounded_ptx.cuh"
 
 #include <cmath>
 
