@@ -222,6 +222,10 @@ DecodePlan plan_decode(int batch, int q_len, int num_qo_heads, int num_kv_heads,
   return plan;
 }
 
+// A bound on lengths as the windowed kernels take it: "no bound" is the largest
+// that they can still round up to whole pages and tiles.
+int longest(int bound) { return std::min(bound, 0x7fff0000); }
+
 // Windowed decode: CTAs of 8 or 16 query heads over the pages with a visible
 // key; split only while the CTAs do not fill the GPU twice, and into chunks of
 // at least kWindowMinPages pages.
@@ -739,9 +743,9 @@ int sinkattn_decode_window(const void *q, const void *k_cache, const void *v_cac
   p.num_pages = num_pages;
   p.num_splits = plan.num_splits;
   p.pages_per_chunk = plan.pages_per_chunk;
-  p.window = std::min(window, std::max(max_kv_len, 1));
-  p.first_tokens = std::min(first_tokens, max_kv_len);
-  p.max_kv_len = max_kv_len;
+  p.max_kv_len = longest(max_kv_len);
+  p.window = std::min(window, std::max(p.max_kv_len, 1));
+  p.first_tokens = std::min(first_tokens, p.max_kv_len);
   return cuda_status(sa::launch_window_decode(p, static_cast<cudaStream_t>(stream),
                                               sa::programmatic_for(launch_flags)),
                      "windowed decode launch");
@@ -798,14 +802,14 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
   p.num_seqs = num_seqs;
   p.total_q = total_q;
   p.max_q_len = max_q_len;
-  p.max_kv_len = max_kv_len;
+  p.max_kv_len = longest(max_kv_len);
   p.num_qo_heads = num_qo_heads;
   p.num_kv_heads = num_kv_heads;
   p.group = group;
   p.max_pages_per_seq = max_pages_per_seq;
   p.num_pages = num_pages;
-  p.window = std::min(window, std::max(max_kv_len, 1));
-  p.first_tokens = std::min(first_tokens, max_kv_len);
+  p.window = std::min(window, std::max(p.max_kv_len, 1));
+  p.first_tokens = std::min(first_tokens, p.max_kv_len);
   p.tile_tokens = tile_tokens;
   p.inv_group = static_cast<unsigned>((65536 + group - 1) / group);
   // each request has a tile for every tile_tokens tokens and one more at most

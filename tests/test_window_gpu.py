@@ -60,6 +60,28 @@ def test_a_window_without_bound_is_decode():
         assert_lse_close(b[1], np64(a[1]))
 
 
+@pytest.mark.parametrize("window,first", [(20, 3), (2**40, 0), (20, 2**40), (2**40, 2**40)])
+def test_lengths_without_bound(window, first):
+    # bounds past any int mean none; nothing else changes
+    c = Paged([300, 17], 8, 2)
+    paged, sinks = c.paged(), c.sinks.to(DEV)
+    q = bf16(c.rng, 140, 8, 64).to(DEV)
+    cu = torch.tensor([0, 130, 140], dtype=torch.int32, device=DEV)
+    none = 2**40
+    ours = (min(window, 300), min(first, 300))
+    for free, bound in (
+            (sa.decode_window(q[:2], *paged, sinks, c.scale, none, window, first),
+             sa.decode_window(q[:2], *paged, sinks, c.scale, 300, *ours)),
+            (sa.prefill_paged_window(q, cu, *paged, sinks, c.scale, none, none, window, first),
+             sa.prefill_paged_window(q, cu, *paged, sinks, c.scale, 130, 300, *ours)),
+            (sa.prefill_window(q, *(x[0][:140].to(DEV) for x in (c.k, c.v)), cu, sinks, c.scale, none, window,
+                               first),
+             sa.prefill_window(q, *(x[0][:140].to(DEV) for x in (c.k, c.v)), cu, sinks, c.scale, 130, *ours))):
+        assert torch.isfinite(bound[0]).all()
+        assert_out_close(free[0], np64(bound[0]))
+        assert_lse_close(free[1], np64(bound[1]))
+
+
 def test_decode_window_masked_heads_and_zero_scale():
     # a sink of -inf on some heads; a request that sees nothing; scale 0 and below
     c = Paged([40, 0, 200], 8, 2)
