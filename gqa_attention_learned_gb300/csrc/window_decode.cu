@@ -289,8 +289,9 @@ window_decode_kernel(const WindowDecodeParams p) {
       acc[2] += wt * ov.z;
       acc[3] += wt * ov.w;
     }
-    const float inv = failed ? NAN : den > 0.f ? 1.f / den : 0.f;
-    const float lse2 = failed ? NAN : den > 0.f ? mx + lg2(den) : -INFINITY;
+    // (a NaN score leaves den NaN, and so the row and its lse)
+    const float inv = failed ? NAN : den == 0.f ? 0.f : 1.f / den;
+    const float lse2 = failed ? NAN : den == 0.f ? -INFINITY : mx + lg2(den);
     const size_t row = head0 + r;
     if (nchunks == 1) {
       uint2 packed;
@@ -320,7 +321,7 @@ window_decode_kernel(const WindowDecodeParams p) {
     const int r = item / (kHeadDim / 4), dq = (item % (kHeadDim / 4)) * 4;
     const size_t row = head0 + r;
     float mx = -INFINITY, den = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    bool poisoned = false;       // a chunk met a page outside the pool
+    bool poisoned = false;       // a chunk met a page outside the pool, or a NaN score
     for (int c = 0; c < nchunks; ++c) {
       const float lc = __ldcg(p.ws_lse + c * stride + row);
       poisoned = poisoned || lc != lc;
@@ -336,12 +337,12 @@ window_decode_kernel(const WindowDecodeParams p) {
       acc[3] = acc[3] * a + wt * ov.w;
       mx = nm;
     }
-    const float inv = poisoned ? NAN : den > 0.f ? 1.f / den : 0.f;
+    const float inv = poisoned ? NAN : den == 0.f ? 0.f : 1.f / den;
     uint2 packed;
     packed.x = pack_bf16(acc[0] * inv, acc[1] * inv);
     packed.y = pack_bf16(acc[2] * inv, acc[3] * inv);
     *reinterpret_cast<uint2 *>(p.out + row * kHeadDim + dq) = packed;
-    if (dq == 0 && p.lse) p.lse[row] = poisoned ? NAN : (den > 0.f ? (mx + lg2(den)) * kLn2 : -INFINITY);
+    if (dq == 0 && p.lse) p.lse[row] = poisoned ? NAN : (den == 0.f ? -INFINITY : (mx + lg2(den)) * kLn2);
   }
   if (threadIdx.x == 0) *counter = 0;
 }

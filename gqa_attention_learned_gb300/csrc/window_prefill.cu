@@ -401,9 +401,9 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     };
     // the query buffer is free since the last QK^T completed
     store_rows(p, reinterpret_cast<uint4 *>(sQ) + (r - lane) * 8, x,
-               failed ? NAN : d > 0.f ? 1.f / d : 0.f, [&](int i) { return row_index(r - lane + i); });
+               failed ? NAN : d == 0.f ? 0.f : 1.f / d, [&](int i) { return row_index(r - lane + i); });
     if (r < rows && p.lse)
-      p.lse[row_index(r)] = failed ? NAN : (d > 0.f ? (m + lg2(d)) * kLn2 : -INFINITY);
+      p.lse[row_index(r)] = failed ? NAN : (d == 0.f ? -INFINITY : (m + lg2(d)) * kLn2);
     return;
   }
   tc_fence_before();

@@ -379,11 +379,11 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       };
       // P V has read V: the stage takes the rows on their way out, then the next
       // copy (written by the asynchronous proxy)
-      store_rows(p, reinterpret_cast<uint4 *>(sV(n)) + (r - lane) * 8, x, bad ? NAN : d > 0.f ? 1.f / d : 0.f,
+      store_rows(p, reinterpret_cast<uint4 *>(sV(n)) + (r - lane) * 8, x, bad ? NAN : d == 0.f ? 0.f : 1.f / d,
                  [&](int i) { return row_index(r - lane + i); });
       fence_proxy_async_smem();
       mbar_arrive(&bar.v_empty[n % kNV]);
-      if (r < rows && p.lse) p.lse[row_index(r)] = bad ? NAN : d > 0.f ? (mu + lg2(d)) * kLn2 : -INFINITY;
+      if (r < rows && p.lse) p.lse[row_index(r)] = bad ? NAN : d == 0.f ? -INFINITY : (mu + lg2(d)) * kLn2;
     }
   }
   tc_fence_before();

@@ -82,6 +82,28 @@ def test_lengths_without_bound(window, first):
         assert_lse_close(free[1], np64(bound[1]))
 
 
+@pytest.mark.parametrize("window", [40, 260])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_keys_that_are_not_finite_spoil_the_rows_that_see_them(window, what):
+    # key 20: the output and the lse of a row that sees it are NaN (an infinite
+    # score is one too: inf - inf), in one chunk or several
+    c = Paged([300], 4, 1)
+    k, v, table, lens = c.paged()
+    k[table[0, 1].long(), 0, 4, 0] = what
+    sinks = c.sinks.to(DEV)
+    q = bf16(c.rng, 300, 4, 64).abs().to(DEV)            # no score of -inf
+    seen = torch.tensor(np.stack([bounded.visible(i, 300, window, 0) for i in range(300)])[:, 20], device=DEV)
+    cu = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+    out, lse = sa.prefill_paged_window(q, cu, k, v, table, lens, sinks, c.scale, 300, 300, window)
+    assert torch.isnan(lse[seen]).all() and torch.isfinite(lse[~seen]).all()
+    assert torch.isnan(out[seen]).all() and torch.isfinite(out[~seen]).all()
+    for splits in (1, 5):
+        out, lse = sa.decode_window(q[:1], k, v, table, lens, sinks, c.scale, 300, 300, num_splits=splits)
+        assert torch.isnan(out).all() and torch.isnan(lse).all()
+        out, lse = sa.decode_window(q[:1], k, v, table, lens, sinks, c.scale, 300, 200, num_splits=splits)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
 def test_decode_window_masked_heads_and_zero_scale():
     # a sink of -inf on some heads; a request that sees nothing; scale 0 and below
     c = Paged([40, 0, 200], 8, 2)
