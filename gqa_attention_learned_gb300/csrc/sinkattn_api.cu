@@ -934,8 +934,8 @@ int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_se
   if (p.num_sms == 0) return fail_msg("no CUDA device (SM count query failed)");
   // Many query tiles per key pair: a pair and its mirror image per cluster,
   // with as many CTAs to share them as fill the GPU one and a half times (4
-  // prompts of up to 4096 tokens, 64 / 8 heads: 241 us with 2, 254 with 4, 278
-  // with 8, which each start and end more often).
+  // prompts of up to 4096 tokens, 64 / 8 heads: 217 us with 2, 329 with 1; 228
+  // with 4, 247 with 8, which each start and end more often).
   const long long tiles = ceil_div(max_q_len, p.tile_tokens);
   p.mirror = tiles >= kMassTiles;
   if (p.mirror) {
