@@ -6,7 +6,7 @@
 //
 // select: a cluster of CTAs per (request, KV head), each with a contiguous
 //   share of the keys, whose weights it keeps in shared memory (what exceeds
-//   100 KB is read again, from L2, in each pass).  A radix select over
+//   104 KB is read again, from L2, in each pass).  A radix select over
 //   the weights' order-preserving bits (11 + 11 + 10 bits; histograms in shared
 //   memory, joined in the first CTA's through distributed shared memory) gives
 //   the weight of the last key that stays and how many of its equals stay,
@@ -19,7 +19,7 @@
 //   keys, 8 heads, cut to 1024: 53 us, 4.5 TB/s, against 60 us with a second
 //   kernel); where a cluster shares a row a second kernel, launched under the
 //   first one's end, moves K, V and mass in CTAs of their own with 64 KB in
-//   flight (8 rows of up to 131072 keys cut to 8192: 97 us, half of it the
+//   flight (8 rows of up to 131072 keys cut to 8192: 95 us, 40% of it the
 //   selection's 5 passes over each weight, bound by their instructions).  In
 //   place is safe because the r-th kept key has index >= r: a batch of rows is
 //   read whole before any of it is written, and a write to slot r can only hit
@@ -45,7 +45,7 @@ constexpr int kBins = 2048;
 constexpr int kMaxSplit = 8;             // CTAs per (request, KV head)
 constexpr int kKeysPerCta = 4096;        // keys per CTA at least, where a row has more than one
 constexpr int kGroup = 128;              // keys a warp looks at together, four per lane
-constexpr int kMaxCached = 1536;         // weights per warp in shared memory
+constexpr int kMaxCached = 1664;         // weights per warp in shared memory: what two CTAs per SM hold
 constexpr int kMoveThreads = 1024;
 constexpr int kMoveRows = 4;             // rows in flight per thread and batch
 
@@ -432,7 +432,7 @@ evict_move_kernel(const EvictParams p) {
 cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream) {
   const unsigned long long units = static_cast<unsigned long long>(p.batch) * p.num_kv_heads;
   if (units == 0) return cudaSuccess;
-  // CTAs per row: as many as are resident at once (two per SM with 100 KB of
+  // CTAs per row: as many as are resident at once (two per SM with 104 KB of
   // weights each), of kKeysPerCta keys at least
   p.split = 1;
   while (p.split < kMaxSplit && p.max_kv_len > kKeysPerCta * p.split &&
@@ -440,7 +440,7 @@ cudaError_t launch_evict(EvictParams &p, int num_sms, cudaStream_t stream) {
     p.split *= 2;
   if (3 * units > 0x7fffffffull || p.split * units > 0x7fffffffull)
     return cudaErrorInvalidConfiguration;
-  // every weight of a CTA's share where 100 KB hold them
+  // every weight of a CTA's share where 104 KB hold them
   const long long share = cdiv(p.max_kv_len, p.split * kSelectWarps);
   p.cached = static_cast<int>(std::min<long long>((share + kGroup - 1) / kGroup * kGroup, kMaxCached));
   if (p.split == 1) {
