@@ -547,7 +547,7 @@ def decode_window(q, k_cache, v_cache, page_table, kv_lens, sinks, scale, max_kv
             ws_ptr, ws_len = workspace.data_ptr(), workspace.nbytes
         status = load().sinkattn_decode_window(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-            page_table.shape[1], kv_lens.data_ptr(), sinks.data_ptr(), scale, window, first,
+            page_table.shape[1], kv_lens.data_ptr(), sinks.data_ptr(), float(scale), window, first,
             out.data_ptr(), None if lse is None else lse.data_ptr(), batch, hq, hkv, d, page,
             num_pages, max_kv_len, num_splits, ws_ptr, ws_len or 0,
             0 if programmatic is None else _launch_flags(programmatic), _raw_stream(dev))
@@ -562,25 +562,31 @@ def prefill_window(q, k, v, cu_seqlens, sinks, scale, max_seqlen, window, first_
     i - window + 1 .. i and the sequence's `first_tokens` first ones (up to
     itself).  Returns (out [T, Hq, 64], lse [T, Hq] or None)."""
     dev = q.device
-    _want(q, "q", torch.bfloat16, 3)
-    _want(k, "k", torch.bfloat16, 3, dev)
-    _want(v, "v", torch.bfloat16, 3, dev)
-    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, dev)
-    _want(sinks, "sinks", torch.float32, 1, dev)
+    if not (_is(q, _BF16, 3, dev) and _is(k, _BF16, 3, dev) and _is(v, _BF16, 3, dev)
+            and _is(cu_seqlens, _I32, 1, dev) and _is(sinks, _F32, 1, dev) and dev.type == "cuda"):
+        _want(q, "q", _BF16, 3)
+        _want(k, "k", _BF16, 3, dev)
+        _want(v, "v", _BF16, 3, dev)
+        _want(cu_seqlens, "cu_seqlens", _I32, 1, dev)
+        _want(sinks, "sinks", _F32, 1, dev)
     total, hq, d = q.shape
     hkv = k.shape[1]
+    num_seqs = cu_seqlens.shape[0] - 1
     _shape(k, "k", (total, hkv, d))
     _shape(v, "v", k.shape)
     _shape(sinks, "sinks", (hq,))
-    if cu_seqlens.numel() < 1:
+    if num_seqs < 0:
         raise ValueError("cu_seqlens must hold num_seqs + 1 entries")
     window, first = _size(window, "window", 1), _size(first_tokens, "first_tokens")
+    max_seqlen = _size(max_seqlen, "max_seqlen")
     with _at(dev, stream):
         out, lse = _rows_out(q, out, lse, want_lse)
-        _check("sinkattn_prefill_window", load().sinkattn_prefill_window(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), cu_seqlens.numel() - 1, total,
-            _size(max_seqlen, "max_seqlen"), _ptr(sinks), float(scale), window, first, _ptr(out),
-            _ptr(lse), hq, hkv, d, _raw_stream(q.device)))
+        status = load().sinkattn_prefill_window(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), num_seqs, total,
+            max_seqlen, sinks.data_ptr(), float(scale), window, first, out.data_ptr(), _ptr(lse),
+            hq, hkv, d, _raw_stream(dev))
+        if status:
+            _check("sinkattn_prefill_window", status)
     return out, lse
 
 
@@ -590,35 +596,42 @@ def prefill_paged_window(q, cu_seqlens_q, k_cache, v_cache, page_table, kv_lens,
     """`prefill_paged` with a sliding window (see `prefill_window`; positions
     count from the request's first cached key)."""
     dev = q.device
-    _want(q, "q", torch.bfloat16, 3)
-    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
+    if not (_is(q, _BF16, 3, dev) and _is(cu_seqlens_q, _I32, 1, dev) and _is(sinks, _F32, 1, dev)):
+        _want(q, "q", _BF16, 3)
+        _want(cu_seqlens_q, "cu_seqlens_q", _I32, 1, dev)
+        _want(sinks, "sinks", _F32, 1, dev)
     total, hq, d = q.shape
-    _paged_args(dev, cu_seqlens_q.numel() - 1, page_table, kv_lens, k_cache, v_cache)
-    _want(sinks, "sinks", torch.float32, 1, dev)
+    num_seqs = cu_seqlens_q.shape[0] - 1
+    _paged_args(dev, num_seqs, page_table, kv_lens, k_cache, v_cache)
     _shape(sinks, "sinks", (hq,))
     num_pages, hkv, page, d2 = k_cache.shape
     if d2 != d:
         raise ValueError("k_cache and q disagree in head_dim")
     window, first = _size(window, "window", 1), _size(first_tokens, "first_tokens")
+    max_q_len, max_kv_len = _size(max_q_len, "max_q_len"), _size(max_kv_len, "max_kv_len")
     with _at(dev, stream):
         out, lse = _rows_out(q, out, lse, want_lse)
-        _check("sinkattn_prefill_paged_window", load().sinkattn_prefill_paged_window(
-            _ptr(q), _ptr(cu_seqlens_q), cu_seqlens_q.numel() - 1, total,
-            _size(max_q_len, "max_q_len"), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
-            page_table.shape[1], _ptr(kv_lens), num_pages, _size(max_kv_len, "max_kv_len"),
-            _ptr(sinks), float(scale), window, first, _ptr(out), _ptr(lse), hq, hkv, d, page,
-            _raw_stream(q.device)))
+        status = load().sinkattn_prefill_paged_window(
+            q.data_ptr(), cu_seqlens_q.data_ptr(), num_seqs, total, max_q_len, k_cache.data_ptr(),
+            v_cache.data_ptr(), page_table.data_ptr(), page_table.shape[1], kv_lens.data_ptr(),
+            num_pages, max_kv_len, sinks.data_ptr(), float(scale), window, first, out.data_ptr(),
+            _ptr(lse), hq, hkv, d, page, _raw_stream(dev))
+        if status:
+            _check("sinkattn_prefill_paged_window", status)
     return out, lse
 
 
 def _mass_args(q, k_cache, page_table, kv_lens, lse, mass, batch):
     dev = q.device
-    _want(q, "q", torch.bfloat16, 3)
+    if not (_is(q, _BF16, 3, dev) and _is(lse, _F32, 2, dev) and _is(mass, _F32, 3, dev)):
+        _want(q, "q", _BF16, 3)
+        _want(lse, "lse", _F32, 2, dev)
+        _want(mass, "mass", _F32, 3, dev)
     _paged_args(dev, batch, page_table, kv_lens, k_cache)
-    _want(lse, "lse", torch.float32, 2, dev)
-    _shape(lse, "lse", q.shape[:2])
-    _want(mass, "mass", torch.float32, 3, dev)
-    _shape(mass, "mass", (batch, k_cache.shape[1], mass.shape[2]))
+    if lse.shape != q.shape[:2]:
+        _shape(lse, "lse", q.shape[:2])
+    if mass.shape[0] != batch or mass.shape[1] != k_cache.shape[1]:
+        raise ValueError(f"mass must be [{batch}, {k_cache.shape[1]}, ...], got {list(mass.shape)}")
     if k_cache.shape[3] != q.shape[2]:
         raise ValueError("k_cache and q disagree in head_dim")
 
