@@ -194,7 +194,12 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
           break;
         }
         if (lane == 0) {
-          bar.work[n % kNV] = w;                         // published by the arrival below
+          // for the softmax warps by the arrival on info, for the products' by
+          // k_full's.  (Not for both by k_full: its stage may be filled twice more
+          // while the softmax warps are behind; this slot's next arrival needs
+          // them to have taken this one.)
+          bar.work[n % kNV] = w;
+          mbar_arrive(&bar.info[n % kSlots]);
           const uint32_t bytes = __popc(boxes) * kBoxBytes;
           mbar_arrive_expect_tx(k_full, p.tile_tokens * p.group * kHeadDim * 2 + bytes);
           mbar_arrive_expect_tx(v_full, bytes);
@@ -219,6 +224,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
         break;
       if (lane == 0) {
         bar.work[n % kNV].stop = 1;
+        mbar_arrive(&bar.info[n % kSlots]);
         mbar_arrive(&bar.k_full[n % kNK]);
       }
       __syncwarp();
@@ -229,10 +235,6 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint32_t tS = tmem + slot * Sh::kSlotCols;
     for (int n = slot, k = 0;; n += kSlots, ++k) {
       if (!wait(&bar.k_full[n % kNK], n / kNK)) break;
-      // hands the geometry on: the softmax warps cannot wait for k_full, whose
-      // stage may be filled twice more while they store the previous tile
-      if (lane == 0) mbar_arrive(&bar.info[slot]);
-      __syncwarp();
       if (bar.work[n % kNV].stop) break;
       const Tile tile = bar.work[n % kNV].tile;
       if (k > 0 && !wait(&bar.free[slot], k - 1)) break;
@@ -272,28 +274,37 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     const int row_skip = p.num_qo_heads - p.group;       // from a token's last row to the next one's first
     const float sl2 = p.scale_log2;
     const uint64_t scale2 = f2_pack(sl2, sl2);
-    for (int n = slot, k = 0;; n += kSlots, ++k) {
-      if (!wait(&bar.info[slot], k)) break;              // the geometry
+    // What a tile's softmax needs to know; false: no further tile, or a wait ran out.
+    struct Geometry {
+      RowSlots see;
+      int pieces, lead, edges;
+      float sink;
+    };
+    auto look = [&](int n, int k, Geometry &geo) -> bool {
+      if (!wait(&bar.info[slot], k)) return false;
       const Work &w = bar.work[n % kNV];
-      if (w.stop) break;
-      const Tile tile = w.tile;
-      const bool bad = w.bad != 0;
-      const int rows = tile.tokens * p.group;
-      const int head = w.kvh * p.group + in_group;
-      const size_t first_row =
-          static_cast<size_t>(w.req.q_start + tile.i0) * p.num_qo_heads + w.kvh * p.group;
+      if (w.stop) return false;
+      const Tile &tile = w.tile;
       // lanes past the rows repeat the last token
-      const RowSlots see = tile.row(p, tile.pos0 + min(token, tile.tokens - 1));
-      const float sink = r < rows ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
+      geo.see = tile.row(p, tile.pos0 + min(token, tile.tokens - 1));
+      geo.sink = r < tile.tokens * p.group ? __ldg(p.sinks + w.kvh * p.group + in_group) * kLog2e : -INFINITY;
       // Pieces of 16 slots.  Away from a request's ends only the first one or two
       // of the run, the last one or two, and the first tokens' can hold slots
       // that some row does not see; elsewhere all are taken as such edges.
-      const int pieces = tile.n_boxes;
-      const uint32_t full = __reduce_and_sync(0xffffffffu, full_pieces(see));
-      int lead = tile.first_boxes + ((full >> (tile.first_boxes + 1)) & 1u ? 1 : 2);
-      int edges = lead + ((full >> max(pieces - 2, 0)) & 1u ? 1 : 2);
-      const uint32_t inner = low_bits(pieces - (edges - lead)) & ~low_bits(lead);
-      if (edges > pieces || (full & inner) != inner) lead = edges = pieces;
+      geo.pieces = tile.n_boxes;
+      const uint32_t full = __reduce_and_sync(0xffffffffu, full_pieces(geo.see));
+      geo.lead = tile.first_boxes + ((full >> (tile.first_boxes + 1)) & 1u ? 1 : 2);
+      geo.edges = geo.lead + ((full >> max(geo.pieces - 2, 0)) & 1u ? 1 : 2);
+      const uint32_t inner = low_bits(geo.pieces - (geo.edges - geo.lead)) & ~low_bits(geo.lead);
+      if (geo.edges > geo.pieces || (full & inner) != inner) geo.lead = geo.edges = geo.pieces;
+      return true;
+    };
+    Geometry geo;
+    bool more = look(slot, 0, geo);
+    for (int n = slot, k = 0; more; n += kSlots, ++k) {
+      const int pieces = geo.pieces, lead = geo.lead, edges = geo.edges;
+      const RowSlots see = geo.see;
+      const float sink = geo.sink;
       if (!wait(&bar.s_full[slot], k)) break;
       tc_fence_after();
       // several pieces at a time, straight-line code: `at(u)` is the u-th piece
@@ -365,6 +376,19 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bar.p_full[slot]);
+      // while P V is made: lse, and the next tile's geometry (its K takes this
+      // tile's place, so it is known by now)
+      const Work &w = bar.work[n % kNV];
+      const bool bad = w.bad != 0;
+      const int rows = w.tile.tokens * p.group;
+      const size_t first_row =
+          static_cast<size_t>(w.req.q_start + w.tile.i0) * p.num_qo_heads + w.kvh * p.group;
+      auto row_index = [&](int i) -> long long {         // row i of the tile
+        return i < rows ? static_cast<long long>(first_row + static_cast<size_t>(token_of(i)) * row_skip + i) : -1;
+      };
+      if (r < rows && p.lse) p.lse[row_index(r)] = bad ? NAN : d == 0.f ? -INFINITY : (mu + lg2(d)) * kLn2;
+      const float inv = bad ? NAN : d == 0.f ? 0.f : 1.f / d;
+      more = look(n + kSlots, k + 1, geo);
       if (!wait(&bar.o_full[slot], k)) break;
       tc_fence_after();
 #pragma unroll
@@ -374,16 +398,12 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       for (int i = 0; i < 4; ++i) reg_tie16(x[i]);
       tc_fence_before();
       mbar_arrive(&bar.free[slot]);
-      auto row_index = [&](int i) -> long long {         // row i of the tile
-        return i < rows ? static_cast<long long>(first_row + static_cast<size_t>(token_of(i)) * row_skip + i) : -1;
-      };
       // P V has read V: the stage takes the rows on their way out, then the next
       // copy (written by the asynchronous proxy)
-      store_rows(p, reinterpret_cast<uint4 *>(sV(n)) + (r - lane) * 8, x, bad ? NAN : d == 0.f ? 0.f : 1.f / d,
+      store_rows(p, reinterpret_cast<uint4 *>(sV(n)) + (r - lane) * 8, x, inv,
                  [&](int i) { return row_index(r - lane + i); });
       fence_proxy_async_smem();
       mbar_arrive(&bar.v_empty[n % kNV]);
-      if (r < rows && p.lse) p.lse[row_index(r)] = bad ? NAN : d == 0.f ? -INFINITY : (mu + lg2(d)) * kLn2;
     }
   }
   tc_fence_before();
