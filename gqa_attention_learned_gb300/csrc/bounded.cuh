@@ -47,6 +47,7 @@ struct WindowDecodeParams {
   int head_blocks;                 // CTAs per (request, KV head, chunk)
   int num_pages, num_splits, pages_per_chunk;
   int window, first_tokens, max_kv_len;   // window and first_tokens <= max_kv_len
+  int num_sms;
 };
 
 int window_decode_ctas_per_sm();

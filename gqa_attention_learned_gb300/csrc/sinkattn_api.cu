@@ -746,6 +746,7 @@ int sinkattn_decode_window(const void *q, const void *k_cache, const void *v_cac
   p.max_kv_len = longest(max_kv_len);
   p.window = std::min(window, std::max(p.max_kv_len, 1));
   p.first_tokens = std::min(first_tokens, p.max_kv_len);
+  p.num_sms = sms;
   return cuda_status(sa::launch_window_decode(p, static_cast<cudaStream_t>(stream),
                                               sa::programmatic_for(launch_flags)),
                      "windowed decode launch");

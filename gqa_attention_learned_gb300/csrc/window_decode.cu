@@ -24,10 +24,10 @@
 // last CTA of a request to finish, in chunk order (as in plain decode).
 //
 // Measured (64 / 8 heads, replayed from a graph): one request of window 128
-// 6.3 us, 64 requests 12.5 us (2.6 us at the copy bandwidth: two waves of loads
-// that depend on one another), 8 requests of window 16384 49 us (5.4 TB/s).  With
-// one page per warp and 4 CTAs per SM 10.4 us for the 64 and 52.9 us for the 8;
-// more pages per warp, or more CTAs with fewer registers, are slower in both.
+// 6.3 us, 64 requests 10.4 us (2.6 us at the copy bandwidth: two waves of loads
+// that depend on one another), 8 requests of window 16384 50 us (5.4 TB/s; 52.7
+// with one page in flight and 4 CTAs per SM).  Three pages in flight and 2 CTAs
+// per SM, 2 warps per CTA, or more CTAs with fewer registers are slower.
 
 #include "bounded.cuh"
 #include "bounded_ptx.cuh"
@@ -39,8 +39,8 @@ namespace sa {
 namespace {
 
 constexpr int kNW = 4;                       // warps per CTA
-constexpr int kCtasPerSm = 3;
-constexpr int kAhead = 2;                    // pages in flight per warp
+constexpr int kCtasPerSm = 3;                // with two pages in flight per warp; four with one
+constexpr int kFewPages = 8 * kNW;           // pages per CTA that count as few
 constexpr int kPieces = kHeadDim * 2 / 16;   // 16-byte pieces of a row
 constexpr int kStride = kHeadDim + 4;        // floats per joined row
 
@@ -73,8 +73,8 @@ struct Page {
   uint4 v[4];         // keys 2t, 2t + 1, 2t + 8, 2t + 9, piece g
 };
 
-template <int NB>       // 8-head blocks per CTA: 1 or 2
-__global__ void __launch_bounds__(kNW * 32, kCtasPerSm)
+template <int NB, int kAhead>       // 8-head blocks per CTA, pages in flight per warp: 1 or 2
+__global__ void __launch_bounds__(kNW * 32, kCtasPerSm + 2 - kAhead)
 window_decode_kernel(const WindowDecodeParams p) {
   constexpr int kRows = 8 * NB;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -347,12 +347,12 @@ window_decode_kernel(const WindowDecodeParams p) {
   if (threadIdx.x == 0) *counter = 0;
 }
 
-template <int NB>
+template <int NB, int kAhead>
 cudaError_t launch_variant(const WindowDecodeParams &p, cudaStream_t stream, bool programmatic) {
   const unsigned long long ctas =
       static_cast<unsigned long long>(p.num_splits) * p.batch * p.num_kv_heads * p.head_blocks;
   if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-  return launch_kernel(window_decode_kernel<NB>, static_cast<unsigned>(ctas), kNW * 32, 0, stream,
+  return launch_kernel(window_decode_kernel<NB, kAhead>, static_cast<unsigned>(ctas), kNW * 32, 0, stream,
                        programmatic, p);
 }
 
@@ -361,8 +361,16 @@ cudaError_t launch_variant(const WindowDecodeParams &p, cudaStream_t stream, boo
 int window_decode_ctas_per_sm() { return kCtasPerSm; }
 
 cudaError_t launch_window_decode(const WindowDecodeParams &p, cudaStream_t stream, bool programmatic) {
-  return p.col_blocks == 1 ? launch_variant<1>(p, stream, programmatic)
-                           : launch_variant<2>(p, stream, programmatic);
+  // More CTAs of few pages than three per SM hold: four fit with one page in
+  // flight per warp (64 / 8 heads: 64 requests of window 128 10.4 us instead of
+  // 12.6, of window 512 17.8 instead of 19.2; of window 2048 45.2 instead of
+  // 40.8, and 8 of window 256 9.7 instead of 8.9).
+  const long long units = static_cast<long long>(p.batch) * p.num_kv_heads * p.head_blocks;
+  const bool many = p.num_splits == 1 && units > kCtasPerSm * static_cast<long long>(p.num_sms) &&
+                    p.pages_per_chunk <= kFewPages + 1;
+  if (p.col_blocks == 1)
+    return many ? launch_variant<1, 1>(p, stream, programmatic) : launch_variant<1, 2>(p, stream, programmatic);
+  return many ? launch_variant<2, 1>(p, stream, programmatic) : launch_variant<2, 2>(p, stream, programmatic);
 }
 
 }  // namespace sa

@@ -23,7 +23,7 @@
 // for the product with V, the output once to bf16; max, sum and O in fp32.
 //
 // Measured (window 128, 4 sequences of 20.9k tokens, 64 / 8 heads; 57 us at the
-// copy bandwidth): 93 us, against 299 us with a CTA per tile (window_prefill.cu as
+// copy bandwidth): 90 us, against 299 us with a CTA per tile (window_prefill.cu as
 // it was then).  Issue slots are 56% busy, the tensor pipe 38%: the steps of a tile
 // follow one another, and three tiles hide part of that.  Tried: two threads per
 // row (194 us, registers spill where shared memory leaves no L1), pieces behind

@@ -49,6 +49,29 @@ def test_decode_window(heads, window, first):
     assert torch.equal(again, out) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("heads,batch", [((64, 8), 64), ((48, 4), 130)])
+@pytest.mark.parametrize("window,first", [(40, 3), (130, 0)])
+def test_decode_window_of_many_requests(heads, batch, window, first):
+    # more CTAs than the GPU holds with two pages in flight per warp
+    lens = [int(n) for n in np.random.default_rng(batch).integers(0, 400, batch)]
+    c = Paged(lens, *heads, seed=window)
+    q = bf16(c.rng, batch, heads[0], 64)
+    ro, rl = _decode_ref(c, q, window, first)
+    for b, n in enumerate(c.lens):
+        c.hide(b, bounded.visible(n - 1, n, window, first))
+    k, v, table, kv_lens = c.paged()
+    args = (q.to(DEV), k, v, table, kv_lens, c.sinks.to(DEV), c.scale, c.max_kv, window, first)
+    out, lse = sa.decode_window(*args)
+    assert_out_close(out, ro)
+    assert_lse_close(lse, rl)
+    b = int(np.argmax(lens))                             # a visible page outside the pool
+    table[b, (lens[b] - 1) // 16] = c.pages
+    bad, bad_lse = sa.decode_window(*args)
+    assert torch.isnan(bad[b]).all() and torch.isnan(bad_lse[b]).all()
+    rest = torch.arange(batch, device=DEV) != b
+    assert torch.equal(bad[rest], out[rest]) and torch.equal(bad_lse[rest], lse[rest])
+
+
 def test_a_window_without_bound_is_decode():
     c = Paged([300, 17, 1], 64, 8)
     q = bf16(c.rng, 3, 64, 64).to(DEV)
