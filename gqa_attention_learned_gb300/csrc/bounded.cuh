@@ -71,6 +71,7 @@ struct WindowPrefillParams {
   int tile_tokens;               // tokens per query tile = 128 / group
   unsigned inv_group;            // ceil(2^16 / group): i / group for i < 128
   int num_tiles;                 // query tiles per KV head, at most
+  int tiles_each;                // > 0: request r has tiles r * tiles_each ..; 0: numbered through
 };
 
 cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,

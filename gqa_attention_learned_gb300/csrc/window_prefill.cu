@@ -25,8 +25,8 @@
 // loads Q and K and issues S = Q K^T, warp 5 loads V and issues O += P V,
 // warps 0..3 run the online softmax, one thread per row, between them.
 //
-// Measured (64 / 8 heads): 568 us for 4 chunks of 2048 new tokens on up to 14336
-// cached ones with window 4096, 901 TFLOP/s of the pairs that are seen: tensor pipe
+// Measured (64 / 8 heads): 561 us for 4 chunks of 2048 new tokens on up to 14336
+// cached ones with window 4096, 912 TFLOP/s of the pairs that are seen: tensor pipe
 // 52%, exponential unit 40%, issue slots 50% busy; as in plain prefill the tile's
 // chain of S, softmax, P V binds.  Few tiles per CTA cost more: 59 us for 7.6k
 // tokens of 16 / 2 heads with window 1023 (16.5 us by the tensor peak), where a CTA
@@ -180,18 +180,28 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   // windows are full) first
   const int item = static_cast<int>(blockIdx.x) / p.num_kv_heads;
   const int kvh = static_cast<int>(blockIdx.x) - item * p.num_kv_heads;
-  Walk<kPaged> walk;
-  do {
-    if (!walk.advance(p)) return;
-  } while (walk.next <= item);
-  int first;
-  // the last lane with from <= item
-  const Request req = walk.request(31 - __clz(__ballot_sync(0xffffffffu, walk.from <= item)), first);
+  Request req;
+  int qt;
+  if (p.tiles_each > 0) {
+    const int seq = item / p.tiles_each;
+    req = Request::load<kPaged>(p, seq);
+    qt = p.tiles_each - 1 - (item - seq * p.tiles_each);
+    if (req.bad ? qt != 0 : qt * p.tile_tokens >= req.q_len) return;
+  } else {
+    Walk<kPaged> walk;
+    do {
+      if (!walk.advance(p)) return;
+    } while (walk.next <= item);
+    int first;
+    // the last lane with from <= item
+    req = walk.request(31 - __clz(__ballot_sync(0xffffffffu, walk.from <= item)), first);
+    qt = cdiv(req.q_len, p.tile_tokens) - 1 - (item - first);
+  }
   if (req.bad) {
     poison(p, kvh, req.q_start, max(req.q_len, 0), threadIdx.x, kThreads);
     return;
   }
-  const Tile tile = Tile::make<kPaged>(p, req, cdiv(req.q_len, p.tile_tokens) - 1 - (item - first));
+  const Tile tile = Tile::make<kPaged>(p, req, qt);
   const int rows = tile.tokens * p.group;
   const int n_tiles = cdiv(tile.n_boxes, kBoxes);
   const int live_threads = min(kBM, 32 * cdiv(rows, 32));

@@ -148,7 +148,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     int n = 0;                                           // tiles handed out
     bool ok = true;
     Walk<kPaged> walk;
-    walk.advance(p);
+    if (p.tiles_each == 0) walk.advance(p);
     for (int base = static_cast<int>(blockIdx.x); ok && base < items;) {
       // 32 items at a time, one per lane
       const long long mine = base + static_cast<long long>(lane) * stride;
@@ -156,7 +156,13 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       const int kvh = static_cast<int>(mine) - tile_no * p.num_kv_heads;
       int qt = -1;
       Request r{};
-      while (true) {
+      if (p.tiles_each > 0 && tile_no >= 0) {
+        const int seq = tile_no / p.tiles_each;
+        r = Request::load<kPaged>(p, seq);
+        qt = tile_no - seq * p.tiles_each;
+        if (r.bad ? qt != 0 : qt * p.tile_tokens >= r.q_len) qt = -1;     // a tile without rows
+      }
+      while (p.tiles_each == 0) {
         int first;
         const Request x = walk.request(walk.lane_of(tile_no), first);
         if (qt < 0 && tile_no >= 0 && tile_no < walk.next) {
@@ -415,15 +421,21 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   if (bar.dead) {
     // a wait ran out: none of this CTA's tiles can be trusted
     Walk<kPaged> walk;
-    walk.advance(p);
+    if (p.tiles_each == 0) walk.advance(p);
     for (long long item = blockIdx.x; item < items; item += stride) {
       const int tile_no = static_cast<int>(item) / p.num_kv_heads;
-      while (walk.next <= tile_no)
-        if (!walk.advance(p)) return;
+      Request r;
       int first;
-      const Request r = walk.request(walk.lane_of(tile_no), first);
+      if (p.tiles_each > 0) {
+        r = Request::load<kPaged>(p, tile_no / p.tiles_each);
+        first = r.seq * p.tiles_each;
+      } else {
+        while (walk.next <= tile_no)
+          if (!walk.advance(p)) return;
+        r = walk.request(walk.lane_of(tile_no), first);
+      }
       const int i0 = (tile_no - first) * p.tile_tokens;
-      if (!r.bad)
+      if (!r.bad && i0 < r.q_len)
         poison(p, static_cast<int>(item) - tile_no * p.num_kv_heads, r.q_start + i0,
                min(p.tile_tokens, r.q_len - i0), threadIdx.x, kThreads);
     }

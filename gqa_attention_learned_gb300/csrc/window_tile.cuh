@@ -122,7 +122,7 @@ struct Request {
   }
 };
 
-// The query tiles of a launch, numbered through request by request; a request
+// The query tiles of a launch numbered through request by request; a request
 // whose arguments are out of range counts as one tile (its rows become NaN), and
 // so does one that starts before an earlier one's end, so there are never more
 // than num_tiles.  Numbering the tiles that exist matters: with an empty CTA for

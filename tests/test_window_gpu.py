@@ -291,11 +291,34 @@ def test_prefill_window_of_many_requests(window):
     assert_lse_close(lse[good], rl[good])
 
 
+@pytest.mark.parametrize("window", [20, 280])
+def test_prefill_window_of_requests_alike(window):
+    # tiles of equal requests; one longer than the bound, one past the rows
+    rng = np.random.default_rng(8)
+    q, k, v = (bf16(rng, 1500, h, 64) for h in (4, 1, 1))
+    sinks = torch.zeros(4)
+    cu = [0, 290, 580, 870, 1160, 1500]
+    parts = [slice(a, b) for a, b in zip(cu, cu[1:])]
+    ro, rl = _prefill_ref(([k[p] for p in parts], [v[p] for p in parts]), q, cu, [0] * 5, np64(sinks), 0.125,
+                          window, 0)
+    for bound, ends in ((340, 1500), (300, 1500), (340, 1600)):
+        at = cu[:5] + [ends]
+        out, lse = sa.prefill_window(q.to(DEV), k.to(DEV), v.to(DEV),
+                                     torch.tensor(at, dtype=torch.int32, device=DEV), sinks.to(DEV), 0.125,
+                                     bound, window)
+        good = 1500 if bound >= 340 and ends == 1500 else 1160
+        assert_out_close(out[:good], ro[:good])
+        assert_lse_close(lse[:good], rl[:good])
+        assert torch.isnan(out[good:]).all() and torch.isnan(lse[good:]).all()
+
+
 @pytest.mark.parametrize("window", [100, 400])
-def test_prefill_window_of_a_request_does_not_depend_on_the_batch(window):
-    # more tiles than the persistent CTAs look up at a time
+@pytest.mark.parametrize("batch,longest", [(90, 300), (300, 60)])
+def test_prefill_window_of_a_request_does_not_depend_on_the_batch(window, batch, longest):
+    # more tiles than the persistent CTAs look up at a time, more requests than are
+    # numbered through
     rng = np.random.default_rng(7)
-    lens = [int(n) for n in rng.integers(0, 300, 90)]
+    lens = [int(n) for n in rng.integers(0, longest, batch)]
     lens[5] = 450
     cu = np.concatenate([[0], np.cumsum(lens)])
     total = int(cu[-1])
@@ -308,7 +331,7 @@ def test_prefill_window_of_a_request_does_not_depend_on_the_batch(window):
 
     out, lse = sa.prefill_window(q, k, v, ints(cu), sinks, 0.125, 450, window)
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
-    for b in (0, 5, 31, 32, 50, 63, 64, 88, 89):
+    for b in (0, 5, 31, 32, 50, 63, 64, batch - 2, batch - 1):
         at = slice(cu[b], cu[b + 1])
         if lens[b]:
             # the same bound on lengths: the same kernel
