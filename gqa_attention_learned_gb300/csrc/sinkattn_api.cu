@@ -112,7 +112,7 @@ constexpr int kPrefillKvTile = 128;   // keys per prefill K/V tile
 constexpr int kWindowWaves = 1;       // windowed decode: split up to this many times the CTA slots (2:
                                       // 59.7 us instead of 50.7 for 8 requests of window 16384)
 constexpr int kWindowMinPages = 16;   // and no finer than this
-constexpr int kWalkSeqs = 256;        // windowed prefill: requests that a CTA walks over at most
+constexpr int kWalkSeqs = 128;        // windowed prefill: requests that a CTA walks over at most
 constexpr int kMassTiles = 16;        // prefill mass: query tiles that count as many
 constexpr int kMaxCluster = 8;        // portable cluster size
 constexpr int kMassPagesPerWarp = 8;  // decode mass: pages a warp takes, one CTA's share
@@ -817,18 +817,21 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
   // Query tiles: as many for each request as the longest may have, or, if that
   // leaves many without rows, numbered through (a request has a tile for every
   // tile_tokens tokens and one more at most).  That costs a CTA a walk over the
-  // requests (64 / 8 heads, window 1000, 4 new tokens each: 230 us instead of 205
-  // for 512 requests, 539 instead of 389 for 1024) and gains where lengths differ
-  // (window 600, 64 prompts of up to 700 tokens: 288 us instead of 398).
+  // requests and gains where lengths differ (64 / 8 heads, window 600, 64 prompts of
+  // up to 700 tokens: 286 us instead of 354; window 400, 128 of up to 300: 257
+  // instead of 283, 256 of up to 200: 370 instead of 351; window 1000, 1024 requests
+  // of 4 new tokens: 539 instead of 357).  The persistent kernel gains nothing.
+  const bool is_short = sa::window_prefill_is_short(p);
   const int tiles_each = ceil_div(max_q_len, tile_tokens);
   const long long numbered = static_cast<long long>(total_q / tile_tokens) + num_seqs;
-  const bool walk = static_cast<long long>(tiles_each) * num_seqs > numbered && num_seqs <= kWalkSeqs;
+  const bool walk = !is_short && num_seqs <= kWalkSeqs &&
+                    static_cast<long long>(tiles_each) * num_seqs > numbered;
   const long long tiles = walk ? numbered : static_cast<long long>(tiles_each) * num_seqs;
   if (tiles * num_kv_heads > 0x7fffffffll) return SINKATTN_UNSUPPORTED;
   p.num_tiles = static_cast<int>(tiles);
   p.tiles_each = walk ? 0 : tiles_each;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (sa::window_prefill_is_short(p)) {
+  if (is_short) {
     const int sms = device_sm_count();
     if (sms == 0) return fail_msg("no CUDA device (SM count query failed)");
     return cuda_status(sa::launch_window_short(qmap, kmap, vmap, p, sms, st), "windowed prefill launch");

@@ -147,31 +147,21 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     // -------------------------------------------------------------- loads
     int n = 0;                                           // tiles handed out
     bool ok = true;
-    Walk<kPaged> walk;
-    if (p.tiles_each == 0) walk.advance(p);
     for (int base = static_cast<int>(blockIdx.x); ok && base < items;) {
-      // 32 items at a time, one per lane
+      // 32 items at a time, one per lane: most ragged batches have empty ones
       const long long mine = base + static_cast<long long>(lane) * stride;
       const int tile_no = mine < items ? static_cast<int>(mine) / p.num_kv_heads : -1;
       const int kvh = static_cast<int>(mine) - tile_no * p.num_kv_heads;
-      int qt = -1;
+      bool valid = false, poisoned = false;
+      int qt = 0;
       Request r{};
-      if (p.tiles_each > 0 && tile_no >= 0) {
+      if (tile_no >= 0) {
         const int seq = tile_no / p.tiles_each;
         r = Request::load<kPaged>(p, seq);
         qt = tile_no - seq * p.tiles_each;
-        if (r.bad ? qt != 0 : qt * p.tile_tokens >= r.q_len) qt = -1;     // a tile without rows
+        valid = !r.bad && qt * p.tile_tokens < r.q_len;
+        poisoned = r.bad && qt == 0;
       }
-      while (p.tiles_each == 0) {
-        int first;
-        const Request x = walk.request(walk.lane_of(tile_no), first);
-        if (qt < 0 && tile_no >= 0 && tile_no < walk.next) {
-          r = x;
-          qt = tile_no - first;
-        }
-        if (!__any_sync(0xffffffffu, qt < 0 && tile_no >= 0) || !walk.advance(p)) break;
-      }
-      const bool valid = qt >= 0 && !r.bad, poisoned = qt >= 0 && r.bad;
       for (unsigned m = __ballot_sync(0xffffffffu, poisoned); m; m &= m - 1) {
         const int l = __ffs(m) - 1;
         poison(p, __shfl_sync(0xffffffffu, kvh, l), __shfl_sync(0xffffffffu, r.q_start, l),
@@ -420,21 +410,10 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   }
   if (bar.dead) {
     // a wait ran out: none of this CTA's tiles can be trusted
-    Walk<kPaged> walk;
-    if (p.tiles_each == 0) walk.advance(p);
     for (long long item = blockIdx.x; item < items; item += stride) {
       const int tile_no = static_cast<int>(item) / p.num_kv_heads;
-      Request r;
-      int first;
-      if (p.tiles_each > 0) {
-        r = Request::load<kPaged>(p, tile_no / p.tiles_each);
-        first = r.seq * p.tiles_each;
-      } else {
-        while (walk.next <= tile_no)
-          if (!walk.advance(p)) return;
-        r = walk.request(walk.lane_of(tile_no), first);
-      }
-      const int i0 = (tile_no - first) * p.tile_tokens;
+      const Request r = Request::load<kPaged>(p, tile_no / p.tiles_each);
+      const int i0 = (tile_no - r.seq * p.tiles_each) * p.tile_tokens;
       if (!r.bad && i0 < r.q_len)
         poison(p, static_cast<int>(item) - tile_no * p.num_kv_heads, r.q_start + i0,
                min(p.tile_tokens, r.q_len - i0), threadIdx.x, kThreads);

@@ -107,81 +107,21 @@ __device__ __forceinline__ void pack_piece(uint32_t (&x)[16], uint64_t scale2, u
 struct Request {
   int seq, q_start, q_len, kv_len;
   bool bad;
-  template <bool kPaged>
+  // kOrder: a start that falls back spoils this request, too, and not only the one
+  // before it.
+  template <bool kPaged, bool kOrder = true>
   __device__ __forceinline__ static Request load(const WindowPrefillParams &p, int seq) {
     Request r;
     r.seq = seq;
     r.q_start = p.cu_seqlens_q[seq];
     const int q_end = p.cu_seqlens_q[seq + 1];
+    const int before = kOrder ? p.cu_seqlens_q[max(seq - 1, 0)] : r.q_start;
     r.q_len = q_end - r.q_start;
     r.kv_len = kPaged ? p.kv_lens[seq] : r.q_len;
-    r.bad = r.q_start < 0 || r.q_len < 0 || q_end > p.total_q || r.q_len > p.max_q_len ||
+    r.bad = r.q_start < 0 || r.q_start < before || r.q_len < 0 || q_end > p.total_q || r.q_len > p.max_q_len ||
             r.kv_len < r.q_len || r.kv_len > p.max_kv_len ||
             (kPaged && cdiv(r.kv_len, kPageSize) > p.max_pages_per_seq);
     return r;
-  }
-};
-
-// The query tiles of a launch numbered through request by request; a request
-// whose arguments are out of range counts as one tile (its rows become NaN), and
-// so does one that starts before an earlier one's end, so there are never more
-// than num_tiles.  Numbering the tiles that exist matters: with an empty CTA for
-// every tile that a shorter request lacks, an SM's second slot stayed free while
-// CTAs waited (237 of 304 slots taken at a third of empty ones).
-// A warp holds 32 requests at a time, one per lane.
-template <bool kPaged>
-struct Walk {
-  Request r;
-  int from, tiles;             // this lane's tiles: [from, from + tiles)
-  int seq0 = -32, next = 0;    // first request held; tiles up to the last one held
-  int top = 0;                 // the largest start so far
-  __device__ __forceinline__ bool advance(const WindowPrefillParams &p) {
-    if (seq0 + 32 >= p.num_seqs) return false;
-    seq0 += 32;
-    const int lane = threadIdx.x & 31, seq = seq0 + lane;
-    const bool have = seq < p.num_seqs;
-    r = have ? Request::load<kPaged>(p, seq) : Request{};
-    int most = have ? r.q_start : top;
-    if (__any_sync(0xffffffffu, have && (r.q_start < top || r.q_len < 0))) {
-      most = max(most, top);
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, most, d);
-        if (lane >= d) most = max(most, x);
-      }
-      r.bad = r.bad || r.q_start < most;
-    }
-    top = __shfl_sync(0xffffffffu, most, min(31, p.num_seqs - 1 - seq0));
-    tiles = !have ? 0 : r.bad ? 1 : cdiv(r.q_len, p.tile_tokens);
-    int end = tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int x = __shfl_up_sync(0xffffffffu, end, d);
-      if (lane >= d) end += x;
-    }
-    from = next + end - tiles;
-    next += __shfl_sync(0xffffffffu, end, 31);
-    return true;
-  }
-  // The lane with tile `i` of those held, i its own for each lane: the last one
-  // with from <= i, as lanes without tiles start where the next one does.
-  __device__ __forceinline__ int lane_of(int i) const {
-    int at = 0;
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2)
-      if (__shfl_sync(0xffffffffu, from, at + d) <= i) at += d;
-    return at;
-  }
-  // That lane's request and its first tile's number (source lanes may differ).
-  __device__ __forceinline__ Request request(int lane, int &first) const {
-    Request x;
-    x.seq = seq0 + lane;
-    x.q_start = __shfl_sync(0xffffffffu, r.q_start, lane);
-    x.q_len = __shfl_sync(0xffffffffu, r.q_len, lane);
-    x.kv_len = __shfl_sync(0xffffffffu, r.kv_len, lane);
-    x.bad = __shfl_sync(0xffffffffu, static_cast<int>(r.bad), lane) != 0;
-    first = __shfl_sync(0xffffffffu, from, lane);
-    return x;
   }
 };
 
