@@ -6,7 +6,7 @@
 // the column sums of the attention's own weights: lse is what decode /
 // prefill returned for the row, so one pass over K suffices and no softmax
 // state is carried.  Exponents, weights and sums are fp32.  Every sum has a
-// fixed order (no atomics), so equal inputs give equal bits.
+// fixed order (one addition to memory per entry), so equal inputs give equal bits.
 //
 // decode_mass (one token per request) reads 128 bytes of K per (key, KV head)
 // and is bound by HBM.  Each warp takes whole 16-key pages: S^T[16 keys x 8
