@@ -317,6 +317,13 @@ struct Walk {
       if (left == 0) return;
     }
   }
+  // The next pair, by a whole warp, for a walk in shared memory: lanes read it
+  // while others may be ahead, so one of them moves it, between two barriers.
+  __device__ __forceinline__ void next_of_warp(const MassParams &p) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) next(p);
+    __syncwarp();
+  }
   __device__ __forceinline__ void next(const MassParams &p) {
     if (--left == 0) return;
     if (p.mirror) {
@@ -360,14 +367,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap, const MassParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // in shared memory, a copy per warp (every lane writes the same values): it is
-  // looked at between key pairs, and registers are what the loops run out of
+  // in shared memory, a copy per warp: it is looked at between key pairs, and
+  // registers are what the loops run out of
   __shared__ Walk walks[kThreads / 32];
   Walk &walk = walks[warp];
   {
     Walk first;
     first.begin(p);
-    walk = first;
+    if (lane == 0) walk = first;
+    __syncwarp();
   }
   const int step_tokens = p.split * p.tile_tokens;       // from one tile of this CTA to its next
   // requests whose arguments are out of range: NaN over their mass rows
@@ -439,7 +447,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
       for (int u = 0; u < kMine; ++u)                    // columns past the rows add nothing
         l[u] = in_tile[u] < rows ? __ldg(from + row_at[u]) : INFINITY;
     };
-    for (; ok && walk.left > 0; walk.next(p)) {
+    for (; ok && walk.left > 0; walk.next_of_warp(p)) {
       const Steps st = walk.steps(p);
       float lse[1][kMine];
       load_lse(st, 0, lse[0]);
@@ -503,7 +511,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     const int w = warp - kMmaWarp;
     bool ok = true;
     int kn = 0, qn = 0, sn = 0;
-    for (; ok && walk.left > 0; walk.next(p)) {
+    for (; ok && walk.left > 0; walk.next_of_warp(p)) {
       const Steps st = walk.steps(p);
       // number of this group's key tile among those loaded
       const int tile = kn + (w == 1 && st.skip[0] < st.n ? 1 : 0);
@@ -549,7 +557,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint32_t masked = p.scale_log2 >= 0.f ? 0xff800000u : 0x7f800000u;
     bool ok = true;
     int qn = 0, sn = 0;
-    for (int item = 0; ok && walk.left > 0; ++item, walk.next(p)) {
+    for (int item = 0; ok && walk.left > 0; ++item, walk.next_of_warp(p)) {
       const Steps st = walk.steps(p);
       const int my_skip = w == 0 ? st.skip[0] : st.skip[kGroups - 1];
       const int key = st.key0 + w * kKeys + row;
@@ -620,7 +628,7 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     if (!ok) {
       // a wait ran out: none of the sums to come can be made
       atomicOr(&bar.bad_wait, 1);
-      for (; !p.mirror && walk.left > 0; walk.next(p)) {
+      for (; !p.mirror && walk.left > 0; walk.next_of_warp(p)) {
         const int key = walk.kp * kKeys * kGroups + w * kKeys + row;
         if (key < walk.kv_len) walk.row(p)[key] = NAN;
       }

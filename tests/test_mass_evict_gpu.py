@@ -424,3 +424,33 @@ def test_a_decode_step_of_both_kinds_of_layer_chained_programmatically():
 
     for x, y in zip(step(False), step(True)):
         assert torch.equal(x, y)
+
+
+# ------------------------------------------------------ many requests, few rows
+def test_prefill_mass_of_many_requests_with_few_rows():
+    # a decode batch with draft tokens: more requests than a warp looks up at
+    # once, some without rows, one refused, several key pairs each, so that a
+    # CTA's share crosses requests and heads
+    rng = np.random.default_rng(11)
+    q_lens = [int(n) for n in rng.integers(0, 5, 75)]
+    q_lens[31], q_lens[32], q_lens[40] = 0, 0, 3
+    prefix = [int(n) for n in rng.integers(0, 900, 75)]
+    prefix[7], prefix[64] = 1500, 1031
+    c = Paged([a + b for a, b in zip(q_lens, prefix)], 16, 2, seed=12)
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    q = bf16(c.rng, cu[-1], 16, 64)
+    cu_gpu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    k, v, table, kv = c.paged()
+    _, lse = sa.prefill_paged(q.to(DEV), cu_gpu, k, v, table, kv, c.sinks.to(DEV), c.scale, 4, c.max_kv)
+    kv[40] = -3
+    mass = torch.zeros(75, 2, c.max_kv, device=DEV)
+    for times in (1, 2):
+        sa.prefill_mass(q.to(DEV), cu_gpu, k, table, kv, lse, c.scale, 4, c.max_kv, mass)
+        for b, n in enumerate(c.lens):
+            if b == 40:
+                assert torch.isnan(mass[b]).all()
+                continue
+            rows = slice(cu[b], cu[b + 1])
+            want = bounded.mass_rows(np64(q[rows]), np64(c.k[b]), range(prefix[b], n), np64(lse[rows]), c.scale)
+            _mass_close(mass[b, :, :n], times * want)
+            assert (mass[b, :, n:] == 0).all()
