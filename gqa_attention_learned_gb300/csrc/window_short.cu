@@ -76,8 +76,8 @@ struct Work {
 struct Bars {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];   // Q, K and the geometry
   uint64_t v_full[kMaxStages], v_empty[kMaxStages];
+  uint64_t info[kMaxStages];   // the geometry that goes with a stage of V may be read
   uint64_t s_full[kMaxSlots], p_full[kMaxSlots], o_full[kMaxSlots];
-  uint64_t info[kMaxSlots];    // the slot's next geometry may be read
   uint64_t free[kMaxSlots];    // O has been read
   uint32_t tmem_base;
   int dead;                    // a wait ran out
@@ -124,13 +124,13 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
     for (int s = 0; s < kNV; ++s) {
       mbar_init(&bar.v_full[s], 1);
       mbar_init(&bar.v_empty[s], 128);
+      mbar_init(&bar.info[s], 1);
     }
     for (int l = 0; l < kSlots; ++l) {
       mbar_init(&bar.s_full[l], 1);
       mbar_init(&bar.p_full[l], 128);
       mbar_init(&bar.o_full[l], 1);
       mbar_init(&bar.free[l], 128);
-      mbar_init(&bar.info[l], 1);
     }
     bar.dead = 0;
     fence_mbar_init();
@@ -192,10 +192,11 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
         if (lane == 0) {
           // for the softmax warps by the arrival on info, for the products' by
           // k_full's.  (Not for both by k_full: its stage may be filled twice more
-          // while the softmax warps are behind; this slot's next arrival needs
-          // them to have taken this one.)
+          // while the softmax warps are behind.  info goes by V stage: its next
+          // arrival there needs v_empty, where all of them arrive after they have
+          // seen this one, so no phase is passed over unseen.)
           bar.work[n % kNV] = w;
-          mbar_arrive(&bar.info[n % kSlots]);
+          mbar_arrive(&bar.info[n % kNV]);
           const uint32_t bytes = __popc(boxes) * kBoxBytes;
           mbar_arrive_expect_tx(k_full, p.tile_tokens * p.group * kHeadDim * 2 + bytes);
           mbar_arrive_expect_tx(v_full, bytes);
@@ -220,7 +221,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
         break;
       if (lane == 0) {
         bar.work[n % kNV].stop = 1;
-        mbar_arrive(&bar.info[n % kSlots]);
+        mbar_arrive(&bar.info[n % kNV]);
         mbar_arrive(&bar.k_full[n % kNK]);
       }
       __syncwarp();
@@ -276,8 +277,8 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       int pieces, lead, edges;
       float sink;
     };
-    auto look = [&](int n, int k, Geometry &geo) -> bool {
-      if (!wait(&bar.info[slot], k)) return false;
+    auto look = [&](int n, Geometry &geo) -> bool {
+      if (!wait(&bar.info[n % kNV], n / kNV)) return false;
       const Work &w = bar.work[n % kNV];
       if (w.stop) return false;
       const Tile &tile = w.tile;
@@ -296,7 +297,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       return true;
     };
     Geometry geo;
-    bool more = look(slot, 0, geo);
+    bool more = look(slot, geo);
     for (int n = slot, k = 0; more; n += kSlots, ++k) {
       const int pieces = geo.pieces, lead = geo.lead, edges = geo.edges;
       const RowSlots see = geo.see;
@@ -384,7 +385,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       };
       if (r < rows && p.lse) p.lse[row_index(r)] = bad ? NAN : d == 0.f ? -INFINITY : (mu + lg2(d)) * kLn2;
       const float inv = bad ? NAN : d == 0.f ? 0.f : 1.f / d;
-      more = look(n + kSlots, k + 1, geo);
+      more = look(n + kSlots, geo);
       if (!wait(&bar.o_full[slot], k)) break;
       tc_fence_after();
 #pragma unroll

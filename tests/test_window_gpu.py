@@ -416,3 +416,22 @@ def test_another_stream_orders_its_own_workspace():
     side.synchronize()
     for o, l in got:
         assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
+# ------------------------------------------------- few tiles per persistent CTA
+@pytest.mark.parametrize("heads,window,first", [((16, 2), 30, 3), ((16, 2), 100, 40), ((4, 1), 100, 0), ((10, 2), 7, 1)])
+@pytest.mark.parametrize("tokens", [1, 40, 330, 1300])
+def test_short_windows_with_few_tiles_per_cta(heads, window, first, tokens):
+    # a CTA's first tiles and its last entries follow one another without a
+    # stage to wait for: 0, 1, 2 tiles per CTA and some more
+    hq, hkv = heads
+    c = Paged([tokens], hq, hkv, seed=tokens)
+    q = bf16(c.rng, tokens, hq, 64)
+    ro, rl = bounded.window_rows(np64(q), np64(c.k[0]), np64(c.v[0]), range(tokens), np64(c.sinks), c.scale,
+                                 window, first)
+    cu = torch.tensor([0, tokens], dtype=torch.int32, device=DEV)
+    for _ in range(3):
+        out, lse = sa.prefill_paged_window(q.to(DEV), cu, *c.paged(), c.sinks.to(DEV), c.scale, tokens, tokens,
+                                           window, first)
+        assert_out_close(out, ro)
+        assert_lse_close(lse, rl)
