@@ -373,6 +373,7 @@ evict_select_kernel(const EvictParams p) {
     cta_equal += s.warp_equal[w];
   }
   if (split > 1) {
+    if (want == 0) cluster.sync();                        // (no pass has met the peers: they may not run yet)
     if (tid < split) {
       SelectSmem *peer = cluster.map_shared_rank(&s, tid);
       peer->cta_sure[rank] = cta_sure;

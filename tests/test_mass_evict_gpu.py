@@ -454,3 +454,18 @@ def test_prefill_mass_of_many_requests_with_few_rows():
             want = bounded.mass_rows(np64(q[rows]), np64(c.k[b]), range(prefix[b], n), np64(lse[rows]), c.scale)
             _mass_close(mass[b, :, :n], times * want)
             assert (mass[b, :, n:] == 0).all()
+
+
+@pytest.mark.parametrize("first,recent", [(100, 900), (0, 1000), (1000, 0)])
+def test_evict_long_rows_by_place_alone(first, recent):
+    # the first and the recent keys fill the budget: no weight is looked at, and
+    # the CTAs that share a row meet only to number what they keep
+    c = Paged([30000, 999, 16001, 1001], 2, 2, seed=13)
+    mass = torch.from_numpy(_weights(c.rng, "odd", 4, 2, 30000))
+    ref = _evict_ref(c, mass, 1000, first, recent)
+    for _ in range(3):
+        k, v, table, kv = c.paged()
+        m = mass.to(DEV)
+        new, kept = sa.evict(k, v, table, kv, m, 1000, 30000, first_tokens=first, recent=recent)
+        torch.cuda.synchronize()
+        _check(c, ref, kept.cpu(), new.cpu(), 1000, c.table, k, v, c.k_cache, c.v_cache, m, mass, mass)
