@@ -152,15 +152,19 @@ window_decode_kernel(const WindowDecodeParams p) {
     qa[nb][0] = r < rows ? __ldg(q + t) : zero4;
     qa[nb][1] = r < rows ? __ldg(q + t + 4) : zero4;
   }
-  // softmax state of rows g + 8 nb (d: this lane's keys only)
+  // softmax state of rows g + 8 nb (d: this lane's keys only).  A sink that is no
+  // logit (NaN, +inf) is kept out of the running maximum, where a comparison may
+  // not see it, and spoils the sum, which spoils the row and its lse.
   float m[NB], d[NB];
   float o[8][2 * NB];                 // n-tile i: row g dims 16t + i, 16t + 8 + i; then row g + 8
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const int r = g + 8 * nb;
     const bool sink = chunk == 0 && warp == 0 && r < rows;
-    m[nb] = sink ? __ldg(p.sinks + kvh * p.group + row0 + r) * kLog2e : -INFINITY;
-    d[nb] = sink && t == 0 ? 1.f : 0.f;                // e^(sink - m) = 1, counted once
+    const float logit = sink ? __ldg(p.sinks + kvh * p.group + row0 + r) * kLog2e : -INFINITY;
+    const bool fine = logit < INFINITY;
+    m[nb] = fine ? logit : -INFINITY;
+    d[nb] = sink && t == 0 ? (fine ? 1.f : NAN) : 0.f;  // e^(sink - m) = 1, counted once
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)

@@ -435,3 +435,39 @@ def test_short_windows_with_few_tiles_per_cta(heads, window, first, tokens):
                                            window, first)
         assert_out_close(out, ro)
         assert_lse_close(lse, rl)
+
+
+
+# -------------------------------------------------------------------- odd sinks
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("others", [None, 90.0, -float("inf")])
+def test_sinks_that_are_no_logit_spoil_their_heads(what, others):
+    # NaN and +inf: output and lse of the head are NaN, in one chunk or several,
+    # whatever the row sees and whether the other heads' running maxima move (below a
+    # sink of 90 they do not); the other heads are not touched
+    def sinks(c):
+        good = c.sinks if others is None else torch.full_like(c.sinks, others)
+        bad = good.clone()
+        bad[2], bad[7] = what, what
+        return good.to(DEV), bad.to(DEV)
+
+    fine = torch.tensor([h not in (2, 7) for h in range(8)], device=DEV)
+
+    def check(got, want):
+        assert torch.isnan(got[0][:, ~fine]).all() and torch.isnan(got[1][:, ~fine]).all()
+        assert torch.equal(got[0][:, fine], want[0][:, fine]) and torch.equal(got[1][:, fine], want[1][:, fine])
+
+    for hkv in (1, 2):                                   # groups of 8 and of 4
+        c = Paged([300, 0, 20], 8, hkv)
+        q = bf16(c.rng, 3, 8, 64).to(DEV)
+        want, got = ([sa.decode_window(q, *c.paged(), s, c.scale, 300, 200, 3, num_splits=n) for n in (1, 5)]
+                     for s in sinks(c))
+        for x, y in zip(got, want):
+            check(x, y)
+        c = Paged([450], 8, hkv)
+        q = bf16(c.rng, 450, 8, 64).to(DEV)
+        cu = torch.tensor([0, 450], dtype=torch.int32, device=DEV)
+        want, got = ([sa.prefill_paged_window(q, cu, *c.paged(), s, c.scale, 450, 450, w) for w in (20, 400)]
+                     for s in sinks(c))
+        for x, y in zip(got, want):
+            check(x, y)
