@@ -4,6 +4,7 @@
 
 #include "sinkattn.h"
 #include "bounded.cuh"
+#include "workspace.cuh"
 
 #include <cudaTypedefs.h>
 
@@ -221,6 +222,13 @@ DecodePlan plan_decode(int batch, int q_len, int num_qo_heads, int num_kv_heads,
                            ((rows * sizeof(float) + 255) & ~size_t(255));
   }
   return plan;
+}
+
+// Clears the merge counters of a plan that has more of them than the part of
+// the workspace that every call leaves at zero.
+int clear_wide_counters(const DecodePlan &plan, void *workspace, cudaStream_t stream) {
+  if (plan.counters_bytes <= sa::kCounterSpan) return SINKATTN_OK;
+  return cuda_status(cudaMemsetAsync(workspace, 0, plan.counters_bytes, stream), "merge counter clear");
 }
 
 // A bound on lengths as the windowed kernels take it: "no bound" is the largest
@@ -748,8 +756,10 @@ int sinkattn_decode_window(const void *q, const void *k_cache, const void *v_cac
   p.window = std::min(window, std::max(p.max_kv_len, 1));
   p.first_tokens = std::min(first_tokens, p.max_kv_len);
   p.num_sms = sms;
-  return cuda_status(sa::launch_window_decode(p, static_cast<cudaStream_t>(stream),
-                                              sa::programmatic_for(launch_flags)),
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int cleared = clear_wide_counters(plan, workspace, st);
+  if (cleared != SINKATTN_OK) return cleared;
+  return cuda_status(sa::launch_window_decode(p, st, sa::programmatic_for(launch_flags)),
                      "windowed decode launch");
 }
 

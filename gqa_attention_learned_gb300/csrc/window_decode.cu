@@ -31,6 +31,7 @@
 
 #include "bounded.cuh"
 #include "bounded_ptx.cuh"
+#include "workspace.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -349,6 +350,19 @@ window_decode_kernel(const WindowDecodeParams p) {
     if (dq == 0 && p.lse) p.lse[row] = poisoned ? NAN : (den == 0.f ? -INFINITY : (mx + lg2(den)) * kLn2);
   }
   if (threadIdx.x == 0) *counter = 0;
+  // zero again, too: results where another plan has its counters
+  const float *end = counter_span_end(p.counters);
+  __syncthreads();                                     // they have been read
+  for (int c = 0; c < nchunks && p.ws_o + c * stride * kHeadDim < end; ++c)
+    for (int item = threadIdx.x; item < rows * (kHeadDim / 4); item += kNW * 32) {
+      float *at = p.ws_o + (c * stride + head0) * kHeadDim + item * 4;
+      if (at < end) *reinterpret_cast<float4 *>(at) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  if (p.ws_lse < end)
+    for (int item = threadIdx.x; item < nchunks * rows; item += kNW * 32) {
+      float *at = p.ws_lse + (item / rows) * stride + head0 + item % rows;
+      if (at < end) *at = 0.f;
+    }
 }
 
 template <int NB, int kAhead>

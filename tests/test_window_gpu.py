@@ -471,3 +471,30 @@ def test_sinks_that_are_no_logit_spoil_their_heads(what, others):
                      for s in sinks(c))
         for x, y in zip(got, want):
             check(x, y)
+
+
+
+# ---------------------------------------------------------- one workspace for all
+def test_one_workspace_serves_windowed_plans_of_every_shape():
+    # zero-filled once: plans keep their counters where others keep partial results,
+    # so every call has to leave all of that at zero
+    cases = []
+    for batch, hq, hkv, window, splits in ((8, 64, 8, 1500, 4), (28, 64, 8, 1500, 3), (8, 64, 8, 1500, 4),
+                                           (64, 8, 8, 700, 5), (3, 128, 1, 900, 7), (9, 64, 8, 1500, 0),
+                                           (1, 4, 1, 2000, 9), (28, 64, 8, 1500, 3), (700, 8, 8, 64, 2),
+                                           (28, 64, 8, 1500, 3)):
+        rng = np.random.default_rng(batch)
+        c = Paged([int(n) for n in rng.integers(600, 2000, batch)] if batch < 100 else [70] * batch, hq, hkv,
+                  seed=batch)
+        q = bf16(c.rng, batch, hq, 64).to(DEV)
+        cases.append(((q, *c.paged(), c.sinks.to(DEV), c.scale, 2000, window, 5), splits))
+    sizes = [sa.decode_window_plan(a[0].shape[0], a[0].shape[1], a[1].shape[1], 2000, a[8], 5, s)
+             for a, s in cases]
+    assert min(s for s, _ in sizes) > 1
+    shared = torch.zeros(max(b for _, b in sizes), dtype=torch.uint8, device=DEV)
+    for args, splits in cases:
+        want = sa.decode_window(*args, num_splits=splits)
+        out = torch.full_like(want[0], 7.0)
+        lse = torch.full_like(want[1], 7.0)
+        sa.decode_window(*args, num_splits=splits, workspace=shared, out=out, lse=lse)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
