@@ -48,9 +48,10 @@ DECODE_WORKLOAD = ("gpt-oss-20b decode: 64 q / 8 KV heads, head_dim 64, batch 64
 # once a source changes, the traffic is reported as unknown (null).
 TRAFFIC = {
     "decode": {"sources": ("gqa_attention_learned_gb300/csrc/decode.cu",
+                           "gqa_attention_learned_gb300/csrc/workspace.cuh",
                            "gqa_attention_learned_gb300/csrc/kernels.cuh",
                            "gqa_attention_learned_gb300/csrc/ptx.cuh"),
-               "sha256_16": "32c82e9d91842e7b", "bytes": 261_699_328 + 2_998_272},
+               "sha256_16": "5a057f971a1dd766", "bytes": 261_724_928 + 2_755_072},
     "prefill": {"sources": ("gqa_attention_learned_gb300/csrc/prefill.cu",
                             "gqa_attention_learned_gb300/csrc/kernels.cuh",
                             "gqa_attention_learned_gb300/csrc/ptx.cuh"),

@@ -39,6 +39,7 @@
 
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "workspace.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -634,6 +635,25 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       p.lse[row] = poisoned ? NAN : (den > 0.f ? (mx + lg2(den)) * kLn2 : -INFINITY);
   }
   if (threadIdx.x == 0) p.counters[unit] = 0;
+  // zero again, too: results where another plan has its counters
+  const float *end = counter_span_end(p.counters);
+  __syncthreads();                                     // they have been read
+  for (int c = 0; c < nchunks && p.ws_o + c * stride * kHeadDim < end; ++c)
+    for (int item = threadIdx.x; item < kCols * (kHeadDim / 4); item += kNW * 32) {
+      int head;
+      const long long ri = row_index<kVerify>(p, b, kvh, row0 + item / (kHeadDim / 4), head);
+      if (ri < 0) continue;
+      float *at = p.ws_o + (c * stride + static_cast<size_t>(ri)) * kHeadDim + item % (kHeadDim / 4) * 4;
+      if (at < end) *reinterpret_cast<float4 *>(at) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  if (p.ws_lse < end)
+    for (int item = threadIdx.x; item < nchunks * kCols; item += kNW * 32) {
+      int head;
+      const long long ri = row_index<kVerify>(p, b, kvh, row0 + item % kCols, head);
+      if (ri < 0) continue;
+      float *at = p.ws_lse + item / kCols * stride + static_cast<size_t>(ri);
+      if (at < end) *at = 0.f;
+    }
 }
 
 template <int NB, bool kVerify>

@@ -472,6 +472,9 @@ int decode_entry(const void *q, const void *k_cache, const void *v_cache,
     // within workspace_bytes (checked above)
     const cudaError_t e = cudaMemsetAsync(workspace, 0, plan.counters_bytes, st);
     if (e != cudaSuccess) return cuda_status(e, "merge counter clear");
+  } else {
+    const int cleared = clear_wide_counters(plan, workspace, st);
+    if (cleared != SINKATTN_OK) return cleared;
   }
   return cuda_status(launch_decode(kmap, vmap, p, st, programmatic), "decode launch");
 }

@@ -164,9 +164,12 @@ SINKATTN_API size_t sinkattn_decode_workspace_bytes(int batch, int num_qo_heads,
  *   workspace  : device scratch of workspace_bytes (>= the plan's figure),
  *                256-byte aligned; may be NULL when the plan has a single
  *                split.  It must be ZERO-FILLED BEFORE ITS FIRST USE; every
- *                call leaves it ready for the next (its merge counters return
- *                to zero), so it is zeroed once, not per call.  Calls sharing
- *                a workspace must not overlap on the GPU.
+ *                call leaves it ready for the next (what may hold merge
+ *                counters returns to zero), so it is zeroed once, not per
+ *                call.  It may serve calls of sinkattn_decode, sinkattn_verify
+ *                and sinkattn_decode_window of any batch, heads and split
+ *                count in turn; nothing else may write to it in between.
+ *                Calls sharing a workspace must not overlap on the GPU.
  * Long contexts run as num_splits KV chunks per (request, KV head), the sink
  * entering chunk 0 only; the last chunk to finish merges them by
  * log-sum-exp inside the same kernel.

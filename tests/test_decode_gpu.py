@@ -233,3 +233,32 @@ def test_large_batch_heaviest_first_dispatch():
     ro, rl = ref_decode(w)
     assert_out_close(out, ro)
     assert_lse_close(lse, rl)
+
+
+def test_one_workspace_serves_plans_of_every_shape():
+    # zero-filled once, used by decode, verification and windowed decode of other
+    # batches, heads and split counts: each keeps its counters where another keeps
+    # partial results
+    cases = []
+    for batch, hq, hkv, q_len, splits in ((8, 64, 8, 1, 4), (28, 64, 8, 1, 3), (8, 64, 8, 1, 4), (3, 128, 1, 1, 7),
+                                          (8, 64, 8, 4, 4), (9, 64, 8, 1, 0), (64, 8, 8, 2, 5), (28, 64, 8, 1, 3),
+                                          (1, 4, 1, 1, 9), (700, 8, 8, 1, 2), (28, 64, 8, 1, 3)):
+        w = workloads.decode_batch(seed=batch, batch=batch, min_len=20 if batch > 100 else 600,
+                                   max_len=70 if batch > 100 else 2000, num_qo_heads=hq, num_kv_heads=hkv)
+        gen = torch.Generator(DEV).manual_seed(batch)
+        q = torch.randn(batch, q_len, hq, 64, generator=gen, device=DEV).bfloat16()
+        rest = (*_dev(w, "k_cache", "v_cache", "page_table", "kv_lens", "sinks"), w["scale"], 2000)
+        plan = sa.verify_plan(batch, q_len, hq, hkv, 2000, splits)
+        assert plan[0] > 1
+        if q_len > 1:
+            cases.append((plan[1], sa.verify, (q, *rest), splits))
+        else:
+            cases.append((plan[1], sa.decode, (q[:, 0], *rest), splits))
+            window = sa.decode_window_plan(batch, hq, hkv, 2000, 1500, 3, splits)
+            cases.append((window[1], sa.decode_window, (q[:, 0], *rest, 1500, 3), splits))
+    shared = torch.zeros(max(n for n, *_ in cases), dtype=torch.uint8, device=DEV)
+    for _, call, args, splits in cases:
+        want = call(*args, num_splits=splits)
+        out, lse = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+        call(*args, num_splits=splits, workspace=shared, out=out, lse=lse)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])

@@ -437,7 +437,6 @@ def test_short_windows_with_few_tiles_per_cta(heads, window, first, tokens):
         assert_lse_close(lse, rl)
 
 
-
 # -------------------------------------------------------------------- odd sinks
 @pytest.mark.parametrize("what", [float("nan"), float("inf")])
 @pytest.mark.parametrize("others", [None, 90.0, -float("inf")])
@@ -471,7 +470,6 @@ def test_sinks_that_are_no_logit_spoil_their_heads(what, others):
                      for s in sinks(c))
         for x, y in zip(got, want):
             check(x, y)
-
 
 
 # ---------------------------------------------------------- one workspace for all
