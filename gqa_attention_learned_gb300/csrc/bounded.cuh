@@ -97,7 +97,7 @@ struct MassParams {
   const int32_t *kv_lens;        // [n]
   const float *lse;              // [Tq][Hq]
   float *mass;                   // [n][Hkv][mass_stride]
-  float scale_log2;              // not 0: masked scores are infinities that it keeps infinite
+  float scale_log2;
   int num_seqs, total_q, max_q_len, max_kv_len, mass_stride;
   int num_qo_heads, num_kv_heads, group;
   int max_pages_per_seq, num_pages;

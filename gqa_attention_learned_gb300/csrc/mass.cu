@@ -198,10 +198,13 @@ __device__ __forceinline__ uint32_t first_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// Sum over 32 columns of 2^(s * scale + nl), s in r, nl in shared memory.
-template <int E = 0>
+// Sum over 32 columns of 2^(s * scale + nl), s in r, nl in shared memory; on an
+// edge over those with a bit in `see`.  Hidden columns are left out behind the
+// exponent, not in the score: a row whose lse is NaN would be so in its exponent all
+// the same, and spoil keys that it does not see.
+template <bool kEdge, int E = 0>
 __device__ __forceinline__ void add_chunk(uint32_t (&r)[32], const float4 *nl, uint64_t scale2,
-                                          uint64_t &acc0, uint64_t &acc1) {
+                                          uint32_t see, uint64_t &acc0, uint64_t &acc1) {
   if constexpr (E < 8) {
     const float4 l = nl[E];
     float x0, x1, x2, x3;
@@ -209,9 +212,15 @@ __device__ __forceinline__ void add_chunk(uint32_t (&r)[32], const float4 *nl, u
                      f2_pack(l.x, l.y)), x0, x1);
     f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * E + 2]), __uint_as_float(r[4 * E + 3])), scale2,
                      f2_pack(l.z, l.w)), x2, x3);
+    if constexpr (kEdge) {
+      x0 = (see >> (4 * E)) & 1u ? x0 : -INFINITY;
+      x1 = (see >> (4 * E + 1)) & 1u ? x1 : -INFINITY;
+      x2 = (see >> (4 * E + 2)) & 1u ? x2 : -INFINITY;
+      x3 = (see >> (4 * E + 3)) & 1u ? x3 : -INFINITY;
+    }
     acc0 = f2_add(acc0, f2_pack(ex2(x0), ex2(x1)));
     acc1 = f2_add(acc1, f2_pack(ex2(x2), ex2(x3)));
-    add_chunk<E + 1>(r, nl, scale2, acc0, acc1);
+    add_chunk<kEdge, E + 1>(r, nl, scale2, see, acc0, acc1);
   }
 }
 
@@ -554,7 +563,6 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint32_t trow = tmem + 2 * w * kHalf + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int row = threadIdx.x & 127;
     const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
-    const uint32_t masked = p.scale_log2 >= 0.f ? 0xff800000u : 0x7f800000u;
     bool ok = true;
     int qn = 0, sn = 0;
     for (int item = 0; ok && walk.left > 0; ++item, walk.next_of_warp(p)) {
@@ -597,14 +605,10 @@ prefill_mass_kernel(const __grid_constant__ CUtensorMap qmap,
               tc_fence_before();
               mbar_arrive(&bar.s_free[w][h]);
             }
-            if (edge) {
-              const int c0 = h * kHalf + 32 * c;
-              const uint32_t see = first_bits(rows - c0) & ~first_bits(from - c0);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((see >> e) & 1u)) x[e] = masked;
-            }
-            add_chunk(x, reinterpret_cast<const float4 *>(sL(s) + h * kHalf + 32 * c), scale2, acc0, acc1);
+            const int c0 = h * kHalf + 32 * c;
+            const float4 *nl = reinterpret_cast<const float4 *>(sL(s) + c0);
+            if (edge) add_chunk<true>(x, nl, scale2, first_bits(rows - c0) & ~first_bits(from - c0), acc0, acc1);
+            else add_chunk<false>(x, nl, scale2, 0u, acc0, acc1);
           }
         }
         if (!ok) break;

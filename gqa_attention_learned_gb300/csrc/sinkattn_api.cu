@@ -877,7 +877,7 @@ int mass_params(sa::MassParams &p, const void *q, const void *k_cache, const int
   p.lse = lse;
   p.mass = mass;
   p.mass_stride = mass_stride;
-  p.scale_log2 = masked_scale_log2(scale);
+  p.scale_log2 = scale * sa::kLog2e;
   p.num_seqs = num_seqs;
   p.total_q = total_q;
   p.max_kv_len = max_kv_len;

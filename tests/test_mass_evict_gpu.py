@@ -469,3 +469,20 @@ def test_evict_long_rows_by_place_alone(first, recent):
         new, kept = sa.evict(k, v, table, kv, m, 1000, 30000, first_tokens=first, recent=recent)
         torch.cuda.synchronize()
         _check(c, ref, kept.cpu(), new.cpu(), 1000, c.table, k, v, c.k_cache, c.v_cache, m, mass, mass)
+
+
+# --------------------------------------------------------- what a row does not see
+@pytest.mark.parametrize("tokens,row", [(200, 100), (200, 130), (2300, 777)])
+def test_a_row_without_an_lse_spoils_only_the_keys_that_it_sees(tokens, row):
+    c = Paged([tokens], 8, 1, seed=14)
+    q = bf16(c.rng, tokens, 8, 64)
+    k, v, table, kv = c.paged()
+    cu = torch.tensor([0, tokens], dtype=torch.int32, device=DEV)
+    _, lse = sa.prefill_paged(q.to(DEV), cu, k, v, table, kv, c.sinks.to(DEV), c.scale, tokens, tokens)
+    want = torch.zeros(1, 1, tokens, device=DEV)
+    sa.prefill_mass(q.to(DEV), cu, k, table, kv, lse, c.scale, tokens, tokens, want)
+    lse[row, 3] = float("nan")
+    mass = torch.zeros(1, 1, tokens, device=DEV)
+    sa.prefill_mass(q.to(DEV), cu, k, table, kv, lse, c.scale, tokens, tokens, mass)
+    assert torch.isnan(mass[0, 0, :row + 1]).all()
+    assert torch.equal(mass[0, 0, row + 1:], want[0, 0, row + 1:])
