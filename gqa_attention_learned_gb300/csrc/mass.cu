@@ -692,11 +692,12 @@ int prefill_mass_pair_keys() { return kKeys * kGroups; }
 cudaError_t launch_prefill_mass(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                 const MassParams &p, cudaStream_t stream) {
   // a cluster per (unit, pair and its mirror image), or a share of everything
-  // for each CTA that the GPU holds
+  // for each CTA that the GPU holds (some, even where no key is in bounds: they
+  // flag the requests that have any)
   const unsigned long long units = static_cast<unsigned long long>(p.num_seqs) * p.num_kv_heads;
   const unsigned long long pairs = cdiv(p.max_kv_len, kKeys * kGroups);
   const unsigned long long ctas = p.mirror ? units * ((pairs + 1) / 2) * p.split
-                                              : std::min<unsigned long long>(units * pairs, 2 * p.num_sms);
+                                              : std::min<unsigned long long>(units * std::max(pairs, 1ull), 2 * p.num_sms);
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffull) return cudaErrorInvalidConfiguration;
   cudaError_t err = set_smem_once<prefill_mass_kernel>(kSmemBytes);

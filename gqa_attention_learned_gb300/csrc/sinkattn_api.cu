@@ -951,7 +951,7 @@ int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_se
                              head_dim, page_size, num_pages, max_kv_len);
   if (st != SINKATTN_OK) return st;
   if (p.group > kPrefillTile) return SINKATTN_UNSUPPORTED;
-  if (num_seqs == 0 || total_q == 0 || max_q_len == 0 || mass_stride == 0) return SINKATTN_OK;
+  if (num_seqs == 0 || total_q == 0 || mass_stride == 0) return SINKATTN_OK;
   if (!cu_seqlens_q || !aligned(cu_seqlens_q, 4)) return SINKATTN_INVALID_ARGUMENT;
   p.cu_seqlens_q = cu_seqlens_q;
   p.max_q_len = max_q_len;
@@ -963,7 +963,7 @@ int sinkattn_prefill_mass(const void *q, const int32_t *cu_seqlens_q, int num_se
   // prompts of up to 4096 tokens, 64 / 8 heads: 217 us with 2, 329 with 1; 228
   // with 4, 247 with 8, which each start and end more often).
   const long long tiles = ceil_div(max_q_len, p.tile_tokens);
-  p.mirror = tiles >= kMassTiles;
+  p.mirror = tiles >= kMassTiles && max_kv_len > 0;
   if (p.mirror) {
     const long long pairs = ceil_div(ceil_div(max_kv_len, sa::prefill_mass_pair_keys()), 2);
     const long long clusters = pairs * num_seqs * num_kv_heads;

@@ -467,7 +467,8 @@ SINKATTN_API int sinkattn_prefill_paged_window(const void *q, const int32_t *cu_
  * Sums are in fp32 and in a fixed order: equal calls give equal bits.  No two
  * calls that add to the same mass may overlap on the GPU.  A request whose
  * lengths are out of range gets a NaN mass row (all mass_stride entries of
- * each KV head); keys on a page outside the pool get NaN.
+ * each KV head); keys on a page outside the pool get NaN.  A call without
+ * rows or without mass_stride does nothing.
  *
  * sinkattn_decode_mass: one new token per request (q [batch][num_qo_heads]
  * [head_dim]).  Launched programmatically whatever the default: it reads and

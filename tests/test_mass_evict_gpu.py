@@ -486,3 +486,20 @@ def test_a_row_without_an_lse_spoils_only_the_keys_that_it_sees(tokens, row):
     sa.prefill_mass(q.to(DEV), cu, k, table, kv, lse, c.scale, tokens, tokens, mass)
     assert torch.isnan(mass[0, 0, :row + 1]).all()
     assert torch.equal(mass[0, 0, row + 1:], want[0, 0, row + 1:])
+
+
+def test_mass_of_bounds_of_zero():
+    # lengths past a bound of 0 are out of range as past any other
+    c = Paged([5, 0, 3], 4, 1)
+    q = bf16(c.rng, 3, 4, 64).to(DEV)
+    k, _, table, kv = c.paged()
+    lse = torch.zeros(3, 4, device=DEV)
+    cu = torch.tensor([0, 2, 2, 3], dtype=torch.int32, device=DEV)
+    for call in (lambda m: sa.decode_mass(q, k, table, kv, lse, c.scale, 0, m),
+                 lambda m: sa.prefill_mass(q, cu, k, table, kv, lse, c.scale, 2, 0, m),
+                 lambda m: sa.prefill_mass(q, cu, k, table, kv, lse, c.scale, 300, 0, m),
+                 lambda m: sa.prefill_mass(q, cu, k, table, kv, lse, c.scale, 0, 5, m)):
+        mass = torch.ones(3, 1, 9, device=DEV)
+        call(mass)
+        assert torch.isnan(mass[[0, 2]]).all()
+        assert (mass[1] == 1).all()
