@@ -789,7 +789,7 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
     return SINKATTN_INVALID_ARGUMENT;
   const int group = num_qo_heads / num_kv_heads;
   if (group > kPrefillTile) return SINKATTN_UNSUPPORTED;
-  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return SINKATTN_OK;
+  if (num_seqs == 0 || total_q == 0) return SINKATTN_OK;
   if (!q || !k || !v || !cu_seqlens_q || !sinks || !out || (paged && (!page_table || !kv_lens)))
     return SINKATTN_INVALID_ARGUMENT;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
@@ -835,7 +835,7 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
   // instead of 283, 256 of up to 200: 370 instead of 351; window 1000, 1024 requests
   // of 4 new tokens: 539 instead of 357).  The persistent kernel gains nothing.
   const bool is_short = sa::window_prefill_is_short(p);
-  const int tiles_each = ceil_div(max_q_len, tile_tokens);
+  const int tiles_each = std::max(1, ceil_div(max_q_len, tile_tokens));   // (one flags a request out of range)
   const long long numbered = static_cast<long long>(total_q / tile_tokens) + num_seqs;
   const bool walk = !is_short && num_seqs <= kWalkSeqs &&
                     static_cast<long long>(tiles_each) * num_seqs > numbered;

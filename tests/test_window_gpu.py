@@ -496,3 +496,19 @@ def test_one_workspace_serves_windowed_plans_of_every_shape():
         lse = torch.full_like(want[1], 7.0)
         sa.decode_window(*args, num_splits=splits, workspace=shared, out=out, lse=lse)
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("window", [20, 400])
+def test_requests_longer_than_a_bound_of_zero_give_nan(window):
+    c = Paged([40, 450], 4, 1)
+    q = bf16(c.rng, 10, 4, 64).to(DEV)
+    cu = torch.tensor([0, 4, 8], dtype=torch.int32, device=DEV)
+    sinks = c.sinks.to(DEV)
+    k, v = (x[0][:10].to(DEV) for x in (c.k, c.v))
+    for call in (lambda **kw: sa.prefill_paged_window(q, cu, *c.paged(), sinks, c.scale, 0, 450, window, **kw),
+                 lambda **kw: sa.prefill_paged_window(q, cu, *c.paged(), sinks, c.scale, 4, 0, window, **kw),
+                 lambda **kw: sa.prefill_window(q, k, v, cu, sinks, c.scale, 0, window, **kw)):
+        out, lse = torch.full_like(q, 7.0), torch.full((10, 4), 7.0, device=DEV)
+        call(out=out, lse=lse)
+        assert torch.isnan(out[:8]).all() and torch.isnan(lse[:8]).all()
+        assert (out[8:] == 7).all() and (lse[8:] == 7).all()
