@@ -45,6 +45,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 namespace sa {
@@ -77,7 +78,8 @@ __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
 
 // Columns 8 nb .. 8 nb + 7 of the query heads: Q as B fragments (column g holds
 // pieces t and t + 4 of its head, the k order of K's pieces) and -lse in base 2
-// of columns 2t, 2t + 1.
+// of columns 2t, 2t + 1; -inf marks one that adds nothing, whatever its score (for
+// columns past the heads 0 * inf, where a key is infinite).
 struct HeadBlock {
   uint4 q0, q1;
   float nl0, nl1;
@@ -88,8 +90,8 @@ struct HeadBlock {
     q0 = col < p.group ? __ldg(q + t) : zero;
     q1 = col < p.group ? __ldg(q + t + 4) : zero;
     auto neg = [&](int c) {
-      const float l = c < p.group ? __ldg(p.lse + row0 + c) : INFINITY;
-      return l == -INFINITY ? -INFINITY : -l * kLog2e;   // a row that sees nothing adds nothing
+      const float l = c < p.group ? __ldg(p.lse + row0 + c) : -INFINITY;
+      return l == INFINITY ? -FLT_MAX : l == -INFINITY ? -INFINITY : -l * kLog2e;
     };
     nl0 = neg(nb * 8 + 2 * t);
     nl1 = neg(nb * 8 + 2 * t + 1);
@@ -141,8 +143,11 @@ decode_mass_kernel(const MassParams p) {
       mma_bf16_16816(s, a1, q.q0.z, q.q0.w);
       mma_bf16_16816(s, a2, q.q1.x, q.q1.y);
       mma_bf16_16816(s, a3, q.q1.z, q.q1.w);
-      w_lo += ex2(fmaf(s[0], p.scale_log2, q.nl0)) + ex2(fmaf(s[1], p.scale_log2, q.nl1));
-      w_hi += ex2(fmaf(s[2], p.scale_log2, q.nl0)) + ex2(fmaf(s[3], p.scale_log2, q.nl1));
+      auto weight = [&](float score, float nl) {
+        return nl == -INFINITY ? 0.f : ex2(fmaf(score, p.scale_log2, nl));
+      };
+      w_lo += weight(s[0], q.nl0) + weight(s[1], q.nl1);
+      w_hi += weight(s[2], q.nl0) + weight(s[3], q.nl1);
     };
     if constexpr (kOneBlock) {
       add();

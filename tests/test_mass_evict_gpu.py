@@ -503,3 +503,25 @@ def test_mass_of_bounds_of_zero():
         call(mass)
         assert torch.isnan(mass[[0, 2]]).all()
         assert (mass[1] == 1).all()
+
+
+@pytest.mark.parametrize("heads", [(10, 2), (4, 1), (24, 1), (5, 1), (36, 2), (8, 1)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_infinite_keys_weigh_nothing_where_every_score_is_minus_infinity(heads, sign):
+    # key 20 holds an infinity, its score is -inf for every head: exp(-inf) = 0,
+    # for any number of heads
+    hq, hkv = heads
+    c = Paged([40], hq, hkv)
+    k, v, table, kv = c.paged()
+    k[table[0, 1].long(), :, 4, 9] = sign * float("inf")
+    q = bf16(c.rng, 2, hq, 64)
+    q[..., 9] = -sign
+    q = q.to(DEV)
+    cu = torch.tensor([0, 2], dtype=torch.int32, device=DEV)
+    lse = torch.full((2, hq), 3.0, device=DEV)
+    for call in (lambda m: sa.decode_mass(q[:1], k, table, kv, lse[:1], c.scale, 40, m),
+                 lambda m: sa.prefill_mass(q, cu, k, table, kv, lse, c.scale, 2, 40, m)):
+        mass = torch.ones(1, hkv, 40, device=DEV)
+        call(mass)
+        assert (mass[0, :, 20] == 1).all()
+        assert torch.isfinite(mass).all()
