@@ -72,7 +72,6 @@ struct WindowPrefillParams {
   unsigned inv_group;            // ceil(2^16 / group): i / group for i < 128
   int num_tiles;                 // query tiles per KV head, at most
   int tiles_each;                // > 0: request r has tiles r * tiles_each ..; 0: numbered through
-                                 // (window_prefill.cu only)
 };
 
 cudaError_t launch_window_prefill(const CUtensorMap &qmap, const CUtensorMap &kmap,

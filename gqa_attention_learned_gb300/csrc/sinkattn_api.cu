@@ -113,7 +113,9 @@ constexpr int kPrefillKvTile = 128;   // keys per prefill K/V tile
 constexpr int kWindowWaves = 1;       // windowed decode: split up to this many times the CTA slots (2:
                                       // 59.7 us instead of 50.7 for 8 requests of window 16384)
 constexpr int kWindowMinPages = 16;   // and no finer than this
-constexpr int kWalkSeqs = 128;        // windowed prefill: requests that a CTA walks over at most
+constexpr double kWalkSeqs = 128;     // windowed prefill: requests that a CTA walks over at the cost of one
+                                      // empty CTA per tile
+constexpr double kSparseTiles = 24;   // its persistent kernel: empty tiles at the cost of numbering one
 constexpr int kMassTiles = 16;        // prefill mass: query tiles that count as many
 constexpr int kMaxCluster = 8;        // portable cluster size
 constexpr int kMassPagesPerWarp = 8;  // decode mass: pages a warp takes, one CTA's share
@@ -827,19 +829,25 @@ int window_prefill_entry(const void *q, const int32_t *cu_seqlens_q, int num_seq
   p.first_tokens = std::min(first_tokens, p.max_kv_len);
   p.tile_tokens = tile_tokens;
   p.inv_group = static_cast<unsigned>((65536 + group - 1) / group);
-  // Query tiles: as many for each request as the longest may have, or, if that
-  // leaves many without rows, numbered through (a request has a tile for every
-  // tile_tokens tokens and one more at most).  That costs a CTA a walk over the
-  // requests and gains where lengths differ (64 / 8 heads, window 600, 64 prompts of
-  // up to 700 tokens: 286 us instead of 354; window 400, 128 of up to 300: 257
-  // instead of 283, 256 of up to 200: 370 instead of 351; window 1000, 1024 requests
-  // of 4 new tokens: 539 instead of 357).  The persistent kernel gains nothing.
+  // Query tiles: as many for each request as the bound on lengths allows, or, if
+  // that leaves too many without rows, those that exist, numbered through (a request
+  // has a tile for every tile_tokens tokens and one more at most).  Which costs more:
+  //   long windows: an empty CTA per missing tile against a walk over the requests
+  //     in every CTA.  (64 / 8 heads, window 600, tiles allowed / tiles numbered:
+  //     64 prompts of up to 300 tokens 237 / 193 us at 1.8 times as many, 3217 / 193 at
+  //     113; 256 of up to 200 636 / 593 at 1.7; 1024 of 4 261 / 614 at 0.8, 491 / 614
+  //     at 3.2, 1077 / 614 at 13; 4096 of 4 4276 / 9494 at 13, 12152 / 9494 at 51.)
+  //   short windows: the persistent kernel looks empty tiles up 32 at a time, numbered
+  //     ones singly.  (Window 128: 64 of up to 300 65 / 69 us at 7 times as many, 73 /
+  //     69 at 28, 248 / 69 at 452; 1024 of up to 100 352 / 390 at 12, 589 / 390 at 94.)
+  // Numbered, there are never too many for a launch, whatever the bound.
   const bool is_short = sa::window_prefill_is_short(p);
   const int tiles_each = std::max(1, ceil_div(max_q_len, tile_tokens));   // (one flags a request out of range)
+  const long long allowed = static_cast<long long>(tiles_each) * num_seqs;
   const long long numbered = static_cast<long long>(total_q / tile_tokens) + num_seqs;
-  const bool walk = !is_short && num_seqs <= kWalkSeqs &&
-                    static_cast<long long>(tiles_each) * num_seqs > numbered;
-  const long long tiles = walk ? numbered : static_cast<long long>(tiles_each) * num_seqs;
+  const double worth = is_short ? kSparseTiles : std::max(1.0, num_seqs / kWalkSeqs);
+  const bool walk = allowed > worth * numbered || allowed * num_kv_heads > 0x7fffffffll;
+  const long long tiles = walk ? numbered : allowed;
   if (tiles * num_kv_heads > 0x7fffffffll) return SINKATTN_UNSUPPORTED;
   p.num_tiles = static_cast<int>(tiles);
   p.tiles_each = walk ? 0 : tiles_each;

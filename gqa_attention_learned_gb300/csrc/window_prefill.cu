@@ -75,63 +75,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 2048, "barrier block");
 
-// The query tiles of a launch numbered through request by request; a request
-// whose arguments are out of range counts as one tile (its rows become NaN), and
-// so does one that starts before any earlier one, so there are never more than
-// num_tiles.  Numbering the tiles that exist matters: with an empty CTA for
-// every tile that a shorter request lacks, an SM's second slot stayed free while
-// CTAs waited (237 of 304 slots taken at a third of empty ones).
-// A warp holds 32 requests at a time, one per lane.
-template <bool kPaged>
-struct Walk {
-  Request r;
-  int from, tiles;             // this lane's tiles: [from, from + tiles)
-  int seq0 = -32, next = 0;    // first request held; tiles up to the last one held
-  int top = 0;                 // the largest start so far
-  __device__ __forceinline__ bool advance(const WindowPrefillParams &p) {
-    if (seq0 + 32 >= p.num_seqs) return false;
-    seq0 += 32;
-    const int lane = threadIdx.x & 31, seq = seq0 + lane;
-    const bool have = seq < p.num_seqs;
-    r = have ? Request::load<kPaged, false>(p, seq) : Request{};
-    int most = have ? r.q_start : top;
-    if (__any_sync(0xffffffffu, have && (r.q_start < top || r.q_len < 0))) {
-      most = max(most, top);
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, most, d);
-        if (lane >= d) most = max(most, x);
-      }
-      r.bad = r.bad || r.q_start < most;
-    }
-    top = __shfl_sync(0xffffffffu, most, min(31, p.num_seqs - 1 - seq0));
-    tiles = !have ? 0 : r.bad ? 1 : cdiv(r.q_len, p.tile_tokens);
-    int end = tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int x = __shfl_up_sync(0xffffffffu, end, d);
-      if (lane >= d) end += x;
-    }
-    from = next + end - tiles;
-    next += __shfl_sync(0xffffffffu, end, 31);
-    return true;
-  }
-  // The request with tile `i` of those held, and its first tile's number; i the
-  // same for all lanes.  (The last lane with from <= i, as lanes without tiles start
-  // where the next one does.)
-  __device__ __forceinline__ Request request(int i, int &first) const {
-    const int lane = 31 - __clz(__ballot_sync(0xffffffffu, from <= i));
-    Request x;
-    x.seq = seq0 + lane;
-    x.q_start = __shfl_sync(0xffffffffu, r.q_start, lane);
-    x.q_len = __shfl_sync(0xffffffffu, r.q_len, lane);
-    x.kv_len = __shfl_sync(0xffffffffu, r.kv_len, lane);
-    x.bad = __shfl_sync(0xffffffffu, static_cast<int>(r.bad), lane) != 0;
-    first = __shfl_sync(0xffffffffu, from, lane);
-    return x;
-  }
-};
-
 // Running softmax of a row: reference max m (base 2) that P and the
 // tensor-memory O are relative to, sum d.  m starts at the sink and moves only
 // when a row max exceeds it by more than kRescaleLog2.
@@ -246,9 +189,7 @@ window_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     if (req.bad ? qt != 0 : qt * p.tile_tokens >= req.q_len) return;
   } else {
     Walk<kPaged> walk;
-    do {
-      if (!walk.advance(p)) return;
-    } while (walk.next <= item);
+    if (!walk.reach(p, item)) return;
     int first;
     req = walk.request(item, first);
     qt = cdiv(req.q_len, p.tile_tokens) - 1 - (item - first);

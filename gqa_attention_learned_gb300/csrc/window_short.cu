@@ -146,73 +146,92 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   if (warp == kLoadWarp) {
     // -------------------------------------------------------------- loads
     int n = 0;                                           // tiles handed out
+    // tile qt of a request and a KV head into the next stages; false: a wait ran out
+    auto hand_out = [&](const Request &r, int qt, int kvh) -> bool {
+      Work w;
+      w.req = r;
+      w.kvh = kvh;
+      w.tile = Tile::make<kPaged>(p, r, qt);
+      w.stop = 0;
+      const bool have = lane < w.tile.n_boxes;
+      const int src = have ? w.tile.source<kPaged>(p, r, lane) : -1;
+      const unsigned boxes = __ballot_sync(0xffffffffu, src >= 0);
+      w.bad = __popc(boxes) != w.tile.n_boxes;
+      uint64_t *k_full = &bar.k_full[n % kNK], *v_full = &bar.v_full[n % kNV];
+      // the geometry goes by V stage, so that one has to be free first
+      if ((n >= kNV && !wait(&bar.v_empty[n % kNV], n / kNV + 1)) ||
+          (n >= kNK && !wait(&bar.k_empty[n % kNK], n / kNK + 1)))
+        return false;
+      if (lane == 0) {
+        // for the softmax warps by the arrival on info, for the products' by
+        // k_full's.  (Not for both by k_full: its stage may be filled twice more
+        // while the softmax warps are behind.  info goes by V stage: its next
+        // arrival there needs v_empty, where all of them arrive after they have
+        // seen this one, so no phase is passed over unseen.)
+        bar.work[n % kNV] = w;
+        mbar_arrive(&bar.info[n % kNV]);
+        const uint32_t bytes = __popc(boxes) * kBoxBytes;
+        mbar_arrive_expect_tx(k_full, p.tile_tokens * p.group * kHeadDim * 2 + bytes);
+        mbar_arrive_expect_tx(v_full, bytes);
+        // box {64, group, tile_tokens}: rows (token, head)
+        tma_load_3d(sQ(n), &qmap, k_full, 0, kvh * p.group, r.q_start + w.tile.i0);
+      }
+      __syncwarp();
+      if (src >= 0) {
+        const int y = kPaged ? kvh * kPageSize : kvh;
+        tma_load_3d(sK(n) + lane * kBoxBytes, &kmap, k_full, 0, y, src);
+        tma_load_3d(sV(n) + lane * kBoxBytes, &vmap, v_full, 0, y, src);
+      }
+      __syncwarp();
+      ++n;
+      return true;
+    };
     bool ok = true;
-    for (int base = static_cast<int>(blockIdx.x); ok && base < items;) {
-      // 32 items at a time, one per lane: most ragged batches have empty ones
-      const long long mine = base + static_cast<long long>(lane) * stride;
-      const int tile_no = mine < items ? static_cast<int>(mine) / p.num_kv_heads : -1;
-      const int kvh = static_cast<int>(mine) - tile_no * p.num_kv_heads;
-      bool valid = false, poisoned = false;
-      int qt = 0;
-      Request r{};
-      if (tile_no >= 0) {
-        const int seq = tile_no / p.tiles_each;
-        r = Request::load<kPaged>(p, seq);
-        qt = tile_no - seq * p.tiles_each;
-        valid = !r.bad && qt * p.tile_tokens < r.q_len;
-        poisoned = r.bad && qt == 0;
+    if (p.tiles_each == 0) {
+      Walk<kPaged> walk;
+      for (long long item = blockIdx.x; ok && item < items; item += stride) {
+        const int tile_no = static_cast<int>(item) / p.num_kv_heads;
+        const int kvh = static_cast<int>(item) - tile_no * p.num_kv_heads;
+        if (!walk.reach(p, tile_no)) break;
+        int first;
+        const Request r = walk.request(tile_no, first);
+        if (r.bad) poison(p, kvh, r.q_start, max(r.q_len, 0), lane, 32);
+        else ok = hand_out(r, tile_no - first, kvh);
       }
-      for (unsigned m = __ballot_sync(0xffffffffu, poisoned); m; m &= m - 1) {
-        const int l = __ffs(m) - 1;
-        poison(p, __shfl_sync(0xffffffffu, kvh, l), __shfl_sync(0xffffffffu, r.q_start, l),
-               max(__shfl_sync(0xffffffffu, r.q_len, l), 0), lane, 32);
+    } else {
+      for (int base = static_cast<int>(blockIdx.x); ok && base < items;) {
+        // 32 items at a time, one per lane: most ragged batches have empty ones
+        const long long mine = base + static_cast<long long>(lane) * stride;
+        const int tile_no = mine < items ? static_cast<int>(mine) / p.num_kv_heads : -1;
+        const int kvh = static_cast<int>(mine) - tile_no * p.num_kv_heads;
+        bool valid = false, poisoned = false;
+        int qt = 0;
+        Request r{};
+        if (tile_no >= 0) {
+          const int seq = tile_no / p.tiles_each;
+          r = Request::load<kPaged>(p, seq);
+          qt = tile_no - seq * p.tiles_each;
+          valid = !r.bad && qt * p.tile_tokens < r.q_len;
+          poisoned = r.bad && qt == 0;
+        }
+        for (unsigned m = __ballot_sync(0xffffffffu, poisoned); m; m &= m - 1) {
+          const int l = __ffs(m) - 1;
+          poison(p, __shfl_sync(0xffffffffu, kvh, l), __shfl_sync(0xffffffffu, r.q_start, l),
+                 max(__shfl_sync(0xffffffffu, r.q_len, l), 0), lane, 32);
+        }
+        for (unsigned m = __ballot_sync(0xffffffffu, valid); ok && m; m &= m - 1) {
+          const int l = __ffs(m) - 1;
+          Request x;
+          x.seq = __shfl_sync(0xffffffffu, r.seq, l);
+          x.q_start = __shfl_sync(0xffffffffu, r.q_start, l);
+          x.q_len = __shfl_sync(0xffffffffu, r.q_len, l);
+          x.kv_len = __shfl_sync(0xffffffffu, r.kv_len, l);
+          x.bad = false;
+          ok = hand_out(x, __shfl_sync(0xffffffffu, qt, l), __shfl_sync(0xffffffffu, kvh, l));
+        }
+        if (items - base <= 32ll * stride) break;
+        base += 32 * stride;
       }
-      for (unsigned m = __ballot_sync(0xffffffffu, valid); ok && m; m &= m - 1, ++n) {
-        const int l = __ffs(m) - 1;
-        Work w;
-        w.req.seq = __shfl_sync(0xffffffffu, r.seq, l);
-        w.req.q_start = __shfl_sync(0xffffffffu, r.q_start, l);
-        w.req.q_len = __shfl_sync(0xffffffffu, r.q_len, l);
-        w.req.kv_len = __shfl_sync(0xffffffffu, r.kv_len, l);
-        w.req.bad = false;
-        w.kvh = __shfl_sync(0xffffffffu, kvh, l);
-        w.tile = Tile::make<kPaged>(p, w.req, __shfl_sync(0xffffffffu, qt, l));
-        w.stop = 0;
-        const bool have = lane < w.tile.n_boxes;
-        const int src = have ? w.tile.source<kPaged>(p, w.req, lane) : -1;
-        const unsigned boxes = __ballot_sync(0xffffffffu, src >= 0);
-        w.bad = __popc(boxes) != w.tile.n_boxes;
-        uint64_t *k_full = &bar.k_full[n % kNK], *v_full = &bar.v_full[n % kNV];
-        // the geometry goes by V stage, so that one has to be free first
-        if ((n >= kNV && !wait(&bar.v_empty[n % kNV], n / kNV + 1)) ||
-            (n >= kNK && !wait(&bar.k_empty[n % kNK], n / kNK + 1))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          // for the softmax warps by the arrival on info, for the products' by
-          // k_full's.  (Not for both by k_full: its stage may be filled twice more
-          // while the softmax warps are behind.  info goes by V stage: its next
-          // arrival there needs v_empty, where all of them arrive after they have
-          // seen this one, so no phase is passed over unseen.)
-          bar.work[n % kNV] = w;
-          mbar_arrive(&bar.info[n % kNV]);
-          const uint32_t bytes = __popc(boxes) * kBoxBytes;
-          mbar_arrive_expect_tx(k_full, p.tile_tokens * p.group * kHeadDim * 2 + bytes);
-          mbar_arrive_expect_tx(v_full, bytes);
-          // box {64, group, tile_tokens}: rows (token, head)
-          tma_load_3d(sQ(n), &qmap, k_full, 0, w.kvh * p.group, w.req.q_start + w.tile.i0);
-        }
-        __syncwarp();
-        if (src >= 0) {
-          const int y = kPaged ? w.kvh * kPageSize : w.kvh;
-          tma_load_3d(sK(n) + lane * kBoxBytes, &kmap, k_full, 0, y, src);
-          tma_load_3d(sV(n) + lane * kBoxBytes, &vmap, v_full, 0, y, src);
-        }
-        __syncwarp();
-      }
-      if (items - base <= 32ll * stride) break;
-      base += 32 * stride;
     }
     // one last entry per slot
     for (int l = 0; ok && l < kSlots; ++l, ++n) {
@@ -411,10 +430,19 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   }
   if (bar.dead) {
     // a wait ran out: none of this CTA's tiles can be trusted
+    Walk<kPaged> walk;
     for (long long item = blockIdx.x; item < items; item += stride) {
       const int tile_no = static_cast<int>(item) / p.num_kv_heads;
-      const Request r = Request::load<kPaged>(p, tile_no / p.tiles_each);
-      const int i0 = (tile_no - r.seq * p.tiles_each) * p.tile_tokens;
+      Request r;
+      int first = tile_no;
+      if (p.tiles_each == 0) {
+        if (!walk.reach(p, tile_no)) break;
+        r = walk.request(tile_no, first);
+      } else {
+        r = Request::load<kPaged>(p, tile_no / p.tiles_each);
+        first -= tile_no % p.tiles_each;
+      }
+      const int i0 = (tile_no - first) * p.tile_tokens;
       if (!r.bad && i0 < r.q_len)
         poison(p, static_cast<int>(item) - tile_no * p.num_kv_heads, r.q_start + i0,
                min(p.tile_tokens, r.q_len - i0), threadIdx.x, kThreads);

@@ -512,3 +512,58 @@ def test_requests_longer_than_a_bound_of_zero_give_nan(window):
         call(out=out, lse=lse)
         assert torch.isnan(out[:8]).all() and torch.isnan(lse[:8]).all()
         assert (out[8:] == 7).all() and (lse[8:] == 7).all()
+
+
+# ----------------------------------------------------------------- loose bounds
+@pytest.mark.parametrize("heads,window,requests", [((64, 8), 20, 2), ((64, 8), 20, 150), ((64, 8), 400, 150),
+                                                   ((128, 1), 20, 40), ((6, 2), 100, 200)])
+def test_prefill_window_bounds_need_not_be_tight(heads, window, requests):
+    # lengths far below the bounds, and no bounds: the same rows, whatever the
+    # number of requests and of tiles that none of them has; requests that are refused
+    # stay refused, rows behind the last request stay as they are
+    hq, hkv = heads
+    rng = np.random.default_rng(requests)
+    lens = [int(n) for n in rng.integers(0, 30, requests)]
+    lens[0], lens[1] = 40, 130
+    prefix = [int(n) for n in rng.integers(0, 60, requests)]
+    prefix[1] = 500
+    bad = requests // 2 if requests > 2 else None
+    c = Paged([a + b for a, b in zip(lens, prefix)], hq, hkv, seed=window)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    total = int(cu[-1])
+    q = bf16(c.rng, total + 9, hq, 64).to(DEV)
+    cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    sinks, paged = c.sinks.to(DEV), c.paged()
+    k, v = (torch.cat(x)[:total + 9].to(DEV).contiguous() for x in (c.k, c.v))
+    if bad:
+        paged[3][bad] = -1
+    parts = [slice(a, b) for a, b in zip(cu.tolist(), cu.tolist()[1:])]
+    nan = torch.zeros(total, dtype=torch.bool)
+    if bad:
+        nan[parts[bad]] = True
+    held = ((c.k, c.v, prefix), ([k[p] for p in parts], [v[p] for p in parts], [0] * requests))
+    refs = [_prefill_ref(kv[:2], q[:total], cu.tolist(), kv[2], np64(c.sinks), c.scale, window, 3) for kv in held]
+    # Rows that see few keys: weights p and the output are rounded to bf16, each off by at
+    # most 2^-8 of its value, so out = sum p v is off by at most 2^-8 (sum p |v| + |out|), and
+    # sum p <= 1 bounds the first sum by the largest |v| of the request; 5% on top for the
+    # second order (2^-8) and fp32 (scores of 64 products are off by less than 1e-4).
+    bars = []
+    for (_, vs, _), (ref, _) in zip(held, refs):
+        top = [np.abs(np64(x)).max(0) if len(x) else np.zeros((hkv, 64)) for x in vs]
+        top = np.concatenate([np.broadcast_to(t, (n, hkv, 64)) for t, n in zip(top, lens)])
+        bars.append(1.05 * 2.0**-8 * (np.repeat(top, hq // hkv, 1) + np.abs(ref)))
+    out, lse = torch.empty_like(q), torch.empty(total + 9, hq, device=DEV)
+    for ragged, bounds in ((0, (130, c.max_kv)), (0, (5000, c.max_kv)), (0, (2**40, c.max_kv)), (0, (2**40, 2**40)),
+                           (1, (130,)), (1, (700,)), (1, (131072,)), (1, (2**40,))):
+        out.fill_(7)
+        lse.fill_(7)
+        if ragged:
+            sa.prefill_window(q, k, v, cu, sinks, c.scale, *bounds, window, 3, out=out, lse=lse)
+        else:
+            sa.prefill_paged_window(q, cu, *paged, sinks, c.scale, *bounds, window, 3, out=out, lse=lse)
+        refused = nan if not ragged else torch.zeros_like(nan)
+        assert torch.isnan(out[:total][refused]).all() and torch.isnan(lse[:total][refused]).all()
+        fine = (~refused).numpy()
+        assert (np.abs(np64(out[:total])[fine] - refs[ragged][0][fine]) <= bars[ragged][fine]).all()
+        assert_lse_close(lse[:total][~refused], refs[ragged][1][fine])
+        assert (out[total:] == 7).all() and (lse[total:] == 7).all()
