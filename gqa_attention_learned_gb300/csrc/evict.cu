@@ -217,7 +217,7 @@ evict_select_kernel(const EvictParams p) {
   grid_dependency_wait();
   const int n = p.kv_lens[b];
   int *kept = p.kept + static_cast<size_t>(unit) * p.budget;
-  const int npages = cdiv(max(n, 0), kPageSize);
+  const int npages = cdiv(min(max(n, 0), p.max_kv_len), kPageSize);
   const int count = min(n, p.budget);
   const int dst_pages = cdiv(max(count, 0), kPageSize);
   bool bad = n < 0 || n > p.max_kv_len || n > p.mass_stride || count > p.dst_mass_stride ||
@@ -234,7 +234,9 @@ evict_select_kernel(const EvictParams p) {
   bad = __syncthreads_or(bad);                           // the same in every CTA of the cluster
   if (tid == 0 && rank == 0 && kvh == 0) p.new_kv_lens[b] = bad ? -1 : count;
   const int step = split * kSelectThreads;
-  for (int i = (bad ? 0 : count) + rank * kSelectThreads + tid; i < p.budget; i += step) kept[i] = -1;
+  // (unsigned: a budget may be the largest int)
+  for (unsigned i = (bad ? 0 : count) + rank * kSelectThreads + tid; i < static_cast<unsigned>(p.budget); i += step)
+    kept[i] = -1;
   if (bad) return;
   if (n <= p.budget) {
     for (int i = rank * kSelectThreads + tid; i < n; i += step) kept[i] = i;

@@ -60,7 +60,7 @@ __device__ __forceinline__ bool bad_request(const MassParams &p, int kv_len) {
 
 // NaN over the whole mass row of a request whose arguments are out of range.
 __device__ __forceinline__ void poison_row(const MassParams &p, float *row) {
-  for (int j = threadIdx.x; j < p.mass_stride; j += blockDim.x) row[j] = NAN;
+  for (unsigned j = threadIdx.x; j < static_cast<unsigned>(p.mass_stride); j += blockDim.x) row[j] = NAN;
 }
 
 // ------------------------------------------------------------------ decode

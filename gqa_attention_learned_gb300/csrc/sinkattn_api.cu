@@ -233,8 +233,8 @@ int clear_wide_counters(const DecodePlan &plan, void *workspace, cudaStream_t st
   return cuda_status(cudaMemsetAsync(workspace, 0, plan.counters_bytes, stream), "merge counter clear");
 }
 
-// A bound on lengths as the windowed kernels take it: "no bound" is the largest
-// that they can still round up to whole pages and tiles.
+// A bound on lengths as the kernels of bounded contexts take it: "no bound" is the
+// largest that they can still round up to whole pages and tiles.
 int longest(int bound) { return std::min(bound, 0x7fff0000); }
 
 // Windowed decode: CTAs of 8 or 16 query heads over the pages with a visible
@@ -888,7 +888,7 @@ int mass_params(sa::MassParams &p, const void *q, const void *k_cache, const int
   p.scale_log2 = scale * sa::kLog2e;
   p.num_seqs = num_seqs;
   p.total_q = total_q;
-  p.max_kv_len = max_kv_len;
+  p.max_kv_len = longest(max_kv_len);
   p.num_qo_heads = num_qo_heads;
   p.num_kv_heads = num_kv_heads;
   p.group = num_qo_heads / num_kv_heads;
@@ -1039,7 +1039,7 @@ int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *page_table, int 
   p.batch = batch;
   p.num_kv_heads = num_kv_heads;
   p.num_pages = num_pages;
-  p.max_kv_len = max_kv_len;
+  p.max_kv_len = longest(max_kv_len);
   p.max_pages_per_seq = max_pages_per_seq;
   p.dst_max_pages = dst_max_pages_per_seq;
   p.mass_stride = mass_stride;

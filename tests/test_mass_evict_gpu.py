@@ -525,3 +525,34 @@ def test_infinite_keys_weigh_nothing_where_every_score_is_minus_infinity(heads, 
         call(mass)
         assert (mass[0, :, 20] == 1).all()
         assert torch.isfinite(mass).all()
+
+
+# ------------------------------------------------------------- the largest sizes
+def test_lengths_and_budgets_up_to_the_largest_int():
+    # rows of 2^31 - 1 entries: a length that fits them but not its page table is out of
+    # range, and what is written over a whole row ends at its end
+    top = 2**31 - 1
+    c = Paged([5], 4, 1)
+    k, v, table, kv = c.paged()
+    q, lse = bf16(c.rng, 1, 4, 64).to(DEV), torch.zeros(1, 4, device=DEV)
+    cu = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    mass = torch.empty(1, 1, top, device=DEV)
+    for length in (top, top - 7, -1):
+        kv[0] = length
+        for call in (lambda: sa.decode_mass(q, k, table, kv, lse, c.scale, top, mass),
+                     lambda: sa.prefill_mass(q, cu, k, table, kv, lse, c.scale, 1, top, mass)):
+            mass.zero_()
+            call()
+            for at in (slice(0, 4096), slice(top // 2, top // 2 + 4096), slice(top - 4096, top)):
+                assert torch.isnan(mass[0, 0, at]).all()
+        before = (k.clone(), v.clone())
+        new, kept = sa.evict(k, v, table, kv, mass, 4, top)
+        assert new.tolist() == [-1] and (kept == -1).all()
+        assert torch.equal(k.view(torch.int16), before[0].view(torch.int16))
+        assert torch.equal(v.view(torch.int16), before[1].view(torch.int16))
+    kv[0] = 5
+    kept = torch.zeros(1, 1, top, dtype=torch.int32, device=DEV)
+    new, _ = sa.evict(k, v, table, kv, mass, top, top, kept=kept)
+    assert new.tolist() == [5] and kept[0, 0, :5].tolist() == [0, 1, 2, 3, 4]
+    for at in (slice(5, 4096), slice(top // 2, top // 2 + 4096), slice(top - 4096, top)):
+        assert (kept[0, 0, at] == -1).all()
