@@ -85,7 +85,7 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 
-template <bool kPaged, typename Sh>
+template <bool kPaged, bool kNumbered, typename Sh>     // kNumbered: p.tiles_each == 0
 __global__ void __launch_bounds__(Sh::kThreads, 1)
 window_short_kernel(const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap,
@@ -187,7 +187,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       return true;
     };
     bool ok = true;
-    if (p.tiles_each == 0) {
+    if constexpr (kNumbered) {
       Walk<kPaged> walk;
       for (long long item = blockIdx.x; ok && item < items; item += stride) {
         const int tile_no = static_cast<int>(item) / p.num_kv_heads;
@@ -435,7 +435,7 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
       const int tile_no = static_cast<int>(item) / p.num_kv_heads;
       Request r;
       int first = tile_no;
-      if (p.tiles_each == 0) {
+      if constexpr (kNumbered) {
         if (!walk.reach(p, tile_no)) break;
         r = walk.request(tile_no, first);
       } else {
@@ -450,16 +450,27 @@ window_short_kernel(const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-template <bool kPaged, typename Sh>
+template <bool kPaged, bool kNumbered, typename Sh>
 cudaError_t launch_variant(const CUtensorMap &qmap, const CUtensorMap &kmap,
                            const CUtensorMap &vmap, const WindowPrefillParams &p, int num_sms,
                            cudaStream_t stream) {
-  cudaError_t err = set_smem_once<window_short_kernel<kPaged, Sh>>(Sh::kSmemBytes);
+  cudaError_t err = set_smem_once<window_short_kernel<kPaged, kNumbered, Sh>>(Sh::kSmemBytes);
   if (err != cudaSuccess) return err;
   const int items = p.num_tiles * p.num_kv_heads;
-  return launch_kernel(window_short_kernel<kPaged, Sh>,
+  return launch_kernel(window_short_kernel<kPaged, kNumbered, Sh>,
                        static_cast<unsigned>(std::min(items, num_sms)), Sh::kThreads,
                        Sh::kSmemBytes, stream, false, qmap, kmap, vmap, p);
+}
+
+template <typename Sh>
+cudaError_t launch_shape(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                         const WindowPrefillParams &p, int num_sms, cudaStream_t stream) {
+  const bool numbered = p.tiles_each == 0;
+  if (p.page_table)
+    return numbered ? launch_variant<true, true, Sh>(qmap, kmap, vmap, p, num_sms, stream)
+                    : launch_variant<true, false, Sh>(qmap, kmap, vmap, p, num_sms, stream);
+  return numbered ? launch_variant<false, true, Sh>(qmap, kmap, vmap, p, num_sms, stream)
+                  : launch_variant<false, false, Sh>(qmap, kmap, vmap, p, num_sms, stream);
 }
 
 using Three = Shape<3, 10, 3, 5>;
@@ -481,11 +492,8 @@ bool window_prefill_is_short(const WindowPrefillParams &p) { return most_boxes(p
 cudaError_t launch_window_short(const CUtensorMap &qmap, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, const WindowPrefillParams &p, int num_sms,
                                 cudaStream_t stream) {
-  if (most_boxes(p) <= Three::kBoxes)
-    return p.page_table ? launch_variant<true, Three>(qmap, kmap, vmap, p, num_sms, stream)
-                        : launch_variant<false, Three>(qmap, kmap, vmap, p, num_sms, stream);
-  return p.page_table ? launch_variant<true, Two>(qmap, kmap, vmap, p, num_sms, stream)
-                      : launch_variant<false, Two>(qmap, kmap, vmap, p, num_sms, stream);
+  return most_boxes(p) <= Three::kBoxes ? launch_shape<Three>(qmap, kmap, vmap, p, num_sms, stream)
+                                        : launch_shape<Two>(qmap, kmap, vmap, p, num_sms, stream);
 }
 
 }  // namespace sa
