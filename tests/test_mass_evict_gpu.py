@@ -556,3 +556,36 @@ def test_lengths_and_budgets_up_to_the_largest_int():
     assert new.tolist() == [5] and kept[0, 0, :5].tolist() == [0, 1, 2, 3, 4]
     for at in (slice(5, 4096), slice(top // 2, top // 2 + 4096), slice(top - 4096, top)):
         assert (kept[0, 0, at] == -1).all()
+
+
+def test_the_calls_allocate_nothing_when_handed_their_outputs():
+    c = Paged([700, 300], 16, 2, spare=20)
+    q, q1, sinks = bf16(c.rng, 60, 16, 64).to(DEV), bf16(c.rng, 2, 16, 64).to(DEV), c.sinks.to(DEV)
+    k, v, table, kv = c.paged()
+    cu = torch.tensor([0, 40, 60], dtype=torch.int32, device=DEV)
+    out, lse, out1, lse1 = (torch.empty_like(x) for x in (q, q[..., 0].float(), q1, q1[..., 0].float()))
+    kk, vv = (x[0][:60].to(DEV) for x in (c.k, c.v))
+    mass = torch.zeros(2, 2, 700, device=DEV)
+    new, kept = torch.empty_like(kv), torch.empty(2, 2, 650, dtype=torch.int32, device=DEV)
+    splits, need = sa.decode_window_plan(2, 16, 2, 700, 600, 4, 5)
+    assert splits > 1
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+
+    def run():
+        sa.decode_window(q1, k, v, table, kv, sinks, c.scale, 700, 600, 4, num_splits=5, out=out1, lse=lse1, workspace=ws)
+        for window in (20, 500):
+            sa.prefill_window(q, kk, vv, cu, sinks, c.scale, 40, window, out=out, lse=lse)
+            sa.prefill_paged_window(q, cu, k, v, table, kv, sinks, c.scale, 40, 700, window, out=out, lse=lse)
+        sa.prefill_mass(q, cu, k, table, kv, lse, c.scale, 40, 700, mass)
+        sa.decode_mass(q1, k, table, kv, lse1, c.scale, 700, mass)
+        sa.evict(k, v, table, kv, mass, 650, 700, new_kv_lens=new, kept=kept)
+
+    def held():
+        torch.cuda.synchronize()
+        return torch.cuda.memory_stats()["allocation.all.allocated"], torch.cuda.mem_get_info()[0]
+
+    run()                                                 # kernels are loaded on their first launch
+    before = held()
+    for _ in range(3):
+        run()
+    assert held() == before
