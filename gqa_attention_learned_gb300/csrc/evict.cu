@@ -16,10 +16,10 @@
 //   wave of CTAs costs more than longer shares do.
 // move: copies rows by that list, whole 128-byte rows.  A row that one CTA
 //   selects is moved by it as well, K and V side by side (64 rows of up to 4096
-//   keys, 8 heads, cut to 1024: 53 us, 4.5 TB/s, against 60 us with a second
+//   keys, 8 heads, cut to 1024: 50 us, 4.8 TB/s, against 60 us with a second
 //   kernel); where a cluster shares a row a second kernel, launched under the
 //   first one's end, moves K, V and mass in CTAs of their own with 64 KB in
-//   flight (8 rows of up to 131072 keys cut to 8192: 95 us, 40% of it the
+//   flight (8 rows of up to 131072 keys cut to 8192: 91 us, 40% of it the
 //   selection's 5 passes over each weight, bound by their instructions).  In
 //   place is safe because the r-th kept key has index >= r: a batch of rows is
 //   read whole before any of it is written, and a write to slot r can only hit

@@ -31,7 +31,7 @@
 // pairs, whose K tiles stream as well.
 //
 // Measured (64 / 8 heads): decode_mass 24 us for 64 requests of up to 4096 keys
-// and 106 us for 8 of up to 131072 (6.4 and 6.5 TB/s).  prefill_mass 217 us for 4
+// and 106 us for 8 of up to 131072 (6.4 and 6.5 TB/s).  prefill_mass 218 us for 4
 // whole prompts of up to 4096 tokens, 80 us for the last 32 tokens of 8 prompts
 // of up to 32k: the exponential unit is busy 58% of the time and no single part
 // binds (without exponentials 172 us, without reading lse 205, with a quarter of

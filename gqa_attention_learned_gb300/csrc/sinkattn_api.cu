@@ -238,7 +238,7 @@ int clear_wide_counters(const DecodePlan &plan, void *workspace, cudaStream_t st
 int longest(int bound) { return std::min(bound, 0x7fff0000); }
 
 // Windowed decode: CTAs of 8 or 16 query heads over the pages with a visible
-// key; split only while the CTAs do not fill the GPU twice, and into chunks of
+// key; split only while the CTAs do not fill the GPU once, and into chunks of
 // at least kWindowMinPages pages.
 DecodePlan plan_window_decode(int batch, int num_qo_heads, int num_kv_heads, int max_kv_len,
                               int window, int first_tokens, int num_sms, int requested) {

@@ -25,10 +25,10 @@
 // loads Q and K and issues S = Q K^T, warp 5 loads V and issues O += P V,
 // warps 0..3 run the online softmax, one thread per row, between them.
 //
-// Measured (64 / 8 heads): 561 us for 4 chunks of 2048 new tokens on up to 14336
-// cached ones with window 4096, 912 TFLOP/s of the pairs that are seen: tensor pipe
+// Measured (64 / 8 heads): 563 us for 4 chunks of 2048 new tokens on up to 14336
+// cached ones with window 4096, 910 TFLOP/s of the pairs that are seen: tensor pipe
 // 52%, exponential unit 40%, issue slots 50% busy; as in plain prefill the tile's
-// chain of S, softmax, P V binds.  Few tiles per CTA cost more: 59 us for 7.6k
+// chain of S, softmax, P V binds.  Few tiles per CTA cost more: 57 us for 7.6k
 // tokens of 16 / 2 heads with window 1023 (16.5 us by the tensor peak), where a CTA
 // lasts 30k cycles, 2.4k for each of its 9 tiles and the rest for its start and end.
 

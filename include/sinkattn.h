@@ -463,6 +463,7 @@ SINKATTN_API int sinkattn_prefill_paged_window(const void *q, const int32_t *cu_
  *                 max_kv_len; entry j of a row belongs to key j of the request.
  *                 Entries from kv_len on are neither read nor written.
  *   lse         : fp32 [rows][num_qo_heads]; a row with lse = -inf adds nothing
+ *                 to a key that is finite
  *   other arguments as for the attention call of the same form
  * Sums are in fp32 and in a fixed order: equal calls give equal bits.  No two
  * calls that add to the same mass may overlap on the GPU.  A request whose
