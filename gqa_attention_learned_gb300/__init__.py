@@ -71,11 +71,23 @@ SIGNATURES = {
                              [_c_int] * 8 + [_vp]),
     "sinkattn_prefill_mass": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _vp,
                                        _c_int, _c_int, _vp, _c_float, _vp] + [_c_int] * 5 + [_vp]),
+    "sinkattn_int4_workspace_bytes": (_c_int, [_c_int, ctypes.POINTER(_c_size)]),
+    "sinkattn_qkv_prologue_int4": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _vp, _vp] +
+                                   [_c_int] * 6 + [_vp]),
+    "sinkattn_gather_int4": (_c_int, [_vp, _vp, _c_int, _vp, _vp] + [_c_int] * 4 + [_vp]),
+    "sinkattn_decode_int4": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_float, _vp, _vp] +
+                             [_c_int] * 7 + [_vp, _c_size, _c_int, _vp]),
+    "sinkattn_verify_int4": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _vp, _c_float, _vp, _vp] +
+                             [_c_int] * 8 + [_vp, _c_size, _c_int, _vp]),
+    "sinkattn_prefill_paged_int4": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int,
+                                             _vp, _c_int, _c_int, _vp, _c_float, _vp, _vp] +
+                                    [_c_int] * 4 + [_vp, _c_size, _vp]),
     "sinkattn_evict": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                                 _vp, _c_int, _vp, _c_int, _vp, _vp] + [_c_int] * 6 + [_vp]),
 }
 
 STATIC_SCRATCH_BYTES = 16 << 20
+INT4_BLOCK_BYTES = 1088
 LAUNCH_DEFAULT, LAUNCH_PLAIN, LAUNCH_PROGRAMMATIC = 0, 1, 2
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 MAX_VERIFY_TOKENS = 64
@@ -717,3 +729,207 @@ def evict(k_cache, v_cache, page_table, kv_lens, mass, budget, max_kv_len, *, fi
             0 if dst_mass is None else dst_mass.shape[2], _ptr(new_kv_lens), _ptr(kept), batch,
             hkv, d, page, num_pages, _size(max_kv_len, "max_kv_len"), _raw_stream(dev)))
     return new_kv_lens, kept
+
+
+# ---------------------------------------------- a paged cache held in 4 bits
+_U8 = torch.uint8
+
+
+def int4_cache(num_pages, num_kv_heads, device="cuda"):
+    """A paged cache held in 4 bits, empty: uint8 [pages, Hkv, 1088], K and V
+    together, 68 bytes per key and KV head (bf16: 256).  Each row of 64 values is
+    codes of 4 bits, a scale and a zero point; every value that a row can stand for
+    is a bf16 number.  The block's layout is in include/sinkattn.h."""
+    return torch.zeros(num_pages, num_kv_heads, INT4_BLOCK_BYTES, dtype=_U8, device=device)
+
+
+def rope_table(inv_freq, mscale, num_positions, device="cuda"):
+    """cos and sin of positions 0 .. num_positions - 1 for `qkv_prologue_int4`: fp32
+    [positions, 64] (32 cosines, 32 sines, times mscale), computed in 64 bits.
+    inv_freq, mscale: from `yarn_table`, say.  One table serves all layers."""
+    freq = torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+    angle = torch.arange(num_positions, dtype=torch.float64, device=device)[:, None] * freq
+    return (float(mscale) * torch.cat([angle.cos(), angle.sin()], 1)).float()
+
+
+def _int4_workspace_bytes(num_sms=0):
+    w = _c_size(0)
+    _check("sinkattn_int4_workspace_bytes",
+           load().sinkattn_int4_workspace_bytes(num_sms, ctypes.byref(w)))
+    return w.value
+
+
+def int4_workspace_bytes(num_sms=0):
+    """Bytes of the workspace that `decode_int4`, `verify_int4` and `prefill_paged_int4`
+    need, whatever their sizes (num_sms 0: for the current device).  It must be
+    zero-filled before its first use (torch.zeros)."""
+    return _int4_workspace_bytes(num_sms)
+
+
+def _int4_cache(kv_cache, dev, d=64):
+    if not _is(kv_cache, _U8, 3, dev) or dev.type != "cuda":
+        _want(kv_cache, "kv_cache", _U8, 3, dev)
+    if kv_cache.shape[2] != INT4_BLOCK_BYTES or d != 64:
+        raise ValueError(f"kv_cache must be [pages, Hkv, {INT4_BLOCK_BYTES}] and head_dim 64, got "
+                         f"{list(kv_cache.shape)} and {d}")
+
+
+def qkv_prologue_int4(qkv, bias, positions, slot_mapping, rope, kv_cache, num_qo_heads, num_kv_heads, *,
+                      rope_style=ROPE_HALF, q_out=None, stream=None):
+    """`qkv_prologue` into a cache held in 4 bits: QKV bias, rotary encoding of q and
+    k, and k/v rows quantised into their slots, one launch.  rope: fp32
+    [positions, 64] from `rope_table` (a position outside of it gives NaN).
+    Returns q_out [T, Hq, 64] bf16; kv_cache is written in place."""
+    dev = qkv.device
+    tokens = qkv.shape[0]
+    if not (_is(qkv, _BF16, 2, dev) and _is(positions, _I32, 1, dev) and _is(slot_mapping, _I32, 1, dev)
+            and _is(rope, _F32, 2, dev) and (bias is None or _is(bias, _BF16, 1, dev))):
+        _want(qkv, "qkv", _BF16, 2)
+        _want(positions, "positions", _I32, 1, dev)
+        _want(slot_mapping, "slot_mapping", _I32, 1, dev)
+        _want(rope, "rope", _F32, 2, dev)
+        if bias is not None:
+            _want(bias, "bias", _BF16, 1, dev)
+    _int4_cache(kv_cache, dev)
+    width = (num_qo_heads + 2 * num_kv_heads) * 64
+    if kv_cache.shape[1] != num_kv_heads or qkv.shape[1] != width:
+        raise ValueError("qkv width / cache heads disagree with the head counts")
+    if positions.shape[0] != tokens or slot_mapping.shape[0] != tokens or rope.shape[1] != 64 \
+            or (bias is not None and bias.shape[0] != width):
+        raise ValueError(f"positions and slot_mapping must be [{tokens}], rope [positions, 64], "
+                         f"bias [{width}]")
+    with _at(dev, stream):
+        if q_out is None:
+            q_out = torch.empty(tokens, num_qo_heads, 64, dtype=_BF16, device=dev)
+        else:
+            _want(q_out, "q_out", _BF16, 3, dev)
+            _shape(q_out, "q_out", (tokens, num_qo_heads, 64))
+        status = load().sinkattn_qkv_prologue_int4(
+            qkv.data_ptr(), _ptr(bias), positions.data_ptr(), slot_mapping.data_ptr(), rope.data_ptr(),
+            rope.shape[0], int(rope_style), q_out.data_ptr(), kv_cache.data_ptr(), tokens, num_qo_heads,
+            num_kv_heads, 64, 16, kv_cache.shape[0], _raw_stream(dev))
+        if status:
+            _check("sinkattn_qkv_prologue_int4", status)
+    return q_out
+
+
+def gather_int4(kv_cache, slots, *, k=None, v=None, stream=None):
+    """Rows of a cache held in 4 bits as the values that they stand for: slots [T]
+    int32 (page * 16 + offset; outside of the pool: NaN rows).  Returns k, v
+    [T, Hkv, 64] bf16, exact."""
+    dev = kv_cache.device
+    _int4_cache(kv_cache, dev)
+    if not _is(slots, _I32, 1, dev):
+        _want(slots, "slots", _I32, 1, dev)
+    shape = (slots.shape[0], kv_cache.shape[1], 64)
+    with _at(dev, stream):
+        if k is None:
+            k = torch.empty(shape, dtype=_BF16, device=dev)
+        else:
+            _want(k, "k", _BF16, 3, dev)
+            _shape(k, "k", shape)
+        if v is None:
+            v = torch.empty(shape, dtype=_BF16, device=dev)
+        else:
+            _want(v, "v", _BF16, 3, dev)
+            _shape(v, "v", shape)
+        status = load().sinkattn_gather_int4(
+            kv_cache.data_ptr(), slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), shape[1], 64, 16,
+            kv_cache.shape[0], _raw_stream(dev))
+        if status:
+            _check("sinkattn_gather_int4", status)
+    return k, v
+
+
+def _int4_args(q, dims, kv_cache, page_table, kv_lens, sinks, batch):
+    dev = q.device
+    if not (_is(q, _BF16, dims, dev) and _is(page_table, _I32, 2, dev) and _is(kv_lens, _I32, 1, dev)
+            and _is(sinks, _F32, 1, dev)):
+        _want(q, "q", _BF16, dims)
+        _want(page_table, "page_table", _I32, 2, dev)
+        _want(kv_lens, "kv_lens", _I32, 1, dev)
+        _want(sinks, "sinks", _F32, 1, dev)
+    _int4_cache(kv_cache, dev, q.shape[-1])
+    if page_table.shape[0] != batch or kv_lens.shape[0] != batch:
+        raise ValueError(f"page_table and kv_lens must have {batch} rows, got "
+                         f"{page_table.shape[0]} and {kv_lens.shape[0]}")
+    if sinks.shape[0] != q.shape[-2]:
+        raise ValueError(f"sinks must be [{q.shape[-2]}], got {list(sinks.shape)}")
+
+
+def _int4_workspace(workspace, dev):
+    """The workspace handed in, or a new one (on the stream of the call)."""
+    if workspace is None:
+        return torch.zeros(_plan(_int4_workspace_bytes), dtype=_U8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return workspace
+
+
+def decode_int4(q, kv_cache, page_table, kv_lens, sinks, scale, max_kv_len, *, out=None, lse=None,
+                workspace=None, stream=None, want_lse=True, programmatic=None):
+    """`decode` over a cache held in 4 bits.  q [B, Hq, 64] bf16; kv_cache from
+    `int4_cache`.  workspace: `int4_workspace_bytes` zero-filled bytes that a program
+    keeps (without one, each call makes and clears its own).  Returns (out
+    [B, Hq, 64] bf16, lse [B, Hq] fp32 or None)."""
+    batch, hq, d = q.shape
+    _int4_args(q, 3, kv_cache, page_table, kv_lens, sinks, batch)
+    with _at(q.device, stream):
+        out, lse = _rows_out(q, out, lse, want_lse)
+        workspace = _int4_workspace(workspace, q.device)
+        status = load().sinkattn_decode_int4(
+            q.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+            kv_lens.data_ptr(), sinks.data_ptr(), float(scale), out.data_ptr(), _ptr(lse), batch, hq,
+            kv_cache.shape[1], d, 16, kv_cache.shape[0], _size(max_kv_len, "max_kv_len"),
+            workspace.data_ptr(), workspace.nbytes, _launch_flags(programmatic), _raw_stream(q.device))
+        if status:
+            _check("sinkattn_decode_int4", status)
+    return out, lse
+
+
+def verify_int4(q, kv_cache, page_table, kv_lens, sinks, scale, max_kv_len, *, tree_mask=None, out=None,
+                lse=None, workspace=None, stream=None, want_lse=True, programmatic=None):
+    """`verify` over a cache held in 4 bits.  q [B, q_len, Hq, 64] bf16; tree_mask and
+    the order of tokens as for `verify`, workspace as for `decode_int4`.  Returns
+    (out [B, q_len, Hq, 64], lse [B, q_len, Hq])."""
+    batch, q_len, hq, d = q.shape
+    _int4_args(q, 4, kv_cache, page_table, kv_lens, sinks, batch)
+    if tree_mask is not None:
+        _want(tree_mask, "tree_mask", torch.int64, 2, q.device)
+        _shape(tree_mask, "tree_mask", (batch, q_len))
+    with _at(q.device, stream):
+        out, lse = _rows_out(q, out, lse, want_lse)
+        workspace = _int4_workspace(workspace, q.device)
+        status = load().sinkattn_verify_int4(
+            q.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+            kv_lens.data_ptr(), _ptr(tree_mask), sinks.data_ptr(), float(scale), out.data_ptr(), _ptr(lse),
+            batch, q_len, hq, kv_cache.shape[1], d, 16, kv_cache.shape[0], _size(max_kv_len, "max_kv_len"),
+            workspace.data_ptr(), workspace.nbytes, _launch_flags(programmatic), _raw_stream(q.device))
+        if status:
+            _check("sinkattn_verify_int4", status)
+    return out, lse
+
+
+def prefill_paged_int4(q, cu_seqlens_q, kv_cache, page_table, kv_lens, sinks, scale, max_q_len, max_kv_len,
+                       *, out=None, lse=None, workspace=None, stream=None, want_lse=True):
+    """`prefill_paged` over a cache held in 4 bits, which holds the new tokens' keys
+    too (`qkv_prologue_int4` has written them).  workspace as for `decode_int4`."""
+    total, hq, d = q.shape
+    if not _is(cu_seqlens_q, _I32, 1, q.device):
+        _want(cu_seqlens_q, "cu_seqlens_q", _I32, 1, q.device)
+    num_seqs = cu_seqlens_q.shape[0] - 1
+    if num_seqs < 0:
+        raise ValueError("cu_seqlens_q must hold num_seqs + 1 entries")
+    _int4_args(q, 3, kv_cache, page_table, kv_lens, sinks, num_seqs)
+    with _at(q.device, stream):
+        out, lse = _rows_out(q, out, lse, want_lse)
+        workspace = _int4_workspace(workspace, q.device)
+        status = load().sinkattn_prefill_paged_int4(
+            q.data_ptr(), cu_seqlens_q.data_ptr(), num_seqs, total, _size(max_q_len, "max_q_len"),
+            kv_cache.data_ptr(), page_table.data_ptr(), page_table.shape[1], kv_lens.data_ptr(),
+            kv_cache.shape[0], _size(max_kv_len, "max_kv_len"), sinks.data_ptr(), float(scale),
+            out.data_ptr(), _ptr(lse), hq, kv_cache.shape[1], d, 16, workspace.data_ptr(), workspace.nbytes,
+            _raw_stream(q.device))
+        if status:
+            _check("sinkattn_prefill_paged_int4", status)
+    return out, lse

@@ -1,0 +1,709 @@
+// Attention of few query rows per KV head over a cache held in 4 bits: one token per
+// request, the draft tokens of a verification, or the last few of ragged requests.
+//
+// Mathematics.  Keys are k_j = s_j (n_j - z_j), n_j in 0..15.  The codes go into the
+// products as they are, as bf16 numbers 16 + n (4 bits below a set exponent):
+//     scale q.k_j   = (scale s_j) (q.(16 + n_j) - (16 + z_j) sum q)
+//     sum_j p_j v_j = sum_j (p_j s_j) (16 + n_j) - sum_j (p_j s_j) (16 + z_j)
+// Scales and zero points so cost a few operations per (key, head) instead of one per
+// element, both subtractions are exact up to fp32 sums, and p_j s_j is rounded to
+// bf16 once, the correction using the rounded value.
+//
+// What bounds it: 1088 bytes per page and KV head against the instructions that turn
+// them into fragments.  At the copy bandwidth an SM gets 23 bytes a cycle, a page every
+// 47 cycles: 188 issue slots on its four schedulers.  A word of eight codes becomes
+// four registers by three shifts and four logical operations (V: pairs of keys are put
+// together first), and S^T[16 keys x 8 rows] and O^T[64 x 8] take four mma.sync each.
+//
+// Split: every warp takes an equal, contiguous share of all pages of the call, numbered
+// through over (request, KV head, row block), whatever the requests' lengths: no wave
+// of short ones at the end, and no plan on the host.  A unit (request, KV head, row
+// block) inside one warp's share is finished there; parts join by log-sum-exp in shared
+// memory within a CTA, and CTAs that share a unit through the workspace, by the last one
+// to get there, in page order.  Every warp runs its own ring of bulk copies, two pages
+// (2176 bytes) a stage, across the borders of units.
+//
+// The running maximum is a reference that moves only when a score exceeds it by 2^8
+// (p <= 256 is as good in bf16 and fp32), so a step needs one vote instead of six
+// shuffles.
+
+#include "int4.cuh"
+#include "ptx.cuh"
+#include "workspace.cuh"
+
+#include <algorithm>
+
+namespace sa {
+namespace {
+
+constexpr int kNW = 8;                        // warps per CTA
+constexpr int kThreads = kNW * 32;
+constexpr int kStepPages = 2;                 // pages per stage
+constexpr int kStageBytes = kStepPages * kInt4Block;
+constexpr float kRaise = 8.f;                 // log2 by which a score may exceed the reference
+
+// Stages in flight per warp, and CTAs per SM that shared memory and registers allow.
+template <int NB>
+struct Tuning {
+  static constexpr int kStages = NB == 2 ? 3 : 4;
+  static constexpr int kCtas = NB == 4 ? 1 : 2;
+};
+
+template <int NB>
+struct Part {                                 // one warp's share of a unit
+  float o[8 * NB][kHeadDim];
+  float m[8 * NB], d[8 * NB];
+};
+
+template <int NB>
+struct __align__(128) Shared {
+  uint8_t ring[kNW][Tuning<NB>::kStages][kStageBytes];
+  Part<NB> begun[kNW];                        // of a unit begun before the warp's share
+  uint64_t bars[kNW][Tuning<NB>::kStages];
+  long long prefix[kThreads + 1];
+  long long scan[kNW];
+  int has[2][kNW];
+  int last;
+  // 0: a unit begun before the warp's share; 1: one that goes on after it (in the
+  // ring, which is idle by then)
+  __device__ __forceinline__ Part<NB> &part(int slot, int warp) {
+    static_assert(sizeof(Part<NB>) <= sizeof(ring[0]), "a part fits into a warp's ring");
+    return slot == 0 ? begun[warp] : *reinterpret_cast<Part<NB> *>(&ring[warp][0][0]);
+  }
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// A request's share of the work: `units` (KV head, row block) pairs of `pages` pages
+// each; a request without keys, or one that is out of range (`bad`), counts one page
+// that nothing of is read.
+struct Request {
+  int kv_len, row0, tokens, pages, units;
+  bool bad;
+};
+
+template <int NB, int kMode>
+__device__ __forceinline__ Request request(const Int4AttnParams &p, int b) {
+  Request r;
+  r.kv_len = p.kv_lens[b];
+  if constexpr (kMode == kInt4Ragged) {
+    r.row0 = p.cu_seqlens_q[b];
+    const int end = p.cu_seqlens_q[b + 1];
+    r.tokens = end - r.row0;
+    r.bad = r.row0 < 0 || end < r.row0 || end > p.total_q || r.tokens > p.max_q_len || r.kv_len < r.tokens;
+    if (r.bad)                                 // what lies inside the buffers becomes NaN
+      r.tokens = r.row0 < 0 || r.row0 >= p.total_q ? 0 : min(max(end, r.row0), p.total_q) - r.row0;
+  } else {
+    r.tokens = p.q_len;
+    r.row0 = b * p.q_len;
+    r.bad = r.kv_len < (kMode == kInt4Verify ? p.q_len : 0);
+  }
+  r.bad = r.bad || r.kv_len > p.max_kv_len || (r.kv_len + kPageSize - 1) / kPageSize > p.max_pages_per_seq;
+  r.pages = r.bad ? 1 : max(1, ceil_div(r.kv_len, kPageSize));
+  r.units = r.tokens > 0 ? p.num_kv_heads * ceil_div(r.tokens * p.group, 8 * NB) : 0;
+  return r;
+}
+
+// A place in the numbering of all pages: page `page` of unit `unit` of request b.
+template <int NB, int kMode>
+struct Place {
+  Request r;
+  int b, unit, page;
+  __device__ __forceinline__ void next_unit(const Int4AttnParams &p) {
+    page = 0;
+    if (++unit < r.units) return;
+    unit = 0;
+    do {
+      r.units = 0;
+      if (++b >= p.num_seqs) return;
+      r = request<NB, kMode>(p, b);
+    } while (r.units == 0);
+  }
+};
+
+// Copies `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// Field of 4 bits in each half of w, at bits 3..6 of the half, below the exponent of
+// 16: the bf16 pair (16 + low code, 16 + high code).
+__device__ __forceinline__ uint32_t field(uint32_t w) { return (w & 0x00780078u) | 0x41804180u; }
+
+__device__ __forceinline__ uint32_t word(const uint4 &x, int w) {
+  return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w;
+}
+
+// A key's scale and 16 + zero point, from the low half of m (K) or the high one (V).
+__device__ __forceinline__ float scale_of(uint32_t m, bool v) {
+  return __uint_as_float((v ? m : m << 16) & 0xfff00000u);
+}
+__device__ __forceinline__ float zero_of(uint32_t m, bool v) {
+  return __uint_as_float(((v ? m << 3 : m << 19) & 0x00780000u) | 0x41800000u);
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint4 &v) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+}
+__device__ __forceinline__ void lds64(uint32_t addr, uint2 &v) {
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+}
+
+// Row r of the block of a unit -> its [.., Hq] row in q, out and lse (-1 past the last).
+template <int NB>
+__device__ __forceinline__ long long row_of(const Int4AttnParams &p, const Request &q, int kvh, int rb,
+                                            int r, int &token, int &head) {
+  const int i = rb * 8 * NB + r;
+  token = i / p.group;
+  head = kvh * p.group + (i - token * p.group);
+  return token < q.tokens ? (static_cast<long long>(q.row0) + token) * p.num_qo_heads + head : -1;
+}
+
+// out and lse of a row from its unnormalised sums; 4 elements from dim dq on.
+__device__ __forceinline__ void write_row(const Int4AttnParams &p, long long row, int dq, float4 o,
+                                          float m, float d) {
+  const float inv = d == 0.f ? 0.f : 1.f / d;          // (NaN spoils the row)
+  *reinterpret_cast<uint2 *>(p.out + row * kHeadDim + dq) =
+      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (dq == 0 && p.lse) p.lse[row] = d == 0.f ? -INFINITY : (m + lg2(d)) * kLn2;
+}
+
+template <int NB, int kMode>
+__global__ void __launch_bounds__(kThreads, Tuning<NB>::kCtas)
+int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
+  constexpr int kStages = Tuning<NB>::kStages;
+  constexpr int kRows = 8 * NB;
+  extern __shared__ uint8_t smem_raw[];
+  Shared<NB> &sh = *reinterpret_cast<Shared<NB> *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+
+  // ---- this warp's share of all pages
+  const int per = ceil_div(p.num_seqs, kThreads);      // requests per thread of the scan
+  long long mine = 0;
+  for (int b = threadIdx.x * per; b < min(p.num_seqs, static_cast<int>(threadIdx.x + 1) * per); ++b) {
+    const Request r = request<NB, kMode>(p, b);
+    mine += static_cast<long long>(r.pages) * r.units;
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += x;
+  }
+  if (lane == 31) sh.scan[warp] = upto;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&sh.bars[warp][s], 1);
+    fence_mbar_init();
+    sh.has[0][warp] = sh.has[1][warp] = 0;
+  }
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kNW; ++w) {
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
+  }
+  sh.prefix[threadIdx.x] = before + upto - mine;       // pages before this thread's requests
+  __syncthreads();
+
+  // an even share, so that only its last step is half empty; whole CTAs' worth of it
+  const long long slots = static_cast<long long>(gridDim.x) * kNW;
+  long long share = (total + slots - 1) / slots;
+  share = max(share + (share & 1), static_cast<long long>(p.min_pages));
+  const long long cta_share = share * kNW;
+  const long long from = min(total, blockIdx.x * cta_share + warp * share);
+  const long long to = min(total, from + share);
+  if (blockIdx.x * cta_share >= total) return;         // uniform over the CTA
+
+  using At = Place<NB, kMode>;
+  At at;                                               // where the pages are worked on
+  at.b = at.unit = at.page = 0;
+  if (from < to) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i)
+      n += __popc(__ballot_sync(0xffffffffu, sh.prefix[i * 32 + lane] <= from));
+    at.b = (n - 1) * per;                              // the last threads' requests that begin by `from`
+    long long here = sh.prefix[n - 1];
+    while (true) {
+      at.r = request<NB, kMode>(p, at.b);
+      const long long w = static_cast<long long>(at.r.pages) * at.r.units;
+      if (here + w > from) break;
+      here += w;
+      ++at.b;
+    }
+    at.unit = static_cast<int>((from - here) / at.r.pages);
+    at.page = static_cast<int>((from - here) - static_cast<long long>(at.unit) * at.r.pages);
+  }
+  const long long share_pages = to - from;
+
+  // ---- copies: `to_come` runs ahead of `at` by up to kStages steps
+  At to_come = at;
+  long long unissued = share_pages;
+  int ids = -1, ids_next = -1, ids_at = 0;             // lane j: id of page ids_at + j; of the next 32
+  auto load_ids = [&](int first) -> int {
+    const int page = first + lane;
+    return !to_come.r.bad && page * kPageSize < to_come.r.kv_len
+               ? p.page_table[static_cast<size_t>(to_come.b) * p.max_pages_per_seq + page] : -1;
+  };
+  auto start_ids = [&]() {
+    ids_at = to_come.page;
+    ids = load_ids(ids_at);
+    ids_next = ids_at + 32 < to_come.r.pages ? load_ids(ids_at + 32) : -1;
+  };
+  if (share_pages > 0) start_ids();
+
+  // Up to here only lengths and the page table were read; everything below may
+  // depend on the previous kernel on the stream.
+  grid_dependency_wait();
+  launch_dependents();
+
+  const uint64_t policy = l2_policy_evict_first();
+  uint32_t spoilt = 0;                                 // stages with a page outside of the pool
+  auto issue = [&](int st) {                           // all lanes call
+    const int n = static_cast<int>(min(min(static_cast<long long>(kStepPages), unissued),
+                                       static_cast<long long>(to_come.r.pages - to_come.page)));
+    if (to_come.page - ids_at >= 32) {
+      ids_at += 32;
+      ids = ids_next;
+      ids_next = ids_at + 32 < to_come.r.pages ? load_ids(ids_at + 32) : -1;
+    }
+    const int off = to_come.page - ids_at;
+    int id = __shfl_sync(0xffffffffu, ids, (off + (lane & 1)) & 31);
+    if (off == 31 && n == 2) {                         // the second page is the next batch's first
+      const int other = __shfl_sync(0xffffffffu, ids_next, 0);
+      if (lane & 1) id = other;
+    }
+    const bool wanted = lane < n;
+    const bool ok = wanted && id >= 0 && id < p.num_pages;
+    const unsigned good = __ballot_sync(0xffffffffu, ok);
+    const bool empty = to_come.r.kv_len <= 0 || to_come.r.bad;
+    spoilt &= ~(1u << st);
+    if (!empty && __popc(good) < n) spoilt |= 1u << st;
+    uint64_t *bar = &sh.bars[warp][st];
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(good) * kInt4Block);
+    __syncwarp();
+    if (ok) {
+      fence_proxy_async_smem();
+      const int kvh = to_come.unit % p.num_kv_heads;
+      bulk_load(&sh.ring[warp][st][lane * kInt4Block],
+                p.kv_cache + (static_cast<size_t>(id) * p.num_kv_heads + kvh) * kInt4Block, kInt4Block,
+                bar, policy);
+    }
+    unissued -= n;
+    to_come.page += n;
+    if (to_come.page >= to_come.r.pages && unissued > 0) {
+      to_come.next_unit(p);
+      start_ids();
+    }
+  };
+  int issued = 0, done = 0;                            // steps
+  while (issued < kStages && unissued > 0) issue(issued++);
+
+  // ---- units of this share, one after another
+  bool dead = false;                                   // a copy never landed
+  long long left = share_pages;
+  while (left > 0) {
+    const int kvh = at.unit % p.num_kv_heads, rb = at.unit / p.num_kv_heads;
+    const int first_page = at.page;
+    const int seg = static_cast<int>(min(left, static_cast<long long>(at.r.pages - at.page)));
+    const int seg_end = first_page + seg;
+    // keys [0, old) are visible to every row, key old + u to the rows of token u and
+    // later ones, or by the mask
+    const int old = kMode == kInt4Decode ? at.r.kv_len : at.r.kv_len - at.r.tokens;
+
+    // Q^T as B operand: row g of each block; registers 2k and 2k + 1 hold pairs (dim, dim + 4)
+    uint32_t qb[NB][8];
+    float qs[NB][2];                                   // sum of q, times the scale, of rows 2t and 2t + 1
+    float m[NB][2], d[NB][2], corr[NB][2];
+    int limit[NB][2];                                  // keys that a row sees (causal)
+    uint64_t vis[NB][2];                               // and its bits of the mask
+    float o[NB][4][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      int token, head;
+      const long long row = row_of<NB>(p, at.r, kvh, rb, 8 * nb + g, token, head);
+      uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (row >= 0) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(p.q) + row * (kHeadDim / 8);
+        x[0] = __ldg(q + t);
+        x[1] = __ldg(q + t + 4);
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qb[nb][4 * h + j] = __byte_perm(w[j / 2], w[j / 2 + 2], j & 1 ? 0x7632 : 0x5410);
+          sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
+        }
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        qs[nb][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
+        const long long r = row_of<NB>(p, at.r, kvh, rb, 8 * nb + 2 * t + e, token, head);
+        // a sink that is no logit (NaN, +inf) spoils the sum, not the maximum
+        const bool sink = first_page == 0 && r >= 0;
+        const float logit = sink ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
+        const bool fine = logit < INFINITY;
+        m[nb][e] = fine ? logit : -INFINITY;
+        d[nb][e] = sink && g == 0 ? (fine ? (logit == -INFINITY ? 0.f : 1.f) : NAN) : 0.f;
+        corr[nb][e] = 0.f;
+        limit[nb][e] = kMode == kInt4Decode ? at.r.kv_len : min(at.r.kv_len, old + token + 1);
+        vis[nb][e] = 0;
+        if constexpr (kMode == kInt4Verify) {
+          if (p.tree_mask && r >= 0) {
+            vis[nb][e] = p.tree_mask[static_cast<size_t>(at.b) * p.q_len + token];
+            limit[nb][e] = old;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
+    }
+    bool bad = at.r.bad || dead;
+
+    for (int page = first_page; page < seg_end; page += kStepPages) {
+      const int st = done % kStages;
+      if (!dead && !mbar_wait(&sh.bars[warp][st], (done / kStages) & 1)) {
+        // a copy never landed: let the others in flight land (with the same limit)
+        // before their stages are used otherwise, and start no more
+        dead = bad = true;
+        for (int i = done + 1; i < issued; ++i) mbar_wait(&sh.bars[warp][i % kStages], (i / kStages) & 1);
+      }
+      bad = bad || ((spoilt >> st) & 1);
+      ++done;
+      if (dead) continue;
+      const uint32_t stage = smem_u32(&sh.ring[warp][st][0]);
+      const int tok0 = page * kPageSize;
+      const int tok_end = min(at.r.kv_len, seg_end * kPageSize);
+      const bool edge = tok0 + kStepPages * kPageSize > min(tok_end, old);   // keys that not all rows see
+
+      float acc[kStepPages][NB][4];
+      uint2 meta[kStepPages];                          // keys g and g + 8
+#pragma unroll
+      for (int pg = 0; pg < kStepPages; ++pg) {
+        uint4 kw;
+        lds128(stage + pg * kInt4Block + kInt4K + 16 * lane, kw);
+        lds64(stage + pg * kInt4Block + kInt4Meta + 8 * g, meta[pg]);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[pg][nb][0] = acc[pg][nb][1] = acc[pg][nb][2] = acc[pg][nb][3] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t lo = word(kw, h), hi = word(kw, 2 + h);   // keys g and g + 8
+          const uint32_t a0[4] = {field(lo), field(hi), field(lo >> 4), field(hi >> 4)};
+          const uint32_t a1[4] = {field(lo >> 8), field(hi >> 8), field(__funnelshift_r(lo, lo, 12)),
+                                  field(__funnelshift_r(hi, hi, 12))};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_bf16_16816(acc[pg][nb], a0, qb[nb][4 * h], qb[nb][4 * h + 1]);
+            mma_bf16_16816(acc[pg][nb], a1, qb[nb][4 * h + 2], qb[nb][4 * h + 3]);
+          }
+        }
+      }
+
+      // scores relative to the reference; x[pg][nb][i]: key g + 8 (i / 2), row 2t + i % 2
+      float x[kStepPages][NB][4];
+      auto scores = [&]() {
+#pragma unroll
+        for (int pg = 0; pg < kStepPages; ++pg)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t mt = h ? meta[pg].y : meta[pg].x;
+            const float ks = scale_of(mt, false) * p.scale_log2;
+            const float kz = -zero_of(mt, false) * ks;
+            const uint64_t ks2 = f2_pack(ks, ks), kz2 = f2_pack(kz, kz);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const float r0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0];
+              const float r1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
+              const uint64_t base = f2_fma(kz2, f2_pack(qs[nb][0], qs[nb][1]), f2_pack(-r0, -r1));
+              f2_unpack(f2_fma(ks2, f2_pack(acc[pg][nb][2 * h], acc[pg][nb][2 * h + 1]), base),
+                        x[pg][nb][2 * h], x[pg][nb][2 * h + 1]);
+            }
+          }
+        if (edge) {
+#pragma unroll
+          for (int pg = 0; pg < kStepPages; ++pg)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int tok = tok0 + pg * kPageSize + g + 8 * (i / 2);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const int u = tok - old;
+                const bool drafted = kMode == kInt4Verify && u >= 0 && u < 64 && ((vis[nb][i & 1] >> u) & 1);
+                if (tok >= tok_end || (tok >= limit[nb][i & 1] && !drafted)) x[pg][nb][i] = -INFINITY;
+              }
+            }
+        }
+      };
+      scores();
+      bool raise = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float top = fmaxf(fmaxf(x[0][nb][e], x[0][nb][2 + e]), fmaxf(x[1][nb][e], x[1][nb][2 + e]));
+          raise = raise || top > kRaise || m[nb][e] == -INFINITY;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(fmaxf(x[0][nb][e], x[0][nb][2 + e]), fmaxf(x[1][nb][e], x[1][nb][2 + e]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float was = m[nb][e];
+            const float now = fmaxf(was, top + (was == -INFINITY ? 0.f : was));
+            if (now > was) {
+              const float a = ex2(was - now);
+              m[nb][e] = now;
+              d[nb][e] *= a;
+              corr[nb][e] *= a;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[nb][i][e] *= a;
+                o[nb][i][2 + e] *= a;
+              }
+            }
+          }
+        scores();
+      }
+
+#pragma unroll
+      for (int pg = 0; pg < kStepPages; ++pg) {
+        uint32_t pb[NB][2];                            // P s as B operand: keys 2t.., row g
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t mt = h ? meta[pg].y : meta[pg].x;
+          float vs = scale_of(mt, true);
+          const float vz = -zero_of(mt, true);
+          // a slot past the last key may hold anything, a hidden key's scale may be NaN
+          if (edge && tok0 + pg * kPageSize + g + 8 * h >= tok_end) vs = 0.f;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const float p0 = ex2(x[pg][nb][2 * h]), p1 = ex2(x[pg][nb][2 * h + 1]);
+            d[nb][0] += p0;
+            d[nb][1] += p1;
+            float w0 = p0 * vs, w1 = p1 * vs;
+            if (edge) {
+              if (x[pg][nb][2 * h] == -INFINITY) w0 = 0.f;
+              if (x[pg][nb][2 * h + 1] == -INFINITY) w1 = 0.f;
+            }
+            const uint32_t w = pack_bf16(w0, w1);
+            corr[nb][0] = fmaf(__uint_as_float(w << 16), vz, corr[nb][0]);
+            corr[nb][1] = fmaf(__uint_as_float(w & 0xffff0000u), vz, corr[nb][1]);
+            pb[nb][h] = movmatrix_trans(w);
+          }
+        }
+        uint4 vw;                                      // word g of keys 2t, 2t + 1, 2t + 8, 2t + 9
+        lds128(stage + pg * kInt4Block + kInt4V + 16 * lane, vw);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {                  // dims 8g + 4c ..
+          const uint32_t sel = c ? 0x7632 : 0x5410;
+          const uint32_t lo = __byte_perm(vw.x, vw.y, sel), hi = __byte_perm(vw.z, vw.w, sel);
+          const uint32_t a0[4] = {field(lo << 3), field(lo >> 1), field(hi << 3), field(hi >> 1)};
+          const uint32_t a1[4] = {field(lo >> 5), field(lo >> 9), field(hi >> 5), field(hi >> 9)};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_bf16_16816(o[nb][2 * c], a0, pb[nb][0], pb[nb][1]);
+            mma_bf16_16816(o[nb][2 * c + 1], a1, pb[nb][0], pb[nb][1]);
+          }
+        }
+      }
+      __syncwarp();                                    // the stage has been read
+      if (unissued > 0) issue(issued++ % kStages);
+    }
+
+    // ---- the segment's sums; lane (g, t) has dims 8g .. 8g + 7 of rows 2t, 2t + 1
+    const bool begun = first_page > 0, goes_on = seg_end < at.r.pages;
+    const int slot = begun ? 0 : 1;
+    Part<NB> &part = sh.part(slot, warp);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float dd = d[nb][e], cc = corr[nb][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          dd += __shfl_xor_sync(0xffffffffu, dd, off);
+          cc += __shfl_xor_sync(0xffffffffu, cc, off);
+        }
+        if (bad) dd = NAN;
+        // o[nb][i][e] and [2 + e]: dims 8g + 2i and 8g + 2i + 1
+        const float4 lo = make_float4(o[nb][0][e] + cc, o[nb][0][2 + e] + cc, o[nb][1][e] + cc, o[nb][1][2 + e] + cc);
+        const float4 hi = make_float4(o[nb][2][e] + cc, o[nb][2][2 + e] + cc, o[nb][3][e] + cc, o[nb][3][2 + e] + cc);
+        const int r = 8 * nb + 2 * t + e;
+        if (!begun && !goes_on) {
+          int token, head;
+          const long long row = row_of<NB>(p, at.r, kvh, rb, r, token, head);
+          if (row >= 0) {
+            write_row(p, row, 8 * g, lo, m[nb][e], dd);
+            write_row(p, row, 8 * g + 4, hi, m[nb][e], dd);
+          }
+        } else {
+          *reinterpret_cast<float4 *>(&part.o[r][8 * g]) = lo;
+          *reinterpret_cast<float4 *>(&part.o[r][8 * g + 4]) = hi;
+          if (g == 0) {
+            part.m[r] = m[nb][e];
+            part.d[r] = dd;
+          }
+        }
+      }
+    if (lane == 0 && (begun || goes_on)) sh.has[slot][warp] = 1;
+    left -= seg;
+    at.page = seg_end;
+    if (left > 0) at.next_unit(p);
+  }
+
+  // ---- join the parts.  A unit's parts lie in consecutive warps: slot 1 of the warp
+  // that begins it, slot 0 of the others.
+  __syncthreads();
+  const long long cta_from = blockIdx.x * cta_share, cta_to = min(total, cta_from + cta_share);
+  for (int round = 0; round < kNW + 1; ++round) {      // round 0: the unit begun before the CTA; 1 + w: by warp w
+    const int w0 = max(round - 1, 0), s0 = round == 0 ? 0 : 1;
+    if (!sh.has[s0][w0]) continue;                     // uniform over the CTA
+    int w1 = w0 + 1;                                   // its parts: (s0, w0), (0, w0 + 1 ..)
+    // where the unit is, from the first page of warp w0's share that is its
+    const long long w_from = min(total, cta_from + w0 * share);
+    const long long w_to = min(total, w_from + share);
+    const long long known = s0 == 0 ? w_from : w_to - 1;   // a page of it
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i)
+      n += __popc(__ballot_sync(0xffffffffu, sh.prefix[i * 32 + lane] <= known));
+    At u;
+    u.b = (n - 1) * per;
+    long long here = sh.prefix[n - 1];
+    while (true) {
+      u.r = request<NB, kMode>(p, u.b);
+      const long long w = static_cast<long long>(u.r.pages) * u.r.units;
+      if (here + w > known) break;
+      here += w;
+      ++u.b;
+    }
+    u.unit = static_cast<int>((known - here) / u.r.pages);
+    const long long u_from = here + static_cast<long long>(u.unit) * u.r.pages, u_to = u_from + u.r.pages;
+    while (w1 < kNW && cta_from + w1 * share < min(u_to, total)) ++w1;
+    const int kvh = u.unit % p.num_kv_heads, rb = u.unit / p.num_kv_heads;
+    const bool whole = u_from >= cta_from && u_to <= cta_to;
+
+    constexpr int kItems = kRows * (kHeadDim / 4);
+    const size_t mine_at = static_cast<size_t>(blockIdx.x) * 2 + (u_from >= cta_from ? 1 : 0);
+    for (int item = threadIdx.x; item < kItems; item += kThreads) {
+      const int r = item / (kHeadDim / 4), dq = (item % (kHeadDim / 4)) * 4;
+      float mx = sh.part(s0, w0).m[r];
+      for (int w = w0 + 1; w < w1; ++w) mx = fmaxf(mx, sh.part(0, w).m[r]);
+      float den = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = w0; w < w1; ++w) {
+        const Part<NB> &x = sh.part(w == w0 ? s0 : 0, w);
+        const float wt = x.m[r] == -INFINITY ? 0.f : ex2(x.m[r] - mx);
+        den += x.d[r] != x.d[r] ? NAN : wt * x.d[r];
+        const float4 v = *reinterpret_cast<const float4 *>(&x.o[r][dq]);
+        a.x += wt * v.x;
+        a.y += wt * v.y;
+        a.z += wt * v.z;
+        a.w += wt * v.w;
+      }
+      if (whole) {
+        int token, head;
+        const long long row = row_of<NB>(p, u.r, kvh, rb, r, token, head);
+        if (row >= 0) write_row(p, row, dq, a, mx, den);
+      } else {
+        *reinterpret_cast<float4 *>(p.ws_o + (mine_at * kRows + r) * kHeadDim + dq) = a;
+        if (dq == 0) p.ws_md[mine_at * kRows + r] = make_float2(mx, den);
+      }
+    }
+    if (whole) continue;
+
+    // the last of the CTAs that share the unit joins their parts, in page order, and
+    // leaves the counter at zero for the next call
+    const int c0 = static_cast<int>(u_from / cta_share), c1 = static_cast<int>((u_to - 1) / cta_share);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) sh.last = atomicAdd(&p.counters[c0], 1) == c1 - c0;
+    __syncthreads();
+    if (!sh.last) continue;
+    __threadfence();
+    for (int item = threadIdx.x; item < kItems; item += kThreads) {
+      const int r = item / (kHeadDim / 4), dq = (item % (kHeadDim / 4)) * 4;
+      auto index = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRows + r; };
+      float mx = -INFINITY;
+      for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(&p.ws_md[index(c)]).x);
+      float den = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const float2 md = __ldcg(&p.ws_md[index(c)]);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + index(c) * kHeadDim + dq));
+        const float wt = md.x == -INFINITY ? 0.f : ex2(md.x - mx);
+        den += md.y != md.y ? NAN : wt * md.y;
+        a.x += wt * v.x;
+        a.y += wt * v.y;
+        a.z += wt * v.z;
+        a.w += wt * v.w;
+      }
+      int token, head;
+      const long long row = row_of<NB>(p, u.r, kvh, rb, r, token, head);
+      if (row >= 0) write_row(p, row, dq, a, mx, den);
+    }
+    if (threadIdx.x == 0) p.counters[c0] = 0;
+    __syncthreads();                                   // sh.last has been read
+  }
+}
+
+template <int NB, int kMode>
+cudaError_t launch_variant(const Int4AttnParams &p, int ctas, cudaStream_t stream, bool programmatic) {
+  constexpr int kBytes = static_cast<int>(sizeof(Shared<NB>)) + 128;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+  cudaError_t err = set_smem_once<int4_decode_kernel<NB, kMode>>(kBytes);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(int4_decode_kernel<NB, kMode>, static_cast<unsigned>(ctas), kThreads, kBytes, stream,
+                       programmatic, p);
+}
+
+template <int NB>
+cudaError_t launch_mode(const Int4AttnParams &p, Int4Mode mode, int ctas, cudaStream_t stream,
+                        bool programmatic) {
+  if (mode == kInt4Decode) return launch_variant<NB, kInt4Decode>(p, ctas, stream, programmatic);
+  if (mode == kInt4Verify) return launch_variant<NB, kInt4Verify>(p, ctas, stream, programmatic);
+  return launch_variant<NB, kInt4Ragged>(p, ctas, stream, programmatic);
+}
+
+template <int NB>
+int ctas_per_sm() {
+  return std::min(Tuning<NB>::kCtas, 228 * 1024 / static_cast<int>(sizeof(Shared<NB>) + 128 + 1024));
+}
+
+}  // namespace
+
+int int4_decode_ctas_per_sm(int row_blocks) {
+  return row_blocks == 1 ? ctas_per_sm<1>() : row_blocks == 2 ? ctas_per_sm<2>() : ctas_per_sm<4>();
+}
+
+size_t int4_decode_results_bytes(int row_blocks, int ctas) {
+  return static_cast<size_t>(ctas) * 2 * 8 * row_blocks * (kHeadDim * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_int4_decode(const Int4AttnParams &p, Int4Mode mode, int row_blocks, int ctas,
+                               cudaStream_t stream, bool programmatic) {
+  if (row_blocks == 1) return launch_mode<1>(p, mode, ctas, stream, programmatic);
+  if (row_blocks == 2) return launch_mode<2>(p, mode, ctas, stream, programmatic);
+  return launch_mode<4>(p, mode, ctas, stream, programmatic);
+}
+
+}  // namespace sa

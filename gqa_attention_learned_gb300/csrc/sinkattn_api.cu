@@ -3,6 +3,7 @@
 // include/sinkattn.h.  Nothing here allocates device memory or synchronises.
 
 #include "sinkattn.h"
+#include "api.cuh"
 #include "bounded.cuh"
 #include "workspace.cuh"
 
@@ -274,6 +275,15 @@ DecodePlan plan_window_decode(int batch, int num_qo_heads, int num_kv_heads, int
 }  // namespace
 
 namespace sa {
+
+int api_sm_count() { return device_sm_count(); }
+int api_status(cudaError_t err, const char *where) { return cuda_status(err, where); }
+int api_failure(const char *what) { return fail_msg(what); }
+bool api_encode_map(CUtensorMap *map, const void *base, unsigned long long d1, unsigned long long d2,
+                    unsigned b1, unsigned b2) {
+  return encode_map(map, base, d1, d2, b1, b2);
+}
+
 std::atomic<int> g_programmatic{0};
 
 // Launch mode of one call: its own flag, else the process-wide default.
@@ -298,7 +308,7 @@ const char *sinkattn_status_string(int status) {
   }
 }
 
-int sinkattn_version(void) { return 500; }   // 0.5.0: windowed attention, attention mass, eviction
+int sinkattn_version(void) { return 600; }   // 0.6.0: paged cache held in 4 bits
 
 int sinkattn_set_programmatic_launch(int enable) {
   return sa::g_programmatic.exchange(enable != 0 ? 1 : 0);

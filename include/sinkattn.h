@@ -536,6 +536,109 @@ SINKATTN_API int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *pag
                          int32_t *kept, int batch, int num_kv_heads, int head_dim,
                          int page_size, int num_pages, int max_kv_len, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A paged cache held in 4 bits
+ *
+ * One buffer holds K and V: uint8 [num_pages][num_kv_heads]
+ * [SINKATTN_INT4_BLOCK_BYTES], 68 bytes per key and KV head instead of 256.  A
+ * row x of 64 values (a key's or a value's, of one KV head) is 64 codes n in
+ * 0..15, a scale s and a zero point z:
+ *     lo = min(0, min x), hi = max(0, max x)
+ *     s  = (hi - lo) / 15, rounded up to 4 significant bits, at least 2^-126
+ *     z  = rint(-lo / s)                           (in 0..15)
+ *     n  = clamp(rint(x / s) + z, 0, 15)           (rint: ties to even)
+ * and stands for s * (n - z), which is always a bf16 number: every operator here
+ * computes what its bf16 counterpart computes on a cache of these values.  A row
+ * whose range is not finite stands for 64 NaN.  x is taken in fp32.
+ *
+ * Layout of a block (one page, one KV head), slot j = 0..15, 32-bit words,
+ * little endian:
+ *   K codes   byte 64 (j % 8) + 16 t + 8 (j / 8), t = 0..3: two words, dims
+ *             8t + e and 32 + 8t + e (e = 0..7) at bits 4e, each word rotated
+ *             left by 3
+ *   V codes   byte 512 + 64 g + 16 (j % 8 / 2) + 8 (j / 8) + 4 (j % 2),
+ *             g = 0..7: one word, dims 8g + e at bits 4e
+ *   s and z   byte 1024 + 8 (j % 8) + 4 (j / 8): one word, K's in the low half,
+ *             V's in the high half: s as a bf16 number whose last 4 bits are z
+ * A token owns whole bytes, so tokens of one page may be written at once.
+ * The cache has to be 16-byte aligned; slots that no length covers may hold
+ * anything.
+ *
+ * Page tables, lengths, sinks, scale, out and lse are as for the bf16 cache, and
+ * so is what becomes NaN.  A sink that is NaN or +inf makes its head's rows NaN.
+ *
+ * The attention calls need a workspace of sinkattn_int4_workspace_bytes, whatever
+ * their sizes: 256-byte aligned and ZERO-FILLED BEFORE ITS FIRST USE.  Every call
+ * leaves it ready for the next, and it may serve calls of the other operators in
+ * turn (whose own rules on size hold); calls that share it must not overlap on
+ * the GPU.  num_sms: 0 = ask the current device.
+ */
+#define SINKATTN_INT4_BLOCK_BYTES 1088
+
+SINKATTN_API int sinkattn_int4_workspace_bytes(int num_sms, size_t *workspace_bytes);
+
+/*
+ * sinkattn_qkv_prologue into such a cache: bias, rotary encoding of q and k, and
+ * k and v rows quantised into slot slot_mapping[t].
+ *   rope           : fp32 [rope_positions][64]: for each position the 32 cosines,
+ *                    then the 32 sines of its angles, times the magnitude factor
+ *                    (one table serves all layers)
+ *   positions      : int32 [num_tokens], rows of rope; a position outside of it
+ *                    makes the token's q rows NaN, and its k rows stand for NaN
+ *   other arguments: as for sinkattn_qkv_prologue
+ * x = qkv + bias, then x1 cos - x2 sin and x2 cos + x1 sin, each operation
+ * rounded to fp32 on its own: equal inputs give equal codes on any machine.
+ * Launch: as for sinkattn_qkv_prologue.
+ */
+SINKATTN_API int sinkattn_qkv_prologue_int4(const void *qkv, const void *bias,
+                          const int32_t *positions, const int32_t *slot_mapping,
+                          const float *rope, int rope_positions, int rope_style,
+                          void *q_out, void *kv_cache, int num_tokens,
+                          int num_qo_heads, int num_kv_heads, int head_dim,
+                          int page_size, int num_pages, void *stream);
+
+/*
+ * Rows of the cache as the values that they stand for.
+ *   slots : int32 [num_rows], page * page_size + slot; one outside of the pool
+ *           gives NaN rows
+ *   k, v  : bf16 [num_rows][num_kv_heads][head_dim], exact
+ * Launch: as for sinkattn_qkv_prologue.
+ */
+SINKATTN_API int sinkattn_gather_int4(const void *kv_cache, const int32_t *slots, int num_rows,
+                          void *k, void *v, int num_kv_heads, int head_dim,
+                          int page_size, int num_pages, void *stream);
+
+/* sinkattn_decode_ex over such a cache.  All pages of the call are shared out
+ * evenly over the GPU, whatever the requests' lengths. */
+SINKATTN_API int sinkattn_decode_int4(const void *q, const void *kv_cache,
+                          const int32_t *page_table, int max_pages_per_seq,
+                          const int32_t *kv_lens, const float *sinks, float scale,
+                          void *out, float *lse, int batch, int num_qo_heads,
+                          int num_kv_heads, int head_dim, int page_size,
+                          int num_pages, int max_kv_len, void *workspace,
+                          size_t workspace_bytes, int launch_flags, void *stream);
+
+/* sinkattn_verify_ex over such a cache. */
+SINKATTN_API int sinkattn_verify_int4(const void *q, const void *kv_cache,
+                          const int32_t *page_table, int max_pages_per_seq,
+                          const int32_t *kv_lens, const uint64_t *tree_mask,
+                          const float *sinks, float scale, void *out, float *lse,
+                          int batch, int q_len, int num_qo_heads, int num_kv_heads,
+                          int head_dim, int page_size, int num_pages,
+                          int max_kv_len, void *workspace, size_t workspace_bytes,
+                          int launch_flags, void *stream);
+
+/* sinkattn_prefill_paged over such a cache (the new tokens' keys in it too). */
+SINKATTN_API int sinkattn_prefill_paged_int4(const void *q, const int32_t *cu_seqlens_q,
+                          int num_seqs, int total_q, int max_q_len,
+                          const void *kv_cache, const int32_t *page_table,
+                          int max_pages_per_seq, const int32_t *kv_lens,
+                          int num_pages, int max_kv_len, const float *sinks,
+                          float scale, void *out, float *lse, int num_qo_heads,
+                          int num_kv_heads, int head_dim, int page_size,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
