@@ -32,21 +32,31 @@
 #include "workspace.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace sa {
 namespace {
 
 constexpr int kNW = 8;                        // warps per CTA
 constexpr int kThreads = kNW * 32;
-constexpr int kStepPages = 2;                 // pages per stage
+constexpr int kStepPages = 4;                 // pages per stage
 constexpr int kStageBytes = kStepPages * kInt4Block;
 constexpr float kRaise = 8.f;                 // log2 by which a score may exceed the reference
+constexpr float kUnset = -8e37f;              // reference of a row that has seen no key yet
 
 // Stages in flight per warp, and CTAs per SM that shared memory and registers allow.
 template <int NB>
 struct Tuning {
-  static constexpr int kStages = NB == 2 ? 3 : 4;
+  static constexpr int kStages = 2;
   static constexpr int kCtas = NB == 4 ? 1 : 2;
+};
+
+// A request's share of the work: `units` (KV head, row block) pairs of `pages` pages
+// each; a request without keys, or one that is out of range (`bad`), counts one page
+// that nothing of is read.
+struct Request {
+  int kv_len, row0, tokens, pages, units;
+  bool bad;
 };
 
 template <int NB>
@@ -62,7 +72,11 @@ struct __align__(128) Shared {
   uint64_t bars[kNW][Tuning<NB>::kStages];
   long long prefix[kThreads + 1];
   long long scan[kNW];
-  int has[2][kNW];
+  struct {                                    // the unit of a part; pages 0: there is none
+    long long from;                           // its first page's number
+    Request r;
+    int pages, kvh, rb;
+  } unit[2][kNW];
   int last;
   // 0: a unit begun before the warp's share; 1: one that goes on after it (in the
   // ring, which is idle by then)
@@ -73,14 +87,6 @@ struct __align__(128) Shared {
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// A request's share of the work: `units` (KV head, row block) pairs of `pages` pages
-// each; a request without keys, or one that is out of range (`bad`), counts one page
-// that nothing of is read.
-struct Request {
-  int kv_len, row0, tokens, pages, units;
-  bool bad;
-};
 
 template <int NB, int kMode>
 __device__ __forceinline__ Request request(const Int4AttnParams &p, int b) {
@@ -121,6 +127,21 @@ struct Place {
   }
 };
 
+// KV head of a place's unit, and its row block (usually there is one, and no division).
+template <typename At>
+__device__ __forceinline__ int kv_head(const Int4AttnParams &p, const At &at) {
+  return at.unit < p.num_kv_heads ? at.unit : at.unit % p.num_kv_heads;
+}
+template <typename At>
+__device__ __forceinline__ int row_block(const Int4AttnParams &p, const At &at) {
+  return at.unit < p.num_kv_heads ? 0 : at.unit / p.num_kv_heads;
+}
+
+// a / b, mostly of small numbers.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return a <= 0xffffffffll && b <= 0xffffffffll ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 // Copies `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
                                           uint64_t policy) {
@@ -133,35 +154,63 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 
 // Field of 4 bits in each half of w, at bits 3..6 of the half, below the exponent of
 // 16: the bf16 pair (16 + low code, 16 + high code).
-__device__ __forceinline__ uint32_t field(uint32_t w) { return (w & 0x00780078u) | 0x41804180u; }
+// (One logical operation takes one constant: the other, or both, are kept in registers.)
+struct Fields {
+  uint32_t mask, sixteen;
+  __device__ __forceinline__ Fields() {
+    asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
+    asm volatile("mov.b32 %0, 0x41804180;" : "=r"(sixteen));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t w) const {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(sixteen));   // w & mask | sixteen
+    return r;
+  }
+};
 
 __device__ __forceinline__ uint32_t word(const uint4 &x, int w) {
   return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w;
 }
 
-// A key's scale and 16 + zero point, from the low half of m (K) or the high one (V).
-__device__ __forceinline__ float scale_of(uint32_t m, bool v) {
-  return __uint_as_float((v ? m : m << 16) & 0xfff00000u);
+// A key's scale, and minus 16 plus its zero point, from the low half of m.
+__device__ __forceinline__ float k_scale(uint32_t m) { return __uint_as_float((m << 16) & 0xfff00000u); }
+__device__ __forceinline__ float k_zero(uint32_t m) {
+  return __uint_as_float(((m << 19) & 0x00780000u) | 0xc1800000u);
 }
-__device__ __forceinline__ float zero_of(uint32_t m, bool v) {
-  return __uint_as_float(((v ? m << 3 : m << 19) & 0x00780000u) | 0x41800000u);
+// A value's scale, from the high half.
+__device__ __forceinline__ float v_scale(uint32_t m) { return __uint_as_float(m & 0xfff00000u); }
+// 16 plus the zero points of two values, from their words' high halves.
+__device__ __forceinline__ uint32_t v_zeros(uint32_t m0, uint32_t m1) {
+  return ((__byte_perm(m0, m1, 0x7632) << 3) & 0x00780078u) | 0x41804180u;
 }
 
-__device__ __forceinline__ void lds128(uint32_t addr, uint4 &v) {
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
+// (16 + n) - (16 + z) for two codes: exact.
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
-__device__ __forceinline__ void lds64(uint32_t addr, uint2 &v) {
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+
+// D += A B and D = A B (m16n8k16, bf16, fp32 sums), free for the compiler to move.
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Row r of the block of a unit -> its [.., Hq] row in q, out and lse (-1 past the last).
-template <int NB>
+template <int NB, int kMode>
 __device__ __forceinline__ long long row_of(const Int4AttnParams &p, const Request &q, int kvh, int rb,
                                             int r, int &token, int &head) {
   const int i = rb * 8 * NB + r;
-  token = i / p.group;
+  token = kMode == kInt4Decode ? (i >= p.group ? 1 : 0) : i / p.group;
   head = kvh * p.group + (i - token * p.group);
   return token < q.tokens ? (static_cast<long long>(q.row0) + token) * p.num_qo_heads + head : -1;
 }
@@ -180,9 +229,8 @@ __global__ void __launch_bounds__(kThreads, Tuning<NB>::kCtas)
 int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   constexpr int kStages = Tuning<NB>::kStages;
   constexpr int kRows = 8 * NB;
-  extern __shared__ uint8_t smem_raw[];
-  Shared<NB> &sh = *reinterpret_cast<Shared<NB> *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Shared<NB> &sh = *reinterpret_cast<Shared<NB> *>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
@@ -203,7 +251,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&sh.bars[warp][s], 1);
     fence_mbar_init();
-    sh.has[0][warp] = sh.has[1][warp] = 0;
+    sh.unit[0][warp].pages = sh.unit[1][warp].pages = 0;
   }
   __syncthreads();
   long long before = 0, total = 0;
@@ -217,7 +265,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
 
   // an even share, so that only its last step is half empty; whole CTAs' worth of it
   const long long slots = static_cast<long long>(gridDim.x) * kNW;
-  long long share = (total + slots - 1) / slots;
+  long long share = quotient(total + slots - 1, slots);
   share = max(share + (share & 1), static_cast<long long>(p.min_pages));
   const long long cta_share = share * kNW;
   const long long from = min(total, blockIdx.x * cta_share + warp * share);
@@ -241,14 +289,14 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
       here += w;
       ++at.b;
     }
-    at.unit = static_cast<int>((from - here) / at.r.pages);
+    at.unit = static_cast<int>(quotient(from - here, at.r.pages));
     at.page = static_cast<int>((from - here) - static_cast<long long>(at.unit) * at.r.pages);
   }
-  const long long share_pages = to - from;
+  const int share_pages = static_cast<int>(to - from);
 
   // ---- copies: `to_come` runs ahead of `at` by up to kStages steps
   At to_come = at;
-  long long unissued = share_pages;
+  int unissued = share_pages;
   int ids = -1, ids_next = -1, ids_at = 0;             // lane j: id of page ids_at + j; of the next 32
   auto load_ids = [&](int first) -> int {
     const int page = first + lane;
@@ -268,41 +316,35 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   launch_dependents();
 
   const uint64_t policy = l2_policy_evict_first();
+  const long long page_bytes = static_cast<long long>(p.num_kv_heads) * kInt4Block;
+  const uint8_t *src = p.kv_cache + static_cast<size_t>(kv_head(p, to_come)) * kInt4Block;
   uint32_t spoilt = 0;                                 // stages with a page outside of the pool
   auto issue = [&](int st) {                           // all lanes call
-    const int n = static_cast<int>(min(min(static_cast<long long>(kStepPages), unissued),
-                                       static_cast<long long>(to_come.r.pages - to_come.page)));
+    const int n = min(min(kStepPages, unissued), to_come.r.pages - to_come.page);
     if (to_come.page - ids_at >= 32) {
       ids_at += 32;
       ids = ids_next;
       ids_next = ids_at + 32 < to_come.r.pages ? load_ids(ids_at + 32) : -1;
     }
-    const int off = to_come.page - ids_at;
-    int id = __shfl_sync(0xffffffffu, ids, (off + (lane & 1)) & 31);
-    if (off == 31 && n == 2) {                         // the second page is the next batch's first
-      const int other = __shfl_sync(0xffffffffu, ids_next, 0);
-      if (lane & 1) id = other;
-    }
-    const bool wanted = lane < n;
-    const bool ok = wanted && id >= 0 && id < p.num_pages;
+    // (a batch of 32 is a whole number of steps: it begins where a unit's share does)
+    const int id = __shfl_sync(0xffffffffu, ids, to_come.page - ids_at + (lane & (kStepPages - 1)));
+    const bool ok = lane < n && id >= 0 && id < p.num_pages;
     const unsigned good = __ballot_sync(0xffffffffu, ok);
     const bool empty = to_come.r.kv_len <= 0 || to_come.r.bad;
-    spoilt &= ~(1u << st);
-    if (!empty && __popc(good) < n) spoilt |= 1u << st;
+    const int copies = __popc(good);
+    spoilt = (spoilt & ~(1u << st)) | (!empty && copies < n ? 1u << st : 0u);
     uint64_t *bar = &sh.bars[warp][st];
-    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(good) * kInt4Block);
+    if (lane == 0) mbar_arrive_expect_tx(bar, copies * kInt4Block);
     __syncwarp();
     if (ok) {
       fence_proxy_async_smem();
-      const int kvh = to_come.unit % p.num_kv_heads;
-      bulk_load(&sh.ring[warp][st][lane * kInt4Block],
-                p.kv_cache + (static_cast<size_t>(id) * p.num_kv_heads + kvh) * kInt4Block, kInt4Block,
-                bar, policy);
+      bulk_load(&sh.ring[warp][st][lane * kInt4Block], src + id * page_bytes, kInt4Block, bar, policy);
     }
     unissued -= n;
     to_come.page += n;
     if (to_come.page >= to_come.r.pages && unissued > 0) {
       to_come.next_unit(p);
+      src = p.kv_cache + static_cast<size_t>(kv_head(p, to_come)) * kInt4Block;
       start_ids();
     }
   };
@@ -311,11 +353,11 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
 
   // ---- units of this share, one after another
   bool dead = false;                                   // a copy never landed
-  long long left = share_pages;
+  int left = share_pages;
   while (left > 0) {
-    const int kvh = at.unit % p.num_kv_heads, rb = at.unit / p.num_kv_heads;
+    const int kvh = kv_head(p, at), rb = row_block(p, at);
     const int first_page = at.page;
-    const int seg = static_cast<int>(min(left, static_cast<long long>(at.r.pages - at.page)));
+    const int seg = min(left, at.r.pages - at.page);
     const int seg_end = first_page + seg;
     // keys [0, old) are visible to every row, key old + u to the rows of token u and
     // later ones, or by the mask
@@ -323,15 +365,15 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
 
     // Q^T as B operand: row g of each block; registers 2k and 2k + 1 hold pairs (dim, dim + 4)
     uint32_t qb[NB][8];
-    float qs[NB][2];                                   // sum of q, times the scale, of rows 2t and 2t + 1
-    float m[NB][2], d[NB][2], corr[NB][2];
+    float qs[NB][2];                                   // sum of q of rows 2t and 2t + 1
+    float m[NB][2], d[NB][2];                          // reference (base 2), sum
     int limit[NB][2];                                  // keys that a row sees (causal)
     uint64_t vis[NB][2];                               // and its bits of the mask
     float o[NB][4][4];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       int token, head;
-      const long long row = row_of<NB>(p, at.r, kvh, rb, 8 * nb + g, token, head);
+      const long long row = row_of<NB, kMode>(p, at.r, kvh, rb, 8 * nb + g, token, head);
       uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
       if (row >= 0) {
         const uint4 *q = reinterpret_cast<const uint4 *>(p.q) + row * (kHeadDim / 8);
@@ -353,14 +395,13 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         qs[nb][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
-        const long long r = row_of<NB>(p, at.r, kvh, rb, 8 * nb + 2 * t + e, token, head);
+        const long long r = row_of<NB, kMode>(p, at.r, kvh, rb, 8 * nb + 2 * t + e, token, head);
         // a sink that is no logit (NaN, +inf) spoils the sum, not the maximum
         const bool sink = first_page == 0 && r >= 0;
         const float logit = sink ? __ldg(p.sinks + head) * kLog2e : -INFINITY;
         const bool fine = logit < INFINITY;
-        m[nb][e] = fine ? logit : -INFINITY;
-        d[nb][e] = sink && g == 0 ? (fine ? (logit == -INFINITY ? 0.f : 1.f) : NAN) : 0.f;
-        corr[nb][e] = 0.f;
+        m[nb][e] = fine ? fmaxf(logit, kUnset) : kUnset;
+        d[nb][e] = sink && g == 0 ? (fine ? (logit < kUnset ? 0.f : 1.f) : NAN) : 0.f;
         limit[nb][e] = kMode == kInt4Decode ? at.r.kv_len : min(at.r.kv_len, old + token + 1);
         vis[nb][e] = 0;
         if constexpr (kMode == kInt4Verify) {
@@ -375,6 +416,110 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
     }
     bool bad = at.r.bad || dead;
 
+    const int tok_end = min(at.r.kv_len, seg_end * kPageSize);
+
+    // One page: its block in shared memory, its first key tok0.
+    const Fields field;
+    auto work = [&](const uint8_t *at_block, int tok0, auto is_edge) {
+      constexpr bool kEdge = decltype(is_edge)::value;
+      const uint4 kw = *reinterpret_cast<const uint4 *>(at_block + kInt4K + 16 * lane);
+      const uint2 mt = *reinterpret_cast<const uint2 *>(at_block + kInt4Meta + 8 * g);             // keys g and g + 8
+      float s[NB][4];                      // key g + 8 (i / 2), row 2t + i % 2
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = word(kw, h), hi = word(kw, 2 + h);         // keys g and g + 8
+        const uint32_t a0[4] = {field(lo), field(hi), field(lo >> 4), field(hi >> 4)};
+        const uint32_t a1[4] = {field(lo >> 8), field(hi >> 8), field(__funnelshift_r(lo, lo, 12)),
+                                field(__funnelshift_r(hi, hi, 12))};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          if (h == 0)
+            mma_first(s[nb], a0, qb[nb][0], qb[nb][1]);
+          else
+            mma_add(s[nb], a0, qb[nb][4], qb[nb][5]);
+          mma_add(s[nb], a1, qb[nb][4 * h + 2], qb[nb][4 * h + 3]);
+        }
+      }
+      const float ks[2] = {k_scale(mt.x) * p.scale_log2, k_scale(mt.y) * p.scale_log2};
+      const float kz[2] = {k_zero(mt.x), k_zero(mt.y)};
+      float vs[2] = {v_scale(mt.x), v_scale(mt.y)};
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nb][i] = ks[i / 2] * fmaf(kz[i / 2], qs[nb][i & 1], s[nb][i]);
+      if constexpr (kEdge) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = tok0 + g + 8 * (i / 2), u = tok - old;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            const bool drafted = kMode == kInt4Verify && u >= 0 && u < 64 && ((vis[nb][i & 1] >> u) & 1);
+            if (tok >= tok_end || (tok >= limit[nb][i & 1] && !drafted)) s[nb][i] = -INFINITY;
+          }
+          // a slot past the last key may hold anything
+          if (tok >= tok_end) vs[i / 2] = 0.f;
+        }
+      }
+      // any score far above its row's reference?
+      float top = -INFINITY;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        top = fmax3(top, fmaxf(s[nb][0], s[nb][2]) - m[nb][0], fmaxf(s[nb][1], s[nb][3]) - m[nb][1]);
+      if (__any_sync(0xffffffffu, top > kRaise)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(s[nb][e], s[nb][2 + e]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+            if (x > m[nb][e]) {
+              const float a = ex2(m[nb][e] - x);
+              m[nb][e] = x;
+              d[nb][e] *= a;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[nb][i][e] *= a;
+                o[nb][i][2 + e] *= a;
+              }
+            }
+          }
+      }
+      uint32_t pb[NB][2];                  // p times the value's scale, as B operand: keys 2t.., row g
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = ex2(s[nb][2 * h] - m[nb][0]), p1 = ex2(s[nb][2 * h + 1] - m[nb][1]);
+          d[nb][0] += p0;
+          d[nb][1] += p1;
+          float w0 = p0 * vs[h], w1 = p1 * vs[h];
+          if constexpr (kEdge) {           // a hidden key's scale may be NaN
+            if (s[nb][2 * h] == -INFINITY) w0 = 0.f;
+            if (s[nb][2 * h + 1] == -INFINITY) w1 = 0.f;
+          }
+          pb[nb][h] = movmatrix_trans(pack_bf16(w0, w1));
+        }
+      // word g of keys 2t, 2t + 1, 2t + 8, 2t + 9; and their zero points (2t, 2t + 8, ..)
+      const uint4 vw = *reinterpret_cast<const uint4 *>(at_block + kInt4V + 16 * lane);
+      const uint4 vm = *reinterpret_cast<const uint4 *>(at_block + kInt4Meta + 16 * t);
+      const uint32_t z0 = v_zeros(vm.x, vm.z), z1 = v_zeros(vm.y, vm.w);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {                            // dims 8g + 4c ..
+        const uint32_t sel = c ? 0x7632 : 0x5410;
+        const uint32_t lo = __byte_perm(vw.x, vw.y, sel), hi = __byte_perm(vw.z, vw.w, sel);
+        const uint32_t a0[4] = {sub_bf16x2(field(lo << 3), z0), sub_bf16x2(field(lo >> 1), z0),
+                                sub_bf16x2(field(hi << 3), z1), sub_bf16x2(field(hi >> 1), z1)};
+        const uint32_t a1[4] = {sub_bf16x2(field(lo >> 5), z0), sub_bf16x2(field(lo >> 9), z0),
+                                sub_bf16x2(field(hi >> 5), z1), sub_bf16x2(field(hi >> 9), z1)};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma_add(o[nb][2 * c], a0, pb[nb][0], pb[nb][1]);
+          mma_add(o[nb][2 * c + 1], a1, pb[nb][0], pb[nb][1]);
+        }
+      }
+    };
+
     for (int page = first_page; page < seg_end; page += kStepPages) {
       const int st = done % kStages;
       if (!dead && !mbar_wait(&sh.bars[warp][st], (done / kStages) & 1)) {
@@ -386,143 +531,14 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
       bad = bad || ((spoilt >> st) & 1);
       ++done;
       if (dead) continue;
-      const uint32_t stage = smem_u32(&sh.ring[warp][st][0]);
-      const int tok0 = page * kPageSize;
-      const int tok_end = min(at.r.kv_len, seg_end * kPageSize);
-      const bool edge = tok0 + kStepPages * kPageSize > min(tok_end, old);   // keys that not all rows see
-
-      float acc[kStepPages][NB][4];
-      uint2 meta[kStepPages];                          // keys g and g + 8
+      const uint8_t *block = &sh.ring[warp][st][0];
+      if ((page + kStepPages) * kPageSize <= min(tok_end, old)) {      // whole, keys that all rows see
 #pragma unroll
-      for (int pg = 0; pg < kStepPages; ++pg) {
-        uint4 kw;
-        lds128(stage + pg * kInt4Block + kInt4K + 16 * lane, kw);
-        lds64(stage + pg * kInt4Block + kInt4Meta + 8 * g, meta[pg]);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[pg][nb][0] = acc[pg][nb][1] = acc[pg][nb][2] = acc[pg][nb][3] = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t lo = word(kw, h), hi = word(kw, 2 + h);   // keys g and g + 8
-          const uint32_t a0[4] = {field(lo), field(hi), field(lo >> 4), field(hi >> 4)};
-          const uint32_t a1[4] = {field(lo >> 8), field(hi >> 8), field(__funnelshift_r(lo, lo, 12)),
-                                  field(__funnelshift_r(hi, hi, 12))};
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            mma_bf16_16816(acc[pg][nb], a0, qb[nb][4 * h], qb[nb][4 * h + 1]);
-            mma_bf16_16816(acc[pg][nb], a1, qb[nb][4 * h + 2], qb[nb][4 * h + 3]);
-          }
-        }
-      }
-
-      // scores relative to the reference; x[pg][nb][i]: key g + 8 (i / 2), row 2t + i % 2
-      float x[kStepPages][NB][4];
-      auto scores = [&]() {
-#pragma unroll
-        for (int pg = 0; pg < kStepPages; ++pg)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t mt = h ? meta[pg].y : meta[pg].x;
-            const float ks = scale_of(mt, false) * p.scale_log2;
-            const float kz = -zero_of(mt, false) * ks;
-            const uint64_t ks2 = f2_pack(ks, ks), kz2 = f2_pack(kz, kz);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              const float r0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0];
-              const float r1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
-              const uint64_t base = f2_fma(kz2, f2_pack(qs[nb][0], qs[nb][1]), f2_pack(-r0, -r1));
-              f2_unpack(f2_fma(ks2, f2_pack(acc[pg][nb][2 * h], acc[pg][nb][2 * h + 1]), base),
-                        x[pg][nb][2 * h], x[pg][nb][2 * h + 1]);
-            }
-          }
-        if (edge) {
-#pragma unroll
-          for (int pg = 0; pg < kStepPages; ++pg)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int tok = tok0 + pg * kPageSize + g + 8 * (i / 2);
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                const int u = tok - old;
-                const bool drafted = kMode == kInt4Verify && u >= 0 && u < 64 && ((vis[nb][i & 1] >> u) & 1);
-                if (tok >= tok_end || (tok >= limit[nb][i & 1] && !drafted)) x[pg][nb][i] = -INFINITY;
-              }
-            }
-        }
-      };
-      scores();
-      bool raise = false;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float top = fmaxf(fmaxf(x[0][nb][e], x[0][nb][2 + e]), fmaxf(x[1][nb][e], x[1][nb][2 + e]));
-          raise = raise || top > kRaise || m[nb][e] == -INFINITY;
-        }
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(fmaxf(x[0][nb][e], x[0][nb][2 + e]), fmaxf(x[1][nb][e], x[1][nb][2 + e]));
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float was = m[nb][e];
-            const float now = fmaxf(was, top + (was == -INFINITY ? 0.f : was));
-            if (now > was) {
-              const float a = ex2(was - now);
-              m[nb][e] = now;
-              d[nb][e] *= a;
-              corr[nb][e] *= a;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                o[nb][i][e] *= a;
-                o[nb][i][2 + e] *= a;
-              }
-            }
-          }
-        scores();
-      }
-
-#pragma unroll
-      for (int pg = 0; pg < kStepPages; ++pg) {
-        uint32_t pb[NB][2];                            // P s as B operand: keys 2t.., row g
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t mt = h ? meta[pg].y : meta[pg].x;
-          float vs = scale_of(mt, true);
-          const float vz = -zero_of(mt, true);
-          // a slot past the last key may hold anything, a hidden key's scale may be NaN
-          if (edge && tok0 + pg * kPageSize + g + 8 * h >= tok_end) vs = 0.f;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            const float p0 = ex2(x[pg][nb][2 * h]), p1 = ex2(x[pg][nb][2 * h + 1]);
-            d[nb][0] += p0;
-            d[nb][1] += p1;
-            float w0 = p0 * vs, w1 = p1 * vs;
-            if (edge) {
-              if (x[pg][nb][2 * h] == -INFINITY) w0 = 0.f;
-              if (x[pg][nb][2 * h + 1] == -INFINITY) w1 = 0.f;
-            }
-            const uint32_t w = pack_bf16(w0, w1);
-            corr[nb][0] = fmaf(__uint_as_float(w << 16), vz, corr[nb][0]);
-            corr[nb][1] = fmaf(__uint_as_float(w & 0xffff0000u), vz, corr[nb][1]);
-            pb[nb][h] = movmatrix_trans(w);
-          }
-        }
-        uint4 vw;                                      // word g of keys 2t, 2t + 1, 2t + 8, 2t + 9
-        lds128(stage + pg * kInt4Block + kInt4V + 16 * lane, vw);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {                  // dims 8g + 4c ..
-          const uint32_t sel = c ? 0x7632 : 0x5410;
-          const uint32_t lo = __byte_perm(vw.x, vw.y, sel), hi = __byte_perm(vw.z, vw.w, sel);
-          const uint32_t a0[4] = {field(lo << 3), field(lo >> 1), field(hi << 3), field(hi >> 1)};
-          const uint32_t a1[4] = {field(lo >> 5), field(lo >> 9), field(hi >> 5), field(hi >> 9)};
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            mma_bf16_16816(o[nb][2 * c], a0, pb[nb][0], pb[nb][1]);
-            mma_bf16_16816(o[nb][2 * c + 1], a1, pb[nb][0], pb[nb][1]);
-          }
-        }
+        for (int i = 0; i < kStepPages; ++i) work(block + i * kInt4Block, 0, std::false_type{});
+      } else {
+        const int end = min(page + kStepPages, seg_end);
+#pragma unroll 1
+        for (int i = page; i < end; ++i, block += kInt4Block) work(block, i * kPageSize, std::true_type{});
       }
       __syncwarp();                                    // the stage has been read
       if (unissued > 0) issue(issued++ % kStages);
@@ -536,20 +552,17 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float dd = d[nb][e], cc = corr[nb][e];
+        float dd = d[nb][e];
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          dd += __shfl_xor_sync(0xffffffffu, dd, off);
-          cc += __shfl_xor_sync(0xffffffffu, cc, off);
-        }
+        for (int off = 4; off < 32; off <<= 1) dd += __shfl_xor_sync(0xffffffffu, dd, off);
         if (bad) dd = NAN;
         // o[nb][i][e] and [2 + e]: dims 8g + 2i and 8g + 2i + 1
-        const float4 lo = make_float4(o[nb][0][e] + cc, o[nb][0][2 + e] + cc, o[nb][1][e] + cc, o[nb][1][2 + e] + cc);
-        const float4 hi = make_float4(o[nb][2][e] + cc, o[nb][2][2 + e] + cc, o[nb][3][e] + cc, o[nb][3][2 + e] + cc);
+        const float4 lo = make_float4(o[nb][0][e], o[nb][0][2 + e], o[nb][1][e], o[nb][1][2 + e]);
+        const float4 hi = make_float4(o[nb][2][e], o[nb][2][2 + e], o[nb][3][e], o[nb][3][2 + e]);
         const int r = 8 * nb + 2 * t + e;
         if (!begun && !goes_on) {
           int token, head;
-          const long long row = row_of<NB>(p, at.r, kvh, rb, r, token, head);
+          const long long row = row_of<NB, kMode>(p, at.r, kvh, rb, r, token, head);
           if (row >= 0) {
             write_row(p, row, 8 * g, lo, m[nb][e], dd);
             write_row(p, row, 8 * g + 4, hi, m[nb][e], dd);
@@ -563,7 +576,14 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
           }
         }
       }
-    if (lane == 0 && (begun || goes_on)) sh.has[slot][warp] = 1;
+    if (lane == 0 && (begun || goes_on)) {
+      auto &u = sh.unit[slot][warp];
+      u.from = to - left - first_page;
+      u.r = at.r;
+      u.pages = at.r.pages;
+      u.kvh = kvh;
+      u.rb = rb;
+    }
     left -= seg;
     at.page = seg_end;
     if (left > 0) at.next_unit(p);
@@ -575,30 +595,12 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   const long long cta_from = blockIdx.x * cta_share, cta_to = min(total, cta_from + cta_share);
   for (int round = 0; round < kNW + 1; ++round) {      // round 0: the unit begun before the CTA; 1 + w: by warp w
     const int w0 = max(round - 1, 0), s0 = round == 0 ? 0 : 1;
-    if (!sh.has[s0][w0]) continue;                     // uniform over the CTA
+    const auto &u = sh.unit[s0][w0];
+    if (u.pages == 0) continue;                        // uniform over the CTA
+    const long long u_from = u.from, u_to = u_from + u.pages;
     int w1 = w0 + 1;                                   // its parts: (s0, w0), (0, w0 + 1 ..)
-    // where the unit is, from the first page of warp w0's share that is its
-    const long long w_from = min(total, cta_from + w0 * share);
-    const long long w_to = min(total, w_from + share);
-    const long long known = s0 == 0 ? w_from : w_to - 1;   // a page of it
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i)
-      n += __popc(__ballot_sync(0xffffffffu, sh.prefix[i * 32 + lane] <= known));
-    At u;
-    u.b = (n - 1) * per;
-    long long here = sh.prefix[n - 1];
-    while (true) {
-      u.r = request<NB, kMode>(p, u.b);
-      const long long w = static_cast<long long>(u.r.pages) * u.r.units;
-      if (here + w > known) break;
-      here += w;
-      ++u.b;
-    }
-    u.unit = static_cast<int>((known - here) / u.r.pages);
-    const long long u_from = here + static_cast<long long>(u.unit) * u.r.pages, u_to = u_from + u.r.pages;
     while (w1 < kNW && cta_from + w1 * share < min(u_to, total)) ++w1;
-    const int kvh = u.unit % p.num_kv_heads, rb = u.unit / p.num_kv_heads;
+    const int kvh = u.kvh, rb = u.rb;
     const bool whole = u_from >= cta_from && u_to <= cta_to;
 
     constexpr int kItems = kRows * (kHeadDim / 4);
@@ -611,8 +613,8 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int w = w0; w < w1; ++w) {
         const Part<NB> &x = sh.part(w == w0 ? s0 : 0, w);
-        const float wt = x.m[r] == -INFINITY ? 0.f : ex2(x.m[r] - mx);
-        den += x.d[r] != x.d[r] ? NAN : wt * x.d[r];
+        const float wt = ex2(x.m[r] - mx);
+        den += wt * x.d[r];
         const float4 v = *reinterpret_cast<const float4 *>(&x.o[r][dq]);
         a.x += wt * v.x;
         a.y += wt * v.y;
@@ -621,7 +623,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
       }
       if (whole) {
         int token, head;
-        const long long row = row_of<NB>(p, u.r, kvh, rb, r, token, head);
+        const long long row = row_of<NB, kMode>(p, u.r, kvh, rb, r, token, head);
         if (row >= 0) write_row(p, row, dq, a, mx, den);
       } else {
         *reinterpret_cast<float4 *>(p.ws_o + (mine_at * kRows + r) * kHeadDim + dq) = a;
@@ -632,13 +634,12 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
 
     // the last of the CTAs that share the unit joins their parts, in page order, and
     // leaves the counter at zero for the next call
-    const int c0 = static_cast<int>(u_from / cta_share), c1 = static_cast<int>((u_to - 1) / cta_share);
-    __threadfence();
+    const int c0 = static_cast<int>(quotient(u_from, cta_share));
+    const int c1 = static_cast<int>(quotient(u_to - 1, cta_share));
     __syncthreads();
-    if (threadIdx.x == 0) sh.last = atomicAdd(&p.counters[c0], 1) == c1 - c0;
+    if (threadIdx.x == 0) sh.last = atomic_add_acq_rel(&p.counters[c0], 1) == c1 - c0;
     __syncthreads();
     if (!sh.last) continue;
-    __threadfence();
     for (int item = threadIdx.x; item < kItems; item += kThreads) {
       const int r = item / (kHeadDim / 4), dq = (item % (kHeadDim / 4)) * 4;
       auto index = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRows + r; };
@@ -650,15 +651,15 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
       for (int c = c0; c <= c1; ++c) {
         const float2 md = __ldcg(&p.ws_md[index(c)]);
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + index(c) * kHeadDim + dq));
-        const float wt = md.x == -INFINITY ? 0.f : ex2(md.x - mx);
-        den += md.y != md.y ? NAN : wt * md.y;
+        const float wt = ex2(md.x - mx);
+        den += wt * md.y;
         a.x += wt * v.x;
         a.y += wt * v.y;
         a.z += wt * v.z;
         a.w += wt * v.w;
       }
       int token, head;
-      const long long row = row_of<NB>(p, u.r, kvh, rb, r, token, head);
+      const long long row = row_of<NB, kMode>(p, u.r, kvh, rb, r, token, head);
       if (row >= 0) write_row(p, row, dq, a, mx, den);
     }
     if (threadIdx.x == 0) p.counters[c0] = 0;
@@ -668,7 +669,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
 
 template <int NB, int kMode>
 cudaError_t launch_variant(const Int4AttnParams &p, int ctas, cudaStream_t stream, bool programmatic) {
-  constexpr int kBytes = static_cast<int>(sizeof(Shared<NB>)) + 128;
+  constexpr int kBytes = static_cast<int>(sizeof(Shared<NB>));
   static_assert(kBytes <= 227 * 1024, "shared memory");
   cudaError_t err = set_smem_once<int4_decode_kernel<NB, kMode>>(kBytes);
   if (err != cudaSuccess) return err;
@@ -686,7 +687,7 @@ cudaError_t launch_mode(const Int4AttnParams &p, Int4Mode mode, int ctas, cudaSt
 
 template <int NB>
 int ctas_per_sm() {
-  return std::min(Tuning<NB>::kCtas, 228 * 1024 / static_cast<int>(sizeof(Shared<NB>) + 128 + 1024));
+  return std::min(Tuning<NB>::kCtas, 228 * 1024 / static_cast<int>(sizeof(Shared<NB>) + 1024));
 }
 
 }  // namespace
