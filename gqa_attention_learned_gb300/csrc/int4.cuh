@@ -83,4 +83,9 @@ size_t int4_decode_results_bytes(int row_blocks, int ctas);   // of ws_o and ws_
 cudaError_t launch_int4_decode(const Int4AttnParams &p, Int4Mode mode, int row_blocks, int ctas,
                                cudaStream_t stream, bool programmatic);
 
+// Tensor-core form: for groups of at most 128 heads.  Tokens of a CTA; CTAs for one
+// KV head are at most total_q / tokens + num_seqs.
+int int4_prefill_tokens(int group);
+cudaError_t launch_int4_prefill(const Int4AttnParams &p, long long ctas, cudaStream_t stream);
+
 }  // namespace sa

@@ -17,6 +17,8 @@ using sa::kPageSize;
 
 constexpr int kMinPages = 4;            // pages that a warp takes at least: fewer cost more to join than they save
 
+constexpr int kFewRows = 32;            // query rows per KV head up to which the kernel of few rows is taken
+
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -89,6 +91,12 @@ int attention_entry(sa::Int4Mode mode, const void *q, const int32_t *cu_seqlens_
   p.min_pages = kMinPages;
 
   const int rows = static_cast<int>(std::min<long long>(static_cast<long long>(max_q_len) * p.group, 1 << 20));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (mode != sa::kInt4Decode && p.group <= 128 && rows > kFewRows) {
+    const long long tiles = total_q / sa::int4_prefill_tokens(p.group) + static_cast<long long>(num_seqs);
+    if (tiles * num_kv_heads > 0x7fffffffll) return SINKATTN_UNSUPPORTED;
+    return sa::api_status(sa::launch_int4_prefill(p, tiles * num_kv_heads, st), "int4 attention launch");
+  }
   const int blocks = sa::int4_row_blocks(rows);
   const int slots = sms * sa::int4_decode_ctas_per_sm(blocks);
   const long long pages = std::max(1ll, ceil_div(p.max_kv_len, kPageSize));
@@ -100,7 +108,7 @@ int attention_entry(sa::Int4Mode mode, const void *q, const int32_t *cu_seqlens_
   p.counters = reinterpret_cast<int *>(ws);
   p.ws_o = reinterpret_cast<float *>(ws + sa::kCounterSpan);
   p.ws_md = reinterpret_cast<float2 *>(p.ws_o + static_cast<size_t>(ctas) * 2 * 8 * blocks * kHeadDim);
-  return sa::api_status(sa::launch_int4_decode(p, mode, blocks, ctas, static_cast<cudaStream_t>(stream),
+  return sa::api_status(sa::launch_int4_decode(p, mode, blocks, ctas, st,
                                                mode != sa::kInt4Ragged && sa::programmatic_for(launch_flags)),
                         "int4 attention launch");
 }
