@@ -11,13 +11,13 @@
 // head), as two 128-row tiles that share every K and V tile of 128 keys: turning a tile
 // of codes into bf16 costs half of what it would for one, and one tile's products run
 // during the other's softmax.
-//   warps 8..11   packed pages from global memory into registers, a tile ahead; codes
+//   warps 8..15   packed pages from global memory into registers, a tile ahead; codes
 //                 to bf16 (shift, mask under the exponent of 16, subtract 16 + z,
 //                 multiply by s); stores into K and V rings in the swizzled layout.
 //                 A word of codes gives dims (0 4 1 5 2 6 3 7) of a group of eight in
 //                 that order: Q is permuted likewise, O's columns are put right at the end.
-//   warp 12       S = Q K^T for either tile as soon as its last S has been used
-//   warp 13       O += P V for either tile
+//   warp 16       S = Q K^T for either tile as soon as its last S has been used
+//   warp 17       O += P V for either tile
 //   warps 0..7    softmax, one thread per row.  Scores come 32 at a time and are not
 //                 compared: P = 2^(s - m) with the row's reference m, and only if a
 //                 tile's sum shows that m has become too small (or is not set) the
@@ -39,8 +39,11 @@ constexpr int kBM = 128;                       // rows per tile
 constexpr int kBN = 128;                       // keys per K / V tile
 constexpr int kStages = 3;                     // of the K ring and of the V ring
 constexpr int kTileBytes = kBN * kHeadDim * 2; // 16 KB
-constexpr int kThreads = 448;
-constexpr int kUnpackWarp = 8, kUnpackWarps = 4, kQkWarp = 12, kPvWarp = 13;
+constexpr int kThreads = 640;                  // five warpgroups
+constexpr int kUnpackWarp = 8, kUnpackWarps = 8, kQkWarp = 16, kPvWarp = 17;
+// Registers per thread: the launch has 96 for all; softmax warps take from the others.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 144, kOtherRegs = 64;
+static_assert(2 * kSoftmaxRegs + 3 * kOtherRegs <= 5 * kLaunchRegs, "the split fits the launch's registers");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 192, kColTile = 256;   // of tile 0; tile 1 kColTile on
 constexpr float kUnset = -8e37f;               // reference of a row that has seen no key yet
@@ -164,7 +167,7 @@ __device__ __forceinline__ float weigh_tile(uint32_t trow, float sl2, float m, c
 }
 
 // Largest scaled score of this thread's row among the keys that it sees.
-__device__ __noinline__ float row_max(uint32_t trow, float sl2, Seen seen, int key0) {
+__device__ __forceinline__ float row_max(uint32_t trow, float sl2, Seen seen, int key0) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -178,7 +181,7 @@ __device__ __noinline__ float row_max(uint32_t trow, float sl2, Seen seen, int k
   return mx;
 }
 
-__device__ __noinline__ void scale_o(uint32_t trow, float alpha) {
+__device__ __forceinline__ void scale_o(uint32_t trow, float alpha) {
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     uint32_t x[32];
@@ -223,7 +226,14 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t m, bool v) {
 struct Packed {
   uint4 k, v, vm;        // vm: keys 2t, 2t + 8, 2t + 1, 2t + 9
   uint2 km;              // keys g, g + 8
+  uint32_t own;          // key `lane` (of lanes 0..15), to be looked at for odd values
 };
+
+template <int kRegs, bool kMore>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
 int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
@@ -328,58 +338,81 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
 
   if (warp >= kUnpackWarp && warp < kUnpackWarp + kUnpackWarps) {
     // --------------------------------------------------- packed pages to tiles
-    const int uw = warp - kUnpackWarp;
+    set_registers<kOtherRegs, false>();
+    const int uw = warp - kUnpackWarp;                 // this warp's page of every tile
     const int g = lane >> 2, t = lane & 3;
     const int npages = cdiv(rq.kv_len, kPageSize);
     const int32_t *table = p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq;
     uint32_t mask, sixteen;
     asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
     asm volatile("mov.b32 %0, 0x41804180;" : "=r"(sixteen));
-    // this warp's pages of tile j: 8 j + 2 uw and the next
-    auto page_ids = [&](int j) { return lane < 2 && 8 * j + 2 * uw + lane < npages ? __ldg(table + 8 * j + 2 * uw + lane) : 0; };
-    auto fetch = [&](int ids, int j, Packed (&f)[2]) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        int id = __shfl_sync(0xffffffffu, ids, u);
-        const bool ok = id >= 0 && id < p.num_pages;
-        if (!ok) {
-          id = 0;                                      // never dereferenced as it is
-          if (lane == 0 && 8 * j + 2 * uw + u < npages) atomicOr(&bar.bad, 1);
-        }
-        const uint8_t *block = p.kv_cache + (static_cast<size_t>(id) * p.num_kv_heads + kvh) * kInt4Block;
-        f[u].k = __ldg(reinterpret_cast<const uint4 *>(block + kInt4K) + lane);
-        f[u].v = __ldg(reinterpret_cast<const uint4 *>(block + kInt4V) + lane);
-        f[u].km = __ldg(reinterpret_cast<const uint2 *>(block + kInt4Meta) + g);
-        f[u].vm = __ldg(reinterpret_cast<const uint4 *>(block + kInt4Meta) + t);
+    auto page_id = [&](int j) { return 8 * j + uw < npages ? __ldg(table + 8 * j + uw) : 0; };
+    auto fetch = [&](int id, int j, Packed &f) {
+      if (id < 0 || id >= p.num_pages) {
+        id = 0;                                        // never dereferenced as it is
+        if (lane == 0) atomicOr(&bar.bad, 1);
       }
+      const uint8_t *block = p.kv_cache + (static_cast<size_t>(id) * p.num_kv_heads + kvh) * kInt4Block;
+      f.k = __ldg(reinterpret_cast<const uint4 *>(block + kInt4K) + lane);
+      f.v = __ldg(reinterpret_cast<const uint4 *>(block + kInt4V) + lane);
+      f.km = __ldg(reinterpret_cast<const uint2 *>(block + kInt4Meta) + g);
+      f.vm = __ldg(reinterpret_cast<const uint4 *>(block + kInt4Meta) + t);
+      f.own = __ldg(reinterpret_cast<const uint32_t *>(block + kInt4Meta + 8 * (lane & 7) + 4 * ((lane >> 3) & 1)));
     };
+    // Odd keys of the page: those past the last one become zeros, and a value that is not
+    // finite zeros with a key that is not finite.  Rare but for the last tile.
+    auto mend = [&](int j, Packed &f) {
+      const int key0 = (8 * j + uw) * kPageSize;
+      const unsigned odd = __ballot_sync(0xffffffffu, (f.own & 0x7f800000u) == 0x7f800000u) & 0xffffu;
+      const int live = rq.kv_len - key0;
+      if (odd == 0 && live >= kPageSize) return;
+      const unsigned gone = live >= kPageSize ? 0u : live <= 0 ? 0xffffu : 0xffffu & (0xffffu << live);
+      auto k = [&](uint32_t &m, int key) {
+        if (odd >> key & 1) m |= 0x7fc0u;
+        if (gone >> key & 1) m = 0;
+      };
+      auto v = [&](uint32_t &m, int key) {
+        if ((odd | gone) >> key & 1) m = 0;
+      };
+      k(f.km.x, g);
+      k(f.km.y, g + 8);
+      v(f.vm.x, 2 * t);
+      v(f.vm.y, 2 * t + 8);
+      v(f.vm.z, 2 * t + 1);
+      v(f.vm.w, 2 * t + 9);
+    };
+    // Stores of eight lanes fall into different banks: every other row has its second
+    // chunk first.
+    const int odd_row = g & 1;
+    const uint32_t k_at = 16 * uw * 128 + g * 128;     // row g of the page
+    const uint32_t k_first = (((t + 4 * odd_row) ^ g) << 4), k_second = (((t + 4 - 4 * odd_row) ^ g) << 4);
+    const uint32_t v_at = (16 * uw + 2 * t) * 128;     // row 2t
+    const uint32_t v_even = (g ^ (2 * t)) << 4, v_odd = 128 + ((g ^ (2 * t + 1)) << 4);
+
     bool ok = true;
-    Packed f[2];
-    if (n_tiles > 0) fetch(page_ids(0), 0, f);
-    int ids = page_ids(1);
+    Packed f, next;
+    int id = page_id(1);
+    if (n_tiles > 0) fetch(page_id(0), 0, next);
     for (int j = 0; j < n_tiles; ++j) {
       const int s = j % kStages;
+      f = next;
+      if (j + 1 < n_tiles) {                           // its latency runs under this tile's work
+        fetch(id, j + 1, next);
+        id = page_id(j + 2);
+      }
+      mend(j, f);
       if (j >= kStages && !__all_sync(0xffffffffu, mbar_wait(&bar.k_empty[s], (j / kStages + 1) & 1))) {
         ok = false;
         break;
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int row0 = 32 * uw + 16 * u;             // of the tile
-        const int key0 = j * kBN + row0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = row0 + g + 8 * h;
-          uint32_t m = h ? f[u].km.y : f[u].km.x;
-          // a value that is not finite spoils its key
-          if ((m & 0x7f800000u) == 0x7f800000u) m |= 0x7fc0u;
-          if (key0 + g + 8 * h >= rq.kv_len) m = 0;
-          const uint32_t s2 = pair_scale(m, false), z2 = pair_zero(m, false);
-          const uint32_t w0 = h ? f[u].k.z : f[u].k.x, w1 = h ? f[u].k.w : f[u].k.y;
-          uint8_t *row = sK(s) + r * 128;
-          *reinterpret_cast<uint4 *>(row + ((t ^ (r & 7)) << 4)) = values(w0, s2, z2, mask, sixteen);
-          *reinterpret_cast<uint4 *>(row + (((t + 4) ^ (r & 7)) << 4)) = values(w1, s2, z2, mask, sixteen);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t m = h ? f.km.y : f.km.x;
+        const uint32_t s2 = pair_scale(m, false), z2 = pair_zero(m, false);
+        const uint32_t w0 = h ? f.k.z : f.k.x, w1 = h ? f.k.w : f.k.y;
+        uint8_t *row = sK(s) + k_at + h * 1024;
+        *reinterpret_cast<uint4 *>(row + k_first) = values(odd_row ? w1 : w0, s2, z2, mask, sixteen);
+        *reinterpret_cast<uint4 *>(row + k_second) = values(odd_row ? w0 : w1, s2, z2, mask, sixteen);
       }
       fence_proxy_async_smem();
       mbar_arrive(&bar.k_full[s]);
@@ -388,23 +421,11 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
         break;
       }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int row0 = 32 * uw + 16 * u;
-        const uint32_t ms[4] = {f[u].vm.x, f[u].vm.z, f[u].vm.y, f[u].vm.w};   // keys 2t, 2t + 1, 2t + 8, 2t + 9
-        const uint32_t ws[4] = {f[u].v.x, f[u].v.y, f[u].v.z, f[u].v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = row0 + 2 * t + (i & 1) + 8 * (i >> 1);
-          uint32_t m = ms[i];
-          if ((m & 0x7f800000u) == 0x7f800000u || j * kBN + r >= rq.kv_len) m = 0;
-          *reinterpret_cast<uint4 *>(sV(s) + r * 128 + ((g ^ (r & 7)) << 4)) =
-              values(__funnelshift_l(ws[i], ws[i], 3), pair_scale(m, true), pair_zero(m, true), mask, sixteen);
-        }
-      }
-      // the next tile's pages: their latency runs under the waits above
-      if (j + 1 < n_tiles) {
-        fetch(ids, j + 1, f);
-        ids = page_ids(j + 2);
+      for (int i = 0; i < 4; ++i) {                    // keys 2t, 2t + 1, 2t + 8, 2t + 9
+        const uint32_t m = i == 0 ? f.vm.x : i == 1 ? f.vm.z : i == 2 ? f.vm.y : f.vm.w;
+        const uint32_t w = i == 0 ? f.v.x : i == 1 ? f.v.y : i == 2 ? f.v.z : f.v.w;
+        *reinterpret_cast<uint4 *>(sV(s) + v_at + (i >> 1) * 1024 + (i & 1 ? v_odd : v_even)) =
+            values(__funnelshift_l(w, w, 3), pair_scale(m, true), pair_zero(m, true), mask, sixteen);
       }
       fence_proxy_async_smem();
       mbar_arrive(&bar.v_full[s]);
@@ -412,6 +433,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     if (!ok && lane == 0) atomicOr(&bar.bad, 1);
   } else if (warp == kQkWarp) {
     // ------------------------------------------------------------------ Q K^T
+    set_registers<kOtherRegs, false>();
     bool ok = true;
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kStages;
@@ -438,6 +460,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     if (!ok && lane == 0) atomicOr(&bar.bad, 1);
   } else if (warp == kPvWarp) {
     // -------------------------------------------------------------------- P V
+    set_registers<kOtherRegs, false>();
     bool ok = true;
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kStages;
@@ -464,6 +487,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     if (!ok && lane == 0) atomicOr(&bar.bad, 1);
   } else if (warp < kUnpackWarp) {
     // ---------------------------------------------------------------- softmax
+    set_registers<kSoftmaxRegs, true>();
     const int x = warp >> 2;
     const int r = threadIdx.x & (kBM - 1);             // row = tensor-memory lane
     const uint32_t trow = tmem + x * kColTile + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -545,6 +569,8 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
       if (p.lse) p.lse[row] = failed ? NAN : d == 0.f ? -INFINITY : (m + lg2(d)) * kLn2;
     }
     return;
+  } else {
+    set_registers<kOtherRegs, false>();                // the rest of the last warpgroup
   }
   tc_fence_before();
   __syncthreads();          // the softmax warps have read O: tensor memory is free
