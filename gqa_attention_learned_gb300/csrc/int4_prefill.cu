@@ -37,29 +37,39 @@ namespace {
 
 constexpr int kBM = 128;                       // rows per tile
 constexpr int kBN = 128;                       // keys per K / V tile
-constexpr int kStages = 3;                     // of the K ring and of the V ring
+constexpr int kPages = kBN / kPageSize;        // pages per key tile
+constexpr int kStages = 3;                     // of the ring of K and V tiles
 constexpr int kTileBytes = kBN * kHeadDim * 2; // 16 KB
 constexpr int kThreads = 640;                  // five warpgroups
-constexpr int kUnpackWarp = 8, kUnpackWarps = 8, kQkWarp = 16, kPvWarp = 17;
+constexpr int kUnpackWarp = 8, kUnpackWarps = kPages, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18;
 // Registers per thread: the launch has 96 for all; softmax warps take from the others.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 144, kOtherRegs = 64;
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 152, kOtherRegs = 56;
 static_assert(2 * kSoftmaxRegs + 3 * kOtherRegs <= 5 * kLaunchRegs, "the split fits the launch's registers");
+constexpr int kBuffers = 3;                    // of scores in tensor memory
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColP = 128, kColO = 192, kColTile = 256;   // of tile 0; tile 1 kColTile on
+constexpr uint32_t kColO = kBuffers * kBN;      // behind the scores: 64 columns per tile
 constexpr float kUnset = -8e37f;               // reference of a row that has seen no key yet
 constexpr float kMostSum = 1024.f;             // sum of a tile's P from which the reference is moved
 
 constexpr int kOffQ = 0;                       // two tiles
 constexpr int kOffK = 2 * kTileBytes;
 constexpr int kOffV = kOffK + kStages * kTileBytes;
-constexpr int kOffBars = kOffV + kStages * kTileBytes;
+constexpr int kRaw = 4;                        // key tiles of packed pages on their way or waiting
+constexpr int kOffRaw = kOffV + kStages * kTileBytes;
+constexpr int kOffBars = kOffRaw + kRaw * kPages * kInt4Block;
 
+// Products are numbered through: key tile 0 of query tile 0, of query tile 1, key tile 1
+// of query tile 0, ..; product n uses scores buffer n % 3.  A parity tells two phases
+// apart, no more, so a wait has to be sure of the phase before (S of product n says that
+// P of product n - 3 has been used) and that the one after cannot have passed (P V are
+// done in order: none after product n before its P is there; and a query tile's last
+// product has at most two behind it).
 struct Bars {
-  uint64_t k_full[kStages], k_empty[kStages];
-  uint64_t v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2];      // S of the tile's current keys is in tensor memory
-  uint64_t p_full[2];      // P is, and S has been used
-  uint64_t pv_done[2];     // P has been used and O holds the keys so far
+  uint64_t raw_full[kRaw], raw_empty[kRaw];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[kBuffers];   // S is in the buffer
+  uint64_t p_full[kBuffers];   // P is, in its place
+  uint64_t p_used[kBuffers];   // P V has finished: the buffer is free
   uint32_t tmem_base;
   int bad;
 };
@@ -109,10 +119,10 @@ struct Seen {
   }
 };
 
-// P = 2^(s * scale - m) for 32 scores as bf16 pairs in x[0..15]; their sums in acc.
+// P = 2^(s * scale - m) for 32 scores x as bf16 pairs in y; their sums in acc.
 template <bool kMask>
-__device__ __forceinline__ void weigh(uint32_t (&x)[32], uint64_t scale2, uint64_t negm2, const Seen &seen,
-                                      int key0, uint64_t &acc0, uint64_t &acc1) {
+__device__ __forceinline__ void weigh(const uint32_t (&x)[32], uint32_t (&y)[16], uint64_t scale2, uint64_t negm2,
+                                      const Seen &seen, int key0, uint64_t &acc0, uint64_t &acc1) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     float a, b;
@@ -124,55 +134,38 @@ __device__ __forceinline__ void weigh(uint32_t (&x)[32], uint64_t scale2, uint64
     const float pa = ex2(a), pb = ex2(b);
     if (e & 1) acc1 = f2_add(acc1, f2_pack(pa, pb));
     else acc0 = f2_add(acc0, f2_pack(pa, pb));
-    x[e] = pack_bf16(pa, pb);
+    y[e] = pack_bf16(pa, pb);
   }
 }
 
-__device__ __forceinline__ void store_p(uint32_t taddr, const uint32_t (&x)[32]) {
-  tmem_st16(taddr, *reinterpret_cast<const uint32_t(*)[16]>(&x[0]));
-}
-
-// All 128 scores of this thread's row against its reference m: P into tensor memory once
-// the previous P has been used.  Returns the row's sum, or a negative number if a wait
-// timed out.
+// All 128 scores of this thread's row (at `ts` in tensor memory) against its reference m.
+// P stays in registers: the scores have to be there still if m turns out too small.
+// Returns the row's sum.
 template <bool kMask>
-__device__ __forceinline__ float weigh_tile(uint32_t trow, float sl2, float m, const Seen &seen, int key0,
-                                            uint64_t *pv_done, int parity) {
+__device__ __forceinline__ float weigh_tile(uint32_t ts, float sl2, float m, const Seen &seen, int key0,
+                                            uint32_t (&y)[4][16]) {
   const uint64_t scale2 = f2_pack(sl2, sl2), negm2 = f2_pack(-m, -m);
   uint64_t acc0 = 0, acc1 = 0;
-  uint32_t x0[32], x1[32], x2[32];
-  tmem_ld32(trow + kColS, x0);
-  tmem_ld_wait32(x0);
-  tmem_ld32(trow + kColS + 32, x1);
-  weigh<kMask>(x0, scale2, negm2, seen, key0, acc0, acc1);
-  tmem_ld_wait32(x1);
-  tmem_ld32(trow + kColS + 64, x2);
-  weigh<kMask>(x1, scale2, negm2, seen, key0 + 32, acc0, acc1);
-  bool ok = true;
-  if (parity >= 0) ok = __all_sync(0xffffffffu, mbar_wait(pv_done, parity));
-  tc_fence_after();
-  store_p(trow + kColP, x0);
-  store_p(trow + kColP + 16, x1);
-  tmem_ld_wait32(x2);
-  tmem_ld32(trow + kColS + 96, x0);
-  weigh<kMask>(x2, scale2, negm2, seen, key0 + 64, acc0, acc1);
-  store_p(trow + kColP + 32, x2);
-  tmem_ld_wait32(x0);
-  weigh<kMask>(x0, scale2, negm2, seen, key0 + 96, acc0, acc1);
-  store_p(trow + kColP + 48, x0);
-  tmem_st_wait();
+  uint32_t x[2][32];
+  tmem_ld32(ts, x[0]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld_wait32(x[c & 1]);
+    if (c < 3) tmem_ld32(ts + 32 * (c + 1), x[(c + 1) & 1]);
+    weigh<kMask>(x[c & 1], y[c], scale2, negm2, seen, key0 + 32 * c, acc0, acc1);
+  }
   float a, b;
   f2_unpack(f2_add(acc0, acc1), a, b);
-  return ok ? a + b : -1.f;
+  return a + b;
 }
 
 // Largest scaled score of this thread's row among the keys that it sees.
-__device__ __forceinline__ float row_max(uint32_t trow, float sl2, Seen seen, int key0) {
+__device__ __forceinline__ float row_max(uint32_t ts, float sl2, const Seen &seen, int key0) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t x[32];
-    tmem_ld32(trow + kColS + 32 * c, x);
+    tmem_ld32(ts + 32 * c, x);
     tmem_ld_wait32(x);
 #pragma unroll
     for (int e = 0; e < 32; ++e)
@@ -181,16 +174,16 @@ __device__ __forceinline__ float row_max(uint32_t trow, float sl2, Seen seen, in
   return mx;
 }
 
-__device__ __forceinline__ void scale_o(uint32_t trow, float alpha) {
+__device__ __forceinline__ void scale_o(uint32_t to, float alpha) {
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
     uint32_t x[32];
-    tmem_ld32(trow + kColO + 32 * h, x);
+    tmem_ld32(to + 32 * h, x);
     tmem_ld_wait32(x);
 #pragma unroll
     for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-    tmem_st16(trow + kColO + 32 * h, *reinterpret_cast<uint32_t(*)[16]>(&x[0]));
-    tmem_st16(trow + kColO + 32 * h + 16, *reinterpret_cast<uint32_t(*)[16]>(&x[16]));
+    tmem_st16(to + 32 * h, *reinterpret_cast<uint32_t(*)[16]>(&x[0]));
+    tmem_st16(to + 32 * h + 16, *reinterpret_cast<uint32_t(*)[16]>(&x[16]));
   }
   tmem_st_wait();
 }
@@ -222,12 +215,21 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t m, bool v) {
   return ((__byte_perm(m, 0, v ? 0x3232 : 0x1010) << 3) & 0x00780078u) | 0x41804180u;
 }
 
-// One page's share of a lane: unit (g, t) of K and of V, and the scales it needs.
-struct Packed {
-  uint4 k, v, vm;        // vm: keys 2t, 2t + 8, 2t + 1, 2t + 9
-  uint2 km;              // keys g, g + 8
-  uint32_t own;          // key `lane` (of lanes 0..15), to be looked at for odd values
-};
+// Copies `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+// Pages are read by many CTAs.
+__device__ __forceinline__ uint64_t l2_policy_evict_last() {
+  uint64_t policy;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
 
 template <int kRegs, bool kMore>
 __device__ __forceinline__ void set_registers() {
@@ -293,7 +295,9 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     const int keys = p.tree_mask ? rq.kv_len : shift + tok0 + x * tile_tokens + n;
     ntiles[x] = n > 0 ? cdiv(keys, kBN) : 0;
   }
-  const int n_tiles = max(ntiles[0], ntiles[1]);
+  const int n_tiles = max(ntiles[0], ntiles[1]), both = min(ntiles[0], ntiles[1]);
+  // number of the product of key tile j and query tile x
+  auto product = [&](int j, int x) { return j < both ? 2 * j + x : both + j; };
   auto sK = [&](int s) { return smem + kOffK + s * kTileBytes; };
   auto sV = [&](int s) { return smem + kOffV + s * kTileBytes; };
 
@@ -301,20 +305,50 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     tmem_alloc(&bar.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kQkWarp && lane == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bar.k_full[s], 32 * kUnpackWarps);
-      mbar_init(&bar.k_empty[s], 1);
-      mbar_init(&bar.v_full[s], 32 * kUnpackWarps);
-      mbar_init(&bar.v_empty[s], 1);
+  // Packed pages of key tile j into their ring, once its slot has been unpacked (all
+  // lanes of the loading warp call; lanes 0..7 copy a page each).
+  const int npages = cdiv(rq.kv_len, kPageSize);
+  const int32_t *table = p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq;
+  auto page_id = [&](int j) {
+    const int page = j * kPages + lane;
+    return lane < kPages && page < npages ? __ldg(table + page) : -1;
+  };
+  const uint64_t policy = l2_policy_evict_last();
+  auto load_raw = [&](int j, int id) -> bool {
+    const int s = j % kRaw;
+    if (j >= kRaw && !__all_sync(0xffffffffu, mbar_wait(&bar.raw_empty[s], (j / kRaw + 1) & 1))) return false;
+    const bool ok = id >= 0 && id < p.num_pages;
+    if (lane < kPages && j * kPages + lane < npages && !ok) atomicOr(&bar.bad, 1);
+    const unsigned good = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[s], __popc(good) * kInt4Block);
+    __syncwarp();
+    if (ok) {
+      bulk_load(smem + kOffRaw + (s * kPages + lane) * kInt4Block,
+                p.kv_cache + (static_cast<size_t>(id) * p.num_kv_heads + kvh) * kInt4Block, kInt4Block,
+                &bar.raw_full[s], policy);
     }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&bar.s_full[x], 1);
-      mbar_init(&bar.p_full[x], kBM);
-      mbar_init(&bar.pv_done[x], 1);
+    return true;
+  };
+  if (warp == kLoadWarp) {
+   if (lane == 0) {
+    for (int s = 0; s < kRaw; ++s) {
+      mbar_init(&bar.raw_full[s], 1);
+      mbar_init(&bar.raw_empty[s], kPages);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bar.kv_full[s], kPages);
+      mbar_init(&bar.kv_empty[s], 1);
+    }
+    for (int b = 0; b < kBuffers; ++b) {
+      mbar_init(&bar.s_full[b], 1);
+      mbar_init(&bar.p_full[b], kBM);
+      mbar_init(&bar.p_used[b], 1);
     }
     bar.bad = 0;
     fence_mbar_init();
+   }
+   __syncwarp();
+   for (int j = 0; j < min(kRaw, n_tiles); ++j) load_raw(j, page_id(j));      // fresh slots: no waits
   }
   // Q, its dims permuted as the codes' are; rows of nobody are zero
   for (int i = threadIdx.x; i < 2 * kBM * (kHeadDim / 8); i += kThreads) {
@@ -341,94 +375,74 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     set_registers<kOtherRegs, false>();
     const int uw = warp - kUnpackWarp;                 // this warp's page of every tile
     const int g = lane >> 2, t = lane & 3;
-    const int npages = cdiv(rq.kv_len, kPageSize);
-    const int32_t *table = p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq;
     uint32_t mask, sixteen;
     asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
     asm volatile("mov.b32 %0, 0x41804180;" : "=r"(sixteen));
-    auto page_id = [&](int j) { return 8 * j + uw < npages ? __ldg(table + 8 * j + uw) : 0; };
-    auto fetch = [&](int id, int j, Packed &f) {
-      if (id < 0 || id >= p.num_pages) {
-        id = 0;                                        // never dereferenced as it is
-        if (lane == 0) atomicOr(&bar.bad, 1);
-      }
-      const uint8_t *block = p.kv_cache + (static_cast<size_t>(id) * p.num_kv_heads + kvh) * kInt4Block;
-      f.k = __ldg(reinterpret_cast<const uint4 *>(block + kInt4K) + lane);
-      f.v = __ldg(reinterpret_cast<const uint4 *>(block + kInt4V) + lane);
-      f.km = __ldg(reinterpret_cast<const uint2 *>(block + kInt4Meta) + g);
-      f.vm = __ldg(reinterpret_cast<const uint4 *>(block + kInt4Meta) + t);
-      f.own = __ldg(reinterpret_cast<const uint32_t *>(block + kInt4Meta + 8 * (lane & 7) + 4 * ((lane >> 3) & 1)));
-    };
-    // Odd keys of the page: those past the last one become zeros, and a value that is not
-    // finite zeros with a key that is not finite.  Rare but for the last tile.
-    auto mend = [&](int j, Packed &f) {
-      const int key0 = (8 * j + uw) * kPageSize;
-      const unsigned odd = __ballot_sync(0xffffffffu, (f.own & 0x7f800000u) == 0x7f800000u) & 0xffffu;
-      const int live = rq.kv_len - key0;
-      if (odd == 0 && live >= kPageSize) return;
-      const unsigned gone = live >= kPageSize ? 0u : live <= 0 ? 0xffffu : 0xffffu & (0xffffu << live);
-      auto k = [&](uint32_t &m, int key) {
-        if (odd >> key & 1) m |= 0x7fc0u;
-        if (gone >> key & 1) m = 0;
-      };
-      auto v = [&](uint32_t &m, int key) {
-        if ((odd | gone) >> key & 1) m = 0;
-      };
-      k(f.km.x, g);
-      k(f.km.y, g + 8);
-      v(f.vm.x, 2 * t);
-      v(f.vm.y, 2 * t + 8);
-      v(f.vm.z, 2 * t + 1);
-      v(f.vm.w, 2 * t + 9);
-    };
-    // Stores of eight lanes fall into different banks: every other row has its second
-    // chunk first.
+    // Stores of eight lanes fall into different banks: every other row of K has its
+    // second chunk first.
     const int odd_row = g & 1;
-    const uint32_t k_at = 16 * uw * 128 + g * 128;     // row g of the page
-    const uint32_t k_first = (((t + 4 * odd_row) ^ g) << 4), k_second = (((t + 4 - 4 * odd_row) ^ g) << 4);
-    const uint32_t v_at = (16 * uw + 2 * t) * 128;     // row 2t
-    const uint32_t v_even = (g ^ (2 * t)) << 4, v_odd = 128 + ((g ^ (2 * t + 1)) << 4);
+    const uint32_t k_first = g * 128 + (((t + 4 * odd_row) ^ g) << 4), k_second = g * 128 + (((t + 4 - 4 * odd_row) ^ g) << 4);
+    const uint32_t v_even = 2 * t * 128 + ((g ^ (2 * t)) << 4), v_odd = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4);
 
     bool ok = true;
-    Packed f, next;
-    int id = page_id(1);
-    if (n_tiles > 0) fetch(page_id(0), 0, next);
     for (int j = 0; j < n_tiles; ++j) {
-      const int s = j % kStages;
-      f = next;
-      if (j + 1 < n_tiles) {                           // its latency runs under this tile's work
-        fetch(id, j + 1, next);
-        id = page_id(j + 2);
-      }
-      mend(j, f);
-      if (j >= kStages && !__all_sync(0xffffffffu, mbar_wait(&bar.k_empty[s], (j / kStages + 1) & 1))) {
+      const int s = j % kStages, raw = j % kRaw;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.raw_full[raw], (j / kRaw) & 1))) {
         ok = false;
         break;
       }
+      const uint8_t *block = smem + kOffRaw + (raw * kPages + uw) * kInt4Block;
+      const uint4 kw = *(reinterpret_cast<const uint4 *>(block + kInt4K) + lane);
+      const uint4 vw = *(reinterpret_cast<const uint4 *>(block + kInt4V) + lane);
+      uint2 km = *(reinterpret_cast<const uint2 *>(block + kInt4Meta) + g);      // keys g, g + 8
+      uint4 vm = *(reinterpret_cast<const uint4 *>(block + kInt4Meta) + t);      // keys 2t, 2t + 8, 2t + 1, 2t + 9
+      const uint32_t own = *reinterpret_cast<const uint32_t *>(block + kInt4Meta + 8 * (lane & 7) + 4 * ((lane >> 3) & 1));
+      // Odd keys of the page (`own` is that of lanes 0..15): those past the last one
+      // become zeros, and a value that is not finite zeros with a key that is not finite.
+      const unsigned odd = __ballot_sync(0xffffffffu, (own & 0x7f800000u) == 0x7f800000u) & 0xffffu;
+      const int live = rq.kv_len - j * kBN - uw * kPageSize;
+      if (odd != 0 || live < kPageSize) {
+        const unsigned gone = live >= kPageSize ? 0u : live <= 0 ? 0xffffu : 0xffffu & (0xffffu << live);
+        auto k = [&](uint32_t &m, int key) {
+          if (odd >> key & 1) m |= 0x7fc0u;
+          if (gone >> key & 1) m = 0;
+        };
+        auto v = [&](uint32_t &m, int key) {
+          if ((odd | gone) >> key & 1) m = 0;
+        };
+        k(km.x, g);
+        k(km.y, g + 8);
+        v(vm.x, 2 * t);
+        v(vm.y, 2 * t + 8);
+        v(vm.z, 2 * t + 1);
+        v(vm.w, 2 * t + 9);
+      }
+      if (j >= kStages && !__all_sync(0xffffffffu, mbar_wait(&bar.kv_empty[s], (j / kStages + 1) & 1))) {
+        ok = false;
+        break;
+      }
+      uint8_t *ka = sK(s) + uw * (kPageSize * 128), *va = sV(s) + uw * (kPageSize * 128);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t m = h ? f.km.y : f.km.x;
+      for (int h = 0; h < 2; ++h) {                    // keys g, g + 8
+        const uint32_t m = h ? km.y : km.x;
         const uint32_t s2 = pair_scale(m, false), z2 = pair_zero(m, false);
-        const uint32_t w0 = h ? f.k.z : f.k.x, w1 = h ? f.k.w : f.k.y;
-        uint8_t *row = sK(s) + k_at + h * 1024;
-        *reinterpret_cast<uint4 *>(row + k_first) = values(odd_row ? w1 : w0, s2, z2, mask, sixteen);
-        *reinterpret_cast<uint4 *>(row + k_second) = values(odd_row ? w0 : w1, s2, z2, mask, sixteen);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&bar.k_full[s]);
-      if (j >= kStages && !__all_sync(0xffffffffu, mbar_wait(&bar.v_empty[s], (j / kStages + 1) & 1))) {
-        ok = false;
-        break;
+        const uint32_t w0 = h ? kw.z : kw.x, w1 = h ? kw.w : kw.y;
+        *reinterpret_cast<uint4 *>(ka + h * 1024 + k_first) = values(odd_row ? w1 : w0, s2, z2, mask, sixteen);
+        *reinterpret_cast<uint4 *>(ka + h * 1024 + k_second) = values(odd_row ? w0 : w1, s2, z2, mask, sixteen);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {                    // keys 2t, 2t + 1, 2t + 8, 2t + 9
-        const uint32_t m = i == 0 ? f.vm.x : i == 1 ? f.vm.z : i == 2 ? f.vm.y : f.vm.w;
-        const uint32_t w = i == 0 ? f.v.x : i == 1 ? f.v.y : i == 2 ? f.v.z : f.v.w;
-        *reinterpret_cast<uint4 *>(sV(s) + v_at + (i >> 1) * 1024 + (i & 1 ? v_odd : v_even)) =
+        const uint32_t m = i == 0 ? vm.x : i == 1 ? vm.z : i == 2 ? vm.y : vm.w;
+        const uint32_t w = i == 0 ? vw.x : i == 1 ? vw.y : i == 2 ? vw.z : vw.w;
+        *reinterpret_cast<uint4 *>(va + (i >> 1) * 1024 + (i & 1 ? v_odd : v_even)) =
             values(__funnelshift_l(w, w, 3), pair_scale(m, true), pair_zero(m, true), mask, sixteen);
       }
       fence_proxy_async_smem();
-      mbar_arrive(&bar.v_full[s]);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.kv_full[s]);
+        mbar_arrive(&bar.raw_empty[raw]);
+      }
     }
     if (!ok && lane == 0) atomicOr(&bar.bad, 1);
   } else if (warp == kQkWarp) {
@@ -437,11 +451,12 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     bool ok = true;
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_full[s], (j / kStages) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / kStages) & 1));
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ok || j >= ntiles[x]) continue;
-        if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_full[x], (j - 1) & 1));
+        const int n = product(j, x), b = n % kBuffers;
+        if (n >= kBuffers) ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_used[b], (n / kBuffers + 1) & 1));
         if (!ok) continue;
         tc_fence_after();
         if (lane == 0) {
@@ -449,13 +464,11 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
           const uint64_t dk = umma_desc_sw128(smem_u32(sK(s)), 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < kHeadDim / 16; ++kk)
-            umma_ss(tmem + x * kColTile + kColS, dq + 2 * kk, dk + 2 * kk, kIdescQK, kk > 0);
-          umma_commit(&bar.s_full[x]);
+            umma_ss(tmem + b * kBN, dq + 2 * kk, dk + 2 * kk, kIdescQK, kk > 0);
+          umma_commit(&bar.s_full[b]);
         }
         __syncwarp();
       }
-      if (ok && lane == 0) umma_commit(&bar.k_empty[s]);
-      __syncwarp();
     }
     if (!ok && lane == 0) atomicOr(&bar.bad, 1);
   } else if (warp == kPvWarp) {
@@ -464,24 +477,25 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     bool ok = true;
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar.v_full[s], (j / kStages) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / kStages) & 1));
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ok || j >= ntiles[x]) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_full[x], j & 1));
+        const int n = product(j, x), b = n % kBuffers;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_full[b], (n / kBuffers) & 1));
         if (!ok) continue;
         tc_fence_after();
         if (lane == 0) {
           const uint64_t dv = umma_desc_sw128(smem_u32(sV(s)), kTileBytes, 1024);
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)        // 16 keys = 2 KB
-            umma_ts(tmem + x * kColTile + kColO, tmem + x * kColTile + kColP + 8 * kk, dv + (2048 >> 4) * kk,
-                    kIdescPV, (j > 0) || (kk > 0));
-          umma_commit(&bar.pv_done[x]);
+            umma_ts(tmem + kColO + x * kHeadDim, tmem + b * kBN + 8 * kk, dv + (2048 >> 4) * kk, kIdescPV,
+                    (j > 0) || (kk > 0));
+          umma_commit(&bar.p_used[b]);
         }
         __syncwarp();
       }
-      if (ok && lane == 0) umma_commit(&bar.v_empty[s]);
+      if (ok && lane == 0) umma_commit(&bar.kv_empty[s]);
       __syncwarp();
     }
     if (!ok && lane == 0) atomicOr(&bar.bad, 1);
@@ -490,7 +504,8 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     set_registers<kSoftmaxRegs, true>();
     const int x = warp >> 2;
     const int r = threadIdx.x & (kBM - 1);             // row = tensor-memory lane
-    const uint32_t trow = tmem + x * kColTile + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t to = trow + kColO + x * kHeadDim;
     const int i = tok0 + x * tile_tokens + r / p.group;       // token within the request
     const int head = kvh * p.group + r % p.group;
     const bool live = r < rows[x];
@@ -517,35 +532,49 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     bool ok = true;
     const int mine = ntiles[x];
     for (int j = 0; j < mine; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[x], j & 1))) { ok = false; break; }
+      const int n = product(j, x), b = n % kBuffers;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[b], (n / kBuffers) & 1))) { ok = false; break; }
       tc_fence_after();
       const int key0 = j * kBN;
-      const int parity = j > 0 ? (j - 1) & 1 : -1;
+      const uint32_t ts = trow + b * kBN;
       const bool edge = __any_sync(0xffffffffu, key0 + kBN > seen.limit);
-      float sum = edge ? weigh_tile<true>(trow, sl2, m, seen, key0, &bar.pv_done[x], parity)
-                       : weigh_tile<false>(trow, sl2, m, seen, key0, &bar.pv_done[x], parity);
-      if (__any_sync(0xffffffffu, sum < 0.f)) { ok = false; break; }
+      uint32_t y[4][16];
+      float sum = edge ? weigh_tile<true>(ts, sl2, m, seen, key0, y) : weigh_tile<false>(ts, sl2, m, seen, key0, y);
       if (__any_sync(0xffffffffu, !(sum <= kMostSum))) {
         // some reference is too small: the rows' maxima, and the tile again
-        const float mx = row_max(trow, sl2, seen, key0);
+        const float mx = row_max(ts, sl2, seen, key0);
         const float now = fmaxf(m, mx);
         const float alpha = ex2(m - now);
         m = now;
         d *= alpha;
-        if (j > 0) scale_o(trow, alpha);
-        sum = weigh_tile<true>(trow, sl2, m, seen, key0, &bar.pv_done[x], -1);
+        if (j > 0) {
+          const int before = product(j - 1, x);
+          if (!__all_sync(0xffffffffu, mbar_wait(&bar.p_used[before % kBuffers], (before / kBuffers) & 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          scale_o(to, alpha);
+        }
+        sum = weigh_tile<true>(ts, sl2, m, seen, key0, y);
       }
       d += sum;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_st16(ts + 16 * c, y[c]);
+      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bar.p_full[x]);
+      mbar_arrive(&bar.p_full[b]);
     }
-    if (mine > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&bar.pv_done[x], (mine - 1) & 1));
+    if (mine > 0 && ok) {
+      const int last = product(mine - 1, x);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_used[last % kBuffers], (last / kBuffers) & 1));
+    }
     tc_fence_after();
     if (!ok) atomicOr(&bar.bad, 1);
     uint32_t o[2][32];
     if (mine > 0 && ok) {
-      tmem_ld32(trow + kColO, o[0]);
-      tmem_ld32(trow + kColO + 32, o[1]);
+      tmem_ld32(to, o[0]);
+      tmem_ld32(to + 32, o[1]);
       tmem_ld_wait32(o[0]);
       reg_tie32(o[1]);
     }
@@ -570,7 +599,17 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     }
     return;
   } else {
-    set_registers<kOtherRegs, false>();                // the rest of the last warpgroup
+    set_registers<kOtherRegs, false>();                // the last warpgroup's other two warps
+    if (warp == kLoadWarp) {
+      bool ok = true;
+      int id = page_id(kRaw);
+      for (int j = kRaw; ok && j < n_tiles; ++j) {
+        const int next = page_id(j + 1);
+        ok = load_raw(j, id);
+        id = next;
+      }
+      if (!ok && lane == 0) atomicOr(&bar.bad, 1);
+    }
   }
   tc_fence_before();
   __syncthreads();          // the softmax warps have read O: tensor memory is free
