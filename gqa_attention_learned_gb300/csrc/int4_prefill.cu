@@ -43,7 +43,7 @@ constexpr int kTileBytes = kBN * kHeadDim * 2; // 16 KB
 constexpr int kThreads = 640;                  // five warpgroups
 constexpr int kUnpackWarp = 8, kUnpackWarps = kPages, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 18;
 // Registers per thread: the launch has 96 for all; softmax warps take from the others.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 152, kOtherRegs = 56;
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 168, kOtherRegs = 48;
 static_assert(2 * kSoftmaxRegs + 3 * kOtherRegs <= 5 * kLaunchRegs, "the split fits the launch's registers");
 constexpr int kBuffers = 3;                    // of scores in tensor memory
 constexpr uint32_t kTmemCols = 512;
@@ -215,6 +215,24 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t m, bool v) {
   return ((__byte_perm(m, 0, v ? 0x3232 : 0x1010) << 3) & 0x00780078u) | 0x41804180u;
 }
 
+// mbar_wait that sleeps: most warps wait here for a good part of the time, and what a
+// polling one issues is taken from those that work.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
+  constexpr uint32_t kNap = 100000;                    // ns that one attempt may take
+  for (uint64_t i = 0; i <= kWaitLimitNs / kNap; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kNap)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+
 // Copies `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
                                           uint64_t policy) {
@@ -316,7 +334,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
   const uint64_t policy = l2_policy_evict_last();
   auto load_raw = [&](int j, int id) -> bool {
     const int s = j % kRaw;
-    if (j >= kRaw && !__all_sync(0xffffffffu, mbar_wait(&bar.raw_empty[s], (j / kRaw + 1) & 1))) return false;
+    if (j >= kRaw && !__all_sync(0xffffffffu, wait(&bar.raw_empty[s], (j / kRaw + 1) & 1))) return false;
     const bool ok = id >= 0 && id < p.num_pages;
     if (lane < kPages && j * kPages + lane < npages && !ok) atomicOr(&bar.bad, 1);
     const unsigned good = __ballot_sync(0xffffffffu, ok);
@@ -387,7 +405,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     bool ok = true;
     for (int j = 0; j < n_tiles; ++j) {
       const int s = j % kStages, raw = j % kRaw;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.raw_full[raw], (j / kRaw) & 1))) {
+      if (!__all_sync(0xffffffffu, wait(&bar.raw_full[raw], (j / kRaw) & 1))) {
         ok = false;
         break;
       }
@@ -417,7 +435,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
         v(vm.z, 2 * t + 1);
         v(vm.w, 2 * t + 9);
       }
-      if (j >= kStages && !__all_sync(0xffffffffu, mbar_wait(&bar.kv_empty[s], (j / kStages + 1) & 1))) {
+      if (j >= kStages && !__all_sync(0xffffffffu, wait(&bar.kv_empty[s], (j / kStages + 1) & 1))) {
         ok = false;
         break;
       }
@@ -451,12 +469,12 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     bool ok = true;
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / kStages) & 1));
+      ok = __all_sync(0xffffffffu, wait(&bar.kv_full[s], (j / kStages) & 1));
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ok || j >= ntiles[x]) continue;
         const int n = product(j, x), b = n % kBuffers;
-        if (n >= kBuffers) ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_used[b], (n / kBuffers + 1) & 1));
+        if (n >= kBuffers) ok = __all_sync(0xffffffffu, wait(&bar.p_used[b], (n / kBuffers + 1) & 1));
         if (!ok) continue;
         tc_fence_after();
         if (lane == 0) {
@@ -477,12 +495,12 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     bool ok = true;
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kStages;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / kStages) & 1));
+      ok = __all_sync(0xffffffffu, wait(&bar.kv_full[s], (j / kStages) & 1));
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ok || j >= ntiles[x]) continue;
         const int n = product(j, x), b = n % kBuffers;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_full[b], (n / kBuffers) & 1));
+        ok = __all_sync(0xffffffffu, wait(&bar.p_full[b], (n / kBuffers) & 1));
         if (!ok) continue;
         tc_fence_after();
         if (lane == 0) {
@@ -533,7 +551,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     const int mine = ntiles[x];
     for (int j = 0; j < mine; ++j) {
       const int n = product(j, x), b = n % kBuffers;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar.s_full[b], (n / kBuffers) & 1))) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, wait(&bar.s_full[b], (n / kBuffers) & 1))) { ok = false; break; }
       tc_fence_after();
       const int key0 = j * kBN;
       const uint32_t ts = trow + b * kBN;
@@ -549,7 +567,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
         d *= alpha;
         if (j > 0) {
           const int before = product(j - 1, x);
-          if (!__all_sync(0xffffffffu, mbar_wait(&bar.p_used[before % kBuffers], (before / kBuffers) & 1))) {
+          if (!__all_sync(0xffffffffu, wait(&bar.p_used[before % kBuffers], (before / kBuffers) & 1))) {
             ok = false;
             break;
           }
@@ -567,7 +585,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     }
     if (mine > 0 && ok) {
       const int last = product(mine - 1, x);
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_used[last % kBuffers], (last / kBuffers) & 1));
+      ok = __all_sync(0xffffffffu, wait(&bar.p_used[last % kBuffers], (last / kBuffers) & 1));
     }
     tc_fence_after();
     if (!ok) atomicOr(&bar.bad, 1);
