@@ -15,7 +15,7 @@ namespace {
 using sa::kHeadDim;
 using sa::kPageSize;
 
-constexpr int kMinPages = 4;            // pages that a warp takes at least: fewer cost more to join than they save
+constexpr int kMinPages = 8;            // pages that a warp takes at least: fewer cost more to join than they save
 
 constexpr int kFewRows = 32;            // query rows per KV head up to which the kernel of few rows is taken
 

@@ -41,6 +41,9 @@ constexpr int kNW = 8;                        // warps per CTA
 constexpr int kThreads = kNW * 32;
 constexpr int kStepPages = 4;                 // pages per stage
 constexpr int kStageBytes = kStepPages * kInt4Block;
+// A unit's share of the work beyond its pages, in pages: reading its queries, the first
+// maximum, the end.  (64 requests of 1..4096 tokens, us: 36.1 at 0, see below.)
+constexpr int kUnitCost = 8;
 constexpr float kRaise = 8.f;                 // log2 by which a score may exceed the reference
 constexpr float kUnset = -8e37f;              // reference of a row that has seen no key yet
 
@@ -73,11 +76,11 @@ struct __align__(128) Shared {
   long long prefix[kThreads + 1];
   long long scan[kNW];
   struct {                                    // the unit of a part; pages 0: there is none
-    long long from;                           // its first page's number
+    long long from;                           // the number of its first page
     Request r;
     int pages, kvh, rb;
   } unit[2][kNW];
-  int last;
+  int last[2];
   // 0: a unit begun before the warp's share; 1: one that goes on after it (in the
   // ring, which is idle by then)
   __device__ __forceinline__ Part<NB> &part(int slot, int warp) {
@@ -239,7 +242,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   long long mine = 0;
   for (int b = threadIdx.x * per; b < min(p.num_seqs, static_cast<int>(threadIdx.x + 1) * per); ++b) {
     const Request r = request<NB, kMode>(p, b);
-    mine += static_cast<long long>(r.pages) * r.units;
+    mine += static_cast<long long>(r.pages + kUnitCost) * r.units;
   }
   long long upto = mine;
 #pragma unroll
@@ -284,19 +287,22 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
     long long here = sh.prefix[n - 1];
     while (true) {
       at.r = request<NB, kMode>(p, at.b);
-      const long long w = static_cast<long long>(at.r.pages) * at.r.units;
+      const long long w = static_cast<long long>(at.r.pages + kUnitCost) * at.r.units;
       if (here + w > from) break;
       here += w;
       ++at.b;
     }
-    at.unit = static_cast<int>(quotient(from - here, at.r.pages));
-    at.page = static_cast<int>((from - here) - static_cast<long long>(at.unit) * at.r.pages);
+    const int each = at.r.pages + kUnitCost;           // a unit's cost comes before its pages
+    at.unit = static_cast<int>(quotient(from - here, each));
+    at.page = static_cast<int>((from - here) - static_cast<long long>(at.unit) * each) - kUnitCost;
   }
-  const int share_pages = static_cast<int>(to - from);
+  // this warp's pages and the costs of the units that begin among them
+  const int share_left = max(0, static_cast<int>(to - from) + min(at.page, 0));
+  at.page = max(at.page, 0);
 
   // ---- copies: `to_come` runs ahead of `at` by up to kStages steps
   At to_come = at;
-  int unissued = share_pages;
+  int unissued = share_left;
   int ids = -1, ids_next = -1, ids_at = 0;             // lane j: id of page ids_at + j; of the next 32
   auto load_ids = [&](int first) -> int {
     const int page = first + lane;
@@ -308,7 +314,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
     ids = load_ids(ids_at);
     ids_next = ids_at + 32 < to_come.r.pages ? load_ids(ids_at + 32) : -1;
   };
-  if (share_pages > 0) start_ids();
+  if (share_left > 0) start_ids();
 
   // Up to here only lengths and the page table were read; everything below may
   // depend on the previous kernel on the stream.
@@ -343,9 +349,12 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
     unissued -= n;
     to_come.page += n;
     if (to_come.page >= to_come.r.pages && unissued > 0) {
-      to_come.next_unit(p);
-      src = p.kv_cache + static_cast<size_t>(kv_head(p, to_come)) * kInt4Block;
-      start_ids();
+      unissued = max(unissued - kUnitCost, 0);
+      if (unissued > 0) {
+        to_come.next_unit(p);
+        src = p.kv_cache + static_cast<size_t>(kv_head(p, to_come)) * kInt4Block;
+        start_ids();
+      }
     }
   };
   int issued = 0, done = 0;                            // steps
@@ -353,7 +362,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
 
   // ---- units of this share, one after another
   bool dead = false;                                   // a copy never landed
-  int left = share_pages;
+  int left = share_left;
   while (left > 0) {
     const int kvh = kv_head(p, at), rb = row_block(p, at);
     const int first_page = at.page;
@@ -584,8 +593,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
       u.kvh = kvh;
       u.rb = rb;
     }
-    left -= seg;
-    at.page = seg_end;
+    left = max(left - seg - kUnitCost, 0);
     if (left > 0) at.next_unit(p);
   }
 
@@ -593,62 +601,94 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   // that begins it, slot 0 of the others.
   __syncthreads();
   const long long cta_from = blockIdx.x * cta_share, cta_to = min(total, cta_from + cta_share);
-  for (int round = 0; round < kNW + 1; ++round) {      // round 0: the unit begun before the CTA; 1 + w: by warp w
-    const int w0 = max(round - 1, 0), s0 = round == 0 ? 0 : 1;
-    const auto &u = sh.unit[s0][w0];
-    if (u.pages == 0) continue;                        // uniform over the CTA
-    const long long u_from = u.from, u_to = u_from + u.pages;
-    int w1 = w0 + 1;                                   // its parts: (s0, w0), (0, w0 + 1 ..)
+  constexpr int kQuads = kHeadDim / 4, kItems = kRows * kQuads;
+  // 4 elements of a row over the warps that have parts of the unit which warp w0 has in
+  // slot s0
+  auto join_warps = [&](int s0, int w0, long long u_to, int item, float &mx, float &den) -> float4 {
+    const int row = item / kQuads, dq = item % kQuads * 4;
+    int w1 = w0 + 1;
     while (w1 < kNW && cta_from + w1 * share < min(u_to, total)) ++w1;
-    const int kvh = u.kvh, rb = u.rb;
-    const bool whole = u_from >= cta_from && u_to <= cta_to;
-
-    constexpr int kItems = kRows * (kHeadDim / 4);
-    const size_t mine_at = static_cast<size_t>(blockIdx.x) * 2 + (u_from >= cta_from ? 1 : 0);
-    for (int item = threadIdx.x; item < kItems; item += kThreads) {
-      const int r = item / (kHeadDim / 4), dq = (item % (kHeadDim / 4)) * 4;
-      float mx = sh.part(s0, w0).m[r];
-      for (int w = w0 + 1; w < w1; ++w) mx = fmaxf(mx, sh.part(0, w).m[r]);
-      float den = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = w0; w < w1; ++w) {
-        const Part<NB> &x = sh.part(w == w0 ? s0 : 0, w);
-        const float wt = ex2(x.m[r] - mx);
-        den += wt * x.d[r];
-        const float4 v = *reinterpret_cast<const float4 *>(&x.o[r][dq]);
-        a.x += wt * v.x;
-        a.y += wt * v.y;
-        a.z += wt * v.z;
-        a.w += wt * v.w;
-      }
-      if (whole) {
-        int token, head;
-        const long long row = row_of<NB, kMode>(p, u.r, kvh, rb, r, token, head);
-        if (row >= 0) write_row(p, row, dq, a, mx, den);
-      } else {
-        *reinterpret_cast<float4 *>(p.ws_o + (mine_at * kRows + r) * kHeadDim + dq) = a;
-        if (dq == 0) p.ws_md[mine_at * kRows + r] = make_float2(mx, den);
-      }
+    mx = sh.part(s0, w0).m[row];
+    for (int w = w0 + 1; w < w1; ++w) mx = fmaxf(mx, sh.part(0, w).m[row]);
+    den = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = w0; w < w1; ++w) {
+      const Part<NB> &x = sh.part(w == w0 ? s0 : 0, w);
+      const float wt = ex2(x.m[row] - mx);
+      den += wt * x.d[row];
+      const float4 v = *reinterpret_cast<const float4 *>(&x.o[row][dq]);
+      a.x += wt * v.x;
+      a.y += wt * v.y;
+      a.z += wt * v.z;
+      a.w += wt * v.w;
     }
-    if (whole) continue;
+    return a;
+  };
+  auto write = [&](const auto &u, int item, float4 a, float mx, float den) {
+    int token, head;
+    const long long row = row_of<NB, kMode>(p, u.r, u.kvh, u.rb, item / kQuads, token, head);
+    if (row >= 0) write_row(p, row, item % kQuads * 4, a, mx, den);
+  };
 
-    // the last of the CTAs that share the unit joins their parts, in page order, and
-    // leaves the counter at zero for the next call
-    const int c0 = static_cast<int>(quotient(u_from, cta_share));
-    const int c1 = static_cast<int>(quotient(u_to - 1, cta_share));
-    __syncthreads();
-    if (threadIdx.x == 0) sh.last = atomic_add_acq_rel(&p.counters[c0], 1) == c1 - c0;
-    __syncthreads();
-    if (!sh.last) continue;
+  // units inside the CTA: each by the warp that has its first part
+  {
+    const auto &u = sh.unit[1][warp];
+    if (u.pages > 0 && u.from + u.pages <= cta_to)
+      for (int item = lane; item < kItems; item += 32) {
+        float mx, den;
+        const float4 a = join_warps(1, warp, u.from + u.pages, item, mx, den);
+        write(u, item, a, mx, den);
+      }
+  }
+  // and by the whole CTA the unit that began before it (0) and the one that goes on
+  // after it (1): its part to the workspace.  The last of the CTAs that share a unit
+  // joins their parts, in page order, and leaves the counter at zero for the next call.
+  int shared_by[2], first_cta[2], from_warp[2];        // CTAs that share it (1: no such unit)
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    shared_by[k] = 1;
+    from_warp[k] = 0;
+    if (k == 1) {
+      int w = kNW - 1;                                 // the last warp with a unit of its own beginning
+      while (w >= 0 && !(sh.unit[1][w].pages > 0 && sh.unit[1][w].from + sh.unit[1][w].pages > cta_to)) --w;
+      if (w < 0) continue;
+      from_warp[k] = w;
+    } else if (sh.unit[0][0].pages == 0) {
+      continue;
+    }
+    const auto &u = sh.unit[k][from_warp[k]];
+    first_cta[k] = static_cast<int>(quotient(u.from, cta_share));
+    shared_by[k] = static_cast<int>(quotient(u.from + u.pages - 1, cta_share)) - first_cta[k] + 1;
+    const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + k) * kRows;
     for (int item = threadIdx.x; item < kItems; item += kThreads) {
-      const int r = item / (kHeadDim / 4), dq = (item % (kHeadDim / 4)) * 4;
-      auto index = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRows + r; };
+      float mx, den;
+      const float4 a = join_warps(k, from_warp[k], u.from + u.pages, item, mx, den);
+      *reinterpret_cast<float4 *>(p.ws_o + (at + item / kQuads) * kHeadDim + item % kQuads * 4) = a;
+      if (item % kQuads == 0) p.ws_md[at + item / kQuads] = make_float2(mx, den);
+    }
+  }
+  if (shared_by[0] == 1 && shared_by[1] == 1) return;  // uniform over the CTA
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    const int k = threadIdx.x;
+    sh.last[k] = shared_by[k] > 1 && atomic_add_acq_rel(&p.counters[first_cta[k]], 1) == shared_by[k] - 1;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!sh.last[k]) continue;
+    const auto &u = sh.unit[k][from_warp[k]];
+    const int c0 = first_cta[k], c1 = c0 + shared_by[k];
+    for (int item = threadIdx.x; item < kItems; item += kThreads) {
+      const int row = item / kQuads, dq = item % kQuads * 4;
+      auto index = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRows + row; };
       float mx = -INFINITY;
-      for (int c = c0; c <= c1; ++c) mx = fmaxf(mx, __ldcg(&p.ws_md[index(c)]).x);
+#pragma unroll 4
+      for (int c = c0; c < c1; ++c) mx = fmaxf(mx, __ldcg(&p.ws_md[index(c)]).x);
       float den = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
+      for (int c = c0; c < c1; ++c) {
         const float2 md = __ldcg(&p.ws_md[index(c)]);
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + index(c) * kHeadDim + dq));
         const float wt = ex2(md.x - mx);
@@ -658,12 +698,9 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
         a.z += wt * v.z;
         a.w += wt * v.w;
       }
-      int token, head;
-      const long long row = row_of<NB, kMode>(p, u.r, kvh, rb, r, token, head);
-      if (row >= 0) write_row(p, row, dq, a, mx, den);
+      write(u, item, a, mx, den);
     }
     if (threadIdx.x == 0) p.counters[c0] = 0;
-    __syncthreads();                                   // sh.last has been read
   }
 }
 
