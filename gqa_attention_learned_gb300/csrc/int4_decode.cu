@@ -603,24 +603,39 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   const long long cta_from = blockIdx.x * cta_share, cta_to = min(total, cta_from + cta_share);
   constexpr int kQuads = kHeadDim / 4, kItems = kRows * kQuads;
   // 4 elements of a row over the warps that have parts of the unit which warp w0 has in
-  // slot s0
-  auto join_warps = [&](int s0, int w0, long long u_to, int item, float &mx, float &den) -> float4 {
-    const int row = item / kQuads, dq = item % kQuads * 4;
+  // slot s0, up to warp w1.  All loads at once: the others' are taken from w0, for nothing.
+  auto last_warp = [&](int w0, long long u_to) {
     int w1 = w0 + 1;
     while (w1 < kNW && cta_from + w1 * share < min(u_to, total)) ++w1;
-    mx = sh.part(s0, w0).m[row];
-    for (int w = w0 + 1; w < w1; ++w) mx = fmaxf(mx, sh.part(0, w).m[row]);
+    return w1;
+  };
+  auto join_warps = [&](int s0, int w0, int w1, int item, float &mx, float &den) -> float4 {
+    const int row = item / kQuads, dq = item % kQuads * 4;
+    float wt[kNW];
+    mx = kUnset;
+#pragma unroll
+    for (int w = 0; w < kNW; ++w) {
+      const bool in = w >= w0 && w < w1;
+      const float m = (in && w != w0 ? sh.part(0, w) : sh.part(s0, w0)).m[row];
+      wt[w] = in ? m : -INFINITY;
+      mx = fmaxf(mx, m);
+    }
     den = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = w0; w < w1; ++w) {
-      const Part<NB> &x = sh.part(w == w0 ? s0 : 0, w);
-      const float wt = ex2(x.m[row] - mx);
-      den += wt * x.d[row];
+#pragma unroll
+    for (int w = 0; w < kNW; ++w) {
+      const bool in = w >= w0 && w < w1;
+      const Part<NB> &x = in && w != w0 ? sh.part(0, w) : sh.part(s0, w0);
+      const float d = x.d[row];
       const float4 v = *reinterpret_cast<const float4 *>(&x.o[row][dq]);
-      a.x += wt * v.x;
-      a.y += wt * v.y;
-      a.z += wt * v.z;
-      a.w += wt * v.w;
+      const float e = ex2(wt[w] - mx);
+      if (in) {
+        den += e * d;
+        a.x += e * v.x;
+        a.y += e * v.y;
+        a.z += e * v.z;
+        a.w += e * v.w;
+      }
     }
     return a;
   };
@@ -633,12 +648,15 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   // units inside the CTA: each by the warp that has its first part
   {
     const auto &u = sh.unit[1][warp];
-    if (u.pages > 0 && u.from + u.pages <= cta_to)
+    if (u.pages > 0 && u.from + u.pages <= cta_to) {
+      const int w1 = last_warp(warp, u.from + u.pages);
+#pragma unroll 2
       for (int item = lane; item < kItems; item += 32) {
         float mx, den;
-        const float4 a = join_warps(1, warp, u.from + u.pages, item, mx, den);
+        const float4 a = join_warps(1, warp, w1, item, mx, den);
         write(u, item, a, mx, den);
       }
+    }
   }
   // and by the whole CTA the unit that began before it (0) and the one that goes on
   // after it (1): its part to the workspace.  The last of the CTAs that share a unit
@@ -660,9 +678,10 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
     first_cta[k] = static_cast<int>(quotient(u.from, cta_share));
     shared_by[k] = static_cast<int>(quotient(u.from + u.pages - 1, cta_share)) - first_cta[k] + 1;
     const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + k) * kRows;
+    const int w1 = last_warp(from_warp[k], u.from + u.pages);
     for (int item = threadIdx.x; item < kItems; item += kThreads) {
       float mx, den;
-      const float4 a = join_warps(k, from_warp[k], u.from + u.pages, item, mx, den);
+      const float4 a = join_warps(k, from_warp[k], w1, item, mx, den);
       *reinterpret_cast<float4 *>(p.ws_o + (at + item / kQuads) * kHeadDim + item % kQuads * 4) = a;
       if (item % kQuads == 0) p.ws_md[at + item / kQuads] = make_float2(mx, den);
     }
