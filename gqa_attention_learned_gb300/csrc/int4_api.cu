@@ -17,7 +17,7 @@ using sa::kPageSize;
 
 constexpr int kMinPages = 8;            // pages that a warp takes at least: fewer cost more to join than they save
 
-constexpr int kFewRows = 32;            // query rows per KV head up to which the kernel of few rows is taken
+constexpr int kFewRows = 64;            // query rows per KV head up to which the kernel of few rows is taken
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
