@@ -11,18 +11,31 @@
 // head), as two 128-row tiles that share every K and V tile of 128 keys: turning a tile
 // of codes into bf16 costs half of what it would for one, and one tile's products run
 // during the other's softmax.
-//   warps 8..15   packed pages from global memory into registers, a tile ahead; codes
-//                 to bf16 (shift, mask under the exponent of 16, subtract 16 + z,
-//                 multiply by s); stores into K and V rings in the swizzled layout.
-//                 A word of codes gives dims (0 4 1 5 2 6 3 7) of a group of eight in
-//                 that order: Q is permuted likewise, O's columns are put right at the end.
-//   warp 16       S = Q K^T for either tile as soon as its last S has been used
-//   warp 17       O += P V for either tile
 //   warps 0..7    softmax, one thread per row.  Scores come 32 at a time and are not
 //                 compared: P = 2^(s - m) with the row's reference m, and only if a
 //                 tile's sum shows that m has become too small (or is not set) the
 //                 row's maximum is taken and the tile done once more.  Scores beyond
 //                 the causal limit are left out by index.
+//   warps 8..15   a page of every key tile each: codes to bf16 (shift, mask under the
+//                 exponent of 16, subtract 16 + z, multiply by s), stores into the K and
+//                 V rings in the swizzled layout.  A word of codes gives dims (0 4 1 5 2
+//                 6 3 7) of a group of eight in that order: Q is permuted likewise, O's
+//                 columns are put right at the end.
+//   warp 16       S = Q K^T into one of three score buffers of tensor memory as soon as
+//                 its last P has been used
+//   warp 17       O += P V, P in place of its scores
+//   warp 18       packed pages into a ring of four key tiles, by bulk copies
+//
+// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1481 us, 928 TFLOP/s,
+// where the kernel of the bf16 cache does 1046): the chain score - exponentials - P V of
+// the two tiles in turn.  The tensor pipe is busy for half of it, P V of 128 x 64 x 128
+// from tensor memory taking about twice its arithmetic's time.  Measured on the way: one
+// tile per CTA 1839 us; four unpacking warps 1700; two score buffers 1692; packed pages
+// straight into registers, a tile ahead, 1600; softmax warps with 128 registers 1555.
+// Slower or no better: 16 softmax warps with half a row each; products started by one
+// thread that walks the tiles alone (1558 us); persistent CTAs (1720: spills); four
+// stages of K and V.
+//
 // A value row that is not finite must spoil the rows that see it and no others, but
 // 0 * NaN in P V would spoil the whole tile: such a value is stored as zero and its key
 // as NaN, so the rows that see it get there by their score (and their lse is NaN, too).
@@ -215,8 +228,10 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t m, bool v) {
   return ((__byte_perm(m, 0, v ? 0x3232 : 0x1010) << 3) & 0x00780078u) | 0x41804180u;
 }
 
-// mbar_wait that sleeps: most warps wait here for a good part of the time, and what a
-// polling one issues is taken from those that work.
+// mbar_wait that sleeps: most warps wait for a good part of the time, and what a polling
+// one issues is taken from those that work (1555 us polling for 4 x 2048 tokens on up to
+// 14336 keys, 1537 sleeping).  The two warps that start the products poll: their waits
+// are on the chain (1481).
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
   constexpr uint32_t kNap = 100000;                    // ns that one attempt may take
   for (uint64_t i = 0; i <= kWaitLimitNs / kNap; ++i) {
@@ -467,14 +482,15 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     // ------------------------------------------------------------------ Q K^T
     set_registers<kOtherRegs, false>();
     bool ok = true;
+    int made = 0;                                      // products
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kStages;
-      ok = __all_sync(0xffffffffu, wait(&bar.kv_full[s], (j / kStages) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.kv_full[s], (j / kStages) & 1));
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ok || j >= ntiles[x]) continue;
         const int n = product(j, x), b = n % kBuffers;
-        if (n >= kBuffers) ok = __all_sync(0xffffffffu, wait(&bar.p_used[b], (n / kBuffers + 1) & 1));
+        if (n >= kBuffers) ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_used[b], (n / kBuffers + 1) & 1));
         if (!ok) continue;
         tc_fence_after();
         if (lane == 0) {
@@ -485,22 +501,27 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
             umma_ss(tmem + b * kBN, dq + 2 * kk, dk + 2 * kk, kIdescQK, kk > 0);
           umma_commit(&bar.s_full[b]);
         }
+        made = n + 1;
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) atomicOr(&bar.bad, 1);
+    if (!ok) {
+      if (lane == 0) atomicOr(&bar.bad, 1);
+      if (made > 0) mbar_wait(&bar.s_full[(made - 1) % kBuffers], ((made - 1) / kBuffers) & 1);
+    }
   } else if (warp == kPvWarp) {
     // -------------------------------------------------------------------- P V
+    // (its V is there when P is: S was made after K and V of the key tile had come)
     set_registers<kOtherRegs, false>();
     bool ok = true;
+    int made = 0;
     for (int j = 0; ok && j < n_tiles; ++j) {
       const int s = j % kStages;
-      ok = __all_sync(0xffffffffu, wait(&bar.kv_full[s], (j / kStages) & 1));
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (!ok || j >= ntiles[x]) continue;
         const int n = product(j, x), b = n % kBuffers;
-        ok = __all_sync(0xffffffffu, wait(&bar.p_full[b], (n / kBuffers) & 1));
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar.p_full[b], (n / kBuffers) & 1));
         if (!ok) continue;
         tc_fence_after();
         if (lane == 0) {
@@ -511,12 +532,16 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
                     (j > 0) || (kk > 0));
           umma_commit(&bar.p_used[b]);
         }
+        made = n + 1;
         __syncwarp();
       }
       if (ok && lane == 0) umma_commit(&bar.kv_empty[s]);
       __syncwarp();
     }
-    if (!ok && lane == 0) atomicOr(&bar.bad, 1);
+    if (!ok) {
+      if (lane == 0) atomicOr(&bar.bad, 1);
+      if (made > 0) mbar_wait(&bar.p_used[(made - 1) % kBuffers], ((made - 1) / kBuffers) & 1);
+    }
   } else if (warp < kUnpackWarp) {
     // ---------------------------------------------------------------- softmax
     set_registers<kSoftmaxRegs, true>();
@@ -620,13 +645,16 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     set_registers<kOtherRegs, false>();                // the last warpgroup's other two warps
     if (warp == kLoadWarp) {
       bool ok = true;
-      int id = page_id(kRaw);
+      int id = page_id(kRaw), asked = min(kRaw, n_tiles);
       for (int j = kRaw; ok && j < n_tiles; ++j) {
         const int next = page_id(j + 1);
         ok = load_raw(j, id);
+        if (ok) asked = j + 1;
         id = next;
       }
       if (!ok && lane == 0) atomicOr(&bar.bad, 1);
+      // no copy is in flight when the CTA ends, whoever gave up
+      for (int j = max(asked - kRaw, 0); j < asked; ++j) wait(&bar.raw_full[j % kRaw], (j / kRaw) & 1);
     }
   }
   tc_fence_before();
