@@ -1,31 +1,40 @@
 // Attention of few query rows per KV head over a cache held in 4 bits: one token per
 // request, the draft tokens of a verification, or the last few of ragged requests.
 //
-// Mathematics.  Keys are k_j = s_j (n_j - z_j), n_j in 0..15.  The codes go into the
-// products as they are, as bf16 numbers 16 + n (4 bits below a set exponent):
+// Mathematics.  Keys are k_j = s_j (n_j - z_j), n_j in 0..15.  A code under the exponent
+// of 16 is the bf16 number 16 + n.  K's codes go into the product as that, V's less 16 + z
+// (a bf16 subtraction, exact):
 //     scale q.k_j   = (scale s_j) (q.(16 + n_j) - (16 + z_j) sum q)
-//     sum_j p_j v_j = sum_j (p_j s_j) (16 + n_j) - sum_j (p_j s_j) (16 + z_j)
-// Scales and zero points so cost a few operations per (key, head) instead of one per
-// element, both subtractions are exact up to fp32 sums, and p_j s_j is rounded to
-// bf16 once, the correction using the rounded value.
+//     sum_j p_j v_j = sum_j (p_j s_j) (n_j - z_j)
+// Scales, and zero points of K, so cost a few operations per (key, head) instead of one
+// per element; p_j s_j is rounded to bf16 once.  Zero points of V stay out of the sums:
+// tensor cores cut what they add to a running sum, and 16 + n would give that a sign.
 //
-// What bounds it: 1088 bytes per page and KV head against the instructions that turn
-// them into fragments.  At the copy bandwidth an SM gets 23 bytes a cycle, a page every
-// 47 cycles: 188 issue slots on its four schedulers.  A word of eight codes becomes
-// four registers by three shifts and four logical operations (V: pairs of keys are put
-// together first), and S^T[16 keys x 8 rows] and O^T[64 x 8] take four mma.sync each.
+// What bounds it: the instructions that turn 1088 bytes per page and KV head into
+// fragments.  At the copy bandwidth an SM gets 23 bytes a cycle, a page every 47 cycles,
+// or 188 issue slots and 94 of the integer pipe.  A page takes 185 instructions, 97 of
+// them integer or logical: a word of eight codes becomes four registers by three shifts
+// and four logical operations (V: pairs of keys are put together first, four more
+// subtractions), and S^T[16 keys x 8 rows] and O^T[64 x 8] take four mma.sync each.  So
+// 8 requests of up to 131072 keys run at 3.7 TB/s (92.7 us; the copies alone reach the
+// copy bandwidth), and about 12 us of a call are its start, first data and join.
 //
 // Split: every warp takes an equal, contiguous share of all pages of the call, numbered
 // through over (request, KV head, row block), whatever the requests' lengths: no wave
 // of short ones at the end, and no plan on the host.  A unit (request, KV head, row
 // block) inside one warp's share is finished there; parts join by log-sum-exp in shared
 // memory within a CTA, and CTAs that share a unit through the workspace, by the last one
-// to get there, in page order.  Every warp runs its own ring of bulk copies, two pages
-// (2176 bytes) a stage, across the borders of units.
+// to get there, in page order.  Every warp runs its own ring of bulk copies, four pages
+// (4352 bytes) a stage, across the borders of units.
 //
 // The running maximum is a reference that moves only when a score exceeds it by 2^8
 // (p <= 256 is as good in bf16 and fp32), so a step needs one vote instead of six
 // shuffles.
+//
+// Measured on the way (8 requests of up to 131072 keys): zero points of V as a correction
+// to the sums, two pages a stage 138 us; four pages, subtracted from the operands 94; as
+// it is 92.7.  Slower: one warp of a CTA making all copies (119), 24 warps per SM,
+// two pages of a step in flight at once (96), high halves by multiplication.
 
 #include "int4.cuh"
 #include "ptx.cuh"
@@ -42,12 +51,14 @@ constexpr int kThreads = kNW * 32;
 constexpr int kStepPages = 4;                 // pages per stage
 constexpr int kStageBytes = kStepPages * kInt4Block;
 // A unit's share of the work beyond its pages, in pages: reading its queries, the first
-// maximum, the end.  (64 requests of 1..4096 tokens, us: 36.1 at 0, see below.)
+// maximum, the end.  (64 requests of 1..4096 tokens, us: 36.1 / 32.6 / 33.8 / 33.3 at
+// 0 / 4 / 8 / 12 with one token each, 76.7 / 50.2 / 48.6 / 47.6 with two.)
 constexpr int kUnitCost = 8;
 constexpr float kRaise = 8.f;                 // log2 by which a score may exceed the reference
 constexpr float kUnset = -8e37f;              // reference of a row that has seen no key yet
 
-// Stages in flight per warp, and CTAs per SM that shared memory and registers allow.
+// Stages in flight per warp, and CTAs per SM: 16 warps with 128 registers (three CTAs of
+// fewer registers, or 24 warps, were slower); four blocks of rows keep 255 registers.
 template <int NB>
 struct Tuning {
   static constexpr int kStages = 2;
@@ -99,7 +110,8 @@ __device__ __forceinline__ Request request(const Int4AttnParams &p, int b) {
     r.row0 = p.cu_seqlens_q[b];
     const int end = p.cu_seqlens_q[b + 1];
     r.tokens = end - r.row0;
-    r.bad = r.row0 < 0 || end < r.row0 || end > p.total_q || r.tokens > p.max_q_len || r.kv_len < r.tokens;
+    r.bad = r.row0 < 0 || end < r.row0 || end > p.total_q || r.tokens > p.max_q_len || r.kv_len < r.tokens ||
+            (b > 0 && r.row0 < p.cu_seqlens_q[b - 1]);
     if (r.bad)                                 // what lies inside the buffers becomes NaN
       r.tokens = r.row0 < 0 || r.row0 >= p.total_q ? 0 : min(max(end, r.row0), p.total_q) - r.row0;
   } else {
@@ -270,6 +282,7 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
   const long long slots = static_cast<long long>(gridDim.x) * kNW;
   long long share = quotient(total + slots - 1, slots);
   share = max(share + (share & 1), static_cast<long long>(p.min_pages));
+  if (share > 0x7fffff00ll) return;                    // (the host refuses what lengths allow of this)
   const long long cta_share = share * kNW;
   const long long from = min(total, blockIdx.x * cta_share + warp * share);
   const long long to = min(total, from + share);

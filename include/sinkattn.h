@@ -567,6 +567,8 @@ SINKATTN_API int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *pag
  *
  * Page tables, lengths, sinks, scale, out and lse are as for the bf16 cache, and
  * so is what becomes NaN.  A sink that is NaN or +inf makes its head's rows NaN.
+ * A value row that stands for NaN makes the out of the rows that see it NaN, and
+ * may make their lse NaN, too.
  *
  * The attention calls need a workspace of sinkattn_int4_workspace_bytes, whatever
  * their sizes: 256-byte aligned and ZERO-FILLED BEFORE ITS FIRST USE.  Every call

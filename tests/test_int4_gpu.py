@@ -476,3 +476,73 @@ def test_workspaces_that_do_not_fit_are_refused():
     with pytest.raises(sa.SinkAttnError) as e:
         sa.decode_int4(q, *c.gpu(), 20, workspace=torch.zeros(need + 16, dtype=torch.uint8, device=DEV)[16:])
     assert e.value.status == sa.INVALID_ARGUMENT
+
+
+# ------------------------------------------- both attention kernels, odd arguments
+@pytest.mark.parametrize("bound", [12, 500])             # few rows; tensor cores
+def test_sequences_that_fall_back_are_nan(bound):
+    c = Packed([40, 40, 40, 40], 8, 2)
+    q = c.q(24)
+    cache, table, lens, sinks, scale = c.gpu()
+    # request 1 ends before it starts, request 2 starts before request 1 does
+    out, lse = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV), torch.full(q.shape[:2], 7.0, device=DEV)
+    sa.prefill_paged_int4(q.to(DEV), ints([10, 20, 3, 8, 10]), cache, table, lens, sinks, scale, bound, 40, out=out,
+                          lse=lse)
+    for b, a, e in ((0, 10, 20), (3, 8, 10)):
+        seen = np.arange(40)[None] <= 40 - (e - a) + np.arange(e - a)[:, None]
+        assert_rows([out[a:e], lse[a:e]], rows(np64(q[a:e]), c.k[b], c.v[b], seen, c.sinks, c.scale))
+    assert torch.isnan(out[3:8]).all() and torch.isnan(lse[3:8]).all()
+    rest = [0, 1, 2, 20, 21, 22, 23]
+    assert (out[rest] == 7).all() and (lse[rest] == 7).all()
+
+
+@pytest.mark.parametrize("q_len", [4, 40])               # 16 rows; 160 rows: tensor cores
+def test_hidden_drafts_of_either_kernel_may_be_anything(q_len):
+    n = 130 + q_len
+    c = Packed([n, n, n], 4, 1)
+    q = c.q(3, q_len)
+    masks = workloads.random_tree_masks(c.rng, 3, q_len) & ~(1 << 2)
+    masks[:, 2] |= 1 << 2                                # draft 2 is seen by its own row alone
+    k, v = np.stack([a[132] for a in c.k]), np.stack([a[132] for a in c.v])
+    c.k[0][132], c.v[0][132] = int4.round_trip(k[0]), int4.round_trip(v[0])      # quantised once more
+    want = _verify_want(c, q, masks.numpy())
+    k[1], v[2] = np.nan, np.inf
+    c.put(np.array([s[132] for s in c.slots]), k, v)
+    out, lse = sa.verify_int4(q.to(DEV), *c.gpu(), n, tree_mask=masks.to(DEV))
+    assert torch.isnan(out[1:, 2]).all() and torch.isnan(lse[1, 2]).all()
+    rest = [i for i in range(q_len) if i != 2]
+    assert_rows([out[:, rest], lse[:, rest]], [x[:, rest] for x in want])
+    assert_rows([out[0], lse[0]], [x[0] for x in want])
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("q_lens", [[3, 7], [90, 300]])  # few rows; tensor cores
+def test_odd_sinks_and_rows_of_prompts(q_lens, what):
+    c = Packed(q_lens, 8, 2, seed=3)
+    q = c.q(sum(q_lens))
+    c.sinks[1] = what
+    cu = ints([0, q_lens[0], sum(q_lens)])
+    want = _prefill_want(c, q, q_lens) if what == -float("inf") else None
+    c.sinks[1] = 0.0
+    plain = _prefill_want(c, q, q_lens)
+    c.sinks[1] = what
+    args = c.gpu()
+    out, lse = sa.prefill_paged_int4(q.to(DEV), cu, *args, max(q_lens), max(q_lens))
+    other = [h for h in range(8) if h != 1]
+    assert_rows([out[:, other], lse[:, other]], [x[:, other] for x in plain])
+    if want is not None:
+        assert_rows([out[:, 1], lse[:, 1]], [x[:, 1] for x in want])
+    else:
+        assert torch.isnan(out[:, 1]).all() and torch.isnan(lse[:, 1]).all()
+    # a value row that is not finite: those before it do not see it
+    k, v = np.array(c.k[1][2][None]), np.array(c.v[1][2][None])
+    c.k[1][2], c.v[1][2] = int4.round_trip(k[0]), int4.round_trip(v[0])          # quantised once more
+    c.sinks[1] = 0.0
+    plain = _prefill_want(c, q, q_lens)
+    v[0, 1] = np.nan
+    c.put(np.array([c.slots[1][2]]), k, v)
+    out2, lse2 = sa.prefill_paged_int4(q.to(DEV), cu, c.gpu()[0], *args[1:], max(q_lens), max(q_lens))
+    start = q_lens[0] + 2
+    assert torch.isnan(out2[start:, 4:]).all()
+    assert_rows([out2[:start, 4:], lse2[:start, 4:]], [x[:start, 4:] for x in plain])
+    assert_rows([out2[:, other[:3]], lse2[:, other[:3]]], [x[:, other[:3]] for x in plain])
