@@ -752,6 +752,9 @@ def rope_table(inv_freq, mscale, num_positions, device="cuda"):
     return (float(mscale) * torch.cat([angle.cos(), angle.sin()], 1)).float()
 
 
+_COUNTER_BYTES = 16384          # that a workspace has to hold zeros in
+
+
 def _int4_workspace_bytes(num_sms=0):
     w = _c_size(0)
     _check("sinkattn_int4_workspace_bytes",
@@ -860,7 +863,9 @@ def _int4_args(q, dims, kv_cache, page_table, kv_lens, sinks, batch):
 def _int4_workspace(workspace, dev):
     """The workspace handed in, or a new one (on the stream of the call)."""
     if workspace is None:
-        return torch.zeros(_plan(_int4_workspace_bytes), dtype=_U8, device=dev)
+        workspace = torch.empty(_plan(_int4_workspace_bytes), dtype=_U8, device=dev)
+        workspace[:_COUNTER_BYTES].zero_()         # the rest, some 50 MB, is written before it is read
+        return workspace
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
     return workspace

@@ -65,12 +65,15 @@ struct Int4AttnParams {
   uint16_t *out;                 // bf16 [rows][Hq][64]
   float *lse;                    // [rows][Hq] or null
   int *counters;                 // one per CTA, zero between calls
-  float *ws_o;                   // fp32 [2 ctas][block rows][64]
-  float2 *ws_md;                 // [2 ctas][block rows]: maximum (base 2), sum
+  float *ws_o;                   // fp32 [2 ctas][block rows][64] (tensor cores: [ctas][16][256][4])
+  float2 *ws_md;                 // [2 ctas][block rows] (tensor cores: [ctas][256]): maximum (base 2), sum
   float scale_log2;              // scale * log2(e)
   int max_pages_per_seq, num_seqs, q_len, total_q, max_q_len, max_kv_len;
   int num_qo_heads, num_kv_heads, group, num_pages;
   int min_pages;                 // pages that a warp takes at least
+  int sms;
+  int split_parts, split_from;   // tensor-core form: parts of the keys beyond one for each of split_from
+                                 // blocks of a KV head's rows; 0: none
 };
 
 enum Int4Mode { kInt4Decode, kInt4Verify, kInt4Ragged };
@@ -86,6 +89,8 @@ cudaError_t launch_int4_decode(const Int4AttnParams &p, Int4Mode mode, int row_b
 // Tensor-core form: for groups of at most 128 heads.  Tokens of a CTA; CTAs for one
 // KV head are at most total_q / tokens + num_seqs.
 int int4_prefill_tokens(int group);
+constexpr int kInt4PartKeys = 512;       // keys that a part has at least
+size_t int4_prefill_results_bytes(int ctas);     // of ws_o and ws_md
 cudaError_t launch_int4_prefill(const Int4AttnParams &p, long long ctas, cudaStream_t stream);
 
 }  // namespace sa

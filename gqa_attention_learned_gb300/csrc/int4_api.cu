@@ -17,10 +17,11 @@ using sa::kPageSize;
 
 constexpr int kMinPages = 8;            // pages that a warp takes at least: fewer cost more to join than they save
 
-// Query rows per KV head up to which the kernel of few rows is taken.  It splits a
-// request's keys, the other does not: 64 rows, 16 requests of 4096..32768 keys 204 us
-// against 215.
-constexpr int kFewRows = 64;
+// Query rows per KV head up to which the kernel of few rows is taken.  us of that and of
+// the other, 16 requests of 4096..32768 keys: 32 rows 115 and 146, 64 rows 206 and 146;
+// 64 requests of up to 4096 keys: 32 rows 71 and 85, 64 rows 122 and 86; one of 4000:
+// 20.7 and 17.7, 21.2 and 17.9.
+constexpr int kFewRows = 32;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -34,10 +35,21 @@ bool known_flags(int flags) {
          flags == SINKATTN_LAUNCH_PROGRAMMATIC;
 }
 
+// The kernel of many rows shares a request's keys out among CTAs where there are at most
+// kSplitCtas of them per SM without, with up to kSplitParts more per SM: 64 tokens on
+// 120000 keys 1028 us without, 172 with; two short turns on 20000 and 30000 keys 268 and
+// 196.  What it costs where nothing is gained is 5%: two prompts' chunks of 500 tokens,
+// 256 CTAs, 212 us without, 222 with.
+constexpr int kSplitCtas = 2, kSplitParts = 3;
+int most_split_ctas(int sms) {
+  return std::min<long long>((kSplitCtas + kSplitParts) * static_cast<long long>(sms), sa::kCounterSpan / sizeof(int));
+}
+
 size_t workspace_for(int sms) {
   size_t most = 0;
   for (int blocks : {1, 2, 4})
     most = std::max(most, sa::int4_decode_results_bytes(blocks, sms * sa::int4_decode_ctas_per_sm(blocks)));
+  most = std::max(most, sa::int4_prefill_results_bytes(most_split_ctas(sms)));
   return sa::kCounterSpan + ((most + 255) & ~size_t(255));
 }
 
@@ -92,12 +104,29 @@ int attention_entry(sa::Int4Mode mode, const void *q, const int32_t *cu_seqlens_
   p.group = num_qo_heads / num_kv_heads;
   p.num_pages = num_pages;
   p.min_pages = kMinPages;
+  p.sms = sms;
 
   const int rows = static_cast<int>(std::min<long long>(static_cast<long long>(max_q_len) * p.group, 1 << 20));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t *const ws = static_cast<uint8_t *>(workspace);
   if (mode != sa::kInt4Decode && p.group <= 128 && rows > kFewRows) {
-    const long long tiles = total_q / sa::int4_prefill_tokens(p.group) + static_cast<long long>(num_seqs);
+    const int tokens = sa::int4_prefill_tokens(p.group);
+    long long tiles = mode == sa::kInt4Verify ? num_seqs * ceil_div(max_q_len, tokens)
+                                              : total_q / tokens + static_cast<long long>(num_seqs);
     if (tiles * num_kv_heads > 0x7fffffffll) return SINKATTN_UNSUPPORTED;
+    if (tiles * num_kv_heads <= static_cast<long long>(kSplitCtas) * sms) {
+      const int keys = std::min<long long>(p.max_kv_len, static_cast<long long>(max_pages_per_seq) * kPageSize);
+      p.split_parts = kSplitParts * sms / num_kv_heads;
+      p.split_from = static_cast<int>(tiles);
+      const long long more = std::min<long long>(p.split_parts, tiles * (ceil_div(keys, sa::kInt4PartKeys) - 1));
+      if (more <= 0 || (tiles + more) * num_kv_heads > most_split_ctas(sms)) p.split_parts = 0;
+      else tiles += more;
+    }
+    if (p.split_parts > 0) {
+      p.counters = reinterpret_cast<int *>(ws);
+      p.ws_o = reinterpret_cast<float *>(ws + sa::kCounterSpan);
+      p.ws_md = reinterpret_cast<float2 *>(p.ws_o + static_cast<size_t>(tiles) * num_kv_heads * 256 * kHeadDim);
+    }
     return sa::api_status(sa::launch_int4_prefill(p, tiles * num_kv_heads, st), "int4 attention launch");
   }
   const int blocks = sa::int4_row_blocks(rows);
@@ -109,7 +138,6 @@ int attention_entry(sa::Int4Mode mode, const void *q, const int32_t *cu_seqlens_
   const int ctas = static_cast<int>(std::max(1.0, std::min<double>(slots, std::ceil(work / (8.0 * kMinPages)))));
   // a warp counts its share of the pages, and a unit's start as 8, in ints
   if (work * (1 + 8.0) / (8.0 * ctas) > 0x7f000000) return SINKATTN_UNSUPPORTED;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
   p.counters = reinterpret_cast<int *>(ws);
   p.ws_o = reinterpret_cast<float *>(ws + sa::kCounterSpan);
   p.ws_md = reinterpret_cast<float2 *>(p.ws_o + static_cast<size_t>(ctas) * 2 * 8 * blocks * kHeadDim);

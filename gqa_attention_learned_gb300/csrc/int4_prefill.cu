@@ -26,15 +26,19 @@
 //   warp 17       O += P V, P in place of its scores
 //   warp 18       packed pages into a ring of four key tiles, by bulk copies
 //
-// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1481 us, 928 TFLOP/s,
-// where the kernel of the bf16 cache does 1046): the chain score - exponentials - P V of
-// the two tiles in turn.  The tensor pipe is busy for half of it, P V of 128 x 64 x 128
-// from tensor memory taking about twice its arithmetic's time.  Measured on the way: one
-// tile per CTA 1839 us; four unpacking warps 1700; two score buffers 1692; packed pages
-// straight into registers, a tile ahead, 1600; softmax warps with 128 registers 1555.
-// Slower or no better: 16 softmax warps with half a row each; products started by one
-// thread that walks the tiles alone (1558 us); persistent CTAs (1720: spills); four
-// stages of K and V.
+// Where there are few such CTAs, a request's keys are cut into parts with a CTA each: as
+// many as make the least time (plan_parts()), each at least 512 keys long.  Parts join by
+// log-sum-exp through the workspace, by the last one to get there, in the keys' order.
+//
+// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1338 us, 1027 TFLOP/s, the
+// rate of the bf16 cache's kernel): the chain score - exponentials - P V of the two tiles
+// in turn.  P V of 128 x 64 x 128 from tensor memory takes about twice its arithmetic's
+// time, and start and end of a CTA some 8 us.  Measured on the way: one tile per CTA 1839
+// us; eight unpacking warps, two score buffers 1692; three buffers and a ring of packed
+// pages 1555; softmax warps with 168 registers, sleeping waits 1537; products started by
+// polling warps 1485; a row's mask as bits 1376.  Slower or no better: 16 softmax warps
+// with half a row each; products started by one thread that walks the tiles alone (1558
+// against 1482); persistent CTAs (1720: spills); four stages of K and V.
 //
 // A value row that is not finite must spoil the rows that see it and no others, but
 // 0 * NaN in P V would spoil the whole tile: such a value is stored as zero and its key
@@ -42,6 +46,7 @@
 
 #include "int4.cuh"
 #include "ptx.cuh"
+#include "workspace.cuh"
 
 #include <cmath>
 
@@ -61,6 +66,8 @@ static_assert(2 * kSoftmaxRegs + 3 * kOtherRegs <= 5 * kLaunchRegs, "the split f
 constexpr int kBuffers = 3;                    // of scores in tensor memory
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = kBuffers * kBN;      // behind the scores: 64 columns per tile
+constexpr int kPartTiles = kInt4PartKeys / kBN;        // that a part has at least
+constexpr float kPartCost = 14.f;               // what a part costs beyond its tiles, in tiles
 constexpr float kUnset = -8e37f;               // reference of a row that has seen no key yet
 constexpr float kMostSum = 1024.f;             // sum of a tile's P from which the reference is moved
 
@@ -84,7 +91,9 @@ struct Bars {
   uint64_t p_full[kBuffers];   // P is, in its place
   uint64_t p_used[kBuffers];   // P V has finished: the buffer is free
   uint32_t tmem_base;
-  int bad;
+  int bad, last;
+  int part_tiles, numbers;     // as plan_parts says
+  int shared_by, part, first;  // of the CTAs that share these rows (kept here: registers are short)
 };
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
 
@@ -125,24 +134,28 @@ __device__ __forceinline__ int request_ctas(const Request &r, int tokens) {
 struct Seen {
   int limit, draft;
   uint64_t vis;
-  __device__ __forceinline__ bool operator()(int key) const {
-    if (key < limit) return true;
-    const unsigned u = static_cast<unsigned>(key - draft);
-    return u < 64u && ((vis >> u) & 1);
+  // Bit i: whether the row sees key + i, i < 32.
+  __device__ __forceinline__ uint32_t operator()(int key) const {
+    const int n = limit - key, u = key - draft;
+    uint32_t w = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    if (vis != 0 && u > -32 && u < 64) w |= static_cast<uint32_t>(u >= 0 ? vis >> u : vis << -u);
+    return w;
   }
 };
 
-// P = 2^(s * scale - m) for 32 scores x as bf16 pairs in y; their sums in acc.
+// P = 2^(s * scale - m) for 32 scores x as bf16 pairs in y, of the keys of bits `seen`
+// alone; their sums in acc.  (Bits made once for 32 keys: a comparison per key, and a
+// shift of 64 bits, took 11000 cycles of a tile with an edge.)
 template <bool kMask>
 __device__ __forceinline__ void weigh(const uint32_t (&x)[32], uint32_t (&y)[16], uint64_t scale2, uint64_t negm2,
-                                      const Seen &seen, int key0, uint64_t &acc0, uint64_t &acc1) {
+                                      uint32_t seen, uint64_t &acc0, uint64_t &acc1) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     float a, b;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, negm2), a, b);
     if constexpr (kMask) {
-      if (!seen(key0 + 2 * e)) a = -INFINITY;
-      if (!seen(key0 + 2 * e + 1)) b = -INFINITY;
+      if (!(seen >> (2 * e) & 1)) a = -INFINITY;
+      if (!(seen >> (2 * e + 1) & 1)) b = -INFINITY;
     }
     const float pa = ex2(a), pb = ex2(b);
     if (e & 1) acc1 = f2_add(acc1, f2_pack(pa, pb));
@@ -165,7 +178,7 @@ __device__ __forceinline__ float weigh_tile(uint32_t ts, float sl2, float m, con
   for (int c = 0; c < 4; ++c) {
     tmem_ld_wait32(x[c & 1]);
     if (c < 3) tmem_ld32(ts + 32 * (c + 1), x[(c + 1) & 1]);
-    weigh<kMask>(x[c & 1], y[c], scale2, negm2, seen, key0 + 32 * c, acc0, acc1);
+    weigh<kMask>(x[c & 1], y[c], scale2, negm2, kMask ? seen(key0 + 32 * c) : 0u, acc0, acc1);
   }
   float a, b;
   f2_unpack(f2_add(acc0, acc1), a, b);
@@ -179,10 +192,10 @@ __device__ __forceinline__ float row_max(uint32_t ts, float sl2, const Seen &see
   for (int c = 0; c < 4; ++c) {
     uint32_t x[32];
     tmem_ld32(ts + 32 * c, x);
+    const uint32_t bits = seen(key0 + 32 * c);
     tmem_ld_wait32(x);
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      mx = fmaxf(mx, seen(key0 + 32 * c + e) ? __uint_as_float(x[e]) * sl2 : -INFINITY);
+    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, bits >> e & 1 ? __uint_as_float(x[e]) * sl2 : -INFINITY);
   }
   return mx;
 }
@@ -229,9 +242,8 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t m, bool v) {
 }
 
 // mbar_wait that sleeps: most warps wait for a good part of the time, and what a polling
-// one issues is taken from those that work (1555 us polling for 4 x 2048 tokens on up to
-// 14336 keys, 1537 sleeping).  The two warps that start the products poll: their waits
-// are on the chain (1481).
+// one issues is taken from those that work.  The two warps that start the products poll:
+// their waits are on the chain (1485 us instead of 1537).
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
   constexpr uint32_t kNap = 100000;                    // ns that one attempt may take
   for (uint64_t i = 0; i <= kWaitLimitNs / kNap; ++i) {
@@ -264,29 +276,106 @@ __device__ __forceinline__ uint64_t l2_policy_evict_last() {
   return policy;
 }
 
+constexpr int kSoftmaxThreads = 2 * kBM;
+__device__ __forceinline__ void softmax_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+}
+
 template <int kRegs, bool kMore>
 __device__ __forceinline__ void set_registers() {
   if constexpr (kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// Key tiles that a part of the keys has about, and the parts of all token blocks (one
+// warp calls).  Every lane thinks one length of parts through, and the least time is
+// taken: that of whole waves of equal parts, or of the longest.  There are then no more
+// parts than CTAs: the host launched one for each of split_from blocks, and split_parts
+// more (or what the shortest parts allow).  (More blocks than that, in sequences that
+// overlap: no parts, so nobody waits for one that is not there.)
+__device__ __forceinline__ int2 plan_parts(const Int4AttnParams &p, int tokens, int lane) {
+  constexpr int kWhole = 1 << 30;
+  long long work = 0, ctas = 0;
+  for (int s = lane; s < p.num_seqs; s += 32) {
+    const Request r = request(p, s);
+    const int n = request_ctas(r, tokens);
+    ctas += n;
+    if (!r.bad) work += static_cast<long long>(n) * cdiv(r.kv_len, kBN);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    work += __shfl_xor_sync(0xffffffffu, work, off);
+    ctas += __shfl_xor_sync(0xffffffffu, ctas, off);
+  }
+  if (ctas > p.split_from || work == 0) return make_int2(kWhole, kWhole);
+  const long long aim = p.split_parts * static_cast<long long>(lane + 2);        // of 32
+  const int mine = lane == 31 ? kWhole
+                              : max(kPartTiles, static_cast<int>(min((32 * work + aim - 1) / aim,
+                                                                     static_cast<long long>(kWhole))));
+  int n = 0, longest = 0, bad = 0;
+  for (int s = 0; s < p.num_seqs; ++s) {
+    const Request r = request(p, s);
+    if (r.bad) {
+      ++bad;
+      continue;
+    }
+    const int tiles = cdiv(r.kv_len, kBN), cut = max(1, cdiv(tiles, mine));
+    n += request_ctas(r, tokens) * cut;
+    longest = max(longest, cdiv(tiles, cut));
+  }
+  const float waves = ceilf(static_cast<float>(n) * p.num_kv_heads / p.sms);
+  const float cost = mine == kWhole ? 0.f : kPartCost;
+  const float time = fmaxf(waves * (static_cast<float>(work) / n + cost), longest + cost);
+  const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(time));   // (positive: ordered as integers)
+  const int at = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(time) == best)) - 1;
+  return make_int2(__shfl_sync(0xffffffffu, mine, at), bad + __shfl_sync(0xffffffffu, n, at));
+}
+
+// A number that is the same in all lanes, known to be so: addresses and branches made of
+// the warp's number then take no registers of the lanes (100 bytes spilled
+// without; 490 us to 478 for 2 x 2048 tokens on 6000).
+__device__ __forceinline__ int uniform(int x) {
+  return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(x)));
+}
+
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   Bars &bar = *reinterpret_cast<Bars *>(smem + kOffBars);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int tile_tokens = kBM / p.group, tokens = 2 * tile_tokens;
 
-  // ---- this CTA's request and tokens.  CTAs are numbered through request by request;
-  // the last ones, whose rows see the most keys, are launched first.
+  // ---- this CTA's request, tokens and part of the keys.  CTAs are numbered through
+  // request by request; the last ones, whose rows see the most keys, are launched first.
   const int kvh = static_cast<int>(blockIdx.x % p.num_kv_heads);
-  int number = static_cast<int>(gridDim.x / p.num_kv_heads) - 1 - static_cast<int>(blockIdx.x / p.num_kv_heads);
-  int seq = -1;
-  Request rq;
+  int numbers = static_cast<int>(gridDim.x / p.num_kv_heads);
+  int part_tiles = 0;                                  // key tiles that a part has about
+  if constexpr (kSplit) {
+    if (warp == 0) {
+      const int2 plan = plan_parts(p, tokens, lane);
+      if (lane == 0) {
+        bar.part_tiles = plan.x;
+        bar.numbers = min(plan.y, numbers);
+      }
+    }
+    __syncthreads();
+    part_tiles = bar.part_tiles;
+    numbers = bar.numbers;
+  }
+  // parts of a request's every token block
+  auto request_parts = [&](const Request &r) { return kSplit && !r.bad ? max(1, cdiv(cdiv(r.kv_len, kBN), part_tiles)) : 1; };
+  const int global = numbers - 1 - static_cast<int>(blockIdx.x / p.num_kv_heads);
+  if (global < 0) return;
+  int number = global, seq = -1;
   for (int s0 = 0; s0 < p.num_seqs && seq < 0; s0 += 32) {
     const int s = s0 + lane;
-    const int mine = s < p.num_seqs ? request_ctas(request(p, s), tokens) : 0;
+    int mine = 0;
+    if (s < p.num_seqs) {
+      const Request r = request(p, s);
+      mine = request_ctas(r, tokens) * request_parts(r);
+    }
     int upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -303,7 +392,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     }
   }
   if (seq < 0) return;                                 // fewer than the host allowed for
-  rq = request(p, seq);
+  const Request rq = request(p, seq);
   if (rq.bad) {
     // this request's rows, as far as they lie inside the buffers
     if (rq.q_start < 0 || rq.q_start >= p.total_q) return;
@@ -317,7 +406,9 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     }
     return;
   }
-  const int tok0 = number * tokens;                    // first token of this CTA
+  const int parts = request_parts(rq);
+  const int part = kSplit ? number % parts : 0;
+  const int tok0 = (kSplit ? number / parts : number) * tokens;      // first token of this CTA
   const int shift = rq.kv_len - rq.q_len;              // keys before the new tokens
   // rows and key tiles of either tile (tile 1 may have none)
   int rows[2], ntiles[2];
@@ -327,6 +418,18 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     rows[x] = n * p.group;
     const int keys = p.tree_mask ? rq.kv_len : shift + tok0 + x * tile_tokens + n;
     ntiles[x] = n > 0 ? cdiv(keys, kBN) : 0;
+  }
+  // keys before this CTA's part (keys, pages and key tiles are counted from there on); CTAs
+  // that share its rows
+  int first_key = 0, shared_by = 1;
+  if constexpr (kSplit) {
+    const int all = max(ntiles[0], ntiles[1]), each = cdiv(all, parts);
+    const int first_tile = part * each;
+    first_key = first_tile * kBN;
+    shared_by = cdiv(all, each);
+    if (part >= shared_by) return;                     // uniform over the CTA
+#pragma unroll
+    for (int x = 0; x < 2; ++x) ntiles[x] = min(max(ntiles[x] - first_tile, 0), each);
   }
   const int n_tiles = max(ntiles[0], ntiles[1]), both = min(ntiles[0], ntiles[1]);
   // number of the product of key tile j and query tile x
@@ -340,8 +443,8 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
   }
   // Packed pages of key tile j into their ring, once its slot has been unpacked (all
   // lanes of the loading warp call; lanes 0..7 copy a page each).
-  const int npages = cdiv(rq.kv_len, kPageSize);
-  const int32_t *table = p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq;
+  const int npages = cdiv(rq.kv_len - first_key, kPageSize);
+  const int32_t *table = p.page_table + static_cast<size_t>(seq) * p.max_pages_per_seq + first_key / kPageSize;
   auto page_id = [&](int j) {
     const int page = j * kPages + lane;
     return lane < kPages && page < npages ? __ldg(table + page) : -1;
@@ -378,24 +481,39 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
       mbar_init(&bar.p_used[b], 1);
     }
     bar.bad = 0;
+    if constexpr (kSplit) {
+      bar.shared_by = shared_by;
+      bar.part = part;
+      bar.first = global - part;
+    }
     fence_mbar_init();
    }
    __syncwarp();
    for (int j = 0; j < min(kRaw, n_tiles); ++j) load_raw(j, page_id(j));      // fresh slots: no waits
   }
   // Q, its dims permuted as the codes' are; rows of nobody are zero
-  for (int i = threadIdx.x; i < 2 * kBM * (kHeadDim / 8); i += kThreads) {
-    const int r = i / (kHeadDim / 8), c = i % (kHeadDim / 8);
-    const int x = r / kBM, rr = r % kBM;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (rr < rows[x]) {
-      const int token = rq.q_start + tok0 + x * tile_tokens + rr / p.group;
-      const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p.q) +
-                            (static_cast<size_t>(token) * p.num_qo_heads + kvh * p.group + rr % p.group) * (kHeadDim / 8) + c);
-      w = make_uint4(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632), __byte_perm(q.y, q.w, 0x5410),
-                     __byte_perm(q.y, q.w, 0x7632));
+  {
+    constexpr int kChunks = 2 * kBM * (kHeadDim / 8), kEach = (kChunks + kThreads - 1) / kThreads;
+    uint4 q[kEach];                                    // (all loads at once)
+#pragma unroll
+    for (int n = 0; n < kEach; ++n) {
+      const int i = threadIdx.x + n * kThreads, r = i / (kHeadDim / 8), c = i % (kHeadDim / 8);
+      const int x = r / kBM, rr = r % kBM;
+      q[n] = make_uint4(0, 0, 0, 0);
+      if (i < kChunks && rr < (x ? rows[1] : rows[0])) {
+        const int token = rq.q_start + tok0 + x * tile_tokens + rr / p.group;
+        q[n] = __ldg(reinterpret_cast<const uint4 *>(p.q) +
+                     (static_cast<size_t>(token) * p.num_qo_heads + kvh * p.group + rr % p.group) * (kHeadDim / 8) + c);
+      }
     }
-    *reinterpret_cast<uint4 *>(smem + kOffQ + r * 128 + ((c ^ (r & 7)) << 4)) = w;
+#pragma unroll
+    for (int n = 0; n < kEach; ++n) {
+      const int i = threadIdx.x + n * kThreads, r = i / (kHeadDim / 8), c = i % (kHeadDim / 8);
+      if (i < kChunks)
+        *reinterpret_cast<uint4 *>(smem + kOffQ + r * 128 + ((c ^ (r & 7)) << 4)) =
+            make_uint4(__byte_perm(q[n].x, q[n].z, 0x5410), __byte_perm(q[n].x, q[n].z, 0x7632),
+                       __byte_perm(q[n].y, q[n].w, 0x5410), __byte_perm(q[n].y, q[n].w, 0x7632));
+    }
   }
   fence_proxy_async_smem();
   tc_fence_before();
@@ -408,6 +526,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     set_registers<kOtherRegs, false>();
     const int uw = warp - kUnpackWarp;                 // this warp's page of every tile
     const int g = lane >> 2, t = lane & 3;
+    const int keys = rq.kv_len - first_key - uw * kPageSize;
     uint32_t mask, sixteen;
     asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
     asm volatile("mov.b32 %0, 0x41804180;" : "=r"(sixteen));
@@ -433,7 +552,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
       // Odd keys of the page (`own` is that of lanes 0..15): those past the last one
       // become zeros, and a value that is not finite zeros with a key that is not finite.
       const unsigned odd = __ballot_sync(0xffffffffu, (own & 0x7f800000u) == 0x7f800000u) & 0xffffu;
-      const int live = rq.kv_len - j * kBN - uw * kPageSize;
+      const int live = keys - j * kBN;
       if (odd != 0 || live < kPageSize) {
         const unsigned gone = live >= kPageSize ? 0u : live <= 0 ? 0xffffu : 0xffffu & (0xffffu << live);
         auto k = [&](uint32_t &m, int key) {
@@ -553,17 +672,17 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     const int head = kvh * p.group + r % p.group;
     const bool live = r < rows[x];
     Seen seen;
-    seen.limit = min(shift + i + 1, rq.kv_len);
-    seen.draft = shift;
+    seen.limit = min(shift + i + 1, rq.kv_len) - first_key;
+    seen.draft = shift - first_key;
     seen.vis = 0;
     if (p.tree_mask) {
-      seen.limit = shift;
+      seen.limit = shift - first_key;
       if (live) seen.vis = p.tree_mask[static_cast<size_t>(seq) * p.q_len + i];
     }
     const float sl2 = p.scale_log2;
     // a sink that is no logit (NaN, +inf) spoils the sum, not the reference
     float m = kUnset, d = 0.f;
-    if (live) {
+    if (live && first_key == 0) {
       const float logit = __ldg(p.sinks + head) * kLog2e;
       if (logit < INFINITY) {
         m = fmaxf(logit, kUnset);
@@ -582,7 +701,9 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
       const uint32_t ts = trow + b * kBN;
       const bool edge = __any_sync(0xffffffffu, key0 + kBN > seen.limit);
       uint32_t y[4][16];
-      float sum = edge ? weigh_tile<true>(ts, sl2, m, seen, key0, y) : weigh_tile<false>(ts, sl2, m, seen, key0, y);
+      // a reference that is not set at all needs no try
+      const bool unset = j == 0 && __any_sync(0xffffffffu, m == kUnset);
+      float sum = unset ? INFINITY : edge ? weigh_tile<true>(ts, sl2, m, seen, key0, y) : weigh_tile<false>(ts, sl2, m, seen, key0, y);
       if (__any_sync(0xffffffffu, !(sum <= kMostSum))) {
         // some reference is too small: the rows' maxima, and the tile again
         const float mx = row_max(ts, sl2, seen, key0);
@@ -624,21 +745,85 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     tc_fence_before();
     __syncthreads();
     const bool failed = bar.bad != 0;
-    if (live) {
-      const float inv = failed ? NAN : d == 0.f ? 0.f : 1.f / d;
-      const size_t row = static_cast<size_t>(rq.q_start + i) * p.num_qo_heads + head;
-      uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kHeadDim);
+    if constexpr (kSplit) {
+      const int shared_by = bar.shared_by, part = bar.part, first = bar.first;
+      if (shared_by > 1) {
+        // This part's sums to the workspace; the last of the CTAs that share the rows
+        // joins them, in the keys' order, and leaves the counter at zero.  Sums of a
+        // row: 16 vectors of four, rows next to each other.
+        constexpr int kVectors = kHeadDim / 4;
+        const int row = threadIdx.x;
+        auto slot = [&](int c) { return static_cast<size_t>(first + c) * p.num_kv_heads + kvh; };
+        float4 *ws_o = reinterpret_cast<float4 *>(p.ws_o);
+        if (live) {
+          const bool any = mine > 0 && ok;
+          float4 *dst = ws_o + slot(part) * kVectors * kSoftmaxThreads + row;
 #pragma unroll
-      for (int c = 0; c < kHeadDim / 8; ++c) {
-        // column 8c + 2j holds dim 8c + j, column 8c + 2j + 1 dim 8c + 4 + j
-        auto dim = [&](int e) {
-          const int col = 8 * c + 2 * (e & 3) + (e >> 2);
-          return failed ? NAN : __uint_as_float(o[col >> 5][col & 31]) * inv;
-        };
-        dst[c] = make_uint4(pack_bf16(dim(0), dim(1)), pack_bf16(dim(2), dim(3)), pack_bf16(dim(4), dim(5)),
-                            pack_bf16(dim(6), dim(7)));
+          for (int c = 0; c < kVectors; ++c) {
+            auto sum = [&](int e) { return any ? __uint_as_float(o[(4 * c + e) >> 5][(4 * c + e) & 31]) : 0.f; };
+            dst[c * kSoftmaxThreads] = make_float4(sum(0), sum(1), sum(2), sum(3));
+          }
+          p.ws_md[slot(part) * kSoftmaxThreads + row] = make_float2(m, failed ? NAN : d);
+        }
+        softmax_barrier();
+        int *counter = p.counters + slot(0);
+        if (threadIdx.x == 0) bar.last = atomic_add_acq_rel(counter, 1) == shared_by - 1;
+        softmax_barrier();
+        if (!bar.last) return;
+        if (threadIdx.x == 0) *counter = 0;
+        if (live) {
+          m = kUnset;
+          for (int c = 0; c < shared_by; ++c) m = fmaxf(m, __ldcg(&p.ws_md[slot(c) * kSoftmaxThreads + row]).x);
+          d = 0.f;
+#pragma unroll
+          for (int i = 0; i < kHeadDim; ++i) o[i >> 5][i & 31] = 0;
+#pragma unroll 1
+          for (int c = 0; c < shared_by; ++c) {
+            const float2 md = __ldcg(&p.ws_md[slot(c) * kSoftmaxThreads + row]);
+            const float4 *src = ws_o + slot(c) * kVectors * kSoftmaxThreads + row;
+            const float w = ex2(md.x - m);
+            d = fmaf(w, md.y, d);
+#pragma unroll
+            for (int v = 0; v < kVectors; ++v) {
+              const float4 a = __ldcg(src + v * kSoftmaxThreads);
+              const float f[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t &to_sum = o[(4 * v + e) >> 5][(4 * v + e) & 31];
+                to_sum = __float_as_uint(fmaf(w, f[e], __uint_as_float(to_sum)));
+              }
+            }
+          }
+        }
       }
-      if (p.lse) p.lse[row] = failed ? NAN : d == 0.f ? -INFINITY : (m + lg2(d)) * kLn2;
+    }
+    // rows through shared memory (Q's place), so that a warp stores whole lines
+    const float inv = failed ? NAN : d == 0.f ? 0.f : 1.f / d;           // (a part that failed made d NaN)
+    uint8_t *mine_out = smem + kOffQ + threadIdx.x * 128;
+#pragma unroll
+    for (int c = 0; c < kHeadDim / 8; ++c) {
+      // column 8c + 2j holds dim 8c + j, column 8c + 2j + 1 dim 8c + 4 + j
+      auto dim = [&](int e) {
+        const int col = 8 * c + 2 * (e & 3) + (e >> 2);
+        return failed ? NAN : __uint_as_float(o[col >> 5][col & 31]) * inv;
+      };
+      *reinterpret_cast<uint4 *>(mine_out + ((c ^ (r & 7)) << 4)) =
+          make_uint4(pack_bf16(dim(0), dim(1)), pack_bf16(dim(2), dim(3)), pack_bf16(dim(4), dim(5)),
+                     pack_bf16(dim(6), dim(7)));
+    }
+    if (live && p.lse)
+      p.lse[static_cast<size_t>(rq.q_start + i) * p.num_qo_heads + head] =
+          failed ? NAN : d == 0.f ? -INFINITY : (m + lg2(d)) * kLn2;
+    __syncwarp();
+#pragma unroll 4
+    for (int n = 0; n < 8; ++n) {
+      const int rr = (warp & 3) * 32 + 4 * n + (lane >> 3), c = lane & 7;       // row of the tile
+      if (rr < rows[x]) {
+        const size_t row = static_cast<size_t>(rq.q_start + tok0 + x * tile_tokens + rr / p.group) * p.num_qo_heads +
+                           kvh * p.group + rr % p.group;
+        *reinterpret_cast<uint4 *>(p.out + row * kHeadDim + 8 * c) =
+            *reinterpret_cast<const uint4 *>(smem + kOffQ + (x * kBM + rr) * 128 + ((c ^ (rr & 7)) << 4));
+      }
     }
     return;
   } else {
@@ -669,13 +854,19 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
 
 int int4_prefill_tokens(int group) { return 2 * (kBM / group); }
 
+size_t int4_prefill_results_bytes(int ctas) {
+  return static_cast<size_t>(ctas) * kSoftmaxThreads * (kHeadDim * sizeof(float) + sizeof(float2));
+}
+
 cudaError_t launch_int4_prefill(const Int4AttnParams &p, long long ctas, cudaStream_t stream) {
   static_assert(kSmemBytes > 114 * 1024 && kSmemBytes <= 227 * 1024, "one CTA per SM");
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  cudaError_t err = set_smem_once<int4_prefill_kernel>(kSmemBytes);
+  auto kernel = p.split_parts > 0 ? int4_prefill_kernel<true> : int4_prefill_kernel<false>;
+  cudaError_t err = p.split_parts > 0 ? set_smem_once<int4_prefill_kernel<true>>(kSmemBytes)
+                                      : set_smem_once<int4_prefill_kernel<false>>(kSmemBytes);
   if (err != cudaSuccess) return err;
-  return launch_kernel(int4_prefill_kernel, static_cast<unsigned>(ctas), kThreads, kSmemBytes, stream, false, p);
+  return launch_kernel(kernel, static_cast<unsigned>(ctas), kThreads, kSmemBytes, stream, false, p);
 }
 
 }  // namespace sa

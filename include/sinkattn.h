@@ -570,8 +570,9 @@ SINKATTN_API int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *pag
  * A value row that stands for NaN makes the out of the rows that see it NaN, and
  * may make their lse NaN, too.
  *
- * The attention calls need a workspace of sinkattn_int4_workspace_bytes, whatever
- * their sizes: 256-byte aligned and ZERO-FILLED BEFORE ITS FIRST USE.  Every call
+ * The attention calls need a workspace of sinkattn_int4_workspace_bytes (about
+ * 50 MB), whatever their sizes: 256-byte aligned and ZERO-FILLED BEFORE ITS FIRST
+ * USE (its first 16384 bytes at least).  Every call
  * leaves it ready for the next, and it may serve calls of the other operators in
  * turn (whose own rules on size hold); calls that share it must not overlap on
  * the GPU.  num_sms: 0 = ask the current device.

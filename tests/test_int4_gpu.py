@@ -546,3 +546,82 @@ def test_odd_sinks_and_rows_of_prompts(q_lens, what):
     assert torch.isnan(out2[start:, 4:]).all()
     assert_rows([out2[:start, 4:], lse2[:start, 4:]], [x[:start, 4:] for x in plain])
     assert_rows([out2[:, other[:3]], lse2[:, other[:3]]], [x[:, other[:3]] for x in plain])
+
+
+# ------------------------------------------------- keys in parts (many rows, long caches)
+def _parts_case(seed=5):
+    # 48 rows per KV head; 1 .. 40 key tiles, one request of a single page
+    q_lens, prefix = [6, 6, 1, 6, 3], [5003, 1500, 2100, 0, 770]
+    c = Packed([a + b for a, b in zip(q_lens, prefix)], 16, 2, seed=seed)
+    return c, q_lens, c.q(sum(q_lens)), ints(np.concatenate([[0], np.cumsum(q_lens)]))
+
+
+def test_parts_of_long_caches():
+    c, q_lens, q, cu = _parts_case()
+    want = _prefill_want(c, q, q_lens)
+    ws = torch.zeros(sa.int4_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    first = None
+    for bounds in ((6, c.max_kv), (60, 9000), (2**40, 2**40)):
+        got = sa.prefill_paged_int4(q.to(DEV), cu, *c.gpu(), *bounds, workspace=ws)
+        assert_rows(got, want, str(bounds))
+        assert not ws[:16384].any()                      # ready for the next call
+        again = sa.prefill_paged_int4(q.to(DEV), cu, *c.gpu(), *bounds, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+        first = first or got
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("heads", [(16, 2), (12, 1), (40, 1), (8, 8)])
+def test_parts_of_verifications(heads, tree):
+    q_len = 64 if heads == (8, 8) else 9
+    lens = [3000, 600, q_len, 1100 + q_len]
+    c = Packed(lens, *heads, seed=11)
+    q = c.q(4, q_len)
+    c.sinks[0] = -np.inf
+    masks = workloads.random_tree_masks(c.rng, 4, q_len) if tree else None
+    got = sa.verify_int4(q.to(DEV), *c.gpu(), c.max_kv, tree_mask=None if masks is None else masks.to(DEV))
+    assert_rows(got, _verify_want(c, q, None if masks is None else masks.numpy()))
+
+
+def test_parts_with_bad_pages_values_and_lengths():
+    c, q_lens, q, cu = _parts_case(6)
+    want = _prefill_want(c, q, q_lens)
+    cache, table, lens, sinks, scale = c.gpu()
+    ws = torch.zeros(sa.int4_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    for change in ("first page", "middle page", "last page", "length"):
+        t, n = table.clone(), lens.clone()
+        if change == "length":
+            n[0] = -3
+        else:
+            t[0, {"first page": 0, "middle page": 150, "last page": 312}[change]] = c.pages
+        out, lse = sa.prefill_paged_int4(q.to(DEV), cu, cache, t, n, sinks, scale, 6, c.max_kv, workspace=ws)
+        assert torch.isnan(out[:6]).all() and torch.isnan(lse[:6]).all(), change
+        assert_rows([out[6:], lse[6:]], [x[6:] for x in want], change)
+        assert not ws[:16384].any()
+    k, v = np.array(c.k[0][2500][None]), np.array(c.v[0][2500][None])
+    v[0, 1] = np.inf
+    c.put(np.array([c.slots[0][2500]]), k, v)
+    out, lse = sa.prefill_paged_int4(q.to(DEV), cu, *c.gpu(), 6, c.max_kv, workspace=ws)
+    assert torch.isnan(out[:6, 8:]).all() and torch.isfinite(out[:6, :8]).all()
+    assert_rows([out[6:], lse[6:]], [x[6:] for x in want])
+
+
+def test_parts_captured_and_among_overlapping_sequences():
+    c, q_lens, q, cu = _parts_case(7)
+    want = _prefill_want(c, q, q_lens)
+    ws = torch.zeros(sa.int4_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    args, q_dev = c.gpu(), q.to(DEV)
+    graph = torch.cuda.CUDAGraph()
+    sa.prefill_paged_int4(q_dev, cu, *args, 6, c.max_kv, workspace=ws)
+    with torch.cuda.graph(graph):
+        got = sa.prefill_paged_int4(q_dev, cu, *args, 6, c.max_kv, workspace=ws)
+    for _ in range(3):
+        graph.replay()
+    assert_rows(got, want)
+    # sequences that overlap hold more rows than there are: rows may be anyone's, the
+    # workspace is as it was, and the next call is right
+    many = torch.tensor([0, 22, 0, 0, 22, 0, 0, 22, 0, 0, 22], dtype=torch.int32, device=DEV)
+    wide = [args[1].repeat(2, 1), args[2].repeat(2)]
+    sa.prefill_paged_int4(q_dev, many, args[0], *wide, *args[3:], 40, c.max_kv, workspace=ws)
+    assert not ws[:16384].any()
+    assert_rows(sa.prefill_paged_int4(q_dev, cu, *args, 6, c.max_kv, workspace=ws), want)
