@@ -33,7 +33,7 @@
 // What bounds it, for 4 x 2048 tokens on up to 14336 keys (1338 us, 1027 TFLOP/s, the
 // rate of the bf16 cache's kernel): the chain score - exponentials - P V of the two tiles
 // in turn.  P V of 128 x 64 x 128 from tensor memory takes about twice its arithmetic's
-// time, and start and end of a CTA some 8 us.  Measured on the way: one tile per CTA 1839
+// time, and start and end of a CTA some 5 us.  Measured on the way: one tile per CTA 1839
 // us; eight unpacking warps, two score buffers 1692; three buffers and a ring of packed
 // pages 1555; softmax warps with 168 registers, sleeping waits 1537; products started by
 // polling warps 1485; a row's mask as bits 1376.  Slower or no better: 16 softmax warps
@@ -677,7 +677,7 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     seen.vis = 0;
     if (p.tree_mask) {
       seen.limit = shift - first_key;
-      if (live) seen.vis = p.tree_mask[static_cast<size_t>(seq) * p.q_len + i];
+      if (live) seen.vis = p.tree_mask[static_cast<size_t>(seq) * p.q_len + i] & (~0ull >> (64 - p.q_len));
     }
     const float sl2 = p.scale_log2;
     // a sink that is no logit (NaN, +inf) spoils the sum, not the reference

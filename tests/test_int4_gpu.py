@@ -625,3 +625,32 @@ def test_parts_captured_and_among_overlapping_sequences():
     sa.prefill_paged_int4(q_dev, many, args[0], *wide, *args[3:], 40, c.max_kv, workspace=ws)
     assert not ws[:16384].any()
     assert_rows(sa.prefill_paged_int4(q_dev, cu, *args, 6, c.max_kv, workspace=ws), want)
+
+
+@pytest.mark.parametrize("q_len", [3, 9, 63, 64])
+def test_bits_past_the_drafts_mean_nothing(q_len):
+    n = 700 + q_len
+    c = Packed([n, q_len, n + 20], 4, 1, seed=q_len)
+    q = c.q(3, q_len)
+    masks = workloads.random_tree_masks(c.rng, 3, q_len)
+    want = _verify_want(c, q, masks.numpy())
+    past = -(1 << q_len) if q_len < 64 else 0
+    got = sa.verify_int4(q.to(DEV), *c.gpu(), c.max_kv, tree_mask=(masks | past).to(DEV))
+    assert_rows(got, want)
+
+
+def test_the_same_rows_again_and_slots_shared_between_requests():
+    # two requests over the same pages, a page twice in one request
+    c = Packed([64, 64], 8, 2)
+    q = c.q(2)
+    cache, table, lens, sinks, scale = c.gpu()
+    table[1] = table[0]
+    table[1, 2] = table[0, 1]
+    order = np.r_[0:32, 16:32, 48:64]
+    want = [rows(np64(q[b:b + 1]), c.k[0][o], c.v[0][o], np.ones((1, 64), bool), c.sinks, c.scale)
+            for b, o in enumerate((np.arange(64), order))]
+    got = sa.decode_int4(q.to(DEV), cache, table, lens, sinks, scale, 64)
+    assert_rows(got, [np.concatenate(p) for p in zip(*want)])
+    k, v = sa.gather_int4(cache, ints([int(c.slots[0][5])] * 3 + [-1, 16 * c.pages]))
+    assert torch.equal(k[0], k[2]) and torch.equal(v[1], v[2]) and torch.isnan(k[3:]).all() and torch.isnan(v[3:]).all()
+    assert (np64(k[0]) == c.k[0][5]).all()
