@@ -174,7 +174,7 @@ int sinkattn_qkv_prologue_int4(const void *qkv, const void *bias, const int32_t 
   if (!aligned(qkv, 16) || !aligned(bias, 16) || !aligned(q_out, 16) || !aligned(kv_cache, 16) ||
       !aligned(positions, 4) || !aligned(slot_mapping, 4) || !aligned(rope, 4))
     return SINKATTN_INVALID_ARGUMENT;
-  if (num_qo_heads + 2ll * num_kv_heads > 0x7fffffffll / 4 / num_tokens)
+  if (num_qo_heads + 2ll * num_kv_heads > std::min(0x7ffff000ll / 4 / num_tokens, 0x7fffffffll / kHeadDim))
     return SINKATTN_UNSUPPORTED;
   sa::Int4PrologueParams p{};
   p.qkv = static_cast<const uint16_t *>(qkv);
@@ -201,8 +201,8 @@ int sinkattn_gather_int4(const void *kv_cache, const int32_t *slots, int num_row
   if (!kv_cache || !slots || !k || !v) return SINKATTN_INVALID_ARGUMENT;
   if (!aligned(kv_cache, 16) || !aligned(slots, 4) || !aligned(k, 16) || !aligned(v, 16))
     return SINKATTN_INVALID_ARGUMENT;
-  // 32 rows of a KV head to a CTA
-  if (static_cast<long long>(num_rows) * num_kv_heads > 32ll * 0x7fffffffll) return SINKATTN_UNSUPPORTED;
+  // 16 rows of a KV head to a CTA
+  if (static_cast<long long>(num_rows) * num_kv_heads > 16ll * 0x7fffffffll) return SINKATTN_UNSUPPORTED;
   sa::Int4GatherParams p{};
   p.kv_cache = static_cast<const uint8_t *>(kv_cache);
   p.slots = slots;

@@ -550,7 +550,8 @@ SINKATTN_API int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *pag
  *     n  = clamp(rint(x / s) + z, 0, 15)           (rint: ties to even)
  * and stands for s * (n - z), which is always a bf16 number: every operator here
  * computes what its bf16 counterpart computes on a cache of these values.  A row
- * whose range is not finite stands for 64 NaN.  x is taken in fp32.
+ * whose range is not finite stands for 64 NaN.  x is taken in fp32.  (Of a range above
+ * 2^127 the largest values may be infinite.)
  *
  * Layout of a block (one page, one KV head), slot j = 0..15, 32-bit words,
  * little endian:
@@ -589,7 +590,8 @@ SINKATTN_API int sinkattn_int4_workspace_bytes(int num_sms, size_t *workspace_by
  *                    (one table serves all layers)
  *   positions      : int32 [num_tokens], rows of rope; a position outside of it
  *                    makes the token's q rows NaN, and its k rows stand for NaN
- *   other arguments: as for sinkattn_qkv_prologue
+ *   other arguments: as for sinkattn_qkv_prologue, but two tokens mapped to the
+ *                    same slot may leave a mixture of their rows
  * x = qkv + bias, then x1 cos - x2 sin and x2 cos + x1 sin, each operation
  * rounded to fp32 on its own: equal inputs give equal codes on any machine.
  * Launch: as for sinkattn_qkv_prologue.

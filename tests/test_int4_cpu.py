@@ -111,6 +111,7 @@ def test_prologue_refusals(lib):
     assert call(d=128) == sa.UNSUPPORTED
     assert call(page=32) == sa.UNSUPPORTED
     assert call(tokens=2**28, hq=64, hkv=8) == sa.UNSUPPORTED
+    assert call(hq=2**26) == sa.UNSUPPORTED
 
 
 def test_gather_refusals(lib):
