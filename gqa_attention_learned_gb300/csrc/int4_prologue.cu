@@ -111,7 +111,7 @@ int4_prologue_kernel(const __grid_constant__ Int4PrologueParams p) {
 
   const int rows = p.num_qo_heads + 2 * p.num_kv_heads;
   const int per_tok = rows * 4;
-  const size_t row_elems = static_cast<size_t>(rows) * kHeadDim;
+  const int row_elems = rows * kHeadDim;
   const int items = min(kTok, p.num_tokens - tok0) * per_tok;
   // whole warps stay together for the shuffles: items past the last are left out
   // of the loads and stores only
@@ -122,7 +122,7 @@ int4_prologue_kernel(const __grid_constant__ Int4PrologueParams p) {
     const int t = tok0 + tt;
     const int r = item % per_tok;
     const int h = r >> 2, c = r & 3;
-    const size_t base = t * row_elems + static_cast<size_t>(h) * kHeadDim;
+    const size_t base = static_cast<size_t>(t) * row_elems + h * kHeadDim;
     float a[8], b[8];                          // dims 8c.. and 8c+32..
     unpack8(__ldg(reinterpret_cast<const uint4 *>(p.qkv + base + 8 * c)), a);
     unpack8(__ldg(reinterpret_cast<const uint4 *>(p.qkv + base + 8 * c + 32)), b);
