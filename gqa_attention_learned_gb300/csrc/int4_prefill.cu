@@ -30,13 +30,13 @@
 // many as make the least time (plan_parts()), each at least 512 keys long.  Parts join by
 // log-sum-exp through the workspace, by the last one to get there, in the keys' order.
 //
-// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1338 us, 1027 TFLOP/s, the
-// rate of the bf16 cache's kernel): the chain score - exponentials - P V of the two tiles
+// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1357 us, 1013 TFLOP/s,
+// where the kernel of the bf16 cache does 1046): the chain score - exponentials - P V of the two tiles
 // in turn.  P V of 128 x 64 x 128 from tensor memory takes about twice its arithmetic's
 // time, and start and end of a CTA some 5 us.  Measured on the way: one tile per CTA 1839
 // us; eight unpacking warps, two score buffers 1692; three buffers and a ring of packed
 // pages 1555; softmax warps with 168 registers, sleeping waits 1537; products started by
-// polling warps 1485; a row's mask as bits 1376.  Slower or no better: 16 softmax warps
+// polling warps 1485; a row's mask as bits 1376; fewer spills 1357.  Slower or no better: 16 softmax warps
 // with half a row each; products started by one thread that walks the tiles alone (1558
 // against 1482); persistent CTAs (1720: spills); four stages of K and V.
 //
@@ -93,6 +93,7 @@ struct Bars {
   uint32_t tmem_base;
   int bad, last;
   int part_tiles, numbers;     // as plan_parts says
+  uint64_t vis[2 * kBM];       // mask of a row
   int shared_by, part, first;  // of the CTAs that share these rows (kept here: registers are short)
 };
 constexpr int kSmemBytes = kOffBars + static_cast<int>(sizeof(Bars)) + 1024;
@@ -130,15 +131,19 @@ __device__ __forceinline__ int request_ctas(const Request &r, int tokens) {
   return r.bad ? 1 : cdiv(r.q_len, tokens);
 }
 
-// A row's keys [0, limit), and the draft keys from `draft` on by the bits of `vis`.
+// A row's keys [0, limit), and the draft keys from `draft` on by the bits of *vis (in
+// shared memory, registers are short; null: none).
 struct Seen {
   int limit, draft;
-  uint64_t vis;
+  const uint64_t *vis;
   // Bit i: whether the row sees key + i, i < 32.
   __device__ __forceinline__ uint32_t operator()(int key) const {
-    const int n = limit - key, u = key - draft;
+    const int n = limit - key;
     uint32_t w = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-    if (vis != 0 && u > -32 && u < 64) w |= static_cast<uint32_t>(u >= 0 ? vis >> u : vis << -u);
+    if (vis) {
+      const int u = key - draft;
+      if (u > -32 && u < 64) w |= static_cast<uint32_t>(u >= 0 ? *vis >> u : *vis << -u);
+    }
     return w;
   }
 };
@@ -674,10 +679,11 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
     Seen seen;
     seen.limit = min(shift + i + 1, rq.kv_len) - first_key;
     seen.draft = shift - first_key;
-    seen.vis = 0;
+    seen.vis = nullptr;
     if (p.tree_mask) {
       seen.limit = shift - first_key;
-      if (live) seen.vis = p.tree_mask[static_cast<size_t>(seq) * p.q_len + i] & (~0ull >> (64 - p.q_len));
+      seen.vis = &bar.vis[threadIdx.x];
+      bar.vis[threadIdx.x] = live ? p.tree_mask[static_cast<size_t>(seq) * p.q_len + i] & (~0ull >> (64 - p.q_len)) : 0;
     }
     const float sl2 = p.scale_log2;
     // a sink that is no logit (NaN, +inf) spoils the sum, not the reference
