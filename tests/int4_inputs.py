@@ -95,8 +95,9 @@ def assert_rows(got, want, what=""):
     with |q| < 6, s < 1 (rows of a few units, gains as in the tests), scale 1/8 each of
     the two is below 64 * 6 * 32 / 8 = 1536 and is off by at most some 64 * 2^-24 of that
     in the worst order, 2^-8 in all; the sums are random, so a hundredth of it is taken:
-    2^-14 absolute, which changes p by 2^-14 and the lse by as much.  The value's sums of
-    (16 + n) p s, from which (16 + z) p s is taken, are off by 2^-20 of 31 sum p s."""
+    2^-14 absolute, which changes p by 2^-14 and the lse by as much.  The value's
+    products are exact, and their fp32 sums, which tensor cores cut instead of rounding,
+    are off by less than 2^-20 of 31 sum p s."""
     out, lse = (np64(x) for x in got)
     ref, ref_lse, weight = want
     bar = 1.05 * 2.0**-8 * (weight + np.abs(ref)) + 2.0**-13 * weight + 2.0**-15

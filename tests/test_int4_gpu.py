@@ -654,3 +654,64 @@ def test_the_same_rows_again_and_slots_shared_between_requests():
     k, v = sa.gather_int4(cache, ints([int(c.slots[0][5])] * 3 + [-1, 16 * c.pages]))
     assert torch.equal(k[0], k[2]) and torch.equal(v[1], v[2]) and torch.isnan(k[3:]).all() and torch.isnan(v[3:]).all()
     assert (np64(k[0]) == c.k[0][5]).all()
+
+
+def test_pages_past_four_gigabytes():
+    q_lens = [70, 3, 1]
+    c = Packed([700, 90, 33], 16, 8, spare=0)
+    q, q1 = c.q(sum(q_lens)).to(DEV), c.q(3).to(DEV)
+    cache, table, lens, sinks, scale = c.gpu()
+    pages = 2**32 // (8 * sa.INT4_BLOCK_BYTES) + 5000
+    large = torch.empty(pages, 8, sa.INT4_BLOCK_BYTES, dtype=torch.uint8, device=DEV)
+    large[-c.pages:] = cache
+    far = torch.where(table >= 0, table + (pages - c.pages), table)
+    cu = ints(np.concatenate([[0], np.cumsum(q_lens)]))
+    slots = ints(c.slots[0][:50])
+
+    def everything(cache, table, first):
+        got = list(sa.decode_int4(q1, cache, table, lens, sinks, scale, 700))
+        got += sa.verify_int4(q[:6].view(3, 2, 16, 64), cache, table, lens, sinks, scale, 700)
+        got += sa.prefill_paged_int4(q, cu, cache, table, lens, sinks, scale, 70, 700)
+        got += sa.gather_int4(cache, slots + 16 * first)
+        qkv = q[:8].reshape(8, -1).repeat(1, 2)          # 16 + 2 * 8 heads
+        got += [sa.qkv_prologue_int4(qkv, None, ints(range(8)), slots[:8] + 16 * first,
+                                     torch.ones(8, 64, device=DEV), cache, 16, 8)]
+        return got + list(sa.gather_int4(cache, slots + 16 * first))
+
+    for a, b in zip(everything(large, far, pages - c.pages), everything(cache, table, 0)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_two_streams_with_a_workspace_each():
+    c, q_lens, q, cu = _parts_case(8)
+    want = _prefill_want(c, q, q_lens)
+    args, q_dev = c.gpu(), q.to(DEV)
+    q1 = c.q(len(q_lens))
+    want1 = _decode_want(c, q1)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.zeros(sa.int4_workspace_bytes(), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    q1_dev = q1.to(DEV)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(6):
+        for stream, ws in zip(streams, spaces):
+            got.append((sa.prefill_paged_int4(q_dev, cu, *args, 6, c.max_kv, workspace=ws, stream=stream),
+                        sa.decode_int4(q1_dev, *args, c.max_kv, workspace=ws, stream=stream)))
+    torch.cuda.synchronize()
+    for p, d in got:
+        assert_rows(p, want)
+        assert_rows(d, want1)
+
+
+@pytest.mark.parametrize("requests,hkv", [(33, 1), (100, 2), (700, 2)])
+def test_prompts_of_many_requests(requests, hkv):
+    rng = np.random.default_rng(requests)
+    q_lens = [int(x) for x in rng.integers(0, 6, requests)]
+    lens = [t + int(x) for t, x in zip(q_lens, rng.integers(0, 40, requests))]
+    q_lens[requests - 2], lens[requests - 2] = 4, 2604       # keys in parts where CTAs are few
+    q_lens[0], lens[0] = 0, 0
+    c = Packed(lens, 4 * hkv, hkv, seed=requests)
+    q = c.q(sum(q_lens))
+    cu = ints(np.concatenate([[0], np.cumsum(q_lens)]))
+    got = sa.prefill_paged_int4(q.to(DEV), cu, *c.gpu(), 40, c.max_kv)
+    assert_rows(got, _prefill_want(c, q, q_lens))
