@@ -64,6 +64,10 @@ constexpr int kUnpackWarp = 8, kUnpackWarps = kPages, kQkWarp = 16, kPvWarp = 17
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 168, kOtherRegs = 48;
 static_assert(2 * kSoftmaxRegs + 3 * kOtherRegs <= 5 * kLaunchRegs, "the split fits the launch's registers");
 constexpr int kBuffers = 3;                    // of scores in tensor memory
+// Requests up to which every warp counts through them by itself, 32 at a time, instead of
+// the CTA at once (us of either, prompts of 40..80 tokens: 100 requests 129 and 133, 200
+// 278 and 258, 1000 2416 and 1303).
+constexpr int kFewRequests = 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = kBuffers * kBN;      // behind the scores: 64 columns per tile
 constexpr int kPartTiles = kInt4PartKeys / kBN;        // that a part has at least
@@ -93,6 +97,8 @@ struct Bars {
   uint32_t tmem_base;
   int bad, last;
   int part_tiles, numbers;     // as plan_parts says
+  int seq, number;             // this CTA's request and its place in that
+  long long scan[kThreads / 32];
   uint64_t vis[2 * kBM];       // mask of a row
   int shared_by, part, first;  // of the CTAs that share these rows (kept here: registers are short)
 };
@@ -374,27 +380,66 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
   const int global = numbers - 1 - static_cast<int>(blockIdx.x / p.num_kv_heads);
   if (global < 0) return;
   int number = global, seq = -1;
-  for (int s0 = 0; s0 < p.num_seqs && seq < 0; s0 += 32) {
-    const int s = s0 + lane;
-    int mine = 0;
-    if (s < p.num_seqs) {
-      const Request r = request(p, s);
-      mine = request_ctas(r, tokens) * request_parts(r);
+  if (p.num_seqs <= kFewRequests) {                    // every warp by itself
+    for (int s0 = 0; s0 < p.num_seqs && seq < 0; s0 += 32) {
+      const int s = s0 + lane;
+      int mine = 0;
+      if (s < p.num_seqs) {
+        const Request r = request(p, s);
+        mine = request_ctas(r, tokens) * request_parts(r);
+      }
+      int upto = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += x;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, upto > number);
+      if (hit) {
+        const int at = __ffs(hit) - 1;
+        seq = s0 + at;
+        number -= __shfl_sync(0xffffffffu, upto - mine, at);
+      } else {
+        number -= __shfl_sync(0xffffffffu, upto, 31);
+      }
     }
-    int upto = mine;
+  } else {
+    // every thread counts the CTAs of a few requests in a row; the one in whose requests
+    // this CTA falls finds the very one
+    const int per = cdiv(p.num_seqs, kThreads), s0 = threadIdx.x * per, s1 = min(s0 + per, p.num_seqs);
+    auto ctas = [&](int s) {
+      const Request r = request(p, s);
+      return request_ctas(r, tokens) * request_parts(r);
+    };
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += ctas(s);
+    long long upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, off);
+      const long long x = __shfl_up_sync(0xffffffffu, upto, off);
       if (lane >= off) upto += x;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, upto > number);
-    if (hit) {
-      const int at = __ffs(hit) - 1;
-      seq = s0 + at;
-      number -= __shfl_sync(0xffffffffu, upto - mine, at);
-    } else {
-      number -= __shfl_sync(0xffffffffu, upto, 31);
+    if (lane == 31) bar.scan[warp] = upto;
+    if (threadIdx.x == 0) bar.seq = -1;
+    __syncthreads();
+    long long left = global - (upto - mine);           // CTAs from this thread's first on
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w)
+      if (w < warp) left -= bar.scan[w];
+    if (left >= 0 && left < mine) {
+      int s = s0;
+      while (true) {
+        const int n = ctas(s);
+        if (left < n) break;
+        left -= n;
+        ++s;
+      }
+      bar.seq = s;
+      bar.number = static_cast<int>(left);
     }
+    __syncthreads();
+    seq = bar.seq;
+    number = bar.number;
   }
   if (seq < 0) return;                                 // fewer than the host allowed for
   const Request rq = request(p, seq);

@@ -703,7 +703,7 @@ def test_two_streams_with_a_workspace_each():
         assert_rows(d, want1)
 
 
-@pytest.mark.parametrize("requests,hkv", [(33, 1), (100, 2), (700, 2)])
+@pytest.mark.parametrize("requests,hkv", [(33, 1), (100, 2), (200, 1), (700, 2)])
 def test_prompts_of_many_requests(requests, hkv):
     rng = np.random.default_rng(requests)
     q_lens = [int(x) for x in rng.integers(0, 6, requests)]
