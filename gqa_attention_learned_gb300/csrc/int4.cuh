@@ -89,7 +89,9 @@ cudaError_t launch_int4_decode(const Int4AttnParams &p, Int4Mode mode, int row_b
 // Tensor-core form: for groups of at most 128 heads.  Tokens of a CTA; CTAs for one
 // KV head are at most total_q / tokens + num_seqs.
 int int4_prefill_tokens(int group);
-constexpr int kInt4PartKeys = 512;       // keys that a part has at least
+// Keys that a part has at least (8 tokens on 4000 keys: 32.6 us at 256, 31.4 at 512, 32.9
+// at 1024, 37.9 at 2048).
+constexpr int kInt4PartKeys = 512;
 size_t int4_prefill_results_bytes(int ctas);     // of ws_o and ws_md
 cudaError_t launch_int4_prefill(const Int4AttnParams &p, long long ctas, cudaStream_t stream);
 

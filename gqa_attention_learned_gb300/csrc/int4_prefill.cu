@@ -30,15 +30,17 @@
 // many as make the least time (plan_parts()), each at least 512 keys long.  Parts join by
 // log-sum-exp through the workspace, by the last one to get there, in the keys' order.
 //
-// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1357 us, 1013 TFLOP/s,
-// where the kernel of the bf16 cache does 1046): the chain score - exponentials - P V of the two tiles
-// in turn.  P V of 128 x 64 x 128 from tensor memory takes about twice its arithmetic's
-// time, and start and end of a CTA some 5 us.  Measured on the way: one tile per CTA 1839
-// us; eight unpacking warps, two score buffers 1692; three buffers and a ring of packed
-// pages 1555; softmax warps with 168 registers, sleeping waits 1537; products started by
-// polling warps 1485; a row's mask as bits 1376; fewer spills 1357.  Slower or no better: 16 softmax warps
-// with half a row each; products started by one thread that walks the tiles alone (1558
-// against 1482); persistent CTAs (1720: spills); four stages of K and V.
+// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1357 us, 1013 TFLOP/s, where
+// the kernel of the bf16 cache does 1046): the chain score - exponentials - P V of the two
+// tiles in turn.  P V of 128 x 64 x 128 from tensor memory takes about twice its
+// arithmetic's time, and start and end of a CTA some 5 us.  Measured on the way: one tile
+// per CTA 1839 us; eight unpacking warps, two score buffers 1692; three buffers and a ring
+// of packed pages 1555; softmax warps with 168 registers, sleeping waits 1537; products
+// started by polling warps 1485; a row's mask as bits 1376; fewer spills 1357.  Slower or
+// no better: 16 softmax warps with half a row each; products started by one thread that
+// walks the tiles alone (1558 against 1482); persistent CTAs (1720: spills); four stages
+// of K and V; both halves of a CTA on one query tile where there is one only (64 rows 1%
+// faster, full tiles 3% slower).
 //
 // A value row that is not finite must spoil the rows that see it and no others, but
 // 0 * NaN in P V would spoil the whole tile: such a value is stored as zero and its key
@@ -71,7 +73,9 @@ constexpr int kFewRequests = 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = kBuffers * kBN;      // behind the scores: 64 columns per tile
 constexpr int kPartTiles = kInt4PartKeys / kBN;        // that a part has at least
-constexpr float kPartCost = 14.f;               // what a part costs beyond its tiles, in tiles
+// What a part costs beyond its tiles, in tiles (4 x 128 tokens on 4000..16000 keys: 183 us
+// at 8, 170 at 14, 189 at 20, when an edge still cost three times as much).
+constexpr float kPartCost = 14.f;
 constexpr float kUnset = -8e37f;               // reference of a row that has seen no key yet
 constexpr float kMostSum = 1024.f;             // sum of a tile's P from which the reference is moved
 
