@@ -544,7 +544,8 @@ int4_decode_kernel(const __grid_constant__ Int4AttnParams p) {
 
     for (int page = first_page; page < seg_end; page += kStepPages) {
       const int st = done % kStages;
-      if (!dead && !mbar_wait(&sh.bars[warp][st], (done / kStages) & 1)) {
+      // (one answer for all lanes: at the limit some may see the phase and others not)
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&sh.bars[warp][st], (done / kStages) & 1))) {
         // a copy never landed: let the others in flight land (with the same limit)
         // before their stages are used otherwise, and start no more
         dead = bad = true;
