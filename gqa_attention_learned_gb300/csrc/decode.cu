@@ -392,7 +392,8 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
   for (int i = 0; i < n_my; ++i) {
     const int st = i % kStages;
-    if (!mbar_wait(&bars[st], (i / kStages) & 1)) {
+    // (one answer for all lanes: at the limit some may see the phase and others not)
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars[st], (i / kStages) & 1))) {
       // A copy never landed: report, then drain (bounded) whatever else this
       // warp still has in flight before the stages are reused below.
       lane_bad = true;
