@@ -141,6 +141,20 @@ __device__ __forceinline__ int request_ctas(const Request &r, int tokens) {
   return r.bad ? 1 : cdiv(r.q_len, tokens);
 }
 
+// Rows of `tokens` tokens from `token` on become NaN, as far as they lie inside the
+// buffers (the whole CTA calls).
+__device__ __forceinline__ void spoil_rows(const Int4AttnParams &p, int kvh, int token, int tokens) {
+  if (token < 0 || token >= p.total_q) return;
+  const int rows = min(max(tokens, 0), p.total_q - token) * p.group;
+  for (int i = threadIdx.x; i < rows; i += kThreads) {
+    const size_t row = static_cast<size_t>(token + i / p.group) * p.num_qo_heads + kvh * p.group + i % p.group;
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kHeadDim);
+#pragma unroll
+    for (int c = 0; c < kHeadDim / 8; ++c) dst[c] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+    if (p.lse) p.lse[row] = NAN;
+  }
+}
+
 // A row's keys [0, limit), and the draft keys from `draft` on by the bits of *vis (in
 // shared memory, registers are short; null: none).
 struct Seen {
@@ -367,17 +381,19 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
   const int kvh = static_cast<int>(blockIdx.x % p.num_kv_heads);
   int numbers = static_cast<int>(gridDim.x / p.num_kv_heads);
   int part_tiles = 0;                                  // key tiles that a part has about
+  bool leftover = p.cu_seqlens_q != nullptr;           // whether there may be more blocks than CTAs
   if constexpr (kSplit) {
     if (warp == 0) {
       const int2 plan = plan_parts(p, tokens, lane);
       if (lane == 0) {
         bar.part_tiles = plan.x;
-        bar.numbers = min(plan.y, numbers);
+        bar.numbers = plan.y;
       }
     }
     __syncthreads();
     part_tiles = bar.part_tiles;
-    numbers = bar.numbers;
+    leftover = leftover && bar.numbers > numbers;      // (a plan has counted them)
+    numbers = min(bar.numbers, numbers);
   }
   // parts of a request's every token block
   auto request_parts = [&](const Request &r) { return kSplit && !r.bad ? max(1, cdiv(cdiv(r.kv_len, kBN), part_tiles)) : 1; };
@@ -447,20 +463,22 @@ int4_prefill_kernel(const __grid_constant__ Int4AttnParams p) {
   }
   if (seq < 0) return;                                 // fewer than the host allowed for
   const Request rq = request(p, seq);
-  if (rq.bad) {
-    // this request's rows, as far as they lie inside the buffers
-    if (rq.q_start < 0 || rq.q_start >= p.total_q) return;
-    const int rows = min(max(rq.q_len, 0), p.total_q - rq.q_start) * p.group;
-    for (int i = threadIdx.x; i < rows; i += kThreads) {
-      const size_t row = static_cast<size_t>(rq.q_start + i / p.group) * p.num_qo_heads + kvh * p.group + i % p.group;
-      uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kHeadDim);
-#pragma unroll
-      for (int c = 0; c < kHeadDim / 8; ++c) dst[c] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-      if (p.lse) p.lse[row] = NAN;
+  const int parts = request_parts(rq);
+  if (leftover && global == numbers - 1) {
+    // Sequences that fall back and overlap can hold more rows than the launch has CTAs
+    // for: nobody comes to those behind this CTA's, and they become NaN.  (Of prefix sums
+    // there are none: a CTA with this number then has the last rows of all, if it has any.)
+    const int done = rq.bad ? rq.q_len : (number / parts + 1) * tokens;
+    if (done < rq.q_len) spoil_rows(p, kvh, rq.q_start + done, rq.q_len - done);
+    for (int s = seq + 1; s < p.num_seqs; ++s) {
+      const Request r = request(p, s);
+      spoil_rows(p, kvh, r.q_start, r.q_len);
     }
+  }
+  if (rq.bad) {
+    spoil_rows(p, kvh, rq.q_start, rq.q_len);
     return;
   }
-  const int parts = request_parts(rq);
   const int part = kSplit ? number % parts : 0;
   const int tok0 = (kSplit ? number / parts : number) * tokens;      // first token of this CTA
   const int shift = rq.kv_len - rq.q_len;              // keys before the new tokens

@@ -634,7 +634,10 @@ SINKATTN_API int sinkattn_verify_int4(const void *q, const void *kv_cache,
                           int max_kv_len, void *workspace, size_t workspace_bytes,
                           int launch_flags, void *stream);
 
-/* sinkattn_prefill_paged over such a cache (the new tokens' keys in it too). */
+/* sinkattn_prefill_paged over such a cache (the new tokens' keys in it too).  Where
+ * cu_seqlens_q falls back, sequences after it may share rows: such a row is that of any
+ * of them, or NaN.  If they hold more rows together than there are, the last ones'
+ * may be NaN, too. */
 SINKATTN_API int sinkattn_prefill_paged_int4(const void *q, const int32_t *cu_seqlens_q,
                           int num_seqs, int total_q, int max_q_len,
                           const void *kv_cache, const int32_t *page_table,

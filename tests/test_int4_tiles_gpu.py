@@ -1,0 +1,143 @@
+"""Attention over a paged cache held in 4 bits: what odd sequences ask of the host's plan.
+
+Compared with float64 on the GPU over what the cache stands for (`gather_int4`, whose
+rows tests/test_int4_gpu.py compares with the format's, exactly)."""
+
+import numpy as np
+import pytest
+import torch
+
+import gqa_attention_learned_gb300 as sa
+from gqa_attention_learned_gb300 import workloads
+from int4_inputs import DEV
+
+pytestmark = pytest.mark.gpu
+
+COUNTERS = 16384                 # bytes that a workspace begins with
+SLOT = 256 * 64 * 4              # bytes of one CTA's sums after them (more than 32 rows per KV head)
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+class Batch:
+    """Requests of kv_lens keys, of which the last q_lens are new tokens, on shuffled
+    pages; keys grow by e^gain from a request's first to its last.  Free slots hold
+    bytes of 255 (scales that are NaN)."""
+
+    def __init__(self, q_lens, kv_lens, hq, hkv, seed=0, gain=0.0, sinks=True):
+        self.q_lens, self.kv_lens, self.hq, self.hkv = q_lens, kv_lens, hq, hkv
+        gen = torch.Generator(DEV).manual_seed(seed)
+        need = [-(-n // 16) for n in kv_lens]
+        pages = sum(need) + 3
+        ids = torch.randperm(pages, generator=gen, device=DEV).int()
+        self.table = torch.full((len(kv_lens), max(need + [1])), -1, dtype=torch.int32, device=DEV)
+        self.cache = torch.full((pages, hkv, sa.INT4_BLOCK_BYTES), 255, dtype=torch.uint8, device=DEV)
+        self.slots, at = [], 0
+        rope = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).to(DEV)       # no rotation
+        for b, n in enumerate(kv_lens):
+            self.table[b, :need[b]] = mine = ids[at:at + need[b]]
+            at += need[b]
+            j = torch.arange(n, device=DEV)
+            slots = (mine[j // 16] * 16 + j % 16).int()
+            kv = torch.randn(n, 2, hkv, 64, generator=gen, device=DEV)
+            kv[:, 0] *= torch.exp(gain * j / max(n - 1, 1))[:, None, None]
+            kv[:, 1] += 0.25
+            qkv = torch.cat([torch.zeros(n, 64, device=DEV), kv.flatten(1)], 1).bfloat16()
+            sa.qkv_prologue_int4(qkv, None, torch.zeros_like(slots), slots, rope, self.cache, 1, hkv)
+            self.slots.append(slots)
+        self.lens = ints(kv_lens)
+        self.cu = ints(np.concatenate([[0], np.cumsum(q_lens)]))
+        self.q = torch.randn(sum(q_lens), hq, 64, generator=gen, device=DEV).bfloat16()
+        self.sinks = 2 * torch.randn(hq, generator=gen, device=DEV) if sinks else torch.full((hq,), -torch.inf, device=DEV)
+        self.scale = 0.125
+        self.args = (self.cache, self.table, self.lens, self.sinks, self.scale)
+
+    def attend(self, max_q=None, max_kv=None, **kw):
+        return sa.prefill_paged_int4(self.q, self.cu, *self.args, max_q or max(self.q_lens),
+                                     max_kv or max(self.kv_lens), **kw)
+
+    def check(self, got, masks=None, few=False):
+        """Every row against float64.  Where the bars come from: the weights are rounded to
+        bf16 (2^-8 of their value at most) and the output once more; 5% on top for the second
+        order.  A score is an fp32 sum of 64 exact products, each addition cut at 2^-23 of what
+        there is by then: off by at most d = 2^-17 scale sum |q k|.  The kernel of few rows
+        (`few`) adds up q (16 + n), takes (16 + z) sum q off it and multiplies by the step s:
+        2^-17 for either, of 31 s sum |q|; s is at most 0.15 of the row's largest number
+        before quantisation, which its largest value reaches within s: s <= max |k| / 5.6.  Scores
+        off by d move the output by sum p |v| d + sum p |v| sum p d, and the lse by sum p d.
+        2^-13 for what fp32 adds over some thousand keys (16 at a time, each time cut at 2^-23:
+        2^-14 for 8192) and the exponential (2^-22, its argument below 64 rounded at 2^-24)."""
+        out, lse = (x.double().reshape(-1, *x.shape[-k:]) for x, k in zip(got, (2, 1)))
+        assert torch.isfinite(out).all()
+        at = 0
+        for b, (t, n) in enumerate(zip(self.q_lens, self.kv_lens)):
+            if t == 0:
+                continue
+            k, v = (x.double().repeat_interleave(self.hq // self.hkv, 1) for x in sa.gather_int4(self.cache, self.slots[b]))
+            q = self.q[at:at + t].double()
+            seen = torch.arange(n, device=DEV) <= n - t + torch.arange(t, device=DEV)[:, None]
+            if masks is not None:
+                bits = masks[b][:, None] >> torch.arange(t, device=DEV) & 1
+                seen[:, n - t:] = bits.bool()
+            s = self.scale * torch.einsum("ihd,jhd->hij", q, k)
+            s.masked_fill_(~seen, -torch.inf)
+            sink = self.sinks.double()[:, None]
+            top = torch.logaddexp(torch.logsumexp(s, 2), sink)
+            p = torch.exp(s - top[:, :, None])
+            ref, weight = (torch.einsum("hij,jhd->ihd", p, x) for x in (v, v.abs()))
+            if few:
+                d = 2.0**-16 * self.scale * 31 * torch.einsum("ih,jh->hij", q.abs().sum(2), k.abs().amax(2) / 5.6)
+            else:
+                d = 2.0**-17 * self.scale * torch.einsum("ihd,jhd->hij", q.abs(), k.abs())
+            p *= d
+            moved, d = torch.einsum("hij,jhd->ihd", p, v.abs()), p.sum(2).T
+            bar = 1.05 * 2.0**-8 * (weight + ref.abs()) + 2.0**-13 * weight + moved + d[:, :, None] * weight
+            err = (out[at:at + t] - ref).abs()
+            assert (err <= bar).all(), f"request {b}: {(err / bar).max():.2f} of the bar"
+            off = (lse[at:at + t] - top.T).abs()
+            assert (off <= d + 2.0**-13).all(), f"request {b}: lse off by {off.max():.1e}"
+            at += t
+
+
+def workspace():
+    """Zeros where a workspace has to hold them, a pattern in the rest."""
+    w = torch.full((sa.int4_workspace_bytes(),), 0x5A, dtype=torch.uint8, device=DEV)
+    w[:COUNTERS] = 0
+    return w
+
+
+def parts(w):
+    """CTAs that left sums in a workspace; its counters are zero again."""
+    assert not w[:COUNTERS].any()
+    rest = w[COUNTERS:]
+    rest = rest[:rest.numel() // SLOT * SLOT].view(-1, SLOT)
+    return int((rest != 0x5A).any(1).sum())
+
+
+def sms():
+    return torch.cuda.get_device_properties(DEV).multi_processor_count
+
+
+@pytest.mark.parametrize("times", [10, 60])
+def test_rows_of_sequences_that_overlap_are_written(times):
+    # sequences that fall back again and again hold more rows than there are, more than
+    # the launch has CTAs for; the one behind them is right or NaN, and no row is left
+    # as it was
+    b = Batch([40], [200], 16, 2, seed=8)
+    starts = [0, 40, 0] * times + [0, 40, 80]
+    n = len(starts) - 1
+    table, lens = b.table.repeat(n, 1), ints([200] * n)
+    q = torch.cat([b.q, b.q, b.q[:5]])
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    w = workspace()
+    sa.prefill_paged_int4(q, ints(starts), b.cache, table, lens, b.sinks, b.scale, 40, 200, out=out, lse=lse, workspace=w)
+    assert (out[80:] == 7).all() and (lse[80:] == 7).all()
+    want = b.attend()
+    b.check(want)
+    for rows in (slice(0, 40), slice(40, 80)):
+        for got, ref in zip((out, lse), want):
+            assert ((got[rows] == ref) | torch.isnan(got[rows])).all()
+    assert parts(w) == 0
