@@ -77,6 +77,7 @@ int attention_entry(sa::Int4Mode mode, const void *q, const int32_t *cu_seqlens_
   // rows and units are counted in ints
   if (static_cast<long long>(num_qo_heads) * std::max(total_q, num_seqs) > 0x7fffff00ll)
     return SINKATTN_UNSUPPORTED;
+  max_q_len = std::min(max_q_len, total_q);            // bounds may be loose
   const int sms = sa::api_sm_count();
   if (sms == 0) return sa::api_failure("no CUDA device (SM count query failed)");
   if (!workspace || workspace_bytes < workspace_for(sms)) return SINKATTN_WORKSPACE_TOO_SMALL;
@@ -132,9 +133,13 @@ int attention_entry(sa::Int4Mode mode, const void *q, const int32_t *cu_seqlens_
   const int blocks = sa::int4_row_blocks(rows);
   const int slots = sms * sa::int4_decode_ctas_per_sm(blocks);
   const long long pages = std::max(1ll, std::min<long long>(ceil_div(p.max_kv_len, kPageSize), max_pages_per_seq));
-  // (as a double: the product of loose bounds need not fit an integer)
-  const double work = static_cast<double>(num_seqs) * num_kv_heads * static_cast<double>(pages) *
-                      static_cast<double>(ceil_div(static_cast<long long>(max_q_len) * p.group, 8 * blocks));
+  // Row blocks of a KV head: of the longest requests, or of all tokens, which leave each
+  // request a block that is not full.  (As a double: the product of loose bounds need not
+  // fit an integer.)
+  const double row_blocks =
+      std::min(static_cast<double>(num_seqs) * ceil_div(static_cast<long long>(max_q_len) * p.group, 8 * blocks),
+               static_cast<double>(total_q) * p.group / (8 * blocks) + num_seqs);
+  const double work = row_blocks * num_kv_heads * static_cast<double>(pages);
   const int ctas = static_cast<int>(std::max(1.0, std::min<double>(slots, std::ceil(work / (8.0 * kMinPages)))));
   // a warp counts its share of the pages, and a unit's start as 8, in ints
   if (work * (1 + 8.0) / (8.0 * ctas) > 0x7f000000) return SINKATTN_UNSUPPORTED;

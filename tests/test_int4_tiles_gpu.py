@@ -1,4 +1,5 @@
-"""Attention over a paged cache held in 4 bits: what odd sequences ask of the host's plan.
+"""Attention over a paged cache held in 4 bits: what loose bounds and odd
+sequences ask of the host's plan.
 
 Compared with float64 on the GPU over what the cache stands for (`gather_int4`, whose
 rows tests/test_int4_gpu.py compares with the format's, exactly)."""
@@ -118,6 +119,25 @@ def parts(w):
 
 def sms():
     return torch.cuda.get_device_properties(DEV).multi_processor_count
+
+
+@pytest.mark.parametrize("heads", [(256, 1), (512, 2), (64, 8)])
+def test_bounds_on_new_tokens_need_not_be_tight(heads):
+    # groups of more than 128 heads have a kernel of their own, whatever the rows
+    b = Batch([3, 0, 2], [400, 20, 18], *heads, seed=7)
+    for max_q in (3, 5, 100, 100000, 2**40):
+        b.check(b.attend(max_q=max_q, max_kv=2**40), few=True)
+
+
+def test_many_prompts_of_a_large_group():
+    # row blocks are few beside requests times the longest of them, and the page table is wide
+    q_lens = [1, 700] + [1] * 300
+    b = Batch(q_lens, [t + 20 for t in q_lens], 256, 1, seed=10)
+    wide = torch.full((len(q_lens), 200000), -1, dtype=torch.int32, device=DEV)
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    b.args = (b.cache, wide, *b.args[2:])
+    b.check(b.attend(max_kv=2**40), few=True)
 
 
 @pytest.mark.parametrize("times", [10, 60])
