@@ -348,7 +348,8 @@ __device__ __forceinline__ int2 plan_parts(const Int4AttnParams &p, int tokens, 
       ++bad;
       continue;
     }
-    const int tiles = cdiv(r.kv_len, kBN), cut = max(1, cdiv(tiles, mine));
+    // (the keys of a request without new tokens are nobody's work)
+    const int tiles = r.q_len > 0 ? cdiv(r.kv_len, kBN) : 0, cut = max(1, cdiv(tiles, mine));
     n += request_ctas(r, tokens) * cut;
     longest = max(longest, cdiv(tiles, cut));
   }

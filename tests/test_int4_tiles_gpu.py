@@ -1,5 +1,5 @@
-"""Attention over a paged cache held in 4 bits: what loose bounds and odd
-sequences ask of the host's plan.
+"""Attention over a paged cache held in 4 bits: requests without new tokens,
+and what loose bounds and odd sequences ask of the plan.
 
 Compared with float64 on the GPU over what the cache stands for (`gather_int4`, whose
 rows tests/test_int4_gpu.py compares with the format's, exactly)."""
@@ -119,6 +119,20 @@ def parts(w):
 
 def sms():
     return torch.cuda.get_device_properties(DEV).multi_processor_count
+
+
+def test_requests_without_new_tokens_are_no_work():
+    # 20 short requests want no parts, however long the cache of one that is idle
+    q_lens, kv_lens = [6] * 20 + [0] + [6] * 4, [1000] * 20 + [100000] + [700] * 4
+    b = Batch(q_lens, kv_lens, 16, 2, seed=6)
+    keep = [i for i in range(25) if i != 20]
+    w = workspace()
+    got = b.attend(workspace=w)
+    assert parts(w) == 0
+    b.check(got)
+    alone = sa.prefill_paged_int4(b.q, ints(6 * np.arange(25)), b.cache, b.table[keep].contiguous(),
+                                  b.lens[keep].contiguous(), b.sinks, b.scale, 6, 1000)
+    assert all(torch.equal(x, y) for x, y in zip(got, alone))
 
 
 @pytest.mark.parametrize("heads", [(256, 1), (512, 2), (64, 8)])
