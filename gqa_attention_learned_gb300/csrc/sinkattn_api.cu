@@ -279,10 +279,6 @@ namespace sa {
 int api_sm_count() { return device_sm_count(); }
 int api_status(cudaError_t err, const char *where) { return cuda_status(err, where); }
 int api_failure(const char *what) { return fail_msg(what); }
-bool api_encode_map(CUtensorMap *map, const void *base, unsigned long long d1, unsigned long long d2,
-                    unsigned b1, unsigned b2) {
-  return encode_map(map, base, d1, d2, b1, b2);
-}
 
 std::atomic<int> g_programmatic{0};
 
