@@ -550,8 +550,8 @@ SINKATTN_API int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *pag
  *     n  = clamp(rint(x / s) + z, 0, 15)           (rint: ties to even)
  * and stands for s * (n - z), which is always a bf16 number: every operator here
  * computes what its bf16 counterpart computes on a cache of these values.  A row
- * whose range is not finite stands for 64 NaN.  x is taken in fp32.  (Of a range above
- * 2^127 the largest values may be infinite.)
+ * whose range (hi - lo in fp32) is not finite stands for 64 NaN, any other for finite
+ * values: s is at most 1.125 * 2^124, where |n - z| is at most 14.  x is taken in fp32.
  *
  * Layout of a block (one page, one KV head), slot j = 0..15, 32-bit words,
  * little endian:
@@ -569,7 +569,9 @@ SINKATTN_API int sinkattn_evict(void *k_cache, void *v_cache, const int32_t *pag
  * Page tables, lengths, sinks, scale, out and lse are as for the bf16 cache, and
  * so is what becomes NaN.  A sink that is NaN or +inf makes its head's rows NaN.
  * A value row that stands for NaN makes the out of the rows that see it NaN, and
- * may make their lse NaN, too.
+ * may make their lse NaN, too.  Weights are summed up against a reference that they
+ * may exceed 2^10 times, and divided at the end: out of a request of n keys is finite
+ * where 2^10 n max |v| is below 2^128.
  *
  * The attention calls need a workspace of sinkattn_int4_workspace_bytes (about
  * 50 MB), whatever their sizes: 256-byte aligned and ZERO-FILLED BEFORE ITS FIRST

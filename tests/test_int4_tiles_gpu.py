@@ -1,5 +1,5 @@
 """Attention over a paged cache held in 4 bits: requests without new tokens,
-and what loose bounds and odd sequences ask of the plan.
+and what loose bounds and odd sequences ask of the plan; and the largest values.
 
 Compared with float64 on the GPU over what the cache stands for (`gather_int4`, whose
 rows tests/test_int4_gpu.py compares with the format's, exactly)."""
@@ -11,6 +11,8 @@ import torch
 import gqa_attention_learned_gb300 as sa
 from gqa_attention_learned_gb300 import workloads
 from int4_inputs import DEV
+from oracle import int4
+from test_int4_range_cpu import rows_at_the_top
 
 pytestmark = pytest.mark.gpu
 
@@ -27,7 +29,7 @@ class Batch:
     pages; keys grow by e^gain from a request's first to its last.  Free slots hold
     bytes of 255 (scales that are NaN)."""
 
-    def __init__(self, q_lens, kv_lens, hq, hkv, seed=0, gain=0.0, sinks=True):
+    def __init__(self, q_lens, kv_lens, hq, hkv, seed=0, gain=0.0, sinks=True, v_gain=1.0):
         self.q_lens, self.kv_lens, self.hq, self.hkv = q_lens, kv_lens, hq, hkv
         gen = torch.Generator(DEV).manual_seed(seed)
         need = [-(-n // 16) for n in kv_lens]
@@ -44,7 +46,7 @@ class Batch:
             slots = (mine[j // 16] * 16 + j % 16).int()
             kv = torch.randn(n, 2, hkv, 64, generator=gen, device=DEV)
             kv[:, 0] *= torch.exp(gain * j / max(n - 1, 1))[:, None, None]
-            kv[:, 1] += 0.25
+            kv[:, 1] = v_gain * (kv[:, 1] + 0.25)
             qkv = torch.cat([torch.zeros(n, 64, device=DEV), kv.flatten(1)], 1).bfloat16()
             sa.qkv_prologue_int4(qkv, None, torch.zeros_like(slots), slots, rope, self.cache, 1, hkv)
             self.slots.append(slots)
@@ -175,3 +177,38 @@ def test_rows_of_sequences_that_overlap_are_written(times):
         for got, ref in zip((out, lse), want):
             assert ((got[rows] == ref) | torch.isnan(got[rows])).all()
     assert parts(w) == 0
+
+
+# ------------------------------------------------------------------ large values
+def test_rows_at_the_top_of_the_range():
+    # what the format says, and no value that is not finite
+    with np.errstate(over="ignore"):
+        x = torch.from_numpy(rows_at_the_top(600)).bfloat16()
+        y = x.float().numpy()
+        fine = np.isfinite(y).all(-1) & np.isfinite(np.maximum(y.max(-1), 0) - np.minimum(y.min(-1), 0))
+    rope = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).to(DEV)
+    cache = sa.int4_cache(40, 1, DEV)
+    qkv = torch.cat([torch.zeros_like(x), torch.zeros_like(x), x], 1).to(DEV)
+    slots = ints(range(600))
+    sa.qkv_prologue_int4(qkv, None, torch.zeros_like(slots), slots, rope, cache, 1, 1)
+    v = sa.gather_int4(cache, slots)[1][:, 0].float().cpu().numpy()
+    assert fine.sum() > 500 and np.isfinite(v[fine]).all() and np.isnan(v[~fine]).all()
+    np.testing.assert_array_equal(v[fine], int4.round_trip(y[fine]).astype(np.float32))
+
+
+@pytest.mark.parametrize("tokens", [1, 3, 40])           # one row, few rows, tensor cores
+def test_large_values_are_summed_without_overflow(tokens):
+    # values 2^105 times as large give outputs 2^105 times as large, bit for bit: weights
+    # below 2^10, 300 keys and values below 2^3 make sums below 2^(105 + 10 + 9 + 3)
+    got = []
+    for v_gain in (1.0, 2.0**105):
+        b = Batch([tokens] * 2, [300, 250], 16, 2, seed=11, v_gain=v_gain)
+        calls = [b.attend(), sa.verify_int4(b.q.view(2, tokens, 16, 64), *b.args, 300)]
+        if tokens == 1:
+            calls.append(sa.decode_int4(b.q, *b.args, 300))
+        got.append([x for call in calls for x in call])
+    for small, large in zip(*got):
+        if small.dtype == torch.bfloat16:
+            assert torch.isfinite(large).all() and torch.equal(small.double() * 2.0**105, large.double())
+        else:
+            assert torch.equal(small, large)
