@@ -125,8 +125,9 @@ def status_string(status):
 
 def set_programmatic_launch(enable):
     """Process-wide DEFAULT launch mode of the decode and verification
-    kernels (decode, decode_static_scratch, verify called without
-    `programmatic=`); returns the previous setting.  In programmatic mode,
+    kernels (decode, decode_static_scratch, verify, decode_int4, verify_int4 of up
+    to 32 rows per KV head, called without `programmatic=`); returns the previous
+    setting.  In programmatic mode,
     kv_lens and page_table of a call must not be written by the kernel
     launched just before it on the stream."""
     return bool(load().sinkattn_set_programmatic_launch(1 if enable else 0))
@@ -895,8 +896,9 @@ def decode_int4(q, kv_cache, page_table, kv_lens, sinks, scale, max_kv_len, *, o
 def verify_int4(q, kv_cache, page_table, kv_lens, sinks, scale, max_kv_len, *, tree_mask=None, out=None,
                 lse=None, workspace=None, stream=None, want_lse=True, programmatic=None):
     """`verify` over a cache held in 4 bits.  q [B, q_len, Hq, 64] bf16; tree_mask and
-    the order of tokens as for `verify`, workspace as for `decode_int4`.  Returns
-    (out [B, q_len, Hq, 64], lse [B, q_len, Hq])."""
+    the order of tokens as for `verify`, workspace as for `decode_int4`.  programmatic
+    as for `verify` up to 32 rows (q_len times the group) per KV head; above, this call
+    is an ordinary launch.  Returns (out [B, q_len, Hq, 64], lse [B, q_len, Hq])."""
     batch, q_len, hq, d = q.shape
     _int4_args(q, 4, kv_cache, page_table, kv_lens, sinks, batch)
     if tree_mask is not None:

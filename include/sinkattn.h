@@ -95,7 +95,8 @@ SINKATTN_API int sinkattn_version(void);
  * Programmatic dependent launch of the decode and verification kernels
  * (sinkattn_decode, sinkattn_decode_static_scratch, both routes of
  * sinkattn_verify, and the _ex entry points given SINKATTN_LAUNCH_DEFAULT;
- * prefill is unaffected).  This sets the process-wide DEFAULT, off at load;
+ * over a cache held in 4 bits sinkattn_decode_int4, and sinkattn_verify_int4 of
+ * at most 32 rows per KV head; prefill is unaffected).  This sets the process-wide DEFAULT, off at load;
  * returns the previous setting.  A caller that shares the process with other
  * users of the library should pass its mode per call (the _ex entry points)
  * instead of changing the default.  In programmatic mode a kernel may be scheduled
@@ -626,7 +627,9 @@ SINKATTN_API int sinkattn_decode_int4(const void *q, const void *kv_cache,
                           int num_pages, int max_kv_len, void *workspace,
                           size_t workspace_bytes, int launch_flags, void *stream);
 
-/* sinkattn_verify_ex over such a cache. */
+/* sinkattn_verify_ex over such a cache.  Of more than 32 rows per KV head (q_len
+ * times the group, a group of at most 128 heads) it is an ordinary launch, whatever
+ * launch_flags and the process-wide default ask for. */
 SINKATTN_API int sinkattn_verify_int4(const void *q, const void *kv_cache,
                           const int32_t *page_table, int max_pages_per_seq,
                           const int32_t *kv_lens, const uint64_t *tree_mask,

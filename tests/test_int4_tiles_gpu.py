@@ -179,6 +179,22 @@ def test_rows_of_sequences_that_overlap_are_written(times):
     assert parts(w) == 0
 
 
+def test_verification_of_many_rows_after_the_kernel_that_writes_its_queries():
+    # the launch mode is the caller's to ask for; above 32 rows per KV head there is one only
+    b = Batch([8] * 4, [2000, 8, 500, 1300], 64, 8, seed=9)
+    q = b.q.view(4, 8, 64, 64)
+    want = sa.verify_int4(q, *b.args, 2000, programmatic=False)
+    b.check(want)
+    rope = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).to(DEV)
+    qkv = torch.cat([b.q, torch.zeros(32, 16, 64, device=DEV).bfloat16()], 1).flatten(1)
+    w = workspace()
+    for _ in range(20):
+        made = torch.full_like(b.q, float("nan"))
+        sa.qkv_prologue_int4(qkv, None, ints([0] * 32), ints([-1] * 32), rope, b.cache, 64, 8, q_out=made)
+        got = sa.verify_int4(made.view_as(q), *b.args, 2000, programmatic=True, workspace=w)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 # ------------------------------------------------------------------ large values
 def test_rows_at_the_top_of_the_range():
     # what the format says, and no value that is not finite
