@@ -1,5 +1,7 @@
-"""Attention over a paged cache held in 4 bits: requests without new tokens,
-and what loose bounds and odd sequences ask of the plan; and the largest values.
+"""Attention over a paged cache held in 4 bits where its kernels' rings go round: prompts
+of many key tiles with both query tiles in use, long parts; batches with requests that
+have no new tokens, what loose bounds and odd sequences ask of the plan, and the largest
+values.
 
 Compared with float64 on the GPU over what the cache stands for (`gather_int4`, whose
 rows tests/test_int4_gpu.py compares with the format's, exactly)."""
@@ -123,6 +125,83 @@ def sms():
     return torch.cuda.get_device_properties(DEV).multi_processor_count
 
 
+# A CTA takes 2 * (128 // group) tokens; calls with more than two CTAs per SM are not cut
+# into parts.  16 tokens to a query tile: prefixes of 16 mod 32 put every fourth CTA's
+# tiles on both sides of a key tile's end, so that the second has one more.
+@pytest.mark.parametrize("q_lens,prefix,heads", [([1300], [1488], (64, 8)), ([1290, 45], [1500, 2000], (64, 8)),
+                                                 ([700], [1700], (128, 1)), ([5000], [0], (8, 8)),
+                                                 ([2001], [1600], (48, 8))])
+@pytest.mark.parametrize("gain", [0.0, 2.0])
+def test_prompts_of_many_key_tiles(q_lens, prefix, heads, gain):
+    tokens = 2 * (128 // (heads[0] // heads[1]))
+    blocks = sum(-(-t // tokens) for t in q_lens)
+    if heads != (8, 8):
+        assert blocks * heads[1] > 2 * sms()             # not in parts
+    b = Batch(q_lens, [t + p for t, p in zip(q_lens, prefix)], *heads, seed=1, gain=gain)
+    w = workspace()
+    got = b.attend(workspace=w)
+    assert heads == (8, 8) or parts(w) == 0
+    b.check(got)
+    again = b.attend(workspace=w, max_q=2**40, max_kv=2**40)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+@pytest.mark.parametrize("gain", [0.0, 2.0, -2.0])
+@pytest.mark.parametrize("sinks", [True, False])
+def test_long_parts(gain, sinks):
+    # both query tiles of every CTA full; parts of more key tiles than the rings hold
+    q_lens, kv_lens = [64, 64, 64, 50], [8000, 7777, 8100, 6000]
+    b = Batch(q_lens, kv_lens, 64, 8, seed=2, gain=gain, sinks=sinks)
+    w = workspace()
+    got = b.attend(workspace=w)
+    n = parts(w)
+    blocks = 8 * sum(-(-t // 32) for t in q_lens)
+    assert n > blocks                                    # cut
+    assert sum(8 * -(-t // 32) * -(-k // 128) for t, k in zip(q_lens, kv_lens)) / n > 6      # tiles of a part
+    b.check(got)
+    again = b.attend(workspace=w)
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+def test_short_parts_leave_their_mark_and_do_not_depend_on_bounds():
+    b = Batch([6, 6, 1, 6, 3], [5009, 1506, 2101, 6, 773], 16, 2, seed=3)
+    first = None
+    for max_q, max_kv in ((6, 5009), (60, 9000), (2**40, 2**40)):
+        w = workspace()
+        got = b.attend(workspace=w, max_q=max_q, max_kv=max_kv)
+        assert parts(w) > 10
+        b.check(got)
+        first = first or got
+        assert all(torch.equal(x, y) for x, y in zip(got, first))
+
+
+@pytest.mark.parametrize("q_len,tree", [(8, False), (8, True), (3, True), (1, False), (64, True)])
+def test_rows_of_long_caches(q_len, tree):
+    # verification, and one token, on what the format's own tests do not reach in length
+    kv_lens = [9000 + q_len, 300 + q_len, q_len, 5000]
+    b = Batch([q_len] * 4, kv_lens, 64, 8, seed=4, gain=1.0)
+    masks = workloads.random_tree_masks(np.random.default_rng(0), 4, q_len).to(DEV) if tree else None
+    q = b.q.view(4, q_len, 64, 64)
+    for bound in (max(kv_lens), 2**40):
+        b.check(sa.verify_int4(q, *b.args, bound, tree_mask=masks), masks, few=8 * q_len <= 32)
+    if q_len == 1:
+        b.check(sa.decode_int4(b.q, *b.args, max(kv_lens)), few=True)
+
+
+def test_the_lse_is_that_of_a_bf16_cache():
+    # on both sides of it (fp32 sums of the same exact products, some 2^-17 apart)
+    kv_lens = [100, 333, 16, 1]
+    b = Batch([1] * 4, kv_lens, 64, 8, seed=5)
+    pools = [torch.zeros(b.cache.shape[0], 8, 16, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    for slots in b.slots:
+        for pool, rows in zip(pools, sa.gather_int4(b.cache, slots)):
+            pool[slots.long() // 16, :, slots.long() % 16] = rows
+    want = sa.decode(b.q, *pools, *b.args[1:], 333)
+    got = sa.decode_int4(b.q, *b.args, 333)
+    assert ((got[1] - want[1]).abs() <= 2.0**-12).all()
+
+
+# ------------------------------------------------------------- the plan's arguments
 def test_requests_without_new_tokens_are_no_work():
     # 20 short requests want no parts, however long the cache of one that is idle
     q_lens, kv_lens = [6] * 20 + [0] + [6] * 4, [1000] * 20 + [100000] + [700] * 4
