@@ -15,12 +15,18 @@ namespace {
 using sa::kHeadDim;
 using sa::kPageSize;
 
-constexpr int kMinPages = 8;            // pages that a warp takes at least: fewer cost more to join than they save
+// Pages that a warp takes at least: more warps and parts to join against longer chains.
+// us at 2 / 4 / 8 / 16: one token of one request of 2000 keys 9.2 / 10.5 / 12.5 / 15.2,
+// four tokens on 4000 keys 18.0 / 19.4 / 21.2 / 27.9; calls that fill the GPU do not care
+// (64 requests 32.8 / 32.8 / 32.8 / 32.7).  So 2 is no slower anywhere measured; 8 is what
+// everything else here was measured with.
+constexpr int kMinPages = 8;
 
 // Query rows per KV head up to which the kernel of few rows is taken.  us of that and of
 // the other, 16 requests of 4096..32768 keys: 32 rows 115 and 146, 64 rows 206 and 146;
 // 64 requests of up to 4096 keys: 32 rows 71 and 85, 64 rows 122 and 86; one of 4000:
-// 20.7 and 17.7, 21.2 and 17.9.
+// 20.7 and 17.7, 21.2 and 17.9 (the rule does not look at how few requests there are, and
+// loses those 3 us).
 constexpr int kFewRows = 32;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

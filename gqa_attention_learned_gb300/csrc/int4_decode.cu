@@ -7,17 +7,22 @@
 //     scale q.k_j   = (scale s_j) (q.(16 + n_j) - (16 + z_j) sum q)
 //     sum_j p_j v_j = sum_j (p_j s_j) (n_j - z_j)
 // Scales, and zero points of K, so cost a few operations per (key, head) instead of one
-// per element; p_j s_j is rounded to bf16 once.  Zero points of V stay out of the sums:
-// tensor cores cut what they add to a running sum, and 16 + n would give that a sign.
+// per element; p_j s_j is rounded to bf16 once, the type that the product takes (outputs
+// are 0.0023 of their norm off, with their own rounding alone 0.0017).  Zero points of V
+// stay out of the sums: tensor cores cut what they add to a running sum, and 16 + n would
+// give that a sign.
 //
-// What bounds it: the instructions that turn 1088 bytes per page and KV head into
-// fragments.  At the copy bandwidth an SM gets 23 bytes a cycle, a page every 47 cycles,
-// or 188 issue slots and 94 of the integer pipe.  A page takes 185 instructions, 97 of
-// them integer or logical: a word of eight codes becomes four registers by three shifts
+// What bounds it: latency, over instructions that turn 1088 bytes per page and KV head
+// into fragments.  At the copy bandwidth an SM gets 23 bytes a cycle, a page every 47
+// cycles, or 188 issue slots and 94 of the integer pipe.  A page takes 185 instructions, 97
+// of them integer or logical: a word of eight codes becomes four registers by three shifts
 // and four logical operations (V: pairs of keys are put together first, four more
-// subtractions), and S^T[16 keys x 8 rows] and O^T[64 x 8] take four mma.sync each.  So
-// 8 requests of up to 131072 keys run at 3.7 TB/s (92.7 us; the copies alone reach the
-// copy bandwidth), and about 12 us of a call are its start, first data and join.
+// subtractions), and S^T[16 keys x 8 rows] and O^T[64 x 8] take four mma.sync each.  8
+// requests of up to 131072 keys run at 3.7 TB/s, 92.8 us, of which those instructions are
+// 49 us of issue (a capture of 16 requests of 16384 keys: slots used 55% of the time, the
+// integer pipe 55%).  Four warps per scheduler, with a vote over the warp in every page, do
+// not fill the rest.  Of 64 requests of 1..4096 tokens, 32.8 us, they are 11 us; the rest is
+// start, first data, latency and joins.
 //
 // Split: every warp takes an equal, contiguous share of all pages of the call, numbered
 // through over (request, KV head, row block), whatever the requests' lengths: no wave
@@ -33,7 +38,7 @@
 //
 // Measured on the way (8 requests of up to 131072 keys): zero points of V as a correction
 // to the sums, two pages a stage 138 us; four pages, subtracted from the operands 94; as
-// it is 92.7.  Slower: one warp of a CTA making all copies (119), 24 warps per SM,
+// it is 92.8.  Slower: one warp of a CTA making all copies (119), 24 warps per SM,
 // two pages of a step in flight at once (96), high halves by multiplication.
 
 #include "int4.cuh"

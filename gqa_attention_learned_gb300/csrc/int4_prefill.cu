@@ -5,7 +5,8 @@
 // q_len are its new tokens sees keys j <= kv_len - q_len + i (or the draft keys that its
 // mask names); softmax with the sink as one more term, as in plain prefill.  The keys'
 // and values' codes become bf16 numbers s (n - z) on the way into shared memory, which
-// is exact; P is rounded to bf16 for the product with V, out once.
+// is exact; P is rounded to bf16, the type that the product with V takes, out once (outputs
+// are 0.0023 of their norm off, with their own rounding alone 0.0017).
 //
 // One CTA per SM = the rows of 2 * (128 / group) tokens of one KV head, ordered (token,
 // head), as two 128-row tiles that share every K and V tile of 128 keys: turning a tile
@@ -30,13 +31,13 @@
 // many as make the least time (plan_parts()), each at least 512 keys long.  Parts join by
 // log-sum-exp through the workspace, by the last one to get there, in the keys' order.
 //
-// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1357 us, 1013 TFLOP/s, where
+// What bounds it, for 4 x 2048 tokens on up to 14336 keys (1351 us, 1017 TFLOP/s, where
 // the kernel of the bf16 cache does 1046): the chain score - exponentials - P V of the two
 // tiles in turn.  P V of 128 x 64 x 128 from tensor memory takes about twice its
 // arithmetic's time, and start and end of a CTA some 5 us.  Measured on the way: one tile
 // per CTA 1839 us; eight unpacking warps, two score buffers 1692; three buffers and a ring
 // of packed pages 1555; softmax warps with 168 registers, sleeping waits 1537; products
-// started by polling warps 1485; a row's mask as bits 1376; fewer spills 1357.  Slower or
+// started by polling warps 1485; a row's mask as bits 1376; fewer spills 1351.  Slower or
 // no better: 16 softmax warps with half a row each; products started by one thread that
 // walks the tiles alone (1558 against 1482); persistent CTAs (1720: spills); four stages
 // of K and V; both halves of a CTA on one query tile where there is one only (64 rows 1%
